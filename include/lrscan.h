@@ -33,7 +33,7 @@
  *    default stream).  Argument errors are returned synchronously and launch
  *    nothing.  A failed launch returns LR_ERR_CUDA.
  *  - Errors detected on the device (a bounded wait that ran out, an HGRN2
- *    gate that is not a number) are recorded per call: the first 256 bytes
+ *    gate that is not a number, a log decay above 0) are recorded per call: the first 256 bytes
  *    of the call's workspace hold its status word, stamped with the call, so
  *    the word always describes the latest call that used the workspace.
  *    lr_check_status(workspace, stream) reads and resets it.
@@ -75,7 +75,8 @@ enum {
     LR_ERR_WORKSPACE = -4,    /* workspace NULL or smaller than required */
     LR_ERR_CUDA = -5,         /* a CUDA runtime/driver call failed */
     LR_ERR_TIMEOUT = -6,      /* device side: a bounded wait ran out */
-    LR_ERR_RANGE = -7         /* device side: an HGRN2 gate that is not a finite number */
+    LR_ERR_RANGE = -7         /* device side: an HGRN2 gate that is not a finite number, or a
+                               * log decay that is positive or not a number */
 };
 
 /* Human-readable name of a status code (static storage). */
@@ -262,6 +263,85 @@ int lr_hgrn2_fwd(const void *q, const void *k, const void *v, const void *g,
                  void *workspace, size_t ws_bytes, lr_stream_t stream);
 
 /* ------------------------------------------------------------------------ */
+/* Linear attention with a decay for each head                               */
+/* ------------------------------------------------------------------------ */
+
+/*
+ * Causal linear attention whose matrix state decays by one factor per head
+ * and step (the source pages have no counterpart; HGRN2 above decays every
+ * value channel by its own).  Per batch b and value head h, with the key head
+ * j = h / (H / Hk) and the dv x dk state S = S0[b,h] (zero when NULL):
+ *
+ *   l_t = a_log[h] + g[b,t,h]                 (log decay; see below)
+ *   S_t = exp(l_t) S_{t-1} + v_t k_t^T        (v of head h, k of head j)
+ *   o_t = scale * S_t q_t                     (after the update at t)
+ *
+ * for t < lens[b], and S_final[b,h] = S after the last of them.  Steps
+ * t >= lens[b] are not part of row b: their q, k, v, g are not used, their
+ * o_t is 0 and the state stays, so a right-padded batch of prompts leaves every
+ * row's own state.  lens == NULL: every row has L steps; values outside
+ * [0, L] are clamped to it.
+ *
+ * Log decays: a_log is a per-head parameter, g a per-step gate; either or both
+ * may be NULL (an absent one counts as 0, both absent is plain linear
+ * attention).  l_t <= 0; -inf is a reset (decay 0).  A positive or NaN l_t sets
+ * LR_ERR_RANGE (read with lr_check_status); that call's outputs are then not
+ * meaningful.  Decay products are formed from sums of log decays kept in 64-bit
+ * fixed point, so no range of decays needs a special setting.
+ *
+ * Layouts: q, k: (B, L, Hk*dk); v, o: (B, L, H*dv); g: (B, L, H), all in `io`;
+ *          a_log: (H) fp32; lens: (B) int32; S0, S_final: (B, H, dv, dk) fp32
+ *          (row = value channel).  Optional: a_log, g, lens, S0, S_final.
+ * Requirements: H, Hk, dk, dv >= 1, H % Hk == 0, scale finite (else
+ *          LR_ERR_INVALID_ARG); dk <= 512 (else LR_ERR_UNSUPPORTED).  Outputs
+ *          must not overlap inputs.
+ * Precision: with fp32 I/O the arithmetic is fp32.  With bf16 I/O the decayed
+ *          scores and the copy of the state that the readout uses may be
+ *          rounded to bf16 (tensor-core operands) before o_t is rounded; the
+ *          carried state is not: it is accumulated to fp32 accuracy.
+ * Workspace: the call's device status and, when the library cuts the sequence
+ *          into segments that run in parallel, one state per segment but the
+ *          last of every (batch row, head).
+ */
+size_t lr_decay_attn_workspace_size(int64_t B, int64_t L, int64_t H, int64_t Hk,
+                                    int64_t dk, int64_t dv, lr_dtype io);
+
+int lr_decay_attn_fwd(const void *q, const void *k, const void *v,
+                      const float *a_log, const void *g, const int32_t *lens,
+                      float scale, const float *S0, void *o, float *S_final,
+                      int64_t B, int64_t L, int64_t H, int64_t Hk, int64_t dk,
+                      int64_t dv, lr_dtype io,
+                      void *workspace, size_t ws_bytes, lr_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* Group norm with an activation, channels last                              */
+/* ------------------------------------------------------------------------ */
+
+/* Activation of lr_group_norm_act. */
+typedef enum { LR_ACT_NONE = 0, LR_ACT_SILU = 1 } lr_act;
+
+/*
+ * Normalises every row (token) of x in G groups of d = C / G neighbouring
+ * channels, then applies the affine map, the activation and the gate; the
+ * readout of a matrix-state scan is normalised per head and gated by silu(z)
+ * before its output projection ([HGRN2] forward; G = H there):
+ *
+ *   m = mean(x_g),  s2 = mean((x_g - m)^2)            (over the d channels)
+ *   n = gamma[c] (x[r,c] - m) / sqrt(s2 + eps) + beta[c]
+ *   y[r,c] = act(n) * (z ? silu(z[r,c]) : 1)
+ *
+ * Statistics are per row, so causal.  Layouts: x, z, y: (N, C) in `io`; gamma,
+ * beta: (C) fp32.  Optional: z, gamma (1), beta (0).  y may be x or z itself.
+ * Arithmetic in fp32, y rounded once.  A row with an infinity or a NaN in a
+ * group gives NaN in that group only.
+ * Requirements: N, C >= 0, G >= 1, C % G == 0, eps >= 0 and finite, act one of
+ * the above (else LR_ERR_INVALID_ARG).  No workspace.
+ */
+int lr_group_norm_act(const void *x, const void *z, const float *gamma,
+                      const float *beta, void *y, int64_t N, int64_t C, int64_t G,
+                      float eps, lr_act act, lr_dtype io, lr_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
 /* Gates given before their activation                                       */
 /* ------------------------------------------------------------------------ */
 
@@ -385,8 +465,19 @@ int lr_minmax_scan_fwd_host(const void *r, const void *s, const float *x0, void 
                             lr_dtype io, void *workspace, size_t ws_bytes,
                             lr_stream_t stream);
 
+/* lr_decay_attn_fwd on host buffers; every row has L steps (no lens). */
+size_t lr_decay_attn_fwd_host_workspace_size(int64_t B, int64_t L, int64_t H,
+                                             int64_t Hk, int64_t dk, int64_t dv,
+                                             lr_dtype io);
+int lr_decay_attn_fwd_host(const void *q, const void *k, const void *v,
+                           const float *a_log, const void *g, float scale,
+                           const float *S0, void *o, float *S_final,
+                           int64_t B, int64_t L, int64_t H, int64_t Hk, int64_t dk,
+                           int64_t dv, lr_dtype io,
+                           void *workspace, size_t ws_bytes, lr_stream_t stream);
+
 /*
- * Asynchronous forms of the four host-buffer calls (a library facility; the
+ * Asynchronous forms of the five host-buffer calls (a library facility; the
  * pages specify only the recurrences).  Same arguments, checks and results
  * as the synchronous forms, but each returns once its chunks are queued on
  * the library's streams, so consecutive calls overlap: the next call's
@@ -427,6 +518,12 @@ int lr_minmax_scan_fwd_host_async(const void *r, const void *s, const float *x0,
                                   float *x_final, int64_t B, int64_t L, int64_t D,
                                   lr_dtype io, void *workspace, size_t ws_bytes,
                                   lr_stream_t stream);
+int lr_decay_attn_fwd_host_async(const void *q, const void *k, const void *v,
+                                 const float *a_log, const void *g, float scale,
+                                 const float *S0, void *o, float *S_final,
+                                 int64_t B, int64_t L, int64_t H, int64_t Hk, int64_t dk,
+                                 int64_t dv, lr_dtype io,
+                                 void *workspace, size_t ws_bytes, lr_stream_t stream);
 
 /*
  * Waits until every host-buffer call queued on the current device has
@@ -481,6 +578,17 @@ int lr_hgrn2_step(const void *q, const void *k, const void *v, const void *g,
                   const float *S_in, float *S_out, void *o,
                   int64_t B, int64_t H, int64_t dk, int64_t dv, lr_dtype io,
                   lr_stream_t stream);
+
+/* Decayed linear attention, one token: S_out = exp(a_log[h] + g[b,h]) S_in +
+ * v k^T, o = scale S_out q.  q, k: (B, Hk*dk); v, o: (B, H*dv); g: (B, H), in
+ * io; a_log: (H) fp32; S_in (NULL = zero), S_out: (B, H, dv, dk) fp32.
+ * Requirements as lr_decay_attn_fwd, without its limit on dk; log decays are
+ * not checked on the device (there is no workspace to report to). */
+int lr_decay_attn_step(const void *q, const void *k, const void *v,
+                       const float *a_log, const void *g, float scale,
+                       const float *S_in, float *S_out, void *o,
+                       int64_t B, int64_t H, int64_t Hk, int64_t dk, int64_t dv,
+                       lr_dtype io, lr_stream_t stream);
 
 /* ------------------------------------------------------------------------ */
 /* Tuning and test hooks                                                     */

@@ -20,8 +20,11 @@ Functions (sources are cited in ``lro_oracle.c``):
 * :func:`minmax_scan`     -- minmaxrnc ``MinMaxNeuron`` recurrence
   ``x_t = max(min(r_t, x_{t-1}), s_t)``, every state returned.
 
-All four are pinned against closed forms, brute force and library routines
-in ``tests/test_oracle_pins.py``.
+* :func:`decay_attn`      -- linear attention with a decay for each head.
+* :func:`group_norm_act`  -- group norm per row with an activation and a gate.
+
+All are pinned against closed forms, brute force and library routines in
+``tests/test_oracle_pins.py`` and ``tests/test_decay_oracle_pins.py``.
 """
 from __future__ import annotations
 
@@ -92,6 +95,13 @@ def _load():
             lib.lro_minmax_scan_ref.argtypes = [
                 dp, dp, dp, i64, i64, i64, dp, dp, ctypes.c_int]
             lib.lro_minmax_scan_ref.restype = ctypes.c_int
+            lib.lro_decay_attn_ref.argtypes = [
+                dp, dp, dp, dp, dp, ctypes.POINTER(i64), ctypes.c_double, dp, i64, i64, i64, i64, i64,
+                i64, dp, dp, ctypes.c_int]
+            lib.lro_decay_attn_ref.restype = ctypes.c_int
+            lib.lro_group_norm_act_ref.argtypes = [
+                dp, dp, dp, dp, i64, i64, i64, ctypes.c_double, ctypes.c_int, dp, ctypes.c_int]
+            lib.lro_group_norm_act_ref.restype = ctypes.c_int
             lib.lro_max_threads.argtypes = []
             lib.lro_max_threads.restype = ctypes.c_int
             _lib = lib
@@ -207,3 +217,49 @@ def minmax_scan(r, s, x0=None, threads=0):
     if rc != 0:
         raise ValueError("lro_minmax_scan_ref rejected its arguments")
     return y, xf
+
+
+def decay_attn(q, k, v, H, Hk=None, a_log=None, g=None, S0=None, lens=None, scale=1.0, threads=0):
+    """Linear attention with a decay for each head in float64.
+
+    q, k: (B, L, Hk*dk); v: (B, L, H*dv); a_log: (H,); g: (B, L, H);
+    S0: (B, H, dv, dk); lens: (B,).  Returns ``(o (B, L, H*dv), S_final)``.
+    """
+    q, k, v = map(_f64, (q, k, v))
+    a_log, g, S0 = _f64(a_log), _f64(g), _f64(S0)
+    Hk = H if Hk is None else Hk
+    Bsz, L, HK = q.shape
+    HV = v.shape[-1]
+    assert HK % Hk == 0 and HV % H == 0 and H % Hk == 0
+    dk, dv = HK // Hk, HV // H
+    assert k.shape == q.shape and v.shape[:2] == (Bsz, L)
+    assert a_log is None or a_log.shape == (H,)
+    assert g is None or g.shape == (Bsz, L, H)
+    assert S0 is None or S0.shape == (Bsz, H, dv, dk)
+    n = None
+    if lens is not None:
+        n = np.ascontiguousarray(np.asarray(lens.cpu() if hasattr(lens, "cpu") else lens, dtype=np.int64))
+        assert n.shape == (Bsz,)
+    o = np.zeros((Bsz, L, HV), dtype=np.float64)
+    Sf = np.zeros((Bsz, H, dv, dk), dtype=np.float64)
+    rc = _load().lro_decay_attn_ref(
+        _ptr(q), _ptr(k), _ptr(v), _ptr(a_log), _ptr(g),
+        None if n is None else n.ctypes.data_as(ctypes.POINTER(ctypes.c_int64)), float(scale), _ptr(S0),
+        Bsz, L, H, Hk, dk, dv, _ptr(o), _ptr(Sf), int(threads))
+    if rc != 0:
+        raise ValueError("lro_decay_attn_ref rejected its arguments")
+    return o, Sf
+
+
+def group_norm_act(x, G, gamma=None, beta=None, z=None, act="none", eps=1e-5, threads=0):
+    """Group norm of every row of x (N, C) in float64, then the activation
+    ("none" or "silu") and the gate silu(z).  Returns y (N, C)."""
+    x = _f64(x)
+    gamma, beta, z = _f64(gamma), _f64(beta), _f64(z)
+    N, C = x.shape
+    y = np.zeros((N, C), dtype=np.float64)
+    rc = _load().lro_group_norm_act_ref(_ptr(x), _ptr(z), _ptr(gamma), _ptr(beta), N, C, G, float(eps),
+                                        int(act == "silu"), _ptr(y), int(threads))
+    if rc != 0:
+        raise ValueError("lro_group_norm_act_ref rejected its arguments")
+    return y

@@ -29,8 +29,12 @@
  *           returns the states after every step and the last state) and
  *           minmax_operator.py (apply: f(x) = max(min(a, x), b)).
  *
+ *   Linear attention with a decay for each head and the group norm with an
+ *   activation have no page; their formulas stand at the functions.
+ *
  * Parity pins (closed forms, brute force, library special cases) live in
- * tests/test_oracle_pins.py.  All four functions are pinned there.
+ * tests/test_oracle_pins.py (the page scans) and
+ * tests/test_decay_oracle_pins.py (the other two).
  *
  * Layouts (row-major, contiguous):
  *   selective: x, dt, z, y: (B, L, D); Bm, Cm: (B, L, N); A_log: (D, N);
@@ -237,6 +241,103 @@ int lro_hgrn2_ref(const double *q, const double *k, const double *v,
         free(S);
     }
     return failed ? -1 : 0;
+}
+
+/*
+ * Linear attention with a decay for each head, one step at a time.  For each
+ * (b, h) with the key head j = h / (H / Hk):
+ *
+ *   S = exp(a_log[h] + g[b,t,h]) S + v_t k_t^T,   o_t = scale S q_t
+ *
+ * for t < lens[b] (L when lens == NULL); later o_t are 0.  a_log and g may be
+ * NULL (0).  Layouts: q, k: (B, L, Hk*dk); v, o: (B, L, H*dv); g: (B, L, H);
+ * S0, S_final: (B, H, dv, dk).
+ */
+int lro_decay_attn_ref(const double *q, const double *k, const double *v,
+                       const double *a_log, const double *g, const int64_t *lens,
+                       double scale, const double *S0,
+                       int64_t B, int64_t L, int64_t H, int64_t Hk, int64_t dk, int64_t dv,
+                       double *o, double *S_final, int nthreads)
+{
+    if (!q || !k || !v || !o) return -1;
+    if (B < 0 || L < 0 || H <= 0 || Hk <= 0 || H % Hk || dk <= 0 || dv <= 0) return -1;
+    set_threads(nthreads);
+    int64_t bh;
+    int failed = 0;
+#pragma omp parallel for schedule(static)
+    for (bh = 0; bh < B * H; ++bh) {
+        const int64_t b = bh / H, hd = bh % H, kh = hd / (H / Hk);
+        int64_t n = lens ? lens[b] : L;
+        n = n < 0 ? 0 : (n > L ? L : n);
+        double *S = (double *)malloc((size_t)(dv * dk) * sizeof(double));
+        if (!S) {
+#pragma omp atomic write
+            failed = 1;
+            continue;
+        }
+        for (int64_t e = 0; e < dv * dk; ++e) S[e] = S0 ? S0[bh * dv * dk + e] : 0.0;
+        for (int64_t t = 0; t < L; ++t) {
+            const double *qt = q + ((b * L + t) * Hk + kh) * dk;
+            const double *kt = k + ((b * L + t) * Hk + kh) * dk;
+            const double *vt = v + ((b * L + t) * H + hd) * dv;
+            double *ot = o + ((b * L + t) * H + hd) * dv;
+            if (t >= n) {
+                for (int64_t i = 0; i < dv; ++i) ot[i] = 0.0;
+                continue;
+            }
+            const double a = exp((a_log ? a_log[hd] : 0.0) + (g ? g[(b * L + t) * H + hd] : 0.0));
+            for (int64_t i = 0; i < dv; ++i) {
+                double acc = 0.0;
+                for (int64_t j = 0; j < dk; ++j) {
+                    S[i * dk + j] = a * S[i * dk + j] + vt[i] * kt[j];
+                    acc += S[i * dk + j] * qt[j];
+                }
+                ot[i] = scale * acc;
+            }
+        }
+        if (S_final)
+            memcpy(S_final + bh * dv * dk, S, (size_t)(dv * dk) * sizeof(double));
+        free(S);
+    }
+    return failed ? -1 : 0;
+}
+
+/*
+ * Group norm with an activation: per row r and group of d = C / G channels,
+ *   n = gamma[c] (x - mean) / sqrt(mean((x - mean)^2) + eps) + beta[c]
+ *   y = (silu_act ? silu(n) : n) * (z ? silu(z) : 1)
+ * gamma NULL = 1, beta NULL = 0.  x, z, y: (N, C).
+ */
+int lro_group_norm_act_ref(const double *x, const double *z, const double *gamma,
+                           const double *beta, int64_t N, int64_t C, int64_t G, double eps,
+                           int silu_act, double *y, int nthreads)
+{
+    if (!x || !y || N < 0 || C < 0 || G <= 0 || C % G) return -1;
+    set_threads(nthreads);
+    const int64_t d = C / G;
+    int64_t r;
+#pragma omp parallel for schedule(static)
+    for (r = 0; r < N * G; ++r) {
+        const int64_t c0 = (r % G) * d;
+        const double *xr = x + (r / G) * C + c0;
+        double m = 0.0, s2 = 0.0;
+        for (int64_t i = 0; i < d; ++i) m += xr[i];
+        m /= (double)d;
+        for (int64_t i = 0; i < d; ++i) s2 += (xr[i] - m) * (xr[i] - m);
+        s2 /= (double)d;
+        for (int64_t i = 0; i < d; ++i) {
+            double n = (xr[i] - m) / sqrt(s2 + eps);
+            if (gamma) n *= gamma[c0 + i];
+            if (beta) n += beta[c0 + i];
+            if (silu_act) n = n / (1.0 + exp(-n));
+            if (z) {
+                const double zv = z[(r / G) * C + c0 + i];
+                n *= zv / (1.0 + exp(-zv));
+            }
+            y[(r / G) * C + c0 + i] = n;
+        }
+    }
+    return 0;
 }
 
 /*

@@ -5,7 +5,7 @@ in the library's CUDA kernels:
 
 * ``lr_*`` functions with the C names and signatures (pointers as ints);
 * torch conveniences (:func:`selective_scan`, :func:`rglru_scan`,
-  :func:`hgrn2`) that check shapes and dtypes, allocate outputs and the
+  :func:`hgrn2`, :func:`decay_attn`, ...) that check shapes and dtypes, allocate outputs and the
   workspace with torch, pass the current CUDA stream and raise
   :class:`LrError` on a non-zero status.  Given host tensors they copy the
   inputs to the current CUDA device and the outputs back (the end-to-end
@@ -28,6 +28,7 @@ LR_F32, LR_BF16 = 0, 1
 LR_OK = 0
 LR_ERR_INVALID_ARG, LR_ERR_UNSUPPORTED, LR_ERR_MISALIGNED = -1, -2, -3
 LR_ERR_WORKSPACE, LR_ERR_CUDA, LR_ERR_TIMEOUT, LR_ERR_RANGE = -4, -5, -6, -7
+LR_ACT_NONE, LR_ACT_SILU = 0, 1
 
 _IO = {torch.float32: LR_F32, torch.bfloat16: LR_BF16}
 
@@ -82,6 +83,17 @@ SIGNATURES = {
                                      _I64, _I64, _I, _P, _SZ, _P]),
     "lr_minmax_scan_fwd_host_async": (_I, [_P, _P, _P, _P, _P, _I64, _I64, _I64, _I, _P, _SZ, _P]),
     "lr_host_sync": (_I, []),
+    "lr_decay_attn_workspace_size": (_SZ, [_I64, _I64, _I64, _I64, _I64, _I64, _I]),
+    "lr_decay_attn_fwd": (_I, [_P, _P, _P, _P, _P, _P, _F, _P, _P, _P, _I64, _I64, _I64, _I64, _I64,
+                               _I64, _I, _P, _SZ, _P]),
+    "lr_decay_attn_step": (_I, [_P, _P, _P, _P, _P, _F, _P, _P, _P, _I64, _I64, _I64, _I64, _I64, _I,
+                                _P]),
+    "lr_decay_attn_fwd_host_workspace_size": (_SZ, [_I64, _I64, _I64, _I64, _I64, _I64, _I]),
+    "lr_decay_attn_fwd_host": (_I, [_P, _P, _P, _P, _P, _F, _P, _P, _P, _I64, _I64, _I64, _I64, _I64,
+                                    _I64, _I, _P, _SZ, _P]),
+    "lr_decay_attn_fwd_host_async": (_I, [_P, _P, _P, _P, _P, _F, _P, _P, _P, _I64, _I64, _I64, _I64,
+                                          _I64, _I64, _I, _P, _SZ, _P]),
+    "lr_group_norm_act": (_I, [_P, _P, _P, _P, _P, _I64, _I64, _I64, _F, _I, _I, _P]),
 }
 
 
@@ -303,6 +315,43 @@ def lr_minmax_scan_fwd_host_async(r, s, x0, y, x_final, B, L, D, io, workspace, 
 def lr_host_sync() -> int:
     """Waits for every host-buffer call queued on the current device."""
     return int(_lib.lr_host_sync())
+
+
+def lr_decay_attn_workspace_size(B, L, H, Hk, dk, dv, io) -> int:
+    return int(_lib.lr_decay_attn_workspace_size(B, L, H, Hk, dk, dv, io))
+
+
+def lr_decay_attn_fwd(q, k, v, a_log, g, lens, scale, S0, o, S_final, B, L, H, Hk, dk, dv, io,
+                      workspace, ws_bytes, stream) -> int:
+    return _lib.lr_decay_attn_fwd(q, k, v, a_log, g, lens, scale, S0, o, S_final, B, L, H, Hk, dk, dv,
+                                  io, workspace, ws_bytes, stream)
+
+
+def lr_decay_attn_step(q, k, v, a_log, g, scale, S_in, S_out, o, B, H, Hk, dk, dv, io, stream) -> int:
+    return _lib.lr_decay_attn_step(q, k, v, a_log, g, scale, S_in, S_out, o, B, H, Hk, dk, dv, io,
+                                   stream)
+
+
+def lr_decay_attn_fwd_host_workspace_size(B, L, H, Hk, dk, dv, io) -> int:
+    return int(_lib.lr_decay_attn_fwd_host_workspace_size(B, L, H, Hk, dk, dv, io))
+
+
+def lr_decay_attn_fwd_host(q, k, v, a_log, g, scale, S0, o, S_final, B, L, H, Hk, dk, dv, io, workspace,
+                           ws_bytes, stream) -> int:
+    """Decayed linear attention on host buffers (device workspace only)."""
+    return int(_lib.lr_decay_attn_fwd_host(q, k, v, a_log, g, scale, S0, o, S_final, B, L, H, Hk, dk, dv,
+                                           io, workspace, ws_bytes, stream))
+
+
+def lr_decay_attn_fwd_host_async(q, k, v, a_log, g, scale, S0, o, S_final, B, L, H, Hk, dk, dv, io,
+                                 workspace, ws_bytes, stream) -> int:
+    """As lr_decay_attn_fwd_host, returning once the work is queued."""
+    return int(_lib.lr_decay_attn_fwd_host_async(q, k, v, a_log, g, scale, S0, o, S_final, B, L, H, Hk,
+                                                 dk, dv, io, workspace, ws_bytes, stream))
+
+
+def lr_group_norm_act(x, z, gamma, beta, y, N, C, G, eps, act, io, stream) -> int:
+    return _lib.lr_group_norm_act(x, z, gamma, beta, y, N, C, G, eps, act, io, stream)
 
 
 # ------------------------------------------------------------ torch helpers
@@ -681,6 +730,105 @@ def minmax_scan(r, s, x0=None, workspace=None, out=None,
     return _finish((y, xf), host_out, host, dev, sync_host)
 
 
+def _heads_of(q, k, v, H: int, Hk: Optional[int]):
+    """(Hk, dk, dv) of q, k (..., Hk*dk) and v (..., H*dv)."""
+    Hk = H if Hk is None else Hk
+    if H < 1 or Hk < 1 or H % Hk:
+        raise ValueError(f"{H} value heads cannot share {Hk} key heads")
+    if q.shape[-1] % Hk or v.shape[-1] % H:
+        raise ValueError(f"widths {q.shape[-1]} and {v.shape[-1]} are not divisible by {Hk} key heads "
+                         f"and {H} value heads")
+    if k.shape != q.shape or v.shape[:-1] != q.shape[:-1]:
+        raise ValueError(f"q {tuple(q.shape)}, k {tuple(k.shape)}, v {tuple(v.shape)} do not match")
+    return Hk, q.shape[-1] // Hk, v.shape[-1] // H
+
+
+def _shaped(t: Optional[torch.Tensor], shape, name: str):
+    if t is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+
+
+def decay_attn(q, k, v, H: int, Hk: Optional[int] = None, a_log=None, g=None, S0=None, lens=None,
+               scale: float = 1.0, workspace=None, out=None,
+               sync_host: bool = True) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Causal linear attention with a decay for each head:
+    S_t = exp(a_log[h] + g[b, t, h]) S_{t-1} + v_t k_t^T, o_t = scale S_t q_t.
+
+    q, k: (B, L, Hk*dk); v: (B, L, H*dv); g: (B, L, H) or None, one dtype
+    (bfloat16 or float32); a_log: (H,) fp32 or None; ``Hk`` key heads (default
+    H), each shared by H/Hk value heads; S0: (B, H, dv, dk) fp32 or None;
+    lens: (B,) integers or None: row b has lens[b] steps (its later outputs are
+    0 and its state stays).  Returns (o (B, L, H*dv), S_final (B, H, dv, dk)
+    fp32); ``out=(o, S_final)`` gives the result tensors (GPU or host).  Host
+    inputs with host (or no) ``out`` run the library's host-buffer path (without
+    ``lens``; ``sync_host=False`` queues it, as for ``selective_scan``).  A log
+    decay above 0 sets LR_ERR_RANGE (see ``check_status``)."""
+    Hk, dk, dv = _heads_of(q, k, v, H, Hk)
+    B, L = q.shape[0], q.shape[1]
+    _same(q, k, v, g)
+    io = _io_of(q)
+    _shaped(g, (B, L, H), "g")
+    _shaped(a_log, (H,), "a_log")
+    _shaped(S0, (B, H, dv, dk), "S0")
+    _shaped(lens, (B,), "lens")
+    specs = [((B, L, H * dv), q.dtype), ((B, H, dv, dk), torch.float32)]
+    if lens is None and _host_route((q, k, v, g), out):
+        q, k, v, g = (_h(t) for t in (q, k, v, g))
+        a_log, S0 = (_h(t, torch.float32) for t in (a_log, S0))
+        o, Sf = _host_outputs(out, specs)
+        fn, ws, wsb = _host_entry(lr_decay_attn_fwd_host, lr_decay_attn_fwd_host_async,
+                                  lr_decay_attn_fwd_host_workspace_size(B, L, H, Hk, dk, dv, io), workspace,
+                                  sync_host, (q, k, v, a_log, g, S0, o, Sf))
+        _check(fn(_ptr(q), _ptr(k), _ptr(v), _ptr(a_log), _ptr(g), float(scale), _ptr(S0), _ptr(o), _ptr(Sf),
+                  B, L, H, Hk, dk, dv, io, _ptr(ws), wsb, _host_stream()), fn.__name__)
+        return o, Sf
+    host = q.device.type != "cuda"
+    dev = _target_device(q)
+    q, k, v, g = (_dev(t, dev) for t in (q, k, v, g))
+    a_log, S0 = (_dev(None if t is None else t.float(), dev) for t in (a_log, S0))
+    lens = _dev(None if lens is None else lens.to(torch.int32), dev)
+    (o, Sf), host_out = _outputs(out, specs, dev)
+    ws, wsb = _workspace(lr_decay_attn_workspace_size(B, L, H, Hk, dk, dv, io), dev, workspace)
+    stream = torch.cuda.current_stream(dev).cuda_stream
+    _check(lr_decay_attn_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(a_log), _ptr(g), _ptr(lens), float(scale),
+                             _ptr(S0), _ptr(o), _ptr(Sf), B, L, H, Hk, dk, dv, io, _ptr(ws), wsb, stream),
+           "lr_decay_attn_fwd")
+    return _finish((o, Sf), host_out, host, dev, sync_host)
+
+
+def group_norm_act(x, G: int, gamma=None, beta=None, z=None, act: str = "none", eps: float = 1e-5,
+                   out=None) -> torch.Tensor:
+    """Group norm of every row of x (..., C) on the GPU in G groups of
+    neighbouring channels, then gamma, beta ((C,) fp32 or None), the activation
+    ("none" or "silu") and the gate silu(z) (z like x, or None).  Statistics are
+    per row.  ``out`` gives the result tensor (x or z itself is allowed)."""
+    if act not in _ACT:
+        raise ValueError(f"unknown activation {act!r}; use one of {sorted(_ACT)}")
+    C = x.shape[-1]
+    if G < 1 or C % G:
+        raise ValueError(f"{C} channels cannot be split into {G} groups")
+    _shaped(z, x.shape, "z")
+    _shaped(gamma, (C,), "gamma")
+    _shaped(beta, (C,), "beta")
+    _same(x, z)
+    io = _io_of(x)
+    dev = _target_device(x)
+    x, z = _dev(x, dev), _dev(z, dev)
+    gamma, beta = (_dev(None if t is None else t.float(), dev) for t in (gamma, beta))
+    if out is None:
+        out = torch.empty_like(x)
+    elif out.shape != x.shape or out.dtype != x.dtype or out.device != dev or not out.is_contiguous():
+        raise ValueError(f"out must be a contiguous {x.dtype} GPU tensor of shape {tuple(x.shape)}")
+    stream = torch.cuda.current_stream(dev).cuda_stream
+    _check(lr_group_norm_act(_ptr(x), _ptr(z), _ptr(gamma), _ptr(beta), _ptr(out),
+                             x.numel() // C if C else 0, C, G, float(eps), _ACT[act], io, stream),
+           "lr_group_norm_act")
+    return out
+
+
+_ACT = {"none": LR_ACT_NONE, "silu": LR_ACT_SILU}
+
+
 def _step_state(state, shape, dev, state_out):
     """(state before the step or None, state buffer the step writes)."""
     h_in = None if state is None else _dev(state.float(), dev)
@@ -760,6 +908,30 @@ def hgrn2_step(q, k, v, g, H: int, S=None, S_out=None):
     stream = torch.cuda.current_stream(dev).cuda_stream
     _check(lr_hgrn2_step(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(S_in), _ptr(S_new), _ptr(o),
                          B, H, dk, dv, _io_of(q), stream), "lr_hgrn2_step")
+    return o, S_new
+
+
+def decay_attn_step(q, k, v, H: int, Hk: Optional[int] = None, a_log=None, g=None, S=None, S_out=None,
+                    scale: float = 1.0):
+    """One token of ``decay_attn``.  q, k: (B, Hk*dk); v: (B, H*dv); g: (B, H)
+    or None, one dtype on the GPU; a_log: (H,) fp32 or None; S: (B, H, dv, dk)
+    fp32 or None (zero).  Returns (o (B, H*dv), S_new); ``S_out`` gives the
+    buffer S_new is written to (it may be ``S`` itself)."""
+    Hk, dk, dv = _heads_of(q, k, v, H, Hk)
+    B = q.shape[0]
+    _same(q, k, v, g)
+    io = _io_of(q)
+    _shaped(g, (B, H), "g")
+    _shaped(a_log, (H,), "a_log")
+    _shaped(S, (B, H, dv, dk), "S")
+    dev = _target_device(q)
+    q, k, v, g = (_dev(t, dev) for t in (q, k, v, g))
+    a_log = _dev(None if a_log is None else a_log.float(), dev)
+    S_in, S_new = _step_state(S, (B, H, dv, dk), dev, S_out)
+    o = torch.empty(B, H * dv, dtype=q.dtype, device=dev)
+    stream = torch.cuda.current_stream(dev).cuda_stream
+    _check(lr_decay_attn_step(_ptr(q), _ptr(k), _ptr(v), _ptr(a_log), _ptr(g), float(scale), _ptr(S_in),
+                              _ptr(S_new), _ptr(o), B, H, Hk, dk, dv, io, stream), "lr_decay_attn_step")
     return o, S_new
 
 

@@ -9,6 +9,7 @@
 #include <cstdint>
 #include <cstring>
 
+#include "lr_decay.h"
 #include "lr_internal.h"
 #include "lrscan.h"
 
@@ -159,6 +160,30 @@ int validate_minmax(const void *r, const void *s, const float *x0, const void *y
     return LR_OK;
 }
 
+// sizes shared by the decayed linear attention's prompt and step forms
+int validate_decay_sizes(int64_t B, int64_t L, int64_t H, int64_t Hk, int64_t dk, int64_t dv, lr_dtype io) {
+    if (B < 0 || L < 0 || H <= 0 || Hk <= 0 || dk <= 0 || dv <= 0 || !io_ok(io) || H % Hk != 0)
+        return LR_ERR_INVALID_ARG;
+    if (!fits_int(B) || !fits_int(L) || !fits_int(H) || !fits_int(dv) || !fits_int(dk) || B * H > INT_MAX)
+        return LR_ERR_UNSUPPORTED;
+    return LR_OK;
+}
+
+int validate_decay(const void *q, const void *k, const void *v, const float *a_log, const void *g,
+                   const int32_t *lens, float scale, const float *S0, const void *o, const float *S_final,
+                   int64_t B, int64_t L, int64_t H, int64_t Hk, int64_t dk, int64_t dv, lr_dtype io) {
+    if (!std::isfinite(scale)) return LR_ERR_INVALID_ARG;
+    const int rc = validate_decay_sizes(B, L, H, Hk, dk, dv, io);
+    if (rc == LR_ERR_INVALID_ARG) return rc;
+    if (B > 0 && L > 0 && (!q || !k || !v || !o)) return LR_ERR_INVALID_ARG;
+    if (rc != LR_OK) return rc;
+    if (dk > 512) return LR_ERR_UNSUPPORTED;
+    const void *ptrs[] = {q, k, v, a_log, g, lens, S0, o, S_final};
+    for (const void *p : ptrs)
+        if (misaligned(p)) return LR_ERR_MISALIGNED;
+    return LR_OK;
+}
+
 // Decode steps: the state after the step is always written (h_out
 // required); the state before it is optional (NULL = zero).
 int validate_step_common(const void *const *required, int n_required, const void *const *all, int n_all) {
@@ -182,7 +207,7 @@ const char *lr_status_string(int code) {
         case LR_ERR_WORKSPACE: return "LR_ERR_WORKSPACE: workspace missing or too small";
         case LR_ERR_CUDA: return "LR_ERR_CUDA: a CUDA call failed";
         case LR_ERR_TIMEOUT: return "LR_ERR_TIMEOUT: a bounded device-side wait ran out";
-        case LR_ERR_RANGE: return "LR_ERR_RANGE: an HGRN2 gate is not a finite number";
+        case LR_ERR_RANGE: return "LR_ERR_RANGE: a gate is not a finite number or a log decay is positive";
         default: return "unknown lrscan status";
     }
 }
@@ -473,6 +498,70 @@ extern "C" int lr_minmax_scan_step(const void *r, const void *s, const float *x_
                                   reinterpret_cast<cudaStream_t>(stream));
 }
 
+// ------------------------------------------ decayed linear attention, group norm
+extern "C" size_t lr_decay_attn_workspace_size(int64_t B, int64_t L, int64_t H, int64_t Hk, int64_t dk,
+                                               int64_t dv, lr_dtype io) {
+    if (validate_decay_sizes(B, L, H, Hk, dk, dv, io) != LR_OK || dk > 512) return 0;
+    if (B == 0 || L == 0) return lr::kStatusBytes;
+    lr::DecayPlan p;
+    if (lr::decay_plan(B, L, H, Hk, dk, dv, io, &p) != LR_OK) return SIZE_MAX;
+    return p.ws_bytes;
+}
+
+extern "C" int lr_decay_attn_fwd(const void *q, const void *k, const void *v, const float *a_log, const void *g,
+                                 const int32_t *lens, float scale, const float *S0, void *o, float *S_final,
+                                 int64_t B, int64_t L, int64_t H, int64_t Hk, int64_t dk, int64_t dv,
+                                 lr_dtype io, void *workspace, size_t ws_bytes, lr_stream_t stream) {
+    int rc = validate_decay(q, k, v, a_log, g, lens, scale, S0, o, S_final, B, L, H, Hk, dk, dv, io);
+    if (rc != LR_OK) return rc;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (B == 0) return lr::status_ok_no_launch(workspace, ws_bytes, st);
+    if (L == 0) {
+        if ((rc = copy_state(S0, S_final, size_t(B) * H * dk * dv, st)) != LR_OK) return rc;
+        return lr::status_ok_no_launch(workspace, ws_bytes, st);
+    }
+    lr::DecayPlan p;
+    if ((rc = lr::decay_plan(B, L, H, Hk, dk, dv, io, &p)) != LR_OK) return rc;
+    if (workspace == nullptr || ws_bytes < p.ws_bytes) return LR_ERR_WORKSPACE;
+    if (misaligned(workspace)) return LR_ERR_MISALIGNED;
+    lr::DecayArgs a{};
+    a.q = q, a.k = k, a.v = v, a.a_log = a_log, a.g = g, a.lens = lens, a.S0 = S0, a.o = o, a.S_final = S_final;
+    a.B = B, a.L = L, a.H = int(H), a.Hk = int(Hk), a.dk = int(dk), a.dv = int(dv), a.scale = scale;
+    return lr::decay_attn_launch(a, io, p, workspace, st);
+}
+
+extern "C" int lr_decay_attn_step(const void *q, const void *k, const void *v, const float *a_log, const void *g,
+                                  float scale, const float *S_in, float *S_out, void *o, int64_t B, int64_t H,
+                                  int64_t Hk, int64_t dk, int64_t dv, lr_dtype io, lr_stream_t stream) {
+    if (!std::isfinite(scale)) return LR_ERR_INVALID_ARG;
+    int rc = validate_decay_sizes(B, 1, H, Hk, dk, dv, io);
+    if (rc != LR_OK) return rc;
+    if (B > 0) {
+        const void *req[] = {q, k, v, S_out, o};
+        const void *all[] = {q, k, v, a_log, g, S_in, S_out, o};
+        if ((rc = validate_step_common(req, 5, all, 8)) != LR_OK) return rc;
+    }
+    return lr::decay_step_launch(q, k, v, a_log, g, scale, S_in, S_out, o, B, H, Hk, dk, dv, io == LR_BF16,
+                                 reinterpret_cast<cudaStream_t>(stream));
+}
+
+extern "C" int lr_group_norm_act(const void *x, const void *z, const float *gamma, const float *beta, void *y,
+                                 int64_t N, int64_t C, int64_t G, float eps, lr_act act, lr_dtype io,
+                                 lr_stream_t stream) {
+    if (N < 0 || C < 0 || G <= 0 || !io_ok(io) || !std::isfinite(eps) || eps < 0.0f ||
+        (act != LR_ACT_NONE && act != LR_ACT_SILU) || C % G != 0)
+        return LR_ERR_INVALID_ARG;
+    if (!fits_int(C) || !fits_int(N)) return LR_ERR_UNSUPPORTED;
+    if (N > 0 && C > 0) {
+        const void *req[] = {x, y};
+        const void *all[] = {x, z, gamma, beta, y};
+        const int rc = validate_step_common(req, 2, all, 5);
+        if (rc != LR_OK) return rc;
+    }
+    return lr::group_norm_act_launch(x, z, gamma, beta, y, N, C, G, eps, act, io == LR_BF16,
+                                     reinterpret_cast<cudaStream_t>(stream));
+}
+
 // ---------------------------------------------------------------- host buffers
 // The same scans with every tensor in host memory: the engine in lr_host.cu
 // runs the sequence through the GPU in time chunks, each chunk one call of
@@ -652,6 +741,49 @@ lr::HostJob mm_host_job(const MmHost &a, int64_t L, const void *r, const void *s
     return j;
 }
 
+struct DaHost {
+    int64_t B, H, Hk, dk, dv;
+    lr_dtype io;
+    float scale;
+    bool has_g, has_a;
+};
+
+int da_host_chunk(const void *c, const void *const *in, void *const *out, const void *const *par, int64_t lc,
+                  const float *s_in, float *s_out, void *kws, size_t kws_bytes, cudaStream_t st) {
+    const DaHost &a = *static_cast<const DaHost *>(c);
+    return lr_decay_attn_fwd(in[0], in[1], in[2], a.has_a ? static_cast<const float *>(par[0]) : nullptr,
+                             a.has_g ? in[3] : nullptr, nullptr, a.scale, s_in, out[0], s_out, a.B, lc, a.H, a.Hk,
+                             a.dk, a.dv, a.io, kws, kws_bytes, reinterpret_cast<lr_stream_t>(st));
+}
+
+// The chunk length always counts g's bytes, so the workspace query (which
+// assumes a_log and g) covers calls without them.
+lr::HostJob da_host_job(const DaHost &a, int64_t L, const void *q, const void *k, const void *v,
+                        const float *a_log, const void *g, const float *S0, void *o, float *S_final) {
+    lr::HostJob j;
+    j.B = a.B;
+    j.L = L;
+    j.es = io_bytes(a.io);
+    j.in[0] = {q, nullptr, a.Hk * a.dk};
+    j.in[1] = {k, nullptr, a.Hk * a.dk};
+    j.in[2] = {v, nullptr, a.H * a.dv};
+    if (a.has_g) j.in[3] = {g, nullptr, a.H};
+    j.n_in = a.has_g ? 4 : 3;
+    j.out[0] = {nullptr, o, a.H * a.dv};
+    j.n_out = 1;
+    j.par[0] = {a_log, a.has_a ? size_t(a.H) * sizeof(float) : 0};
+    j.n_par = 1;
+    j.state0 = S0;
+    j.state_final = S_final;
+    j.state_bytes = size_t(a.B) * a.H * a.dv * a.dk * sizeof(float);
+    j.Lc = lr::host_chunk_steps(a.B, L, j.es * size_t(2 * a.Hk * a.dk + a.H * a.dv + a.H));
+    j.kernel_ws = lr_decay_attn_workspace_size(a.B, j.Lc, a.H, a.Hk, a.dk, a.dv, a.io);
+    // (also serves a shorter last chunk: the size does not shrink with L)
+    j.launch = da_host_chunk;
+    j.ctx = &a;
+    return j;
+}
+
 }  // namespace
 
 extern "C" size_t lr_selective_scan_fwd_host_workspace_size(int64_t B, int64_t L, int64_t D, int64_t N,
@@ -808,6 +940,47 @@ extern "C" int lr_minmax_scan_fwd_host_async(const void *r, const void *s, const
                                              float *x_final, int64_t B, int64_t L, int64_t D, lr_dtype io,
                                              void *workspace, size_t ws_bytes, lr_stream_t stream) {
     return minmax_host(r, s, x0, y, x_final, B, L, D, io, workspace, ws_bytes, stream, true);
+}
+
+extern "C" size_t lr_decay_attn_fwd_host_workspace_size(int64_t B, int64_t L, int64_t H, int64_t Hk, int64_t dk,
+                                                        int64_t dv, lr_dtype io) {
+    if (validate_decay_sizes(B, L, H, Hk, dk, dv, io) != LR_OK || dk > 512 || B == 0 || L == 0) return 0;
+    const DaHost a{B, H, Hk, dk, dv, io, 1.0f, true, true};
+    const lr::HostJob j = da_host_job(a, L, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr);
+    return j.kernel_ws == SIZE_MAX ? SIZE_MAX : lr::host_workspace_bytes(j);
+}
+
+static int decay_host(const void *q, const void *k, const void *v, const float *a_log, const void *g, float scale,
+                      const float *S0, void *o, float *S_final, int64_t B, int64_t L, int64_t H, int64_t Hk,
+                      int64_t dk, int64_t dv, lr_dtype io, void *workspace, size_t ws_bytes, lr_stream_t stream,
+                      bool async_) {
+    int rc = validate_decay(q, k, v, a_log, g, nullptr, scale, S0, o, S_final, B, L, H, Hk, dk, dv, io);
+    if (rc != LR_OK) return rc;
+    if (B == 0) return LR_OK;
+    if (L == 0) {
+        host_state_copy(S0, S_final, size_t(B) * H * dk * dv);
+        return LR_OK;
+    }
+    const DaHost a{B, H, Hk, dk, dv, io, scale, g != nullptr, a_log != nullptr};
+    const lr::HostJob j = da_host_job(a, L, q, k, v, a_log, g, S0, o, S_final);
+    if ((rc = host_ws_check(j, workspace, ws_bytes)) != LR_OK) return rc;
+    return lr::run_host_job(j, workspace, ws_bytes, reinterpret_cast<cudaStream_t>(stream), async_);
+}
+
+extern "C" int lr_decay_attn_fwd_host(const void *q, const void *k, const void *v, const float *a_log,
+                                      const void *g, float scale, const float *S0, void *o, float *S_final,
+                                      int64_t B, int64_t L, int64_t H, int64_t Hk, int64_t dk, int64_t dv,
+                                      lr_dtype io, void *workspace, size_t ws_bytes, lr_stream_t stream) {
+    return decay_host(q, k, v, a_log, g, scale, S0, o, S_final, B, L, H, Hk, dk, dv, io, workspace, ws_bytes, stream,
+                      false);
+}
+
+extern "C" int lr_decay_attn_fwd_host_async(const void *q, const void *k, const void *v, const float *a_log,
+                                            const void *g, float scale, const float *S0, void *o, float *S_final,
+                                            int64_t B, int64_t L, int64_t H, int64_t Hk, int64_t dk, int64_t dv,
+                                            lr_dtype io, void *workspace, size_t ws_bytes, lr_stream_t stream) {
+    return decay_host(q, k, v, a_log, g, scale, S0, o, S_final, B, L, H, Hk, dk, dv, io, workspace, ws_bytes, stream,
+                      true);
 }
 
 extern "C" int lr_host_sync(void) { return lr::host_sync(); }

@@ -1,0 +1,49 @@
+// lr_decay.cuh -- device helpers of the decayed linear attention.
+//
+// Log decays are summed in fixed point: a step's log2 decay becomes a 64-bit
+// integer in units of 2^-32, so sums over any range are exact and do not
+// depend on how the sequence is cut, and a reset (a decay of 0) does not eat
+// the precision of the differences after it.
+#pragma once
+
+#include "lr_decay.h"
+#include "lr_device.cuh"
+
+namespace lr {
+namespace dec {
+
+constexpr float kFixInv = 2.3283064365386963e-10f;   // 2^-32
+// a step's floor: exp(-1024) is 0 in fp32, so this is a reset
+constexpr float kFloor = -1024.0f;
+// The running state is kept divided by the decay since the last rescale, and
+// rescaled once that decay falls below 2^-16.  Rescaling rarely matters for
+// accuracy: a factor that is rounded once per chunk, and the same way every
+// time, compounds over the slow heads' thousands of steps.
+constexpr long long kRescale = -(16ll << 32);
+// A chunk of the step-by-step kernel that alone decays further than this is
+// run with the decay applied at every step.  With kRescale it bounds the
+// factors 1 / A_t by 2^48, so v_t k_t products up to 2^80 stay finite.
+constexpr long long kSteep = -(32ll << 32);
+
+// log2 decay of a step in fixed point; `bad` is set for a value above 0 or
+// not a number (read as 0).
+__device__ __forceinline__ long long to_fix(float l, bool &bad) {
+    if (!(l <= 0.0f)) {
+        bad = true;
+        return 0;
+    }
+    return __double2ll_rn(double(fmaxf(l, kFloor)) * (1.4426950408889634 * 4294967296.0));
+}
+
+// 2^x of a fixed-point exponent (accurate exp2f: these factors multiply whole
+// ranges of the state)
+__device__ __forceinline__ float exp2_fix(long long x) { return exp2f(static_cast<float>(x) * kFixInv); }
+
+__device__ __forceinline__ int row_len(const int32_t *lens, int b, int64_t L) {
+    if (lens == nullptr) return static_cast<int>(L);
+    const int n = lens[b];
+    return n < 0 ? 0 : (n > L ? static_cast<int>(L) : n);
+}
+
+}  // namespace dec
+}  // namespace lr

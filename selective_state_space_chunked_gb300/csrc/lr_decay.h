@@ -1,0 +1,57 @@
+// lr_decay.h -- host-side declarations of the decayed linear attention
+// (lr_decay_attn_fwd): the call's arguments, its plan and the two launchers.
+#pragma once
+
+#include "lr_internal.h"
+
+namespace lr {
+
+// One call, as its kernels see it (device pointers; see lr_decay_attn_fwd).
+struct DecayArgs {
+    const void *q, *k, *v;
+    const float *a_log;      // (H) or NULL
+    const void *g;           // (B, L, H) io or NULL
+    const int32_t *lens;     // (B) or NULL
+    const float *S0;         // (B, H, dv, dk) or NULL
+    void *o;
+    float *S_final;          // or NULL
+    int64_t B, L;
+    int H, Hk, dk, dv;
+    float scale;
+    // Time segments: every (batch row, head) is cut into n_seg ranges of
+    // seg_len steps.  With more than one, a first launch leaves the state
+    // that each range but the last builds from its own steps (range 0 from
+    // S0) in seg_state [(b H + h)(n_seg - 1) + s][dv][dk] and its log2 decay,
+    // in units of 2^-32, in seg_tot; the second launch starts every range
+    // from the decayed sum of the ranges before it.
+    int n_seg;
+    int64_t seg_len;
+    float *seg_state;
+    long long *seg_tot;
+};
+
+struct DecayPlan {
+    int path = 0;            // 0: CUDA cores, 1: tensor cores
+    int n_seg = 1;
+    int64_t seg_len = 0;
+    bool narrow = false;     // CUDA cores: few columns per thread (short sequences)
+    size_t ws_bytes = 0;     // status, then seg_tot, then seg_state
+};
+
+int decay_plan(int64_t B, int64_t L, int64_t H, int64_t Hk, int64_t dk, int64_t dv, lr_dtype io, DecayPlan *p);
+int decay_attn_launch(DecayArgs a, lr_dtype io, const DecayPlan &p, void *workspace, cudaStream_t stream);
+
+// CUDA-core kernel, one translation unit per I/O type
+template <typename IO>
+int decay_general_launch(const DecayArgs &a, const DecayPlan &p, StatusRef st, cudaStream_t stream);
+// rows of the state per block of the general kernel
+int decay_general_rows(int64_t dk, bool narrow);
+
+int decay_step_launch(const void *q, const void *k, const void *v, const float *a_log, const void *g,
+                      float scale, const float *S_in, float *S_out, void *o, int64_t B, int64_t H, int64_t Hk,
+                      int64_t dk, int64_t dv, int io_bf16, cudaStream_t stream);
+
+int group_norm_act_launch(const void *x, const void *z, const float *gamma, const float *beta, void *y,
+                          int64_t N, int64_t C, int64_t G, float eps, int act, int io_bf16, cudaStream_t stream);
+
+}  // namespace lr

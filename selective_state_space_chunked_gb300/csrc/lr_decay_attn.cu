@@ -1,0 +1,52 @@
+// lr_decay_attn.cu -- plan and dispatch of the decayed linear attention.
+#include "lr_decay.cuh"
+
+namespace lr {
+
+namespace {
+// CUDA-core kernel: blocks that fill the GPU (three of 64 threads per SM:
+// their staging buffers and state registers), and the shortest segment worth
+// the second pass over k and v.
+constexpr int64_t kGenBlocksPerSm = 3;
+constexpr int64_t kGenMinSeg = 128;
+constexpr int64_t kMaxSeg = 32;
+}  // namespace
+
+int decay_plan(int64_t B, int64_t L, int64_t H, int64_t Hk, int64_t dk, int64_t dv, lr_dtype io, DecayPlan *p) {
+    (void)Hk;
+    (void)io;
+    int sms = 0;
+    if (device_sm_count(&sms) != LR_OK) return LR_ERR_CUDA;
+    p->path = 0;
+    const int64_t want = kGenBlocksPerSm * sms;
+    auto blocks = [&](bool narrow) {
+        const int64_t rows = decay_general_rows(dk, narrow);
+        return B * H * ((dv + rows - 1) / rows);
+    };
+    int64_t n = want / blocks(false);
+    if (n > L / kGenMinSeg) n = L / kGenMinSeg;
+    if (n > kMaxSeg) n = kMaxSeg;
+    if (n < 1) n = 1;
+    p->narrow = n == 1 && blocks(false) < sms;
+    p->seg_len = ((L + n - 1) / n + 15) / 16 * 16;
+    p->n_seg = int((L + p->seg_len - 1) / p->seg_len);
+    // sized for n segments, which does not shrink as L grows, so that a
+    // workspace for L serves every shorter sequence (the host-buffer chunks)
+    const size_t segs = size_t(B) * H * (n - 1);
+    p->ws_bytes = kStatusBytes + (segs * sizeof(long long) + 15) / 16 * 16 + segs * dv * dk * sizeof(float);
+    return LR_OK;
+}
+
+int decay_attn_launch(DecayArgs a, lr_dtype io, const DecayPlan &p, void *workspace, cudaStream_t stream) {
+    unsigned char *ws = static_cast<unsigned char *>(workspace) + kStatusBytes;
+    const size_t segs = size_t(a.B) * a.H * (p.n_seg - 1);
+    a.n_seg = p.n_seg;
+    a.seg_len = p.seg_len;
+    a.seg_tot = reinterpret_cast<long long *>(ws);
+    a.seg_state = reinterpret_cast<float *>(ws + (segs * sizeof(long long) + 15) / 16 * 16);
+    const StatusRef st = call_status(workspace);
+    return io == LR_BF16 ? decay_general_launch<__nv_bfloat16>(a, p, st, stream)
+                         : decay_general_launch<float>(a, p, st, stream);
+}
+
+}  // namespace lr

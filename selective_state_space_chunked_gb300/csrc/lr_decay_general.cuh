@@ -1,0 +1,457 @@
+// lr_decay_general.cuh -- decayed linear attention on the CUDA cores: fp32
+// I/O, head dims the tensor-core kernel does not take, and short sequences.
+//
+//   S_t = a_t S_{t-1} + v_t k_t^T,   o_t = scale S_t q_t,   a_t = exp(l_t)
+//
+// Step by step in fp32.  A block of 64 threads owns RB value rows of one
+// (batch row, head, time segment); a thread owns RT rows and CPT key columns
+// of each, in registers, so P = DKP / CPT consecutive lanes share a row.  The
+// columns come in groups of four dealt round-robin, so the lanes of a row
+// read consecutive 16 bytes of k_t and q_t from shared memory.
+//
+// One decay for the whole state: instead of multiplying S by a_t at every
+// step (a third operation beside the update's and the readout's), the thread
+// keeps S^ = S / A_t, A_t the decay since the last rescale, and takes
+//   S^ += (v_t / A_t) k_t^T,   o_t = scale A_t (S^ q_t),
+// two packed fp32x2 operations per pair of state elements.  After a chunk
+// with A < 2^-16 the state is rescaled.  A chunk that alone decays below
+// 2^-32 (resets included) runs with the multiplication at every step.
+//
+// k, q, v arrive in chunks of TC steps, by TMA where every row start is
+// 16-byte aligned, else element by element, kNB - 1 chunks ahead.
+// The work is 2 dk dv fp32 fused multiply-adds per token and head, which at
+// long sequences is what bounds the kernel; the segments give it the blocks.
+#pragma once
+
+#include "lr_decay.cuh"
+
+namespace lr {
+namespace {
+
+constexpr int kGT = 64;   // threads per block
+constexpr int kGB = 3;    // staging buffers
+
+template <int DKP_, bool NARROW>
+struct DecCfg {
+    static constexpr int DKP = DKP_;
+    static constexpr int CPT = NARROW ? (DKP == 32 ? 8 : 16) : (DKP == 32 ? 16 : 32);
+    static constexpr int RT = NARROW ? 1 : (DKP <= 64 ? 2 : 4);
+    static constexpr int P = DKP / CPT;
+    static constexpr int RB = RT * kGT / P;
+    static constexpr int KB = DKP < 256 ? DKP : 256;   // key columns per TMA box
+    static constexpr int NH = DKP / KB;
+    static constexpr int TC = DKP <= 128 ? 16 : 2048 / DKP;
+    static constexpr int KT = TC * DKP, VT = TC * RB;
+    template <typename IO>
+    __host__ __device__ static constexpr int pitch(int n) {
+        return int((n * sizeof(IO) + 127) / 128 * 128 / sizeof(IO));
+    }
+    template <typename IO>
+    static constexpr size_t smem_bytes() {
+        return sizeof(IO) * size_t(kGB) * (2 * pitch<IO>(KT) + pitch<IO>(VT)) + sizeof(float) * (VT + 8 * TC) +
+               kGB * sizeof(uint64_t) + 128;
+    }
+};
+
+template <typename IO>
+__device__ __forceinline__ float4 dec_ld4(const IO *p);
+template <>
+__device__ __forceinline__ float4 dec_ld4<float>(const float *p) {
+    return *reinterpret_cast<const float4 *>(p);
+}
+template <>
+__device__ __forceinline__ float4 dec_ld4<__nv_bfloat16>(const __nv_bfloat16 *p) {
+    const uint2 u = *reinterpret_cast<const uint2 *>(p);
+    return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u),
+                       __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xffff0000u));
+}
+
+// sums of RT values over the P lanes of a row group: lane p ends with the sum
+// of value p % RT in `r` (for P < RT, with values p, p + P, ...)
+template <int RT, int P>
+__device__ __forceinline__ void row_sums(float (&a)[RT], int p) {
+    if constexpr (RT == 4 && P >= 4) {   // reduce-scatter: 3 shuffles instead of 8
+        const bool b0 = p & 1, b1 = p & 2;
+        float x = b0 ? a[1] : a[0], xs = b0 ? a[0] : a[1];
+        float y = b0 ? a[3] : a[2], ys = b0 ? a[2] : a[3];
+        x += __shfl_xor_sync(0xffffffffu, xs, 1);
+        y += __shfl_xor_sync(0xffffffffu, ys, 1);
+        float w = b1 ? y : x, ws = b1 ? x : y;
+        w += __shfl_xor_sync(0xffffffffu, ws, 2);
+#pragma unroll
+        for (int m = P / 2; m >= 4; m >>= 1) w += __shfl_xor_sync(0xffffffffu, w, m);
+        a[0] = w;   // value p & 3
+    } else {
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+#pragma unroll
+            for (int m = P / 2; m >= 1; m >>= 1) a[i] += __shfl_xor_sync(0xffffffffu, a[i], m);
+        }
+    }
+}
+
+// STATE_ONLY: the first launch of a segmented call (no q, no output; segments
+// 0 .. n_seg - 2).
+template <typename IO, typename C, bool STATE_ONLY>
+__global__ void __launch_bounds__(kGT, C::RT == 4 ? 4 : 6)
+    decay_general_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                         const __grid_constant__ CUtensorMap tm_v, const DecayArgs a, int nrb, bool tma,
+                         uint64_t timeout_ns, StatusRef sref) {
+    constexpr int CPT = C::CPT, RT = C::RT, P = C::P, RB = C::RB, KB = C::KB, TC = C::TC, VT = C::VT;
+    constexpr int KT = C::template pitch<IO>(C::KT), VTP = C::template pitch<IO>(VT);
+    extern __shared__ __align__(128) unsigned char smem[];
+    IO *ks = reinterpret_cast<IO *>(smem);   // [GB][NH][TC][KB] (pitch KT)
+    IO *qs = ks + kGB * KT;
+    IO *vs = qs + kGB * KT;                  // [GB][TC][RB] (pitch VTP)
+    float *os = reinterpret_cast<float *>(vs + kGB * VTP);   // [TC][RB]
+    float *mu = os + VT;                     // [2][TC] readout factors scale A_t
+    float *mw = mu + 2 * TC;                 // [2][TC] 1 / A_t, or a_t of a steep chunk
+    float *mm = mw + 2 * TC;                 // [2][2] factors before and after the chunk
+    uint64_t *full = reinterpret_cast<uint64_t *>(mm + 4 * TC);
+
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int nseg = STATE_ONLY ? a.n_seg - 1 : a.n_seg;
+    int x = blockIdx.x;
+    const int rb = x % nrb;
+    x /= nrb;
+    const int seg = x % nseg, bh = x / nseg;
+    const int b = bh / a.H, h = bh - b * a.H, hk = h / (a.H / a.Hk);
+    if (tid == 0 && blockIdx.x == 0) status_begin(sref);
+    const int p = tid % P, rg = tid / P;
+    const int row0 = rb * RB, dk = a.dk, dv = a.dv;
+    const int rbv = min(RB, dv - row0);
+    const int64_t L = a.L;
+    const int len = dec::row_len(a.lens, b, L);
+    const int64_t s0 = int64_t(seg) * a.seg_len;
+    const int64_t send = min(L, s0 + a.seg_len);             // the segment's end
+    const int nrun = int(max(int64_t(0), min(int64_t(len), send) - s0));   // its steps inside the row
+    const size_t HK = size_t(a.Hk) * dk, HV = size_t(a.H) * dv;
+    const size_t t_base = size_t(b) * L + s0;
+    const IO *kb = static_cast<const IO *>(a.k) + t_base * HK + size_t(hk) * dk;
+    const IO *qb = static_cast<const IO *>(a.q) + t_base * HK + size_t(hk) * dk;
+    const IO *vb = static_cast<const IO *>(a.v) + t_base * HV + size_t(h) * dv + row0;
+    const IO *gb = a.g == nullptr ? nullptr : static_cast<const IO *>(a.g) + t_base * a.H + h;
+    IO *ob = static_cast<IO *>(a.o) + t_base * HV + size_t(h) * dv + row0;
+
+    if (tma) {
+        if (tid == 0) {
+            for (int i = 0; i < kGB; ++i) mbar_init(&full[i], 1);
+            fence_mbar_init();
+        }
+    } else {   // what the element copies never write: columns past dk, rows past dv
+        for (int e = tid; e < kGB * KT; e += kGT) ks[e] = qs[e] = Io<IO>::from_f(0.0f);
+        for (int e = tid; e < kGB * VTP; e += kGT) vs[e] = Io<IO>::from_f(0.0f);
+    }
+
+    const int nchunks = (nrun + TC - 1) / TC;
+    auto stage = [&](int c, int buf) {
+        const int t0 = c * TC;
+        IO *kd = ks + buf * KT, *qd = qs + buf * KT, *vd = vs + buf * VTP;
+        if (tma) {
+            if (tid == 0) {
+                mbar_arrive_expect_tx(&full[buf], uint32_t(sizeof(IO)) * ((STATE_ONLY ? 1 : 2) * C::KT + VT));
+                const int row = int(t_base) + t0;
+#pragma unroll
+                for (int hh = 0; hh < C::NH; ++hh) {
+                    tma_load_3d(kd + hh * TC * KB, &tm_k, &full[buf], hh * KB, hk, row);
+                    if (!STATE_ONLY) tma_load_3d(qd + hh * TC * KB, &tm_q, &full[buf], hh * KB, hk, row);
+                }
+                tma_load_3d(vd, &tm_v, &full[buf], row0, h, row);
+            }
+        } else {
+            const int nt = min(TC, nrun - t0);
+            for (int t = 0; t < nt; ++t) {
+                const size_t sk = size_t(t0 + t) * HK, sv = size_t(t0 + t) * HV;
+                for (int j = tid; j < dk; j += kGT) {
+                    const int at = (j / KB) * TC * KB + t * KB + j % KB;
+                    kd[at] = kb[sk + j];
+                    if (!STATE_ONLY) qd[at] = qb[sk + j];
+                }
+                for (int r = tid; r < rbv; r += kGT) vd[t * RB + r] = vb[sv + r];
+            }
+        }
+    };
+
+    // decay factors of a chunk by warp 0, lane t its step t.  base: log2 decay
+    // since the last rescale; tot: since the segment's start.
+    const float lh = a.a_log == nullptr ? 0.0f : a.a_log[h];
+    long long base = 0, tot = 0;
+    bool bad = false;
+    auto load_g = [&](int c) -> float {
+        const int t = c * TC + lane;
+        return gb != nullptr && lane < TC && t < nrun ? Io<IO>::to_f(gb[size_t(t) * a.H]) : 0.0f;
+    };
+    auto factors = [&](int c, float gv) {   // warp 0
+        const int t = c * TC + lane;
+        const long long own = lane < TC && t < nrun ? dec::to_fix(lh + gv, bad) : 0;
+        long long cum = own;
+#pragma unroll
+        for (int m = 1; m < TC; m <<= 1) {
+            const long long up = __shfl_up_sync(0xffffffffu, cum, m);
+            if (lane >= m) cum += up;
+        }
+        const long long all = __shfl_sync(0xffffffffu, cum, TC - 1);
+        const bool steep = all < dec::kSteep;
+        float *u = mu + (c & 1) * TC, *w = mw + (c & 1) * TC, *m = mm + (c & 1) * 2;
+        if (lane < TC) {
+            u[lane] = a.scale * (steep ? 1.0f : dec::exp2_fix(base + cum));
+            w[lane] = steep ? dec::exp2_fix(own) : dec::exp2_fix(-(base + cum));
+        }
+        if (steep) {
+            if (lane == 0) {
+                m[0] = dec::exp2_fix(base);
+                m[1] = -1.0f;   // marks a steep chunk
+            }
+            base = 0;
+        } else {
+            base += all;
+            const bool re = base < dec::kRescale;
+            if (lane == 0) {
+                m[0] = 1.0f;
+                m[1] = re ? dec::exp2_fix(base) : 1.0f;
+            }
+            if (re) base = 0;
+        }
+        tot = max(tot + all, -(1ll << 60));
+    };
+
+    // S[rr][2m + e] holds columns 4 (m P + p) + 2e + {0, 1} of row row0 + rg RT + rr
+    float2 S[RT][CPT / 2];
+    if (!STATE_ONLY && seg > 0) grid_dependency_wait();   // the first launch's states
+#pragma unroll
+    for (int rr = 0; rr < RT; ++rr) {
+        const int i = row0 + rg * RT + rr;
+        const float *src = seg > 0 ? nullptr : a.S0;
+#pragma unroll
+        for (int m2 = 0; m2 < CPT / 2; ++m2) {
+            const int j = 4 * ((m2 >> 1) * P + p) + 2 * (m2 & 1);
+            float2 s = make_float2(0.0f, 0.0f);
+            if (src != nullptr && i < dv) {
+                const float *r = src + (size_t(bh) * dv + i) * dk;
+                if (j < dk) s.x = r[j];
+                if (j + 1 < dk) s.y = r[j + 1];
+            }
+            S[rr][m2] = s;
+        }
+    }
+    if (!STATE_ONLY && seg > 0) {   // the decayed sum of the ranges before this one
+        long long acc = 0;
+        for (int s = seg - 1; s >= 0; --s) {
+            const float f = dec::exp2_fix(acc);
+            if (f == 0.0f) break;
+            const size_t at = size_t(bh) * (a.n_seg - 1) + s;
+#pragma unroll
+            for (int rr = 0; rr < RT; ++rr) {
+                const int i = row0 + rg * RT + rr;
+                if (i >= dv) continue;
+                const float *r = a.seg_state + (at * dv + i) * dk;
+#pragma unroll
+                for (int m2 = 0; m2 < CPT / 2; ++m2) {
+                    const int j = 4 * ((m2 >> 1) * P + p) + 2 * (m2 & 1);
+                    if (j < dk) S[rr][m2].x = fmaf(f, r[j], S[rr][m2].x);
+                    if (j + 1 < dk) S[rr][m2].y = fmaf(f, r[j + 1], S[rr][m2].y);
+                }
+            }
+            acc = max(acc + a.seg_tot[at], -(1ll << 60));
+        }
+    }
+    if (STATE_ONLY) launch_dependents();
+
+    if (tid < 32 && nchunks > 0) factors(0, load_g(0));
+    __syncthreads();   // barriers initialised or buffers cleared, factors of chunk 0
+    for (int c = 0; c < kGB - 1 && c < nchunks; ++c) stage(c, c);
+    if (!tma) __syncthreads();
+    for (int c = 0; c < nchunks; ++c) {
+        const int buf = c % kGB;
+        const bool more = c + 1 < nchunks;
+        float gn = 0.0f;
+        if (tid < 32 && more) gn = load_g(c + 1);
+        if (c + kGB - 1 < nchunks) stage(c + kGB - 1, (c + kGB - 1) % kGB);
+        const bool ok = !tma || mbar_wait_bounded(&full[buf], (c / kGB) & 1, timeout_ns);
+        if (__syncthreads_or(!ok)) {
+            if (tid == 0) {
+                status_report(sref, LR_ERR_TIMEOUT);
+                for (int c2 = c + 1; c2 < c + kGB && c2 < nchunks; ++c2)
+                    mbar_wait_bounded(&full[c2 % kGB], (c2 / kGB) & 1, timeout_ns);
+            }
+            break;
+        }
+        const int nt = min(TC, nrun - c * TC);
+        const float *u = mu + (c & 1) * TC, *w = mw + (c & 1) * TC, *mf = mm + (c & 1) * 2;
+        const float after = mf[1];
+        const bool steep = after < 0.0f;
+        if (steep) {
+            const float f = mf[0];
+#pragma unroll
+            for (int rr = 0; rr < RT; ++rr)
+#pragma unroll
+                for (int m = 0; m < CPT / 2; ++m) S[rr][m] = __fmul2_rn(S[rr][m], make_float2(f, f));
+        }
+        const IO *vr = vs + buf * VTP + rg * RT;
+        for (int t = 0; t < nt; ++t) {
+            const IO *kr = ks + buf * KT + t * KB + 4 * p, *qr = qs + buf * KT + t * KB + 4 * p;
+            const float wt = w[t];
+            if (steep) {
+                const float2 a2 = make_float2(wt, wt);
+#pragma unroll
+                for (int rr = 0; rr < RT; ++rr)
+#pragma unroll
+                    for (int m = 0; m < CPT / 2; ++m) S[rr][m] = __fmul2_rn(S[rr][m], a2);
+            }
+            const float vw = steep ? 1.0f : wt;
+            float2 v2[RT], acc[RT][2];
+#pragma unroll
+            for (int rr = 0; rr < RT; ++rr) {
+                const float vv = vw * Io<IO>::to_f(vr[t * RB + rr]);
+                v2[rr] = make_float2(vv, vv);
+                acc[rr][0] = acc[rr][1] = make_float2(0.0f, 0.0f);
+            }
+#pragma unroll
+            for (int m = 0; m < CPT / 4; ++m) {
+                const int off = ((4 * P * m) / KB) * TC * KB + (4 * P * m) % KB;
+                const float4 k4 = dec_ld4<IO>(kr + off);
+                const float2 k01 = make_float2(k4.x, k4.y), k23 = make_float2(k4.z, k4.w);
+                float4 q4 = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                if (!STATE_ONLY) q4 = dec_ld4<IO>(qr + off);
+                const float2 q01 = make_float2(q4.x, q4.y), q23 = make_float2(q4.z, q4.w);
+#pragma unroll
+                for (int rr = 0; rr < RT; ++rr) {
+                    S[rr][2 * m] = __ffma2_rn(v2[rr], k01, S[rr][2 * m]);
+                    S[rr][2 * m + 1] = __ffma2_rn(v2[rr], k23, S[rr][2 * m + 1]);
+                    if (!STATE_ONLY) {
+                        acc[rr][0] = __ffma2_rn(S[rr][2 * m], q01, acc[rr][0]);
+                        acc[rr][1] = __ffma2_rn(S[rr][2 * m + 1], q23, acc[rr][1]);
+                    }
+                }
+            }
+            if (!STATE_ONLY) {
+                float r[RT];
+#pragma unroll
+                for (int rr = 0; rr < RT; ++rr)
+                    r[rr] = (acc[rr][0].x + acc[rr][0].y) + (acc[rr][1].x + acc[rr][1].y);
+                row_sums<RT, P>(r, p);
+                const float ut = u[t];
+                if constexpr (RT == 4 && P >= 4) {
+                    if (p < 4) os[t * RB + rg * RT + p] = ut * r[0];
+                } else {
+#pragma unroll
+                    for (int rr = 0; rr < RT; ++rr)
+                        if (p == rr % P) os[t * RB + rg * RT + rr] = ut * r[rr];
+                }
+            }
+        }
+        if (!steep && after != 1.0f) {
+#pragma unroll
+            for (int rr = 0; rr < RT; ++rr)
+#pragma unroll
+                for (int m = 0; m < CPT / 2; ++m) S[rr][m] = __fmul2_rn(S[rr][m], make_float2(after, after));
+        }
+        if (tid < 32 && more) factors(c + 1, gn);   // its buffer was last read in chunk c - 1
+        __syncthreads();   // chunk c's buffer, every os entry, the next factors
+        if (!STATE_ONLY) {
+            for (int e = tid; e < TC * RB; e += kGT) {
+                const int t = e / RB, r = e % RB;
+                if (t < nt && r < rbv) ob[size_t(c * TC + t) * HV + r] = Io<IO>::from_f(os[e]);
+            }
+        }
+    }
+
+    if (tid < 32 && bad) status_report(sref, LR_ERR_RANGE);
+    // steps of the segment past the row's length
+    if (!STATE_ONLY) {
+        const int64_t nseg_steps = send - s0;
+        for (int64_t e = int64_t(nrun) * RB + tid; e < nseg_steps * RB; e += kGT) {
+            const int64_t t = e / RB;
+            const int r = int(e % RB);
+            if (r < rbv) ob[size_t(t) * HV + r] = Io<IO>::from_f(0.0f);
+        }
+    }
+    // the state as it stands is S / 2^base
+    float *dst0 = nullptr;
+    if (STATE_ONLY)
+        dst0 = a.seg_state + (size_t(bh) * (a.n_seg - 1) + seg) * dv * dk;
+    else if (seg == a.n_seg - 1 && a.S_final != nullptr)
+        dst0 = a.S_final + size_t(bh) * dv * dk;
+    if (STATE_ONLY && rb == 0 && tid == 0) a.seg_tot[size_t(bh) * (a.n_seg - 1) + seg] = tot;
+    if (dst0 != nullptr) {
+        if (tid == 0) mm[0] = dec::exp2_fix(base);   // warp 0 holds base
+        __syncthreads();
+        const float f = mm[0];
+#pragma unroll
+        for (int rr = 0; rr < RT; ++rr) {
+            const int i = row0 + rg * RT + rr;
+            if (i >= dv) continue;
+            float *dst = dst0 + size_t(i) * dk;
+#pragma unroll
+            for (int m2 = 0; m2 < CPT / 2; ++m2) {
+                const int j = 4 * ((m2 >> 1) * P + p) + 2 * (m2 & 1);
+                if (j < dk) dst[j] = f * S[rr][m2].x;
+                if (j + 1 < dk) dst[j + 1] = f * S[rr][m2].y;
+            }
+        }
+    }
+}
+
+template <typename IO, typename C>
+int launch_general_cfg(const DecayArgs &a, StatusRef st, cudaStream_t stream) {
+    const int nrb = (a.dv + C::RB - 1) / C::RB;
+    const size_t es = sizeof(IO);
+    auto al = [](const void *x) { return (reinterpret_cast<uintptr_t>(x) & 15u) == 0; };
+    // tensor copies need 16-byte row starts and strides and 32-bit row coordinates
+    bool tma = (a.dk * es) % 16 == 0 && (a.dv * es) % 16 == 0 && (C::RB * es) % 16 == 0 && al(a.q) && al(a.k) &&
+               al(a.v) && a.B * a.L <= INT32_MAX;
+    CUtensorMap mq{}, mk{}, mv{};
+    if (tma) {
+        const auto tt = Io<IO>::kTmType;
+        const uint64_t rows = uint64_t(a.B) * a.L;
+        tma = encode_map_3d(&mq, a.q, tt, es, a.dk, a.Hk, rows, C::KB, 1, C::TC) &&
+              encode_map_3d(&mk, a.k, tt, es, a.dk, a.Hk, rows, C::KB, 1, C::TC) &&
+              encode_map_3d(&mv, a.v, tt, es, a.dv, a.H, rows, C::RB, 1, C::TC);
+    }
+    const size_t smem = C::template smem_bytes<IO>();
+    auto first = decay_general_kernel<IO, C, true>;
+    auto main = decay_general_kernel<IO, C, false>;
+    if (smem > 48 * 1024 &&
+        (cudaFuncSetAttribute(first, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)) != cudaSuccess ||
+         cudaFuncSetAttribute(main, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)) != cudaSuccess))
+        return LR_ERR_CUDA;
+    const int64_t per_seg = a.B * a.H * nrb;
+    if (per_seg * a.n_seg > INT32_MAX) return LR_ERR_UNSUPPORTED;
+    if (a.n_seg > 1) {
+        first<<<unsigned(per_seg * (a.n_seg - 1)), kGT, smem, stream>>>(mq, mk, mv, a, nrb, tma, kDefaultTimeoutNs,
+                                                                        st);
+        if (cudaGetLastError() != cudaSuccess) return LR_ERR_CUDA;
+    }
+    // dependent launch: segment 0 needs nothing of the first launch
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(per_seg * a.n_seg));
+    cfg.blockDim = dim3(kGT);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = a.n_seg > 1 ? 1 : 0;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, main, mq, mk, mv, a, nrb, tma, uint64_t(kDefaultTimeoutNs), st);
+    return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? LR_OK : LR_ERR_CUDA;
+}
+
+template <typename IO, int DKP>
+int launch_general_dk(const DecayArgs &a, bool narrow, StatusRef st, cudaStream_t stream) {
+    return narrow ? launch_general_cfg<IO, DecCfg<DKP, true>>(a, st, stream)
+                  : launch_general_cfg<IO, DecCfg<DKP, false>>(a, st, stream);
+}
+
+}  // namespace
+
+template <typename IO>
+int decay_general_launch(const DecayArgs &a, const DecayPlan &p, StatusRef st, cudaStream_t stream) {
+    if (a.dk <= 32) return launch_general_dk<IO, 32>(a, p.narrow, st, stream);
+    if (a.dk <= 64) return launch_general_dk<IO, 64>(a, p.narrow, st, stream);
+    if (a.dk <= 128) return launch_general_dk<IO, 128>(a, p.narrow, st, stream);
+    if (a.dk <= 256) return launch_general_dk<IO, 256>(a, p.narrow, st, stream);
+    return launch_general_dk<IO, 512>(a, p.narrow, st, stream);
+}
+
+}  // namespace lr

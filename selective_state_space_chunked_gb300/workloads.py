@@ -18,6 +18,10 @@ Distributions follow the source pages' layer definitions:
 * HGRN2 (HGRN2 Attention page): q, k, v ~ N(0, variance 1/128); forget
   pre-activation f ~ N(2, 1); ``g = lb + (1 - lb) * sigmoid(f)``, lb = 0.2.
 
+* Linear attention with a decay for each head: q, k ~ N(0, 1/dk), v ~ N(0, 1/dv);
+  per-head decays 1 - 2^-(5 .. 12) (``a_log``), per-step gates log sigmoid(f)
+  with f ~ N(3, 1) (``g``).
+
 Every tensor is drawn from one ``torch.Generator`` seeded with the config's
 seed, in the fixed order written in each function.  Generation runs on the
 requested device (CPU for oracle-sized cases; the GPU generator for the
@@ -33,7 +37,7 @@ import torch
 
 __all__ = [
     "WORKLOADS", "Config", "multiscale_A_log", "rglru_inputs",
-    "selective_inputs", "hgrn2_inputs", "make_inputs",
+    "selective_inputs", "hgrn2_inputs", "decay_attn_inputs", "make_inputs",
 ]
 
 
@@ -185,6 +189,29 @@ def hgrn2_inputs(B: int, L: int, H: int, head_dim: int, seed: int,
         "g": gate.to(dt).contiguous(),
         "S0": S0,
         "H": H,
+    }
+
+
+def decay_attn_inputs(B: int, L: int, H: int, dk: int, dv: int, seed: int, io: str = "bf16",
+                      Hk: Optional[int] = None, decay: str = "both", with_S0: bool = False,
+                      device="cpu") -> dict:
+    """Inputs of the linear attention with a decay for each head.  ``decay``:
+    "head" (a_log only), "token" (g only), "both" or "none".  Draw order: q, k
+    (B, L, Hk*dk), v (B, L, H*dv), f (B, L, H), then S0 when requested."""
+    gen = _gen(seed, device)
+    Hk = H if Hk is None else Hk
+    q = torch.randn(B, L, Hk * dk, generator=gen, device=device) / math.sqrt(dk)
+    k = torch.randn(B, L, Hk * dk, generator=gen, device=device) / math.sqrt(dk)
+    v = torch.randn(B, L, H * dv, generator=gen, device=device) / math.sqrt(dv)
+    f = 3.0 + torch.randn(B, L, H, generator=gen, device=device)
+    S0 = 0.1 * torch.randn(B, H, dv, dk, generator=gen, device=device) if with_S0 else None
+    dt = _dtype(io)
+    a = 1.0 - 2.0 ** -(5.0 + 7.0 * torch.arange(H, dtype=torch.float32, device=device) / H)
+    return {
+        "q": q.to(dt).contiguous(), "k": k.to(dt).contiguous(), "v": v.to(dt).contiguous(),
+        "a_log": torch.log(a).contiguous() if decay in ("head", "both") else None,
+        "g": torch.log(torch.sigmoid(f)).to(dt).contiguous() if decay in ("token", "both") else None,
+        "S0": S0, "H": H, "Hk": Hk,
     }
 
 
