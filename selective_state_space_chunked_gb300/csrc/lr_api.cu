@@ -777,8 +777,10 @@ lr::HostJob da_host_job(const DaHost &a, int64_t L, const void *q, const void *k
     j.state_final = S_final;
     j.state_bytes = size_t(a.B) * a.H * a.dv * a.dk * sizeof(float);
     j.Lc = lr::host_chunk_steps(a.B, L, j.es * size_t(2 * a.Hk * a.dk + a.H * a.dv + a.H));
-    j.kernel_ws = lr_decay_attn_workspace_size(a.B, j.Lc, a.H, a.Hk, a.dk, a.dv, a.io);
-    // (also serves a shorter last chunk: the size does not shrink with L)
+    // the last chunk may be shorter, and its plan may ask for more segments
+    const size_t ws_full = lr_decay_attn_workspace_size(a.B, j.Lc, a.H, a.Hk, a.dk, a.dv, a.io);
+    const size_t ws_last = lr_decay_attn_workspace_size(a.B, L % j.Lc, a.H, a.Hk, a.dk, a.dv, a.io);
+    j.kernel_ws = ws_full > ws_last ? ws_full : ws_last;
     j.launch = da_host_chunk;
     j.ctx = &a;
     return j;

@@ -13,8 +13,8 @@ namespace lr {
 namespace dec {
 
 constexpr float kFixInv = 2.3283064365386963e-10f;   // 2^-32
-// a step's floor: exp(-1024) is 0 in fp32, so this is a reset
-constexpr float kFloor = -1024.0f;
+// a step's floor: exp(-139) = 2^-200 is 0 in fp32, so this is a reset
+constexpr float kFloor = -139.0f;
 // The running state is kept divided by the decay since the last rescale, and
 // rescaled once that decay falls below 2^-16.  Rescaling rarely matters for
 // accuracy: a factor that is rounded once per chunk, and the same way every

@@ -44,6 +44,10 @@ int decay_attn_launch(DecayArgs a, lr_dtype io, const DecayPlan &p, void *worksp
 // CUDA-core kernel, one translation unit per I/O type
 template <typename IO>
 int decay_general_launch(const DecayArgs &a, const DecayPlan &p, StatusRef st, cudaStream_t stream);
+// tensor-core kernel: bf16 I/O, dk <= 128, dk and dv multiples of 8
+int decay_tensor_launch(const DecayArgs &a, StatusRef st, cudaStream_t stream);
+constexpr int kDecayChunk = 128;    // its steps per chunk (segments are multiples of it)
+constexpr int kDecayRows = 64;      // its value rows per block
 // rows of the state per block of the general kernel
 int decay_general_rows(int64_t dk, bool narrow);
 
