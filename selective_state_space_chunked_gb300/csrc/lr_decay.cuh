@@ -26,18 +26,35 @@ constexpr long long kRescale = -(16ll << 32);
 constexpr long long kSteep = -(32ll << 32);
 
 // log2 decay of a step in fixed point; `bad` is set for a value above 0 or
-// not a number (read as 0).
+// not a number (read as 0).  The product with log2(e) is formed as a sum of two
+// floats (its rounding error is exact by fma) and converted in two 16-bit
+// steps: fp64 arithmetic, at 1/64 of the fp32 rate, made this the slowest
+// link of the tensor-core kernel.
 __device__ __forceinline__ long long to_fix(float l, bool &bad) {
     if (!(l <= 0.0f)) {
         bad = true;
         return 0;
     }
-    return __double2ll_rn(double(fmaxf(l, kFloor)) * (1.4426950408889634 * 4294967296.0));
+    constexpr float kHi = 1.44269504f, kLo = 1.92596299e-8f;   // log2(e) = kHi + kLo
+    l = fmaxf(l, kFloor);
+    const float p = l * kHi, r = fmaf(l, kLo, fmaf(l, kHi, -p));
+    const int i1 = __float2int_rn(p * 65536.0f);                   // units of 2^-16, below 2^24
+    const int i2 = __float2int_rn(fmaf(r, 4294967296.0f, (p * 65536.0f - float(i1)) * 65536.0f));
+    return (static_cast<long long>(i1) << 16) + i2;
 }
 
-// 2^x of a fixed-point exponent (accurate exp2f: these factors multiply whole
-// ranges of the state)
-__device__ __forceinline__ float exp2_fix(long long x) { return exp2f(static_cast<float>(x) * kFixInv); }
+// A fixed-point exponent as a float.
+__device__ __forceinline__ float fix_f(long long x) {
+    return fmaf(static_cast<float>(static_cast<uint32_t>(x)), kFixInv, static_cast<float>(static_cast<int>(x >> 32)));
+}
+
+// 2^x of a fixed-point exponent, for x below 127: 2^fraction times 2^integer,
+// so the result is as exact for large exponents as for small ones (these
+// factors multiply whole ranges of the state); 0 below 2^-126.
+__device__ __forceinline__ float exp2_fix(long long x) {
+    const int n = static_cast<int>(max(x >> 32, -127ll));
+    return ex2_approx(static_cast<float>(static_cast<uint32_t>(x)) * kFixInv) * __int_as_float((n + 127) << 23);
+}
 
 __device__ __forceinline__ int row_len(const int32_t *lens, int b, int64_t L) {
     if (lens == nullptr) return static_cast<int>(L);

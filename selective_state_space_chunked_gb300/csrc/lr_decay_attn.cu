@@ -10,9 +10,11 @@ namespace {
 constexpr int64_t kGenBlocksPerSm = 3;
 constexpr int64_t kGenMinSeg = 128;
 constexpr int64_t kMaxSeg = 32;
-// tensor-core kernel: the shortest sequence it takes, and its segments' costs
+// Tensor-core kernel: the shortest sequence it takes, and costs in units of a
+// chunk's time: a chunk of the first launch, a block's start, and one
+// segment's state read by a later one.
 constexpr int64_t kTensorMinLen = 64;
-constexpr double kFirstCost = 0.6, kSplitCost = 4.0;
+constexpr double kFirstCost = 0.6, kBlockCost = 3.0, kStateCost = 0.5;
 }  // namespace
 
 int decay_plan(int64_t B, int64_t L, int64_t H, int64_t Hk, int64_t dk, int64_t dv, lr_dtype io, DecayPlan *p) {
@@ -23,15 +25,16 @@ int decay_plan(int64_t B, int64_t L, int64_t H, int64_t Hk, int64_t dk, int64_t 
     p->narrow = false;
     p->path = io == LR_BF16 && dk <= 128 && dk % 8 == 0 && dv % 8 == 0 && L >= kTensorMinLen;
     if (p->path == 1) {
-        // one block per SM; the first launch costs kFirstCost of the second's
-        // time per chunk, and a second launch kSplitCost chunks
+        // one block per SM: waves of blocks, each as long as its chunks and a
+        // block's start
         unit = kDecayChunk;
         const int64_t chunks = (L + unit - 1) / unit, blocks = B * H * ((dv + kDecayRows - 1) / kDecayRows);
         auto waves = [&](int64_t b) { return double((b + sms - 1) / sms); };
-        double best = waves(blocks) * double(chunks);
+        double best = waves(blocks) * (double(chunks) + kBlockCost);
         for (int64_t s = 2; s <= kMaxSeg && 2 * s <= chunks; ++s) {
             const double per = double((chunks + s - 1) / s);
-            const double t = per * (waves(blocks * s) + kFirstCost * waves(blocks * (s - 1))) + kSplitCost;
+            const double t = waves(blocks * s) * (per + kBlockCost + kStateCost * double(s)) +
+                             waves(blocks * (s - 1)) * (kFirstCost * per + kBlockCost);
             if (t < best) best = t, n = s;
         }
     } else {

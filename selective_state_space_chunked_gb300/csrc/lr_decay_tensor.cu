@@ -10,32 +10,48 @@
 //   O  = scale ( [(Q K^T) . D] V + diag(2^L) Q S^T ),   D_ts = 2^(L_t - L_s), s <= t
 //   S' = 2^L_C S + sum_s 2^(L_C - L_s) v_s k_s^T
 //
-// Every D_ts <= 1 and is formed from the difference itself: no reference
-// point, no range limit, resets included.
+// A chunk that decays by less than 2^-40 in all takes D as a product: the
+// columns of Q K^T are multiplied by the same w_s that weigh the state's
+// update and the rows of the result by 2^L_t / (their common factor), one
+// multiplication an element.  A steeper chunk (resets included) forms each
+// D_ts <= 1 from its difference, so there is no range limit.
 //
 // Precision.  D . (Q K^T) and the copy of S that Q S^T reads are rounded to
 // bf16 once (matrix operands; o is rounded to bf16 anyway).  The carried state
 // is not: w_s v_s (w_s the decay weight, fp32) is split into three bf16 terms
 // (24 bits), which sit side by side as one N = 192 operand, so that K is read
-// once for the three; their sum is added to the fp32 state.  The state is kept
-// as S^ = S / (decay since the last rescale): w_s = 2^(-L_s) and no
-// multiplication of S while that decay is above 2^-16; the chunk that takes
-// it below uses w_s = 2^(L_C - L_s) and multiplies S once.
+// once for the three, and accumulate in fp32.  The state is kept as S^ = S /
+// (decay since the last rescale): w_s = 2^(-L_s) and no multiplication of S
+// while that decay is above 2^-48; the chunk that takes it below uses
+// w_s = 2^(L_C - L_s) and multiplies S once.  Scores and state carry the same
+// factor, so Q S^T and PD V meet in one accumulator and o_t takes 1 / w_t.
 //
 // A thread block owns 64 value rows of one (batch row, head, time segment),
 // 128 key columns.  Roles, connected by mbarriers:
-//   TMA warp   Q, K, V two chunks deep, released separately (K first: it is
-//              not needed once dS is done)
-//   scan warp  log decays of the next chunk -> L (fp32), w, the chunk's factors
-//   weight (4) w_s v_s in three terms; rows past the end of the row zeroed
-//   MMA warp   dS = K^T [W1 W2 W3]  M=128 N=192   (independent of the state)
-//              P  = Q K^T           M=128 N=128   one chunk ahead
-//              OI = PD V            M=128 N=64    PD from TMEM
-//   front (4)  PD = bf16(D . P), in place in P's first 64 columns
-//   OX warp    OX = Q S^T           M=128 N=64    into P's other 64 columns
-//   back (4)   S = m S + dS (fp32, thread j holds key column j of the 64
-//              rows), its bf16 copy, then the outputs
-// TMEM: P 2 x 128 columns (PD and OX inside), OI 64, dS 192: all 512.
+//   TMA warps    Q, K, V two chunks deep, one warp each: they are released at
+//                different points of a chunk
+//   scan warp    log decays -> w (and L where the chunk is steep) and the
+//                chunk's factors, up to four chunks ahead
+//   weight (4)   w_s v_s in three terms, 32 steps a warp, each quarter handed
+//                over by itself; rows past the end of the row zeroed
+//   dS warp      dS = K^T [W1 W2 W3]   M=128 N=192
+//   O warp       O  = Q S^T            M=128 N=64
+//                O += PD V             M=128 N=64, PD from TMEM
+//   P warp       P  = Q K^T            M=128 N=128, one chunk ahead
+//                (a whole warp runs each issue loop, one elected lane issues:
+//                in code that only one lane reaches, the operands' moves to
+//                uniform registers made the issue the bottleneck)
+//   front (8)    PD = bf16(D . P) in place, 64 columns a warp
+//   state (8)    S = m S + dS (fp32, in registers: a thread holds 32 value rows of
+//                one key column), its bf16 copy for the next Q S^T.  dS is
+//                released as soon as it is read, so the next chunk's dS waits
+//                for nothing else of the state's
+//   output (4)   o = scale / w O (a steep chunk's Q S^T is scaled by rows before
+//                PD V is added)
+// TMEM: P 2 x 128 columns (PD inside), O 64, dS 3 x 64: all 512.
+// Loops over columns stay rolled and waits share one slow path: with every
+// role's code unrolled the warps waited for instruction fetches more than for
+// anything else.
 #include <cudaTypedefs.h>
 
 #include <mutex>
@@ -47,30 +63,49 @@ namespace lr {
 namespace dt {
 constexpr int C = kDecayChunk;
 constexpr int RB = kDecayRows;
-constexpr int FRONT = 4, WEIGHT = 8, TMA_WARP = 12, MMA_WARP = 13, OX_WARP = 14, SCAN_WARP = 15;
-constexpr int THREADS = 16 * 32;
+constexpr int OUT = 8, FRONT = 12, WEIGHT = 20, K_WARP = 24, Q_WARP = 25, V_WARP = 26, DS_WARP = 27, P_WARP = 28,
+              O_WARP = 29, SCAN_WARP = 30;
+constexpr int THREADS = 31 * 32;
+// the state is rescaled past this decay (log2)
+constexpr long long kRescaleTensor = -(48ll << 32);
+// decay of a chunk (log2) past which D is formed from differences
+constexpr long long kSteepChunk = -(40ll << 32);
 
 constexpr uint32_t HALF = C * 128;              // 64 columns of Q or K: 128 rows of 128 bytes
 constexpr uint32_t Q_BYTES = 2 * HALF, V_BYTES = C * RB * 2;
 constexpr uint32_t OFF_Q = 0, OFF_K = 2 * Q_BYTES, OFF_V = 4 * Q_BYTES;
 constexpr uint32_t OFF_W = OFF_V + 2 * V_BYTES;     // three terms [128 s][64 i]
 constexpr uint32_t OFF_SB = OFF_W + 3 * V_BYTES;    // bf16 state [128 j][64 i]
-constexpr uint32_t OFF_L = OFF_SB + 128 * RB * 2;   // 2 x L [128] fp32
-constexpr uint32_t OFF_WT = OFF_L + 2 * C * 4;      // 2 x w [128] fp32
-constexpr uint32_t OFF_F = OFF_WT + 2 * C * 4;      // 2 x (m, base as log2)
-constexpr uint32_t OFF_BAR = OFF_F + 2 * 8;
-// barriers
+constexpr int NM = 4;                               // chunks whose factors are held
+constexpr uint32_t OFF_WT = OFF_SB + 128 * RB * 2;  // NM x [128] fp32: w
+constexpr uint32_t OFF_L = OFF_WT + NM * C * 4;     // [128] fp32: L of the last steep chunk
+// NM x (m: the state's factor, steep: the readout's base, 0 in a steep chunk, -)
+constexpr uint32_t OFF_F = OFF_L + C * 4;
+constexpr uint32_t OFF_BAR = OFF_F + NM * 16;
+// barriers; [2] by chunk parity, [4] by quarter
 enum {
-    FULL_Q = 0, EMPTY_Q = 2, FULL_K = 4, EMPTY_K = 6, FULL_V = 8, EMPTY_V = 10, P_READY = 12, F_DONE = 14,
-    K_DONE = 16, M_READY = 18, OI_DONE = 20, OX_DONE, SB_READY, DS_DONE, DS_FREE, W_READY, MMA_END, NBAR
+    FULL_Q = 0, EMPTY_Q = 2, FULL_K = 4, EMPTY_K = 6, FULL_V = 8, EMPTY_V = 10,
+    P_READY = 12,    // P_c complete
+    F_DONE = 14,     // PD_c written (8 front warps)
+    K_DONE = 16,     // chunk c's outputs read (4 output warps)
+    OX_DONE = 18,    // Q S^T complete: the bf16 state has been read
+    O_DONE = 20,
+    W_READY = 22,    // weighted values of a quarter
+    W_FREE = 26,
+    M_READY = 30,    // decay factors of chunk c, [NM]
+    M_FREE = 34,     // taken by the 4 weight, 4 output (or 8 state) warps, [NM]
+    SB_READY = 38,   // bf16 state before chunk c (8 state warps)
+    DS_DONE, DS_FREE,
+    FIX,             // a steep chunk's Q S^T scaled (4 output warps)
+    MMA_END, NBAR
 };
 constexpr uint32_t OFF_TMEM = OFF_BAR + NBAR * 8;
 constexpr uint32_t OFF_END = OFF_TMEM + 4;
-constexpr uint32_t OFF_FLAG = OFF_TMEM + 8;
-constexpr uint32_t SMEM = OFF_FLAG + 8;
+constexpr uint32_t OFF_CTL = OFF_TMEM + 8;
+constexpr uint32_t SMEM = OFF_CTL + 32;
 static_assert(SMEM <= 227 * 1024, "one block per SM");
 
-constexpr uint32_t T_P = 0, T_OI = 256, T_DS = 320;
+constexpr uint32_t T_P = 0, T_O = 256, T_DS = 320;
 constexpr uint32_t IDESC_P = umma_idesc_bf16(128, 128, 0, 0);
 constexpr uint32_t IDESC_O = umma_idesc_bf16(128, 64, 0, 1);
 constexpr uint32_t IDESC_DS = umma_idesc_bf16(128, 192, 1, 1);
@@ -82,23 +117,49 @@ __device__ __forceinline__ uint32_t pack(float a, float b) {
     const __nv_bfloat162 p = __floats2bfloat162_rn(a, b);
     return *reinterpret_cast<const uint32_t *>(&p);
 }
+// One lane of a converged warp, the same at every call.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
 __device__ __forceinline__ float lo_f(uint32_t u) { return __uint_as_float(u << 16); }
 __device__ __forceinline__ float hi_f(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
 
-// Bounded wait; the first to run out makes every role leave its loop.
-__device__ __forceinline__ bool wait_or_abort(uint64_t *bar, uint32_t parity, volatile int *abort_flag,
-                                              uint64_t timeout_ns, StatusRef sref) {
-    if (mbar_try_wait(bar, parity)) return true;
-    const uint64_t t0 = globaltimer_ns();
-    while (!mbar_try_wait(bar, parity)) {
-        if (*abort_flag != 0) return false;
-        if (globaltimer_ns() - t0 > timeout_ns) {
-            *abort_flag = 1;
-            status_report(sref, LR_ERR_TIMEOUT);
+// What a wait that does not succeed at once needs, in shared memory.
+struct Ctl {
+    unsigned long long *word;
+    unsigned long long stamp;
+    uint64_t timeout_ns;
+    int abort_flag;
+};
+static_assert(sizeof(Ctl) <= 32, "");
+
+// The slow path of every wait (one copy of the code): bounded; the first to
+// run out makes every role leave its loop.
+__device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, Ctl *ctl) {
+    uint64_t t0 = 0;
+    for (uint32_t n = 1;; ++n) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity)
+            : "memory");
+        if (ok) return true;
+        if ((n & 15) != 0) continue;
+        // reading the timer is slow: every 16th try
+        if (*reinterpret_cast<volatile int *>(&ctl->abort_flag) != 0) return false;
+        const uint64_t now = globaltimer_ns();
+        if (t0 == 0) t0 = now;
+        if (now - t0 > ctl->timeout_ns) {
+            *reinterpret_cast<volatile int *>(&ctl->abort_flag) = 1;
+            status_report(StatusRef{ctl->word, ctl->stamp}, LR_ERR_TIMEOUT);
             return false;
         }
     }
-    return true;
 }
 }  // namespace dt
 
@@ -134,15 +195,25 @@ __global__ void __launch_bounds__(dt::THREADS, 1)
 
     uint64_t *bar = reinterpret_cast<uint64_t *>(sm + OFF_BAR);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + OFF_TMEM);
-    volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + OFF_FLAG);
-    float *sL = reinterpret_cast<float *>(sm + OFF_L), *sW = reinterpret_cast<float *>(sm + OFF_WT),
+    Ctl *ctl = reinterpret_cast<Ctl *>(sm + OFF_CTL);
+    float *sW = reinterpret_cast<float *>(sm + OFF_WT), *sL = reinterpret_cast<float *>(sm + OFF_L),
           *sF = reinterpret_cast<float *>(sm + OFF_F);
     if (tid == 0) {
         for (int i = 0; i < NBAR; ++i) {
-            const bool four = (i >= F_DONE && i < M_READY) || i == SB_READY || i == DS_FREE || i == W_READY;
-            mbar_init(&bar[i], four ? 4 : i == MMA_END ? 2 : 1);
+            int n = 1;
+            if (i >= F_DONE && i < F_DONE + 2) n = 8;
+            if (i >= K_DONE && i < K_DONE + 2) n = 4;
+            if (i >= M_FREE && i < M_FREE + NM) n = STATE_ONLY ? 12 : 8;
+            if (i == SB_READY || i == DS_FREE) n = 8;
+            if (i == FIX) n = 4;
+            // K is read by dS and P, Q by P and OX, V by the weight warps (through dS) and OI
+            if (!STATE_ONLY && ((i >= EMPTY_Q && i < EMPTY_Q + 2) || (i >= EMPTY_K && i < EMPTY_K + 2) ||
+                                (i >= EMPTY_V && i < EMPTY_V + 2)))
+                n = 2;
+            if (i == MMA_END) n = 3;
+            mbar_init(&bar[i], n);
         }
-        *abort_flag = 0;
+        *ctl = Ctl{sref.word, sref.stamp, timeout_ns, 0};
         fence_mbar_init();
     }
     if (warp == 0) tmem_alloc(tmem_slot, 512);
@@ -151,122 +222,136 @@ __global__ void __launch_bounds__(dt::THREADS, 1)
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     auto hw = [&](int i, int phase) -> bool {
-        return wait_or_abort(&bar[i], uint32_t(phase) & 1u, abort_flag, timeout_ns, sref);
+        const uint32_t parity = uint32_t(phase) & 1u;
+        return mbar_try_wait(&bar[i], parity) || wait_slow(smem_u32(&bar[i]), parity, ctl);
     };
 
-    if (warp == TMA_WARP) {   // ------------------------------------------- TMA
-        if (lane == 0) {
-            int nk = 0, nq = 0, nv = 0;
-            for (int c = 0; c < n_chunks; ++c) {
-                const int st = c & 1, t = s0 + c * C;
-                if (c >= 2 && !hw(EMPTY_K + st, (c - 2) >> 1)) break;
-                mbar_arrive_expect_tx(&bar[FULL_K + st], two ? Q_BYTES : HALF);
-                tma_load_4d(sm + OFF_K + st * Q_BYTES, &tm_k, &bar[FULL_K + st], 0, hk, t, b);
-                if (two) tma_load_4d(sm + OFF_K + st * Q_BYTES + HALF, &tm_k, &bar[FULL_K + st], 64, hk, t, b);
-                ++nk;
-                if (!STATE_ONLY) {
-                    if (c >= 2 && !hw(EMPTY_Q + st, (c - 2) >> 1)) break;
-                    mbar_arrive_expect_tx(&bar[FULL_Q + st], two ? Q_BYTES : HALF);
-                    tma_load_4d(sm + OFF_Q + st * Q_BYTES, &tm_q, &bar[FULL_Q + st], 0, hk, t, b);
-                    if (two) tma_load_4d(sm + OFF_Q + st * Q_BYTES + HALF, &tm_q, &bar[FULL_Q + st], 64, hk, t, b);
-                    ++nq;
-                }
-                if (c >= 2 && !hw(EMPTY_V + st, (c - 2) >> 1)) break;
-                mbar_arrive_expect_tx(&bar[FULL_V + st], V_BYTES);
-                tma_load_4d(sm + OFF_V + st * V_BYTES, &tm_v, &bar[FULL_V + st], vt * RB, h, t, b);
-                ++nv;
+    if (warp == K_WARP || warp == Q_WARP || warp == V_WARP) {   // --------- TMA
+        if (lane == 0 && !(STATE_ONLY && warp == Q_WARP)) {
+            const CUtensorMap *tm = warp == K_WARP ? &tm_k : warp == Q_WARP ? &tm_q : &tm_v;
+            const int full = warp == K_WARP ? FULL_K : warp == Q_WARP ? FULL_Q : FULL_V;
+            const int empty = warp == K_WARP ? EMPTY_K : warp == Q_WARP ? EMPTY_Q : EMPTY_V;
+            const bool halves = two && warp != V_WARP;
+            const uint32_t bytes = warp == V_WARP ? V_BYTES : Q_BYTES;
+            unsigned char *dst = sm + (warp == K_WARP ? OFF_K : warp == Q_WARP ? OFF_Q : OFF_V);
+            const int x0 = warp == V_WARP ? vt * RB : 0, head = warp == V_WARP ? h : hk;
+            prefetch_tensormap(tm);
+            int n = 0;
+            for (; n < n_chunks; ++n) {
+                const int st = n & 1, t = s0 + n * C;
+                if (n >= 2 && !hw(empty + st, (n - 2) >> 1)) break;
+                mbar_arrive_expect_tx(&bar[full + st], halves ? 2 * HALF : HALF);
+                tma_load_4d(dst + st * bytes, tm, &bar[full + st], x0, head, t, b);
+                if (halves) tma_load_4d(dst + st * bytes + HALF, tm, &bar[full + st], 64, head, t, b);
             }
             // copies still in flight land before the block exits
-            for (int c = max(nk - 2, 0); c < nk; ++c)
-                mbar_wait_bounded(&bar[FULL_K + (c & 1)], (c >> 1) & 1, timeout_ns);
-            for (int c = max(nq - 2, 0); c < nq; ++c)
-                mbar_wait_bounded(&bar[FULL_Q + (c & 1)], (c >> 1) & 1, timeout_ns);
-            for (int c = max(nv - 2, 0); c < nv; ++c)
-                mbar_wait_bounded(&bar[FULL_V + (c & 1)], (c >> 1) & 1, timeout_ns);
+            for (int c = max(n - 2, 0); c < n; ++c) mbar_wait_bounded(&bar[full + (c & 1)], (c >> 1) & 1, timeout_ns);
         }
-    } else if (warp == MMA_WARP) {   // ------------------------------------ MMA
-        if (lane == 0) {
-            auto issue_p = [&](int c) {
-                const uint32_t sQ = smem_u32(sm + OFF_Q + (c & 1) * Q_BYTES),
-                               sK = smem_u32(sm + OFF_K + (c & 1) * Q_BYTES);
-                for (int kk = 0; kk < nkk; ++kk) {
-                    const uint32_t off = (kk >> 2) * HALF + (kk & 3) * 32;
-                    umma_bf16(tmem + T_P + (c & 1) * 128, umma_smem_desc(sQ + off, 16, 1024),
-                              umma_smem_desc(sK + off, 16, 1024), IDESC_P, kk > 0);
-                }
-                umma_commit(&bar[P_READY + (c & 1)]);
-            };
-            bool ok = n_chunks > 0;
-            if (ok) ok = hw(FULL_K, 0);
-            if (ok && !STATE_ONLY) {
-                ok = hw(FULL_Q, 0);
-                if (ok) {
-                    tc_fence_after();
-                    issue_p(0);
-                }
-            }
-            for (int c = 0; ok && c < n_chunks; ++c) {
+    } else if (warp >= DS_WARP && warp <= O_WARP) {   // ------------ products
+        // every wait's answer is made warp-uniform, and so is all that follows
+        auto hu = [&](int i, int phase) -> bool { return __all_sync(0xffffffffu, hw(i, phase)); };
+        const bool lead = elect_one();
+        const uint32_t base = __shfl_sync(0xffffffffu, smem_u32(sm), 0);
+        if (warp == DS_WARP) {
+            const uint64_t dW = umma_smem_desc(base + OFF_W, V_BYTES, 1024);
+            for (int c = 0; c < n_chunks; ++c) {
                 const int st = c & 1;
-                const uint32_t sK = smem_u32(sm + OFF_K + st * Q_BYTES), sV = smem_u32(sm + OFF_V + st * V_BYTES),
-                               sWt = smem_u32(sm + OFF_W);
-                // dS once the weighted values are there and the back has read the last one
-                if (STATE_ONLY && !hw(FULL_K + st, c >> 1)) break;
-                if (!hw(W_READY, c) || (c >= 1 && !hw(DS_FREE, c - 1))) break;
-                tc_fence_after();
+                // the last dS has been read
+                if (!hu(FULL_K + st, c >> 1) || (c >= 1 && !hu(DS_FREE, c - 1))) break;
+                const uint64_t dK = umma_smem_desc(base + OFF_K + st * Q_BYTES, HALF, 1024);
+                bool ok = true;
 #pragma unroll
-                for (int kk = 0; kk < C / 16; ++kk)
-                    umma_bf16(tmem + T_DS, umma_smem_desc(sK + kk * 2048, HALF, 1024),
-                              umma_smem_desc(sWt + kk * 2048, V_BYTES, 1024), IDESC_DS, kk > 0);
-                umma_commit(&bar[DS_DONE]);
-                umma_commit(&bar[EMPTY_K + st]);   // P_c, issued before, is covered too
-                if (STATE_ONLY) {
+                for (int qt = 0; qt < 4; ++qt) {
+                    ok = ok && hu(W_READY + qt, c);
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (lead) {   // 16 steps are 2048 bytes on, 128 in the descriptors' units
+                        umma_bf16(tmem + T_DS, dK + 256 * qt, dW + 256 * qt, IDESC_DS, qt > 0);
+                        umma_bf16(tmem + T_DS, dK + 256 * qt + 128, dW + 256 * qt + 128, IDESC_DS, 1);
+                        umma_commit(&bar[W_FREE + qt]);
+                        if (qt == 3) {
+                            umma_commit(&bar[DS_DONE]);
+                            umma_commit(&bar[EMPTY_K + st]);
+                            umma_commit(&bar[EMPTY_V + st]);
+                        }
+                    }
+                    __syncwarp();
+                }
+                if (!ok) break;
+            }
+        } else if (!STATE_ONLY && warp == P_WARP) {
+            for (int c = 0; c < n_chunks; ++c) {
+                const int st = c & 1;
+                if (!hu(FULL_K + st, c >> 1) || !hu(FULL_Q + st, c >> 1)) break;
+                if (c >= 2 && !hu(O_DONE + st, (c - 2) >> 1)) break;   // chunk c - 2's PD has been used
+                tc_fence_after();
+                const uint64_t dQ = umma_smem_desc(base + OFF_Q + st * Q_BYTES, 16, 1024),
+                               dK = umma_smem_desc(base + OFF_K + st * Q_BYTES, 16, 1024);
+                if (lead) {
+#pragma unroll
+                    for (int kk = 0; kk < 8; ++kk)
+                        if (kk < nkk) {
+                            const uint32_t off = ((kk >> 2) * HALF + (kk & 3) * 32) >> 4;
+                            umma_bf16(tmem + T_P + st * 128, dQ + off, dK + off, IDESC_P, kk > 0);
+                        }
+                    umma_commit(&bar[P_READY + st]);
+                    umma_commit(&bar[EMPTY_K + st]);
+                    umma_commit(&bar[EMPTY_Q + st]);
+                }
+                __syncwarp();
+            }
+        } else if (!STATE_ONLY && warp == O_WARP) {
+            const uint64_t dS = umma_smem_desc(base + OFF_SB, HALF, 1024);
+            int n_steep = 0;
+            for (int c = 0; c < n_chunks; ++c) {
+                const int st = c & 1;
+                // the state before chunk c; the last outputs have been read
+                if (!hu(SB_READY, c) || !hu(FULL_Q + st, c >> 1)) break;
+                if (c >= 1 && !hu(K_DONE + ((c - 1) & 1), (c - 1) >> 1)) break;
+                tc_fence_after();
+                const uint64_t dQ = umma_smem_desc(base + OFF_Q + st * Q_BYTES, 16, 1024);
+                if (lead) {
+#pragma unroll
+                    for (int kk = 0; kk < 8; ++kk)
+                        if (kk < nkk)
+                            umma_bf16(tmem + T_O, dQ + (((kk >> 2) * HALF + (kk & 3) * 32) >> 4), dS + 128 * kk, IDESC_O,
+                                      kk > 0);
+                    umma_commit(&bar[OX_DONE + st]);
+                    umma_commit(&bar[EMPTY_Q + st]);
+                }
+                __syncwarp();
+                if (!hu(F_DONE + st, c >> 1) || !hu(FULL_V + st, c >> 1)) break;
+                if (sF[4 * (c & (NM - 1)) + 2] == 0.0f && !hu(FIX, n_steep++)) break;
+                if (c * C + C > nrun) {   // the last chunk: V's rows past the end have been zeroed
+                    bool ok = true;
+                    for (int qt = 0; qt < 4; ++qt) ok = ok && hu(W_READY + qt, c);
+                    if (!ok) break;
+                }
+                tc_fence_after();
+                const uint64_t dV = umma_smem_desc(base + OFF_V + st * V_BYTES, HALF, 1024);
+                if (lead) {   // onto Q S^T: same shape and accumulator, so in order
+#pragma unroll
+                    for (int kk = 0; kk < C / 16; ++kk)
+                        umma_bf16_ts(tmem + T_O, tmem + T_P + st * 128 + (kk >> 2) * 64 + (kk & 3) * 8, dV + 128 * kk,
+                                     IDESC_O, 1);
+                    umma_commit(&bar[O_DONE + st]);
                     umma_commit(&bar[EMPTY_V + st]);
-                    continue;
                 }
-                // P of the next chunk; its buffer (and OI's) held chunk c - 1's
-                if (c >= 1 && !hw(K_DONE + ((c - 1) & 1), (c - 1) >> 1)) break;
-                if (c + 1 < n_chunks) {
-                    const int sn = (c + 1) & 1;
-                    if (!hw(FULL_K + sn, (c + 1) >> 1) || !hw(FULL_Q + sn, (c + 1) >> 1)) break;
-                    tc_fence_after();
-                    issue_p(c + 1);
-                }
-                if (!hw(F_DONE + st, c >> 1)) break;
-                tc_fence_after();
-#pragma unroll
-                for (int kk = 0; kk < C / 16; ++kk)
-                    umma_bf16_ts(tmem + T_OI, tmem + T_P + st * 128 + kk * 8,
-                                 umma_smem_desc(sV + kk * 2048, HALF, 1024), IDESC_O, kk > 0);
-                umma_commit(&bar[OI_DONE]);
-                umma_commit(&bar[EMPTY_V + st]);
+                __syncwarp();
             }
-            // nothing of this block's may still run on the tensor cores when its TMEM is released
+        }
+        // nothing of this block's may still run on the tensor cores when its TMEM is released
+        if (lead) {
             umma_commit(&bar[MMA_END]);
             mbar_wait_bounded(&bar[MMA_END], 0, timeout_ns);
         }
-    } else if (warp == OX_WARP) {   // -------------------------------------- OX
-        if (lane == 0) {
-            for (int c = 0; !STATE_ONLY && c < n_chunks; ++c) {
-                const int st = c & 1;
-                // the state before chunk c; P_c read (its columns 64.. are free)
-                if (!hw(SB_READY, c) || !hw(F_DONE + st, c >> 1)) break;
-                tc_fence_after();
-                const uint32_t sQ = smem_u32(sm + OFF_Q + st * Q_BYTES), sS = smem_u32(sm + OFF_SB);
-                for (int kk = 0; kk < nkk; ++kk)
-                    umma_bf16(tmem + T_P + st * 128 + 64,
-                              umma_smem_desc(sQ + (kk >> 2) * HALF + (kk & 3) * 32, 16, 1024),
-                              umma_smem_desc(sS + kk * 2048, HALF, 1024), IDESC_O, kk > 0);
-                umma_commit(&bar[OX_DONE]);
-                umma_commit(&bar[EMPTY_Q + st]);
-            }
-            umma_commit(&bar[MMA_END]);
-            mbar_wait_bounded(&bar[MMA_END], 0, timeout_ns);
-        }
+        __syncwarp();
     } else if (warp == SCAN_WARP) {   // ---------------------------------- scan
         // lane i: steps 4 i .. 4 i + 3 of the chunk
         const float lh = a.a_log == nullptr ? 0.0f : a.a_log[h];
         const bf *g = a.g == nullptr ? nullptr : static_cast<const bf *>(a.g) + (size_t(b) * a.L + s0) * a.H + h;
         long long base = 0, tot = 0;
+        int last = -1;   // the last steep chunk
         bool bad = false;
         float gn[4];
         auto load = [&](int c) {
@@ -293,25 +378,29 @@ __global__ void __launch_bounds__(dt::THREADS, 1)
             }
             const long long all = __shfl_sync(0xffffffffu, incl, 31), before = incl - run;
             const long long end = base + all;            // since the last rescale
-            const bool re = end < dec::kRescale;
-            bool ok = c < 2 || hw(K_DONE + (c & 1), (c - 2) >> 1);
+            const bool steep = all < kSteepChunk, re = steep || end < kRescaleTensor;
+            bool ok = c < NM || hw(M_FREE + (c & (NM - 1)), (c - NM) / NM);
             if (!__all_sync(0xffffffffu, ok)) break;
-            float lv[4], wv[4];
+            float wv[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const long long l = before + cum[i];
-                lv[i] = float(l) * dec::kFixInv;
                 wv[i] = dec::exp2_fix(re ? all - l : -(base + l));
             }
-            float *pl = sL + (c & 1) * C + 4 * lane, *pw = sW + (c & 1) * C + 4 * lane;
-            *reinterpret_cast<float4 *>(pl) = make_float4(lv[0], lv[1], lv[2], lv[3]);
-            *reinterpret_cast<float4 *>(pw) = make_float4(wv[0], wv[1], wv[2], wv[3]);
-            if (lane == 0) {
-                sF[2 * (c & 1)] = re ? dec::exp2_fix(end) : 1.0f;
-                sF[2 * (c & 1) + 1] = float(base) * dec::kFixInv;
+            if (steep) {   // the one L buffer: free once the last steep chunk's outputs are done
+                ok = last < 0 || c - last >= NM || hw(M_FREE + (last & (NM - 1)), last / NM);
+                if (!__all_sync(0xffffffffu, ok)) break;
+                last = c;
+                *reinterpret_cast<float4 *>(sL + 4 * lane) =
+                    make_float4(dec::fix_f(before + cum[0]), dec::fix_f(before + cum[1]), dec::fix_f(before + cum[2]),
+                                dec::fix_f(before + cum[3]));
             }
+            *reinterpret_cast<float4 *>(sW + (c & (NM - 1)) * C + 4 * lane) = make_float4(wv[0], wv[1], wv[2], wv[3]);
+            if (lane == 0)
+                *reinterpret_cast<float4 *>(sF + 4 * (c & (NM - 1))) =
+                    make_float4(re ? dec::exp2_fix(end) : 1.0f, dec::fix_f(base), steep ? 0.0f : 1.0f, 0.0f);
             __syncwarp();
-            if (lane == 0) arrive(&bar[M_READY + (c & 1)]);
+            if (lane == 0) arrive(&bar[M_READY + (c & (NM - 1))]);
             base = re ? 0 : end;
             tot = max(tot + all, -(1ll << 60));
         }
@@ -321,37 +410,41 @@ __global__ void __launch_bounds__(dt::THREADS, 1)
         if (lane == 0) *reinterpret_cast<float *>(sm + OFF_END) = dec::exp2_fix(base);
     } else if (warp >= WEIGHT) {   // ----------------------------------- weight
         const int s = tid - 32 * WEIGHT;   // this thread's step of the chunk
+        const int qt = warp - WEIGHT;
         for (int c = 0; c < n_chunks; ++c) {
             const int st = c & 1;
             unsigned char *V = sm + OFF_V + st * V_BYTES;
             const bool in = c * C + s < nrun;
-            bool ok = hw(M_READY + st, c >> 1) && hw(FULL_V + st, c >> 1);
+            const int mt = c & (NM - 1);
+            bool ok = hw(M_READY + mt, c / NM) && hw(FULL_V + st, c >> 1);
             if (ok && c * C + C > nrun) ok = hw(FULL_K + st, c >> 1);
-            if (ok && c >= 1) ok = hw(DS_DONE, c - 1);   // the three terms' buffer is free
+            if (ok && c >= 1) ok = hw(W_FREE + qt, c - 1);
             if (!__all_sync(0xffffffffu, ok)) break;
-            const float w = sW[st * C + s];
-#pragma unroll
+            const float w = sW[mt * C + s];
+            const float2 w2 = make_float2(w, w);
+#pragma unroll 1
             for (int k = 0; k < 8; ++k) {
                 const uint32_t at = sw128_offset(s, 8 * k);
-                const uint4 u = *reinterpret_cast<const uint4 *>(V + at);
+                uint4 u = *reinterpret_cast<const uint4 *>(V + at);
+                if (!in) u = make_uint4(0, 0, 0, 0);
                 const uint32_t uv[4] = {u.x, u.y, u.z, u.w};
-                uint32_t w1[4], w2[4], w3[4];
+                uint32_t t1[4], t2[4], t3[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    float y0 = in ? w * lo_f(uv[e]) : 0.0f, y1 = in ? w * hi_f(uv[e]) : 0.0f;
-                    w1[e] = pack(y0, y1);
-                    y0 -= lo_f(w1[e]), y1 -= hi_f(w1[e]);
-                    w2[e] = pack(y0, y1);
-                    y0 -= lo_f(w2[e]), y1 -= hi_f(w2[e]);
-                    w3[e] = pack(y0, y1);
+                for (int e = 0; e < 4; ++e) {   // what each term leaves goes to the next
+                    float2 y = __fmul2_rn(w2, make_float2(lo_f(uv[e]), hi_f(uv[e])));
+                    t1[e] = pack(y.x, y.y);
+                    y = __fadd2_rn(y, make_float2(-lo_f(t1[e]), -hi_f(t1[e])));
+                    t2[e] = pack(y.x, y.y);
+                    y = __fadd2_rn(y, make_float2(-lo_f(t2[e]), -hi_f(t2[e])));
+                    t3[e] = pack(y.x, y.y);
                 }
-                *reinterpret_cast<uint4 *>(sm + OFF_W + at) = make_uint4(w1[0], w1[1], w1[2], w1[3]);
-                *reinterpret_cast<uint4 *>(sm + OFF_W + V_BYTES + at) = make_uint4(w2[0], w2[1], w2[2], w2[3]);
-                *reinterpret_cast<uint4 *>(sm + OFF_W + 2 * V_BYTES + at) = make_uint4(w3[0], w3[1], w3[2], w3[3]);
+                *reinterpret_cast<uint4 *>(sm + OFF_W + at) = make_uint4(t1[0], t1[1], t1[2], t1[3]);
+                *reinterpret_cast<uint4 *>(sm + OFF_W + V_BYTES + at) = make_uint4(t2[0], t2[1], t2[2], t2[3]);
+                *reinterpret_cast<uint4 *>(sm + OFF_W + 2 * V_BYTES + at) = make_uint4(t3[0], t3[1], t3[2], t3[3]);
             }
             if (!in) {   // past the row's end: whatever stands there must not reach a product
                 const uint4 z = make_uint4(0, 0, 0, 0);
-#pragma unroll
+#pragma unroll 1
                 for (int k = 0; k < 8; ++k) {
                     *reinterpret_cast<uint4 *>(V + s * 128 + 16 * k) = z;
                     *reinterpret_cast<uint4 *>(sm + OFF_K + st * Q_BYTES + s * 128 + 16 * k) = z;
@@ -360,154 +453,239 @@ __global__ void __launch_bounds__(dt::THREADS, 1)
             }
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) arrive(&bar[W_READY]);
+            if (lane == 0) {
+                arrive(&bar[W_READY + qt]);
+                arrive(&bar[M_FREE + mt]);
+            }
         }
     } else if (warp >= FRONT) {   // ------------------------------------- front
-        const int fw = warp - FRONT, t = 32 * fw + lane;   // this thread's row
-        const uint32_t lanes = uint32_t(fw * 32) << 16;
+        // rows 32 fw .. of P, columns 64 hf .. in blocks of 16; PD's go to the
+        // first half of the same columns, which the warp has read by then
+        const int fw = warp & 3, hf = (warp - FRONT) >> 2, t = 32 * fw + lane;
         for (int c = 0; !STATE_ONLY && c < n_chunks; ++c) {
             const int st = c & 1;
-            const uint32_t P = tmem + T_P + st * 128 + lanes;
-            const bool ok = hw(M_READY + st, c >> 1) && hw(P_READY + st, c >> 1);
+            const uint32_t P = tmem + T_P + st * 128 + 64 * hf + (uint32_t(fw * 32) << 16);
+            const int mt = c & (NM - 1);
+            const bool ok = hw(M_READY + mt, c / NM) && hw(P_READY + st, c >> 1);
             if (!__all_sync(0xffffffffu, ok)) break;
             tc_fence_after();
-            const float *l = sL + st * C;
-            const float lt = l[t];
-            const int nv = nrun - c * C;   // valid steps of the chunk
+            const int n = min(t + 1, nrun - c * C) - 64 * hf;   // columns that this row sees
+            const bool cut = nrun - c * C < C;
+            if (sF[4 * mt + 2] != 0.0f) {
+                const float *f = sW + mt * C + 64 * hf;
 #pragma unroll 1
-            for (int kb = 0; kb < 4; ++kb) {
-                uint32_t r[16];
-                if (kb <= fw) {
-                    float p[32];
-                    tmem_ld32_nowait(P + 32 * kb, p);
-                    tmem_ld_wait_tied(p);
+                for (int kb = 0; kb < 4; ++kb) {
+                    uint32_t r[8];
+                    if (64 * hf + 16 * kb <= 32 * fw + 31) {   // some row of the warp sees the block
+                        float p[16];
+                        tmem_ld16_nowait(P + 16 * kb, p);
+                        float4 w4[4];
 #pragma unroll
-                    for (int e = 0; e < 32; e += 4) {
-                        const int sx = 32 * kb + e;
-                        const float4 ls = *reinterpret_cast<const float4 *>(l + sx);
-                        const float y0 = sx <= t && sx < nv ? p[e] * ex2_approx(lt - ls.x) : 0.0f;
-                        const float y1 = sx + 1 <= t && sx + 1 < nv ? p[e + 1] * ex2_approx(lt - ls.y) : 0.0f;
-                        const float y2 = sx + 2 <= t && sx + 2 < nv ? p[e + 2] * ex2_approx(lt - ls.z) : 0.0f;
-                        const float y3 = sx + 3 <= t && sx + 3 < nv ? p[e + 3] * ex2_approx(lt - ls.w) : 0.0f;
-                        r[e / 2] = pack(y0, y1);
-                        r[e / 2 + 1] = pack(y2, y3);
+                        for (int e = 0; e < 4; ++e) w4[e] = *reinterpret_cast<const float4 *>(f + 16 * kb + 4 * e);
+                        tmem_ld_wait_tied(p);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float2 y0 = __fmul2_rn(make_float2(p[4 * e], p[4 * e + 1]), make_float2(w4[e].x, w4[e].y));
+                            const float2 y1 =
+                                __fmul2_rn(make_float2(p[4 * e + 2], p[4 * e + 3]), make_float2(w4[e].z, w4[e].w));
+                            r[2 * e] = pack(y0.x, y0.y);
+                            r[2 * e + 1] = pack(y1.x, y1.y);
+                        }
+                        if (cut || 64 * hf + 16 * kb + 15 > 32 * fw) {   // cut bits, whatever the others hold
+                            const int m = n - 16 * kb;
+#pragma unroll
+                            for (int e = 0; e < 8; ++e)
+                                r[e] &= 2 * e + 1 < m ? 0xffffffffu : 2 * e < m ? 0xffffu : 0u;
+                        }
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) r[e] = 0;
                     }
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) r[e] = 0;
+                    tmem_st8_nowait(P + 8 * kb, r);
                 }
-                // columns 16 kb .. hold P columns that this thread has read
-                tmem_st16_nowait(P + 16 * kb, r);
+            } else {   // a steep chunk
+                const float *f = sL + 64 * hf;
+                const float lt = sL[t];
+#pragma unroll 1
+                for (int kb = 0; kb < 4; ++kb) {
+                    float p[16];
+                    tmem_ld16_nowait(P + 16 * kb, p);
+                    tmem_ld_wait_tied(p);
+                    uint32_t r[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const int s = 16 * kb + 2 * e;
+                        const float2 ls = *reinterpret_cast<const float2 *>(f + s);
+                        r[e] = pack(s < n ? p[2 * e] * ex2_approx(lt - ls.x) : 0.0f,
+                                    s + 1 < n ? p[2 * e + 1] * ex2_approx(lt - ls.y) : 0.0f);
+                    }
+                    tmem_st8_nowait(P + 8 * kb, r);
+                }
             }
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) arrive(&bar[F_DONE + st]);
         }
-    } else {   // ---------------------------------------------------------- back
-        const int j = tid;   // key column
-        const uint32_t lanes = uint32_t(warp * 32) << 16;
+    } else if (warp >= OUT) {   // --------------------------------------- output
+        const int row = tid - 32 * OUT;   // this thread's step of the chunk
+        const uint32_t lanes = uint32_t((warp - OUT) * 32) << 16;
         const int i0 = vt * RB;
-        float S[RB];
-        const float *s_in = seg > 0 ? nullptr : a.S0;
+        const size_t HV = size_t(a.H) * dv;
+        bf *ob = static_cast<bf *>(a.o) + (size_t(b) * a.L + s0) * HV + size_t(h) * dv + i0;
+        for (int c = 0; !STATE_ONLY && c < n_chunks; ++c) {
+            const int st = c & 1, mt = c & (NM - 1);
+            const uint32_t O = tmem + T_O + lanes;
+            if (!__all_sync(0xffffffffu, hw(M_READY + mt, c / NM))) break;
+            const float4 f = *reinterpret_cast<const float4 *>(sF + 4 * mt);
+            float u = a.scale;
+            if (f.z == 0.0f) {   // steep: rows of Q S^T by 2^(base + L) before PD V is added
+                if (!__all_sync(0xffffffffu, hw(OX_DONE + st, c >> 1))) break;
+                tc_fence_after();
+                const float e = exp2f(f.y + sL[row]);
+#pragma unroll 1
+                for (int q = 0; q < RB; q += 16) {
+                    float d[16];
+                    tmem_ld16_nowait(O + q, d);
+                    tmem_ld_wait_tied(d);
+                    uint32_t w[16];
 #pragma unroll
-        for (int r = 0; r < RB; ++r)
-            S[r] = s_in != nullptr && j < dk && i0 + r < dv ? s_in[(size_t(bh) * dv + i0 + r) * dk + j] : 0.0f;
-        if (!STATE_ONLY && seg > 0) {   // the decayed sum of the ranges before this one
+                    for (int r = 0; r < 16; ++r) w[r] = __float_as_uint(e * d[r]);
+                    tmem_st16_nowait(O + q, w);
+                }
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) arrive(&bar[FIX]);
+            } else {
+                u /= sW[mt * C + row];
+            }
+            if (!__all_sync(0xffffffffu, hw(O_DONE + st, c >> 1))) break;
+            tc_fence_after();
+            const int t = c * C + row;
+            const bool valid = t < nrun, store = s0 + t < send, cut = nrun - c * C < C;
+            const float2 u2 = make_float2(u, u);
+            uint32_t w[RB / 2];
+#pragma unroll
+            for (int q = 0; q < RB; q += 16) {
+                float d[16];
+                tmem_ld16_nowait(O + q, d);
+                tmem_ld_wait_tied(d);
+#pragma unroll
+                for (int r = 0; r < 8; ++r) {
+                    const float2 y = __fmul2_rn(u2, make_float2(d[2 * r], d[2 * r + 1]));
+                    w[q / 2 + r] = pack(y.x, y.y);
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {   // the accumulator is free before the stores go out
+                arrive(&bar[K_DONE + st]);
+                arrive(&bar[M_FREE + mt]);
+            }
+            if (cut) {
+#pragma unroll
+                for (int r = 0; r < RB / 2; ++r) w[r] = valid ? w[r] : 0u;
+            }
+            bf *dst = ob + size_t(t) * HV;
+            if (store) {
+#pragma unroll
+                for (int q = 0; q < 8; ++q)
+                    if (i0 + 8 * q < dv)
+                        *reinterpret_cast<uint4 *>(dst + 8 * q) =
+                            make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
+            }
+        }
+    } else {   // --------------------------------------------------------- state
+        // key column: this thread's TMEM lane; value rows 32 sh .. of the block's 64
+        const int j = tid & 127, sh = warp >> 2;
+        const uint32_t D = tmem + T_DS + 32 * sh + (uint32_t((warp & 3) * 32) << 16);
+        const int i0 = vt * RB + 32 * sh;
+        // the state before the segment: S0, or the decayed sum of the ranges before
+        float S[32];
+#pragma unroll
+        for (int r = 0; r < 32; ++r)
+            S[r] = a.S0 != nullptr && seg == 0 && j < dk && i0 + r < dv ? a.S0[(size_t(bh) * dv + i0 + r) * dk + j]
+                                                                        : 0.0f;
+        if (!STATE_ONLY && seg > 0) {
             grid_dependency_wait();
             long long acc = 0;
-            for (int s = seg - 1; s >= 0; --s) {
+#pragma unroll 1
+            for (int e = seg - 1; e >= 0; --e) {
                 const float f = dec::exp2_fix(acc);
                 if (f == 0.0f) break;
-                const size_t at = size_t(bh) * (a.n_seg - 1) + s;
+                const size_t at = size_t(bh) * (a.n_seg - 1) + e;
                 const float *src = a.seg_state + (at * dv + i0) * dk + j;
 #pragma unroll
-                for (int r = 0; r < RB; ++r)
+                for (int r = 0; r < 32; ++r)
                     if (j < dk && i0 + r < dv) S[r] = fmaf(f, src[size_t(r) * dk], S[r]);
                 acc = max(acc + a.seg_tot[at], -(1ll << 60));
             }
         }
-        auto publish = [&]() {   // bf16 copy: row j, 64 value rows in 8 swizzled groups
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-                *reinterpret_cast<uint4 *>(sm + OFF_SB + sw128_offset(j, 8 * k)) =
-                    make_uint4(pack(S[8 * k], S[8 * k + 1]), pack(S[8 * k + 2], S[8 * k + 3]),
-                               pack(S[8 * k + 4], S[8 * k + 5]), pack(S[8 * k + 6], S[8 * k + 7]));
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) arrive(&bar[SB_READY]);
-        };
-        if (!STATE_ONLY) publish();
-        const size_t HV = size_t(a.H) * dv;
-        bf *ob = static_cast<bf *>(a.o) + (size_t(b) * a.L + s0) * HV + size_t(h) * dv + i0;
         for (int c = 0; c < n_chunks; ++c) {
-            const int st = c & 1;
-            bool ok = hw(M_READY + st, c >> 1) && hw(DS_DONE, c);
+            const int mt = c & (NM - 1);
+            bool ok = hw(M_READY + mt, c / NM);
+            // the bf16 copy's buffer is free
+            if (ok && !STATE_ONLY && c >= 1) ok = hw(OX_DONE + ((c - 1) & 1), (c - 1) >> 1);
             if (!__all_sync(0xffffffffu, ok)) break;
+            const float m = sF[4 * mt];
+            // the copy: what this chunk's weights assume, S or m S (a steep chunk
+            // applies its factors by rows), as row j of 64 value rows in 8 swizzled groups
+            const float pm = sF[4 * mt + 2] == 0.0f ? 1.0f : m;
+            if (!STATE_ONLY) {
+                const float2 p2 = make_float2(pm, pm);
+#pragma unroll
+                for (int q = 0; q < 32; q += 8) {
+                    uint32_t r[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float2 y = __fmul2_rn(p2, make_float2(S[q + 2 * e], S[q + 2 * e + 1]));
+                        r[e] = pack(y.x, y.y);
+                    }
+                    *reinterpret_cast<uint4 *>(sm + OFF_SB + sw128_offset(j, 32 * sh + q)) =
+                        make_uint4(r[0], r[1], r[2], r[3]);
+                }
+                fence_proxy_async_smem();
+            }
+            __syncwarp();
+            if (lane == 0) {
+                if (!STATE_ONLY) arrive(&bar[SB_READY]);
+                if (STATE_ONLY) arrive(&bar[M_FREE + mt]);
+            }
+            if (!__all_sync(0xffffffffu, hw(DS_DONE, c))) break;
             tc_fence_after();
-            const float m = sF[2 * st], base = sF[2 * st + 1];
+            const float2 m2 = make_float2(m, m);
 #pragma unroll
-            for (int q = 0; q < RB; q += 16) {   // small terms first
-                float d1[16], d2[16];
-                tmem_ld16_nowait(tmem + T_DS + lanes + 128 + q, d1);
-                tmem_ld16_nowait(tmem + T_DS + lanes + 64 + q, d2);
-                tmem_ld_wait_tied(d1, d2);
+            for (int q = 0; q < 32; q += 8) {   // small terms first
+                float d1[8], d2[8], d3[8];
+                tmem_ld8_nowait(D + q, d1);
+                tmem_ld8_nowait(D + 64 + q, d2);
+                tmem_ld8_nowait(D + 128 + q, d3);
+                tmem_ld_wait_tied(d1, d2, d3);
 #pragma unroll
-                for (int r = 0; r < 16; ++r) d2[r] += d1[r];
-                tmem_ld16_nowait(tmem + T_DS + lanes + q, d1);
-                tmem_ld_wait_tied(d1);
-#pragma unroll
-                for (int r = 0; r < 16; ++r) S[q + r] = fmaf(m, S[q + r], d1[r] + d2[r]);
+                for (int e = 0; e < 8; e += 2) {
+                    const float2 y = __fadd2_rn(make_float2(d1[e], d1[e + 1]),
+                                                __fadd2_rn(make_float2(d2[e], d2[e + 1]), make_float2(d3[e], d3[e + 1])));
+                    const float2 z = __ffma2_rn(m2, make_float2(S[q + e], S[q + e + 1]), y);
+                    S[q + e] = z.x, S[q + e + 1] = z.y;
+                }
             }
             tc_fence_before();
             __syncwarp();
             if (lane == 0) arrive(&bar[DS_FREE]);
-            if (!STATE_ONLY) {
-                ok = hw(OX_DONE, c);   // the bf16 copy has been read
-                if (!__all_sync(0xffffffffu, ok)) break;
-                if (c + 1 < n_chunks) publish();
-                ok = hw(OI_DONE, c);
-                if (!__all_sync(0xffffffffu, ok)) break;
-                tc_fence_after();
-                const int t = c * C + tid;   // this thread's row of the outputs
-                const float u = exp2f(base + sL[st * C + tid]) * a.scale;
-                const bool valid = t < nrun, store = s0 + t < send;
-                bf *dst = ob + size_t(t) * HV;
-#pragma unroll
-                for (int q = 0; q < RB; q += 16) {
-                    float oi[16], ox[16];
-                    tmem_ld16_nowait(tmem + T_OI + lanes + q, oi);
-                    tmem_ld16_nowait(tmem + T_P + st * 128 + 64 + lanes + q, ox);
-                    tmem_ld_wait_tied(oi, ox);
-                    uint32_t w[8];
-#pragma unroll
-                    for (int r = 0; r < 8; ++r)
-                        w[r] = valid ? pack(fmaf(u, ox[2 * r], a.scale * oi[2 * r]),
-                                            fmaf(u, ox[2 * r + 1], a.scale * oi[2 * r + 1]))
-                                     : 0u;
-                    if (store && i0 + q < dv)
-                        *reinterpret_cast<uint4 *>(dst + q) = make_uint4(w[0], w[1], w[2], w[3]);
-                    if (store && i0 + q + 8 < dv)
-                        *reinterpret_cast<uint4 *>(dst + q + 8) = make_uint4(w[4], w[5], w[6], w[7]);
-                }
-                tc_fence_before();
-            }
-            __syncwarp();
-            if (lane == 0) arrive(&bar[K_DONE + st]);
         }
-        // the state after the segment, in the launch's last lines below
-        asm volatile("bar.sync 1, 160;" ::: "memory");   // the scan warp's last factor
+        asm volatile("bar.sync 1, 288;" ::: "memory");   // the scan warp's last factor
         float *out = STATE_ONLY ? a.seg_state + (size_t(bh) * (a.n_seg - 1) + seg) * dv * dk
                      : seg == a.n_seg - 1 && a.S_final != nullptr ? a.S_final + size_t(bh) * dv * dk
                                                                   : nullptr;
         if (out != nullptr && j < dk) {
             const float f = *reinterpret_cast<const float *>(sm + OFF_END);
 #pragma unroll
-            for (int r = 0; r < RB; ++r)
+            for (int r = 0; r < 32; ++r)
                 if (i0 + r < dv) out[size_t(i0 + r) * dk + j] = f * S[r];
         }
     }
-    if (warp == SCAN_WARP) asm volatile("bar.sync 1, 160;" ::: "memory");
+    if (warp == SCAN_WARP) asm volatile("bar.sync 1, 288;" ::: "memory");
 
     if (!STATE_ONLY) {   // whole chunks past the row's end
         const int g8 = min(RB, dv - vt * RB) / 8;
