@@ -744,8 +744,48 @@ def _heads_of(q, k, v, H: int, Hk: Optional[int]):
 
 
 def _shaped(t: Optional[torch.Tensor], shape, name: str):
-    if t is not None and tuple(t.shape) != tuple(shape):
+    if t is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+
+
+# The helpers below are called once per layer and token, where the GPU's own
+# time is a few microseconds: tensors that are already what the kernel takes
+# pass through one test each, and the stream is read as a raw handle.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream_of(t: torch.Tensor) -> int:
+    """The current stream of t's GPU (a cudaStream_t as an int)."""
+    if _raw_stream is not None:
+        return _raw_stream(t.get_device())
+    return torch.cuda.current_stream(t.device).cuda_stream
+
+
+def _act(t: Optional[torch.Tensor], dev) -> Optional[torch.Tensor]:
+    """t on the GPU, contiguous."""
+    if t is None or (t.is_cuda and t.is_contiguous()):
+        return t
+    return _dev(t, dev)
+
+
+def _par(t: Optional[torch.Tensor], dev) -> Optional[torch.Tensor]:
+    """As _act, in float32 (parameters and states)."""
+    if t is None or (t.dtype is torch.float32 and t.is_cuda and t.is_contiguous()):
+        return t
+    return _dev(t.float(), dev)
+
+
+# workspace sizes by problem (the query runs the library's plan)
+_DECAY_WS = {}
+
+
+def _decay_workspace_size(key) -> int:
+    n = _DECAY_WS.get(key)
+    if n is None:
+        if len(_DECAY_WS) >= 1024:
+            _DECAY_WS.clear()
+        n = _DECAY_WS[key] = lr_decay_attn_workspace_size(*key)
+    return n
 
 
 def decay_attn(q, k, v, H: int, Hk: Optional[int] = None, a_log=None, g=None, S0=None, lens=None,
@@ -771,8 +811,8 @@ def decay_attn(q, k, v, H: int, Hk: Optional[int] = None, a_log=None, g=None, S0
     _shaped(a_log, (H,), "a_log")
     _shaped(S0, (B, H, dv, dk), "S0")
     _shaped(lens, (B,), "lens")
-    specs = [((B, L, H * dv), q.dtype), ((B, H, dv, dk), torch.float32)]
-    if lens is None and _host_route((q, k, v, g), out):
+    specs = (((B, L, H * dv), q.dtype), ((B, H, dv, dk), torch.float32))
+    if lens is None and not q.is_cuda and _host_route((q, k, v, g), out):
         q, k, v, g = (_h(t) for t in (q, k, v, g))
         a_log, S0 = (_h(t, torch.float32) for t in (a_log, S0))
         o, Sf = _host_outputs(out, specs)
@@ -782,18 +822,26 @@ def decay_attn(q, k, v, H: int, Hk: Optional[int] = None, a_log=None, g=None, S0
         _check(fn(_ptr(q), _ptr(k), _ptr(v), _ptr(a_log), _ptr(g), float(scale), _ptr(S0), _ptr(o), _ptr(Sf),
                   B, L, H, Hk, dk, dv, io, _ptr(ws), wsb, _host_stream()), fn.__name__)
         return o, Sf
-    host = q.device.type != "cuda"
+    host = not q.is_cuda
     dev = _target_device(q)
-    q, k, v, g = (_dev(t, dev) for t in (q, k, v, g))
-    a_log, S0 = (_dev(None if t is None else t.float(), dev) for t in (a_log, S0))
-    lens = _dev(None if lens is None else lens.to(torch.int32), dev)
-    (o, Sf), host_out = _outputs(out, specs, dev)
-    ws, wsb = _workspace(lr_decay_attn_workspace_size(B, L, H, Hk, dk, dv, io), dev, workspace)
-    stream = torch.cuda.current_stream(dev).cuda_stream
-    _check(lr_decay_attn_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(a_log), _ptr(g), _ptr(lens), float(scale),
-                             _ptr(S0), _ptr(o), _ptr(Sf), B, L, H, Hk, dk, dv, io, _ptr(ws), wsb, stream),
-           "lr_decay_attn_fwd")
-    return _finish((o, Sf), host_out, host, dev, sync_host)
+    q, k, v, g = _act(q, dev), _act(k, dev), _act(v, dev), _act(g, dev)
+    a_log, S0 = _par(a_log, dev), _par(S0, dev)
+    if lens is not None:
+        lens = _act(lens if lens.dtype is torch.int32 else lens.to(torch.int32), dev)
+    if out is None:
+        o, Sf = (torch.empty(sh, dtype=dt, device=dev) for sh, dt in specs)
+        host_out = None
+    else:
+        (o, Sf), host_out = _outputs(out, specs, dev)
+    ws, wsb = _workspace(_decay_workspace_size((B, L, H, Hk, dk, dv, io)), dev, workspace)
+    rc = _lib.lr_decay_attn_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(a_log), _ptr(g), _ptr(lens), scale,
+                                _ptr(S0), o.data_ptr(), Sf.data_ptr(), B, L, H, Hk, dk, dv, io, ws.data_ptr(), wsb,
+                                _stream_of(q))
+    if rc != LR_OK:
+        _check(rc, "lr_decay_attn_fwd")
+    if host or host_out is not None:
+        return _finish((o, Sf), host_out, host, dev, sync_host)
+    return o, Sf
 
 
 def group_norm_act(x, G: int, gamma=None, beta=None, z=None, act: str = "none", eps: float = 1e-5,
@@ -813,16 +861,16 @@ def group_norm_act(x, G: int, gamma=None, beta=None, z=None, act: str = "none", 
     _same(x, z)
     io = _io_of(x)
     dev = _target_device(x)
-    x, z = _dev(x, dev), _dev(z, dev)
-    gamma, beta = (_dev(None if t is None else t.float(), dev) for t in (gamma, beta))
+    x, z = _act(x, dev), _act(z, dev)
+    gamma, beta = _par(gamma, dev), _par(beta, dev)
     if out is None:
         out = torch.empty_like(x)
     elif out.shape != x.shape or out.dtype != x.dtype or out.device != dev or not out.is_contiguous():
         raise ValueError(f"out must be a contiguous {x.dtype} GPU tensor of shape {tuple(x.shape)}")
-    stream = torch.cuda.current_stream(dev).cuda_stream
-    _check(lr_group_norm_act(_ptr(x), _ptr(z), _ptr(gamma), _ptr(beta), _ptr(out),
-                             x.numel() // C if C else 0, C, G, float(eps), _ACT[act], io, stream),
-           "lr_group_norm_act")
+    rc = _lib.lr_group_norm_act(x.data_ptr(), _ptr(z), _ptr(gamma), _ptr(beta), out.data_ptr(),
+                                x.numel() // C if C else 0, C, G, eps, _ACT[act], io, _stream_of(x))
+    if rc != LR_OK:
+        _check(rc, "lr_group_norm_act")
     return out
 
 
@@ -925,14 +973,19 @@ def decay_attn_step(q, k, v, H: int, Hk: Optional[int] = None, a_log=None, g=Non
     _shaped(a_log, (H,), "a_log")
     _shaped(S, (B, H, dv, dk), "S")
     dev = _target_device(q)
-    q, k, v, g = (_dev(t, dev) for t in (q, k, v, g))
-    a_log = _dev(None if a_log is None else a_log.float(), dev)
-    S_in, S_new = _step_state(S, (B, H, dv, dk), dev, S_out)
-    o = torch.empty(B, H * dv, dtype=q.dtype, device=dev)
-    stream = torch.cuda.current_stream(dev).cuda_stream
-    _check(lr_decay_attn_step(_ptr(q), _ptr(k), _ptr(v), _ptr(a_log), _ptr(g), float(scale), _ptr(S_in),
-                              _ptr(S_new), _ptr(o), B, H, Hk, dk, dv, io, stream), "lr_decay_attn_step")
-    return o, S_new
+    q, k, v, g = _act(q, dev), _act(k, dev), _act(v, dev), _act(g, dev)
+    a_log, S = _par(a_log, dev), _par(S, dev)
+    shape = (B, H, dv, dk)
+    if S_out is None:
+        S_out = torch.empty(shape, dtype=torch.float32, device=dev)
+    elif S_out.shape != shape or S_out.dtype is not torch.float32 or S_out.device != dev or not S_out.is_contiguous():
+        raise ValueError(f"S_out must be a contiguous fp32 GPU tensor of shape {shape}")
+    o = torch.empty((B, H * dv), dtype=q.dtype, device=dev)
+    rc = _lib.lr_decay_attn_step(q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(a_log), _ptr(g), scale, _ptr(S),
+                                 S_out.data_ptr(), o.data_ptr(), B, H, Hk, dk, dv, io, _stream_of(q))
+    if rc != LR_OK:
+        _check(rc, "lr_decay_attn_step")
+    return o, S_out
 
 
 def status(workspace=None, stream=None) -> int:

@@ -6,28 +6,36 @@
 // Every value is read once and written once, so memory bandwidth bounds the
 // kernel.  A group stays in the registers of the lanes that share it: the
 // mean, then the centred squares (no cancellation), then the output.
+//
+//   lanes   groups of 16-byte multiples up to 1024 bytes (the head dims): TL
+//           lanes of a warp hold a group, one or two 16-byte vectors each; a
+//           warp walks groups that share their channels' phase where it can
+//   block   larger groups of 16-byte multiples: a block holds the group, up to
+//           four vectors per thread
+//   any     the rest (odd sizes, groups past a block's registers): a block per
+//           group, three passes
 #include "lr_decay.cuh"
 
 namespace lr {
 namespace {
 
-__device__ __forceinline__ float silu_f(float x) { return x / (1.0f + expf(-x)); }
+// silu in fp32: x / (1 + e^-x), with e^-x kept below 2^125 (the fast division
+// is exact to 2 ulp for divisors up to 2^126; the quotient is 0 to fp32 there)
+__device__ __forceinline__ float silu_f(float x) {
+    return __fdividef(x, 1.0f + ex2_approx(fminf(-x * kLog2e, 125.0f)));
+}
 
 template <typename IO> struct Vec16;
 template <> struct Vec16<float> {
     static constexpr int N = 4;
-    __device__ __forceinline__ static void load(const float *p, float *v) {
-        const float4 u = __ldcs(reinterpret_cast<const float4 *>(p));
-        v[0] = u.x, v[1] = u.y, v[2] = u.z, v[3] = u.w;
-    }
-    __device__ __forceinline__ static void store(float *p, const float *v) {
-        __stcs(reinterpret_cast<float4 *>(p), make_float4(v[0], v[1], v[2], v[3]));
-    }
+    using Raw = float4;
+    __device__ __forceinline__ static void widen(const Raw &u, float *v) { v[0] = u.x, v[1] = u.y, v[2] = u.z, v[3] = u.w; }
+    __device__ __forceinline__ static Raw narrow(const float *v) { return make_float4(v[0], v[1], v[2], v[3]); }
 };
 template <> struct Vec16<__nv_bfloat16> {
     static constexpr int N = 8;
-    __device__ __forceinline__ static void load(const __nv_bfloat16 *p, float *v) {
-        const uint4 u = __ldcs(reinterpret_cast<const uint4 *>(p));
+    using Raw = uint4;
+    __device__ __forceinline__ static void widen(const Raw &u, float *v) {
         const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -35,51 +43,227 @@ template <> struct Vec16<__nv_bfloat16> {
             v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
         }
     }
-    __device__ __forceinline__ static void store(__nv_bfloat16 *p, const float *v) {
+    __device__ __forceinline__ static Raw narrow(const float *v) {
         uint32_t w[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const __nv_bfloat162 t = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
             w[i] = *reinterpret_cast<const uint32_t *>(&t);
         }
-        __stcs(reinterpret_cast<uint4 *>(p), make_uint4(w[0], w[1], w[2], w[3]));
+        return make_uint4(w[0], w[1], w[2], w[3]);
     }
 };
+
+struct NormArgs {
+    const void *x, *z;
+    const float *gamma, *beta;
+    void *y;
+    int64_t N;
+    int C, G, d;
+    float eps, inv_d;
+    int act;
+};
+
+// y of one 16-byte vector whose values are already centred
+template <typename IO, bool GATE>
+__device__ __forceinline__ typename Vec16<IO>::Raw finish(float *v, float rs, const float *ga, const float *be,
+                                                          const typename Vec16<IO>::Raw &zr, int act) {
+    constexpr int VN = Vec16<IO>::N;
+    float z[VN];
+    if (GATE) Vec16<IO>::widen(zr, z);
+#pragma unroll
+    for (int i = 0; i < VN; ++i) {
+        float n = fmaf(v[i] * rs, ga[i], be[i]);
+        if (act == LR_ACT_SILU) n = silu_f(n);
+        if (GATE) n *= silu_f(z[i]);
+        v[i] = n;
+    }
+    return Vec16<IO>::narrow(v);
+}
+
+template <int VN>
+__device__ __forceinline__ void load_affine(const float *gamma, const float *beta, int c, bool in, float *ga, float *be) {
+#pragma unroll
+    for (int i = 0; i < VN; i += 4) {
+        const float4 one = make_float4(1.0f, 1.0f, 1.0f, 1.0f), zero = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        const float4 g = gamma != nullptr && in ? *reinterpret_cast<const float4 *>(gamma + c + i) : one;
+        const float4 b = beta != nullptr && in ? *reinterpret_cast<const float4 *>(beta + c + i) : zero;
+        ga[i] = g.x, ga[i + 1] = g.y, ga[i + 2] = g.z, ga[i + 3] = g.w;
+        be[i] = b.x, be[i + 1] = b.y, be[i + 2] = b.z, be[i + 3] = b.w;
+    }
+}
+
+// TL lanes per group, V vectors per lane (vector u of lane l: l + u TL).  A
+// thread keeps its group (its channels, so gamma and beta stay in registers)
+// and walks rows, ROWS of them in flight: groups are dealt over grid.y and the
+// lane sets of a block, rows over grid.x.
+template <typename IO, int TL, int V, int ROWS, bool GATE>
+__global__ void __launch_bounds__(256)
+    group_norm_lanes_kernel(const NormArgs a) {
+    using X = Vec16<IO>;
+    using Raw = typename X::Raw;
+    constexpr int VN = X::N, SETS = 256 / TL;   // lane sets of a block
+    const int set = threadIdx.x / TL, l = threadIdx.x % TL;
+    // sets of a block: consecutive groups of a row, then rows
+    const int gper = min(a.G, SETS), rper = SETS / gper;
+    const int gi = blockIdx.y * gper + set % gper;
+    const int r0 = set / gper;
+    const bool live = gi < a.G && r0 < rper;
+    const int nv = a.d / VN;
+    float ga[V][VN], be[V][VN];
+    bool in[V];
+#pragma unroll
+    for (int u = 0; u < V; ++u) {
+        in[u] = live && l + u * TL < nv;
+        load_affine<VN>(a.gamma, a.beta, gi * a.d + (l + u * TL) * VN, in[u], ga[u], be[u]);
+    }
+    const Raw *x = static_cast<const Raw *>(a.x);
+    const Raw *z = static_cast<const Raw *>(a.z);
+    Raw *y = static_cast<Raw *>(a.y);
+    const int64_t row_vecs = a.C / VN, col = int64_t(gi) * nv + l;
+    const int64_t step = int64_t(gridDim.x) * rper;
+    for (int64_t base = int64_t(blockIdx.x) * rper; base < a.N; base += step * ROWS) {
+        Raw xr[ROWS][V], zr[ROWS][V];
+#pragma unroll
+        for (int k = 0; k < ROWS; ++k) {
+            const int64_t r = base + k * step + r0;
+#pragma unroll
+            for (int u = 0; u < V; ++u) {
+                xr[k][u] = Raw{};
+                zr[k][u] = Raw{};
+                if (in[u] && r < a.N) {
+                    xr[k][u] = __ldcs(x + r * row_vecs + col + u * TL);
+                    if (GATE) zr[k][u] = __ldcs(z + r * row_vecs + col + u * TL);
+                }
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < ROWS; ++k) {
+            const int64_t r = base + k * step + r0;
+            float v[V][VN], s = 0.0f;
+#pragma unroll
+            for (int u = 0; u < V; ++u) {
+                X::widen(xr[k][u], v[u]);
+#pragma unroll
+                for (int i = 0; i < VN; ++i) s += v[u][i];
+            }
+#pragma unroll
+            for (int m = TL / 2; m >= 1; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
+            const float mean = s * a.inv_d;
+            s = 0.0f;
+#pragma unroll
+            for (int u = 0; u < V; ++u) {
+#pragma unroll
+                for (int i = 0; i < VN; ++i) {
+                    v[u][i] -= mean;
+                    if (in[u]) s = fmaf(v[u][i], v[u][i], s);
+                }
+            }
+#pragma unroll
+            for (int m = TL / 2; m >= 1; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
+            const float rs = 1.0f / sqrtf(fmaf(s, a.inv_d, a.eps));
+#pragma unroll
+            for (int u = 0; u < V; ++u)
+                if (in[u] && r < a.N)
+                    __stcs(y + r * row_vecs + col + u * TL, finish<IO, GATE>(v[u], rs, ga[u], be[u], zr[k][u], a.act));
+        }
+    }
+}
+
+// sum over a block of NT threads, to all of them
+template <int NT>
+__device__ __forceinline__ float block_sum(float s, float *red) {
+#pragma unroll
+    for (int m = 16; m >= 1; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
+    __syncthreads();   // the last sum has been read
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = s;
+    __syncthreads();
+    s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NT / 32; ++i) s += red[i];
+    return s;
+}
+
+// a block per group (grid-stride over row-groups), V vectors per thread
+template <typename IO, int NT, int V, bool GATE>
+__global__ void __launch_bounds__(NT)
+    group_norm_block_kernel(const NormArgs a) {
+    using X = Vec16<IO>;
+    using Raw = typename X::Raw;
+    constexpr int VN = X::N;
+    __shared__ float red[NT / 32];
+    const int nv = a.d / VN;
+    for (int64_t rg = blockIdx.x; rg < a.N * a.G; rg += gridDim.x) {
+        const int gi = int(rg % a.G);
+        const int64_t at = rg * nv;
+        const Raw *x = static_cast<const Raw *>(a.x) + at;
+        const Raw *z = static_cast<const Raw *>(a.z) + at;
+        Raw xr[V], zr[V];
+#pragma unroll
+        for (int u = 0; u < V; ++u) {
+            const int i = threadIdx.x + u * NT;
+            xr[u] = Raw{};
+            zr[u] = Raw{};
+            if (i < nv) {
+                xr[u] = __ldcs(x + i);
+                if (GATE) zr[u] = __ldcs(z + i);
+            }
+        }
+        float v[V][VN], s = 0.0f;
+#pragma unroll
+        for (int u = 0; u < V; ++u) {
+            X::widen(xr[u], v[u]);
+#pragma unroll
+            for (int i = 0; i < VN; ++i) s += v[u][i];
+        }
+        const float mean = block_sum<NT>(s, red) * a.inv_d;
+        s = 0.0f;
+#pragma unroll
+        for (int u = 0; u < V; ++u) {
+#pragma unroll
+            for (int i = 0; i < VN; ++i) {
+                v[u][i] -= mean;
+                if (threadIdx.x + u * NT < nv) s = fmaf(v[u][i], v[u][i], s);
+            }
+        }
+        const float rs = 1.0f / sqrtf(fmaf(block_sum<NT>(s, red), a.inv_d, a.eps));
+#pragma unroll
+        for (int u = 0; u < V; ++u) {
+            const int i = threadIdx.x + u * NT;
+            if (i < nv) {
+                float ga[VN], be[VN];
+                load_affine<VN>(a.gamma, a.beta, gi * a.d + i * VN, true, ga, be);
+                __stcs(static_cast<Raw *>(a.y) + at + i, finish<IO, GATE>(v[u], rs, ga, be, zr[u], a.act));
+            }
+        }
+    }
+}
 
 // any sizes: one block per (row, group), three passes over the group
 template <typename IO>
 __global__ void __launch_bounds__(128)
-    group_norm_any_kernel(const IO *__restrict__ x, const IO *__restrict__ z, const float *__restrict__ gamma,
-                          const float *__restrict__ beta, IO *__restrict__ y, int64_t NG, int64_t C, int64_t G,
-                          int64_t d, float eps, int act) {
+    group_norm_any_kernel(const NormArgs a) {
     __shared__ float red[4];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    auto total = [&](float v) -> float {
-#pragma unroll
-        for (int m = 16; m >= 1; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
-        __syncthreads();
-        if (lane == 0) red[warp] = v;
-        __syncthreads();
-        return (red[0] + red[1]) + (red[2] + red[3]);
-    };
-    for (int64_t r = blockIdx.x; r < NG; r += gridDim.x) {
-        const int64_t row = r / G, gi = r - row * G;
-        const int64_t at = row * C + gi * d;
+    const IO *x = static_cast<const IO *>(a.x), *z = static_cast<const IO *>(a.z);
+    IO *y = static_cast<IO *>(a.y);
+    for (int64_t rg = blockIdx.x; rg < a.N * a.G; rg += gridDim.x) {
+        const int gi = int(rg % a.G);
+        const int64_t at = rg * a.d;
         float s = 0.0f;
-        for (int64_t i = threadIdx.x; i < d; i += 128) s += Io<IO>::to_f(x[at + i]);
-        const float mean = total(s) / float(d);
+        for (int i = threadIdx.x; i < a.d; i += 128) s += Io<IO>::to_f(x[at + i]);
+        const float mean = block_sum<128>(s, red) * a.inv_d;
         s = 0.0f;
-        for (int64_t i = threadIdx.x; i < d; i += 128) {
+        for (int i = threadIdx.x; i < a.d; i += 128) {
             const float t = Io<IO>::to_f(x[at + i]) - mean;
             s = fmaf(t, t, s);
         }
-        const float rs = 1.0f / sqrtf(total(s) / float(d) + eps);
-        for (int64_t i = threadIdx.x; i < d; i += 128) {
-            const int64_t c = gi * d + i;
+        const float rs = 1.0f / sqrtf(fmaf(block_sum<128>(s, red), a.inv_d, a.eps));
+        for (int i = threadIdx.x; i < a.d; i += 128) {
+            const int c = gi * a.d + i;
             float n = (Io<IO>::to_f(x[at + i]) - mean) * rs;
-            if (gamma != nullptr) n *= gamma[c];
-            if (beta != nullptr) n += beta[c];
-            if (act == LR_ACT_SILU) n = silu_f(n);
+            if (a.gamma != nullptr) n *= a.gamma[c];
+            if (a.beta != nullptr) n += a.beta[c];
+            if (a.act == LR_ACT_SILU) n = silu_f(n);
             if (z != nullptr) n *= silu_f(Io<IO>::to_f(z[at + i]));
             y[at + i] = Io<IO>::from_f(n);
         }
@@ -87,12 +271,60 @@ __global__ void __launch_bounds__(128)
 }
 
 template <typename IO>
-int norm_io(const IO *x, const IO *z, const float *gamma, const float *beta, IO *y, int64_t N, int64_t C,
-            int64_t G, float eps, int act, cudaStream_t s) {
-    const int64_t NG = N * G;
-    const unsigned grid = unsigned(NG < (1 << 20) ? NG : (1 << 20));
-    group_norm_any_kernel<IO><<<grid, 128, 0, s>>>(x, z, gamma, beta, y, NG, C, G, C / G, eps, act);
+int launch_any(const NormArgs &a, int sms, cudaStream_t s) {
+    const int64_t ng = a.N * a.G, most = int64_t(sms) * 128;
+    group_norm_any_kernel<IO><<<unsigned(ng < most ? ng : most), 128, 0, s>>>(a);
     return cudaGetLastError() == cudaSuccess ? LR_OK : LR_ERR_CUDA;
+}
+
+template <typename IO, int TL, int V, bool GATE>
+int launch_lanes(const NormArgs &a, int sms, cudaStream_t s) {
+    constexpr int SETS = 256 / TL;
+    const int gper = a.G < SETS ? a.G : SETS, rper = SETS / gper;
+    const int gy = (a.G + gper - 1) / gper;
+    // rows in flight per thread: enough bytes to cover the memory latency once
+    // every SM has its blocks, one row each where there are few
+    const int64_t row_blocks = (a.N + rper - 1) / rper;
+    const int64_t full = int64_t(sms) * 6;   // resident blocks
+    constexpr int R = V == 1 ? 4 : 2;
+    const bool deep = row_blocks * gy >= full * R;
+    int64_t gx = deep ? (full + gy - 1) / gy : row_blocks;
+    if (gx > row_blocks) gx = row_blocks;
+    if (gy > 65535) return launch_any<IO>(a, sms, s);
+    const dim3 grid{unsigned(gx), unsigned(gy), 1};
+    if (deep)
+        group_norm_lanes_kernel<IO, TL, V, R, GATE><<<grid, 256, 0, s>>>(a);
+    else
+        group_norm_lanes_kernel<IO, TL, V, 1, GATE><<<grid, 256, 0, s>>>(a);
+    return cudaGetLastError() == cudaSuccess ? LR_OK : LR_ERR_CUDA;
+}
+
+template <typename IO, int NT, int V, bool GATE>
+int launch_block(const NormArgs &a, int sms, cudaStream_t s) {
+    const int64_t ng = a.N * a.G, most = int64_t(sms) * (2048 / NT) * 8;
+    group_norm_block_kernel<IO, NT, V, GATE><<<unsigned(ng < most ? ng : most), NT, 0, s>>>(a);
+    return cudaGetLastError() == cudaSuccess ? LR_OK : LR_ERR_CUDA;
+}
+
+template <typename IO, bool GATE>
+int norm_gate(const NormArgs &a, cudaStream_t s) {
+    constexpr int VN = Vec16<IO>::N;
+    int sms = 0;
+    if (device_sm_count(&sms) != LR_OK) return LR_ERR_CUDA;
+    if (a.d % VN == 0) {   // C is a multiple of d, so every group starts on 16 bytes
+        const int nv = a.d / VN;
+        if (nv <= 4) return launch_lanes<IO, 4, 1, GATE>(a, sms, s);
+        if (nv <= 8) return launch_lanes<IO, 8, 1, GATE>(a, sms, s);
+        if (nv <= 16) return launch_lanes<IO, 16, 1, GATE>(a, sms, s);
+        if (nv <= 32) return launch_lanes<IO, 32, 1, GATE>(a, sms, s);
+        if (nv <= 64) return launch_lanes<IO, 32, 2, GATE>(a, sms, s);
+        if (nv <= 128) return launch_block<IO, 128, 1, GATE>(a, sms, s);
+        if (nv <= 256) return launch_block<IO, 256, 1, GATE>(a, sms, s);
+        if (nv <= 512) return launch_block<IO, 256, 2, GATE>(a, sms, s);
+        if (nv <= 1024) return launch_block<IO, 256, 4, GATE>(a, sms, s);
+        if (nv <= 2048) return launch_block<IO, 512, 4, GATE>(a, sms, s);
+    }
+    return launch_any<IO>(a, sms, s);
 }
 
 }  // namespace
@@ -100,11 +332,10 @@ int norm_io(const IO *x, const IO *z, const float *gamma, const float *beta, IO 
 int group_norm_act_launch(const void *x, const void *z, const float *gamma, const float *beta, void *y,
                           int64_t N, int64_t C, int64_t G, float eps, int act, int io_bf16, cudaStream_t stream) {
     if (N == 0 || C == 0) return LR_OK;
-    using bf = __nv_bfloat16;
-    return io_bf16 ? norm_io<bf>(static_cast<const bf *>(x), static_cast<const bf *>(z), gamma, beta,
-                                 static_cast<bf *>(y), N, C, G, eps, act, stream)
-                   : norm_io<float>(static_cast<const float *>(x), static_cast<const float *>(z), gamma, beta,
-                                    static_cast<float *>(y), N, C, G, eps, act, stream);
+    const int d = int(C / G);
+    const NormArgs a{x, z, gamma, beta, y, N, int(C), int(G), d, eps, 1.0f / float(d), act};
+    if (io_bf16) return z != nullptr ? norm_gate<__nv_bfloat16, true>(a, stream) : norm_gate<__nv_bfloat16, false>(a, stream);
+    return z != nullptr ? norm_gate<float, true>(a, stream) : norm_gate<float, false>(a, stream);
 }
 
 }  // namespace lr
