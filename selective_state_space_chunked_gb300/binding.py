@@ -850,25 +850,31 @@ def group_norm_act(x, G: int, gamma=None, beta=None, z=None, act: str = "none", 
     neighbouring channels, then gamma, beta ((C,) fp32 or None), the activation
     ("none" or "silu") and the gate silu(z) (z like x, or None).  Statistics are
     per row.  ``out`` gives the result tensor (x or z itself is allowed)."""
-    if act not in _ACT:
+    a = _ACT.get(act)
+    if a is None:
         raise ValueError(f"unknown activation {act!r}; use one of {sorted(_ACT)}")
-    C = x.shape[-1]
+    shape = x.shape
+    C = shape[-1]
     if G < 1 or C % G:
         raise ValueError(f"{C} channels cannot be split into {G} groups")
-    _shaped(z, x.shape, "z")
-    _shaped(gamma, (C,), "gamma")
-    _shaped(beta, (C,), "beta")
-    _same(x, z)
     io = _io_of(x)
-    dev = _target_device(x)
-    x, z = _act(x, dev), _act(z, dev)
-    gamma, beta = _par(gamma, dev), _par(beta, dev)
+    if z is not None:
+        _shaped(z, shape, "z")
+        _same(x, z)
+    if gamma is not None:
+        _shaped(gamma, (C,), "gamma")
+    if beta is not None:
+        _shaped(beta, (C,), "beta")
+    dev = x.device if x.is_cuda else _target_device(x)
+    z, gamma, beta = _act(z, dev), _par(gamma, dev), _par(beta, dev)
+    if not (x.is_cuda and x.is_contiguous()):
+        x = _dev(x, dev)
     if out is None:
         out = torch.empty_like(x)
-    elif out.shape != x.shape or out.dtype != x.dtype or out.device != dev or not out.is_contiguous():
-        raise ValueError(f"out must be a contiguous {x.dtype} GPU tensor of shape {tuple(x.shape)}")
+    elif out.shape != shape or out.dtype != x.dtype or out.device != dev or not out.is_contiguous():
+        raise ValueError(f"out must be a contiguous {x.dtype} GPU tensor of shape {tuple(shape)}")
     rc = _lib.lr_group_norm_act(x.data_ptr(), _ptr(z), _ptr(gamma), _ptr(beta), out.data_ptr(),
-                                x.numel() // C if C else 0, C, G, eps, _ACT[act], io, _stream_of(x))
+                                x.numel() // C if C else 0, C, G, eps, a, io, _stream_of(x))
     if rc != LR_OK:
         _check(rc, "lr_group_norm_act")
     return out

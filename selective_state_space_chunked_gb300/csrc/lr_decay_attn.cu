@@ -4,10 +4,9 @@
 namespace lr {
 
 namespace {
-// CUDA-core kernel: blocks that fill the GPU (three of 64 threads per SM:
-// their staging buffers and state registers), and the shortest segment worth
-// the second pass over k and v.
-constexpr int64_t kGenBlocksPerSm = 3;
+// CUDA-core kernel: blocks that fill the GPU (four of 128 threads per SM: their
+// state registers), and the shortest segment worth the second pass over k and v.
+constexpr int64_t kGenBlocksPerSm = 4;
 constexpr int64_t kGenMinSeg = 128;
 constexpr int64_t kMaxSeg = 32;
 // Tensor-core kernel: the shortest sequence it takes, and costs in units of a

@@ -3,7 +3,7 @@
 //
 //   S_t = a_t S_{t-1} + v_t k_t^T,   o_t = scale S_t q_t,   a_t = exp(l_t)
 //
-// Step by step in fp32.  A block of 64 threads owns RB value rows of one
+// Step by step in fp32.  A block owns RB value rows of one
 // (batch row, head, time segment); a thread owns RT rows and CPT key columns
 // of each, in registers, so P = DKP / CPT consecutive lanes share a row.  The
 // columns come in groups of four dealt round-robin, so the lanes of a row
@@ -28,28 +28,36 @@
 namespace lr {
 namespace {
 
-constexpr int kGT = 64;   // threads per block
 constexpr int kGB = 3;    // staging buffers
 
+// A thread holds RT x CPT state elements.  4 x 16 leaves room for four warps
+// per scheduler; 4 x 32 and 8 x 16 read less from shared memory per element but
+// leave 1.5, and the packed fp32 pipe was then busy 37 % of the time (278 us at
+// B2 L2048 H16 d128 fp32).
 template <int DKP_, bool NARROW>
 struct DecCfg {
     static constexpr int DKP = DKP_;
-    static constexpr int CPT = NARROW ? (DKP == 32 ? 8 : 16) : (DKP == 32 ? 16 : 32);
-    static constexpr int RT = NARROW ? 1 : (DKP <= 64 ? 2 : 4);
+    static constexpr int CPT = DKP == 32 ? 8 : 16;
+    static constexpr int RT = NARROW ? 1 : 4;
+    static constexpr int NT = NARROW || DKP <= 64 ? 64 : 128;   // threads per block
     static constexpr int P = DKP / CPT;
-    static constexpr int RB = RT * kGT / P;
+    static constexpr int RB = RT * NT / P;
     static constexpr int KB = DKP < 256 ? DKP : 256;   // key columns per TMA box
     static constexpr int NH = DKP / KB;
-    static constexpr int TC = DKP <= 128 ? 16 : 2048 / DKP;
-    static constexpr int KT = TC * DKP, VT = TC * RB;
+    // steps per staged chunk: 4 KB of k at most
+    template <typename IO>
+    __host__ __device__ static constexpr int steps() {
+        return 4096 / int(DKP * sizeof(IO)) < 16 ? 4096 / int(DKP * sizeof(IO)) : 16;
+    }
     template <typename IO>
     __host__ __device__ static constexpr int pitch(int n) {
         return int((n * sizeof(IO) + 127) / 128 * 128 / sizeof(IO));
     }
     template <typename IO>
     static constexpr size_t smem_bytes() {
-        return sizeof(IO) * size_t(kGB) * (2 * pitch<IO>(KT) + pitch<IO>(VT)) + sizeof(float) * (VT + 8 * TC) +
-               kGB * sizeof(uint64_t) + 128;
+        constexpr int TC = steps<IO>();
+        return sizeof(IO) * size_t(kGB) * (2 * pitch<IO>(TC * DKP) + pitch<IO>(TC * RB)) +
+               sizeof(float) * (TC * RB + 8 * TC) + kGB * sizeof(uint64_t) + 128;
     }
 };
 
@@ -66,39 +74,35 @@ __device__ __forceinline__ float4 dec_ld4<__nv_bfloat16>(const __nv_bfloat16 *p)
                        __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xffff0000u));
 }
 
-// sums of RT values over the P lanes of a row group: lane p ends with the sum
-// of value p % RT in `r` (for P < RT, with values p, p + P, ...)
+// Sums of RT values over the P lanes of a row group.  RT <= P: a reduce-scatter
+// (RT - 1 shuffles), after which lane p holds the sum of value p % RT in a[0];
+// RT = 1: every lane holds the sum.
 template <int RT, int P>
 __device__ __forceinline__ void row_sums(float (&a)[RT], int p) {
-    if constexpr (RT == 4 && P >= 4) {   // reduce-scatter: 3 shuffles instead of 8
-        const bool b0 = p & 1, b1 = p & 2;
-        float x = b0 ? a[1] : a[0], xs = b0 ? a[0] : a[1];
-        float y = b0 ? a[3] : a[2], ys = b0 ? a[2] : a[3];
-        x += __shfl_xor_sync(0xffffffffu, xs, 1);
-        y += __shfl_xor_sync(0xffffffffu, ys, 1);
-        float w = b1 ? y : x, ws = b1 ? x : y;
-        w += __shfl_xor_sync(0xffffffffu, ws, 2);
+    static_assert(RT <= P, "a lane per value");
 #pragma unroll
-        for (int m = P / 2; m >= 4; m >>= 1) w += __shfl_xor_sync(0xffffffffu, w, m);
-        a[0] = w;   // value p & 3
-    } else {
+    for (int m = 1, n = RT; m < RT; m <<= 1, n >>= 1) {   // n values left, lanes m apart
+        const bool up = p & m;
 #pragma unroll
-        for (int i = 0; i < RT; ++i) {
-#pragma unroll
-            for (int m = P / 2; m >= 1; m >>= 1) a[i] += __shfl_xor_sync(0xffffffffu, a[i], m);
+        for (int i = 0; i < n / 2; ++i) {
+            const float keep = up ? a[2 * i + 1] : a[2 * i], send = up ? a[2 * i] : a[2 * i + 1];
+            a[i] = keep + __shfl_xor_sync(0xffffffffu, send, m);
         }
     }
+#pragma unroll
+    for (int m = RT; m < P; m <<= 1) a[0] += __shfl_xor_sync(0xffffffffu, a[0], m);
 }
 
 // STATE_ONLY: the first launch of a segmented call (no q, no output; segments
 // 0 .. n_seg - 2).
 template <typename IO, typename C, bool STATE_ONLY>
-__global__ void __launch_bounds__(kGT, C::RT == 4 ? 4 : 6)
+__global__ void __launch_bounds__(C::NT, C::NT == 128 ? 4 : 8)
     decay_general_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                          const __grid_constant__ CUtensorMap tm_v, const DecayArgs a, int nrb, bool tma,
                          uint64_t timeout_ns, StatusRef sref) {
-    constexpr int CPT = C::CPT, RT = C::RT, P = C::P, RB = C::RB, KB = C::KB, TC = C::TC, VT = C::VT;
-    constexpr int KT = C::template pitch<IO>(C::KT), VTP = C::template pitch<IO>(VT);
+    constexpr int CPT = C::CPT, RT = C::RT, P = C::P, RB = C::RB, KB = C::KB, NT = C::NT;
+    constexpr int TC = C::template steps<IO>(), VT = TC * RB;
+    constexpr int KT = C::template pitch<IO>(TC * C::DKP), VTP = C::template pitch<IO>(VT);
     extern __shared__ __align__(128) unsigned char smem[];
     IO *ks = reinterpret_cast<IO *>(smem);   // [GB][NH][TC][KB] (pitch KT)
     IO *qs = ks + kGB * KT;
@@ -139,8 +143,8 @@ __global__ void __launch_bounds__(kGT, C::RT == 4 ? 4 : 6)
             fence_mbar_init();
         }
     } else {   // what the element copies never write: columns past dk, rows past dv
-        for (int e = tid; e < kGB * KT; e += kGT) ks[e] = qs[e] = Io<IO>::from_f(0.0f);
-        for (int e = tid; e < kGB * VTP; e += kGT) vs[e] = Io<IO>::from_f(0.0f);
+        for (int e = tid; e < kGB * KT; e += NT) ks[e] = qs[e] = Io<IO>::from_f(0.0f);
+        for (int e = tid; e < kGB * VTP; e += NT) vs[e] = Io<IO>::from_f(0.0f);
     }
 
     const int nchunks = (nrun + TC - 1) / TC;
@@ -149,7 +153,7 @@ __global__ void __launch_bounds__(kGT, C::RT == 4 ? 4 : 6)
         IO *kd = ks + buf * KT, *qd = qs + buf * KT, *vd = vs + buf * VTP;
         if (tma) {
             if (tid == 0) {
-                mbar_arrive_expect_tx(&full[buf], uint32_t(sizeof(IO)) * ((STATE_ONLY ? 1 : 2) * C::KT + VT));
+                mbar_arrive_expect_tx(&full[buf], uint32_t(sizeof(IO)) * ((STATE_ONLY ? 1 : 2) * TC * C::DKP + VT));
                 const int row = int(t_base) + t0;
 #pragma unroll
                 for (int hh = 0; hh < C::NH; ++hh) {
@@ -162,12 +166,12 @@ __global__ void __launch_bounds__(kGT, C::RT == 4 ? 4 : 6)
             const int nt = min(TC, nrun - t0);
             for (int t = 0; t < nt; ++t) {
                 const size_t sk = size_t(t0 + t) * HK, sv = size_t(t0 + t) * HV;
-                for (int j = tid; j < dk; j += kGT) {
+                for (int j = tid; j < dk; j += NT) {
                     const int at = (j / KB) * TC * KB + t * KB + j % KB;
                     kd[at] = kb[sk + j];
                     if (!STATE_ONLY) qd[at] = qb[sk + j];
                 }
-                for (int r = tid; r < rbv; r += kGT) vd[t * RB + r] = vb[sv + r];
+                for (int r = tid; r < rbv; r += NT) vd[t * RB + r] = vb[sv + r];
             }
         }
     };
@@ -331,13 +335,7 @@ __global__ void __launch_bounds__(kGT, C::RT == 4 ? 4 : 6)
                     r[rr] = (acc[rr][0].x + acc[rr][0].y) + (acc[rr][1].x + acc[rr][1].y);
                 row_sums<RT, P>(r, p);
                 const float ut = u[t];
-                if constexpr (RT == 4 && P >= 4) {
-                    if (p < 4) os[t * RB + rg * RT + p] = ut * r[0];
-                } else {
-#pragma unroll
-                    for (int rr = 0; rr < RT; ++rr)
-                        if (p == rr % P) os[t * RB + rg * RT + rr] = ut * r[rr];
-                }
+                if (p < RT) os[t * RB + rg * RT + p] = ut * r[0];
             }
         }
         if (!steep && after != 1.0f) {
@@ -349,7 +347,7 @@ __global__ void __launch_bounds__(kGT, C::RT == 4 ? 4 : 6)
         if (tid < 32 && more) factors(c + 1, gn);   // its buffer was last read in chunk c - 1
         __syncthreads();   // chunk c's buffer, every os entry, the next factors
         if (!STATE_ONLY) {
-            for (int e = tid; e < TC * RB; e += kGT) {
+            for (int e = tid; e < TC * RB; e += NT) {
                 const int t = e / RB, r = e % RB;
                 if (t < nt && r < rbv) ob[size_t(c * TC + t) * HV + r] = Io<IO>::from_f(os[e]);
             }
@@ -360,7 +358,7 @@ __global__ void __launch_bounds__(kGT, C::RT == 4 ? 4 : 6)
     // steps of the segment past the row's length
     if (!STATE_ONLY) {
         const int64_t nseg_steps = send - s0;
-        for (int64_t e = int64_t(nrun) * RB + tid; e < nseg_steps * RB; e += kGT) {
+        for (int64_t e = int64_t(nrun) * RB + tid; e < nseg_steps * RB; e += NT) {
             const int64_t t = e / RB;
             const int r = int(e % RB);
             if (r < rbv) ob[size_t(t) * HV + r] = Io<IO>::from_f(0.0f);
@@ -394,6 +392,7 @@ __global__ void __launch_bounds__(kGT, C::RT == 4 ? 4 : 6)
 
 template <typename IO, typename C>
 int launch_general_cfg(const DecayArgs &a, StatusRef st, cudaStream_t stream) {
+    constexpr int TC = C::template steps<IO>();
     const int nrb = (a.dv + C::RB - 1) / C::RB;
     const size_t es = sizeof(IO);
     auto al = [](const void *x) { return (reinterpret_cast<uintptr_t>(x) & 15u) == 0; };
@@ -404,9 +403,9 @@ int launch_general_cfg(const DecayArgs &a, StatusRef st, cudaStream_t stream) {
     if (tma) {
         const auto tt = Io<IO>::kTmType;
         const uint64_t rows = uint64_t(a.B) * a.L;
-        tma = encode_map_3d(&mq, a.q, tt, es, a.dk, a.Hk, rows, C::KB, 1, C::TC) &&
-              encode_map_3d(&mk, a.k, tt, es, a.dk, a.Hk, rows, C::KB, 1, C::TC) &&
-              encode_map_3d(&mv, a.v, tt, es, a.dv, a.H, rows, C::RB, 1, C::TC);
+        tma = encode_map_3d(&mq, a.q, tt, es, a.dk, a.Hk, rows, C::KB, 1, TC) &&
+              encode_map_3d(&mk, a.k, tt, es, a.dk, a.Hk, rows, C::KB, 1, TC) &&
+              encode_map_3d(&mv, a.v, tt, es, a.dv, a.H, rows, C::RB, 1, TC);
     }
     const size_t smem = C::template smem_bytes<IO>();
     auto first = decay_general_kernel<IO, C, true>;
@@ -418,14 +417,14 @@ int launch_general_cfg(const DecayArgs &a, StatusRef st, cudaStream_t stream) {
     const int64_t per_seg = a.B * a.H * nrb;
     if (per_seg * a.n_seg > INT32_MAX) return LR_ERR_UNSUPPORTED;
     if (a.n_seg > 1) {
-        first<<<unsigned(per_seg * (a.n_seg - 1)), kGT, smem, stream>>>(mq, mk, mv, a, nrb, tma, kDefaultTimeoutNs,
+        first<<<unsigned(per_seg * (a.n_seg - 1)), C::NT, smem, stream>>>(mq, mk, mv, a, nrb, tma, kDefaultTimeoutNs,
                                                                         st);
         if (cudaGetLastError() != cudaSuccess) return LR_ERR_CUDA;
     }
     // dependent launch: segment 0 needs nothing of the first launch
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(unsigned(per_seg * a.n_seg));
-    cfg.blockDim = dim3(kGT);
+    cfg.blockDim = dim3(C::NT);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
