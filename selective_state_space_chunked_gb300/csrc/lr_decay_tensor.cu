@@ -93,7 +93,7 @@ enum {
     W_READY = 22,    // weighted values of a quarter
     W_FREE = 26,
     M_READY = 30,    // decay factors of chunk c, [NM]
-    M_FREE = 34,     // taken by the 4 weight, 4 output (or 8 state) warps, [NM]
+    M_FREE = 34,     // taken by the 4 weight and 4 output warps, [NM]
     SB_READY = 38,   // bf16 state before chunk c (8 state warps)
     DS_DONE, DS_FREE,
     FIX,             // a steep chunk's Q S^T scaled (4 output warps)
@@ -125,6 +125,18 @@ __device__ __forceinline__ bool elect_one() {
 }
 __device__ __forceinline__ float lo_f(uint32_t u) { return __uint_as_float(u << 16); }
 __device__ __forceinline__ float hi_f(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
+
+// w times a pair of bf16 values in three bf16 terms: what each leaves goes to
+// the next, 24 bits in all.
+__device__ __forceinline__ void three_terms(float w, uint32_t v, uint32_t &t1, uint32_t &t2, uint32_t &t3) {
+    const float2 neg = make_float2(-1.0f, -1.0f);
+    float2 y = __fmul2_rn(make_float2(w, w), make_float2(lo_f(v), hi_f(v)));
+    t1 = pack(y.x, y.y);
+    y = __ffma2_rn(neg, make_float2(lo_f(t1), hi_f(t1)), y);
+    t2 = pack(y.x, y.y);
+    y = __ffma2_rn(neg, make_float2(lo_f(t2), hi_f(t2)), y);
+    t3 = pack(y.x, y.y);
+}
 
 // What a wait that does not succeed at once needs, in shared memory.
 struct Ctl {
@@ -163,7 +175,300 @@ __device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, Ctl *ctl) 
 }
 }  // namespace dt
 
-template <bool STATE_ONLY>
+
+// ---------------------------------------------------------------------------
+// The state that a segment builds from its own steps (the first launch of a
+// segmented call).  Every step's weight is taken to the segment's end,
+// w_s = 2^(the log2 decay of the steps after s) <= 1, so the update
+//   dS = K^T diag(w) V
+// runs through all chunks in one accumulator, with nothing read back between
+// them.  The total decay comes first, from a sum over the segment's gates.
+// Roles: TMA (K, V three chunks deep), scan (4 warps, a step per lane: weights
+// of the next chunks), weight (8 warps: the three terms of w_s v_s, half chunks
+// in a ring of three), MMA (M=128 N=192).
+namespace ds {
+constexpr int C = kDecayChunk, RB = kDecayRows;
+constexpr int NS = 3, NW = 3, NM = 4;
+constexpr int WEIGHTS = 8, SCAN = 8, TMA_WARP = 12, MMA_WARP = 13, THREADS = 14 * 32;
+constexpr uint32_t HALF = C * 128, K_BYTES = 2 * HALF, V_BYTES = C * RB * 2;
+constexpr uint32_t T_BYTES = 64 * RB * 2;      // one term of half a chunk
+constexpr uint32_t OFF_K = 0, OFF_V = NS * K_BYTES, OFF_W = OFF_V + NS * V_BYTES;
+constexpr uint32_t OFF_WT = OFF_W + NW * 3 * T_BYTES;
+constexpr uint32_t OFF_BAR = OFF_WT + NM * C * 4;
+enum {
+    FULL_K = 0, EMPTY_K = FULL_K + NS, FULL_V = EMPTY_K + NS, EMPTY_V = FULL_V + NS,
+    W_READY = EMPTY_V + NS, W_FREE = W_READY + NW, M_READY = W_FREE + NW, M_FREE = M_READY + NM,
+    DONE = M_FREE + NM, NBAR
+};
+constexpr uint32_t OFF_TOT = OFF_BAR + NBAR * 8;   // the total, then 2 x 4 sums of the scan warps
+constexpr uint32_t OFF_CTL = OFF_TOT + 9 * 8;
+constexpr uint32_t OFF_TMEM = OFF_CTL + 32;
+constexpr uint32_t SMEM = OFF_TMEM + 8;
+static_assert(SMEM <= 227 * 1024, "one block per SM");
+constexpr uint32_t TMEM_COLS = 256;
+constexpr uint32_t IDESC = umma_idesc_bf16(128, 192, 1, 1);
+}  // namespace ds
+
+__global__ void __launch_bounds__(ds::THREADS, 1)
+    decay_state_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                       const DecayArgs a, int n_vt, uint64_t timeout_ns, StatusRef sref) {
+    using namespace ds;
+    using dt::arrive;
+    using dt::Ctl;
+    using dt::hi_f;
+    using dt::lo_f;
+    using dt::pack;
+    using bf = __nv_bfloat16;
+    extern __shared__ __align__(1024) unsigned char sm[];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    launch_dependents();
+    if (tid == 0 && blockIdx.x == 0) status_begin(sref);
+    if ((smem_u32(sm) & 1023u) != 0) {   // swizzled tiles need a 1024-byte aligned base
+        if (tid == 0) status_report(sref, LR_ERR_CUDA);
+        return;
+    }
+    const int nseg = a.n_seg - 1;
+    int x = blockIdx.x;
+    const int vt = x % n_vt;
+    x /= n_vt;
+    const int seg = x % nseg, bh = x / nseg;
+    const int b = bh / a.H, h = bh - b * a.H, hk = h / (a.H / a.Hk);
+    const int len = dec::row_len(a.lens, b, a.L);
+    const int s0 = int(int64_t(seg) * a.seg_len);
+    const int nrun = max(0, min(len, int(min(a.L, int64_t(s0) + a.seg_len))) - s0);
+    const int n_chunks = (nrun + C - 1) / C;
+    const int dk = a.dk, dv = a.dv;
+    const bool two = dk > 64;
+
+    uint64_t *bar = reinterpret_cast<uint64_t *>(sm + OFF_BAR);
+    unsigned long long *total = reinterpret_cast<unsigned long long *>(sm + OFF_TOT);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + OFF_TMEM);
+    Ctl *ctl = reinterpret_cast<Ctl *>(sm + OFF_CTL);
+    float *sW = reinterpret_cast<float *>(sm + OFF_WT);
+    if (tid == 0) {
+        for (int i = 0; i < NBAR; ++i) {
+            const bool by_weights = (i >= EMPTY_V && i < W_FREE) || (i >= M_FREE && i < DONE);
+            mbar_init(&bar[i], by_weights ? WEIGHTS : i >= M_READY && i < M_FREE ? 4 : 1);
+        }
+        *ctl = Ctl{sref.word, sref.stamp, timeout_ns, 0};
+        *total = 0;
+        fence_mbar_init();
+    }
+    if (warp == 0) tmem_alloc(tmem_slot, TMEM_COLS);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    auto hw = [&](int i, int phase) -> bool {
+        const uint32_t parity = uint32_t(phase) & 1u;
+        return mbar_try_wait(&bar[i], parity) || dt::wait_slow(smem_u32(&bar[i]), parity, ctl);
+    };
+    if (warp == TMA_WARP && lane == 0) {   // the first chunks are on their way during the sum
+        prefetch_tensormap(&tm_k);
+        prefetch_tensormap(&tm_v);
+    }
+    auto load_k = [&](int c) {
+        const int st = c % NS;
+        mbar_arrive_expect_tx(&bar[FULL_K + st], two ? K_BYTES : HALF);
+        tma_load_4d(sm + OFF_K + st * K_BYTES, &tm_k, &bar[FULL_K + st], 0, hk, s0 + c * C, b);
+        if (two) tma_load_4d(sm + OFF_K + st * K_BYTES + HALF, &tm_k, &bar[FULL_K + st], 64, hk, s0 + c * C, b);
+    };
+    auto load_v = [&](int c) {
+        const int st = c % NS;
+        mbar_arrive_expect_tx(&bar[FULL_V + st], V_BYTES);
+        tma_load_4d(sm + OFF_V + st * V_BYTES, &tm_v, &bar[FULL_V + st], vt * RB, h, s0 + c * C, b);
+    };
+    const int first = min(NS, n_chunks);
+    if (warp == TMA_WARP && lane == 0)
+        for (int c = 0; c < first; ++c) {
+            load_k(c);
+            load_v(c);
+        }
+    // the segment's total log2 decay
+    const float lh = a.a_log == nullptr ? 0.0f : a.a_log[h];
+    const bf *g = a.g == nullptr ? nullptr : static_cast<const bf *>(a.g) + (size_t(b) * a.L + s0) * a.H + h;
+    bool bad = false;
+    {
+        long long sum = 0;
+        for (int t = tid; t < nrun; t += THREADS)
+            sum += dec::to_fix(lh + (g != nullptr ? __bfloat162float(g[size_t(t) * a.H]) : 0.0f), bad);
+#pragma unroll
+        for (int m = 16; m >= 1; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
+        if (lane == 0 && sum != 0) atomicAdd(total, static_cast<unsigned long long>(sum));
+        if (bad) status_report(sref, LR_ERR_RANGE);
+    }
+    __syncthreads();
+    const long long tot = static_cast<long long>(*total);
+
+    if (warp == TMA_WARP) {
+        if (lane == 0) {
+            int nk = first, nv = first;
+            for (; nv < n_chunks; ++nv) {   // V is released first
+                if (!hw(EMPTY_V + nv % NS, nv / NS - 1)) break;
+                load_v(nv);
+                if (!hw(EMPTY_K + nk % NS, nk / NS - 1)) break;
+                load_k(nk);
+                ++nk;
+            }
+            // copies still in flight land before the block exits
+            for (int c = max(nk - NS, 0); c < nk; ++c) mbar_wait_bounded(&bar[FULL_K + c % NS], (c / NS) & 1, timeout_ns);
+            for (int c = max(nv - NS, 0); c < nv; ++c) mbar_wait_bounded(&bar[FULL_V + c % NS], (c / NS) & 1, timeout_ns);
+        }
+    } else if (warp == MMA_WARP) {
+        auto hu = [&](int i, int phase) -> bool { return __all_sync(0xffffffffu, hw(i, phase)); };
+        const bool lead = dt::elect_one();
+        const uint32_t base = __shfl_sync(0xffffffffu, smem_u32(sm), 0);
+        bool ok = true;
+        for (int c = 0; ok && c < n_chunks; ++c) {
+            const int st = c % NS;
+            ok = hu(FULL_K + st, c / NS);
+            const uint64_t dK = umma_smem_desc(base + OFF_K + st * K_BYTES, HALF, 1024);
+            for (int hf = 0; ok && hf < 2; ++hf) {
+                const int q = 2 * c + hf, slot = q % NW;
+                ok = hu(W_READY + slot, q / NW);
+                if (!ok) break;
+                tc_fence_after();
+                const uint64_t dW = umma_smem_desc(base + OFF_W + slot * 3 * T_BYTES, T_BYTES, 1024);
+                if (lead) {   // 16 steps are 2048 bytes on, 128 in the descriptors' units
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        umma_bf16(tmem, dK + 512 * hf + 128 * kk, dW + 128 * kk, IDESC, q > 0 || kk > 0);
+                    umma_commit(&bar[W_FREE + slot]);
+                    if (hf == 1) umma_commit(&bar[EMPTY_K + st]);
+                }
+                __syncwarp();
+            }
+        }
+        if (lead) {
+            umma_commit(&bar[DONE]);
+            mbar_wait_bounded(&bar[DONE], 0, timeout_ns);
+        }
+        __syncwarp();
+    } else if (warp >= SCAN && warp < SCAN + 4) {
+        // lane i of scan warp w: step 32 w + i of the chunk
+        const int w4 = warp - SCAN, step = 32 * w4 + lane;
+        long long *sums = reinterpret_cast<long long *>(sm + OFF_TOT + 8);
+        long long run = 0;
+        auto load = [&](int c) -> float {
+            const int t = c * C + step;
+            return g != nullptr && t < nrun ? __bfloat162float(g[size_t(t) * a.H]) : 0.0f;
+        };
+        float gn = load(0);
+        for (int c = 0; c < n_chunks; ++c) {
+            long long incl = c * C + step < nrun ? dec::to_fix(lh + gn, bad) : 0;
+            if (c + 1 < n_chunks) gn = load(c + 1);
+#pragma unroll
+            for (int m = 1; m < 32; m <<= 1) {
+                const long long up = __shfl_up_sync(0xffffffffu, incl, m);
+                if (lane >= m) incl += up;
+            }
+            if (lane == 31) sums[4 * (c & 1) + w4] = incl;
+            const bool ok = c < NM || hw(M_FREE + c % NM, c / NM - 1);
+            int stop;   // the four warps leave together
+            asm volatile(
+                "{\n\t.reg .pred p, q;\n\tsetp.eq.s32 p, %1, 0;\n\tbar.red.or.pred q, 1, 128, p;\n\t"
+                "selp.s32 %0, 1, 0, q;\n\t}"
+                : "=r"(stop)
+                : "r"(ok ? 1 : 0)
+                : "memory");
+            if (stop) break;
+            long long before = run;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const long long v = sums[4 * (c & 1) + i];
+                if (i < w4) before += v;
+                run += v;
+            }
+            sW[(c % NM) * C + step] = dec::exp2_fix(tot - (before + incl));
+            __syncwarp();
+            if (lane == 0) arrive(&bar[M_READY + c % NM]);
+        }
+    } else if (warp < WEIGHTS) {
+        // 16-byte group (8 value rows) k8 of steps r32 and r32 + 32 of each half
+        const int r32 = tid >> 3, k8 = tid & 7;
+        for (int c = 0; c < n_chunks; ++c) {
+            const int st = c % NS, mt = c % NM;
+            unsigned char *V = sm + OFF_V + st * V_BYTES;
+            const bool tail = c * C + C > nrun;
+            bool ok = hw(M_READY + mt, c / NM) && hw(FULL_V + st, c / NS);
+            if (ok && tail) ok = hw(FULL_K + st, c / NS);
+            ok = __all_sync(0xffffffffu, ok);
+#pragma unroll 1
+            for (int hf = 0; ok && hf < 2; ++hf) {
+                const int q = 2 * c + hf, slot = q % NW;
+                uint4 u[2];
+                float w[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int s = 64 * hf + 32 * i + r32;   // step of the chunk
+                    const uint32_t at = sw128_offset(s, 8 * k8);
+                    u[i] = *reinterpret_cast<const uint4 *>(V + at);
+                    w[i] = sW[mt * C + s];
+                    if (tail && c * C + s >= nrun) {   // whatever stands there must not reach the product
+                        u[i] = make_uint4(0, 0, 0, 0);
+                        *reinterpret_cast<uint4 *>(sm + OFF_K + st * K_BYTES + at) = u[i];
+                        if (two) *reinterpret_cast<uint4 *>(sm + OFF_K + st * K_BYTES + HALF + at) = u[i];
+                    }
+                }
+                if (q >= NW && !__all_sync(0xffffffffu, hw(W_FREE + slot, q / NW - 1))) {
+                    ok = false;
+                    break;
+                }
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const uint32_t uv[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+                    uint32_t t1[4], t2[4], t3[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) dt::three_terms(w[i], uv[e], t1[e], t2[e], t3[e]);
+                    unsigned char *W = sm + OFF_W + slot * 3 * T_BYTES + sw128_offset(32 * i + r32, 8 * k8);
+                    *reinterpret_cast<uint4 *>(W) = make_uint4(t1[0], t1[1], t1[2], t1[3]);
+                    *reinterpret_cast<uint4 *>(W + T_BYTES) = make_uint4(t2[0], t2[1], t2[2], t2[3]);
+                    *reinterpret_cast<uint4 *>(W + 2 * T_BYTES) = make_uint4(t3[0], t3[1], t3[2], t3[3]);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) arrive(&bar[W_READY + slot]);
+            }
+            if (!ok) break;
+            if (lane == 0) {
+                arrive(&bar[EMPTY_V + st]);
+                arrive(&bar[M_FREE + mt]);
+            }
+        }
+        // key column j, value rows 32 sh .. of the block's 64
+        const int j = 32 * (warp & 3) + lane, sh = warp >> 2, i0 = vt * RB + 32 * sh;
+        const bool done = n_chunks > 0 && __all_sync(0xffffffffu, hw(DONE, 0));
+        tc_fence_after();
+        const uint32_t D = tmem + 32 * sh + (uint32_t((warp & 3) * 32) << 16);
+        const float f = dec::exp2_fix(tot);
+        const float *src = seg == 0 && a.S0 != nullptr ? a.S0 + (size_t(bh) * dv + i0) * dk + j : nullptr;
+        float *dst = a.seg_state + ((size_t(bh) * nseg + seg) * dv + i0) * dk + j;
+#pragma unroll
+        for (int q = 0; q < 32; q += 16) {
+            float d1[16] = {}, d2[16] = {}, d3[16] = {};
+            if (done) {
+                tmem_ld16_nowait(D + q, d1);
+                tmem_ld16_nowait(D + 64 + q, d2);
+                tmem_ld16_nowait(D + 128 + q, d3);
+                tmem_ld_wait_tied(d1, d2);
+                tmem_ld_wait_tied(d3);
+            }
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+                if (j < dk && i0 + q + r < dv) {
+                    const float y = d1[r] + (d2[r] + d3[r]);
+                    dst[size_t(q + r) * dk] = src != nullptr ? fmaf(f, src[size_t(q + r) * dk], y) : y;
+                }
+        }
+        if (vt == 0 && tid == 0) a.seg_tot[size_t(bh) * nseg + seg] = tot;
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 0) tmem_dealloc(tmem, TMEM_COLS);
+}
+
+// ---------------------------------------------------------------------------
 __global__ void __launch_bounds__(dt::THREADS, 1)
     decay_tensor_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                         const __grid_constant__ CUtensorMap tm_v, const DecayArgs a, int n_vt, uint64_t timeout_ns,
@@ -172,13 +477,12 @@ __global__ void __launch_bounds__(dt::THREADS, 1)
     using bf = __nv_bfloat16;
     extern __shared__ __align__(1024) unsigned char sm[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    if (STATE_ONLY) launch_dependents();
     if (tid == 0 && blockIdx.x == 0) status_begin(sref);
     if ((smem_u32(sm) & 1023u) != 0) {   // swizzled tiles need a 1024-byte aligned base
         if (tid == 0) status_report(sref, LR_ERR_CUDA);
         return;
     }
-    const int nseg = STATE_ONLY ? a.n_seg - 1 : a.n_seg;
+    const int nseg = a.n_seg;
     int x = blockIdx.x;
     const int vt = x % n_vt;
     x /= n_vt;
@@ -203,11 +507,11 @@ __global__ void __launch_bounds__(dt::THREADS, 1)
             int n = 1;
             if (i >= F_DONE && i < F_DONE + 2) n = 8;
             if (i >= K_DONE && i < K_DONE + 2) n = 4;
-            if (i >= M_FREE && i < M_FREE + NM) n = STATE_ONLY ? 12 : 8;
+            if (i >= M_FREE && i < M_FREE + NM) n = 8;
             if (i == SB_READY || i == DS_FREE) n = 8;
             if (i == FIX) n = 4;
             // K is read by dS and P, Q by P and OX, V by the weight warps (through dS) and OI
-            if (!STATE_ONLY && ((i >= EMPTY_Q && i < EMPTY_Q + 2) || (i >= EMPTY_K && i < EMPTY_K + 2) ||
+            if (((i >= EMPTY_Q && i < EMPTY_Q + 2) || (i >= EMPTY_K && i < EMPTY_K + 2) ||
                                 (i >= EMPTY_V && i < EMPTY_V + 2)))
                 n = 2;
             if (i == MMA_END) n = 3;
@@ -227,7 +531,7 @@ __global__ void __launch_bounds__(dt::THREADS, 1)
     };
 
     if (warp == K_WARP || warp == Q_WARP || warp == V_WARP) {   // --------- TMA
-        if (lane == 0 && !(STATE_ONLY && warp == Q_WARP)) {
+        if (lane == 0) {
             const CUtensorMap *tm = warp == K_WARP ? &tm_k : warp == Q_WARP ? &tm_q : &tm_v;
             const int full = warp == K_WARP ? FULL_K : warp == Q_WARP ? FULL_Q : FULL_V;
             const int empty = warp == K_WARP ? EMPTY_K : warp == Q_WARP ? EMPTY_Q : EMPTY_V;
@@ -279,7 +583,7 @@ __global__ void __launch_bounds__(dt::THREADS, 1)
                 }
                 if (!ok) break;
             }
-        } else if (!STATE_ONLY && warp == P_WARP) {
+        } else if (warp == P_WARP) {
             for (int c = 0; c < n_chunks; ++c) {
                 const int st = c & 1;
                 if (!hu(FULL_K + st, c >> 1) || !hu(FULL_Q + st, c >> 1)) break;
@@ -300,7 +604,7 @@ __global__ void __launch_bounds__(dt::THREADS, 1)
                 }
                 __syncwarp();
             }
-        } else if (!STATE_ONLY && warp == O_WARP) {
+        } else if (warp == O_WARP) {
             const uint64_t dS = umma_smem_desc(base + OFF_SB, HALF, 1024);
             int n_steep = 0;
             for (int c = 0; c < n_chunks; ++c) {
@@ -350,7 +654,7 @@ __global__ void __launch_bounds__(dt::THREADS, 1)
         // lane i: steps 4 i .. 4 i + 3 of the chunk
         const float lh = a.a_log == nullptr ? 0.0f : a.a_log[h];
         const bf *g = a.g == nullptr ? nullptr : static_cast<const bf *>(a.g) + (size_t(b) * a.L + s0) * a.H + h;
-        long long base = 0, tot = 0;
+        long long base = 0;
         int last = -1;   // the last steep chunk
         bool bad = false;
         float gn[4];
@@ -402,10 +706,8 @@ __global__ void __launch_bounds__(dt::THREADS, 1)
             __syncwarp();
             if (lane == 0) arrive(&bar[M_READY + (c & (NM - 1))]);
             base = re ? 0 : end;
-            tot = max(tot + all, -(1ll << 60));
         }
         if (bad) status_report(sref, LR_ERR_RANGE);
-        if (STATE_ONLY && vt == 0 && lane == 0) a.seg_tot[size_t(bh) * (a.n_seg - 1) + seg] = tot;
         // the decay that S^ still lacks, for the state that the block leaves
         if (lane == 0) *reinterpret_cast<float *>(sm + OFF_END) = dec::exp2_fix(base);
     } else if (warp >= WEIGHT) {   // ----------------------------------- weight
@@ -421,7 +723,6 @@ __global__ void __launch_bounds__(dt::THREADS, 1)
             if (ok && c >= 1) ok = hw(W_FREE + qt, c - 1);
             if (!__all_sync(0xffffffffu, ok)) break;
             const float w = sW[mt * C + s];
-            const float2 w2 = make_float2(w, w);
 #pragma unroll 1
             for (int k = 0; k < 8; ++k) {
                 const uint32_t at = sw128_offset(s, 8 * k);
@@ -430,14 +731,7 @@ __global__ void __launch_bounds__(dt::THREADS, 1)
                 const uint32_t uv[4] = {u.x, u.y, u.z, u.w};
                 uint32_t t1[4], t2[4], t3[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {   // what each term leaves goes to the next
-                    float2 y = __fmul2_rn(w2, make_float2(lo_f(uv[e]), hi_f(uv[e])));
-                    t1[e] = pack(y.x, y.y);
-                    y = __fadd2_rn(y, make_float2(-lo_f(t1[e]), -hi_f(t1[e])));
-                    t2[e] = pack(y.x, y.y);
-                    y = __fadd2_rn(y, make_float2(-lo_f(t2[e]), -hi_f(t2[e])));
-                    t3[e] = pack(y.x, y.y);
-                }
+                for (int e = 0; e < 4; ++e) three_terms(w, uv[e], t1[e], t2[e], t3[e]);
                 *reinterpret_cast<uint4 *>(sm + OFF_W + at) = make_uint4(t1[0], t1[1], t1[2], t1[3]);
                 *reinterpret_cast<uint4 *>(sm + OFF_W + V_BYTES + at) = make_uint4(t2[0], t2[1], t2[2], t2[3]);
                 *reinterpret_cast<uint4 *>(sm + OFF_W + 2 * V_BYTES + at) = make_uint4(t3[0], t3[1], t3[2], t3[3]);
@@ -462,7 +756,7 @@ __global__ void __launch_bounds__(dt::THREADS, 1)
         // rows 32 fw .. of P, columns 64 hf .. in blocks of 16; PD's go to the
         // first half of the same columns, which the warp has read by then
         const int fw = warp & 3, hf = (warp - FRONT) >> 2, t = 32 * fw + lane;
-        for (int c = 0; !STATE_ONLY && c < n_chunks; ++c) {
+        for (int c = 0; c < n_chunks; ++c) {
             const int st = c & 1;
             const uint32_t P = tmem + T_P + st * 128 + 64 * hf + (uint32_t(fw * 32) << 16);
             const int mt = c & (NM - 1);
@@ -533,7 +827,7 @@ __global__ void __launch_bounds__(dt::THREADS, 1)
         const int i0 = vt * RB;
         const size_t HV = size_t(a.H) * dv;
         bf *ob = static_cast<bf *>(a.o) + (size_t(b) * a.L + s0) * HV + size_t(h) * dv + i0;
-        for (int c = 0; !STATE_ONLY && c < n_chunks; ++c) {
+        for (int c = 0; c < n_chunks; ++c) {
             const int st = c & 1, mt = c & (NM - 1);
             const uint32_t O = tmem + T_O + lanes;
             if (!__all_sync(0xffffffffu, hw(M_READY + mt, c / NM))) break;
@@ -607,7 +901,7 @@ __global__ void __launch_bounds__(dt::THREADS, 1)
         for (int r = 0; r < 32; ++r)
             S[r] = a.S0 != nullptr && seg == 0 && j < dk && i0 + r < dv ? a.S0[(size_t(bh) * dv + i0 + r) * dk + j]
                                                                         : 0.0f;
-        if (!STATE_ONLY && seg > 0) {
+        if (seg > 0) {
             grid_dependency_wait();
             long long acc = 0;
 #pragma unroll 1
@@ -626,13 +920,13 @@ __global__ void __launch_bounds__(dt::THREADS, 1)
             const int mt = c & (NM - 1);
             bool ok = hw(M_READY + mt, c / NM);
             // the bf16 copy's buffer is free
-            if (ok && !STATE_ONLY && c >= 1) ok = hw(OX_DONE + ((c - 1) & 1), (c - 1) >> 1);
+            if (ok && c >= 1) ok = hw(OX_DONE + ((c - 1) & 1), (c - 1) >> 1);
             if (!__all_sync(0xffffffffu, ok)) break;
             const float m = sF[4 * mt];
             // the copy: what this chunk's weights assume, S or m S (a steep chunk
             // applies its factors by rows), as row j of 64 value rows in 8 swizzled groups
             const float pm = sF[4 * mt + 2] == 0.0f ? 1.0f : m;
-            if (!STATE_ONLY) {
+            {
                 const float2 p2 = make_float2(pm, pm);
 #pragma unroll
                 for (int q = 0; q < 32; q += 8) {
@@ -648,10 +942,7 @@ __global__ void __launch_bounds__(dt::THREADS, 1)
                 fence_proxy_async_smem();
             }
             __syncwarp();
-            if (lane == 0) {
-                if (!STATE_ONLY) arrive(&bar[SB_READY]);
-                if (STATE_ONLY) arrive(&bar[M_FREE + mt]);
-            }
+            if (lane == 0) arrive(&bar[SB_READY]);
             if (!__all_sync(0xffffffffu, hw(DS_DONE, c))) break;
             tc_fence_after();
             const float2 m2 = make_float2(m, m);
@@ -675,9 +966,7 @@ __global__ void __launch_bounds__(dt::THREADS, 1)
             if (lane == 0) arrive(&bar[DS_FREE]);
         }
         asm volatile("bar.sync 1, 288;" ::: "memory");   // the scan warp's last factor
-        float *out = STATE_ONLY ? a.seg_state + (size_t(bh) * (a.n_seg - 1) + seg) * dv * dk
-                     : seg == a.n_seg - 1 && a.S_final != nullptr ? a.S_final + size_t(bh) * dv * dk
-                                                                  : nullptr;
+        float *out = seg == a.n_seg - 1 && a.S_final != nullptr ? a.S_final + size_t(bh) * dv * dk : nullptr;
         if (out != nullptr && j < dk) {
             const float f = *reinterpret_cast<const float *>(sm + OFF_END);
 #pragma unroll
@@ -687,7 +976,7 @@ __global__ void __launch_bounds__(dt::THREADS, 1)
     }
     if (warp == SCAN_WARP) asm volatile("bar.sync 1, 288;" ::: "memory");
 
-    if (!STATE_ONLY) {   // whole chunks past the row's end
+    {   // whole chunks past the row's end
         const int g8 = min(RB, dv - vt * RB) / 8;
         const int64_t first = s0 + int64_t(n_chunks) * C;
         bf *ob = static_cast<bf *>(a.o) + size_t(h) * dv + vt * RB;
@@ -735,10 +1024,10 @@ bool dt_setup_once() {
     static std::once_flag once;
     static bool ok = false;
     std::call_once(once, [] {
-        ok = cudaFuncSetAttribute(decay_tensor_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                  int(dt::SMEM)) == cudaSuccess &&
-             cudaFuncSetAttribute(decay_tensor_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                  int(dt::SMEM)) == cudaSuccess;
+        ok = cudaFuncSetAttribute(decay_state_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(ds::SMEM)) ==
+                 cudaSuccess &&
+             cudaFuncSetAttribute(decay_tensor_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(dt::SMEM)) ==
+                 cudaSuccess;
     });
     return ok;
 }
@@ -754,8 +1043,8 @@ int decay_tensor_launch(const DecayArgs &a, StatusRef st, cudaStream_t stream) {
     const int64_t per_seg = a.B * a.H * n_vt;
     if (per_seg * a.n_seg > INT32_MAX) return LR_ERR_UNSUPPORTED;
     if (a.n_seg > 1) {
-        decay_tensor_kernel<true><<<unsigned(per_seg * (a.n_seg - 1)), dt::THREADS, dt::SMEM, stream>>>(
-            mq, mk, mv, a, n_vt, kDefaultTimeoutNs, st);
+        decay_state_kernel<<<unsigned(per_seg * (a.n_seg - 1)), ds::THREADS, ds::SMEM, stream>>>(
+            mk, mv, a, n_vt, kDefaultTimeoutNs, st);
         if (cudaGetLastError() != cudaSuccess) return LR_ERR_CUDA;
     }
     // dependent launch: segment 0 needs nothing of the first launch
@@ -769,7 +1058,7 @@ int decay_tensor_launch(const DecayArgs &a, StatusRef st, cudaStream_t stream) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = a.n_seg > 1 ? 1 : 0;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, decay_tensor_kernel<false>, mq, mk, mv, a, n_vt,
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, decay_tensor_kernel, mq, mk, mv, a, n_vt,
                                              uint64_t(kDefaultTimeoutNs), st);
     return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? LR_OK : LR_ERR_CUDA;
 }
