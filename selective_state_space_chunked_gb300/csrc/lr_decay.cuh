@@ -52,7 +52,7 @@ __device__ __forceinline__ float fix_f(long long x) {
 // so the result is as exact for large exponents as for small ones (these
 // factors multiply whole ranges of the state); 0 below 2^-126.
 __device__ __forceinline__ float exp2_fix(long long x) {
-    const int n = static_cast<int>(max(x >> 32, -127ll));
+    const int n = max(static_cast<int>(x >> 32), -127);
     return ex2_approx(static_cast<float>(static_cast<uint32_t>(x)) * kFixInv) * __int_as_float((n + 127) << 23);
 }
 

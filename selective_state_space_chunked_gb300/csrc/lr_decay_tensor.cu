@@ -564,7 +564,7 @@ __global__ void __launch_bounds__(dt::THREADS, 1)
                 if (!hu(FULL_K + st, c >> 1) || (c >= 1 && !hu(DS_FREE, c - 1))) break;
                 const uint64_t dK = umma_smem_desc(base + OFF_K + st * Q_BYTES, HALF, 1024);
                 bool ok = true;
-#pragma unroll
+#pragma unroll 1
                 for (int qt = 0; qt < 4; ++qt) {
                     ok = ok && hu(W_READY + qt, c);
                     if (!ok) break;
@@ -592,12 +592,11 @@ __global__ void __launch_bounds__(dt::THREADS, 1)
                 const uint64_t dQ = umma_smem_desc(base + OFF_Q + st * Q_BYTES, 16, 1024),
                                dK = umma_smem_desc(base + OFF_K + st * Q_BYTES, 16, 1024);
                 if (lead) {
-#pragma unroll
-                    for (int kk = 0; kk < 8; ++kk)
-                        if (kk < nkk) {
-                            const uint32_t off = ((kk >> 2) * HALF + (kk & 3) * 32) >> 4;
-                            umma_bf16(tmem + T_P + st * 128, dQ + off, dK + off, IDESC_P, kk > 0);
-                        }
+#pragma unroll 1
+                    for (int kk = 0; kk < nkk; ++kk) {
+                        const uint32_t off = ((kk >> 2) * HALF + (kk & 3) * 32) >> 4;
+                        umma_bf16(tmem + T_P + st * 128, dQ + off, dK + off, IDESC_P, kk > 0);
+                    }
                     umma_commit(&bar[P_READY + st]);
                     umma_commit(&bar[EMPTY_K + st]);
                     umma_commit(&bar[EMPTY_Q + st]);
@@ -615,11 +614,10 @@ __global__ void __launch_bounds__(dt::THREADS, 1)
                 tc_fence_after();
                 const uint64_t dQ = umma_smem_desc(base + OFF_Q + st * Q_BYTES, 16, 1024);
                 if (lead) {
-#pragma unroll
-                    for (int kk = 0; kk < 8; ++kk)
-                        if (kk < nkk)
-                            umma_bf16(tmem + T_O, dQ + (((kk >> 2) * HALF + (kk & 3) * 32) >> 4), dS + 128 * kk, IDESC_O,
-                                      kk > 0);
+#pragma unroll 1
+                    for (int kk = 0; kk < nkk; ++kk)
+                        umma_bf16(tmem + T_O, dQ + (((kk >> 2) * HALF + (kk & 3) * 32) >> 4), dS + 128 * kk, IDESC_O,
+                                  kk > 0);
                     umma_commit(&bar[OX_DONE + st]);
                     umma_commit(&bar[EMPTY_Q + st]);
                 }
@@ -634,7 +632,7 @@ __global__ void __launch_bounds__(dt::THREADS, 1)
                 tc_fence_after();
                 const uint64_t dV = umma_smem_desc(base + OFF_V + st * V_BYTES, HALF, 1024);
                 if (lead) {   // onto Q S^T: same shape and accumulator, so in order
-#pragma unroll
+#pragma unroll 1
                     for (int kk = 0; kk < C / 16; ++kk)
                         umma_bf16_ts(tmem + T_O, tmem + T_P + st * 128 + (kk >> 2) * 64 + (kk & 3) * 8, dV + 128 * kk,
                                      IDESC_O, 1);
@@ -725,7 +723,7 @@ __global__ void __launch_bounds__(dt::THREADS, 1)
             const float w = sW[mt * C + s];
 #pragma unroll 1
             for (int k = 0; k < 8; ++k) {
-                const uint32_t at = sw128_offset(s, 8 * k);
+                const uint32_t at = sw128_offset(s, 0) ^ (k << 4);   // group k of row s
                 uint4 u = *reinterpret_cast<const uint4 *>(V + at);
                 if (!in) u = make_uint4(0, 0, 0, 0);
                 const uint32_t uv[4] = {u.x, u.y, u.z, u.w};
@@ -923,29 +921,26 @@ __global__ void __launch_bounds__(dt::THREADS, 1)
             if (ok && c >= 1) ok = hw(OX_DONE + ((c - 1) & 1), (c - 1) >> 1);
             if (!__all_sync(0xffffffffu, ok)) break;
             const float m = sF[4 * mt];
-            // the copy: what this chunk's weights assume, S or m S (a steep chunk
-            // applies its factors by rows), as row j of 64 value rows in 8 swizzled groups
-            const float pm = sF[4 * mt + 2] == 0.0f ? 1.0f : m;
-            {
-                const float2 p2 = make_float2(pm, pm);
+            // a rescale belongs before the copy (the chunk's weights assume it) but
+            // after it in a steep chunk, which applies its factors by rows
+            const bool steep = sF[4 * mt + 2] == 0.0f;
+            auto scale_state = [&]() {
 #pragma unroll
-                for (int q = 0; q < 32; q += 8) {
-                    uint32_t r[4];
+                for (int e = 0; e < 32; ++e) S[e] *= m;
+            };
+            if (m != 1.0f && !steep) scale_state();
+            // the copy: row j of 64 value rows in 8 swizzled groups
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float2 y = __fmul2_rn(p2, make_float2(S[q + 2 * e], S[q + 2 * e + 1]));
-                        r[e] = pack(y.x, y.y);
-                    }
-                    *reinterpret_cast<uint4 *>(sm + OFF_SB + sw128_offset(j, 32 * sh + q)) =
-                        make_uint4(r[0], r[1], r[2], r[3]);
-                }
-                fence_proxy_async_smem();
-            }
+            for (int q = 0; q < 32; q += 8)
+                *reinterpret_cast<uint4 *>(sm + OFF_SB + sw128_offset(j, 32 * sh + q)) =
+                    make_uint4(pack(S[q], S[q + 1]), pack(S[q + 2], S[q + 3]), pack(S[q + 4], S[q + 5]),
+                               pack(S[q + 6], S[q + 7]));
+            fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) arrive(&bar[SB_READY]);
+            if (steep) scale_state();
             if (!__all_sync(0xffffffffu, hw(DS_DONE, c))) break;
             tc_fence_after();
-            const float2 m2 = make_float2(m, m);
 #pragma unroll
             for (int q = 0; q < 32; q += 8) {   // small terms first
                 float d1[8], d2[8], d3[8];
@@ -957,7 +952,7 @@ __global__ void __launch_bounds__(dt::THREADS, 1)
                 for (int e = 0; e < 8; e += 2) {
                     const float2 y = __fadd2_rn(make_float2(d1[e], d1[e + 1]),
                                                 __fadd2_rn(make_float2(d2[e], d2[e + 1]), make_float2(d3[e], d3[e + 1])));
-                    const float2 z = __ffma2_rn(m2, make_float2(S[q + e], S[q + e + 1]), y);
+                    const float2 z = __fadd2_rn(make_float2(S[q + e], S[q + e + 1]), y);
                     S[q + e] = z.x, S[q + e + 1] = z.y;
                 }
             }
