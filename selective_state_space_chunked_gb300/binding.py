@@ -730,17 +730,23 @@ def minmax_scan(r, s, x0=None, workspace=None, out=None,
     return _finish((y, xf), host_out, host, dev, sync_host)
 
 
-def _heads_of(q, k, v, H: int, Hk: Optional[int]):
-    """(Hk, dk, dv) of q, k (..., Hk*dk) and v (..., H*dv)."""
+def _heads_of(q, k, v, g, H: int, Hk: Optional[int], ndim: int):
+    """(shape of q, Hk, dk, dv, I/O type) of q, k (..., Hk*dk), v (..., H*dv)
+    and g (..., H) or None."""
     Hk = H if Hk is None else Hk
     if H < 1 or Hk < 1 or H % Hk:
         raise ValueError(f"{H} value heads cannot share {Hk} key heads")
-    if q.shape[-1] % Hk or v.shape[-1] % H:
-        raise ValueError(f"widths {q.shape[-1]} and {v.shape[-1]} are not divisible by {Hk} key heads "
-                         f"and {H} value heads")
-    if k.shape != q.shape or v.shape[:-1] != q.shape[:-1]:
-        raise ValueError(f"q {tuple(q.shape)}, k {tuple(k.shape)}, v {tuple(v.shape)} do not match")
-    return Hk, q.shape[-1] // Hk, v.shape[-1] // H
+    qs, vs = q.shape, v.shape
+    if len(qs) != ndim or k.shape != qs or len(vs) != ndim or vs[:-1] != qs[:-1]:
+        raise ValueError(f"q {tuple(qs)}, k {tuple(k.shape)}, v {tuple(vs)} do not match")
+    if qs[-1] % Hk or vs[-1] % H:
+        raise ValueError(f"widths {qs[-1]} and {vs[-1]} are not divisible by {Hk} key heads and {H} value heads")
+    if g is not None and g.shape != (*qs[:-1], H):
+        raise ValueError(f"g must have shape {(*qs[:-1], H)}, not {tuple(g.shape)}")
+    dt = q.dtype
+    if k.dtype != dt or v.dtype != dt or (g is not None and g.dtype != dt):
+        raise TypeError("all activation tensors must share one dtype")
+    return qs, Hk, qs[-1] // Hk, vs[-1] // H, _io_of(q)
 
 
 def _shaped(t: Optional[torch.Tensor], shape, name: str):
@@ -803,14 +809,13 @@ def decay_attn(q, k, v, H: int, Hk: Optional[int] = None, a_log=None, g=None, S0
     inputs with host (or no) ``out`` run the library's host-buffer path (without
     ``lens``; ``sync_host=False`` queues it, as for ``selective_scan``).  A log
     decay above 0 sets LR_ERR_RANGE (see ``check_status``)."""
-    Hk, dk, dv = _heads_of(q, k, v, H, Hk)
-    B, L = q.shape[0], q.shape[1]
-    _same(q, k, v, g)
-    io = _io_of(q)
-    _shaped(g, (B, L, H), "g")
-    _shaped(a_log, (H,), "a_log")
-    _shaped(S0, (B, H, dv, dk), "S0")
-    _shaped(lens, (B,), "lens")
+    (B, L, _), Hk, dk, dv, io = _heads_of(q, k, v, g, H, Hk, 3)
+    if a_log is not None:
+        _shaped(a_log, (H,), "a_log")
+    if S0 is not None:
+        _shaped(S0, (B, H, dv, dk), "S0")
+    if lens is not None:
+        _shaped(lens, (B,), "lens")
     specs = (((B, L, H * dv), q.dtype), ((B, H, dv, dk), torch.float32))
     if lens is None and not q.is_cuda and _host_route((q, k, v, g), out):
         q, k, v, g = (_h(t) for t in (q, k, v, g))
@@ -826,11 +831,12 @@ def decay_attn(q, k, v, H: int, Hk: Optional[int] = None, a_log=None, g=None, S0
     dev = _target_device(q)
     q, k, v, g = _act(q, dev), _act(k, dev), _act(v, dev), _act(g, dev)
     a_log, S0 = _par(a_log, dev), _par(S0, dev)
-    if lens is not None:
-        lens = _act(lens if lens.dtype is torch.int32 else lens.to(torch.int32), dev)
+    if lens is not None:   # (clamped before it is narrowed)
+        lens = _act(lens if lens.dtype is torch.int32 else lens.clamp(0, L).to(torch.int32), dev)
+    host_out = None
     if out is None:
-        o, Sf = (torch.empty(sh, dtype=dt, device=dev) for sh, dt in specs)
-        host_out = None
+        o = torch.empty((B, L, H * dv), dtype=q.dtype, device=dev)
+        Sf = torch.empty((B, H, dv, dk), dtype=torch.float32, device=dev)
     else:
         (o, Sf), host_out = _outputs(out, specs, dev)
     ws, wsb = _workspace(_decay_workspace_size((B, L, H, Hk, dk, dv, io)), dev, workspace)
@@ -971,17 +977,15 @@ def decay_attn_step(q, k, v, H: int, Hk: Optional[int] = None, a_log=None, g=Non
     or None, one dtype on the GPU; a_log: (H,) fp32 or None; S: (B, H, dv, dk)
     fp32 or None (zero).  Returns (o (B, H*dv), S_new); ``S_out`` gives the
     buffer S_new is written to (it may be ``S`` itself)."""
-    Hk, dk, dv = _heads_of(q, k, v, H, Hk)
-    B = q.shape[0]
-    _same(q, k, v, g)
-    io = _io_of(q)
-    _shaped(g, (B, H), "g")
-    _shaped(a_log, (H,), "a_log")
-    _shaped(S, (B, H, dv, dk), "S")
+    (B, _), Hk, dk, dv, io = _heads_of(q, k, v, g, H, Hk, 2)
+    shape = (B, H, dv, dk)
+    if a_log is not None:
+        _shaped(a_log, (H,), "a_log")
+    if S is not None:
+        _shaped(S, shape, "S")
     dev = _target_device(q)
     q, k, v, g = _act(q, dev), _act(k, dev), _act(v, dev), _act(g, dev)
     a_log, S = _par(a_log, dev), _par(S, dev)
-    shape = (B, H, dv, dk)
     if S_out is None:
         S_out = torch.empty(shape, dtype=torch.float32, device=dev)
     elif S_out.shape != shape or S_out.dtype is not torch.float32 or S_out.device != dev or not S_out.is_contiguous():

@@ -7,9 +7,10 @@
 // kernel.  A group stays in the registers of the lanes that share it: the
 // mean, then the centred squares (no cancellation), then the output.
 //
-//   lanes   groups of 16-byte multiples up to 1024 bytes (the head dims): TL
-//           lanes of a warp hold a group, one or two 16-byte vectors each; a
-//           warp walks groups that share their channels' phase where it can
+//   lanes   groups of up to 128 vectors (16 bytes; 8 for a bf16 group of an odd
+//           number of those): TL lanes of a warp hold a group, up to four vectors
+//           each, with the fewest idle slots; a thread keeps its group and walks
+//           rows, several in flight
 //   block   larger groups of 16-byte multiples: a block holds the group, up to
 //           four vectors per thread
 //   any     the rest (odd sizes, groups past a block's registers): a block per
@@ -25,33 +26,36 @@ __device__ __forceinline__ float silu_f(float x) {
     return __fdividef(x, 1.0f + ex2_approx(fminf(-x * kLog2e, 125.0f)));
 }
 
-template <typename IO> struct Vec16;
-template <> struct Vec16<float> {
+// N neighbouring values as one load
+template <typename IO, int N_> struct Vec;
+template <> struct Vec<float, 4> {
     static constexpr int N = 4;
     using Raw = float4;
     __device__ __forceinline__ static void widen(const Raw &u, float *v) { v[0] = u.x, v[1] = u.y, v[2] = u.z, v[3] = u.w; }
     __device__ __forceinline__ static Raw narrow(const float *v) { return make_float4(v[0], v[1], v[2], v[3]); }
 };
-template <> struct Vec16<__nv_bfloat16> {
+__device__ __forceinline__ void widen2(uint32_t w, float *v) {
+    v[0] = __uint_as_float(w << 16), v[1] = __uint_as_float(w & 0xffff0000u);
+}
+__device__ __forceinline__ uint32_t narrow2(const float *v) {
+    const __nv_bfloat162 t = __floats2bfloat162_rn(v[0], v[1]);
+    return *reinterpret_cast<const uint32_t *>(&t);
+}
+template <> struct Vec<__nv_bfloat16, 8> {
     static constexpr int N = 8;
     using Raw = uint4;
     __device__ __forceinline__ static void widen(const Raw &u, float *v) {
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[2 * i] = __uint_as_float(w[i] << 16);
-            v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-        }
+        widen2(u.x, v), widen2(u.y, v + 2), widen2(u.z, v + 4), widen2(u.w, v + 6);
     }
     __device__ __forceinline__ static Raw narrow(const float *v) {
-        uint32_t w[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const __nv_bfloat162 t = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-            w[i] = *reinterpret_cast<const uint32_t *>(&t);
-        }
-        return make_uint4(w[0], w[1], w[2], w[3]);
+        return make_uint4(narrow2(v), narrow2(v + 2), narrow2(v + 4), narrow2(v + 6));
     }
+};
+template <> struct Vec<__nv_bfloat16, 4> {
+    static constexpr int N = 4;
+    using Raw = uint2;
+    __device__ __forceinline__ static void widen(const Raw &u, float *v) { widen2(u.x, v), widen2(u.y, v + 2); }
+    __device__ __forceinline__ static Raw narrow(const float *v) { return make_uint2(narrow2(v), narrow2(v + 2)); }
 };
 
 struct NormArgs {
@@ -64,13 +68,13 @@ struct NormArgs {
     int act;
 };
 
-// y of one 16-byte vector whose values are already centred
-template <typename IO, bool GATE>
-__device__ __forceinline__ typename Vec16<IO>::Raw finish(float *v, float rs, const float *ga, const float *be,
-                                                          const typename Vec16<IO>::Raw &zr, int act) {
-    constexpr int VN = Vec16<IO>::N;
+// y of one vector whose values are already centred
+template <typename X, bool GATE>
+__device__ __forceinline__ typename X::Raw finish(float *v, float rs, const float *ga, const float *be,
+                                                  const typename X::Raw &zr, int act) {
+    constexpr int VN = X::N;
     float z[VN];
-    if (GATE) Vec16<IO>::widen(zr, z);
+    if (GATE) X::widen(zr, z);
 #pragma unroll
     for (int i = 0; i < VN; ++i) {
         float n = fmaf(v[i] * rs, ga[i], be[i]);
@@ -78,7 +82,7 @@ __device__ __forceinline__ typename Vec16<IO>::Raw finish(float *v, float rs, co
         if (GATE) n *= silu_f(z[i]);
         v[i] = n;
     }
-    return Vec16<IO>::narrow(v);
+    return X::narrow(v);
 }
 
 template <int VN>
@@ -97,15 +101,14 @@ __device__ __forceinline__ void load_affine(const float *gamma, const float *bet
 // thread keeps its group (its channels, so gamma and beta stay in registers)
 // and walks rows, ROWS of them in flight: groups are dealt over grid.y and the
 // lane sets of a block, rows over grid.x.
-template <typename IO, int TL, int V, int ROWS, bool GATE>
+template <typename X, int TL, int V, int ROWS, bool GATE>
 __global__ void __launch_bounds__(256)
-    group_norm_lanes_kernel(const NormArgs a) {
-    using X = Vec16<IO>;
+    group_norm_lanes_kernel(const NormArgs a, int gper) {
     using Raw = typename X::Raw;
     constexpr int VN = X::N, SETS = 256 / TL;   // lane sets of a block
     const int set = threadIdx.x / TL, l = threadIdx.x % TL;
     // sets of a block: consecutive groups of a row, then rows
-    const int gper = min(a.G, SETS), rper = SETS / gper;
+    const int rper = SETS / gper;
     const int gi = blockIdx.y * gper + set % gper;
     const int r0 = set / gper;
     const bool live = gi < a.G && r0 < rper;
@@ -165,7 +168,7 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
             for (int u = 0; u < V; ++u)
                 if (in[u] && r < a.N)
-                    __stcs(y + r * row_vecs + col + u * TL, finish<IO, GATE>(v[u], rs, ga[u], be[u], zr[k][u], a.act));
+                    __stcs(y + r * row_vecs + col + u * TL, finish<X, GATE>(v[u], rs, ga[u], be[u], zr[k][u], a.act));
         }
     }
 }
@@ -185,10 +188,9 @@ __device__ __forceinline__ float block_sum(float s, float *red) {
 }
 
 // a block per group (grid-stride over row-groups), V vectors per thread
-template <typename IO, int NT, int V, bool GATE>
+template <typename X, int NT, int V, bool GATE>
 __global__ void __launch_bounds__(NT)
     group_norm_block_kernel(const NormArgs a) {
-    using X = Vec16<IO>;
     using Raw = typename X::Raw;
     constexpr int VN = X::N;
     __shared__ float red[NT / 32];
@@ -233,7 +235,7 @@ __global__ void __launch_bounds__(NT)
             if (i < nv) {
                 float ga[VN], be[VN];
                 load_affine<VN>(a.gamma, a.beta, gi * a.d + i * VN, true, ga, be);
-                __stcs(static_cast<Raw *>(a.y) + at + i, finish<IO, GATE>(v[u], rs, ga, be, zr[u], a.act));
+                __stcs(static_cast<Raw *>(a.y) + at + i, finish<X, GATE>(v[u], rs, ga, be, zr[u], a.act));
             }
         }
     }
@@ -270,6 +272,44 @@ __global__ void __launch_bounds__(128)
     }
 }
 
+template <typename X, int TL, int V, bool GATE>
+int launch_lanes(const NormArgs &a, int sms, cudaStream_t s) {
+    constexpr int SETS = 256 / TL;
+    // groups of a row per block: the count that leaves the fewest sets idle, the
+    // larger of two (neighbouring groups are neighbouring bytes)
+    int gper = 1;
+    double best = 0.0;
+    for (int g = 1; g <= SETS && g <= a.G; ++g) {
+        const double used = double(g * (SETS / g)) / SETS * double(a.G) / double((a.G + g - 1) / g * g);
+        if (used >= best - 1e-9) best = used, gper = g;
+    }
+    const int rper = SETS / gper, gy = (a.G + gper - 1) / gper;
+    const int64_t row_blocks = (a.N + rper - 1) / rper;
+    // rows in flight per thread, about four vectors in all, once every SM has
+    // its blocks (16384 x 2048 bf16 with gate: 4 rows of one vector 38 us, 2
+    // rows 41 us, 1 row 49 us; 8192 x 4096 without: 35 us, with 8 rows 45 us; 4,
+    // 8 or 16 blocks per SM instead of 6: 46, 41, 42 us); one row where there
+    // are few
+    constexpr int R = V == 1 ? 4 : V == 2 ? 2 : 1;
+    const int64_t full = int64_t(sms) * 6;
+    const bool deep = row_blocks * gy >= full * R;
+    int64_t gx = deep ? (full + gy - 1) / gy : row_blocks;
+    if (gx > row_blocks) gx = row_blocks;
+    const dim3 grid{unsigned(gx), unsigned(gy), 1};
+    if (deep)
+        group_norm_lanes_kernel<X, TL, V, R, GATE><<<grid, 256, 0, s>>>(a, gper);
+    else
+        group_norm_lanes_kernel<X, TL, V, 1, GATE><<<grid, 256, 0, s>>>(a, gper);
+    return cudaGetLastError() == cudaSuccess ? LR_OK : LR_ERR_CUDA;
+}
+
+template <typename X, int NT, int V, bool GATE>
+int launch_block(const NormArgs &a, int sms, cudaStream_t s) {
+    const int64_t ng = a.N * a.G, most = int64_t(sms) * (2048 / NT) * 8;
+    group_norm_block_kernel<X, NT, V, GATE><<<unsigned(ng < most ? ng : most), NT, 0, s>>>(a);
+    return cudaGetLastError() == cudaSuccess ? LR_OK : LR_ERR_CUDA;
+}
+
 template <typename IO>
 int launch_any(const NormArgs &a, int sms, cudaStream_t s) {
     const int64_t ng = a.N * a.G, most = int64_t(sms) * 128;
@@ -277,52 +317,39 @@ int launch_any(const NormArgs &a, int sms, cudaStream_t s) {
     return cudaGetLastError() == cudaSuccess ? LR_OK : LR_ERR_CUDA;
 }
 
-template <typename IO, int TL, int V, bool GATE>
-int launch_lanes(const NormArgs &a, int sms, cudaStream_t s) {
-    constexpr int SETS = 256 / TL;
-    const int gper = a.G < SETS ? a.G : SETS, rper = SETS / gper;
-    const int gy = (a.G + gper - 1) / gper;
-    // rows in flight per thread: enough bytes to cover the memory latency once
-    // every SM has its blocks, one row each where there are few
-    const int64_t row_blocks = (a.N + rper - 1) / rper;
-    const int64_t full = int64_t(sms) * 6;   // resident blocks
-    constexpr int R = V == 1 ? 4 : 2;
-    const bool deep = row_blocks * gy >= full * R;
-    int64_t gx = deep ? (full + gy - 1) / gy : row_blocks;
-    if (gx > row_blocks) gx = row_blocks;
-    if (gy > 65535) return launch_any<IO>(a, sms, s);
-    const dim3 grid{unsigned(gx), unsigned(gy), 1};
-    if (deep)
-        group_norm_lanes_kernel<IO, TL, V, R, GATE><<<grid, 256, 0, s>>>(a);
-    else
-        group_norm_lanes_kernel<IO, TL, V, 1, GATE><<<grid, 256, 0, s>>>(a);
-    return cudaGetLastError() == cudaSuccess ? LR_OK : LR_ERR_CUDA;
-}
-
-template <typename IO, int NT, int V, bool GATE>
-int launch_block(const NormArgs &a, int sms, cudaStream_t s) {
-    const int64_t ng = a.N * a.G, most = int64_t(sms) * (2048 / NT) * 8;
-    group_norm_block_kernel<IO, NT, V, GATE><<<unsigned(ng < most ? ng : most), NT, 0, s>>>(a);
-    return cudaGetLastError() == cudaSuccess ? LR_OK : LR_ERR_CUDA;
+// nv vectors per group: lanes x vectors with the fewest idle slots, the wider
+// lane set where two are equal
+template <typename X, bool GATE>
+int launch_vec(const NormArgs &a, int nv, int sms, cudaStream_t s) {
+    if (nv <= 4) return launch_lanes<X, 4, 1, GATE>(a, sms, s);
+    if (nv <= 8) return launch_lanes<X, 8, 1, GATE>(a, sms, s);
+    if (nv <= 12) return launch_lanes<X, 4, 3, GATE>(a, sms, s);
+    // two vectors a lane halve the shuffles (8192 x 4096 bf16 29 us against 35);
+    // with a gate's loads the narrower rows win (39 us against 43)
+    if (nv <= 16) return launch_lanes<X, GATE ? 16 : 8, GATE ? 1 : 2, GATE>(a, sms, s);
+    if (nv <= 24) return launch_lanes<X, 8, 3, GATE>(a, sms, s);
+    if (nv <= 32) return launch_lanes<X, 16, 2, GATE>(a, sms, s);
+    if (nv <= 48) return launch_lanes<X, 16, 3, GATE>(a, sms, s);
+    if (nv <= 64) return launch_lanes<X, 32, 2, GATE>(a, sms, s);
+    if (nv <= 96) return launch_lanes<X, 32, 3, GATE>(a, sms, s);
+    if (nv <= 128) return launch_lanes<X, 32, 4, GATE>(a, sms, s);
+    if (nv <= 256) return launch_block<X, 128, 2, GATE>(a, sms, s);
+    if (nv <= 512) return launch_block<X, 256, 2, GATE>(a, sms, s);
+    if (nv <= 1024) return launch_block<X, 256, 4, GATE>(a, sms, s);
+    return launch_block<X, 512, 4, GATE>(a, sms, s);
 }
 
 template <typename IO, bool GATE>
 int norm_gate(const NormArgs &a, cudaStream_t s) {
-    constexpr int VN = Vec16<IO>::N;
+    constexpr bool BF = sizeof(IO) == 2;
     int sms = 0;
     if (device_sm_count(&sms) != LR_OK) return LR_ERR_CUDA;
-    if (a.d % VN == 0) {   // C is a multiple of d, so every group starts on 16 bytes
-        const int nv = a.d / VN;
-        if (nv <= 4) return launch_lanes<IO, 4, 1, GATE>(a, sms, s);
-        if (nv <= 8) return launch_lanes<IO, 8, 1, GATE>(a, sms, s);
-        if (nv <= 16) return launch_lanes<IO, 16, 1, GATE>(a, sms, s);
-        if (nv <= 32) return launch_lanes<IO, 32, 1, GATE>(a, sms, s);
-        if (nv <= 64) return launch_lanes<IO, 32, 2, GATE>(a, sms, s);
-        if (nv <= 128) return launch_block<IO, 128, 1, GATE>(a, sms, s);
-        if (nv <= 256) return launch_block<IO, 256, 1, GATE>(a, sms, s);
-        if (nv <= 512) return launch_block<IO, 256, 2, GATE>(a, sms, s);
-        if (nv <= 1024) return launch_block<IO, 256, 4, GATE>(a, sms, s);
-        if (nv <= 2048) return launch_block<IO, 512, 4, GATE>(a, sms, s);
+    // C is a multiple of d, so every group starts on a vector's boundary
+    constexpr int W = BF ? 8 : 4;
+    if (a.G <= 65535) {
+        if (a.d % W == 0 && a.d / W <= 2048) return launch_vec<Vec<IO, W>, GATE>(a, a.d / W, sms, s);
+        if constexpr (BF)
+            if (a.d % 4 == 0 && a.d / 4 <= 2048) return launch_vec<Vec<IO, 4>, GATE>(a, a.d / 4, sms, s);
     }
     return launch_any<IO>(a, sms, s);
 }
