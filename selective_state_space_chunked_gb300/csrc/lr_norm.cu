@@ -20,11 +20,10 @@
 namespace lr {
 namespace {
 
-// silu in fp32: x / (1 + e^-x), with e^-x kept below 2^125 (the fast division
-// is exact to 2 ulp for divisors up to 2^126; the quotient is 0 to fp32 there)
-__device__ __forceinline__ float silu_f(float x) {
-    return __fdividef(x, 1.0f + ex2_approx(fminf(-x * kLog2e, 125.0f)));
-}
+// silu in fp32: x / (1 + e^-x).  The fast division gives 0 for divisors past
+// 2^126, where the quotient is 0 to fp32.
+__device__ __forceinline__ float silu_f(float x) { return __fdividef(x, 1.0f + ex2_approx(-x * kLog2e)); }
+__device__ __forceinline__ float2 pair(const float *v) { return make_float2(v[0], v[1]); }
 
 // N neighbouring values as one load
 template <typename IO, int N_> struct Vec;
@@ -75,12 +74,19 @@ __device__ __forceinline__ typename X::Raw finish(float *v, float rs, const floa
     constexpr int VN = X::N;
     float z[VN];
     if (GATE) X::widen(zr, z);
+    const float2 rs2 = make_float2(rs, rs);
 #pragma unroll
-    for (int i = 0; i < VN; ++i) {
-        float n = fmaf(v[i] * rs, ga[i], be[i]);
-        if (act == LR_ACT_SILU) n = silu_f(n);
-        if (GATE) n *= silu_f(z[i]);
-        v[i] = n;
+    for (int i = 0; i < VN; i += 2) {
+        const float2 n = __ffma2_rn(__fmul2_rn(pair(v + i), rs2), pair(ga + i), pair(be + i));
+        v[i] = n.x, v[i + 1] = n.y;
+    }
+    if (act == LR_ACT_SILU) {
+#pragma unroll
+        for (int i = 0; i < VN; ++i) v[i] = silu_f(v[i]);
+    }
+    if (GATE) {
+#pragma unroll
+        for (int i = 0; i < VN; ++i) v[i] *= silu_f(z[i]);
     }
     return X::narrow(v);
 }
@@ -143,24 +149,29 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
         for (int k = 0; k < ROWS; ++k) {
             const int64_t r = base + k * step + r0;
-            float v[V][VN], s = 0.0f;
+            float v[V][VN];
+            float2 s2 = make_float2(0.0f, 0.0f);
 #pragma unroll
             for (int u = 0; u < V; ++u) {
                 X::widen(xr[k][u], v[u]);
 #pragma unroll
-                for (int i = 0; i < VN; ++i) s += v[u][i];
+                for (int i = 0; i < VN; i += 2) s2 = __fadd2_rn(s2, pair(v[u] + i));
             }
+            float s = s2.x + s2.y;
 #pragma unroll
             for (int m = TL / 2; m >= 1; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
             const float mean = s * a.inv_d;
             s = 0.0f;
 #pragma unroll
             for (int u = 0; u < V; ++u) {
+                s2 = make_float2(0.0f, 0.0f);
 #pragma unroll
-                for (int i = 0; i < VN; ++i) {
-                    v[u][i] -= mean;
-                    if (in[u]) s = fmaf(v[u][i], v[u][i], s);
+                for (int i = 0; i < VN; i += 2) {
+                    const float2 c = __fadd2_rn(pair(v[u] + i), make_float2(-mean, -mean));
+                    s2 = __ffma2_rn(c, c, s2);
+                    v[u][i] = c.x, v[u][i + 1] = c.y;
                 }
+                if (in[u]) s += s2.x + s2.y;
             }
 #pragma unroll
             for (int m = TL / 2; m >= 1; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
