@@ -4,14 +4,23 @@
 namespace lr {
 
 namespace {
-// CUDA-core kernel: blocks that fill the GPU (four of 128 threads per SM: their
-// state registers), and the shortest segment worth the second pass over k and v.
-constexpr int64_t kGenBlocksPerSm = 4;
-constexpr int64_t kGenMinSeg = 128;
+// CUDA-core kernel: the shortest segment, and costs in units of a step of a
+// block: a block's start, one segment's state read by a later one, and the
+// second launch.  Fitted to sweeps of the segment count over 13 shapes, of which
+// the plan's choice is within 5 % of the best on 12 and within 12 % on one; at
+// fp32 H16 d128, B2 L2048: 4 segments 271 us, 7 242, 9 (chosen) 211, 12 246;
+// B4 L4096: 4 748, 9 (chosen) 682, 14 690; B1 L32768: 9 1821, 19 (chosen) 1304,
+// 24 1490.
+// Calls in one segment whose narrow blocks (one state row a thread) are no more
+// than two per SM take those: fp32 L100 d128, H4 25 us against 31, H16 26
+// against 32, but H64 59 against 32; at dk 512 98 against 41.
+constexpr int64_t kGenMinSeg = 64;
+constexpr double kGenBlockCost = 40.0, kGenStateCost = 0.5, kGenLaunchCost = 50.0;
 constexpr int64_t kMaxSeg = 32;
-// Tensor-core kernel: the shortest sequence it takes, and costs in units of a
-// chunk's time: a chunk of the first launch, a block's start, and one
-// segment's state read by a later one.
+// Tensor-core kernel: the shortest sequence it takes (bf16 B8 H16 d128: L48 25
+// us on either kernel, L64 24 against 28 on the CUDA cores, L96 24 against 39),
+// and costs in units of a chunk's time: a chunk of the first launch, a block's
+// start, and one segment's state read by a later one.
 constexpr int64_t kTensorMinLen = 64;
 constexpr double kFirstCost = 0.6, kBlockCost = 3.0, kStateCost = 0.5;
 }  // namespace
@@ -37,16 +46,26 @@ int decay_plan(int64_t B, int64_t L, int64_t H, int64_t Hk, int64_t dk, int64_t 
             if (t < best) best = t, n = s;
         }
     } else {
-        const int64_t want = kGenBlocksPerSm * sms;
-        auto blocks = [&](bool narrow) {
-            const int64_t rows = decay_general_rows(dk, narrow);
-            return B * H * ((dv + rows - 1) / rows);
+        // Blocks of an SM share its fp32 pipes.  The SM with the most of them
+        // takes, per step and in units of a block's share of a full SM, as long
+        // as its slots for each full round (a partly filled last round of
+        // dependent launches packs three blocks as four) and 1.5 for a block
+        // that has the SM to itself.
+        const int64_t rows = decay_general_rows(dk, false), threads = dk <= 64 ? 64 : 128, slots = dk <= 128 ? 4 : 3;
+        const int64_t blocks = B * H * ((dv + rows - 1) / rows);
+        auto load = [&](int64_t b) {
+            const int64_t most = (b * threads + 128 * sms - 1) / (128 * sms), rest = most % slots;
+            return double(most - rest) + (rest == 0 ? 0.0 : rest == 1 ? 1.5 : rest == 2 ? 2.75 : double(slots));
         };
-        n = want / blocks(false);
-        if (n > L / kGenMinSeg) n = L / kGenMinSeg;
-        if (n > kMaxSeg) n = kMaxSeg;
-        if (n < 1) n = 1;
-        p->narrow = n == 1 && blocks(false) < sms;
+        double best = load(blocks) * (double(L) + kGenBlockCost);
+        for (int64_t s = 2; s <= kMaxSeg && s * kGenMinSeg <= L; ++s) {
+            const double per = double((L + s - 1) / s);
+            const double t = load(blocks * s) * (per + kGenBlockCost + kGenStateCost * double(s)) +
+                             load(blocks * (s - 1)) * (0.5 * per + kGenBlockCost) + kGenLaunchCost;
+            if (t < best) best = t, n = s;
+        }
+        const int64_t nrows = decay_general_rows(dk, true);
+        p->narrow = n == 1 && dk <= 256 && B * H * ((dv + nrows - 1) / nrows) <= 2 * sms;
     }
     p->seg_len = ((L + n - 1) / n + unit - 1) / unit * unit;
     p->n_seg = int((L + p->seg_len - 1) / p->seg_len);

@@ -18,9 +18,18 @@
 // 2^-32 (resets included) runs with the multiplication at every step.
 //
 // k, q, v arrive in chunks of TC steps, by TMA where every row start is
-// 16-byte aligned, else element by element, kNB - 1 chunks ahead.
-// The work is 2 dk dv fp32 fused multiply-adds per token and head, which at
-// long sequences is what bounds the kernel; the segments give it the blocks.
+// 16-byte aligned, else element by element, kGB - 1 chunks ahead.
+//
+// The work is 2 dk dv fp32 fused multiply-adds per token and head and, in the
+// n - 1 of n segments that the first launch runs, dk dv more.  Measured (fp32,
+// H16 d128): B2 L2048 211 us, 9 segments, 3.1 G fused multiply-adds, 38 % of
+// the fp32 pipes' rate; B4 L4096 682 us; B1 L32768 1304 us.  What is left of
+// the rate goes to the latency of a step (its loads from shared memory, the
+// 16-deep chains of dependent sums, the sums over lanes), which four warps per
+// scheduler do not cover.  Chunks of 16 steps in two buffers rather than 8 in
+// three: 239 -> 222 us; the steep chunk's multiplications in a loop of their
+// own: 222 -> 205-211.  Two steps' sums over lanes taken together (spills): 210
+// against 205.  Blocks of 256 threads: 211.
 #pragma once
 
 #include "lr_decay.cuh"
@@ -28,12 +37,15 @@
 namespace lr {
 namespace {
 
-constexpr int kGB = 3;    // staging buffers
+constexpr int kGB = 2;    // staging buffers
 
 // A thread holds RT x CPT state elements.  4 x 16 leaves room for four warps
 // per scheduler; 4 x 32 and 8 x 16 read less from shared memory per element but
-// leave 1.5, and the packed fp32 pipe was then busy 37 % of the time (278 us at
-// B2 L2048 H16 d128 fp32).
+// leave 1.5, and the packed fp32 pipe was then busy 37 % of the time (278 against
+// 242 us at B2 L2048 H16 d128 fp32).  From 256 key columns three blocks per SM,
+// without spills, take 115 us against 137 (fp32 B3 L1111 H6 dk192 dv96); up to
+// 64 key columns chunks of 32 steps take 104 us against 118 (fp32 B1 L8192 H4
+// d64).
 template <int DKP_, bool NARROW>
 struct DecCfg {
     static constexpr int DKP = DKP_;
@@ -44,10 +56,12 @@ struct DecCfg {
     static constexpr int RB = RT * NT / P;
     static constexpr int KB = DKP < 256 ? DKP : 256;   // key columns per TMA box
     static constexpr int NH = DKP / KB;
-    // steps per staged chunk: 4 KB of k at most
+    static constexpr int BPS = DKP >= 256 ? 3 : 512 / NT;   // blocks an SM is to hold
+    // steps per staged chunk
     template <typename IO>
     __host__ __device__ static constexpr int steps() {
-        return 4096 / int(DKP * sizeof(IO)) < 16 ? 4096 / int(DKP * sizeof(IO)) : 16;
+        constexpr int most = DKP <= 64 ? 32 : 16;
+        return 16384 / int(DKP * sizeof(IO)) < most ? 16384 / int(DKP * sizeof(IO)) : most;
     }
     template <typename IO>
     __host__ __device__ static constexpr int pitch(int n) {
@@ -93,10 +107,27 @@ __device__ __forceinline__ void row_sums(float (&a)[RT], int p) {
     for (int m = RT; m < P; m <<= 1) a[0] += __shfl_xor_sync(0xffffffffu, a[0], m);
 }
 
+// Columns j .. j + 3 of a state row of dk columns; v4: 16-byte rows.
+__device__ __forceinline__ float4 state_ld4(const float *r, int j, int dk, bool v4) {
+    if (v4) return j < dk ? *reinterpret_cast<const float4 *>(r + j) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    return make_float4(j < dk ? r[j] : 0.0f, j + 1 < dk ? r[j + 1] : 0.0f, j + 2 < dk ? r[j + 2] : 0.0f,
+                       j + 3 < dk ? r[j + 3] : 0.0f);
+}
+__device__ __forceinline__ void state_st4(float *r, int j, int dk, bool v4, float4 s) {
+    if (v4) {
+        if (j < dk) *reinterpret_cast<float4 *>(r + j) = s;
+        return;
+    }
+    if (j < dk) r[j] = s.x;
+    if (j + 1 < dk) r[j + 1] = s.y;
+    if (j + 2 < dk) r[j + 2] = s.z;
+    if (j + 3 < dk) r[j + 3] = s.w;
+}
+
 // STATE_ONLY: the first launch of a segmented call (no q, no output; segments
 // 0 .. n_seg - 2).
 template <typename IO, typename C, bool STATE_ONLY>
-__global__ void __launch_bounds__(C::NT, C::NT == 128 ? 4 : 8)
+__global__ void __launch_bounds__(C::NT, C::BPS)
     decay_general_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                          const __grid_constant__ CUtensorMap tm_v, const DecayArgs a, int nrb, bool tma,
                          uint64_t timeout_ns, StatusRef sref) {
@@ -109,9 +140,10 @@ __global__ void __launch_bounds__(C::NT, C::NT == 128 ? 4 : 8)
     IO *vs = qs + kGB * KT;                  // [GB][TC][RB] (pitch VTP)
     float *os = reinterpret_cast<float *>(vs + kGB * VTP);   // [TC][RB]
     float *mu = os + VT;                     // [2][TC] readout factors scale A_t
-    float *mw = mu + 2 * TC;                 // [2][TC] 1 / A_t, or a_t of a steep chunk
-    float *mm = mw + 2 * TC;                 // [2][2] factors before and after the chunk
-    uint64_t *full = reinterpret_cast<uint64_t *>(mm + 4 * TC);
+    float *mw = mu + 2 * TC;                 // [2][TC] 1 / A_t (1 in a steep chunk)
+    float *ma = mw + 2 * TC;                 // [2][TC] a_t of a steep chunk
+    float *mm = ma + 2 * TC;                 // [2][2] factors before and after the chunk
+    uint64_t *full = reinterpret_cast<uint64_t *>(mm + 2 * TC);
 
     const int tid = threadIdx.x, lane = tid & 31;
     const int nseg = STATE_ONLY ? a.n_seg - 1 : a.n_seg;
@@ -199,7 +231,8 @@ __global__ void __launch_bounds__(C::NT, C::NT == 128 ? 4 : 8)
         float *u = mu + (c & 1) * TC, *w = mw + (c & 1) * TC, *m = mm + (c & 1) * 2;
         if (lane < TC) {
             u[lane] = a.scale * (steep ? 1.0f : dec::exp2_fix(base + cum));
-            w[lane] = steep ? dec::exp2_fix(own) : dec::exp2_fix(-(base + cum));
+            w[lane] = steep ? 1.0f : dec::exp2_fix(-(base + cum));
+            ma[(c & 1) * TC + lane] = steep ? dec::exp2_fix(own) : 1.0f;
         }
         if (steep) {
             if (lane == 0) {
@@ -222,40 +255,33 @@ __global__ void __launch_bounds__(C::NT, C::NT == 128 ? 4 : 8)
     // S[rr][2m + e] holds columns 4 (m P + p) + 2e + {0, 1} of row row0 + rg RT + rr
     float2 S[RT][CPT / 2];
     if (!STATE_ONLY && seg > 0) grid_dependency_wait();   // the first launch's states
+    auto rows16 = [&](const float *x) { return (dk & 3) == 0 && (reinterpret_cast<uintptr_t>(x) & 15) == 0; };
+    auto add_state = [&](const float *src, float f) {   // S += f src, a dv x dk state
+        const bool v4 = rows16(src);
 #pragma unroll
-    for (int rr = 0; rr < RT; ++rr) {
-        const int i = row0 + rg * RT + rr;
-        const float *src = seg > 0 ? nullptr : a.S0;
+        for (int rr = 0; rr < RT; ++rr) {
+            const int i = row0 + rg * RT + rr;
+            if (i >= dv) continue;
 #pragma unroll
-        for (int m2 = 0; m2 < CPT / 2; ++m2) {
-            const int j = 4 * ((m2 >> 1) * P + p) + 2 * (m2 & 1);
-            float2 s = make_float2(0.0f, 0.0f);
-            if (src != nullptr && i < dv) {
-                const float *r = src + (size_t(bh) * dv + i) * dk;
-                if (j < dk) s.x = r[j];
-                if (j + 1 < dk) s.y = r[j + 1];
+            for (int m = 0; m < CPT / 4; ++m) {
+                const float4 s = state_ld4(src + size_t(i) * dk, 4 * (m * P + p), dk, v4);
+                S[rr][2 * m] = __ffma2_rn(make_float2(f, f), make_float2(s.x, s.y), S[rr][2 * m]);
+                S[rr][2 * m + 1] = __ffma2_rn(make_float2(f, f), make_float2(s.z, s.w), S[rr][2 * m + 1]);
             }
-            S[rr][m2] = s;
         }
-    }
+    };
+#pragma unroll
+    for (int rr = 0; rr < RT; ++rr)
+#pragma unroll
+        for (int m = 0; m < CPT / 2; ++m) S[rr][m] = make_float2(0.0f, 0.0f);
+    if (seg == 0 && a.S0 != nullptr) add_state(a.S0 + size_t(bh) * dv * dk, 1.0f);
     if (!STATE_ONLY && seg > 0) {   // the decayed sum of the ranges before this one
         long long acc = 0;
         for (int s = seg - 1; s >= 0; --s) {
             const float f = dec::exp2_fix(acc);
             if (f == 0.0f) break;
             const size_t at = size_t(bh) * (a.n_seg - 1) + s;
-#pragma unroll
-            for (int rr = 0; rr < RT; ++rr) {
-                const int i = row0 + rg * RT + rr;
-                if (i >= dv) continue;
-                const float *r = a.seg_state + (at * dv + i) * dk;
-#pragma unroll
-                for (int m2 = 0; m2 < CPT / 2; ++m2) {
-                    const int j = 4 * ((m2 >> 1) * P + p) + 2 * (m2 & 1);
-                    if (j < dk) S[rr][m2].x = fmaf(f, r[j], S[rr][m2].x);
-                    if (j + 1 < dk) S[rr][m2].y = fmaf(f, r[j + 1], S[rr][m2].y);
-                }
-            }
+            add_state(a.seg_state + at * dv * dk, f);
             acc = max(acc + a.seg_tot[at], -(1ll << 60));
         }
     }
@@ -281,32 +307,24 @@ __global__ void __launch_bounds__(C::NT, C::NT == 128 ? 4 : 8)
             break;
         }
         const int nt = min(TC, nrun - c * TC);
-        const float *u = mu + (c & 1) * TC, *w = mw + (c & 1) * TC, *mf = mm + (c & 1) * 2;
+        const float *u = mu + (c & 1) * TC, *w = mw + (c & 1) * TC, *wa = ma + (c & 1) * TC, *mf = mm + (c & 1) * 2;
         const float after = mf[1];
         const bool steep = after < 0.0f;
-        if (steep) {
-            const float f = mf[0];
+        const IO *vr = vs + buf * VTP + rg * RT;
+        auto mul = [&](float f) {
+            const float2 f2 = make_float2(f, f);
 #pragma unroll
             for (int rr = 0; rr < RT; ++rr)
 #pragma unroll
-                for (int m = 0; m < CPT / 2; ++m) S[rr][m] = __fmul2_rn(S[rr][m], make_float2(f, f));
-        }
-        const IO *vr = vs + buf * VTP + rg * RT;
-        for (int t = 0; t < nt; ++t) {
+                for (int m = 0; m < CPT / 2; ++m) S[rr][m] = __fmul2_rn(S[rr][m], f2);
+        };
+        auto step = [&](int t) {
             const IO *kr = ks + buf * KT + t * KB + 4 * p, *qr = qs + buf * KT + t * KB + 4 * p;
             const float wt = w[t];
-            if (steep) {
-                const float2 a2 = make_float2(wt, wt);
-#pragma unroll
-                for (int rr = 0; rr < RT; ++rr)
-#pragma unroll
-                    for (int m = 0; m < CPT / 2; ++m) S[rr][m] = __fmul2_rn(S[rr][m], a2);
-            }
-            const float vw = steep ? 1.0f : wt;
             float2 v2[RT], acc[RT][2];
 #pragma unroll
             for (int rr = 0; rr < RT; ++rr) {
-                const float vv = vw * Io<IO>::to_f(vr[t * RB + rr]);
+                const float vv = wt * Io<IO>::to_f(vr[t * RB + rr]);
                 v2[rr] = make_float2(vv, vv);
                 acc[rr][0] = acc[rr][1] = make_float2(0.0f, 0.0f);
             }
@@ -337,12 +355,18 @@ __global__ void __launch_bounds__(C::NT, C::NT == 128 ? 4 : 8)
                 const float ut = u[t];
                 if (p < RT) os[t * RB + rg * RT + p] = ut * r[0];
             }
-        }
-        if (!steep && after != 1.0f) {
-#pragma unroll
-            for (int rr = 0; rr < RT; ++rr)
-#pragma unroll
-                for (int m = 0; m < CPT / 2; ++m) S[rr][m] = __fmul2_rn(S[rr][m], make_float2(after, after));
+        };
+        if (steep) {   // a loop of its own: the common one carries no trace of it
+            mul(mf[0]);
+#pragma unroll 1
+            for (int t = 0; t < nt; ++t) {
+                mul(wa[t]);
+                step(t);
+            }
+        } else {
+#pragma unroll 1
+            for (int t = 0; t < nt; ++t) step(t);
+            if (after != 1.0f) mul(after);
         }
         if (tid < 32 && more) factors(c + 1, gn);   // its buffer was last read in chunk c - 1
         __syncthreads();   // chunk c's buffer, every os entry, the next factors
@@ -375,16 +399,16 @@ __global__ void __launch_bounds__(C::NT, C::NT == 128 ? 4 : 8)
         if (tid == 0) mm[0] = dec::exp2_fix(base);   // warp 0 holds base
         __syncthreads();
         const float f = mm[0];
+        const bool v4 = rows16(dst0);
 #pragma unroll
         for (int rr = 0; rr < RT; ++rr) {
             const int i = row0 + rg * RT + rr;
             if (i >= dv) continue;
-            float *dst = dst0 + size_t(i) * dk;
 #pragma unroll
-            for (int m2 = 0; m2 < CPT / 2; ++m2) {
-                const int j = 4 * ((m2 >> 1) * P + p) + 2 * (m2 & 1);
-                if (j < dk) dst[j] = f * S[rr][m2].x;
-                if (j + 1 < dk) dst[j + 1] = f * S[rr][m2].y;
+            for (int m = 0; m < CPT / 4; ++m) {
+                const float2 s0 = S[rr][2 * m], s1 = S[rr][2 * m + 1];
+                state_st4(dst0 + size_t(i) * dk, 4 * (m * P + p), dk, v4,
+                          make_float4(f * s0.x, f * s0.y, f * s1.x, f * s1.y));
             }
         }
     }
@@ -450,7 +474,7 @@ int decay_general_launch(const DecayArgs &a, const DecayPlan &p, StatusRef st, c
     if (a.dk <= 64) return launch_general_dk<IO, 64>(a, p.narrow, st, stream);
     if (a.dk <= 128) return launch_general_dk<IO, 128>(a, p.narrow, st, stream);
     if (a.dk <= 256) return launch_general_dk<IO, 256>(a, p.narrow, st, stream);
-    return launch_general_dk<IO, 512>(a, p.narrow, st, stream);
+    return launch_general_cfg<IO, DecCfg<512, false>>(a, st, stream);
 }
 
 }  // namespace lr
