@@ -2,10 +2,23 @@
 //   S = a S + v k^T,  o = scale S q,  a = exp(a_log[h] + g[b, h]).
 //
 // The state is read and written once: 8 dk dv bytes per (batch row, head)
-// against 4 dk dv operations, so the kernel is bound by memory bandwidth (by
+// against 5 dk dv operations, so the kernel is bound by memory bandwidth (by
 // the launch and one trip to memory at one sequence).  TL lanes share a state
 // row, each holding groups of four consecutive keys; a warp has its R rows'
-// loads in flight before the first is used.
+// loads in flight before the first is used.  fp32 throughout; o is rounded once.
+//
+// Measured back to back in one graph, state larger than L2 (bf16 H16 d128): B64
+// 22.6 us, 88 % of the copy bandwidth; B32 12.9; B8 5.3; B1 2.5.  fp32 B32 H16
+// dk256 dv128 21.2 us, 93 %.
+//   four rows of a warp in flight against one: B64 23 us against 35, B8 5.4
+//   against 6.2; at B1, where it leaves fewer warps, 2.4 against 2.3.  Eight: B64
+//   22.6 against 23.2, but B1 3.1
+//   blocks of 64 threads against 128: B64 22.6 us against 23.2, B32 12.9
+//   against 13.1, B1 2.6 against 2.4; of 256: 23.7
+//   streaming loads and stores, the state being larger than the cache over a
+//   model's layers: B64 23.2 us against 23.5
+//   dk up to 512 in the same form: B32 H16 dk192 16.9 us against 36 with a row
+//   read element by element, which stays for dk that is no multiple of four
 #include "lr_decay.cuh"
 
 namespace lr {
@@ -24,13 +37,11 @@ __device__ __forceinline__ float4 step_ld4<__nv_bfloat16>(const __nv_bfloat16 *p
                        __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xffff0000u));
 }
 
-constexpr int kStepT = 128;
+constexpr int kStepT = 64;
 
-__device__ __forceinline__ float decay_of(float l) { return expf(l); }
-
-// VEC rows: dk % 4 == 0 and dk <= 4 TL (one group of four keys per lane).
+// dk % 4 == 0 and dk <= 4 TL V: V groups of four keys per lane.
 // A warp takes 32 / TL rows at a time, R times.
-template <typename IO, int TL, int R>
+template <typename IO, int TL, int R, int V>
 __global__ void __launch_bounds__(kStepT)
     decay_step_kernel(const IO *__restrict__ q, const IO *__restrict__ k, const IO *__restrict__ v,
                       const float *__restrict__ a_log, const IO *__restrict__ g, float scale,
@@ -38,37 +49,53 @@ __global__ void __launch_bounds__(kStepT)
                       int dv, int tiles) {
     constexpr int RPW = 32 / TL;          // rows a warp holds at once
     constexpr int ROWS = RPW * R;         // rows per warp
-    const int lane = threadIdx.x & 31, sub = lane / TL, j = 4 * (lane % TL);
+    const int lane = threadIdx.x & 31, sub = lane / TL, j0 = 4 * (lane % TL);
     const int64_t w = int64_t(blockIdx.x) * (kStepT / 32) + (threadIdx.x >> 5);
     if (w >= BH * tiles) return;   // warp-uniform
     const int64_t bh = w / tiles;
     const int row0 = int(w - bh * tiles) * ROWS;
     const int64_t b = bh / H;
     const int h = int(bh - b * H), hk = h / (H / Hk);
-    const bool col = j < dk;
     const float4 zero = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     const int64_t base = bh * dv;
-    float4 s[R];
+    float4 s[R][V];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
         const int i = row0 + r * RPW + sub;
-        s[r] = S_in != nullptr && col && i < dv ? __ldcs(reinterpret_cast<const float4 *>(S_in + (base + i) * dk + j))
-                                                : zero;
+#pragma unroll
+        for (int u = 0; u < V; ++u) {
+            const int j = j0 + 4 * TL * u;
+            s[r][u] = S_in != nullptr && j < dk && i < dv
+                          ? __ldcs(reinterpret_cast<const float4 *>(S_in + (base + i) * dk + j))
+                          : zero;
+        }
     }
-    const int64_t kat = (b * Hk + hk) * dk + j;
-    const float4 k4 = col ? step_ld4(k + kat) : zero, q4 = col ? step_ld4(q + kat) : zero;
+    float4 k4[V], q4[V];
+#pragma unroll
+    for (int u = 0; u < V; ++u) {
+        const int j = j0 + 4 * TL * u;
+        const int64_t kat = (b * Hk + hk) * dk + j;
+        k4[u] = j < dk ? step_ld4(k + kat) : zero;
+        q4[u] = j < dk ? step_ld4(q + kat) : zero;
+    }
     float l = a_log != nullptr ? a_log[h] : 0.0f;
     if (g != nullptr) l += Io<IO>::to_f(g[bh]);
-    const float a = decay_of(l);
+    const float a = expf(l);
 #pragma unroll
     for (int r = 0; r < R; ++r) {
         const int i = row0 + r * RPW + sub;
         const bool in = i < dv;
         const float vi = in ? Io<IO>::to_f(v[base + i]) : 0.0f;
-        s[r] = make_float4(fmaf(a, s[r].x, vi * k4.x), fmaf(a, s[r].y, vi * k4.y), fmaf(a, s[r].z, vi * k4.z),
-                           fmaf(a, s[r].w, vi * k4.w));
-        if (in && col) __stcs(reinterpret_cast<float4 *>(S_out + (base + i) * dk + j), s[r]);
-        float acc = fmaf(s[r].x, q4.x, fmaf(s[r].y, q4.y, fmaf(s[r].z, q4.z, s[r].w * q4.w)));
+        float acc = 0.0f;
+#pragma unroll
+        for (int u = 0; u < V; ++u) {
+            const int j = j0 + 4 * TL * u;
+            float4 &x = s[r][u];
+            x = make_float4(fmaf(a, x.x, vi * k4[u].x), fmaf(a, x.y, vi * k4[u].y), fmaf(a, x.z, vi * k4[u].z),
+                            fmaf(a, x.w, vi * k4[u].w));
+            if (in && j < dk) __stcs(reinterpret_cast<float4 *>(S_out + (base + i) * dk + j), x);
+            acc += fmaf(x.x, q4[u].x, fmaf(x.y, q4[u].y, fmaf(x.z, q4[u].z, x.w * q4[u].w)));
+        }
 #pragma unroll
         for (int m = TL / 2; m >= 1; m >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, m);
         if (in && lane % TL == 0) o[base + i] = Io<IO>::from_f(scale * acc);
@@ -89,7 +116,7 @@ __global__ void __launch_bounds__(kStepT)
     const int h = int(bh - b * H), hk = h / (H / Hk);
     float l = a_log != nullptr ? a_log[h] : 0.0f;
     if (g != nullptr) l += Io<IO>::to_f(g[bh]);
-    const float a = decay_of(l), vi = Io<IO>::to_f(v[row]);
+    const float a = expf(l), vi = Io<IO>::to_f(v[row]);
     const IO *kb = k + (b * Hk + hk) * dk, *qb = q + (b * Hk + hk) * dk;
     float acc = 0.0f;
 #pragma unroll 4
@@ -109,8 +136,6 @@ int step_io(const IO *q, const IO *k, const IO *v, const float *a_log, const IO 
             const float *S_in, float *S_out, IO *o, int64_t B, int64_t H, int64_t Hk, int64_t dk, int64_t dv,
             cudaStream_t s) {
     const int64_t BH = B * H;
-    int sms = 0;
-    if (device_sm_count(&sms) != LR_OK) return LR_ERR_CUDA;
     auto go = [&](auto kern, int rows) -> int {
         const int64_t tiles = (dv + rows - 1) / rows;
         const int64_t grid = (BH * tiles + kStepT / 32 - 1) / (kStepT / 32);
@@ -119,12 +144,12 @@ int step_io(const IO *q, const IO *k, const IO *v, const float *a_log, const IO 
                                                int(dk), int(dv), int(tiles));
         return cudaGetLastError() == cudaSuccess ? LR_OK : LR_ERR_CUDA;
     };
-    if (dk % 4 == 0 && dk <= 128) {
-        // four rows in flight per lane once that still fills the SMs
-        const bool deep = BH * dv * dk >= int64_t(sms) * 64 * 512;
-        if (dk <= 32) return deep ? go(decay_step_kernel<IO, 8, 4>, 16) : go(decay_step_kernel<IO, 8, 1>, 4);
-        if (dk <= 64) return deep ? go(decay_step_kernel<IO, 16, 4>, 8) : go(decay_step_kernel<IO, 16, 1>, 2);
-        return deep ? go(decay_step_kernel<IO, 32, 4>, 4) : go(decay_step_kernel<IO, 32, 1>, 1);
+    if (dk % 4 == 0 && dk <= 512) {
+        if (dk <= 32) return go(decay_step_kernel<IO, 8, 4, 1>, 16);
+        if (dk <= 64) return go(decay_step_kernel<IO, 16, 4, 1>, 8);
+        if (dk <= 128) return go(decay_step_kernel<IO, 32, 4, 1>, 4);
+        if (dk <= 256) return go(decay_step_kernel<IO, 32, 2, 2>, 2);
+        return go(decay_step_kernel<IO, 32, 2, 4>, 2);
     }
     const int64_t grid = (BH * dv + kStepT / 32 - 1) / (kStepT / 32);
     if (grid > INT32_MAX) return LR_ERR_UNSUPPORTED;

@@ -7,6 +7,12 @@
 // kernel.  A group stays in the registers of the lanes that share it: the
 // mean, then the centred squares (no cancellation), then the output.
 //
+// Measured, inputs larger than L2 (share of the copy bandwidth): bf16 16384 x
+// 2048, G 16, gate 34.4 us (86 %); fp32 61 us (97 %); bf16 8192 x 4096, G 32 26.5
+// us (75 %); fp32 3001 x 1920, G 24 8.8 us (77 %); bf16 8192 x 4096, G 2, gate
+// 35.5 us (84 %; element by element 82 us).  Sums and the affine step in packed
+// fp32 pairs: the first 38.4 -> 36.7 us.
+//
 //   lanes   groups of up to 128 vectors (16 bytes; 8 for a bf16 group of an odd
 //           number of those): TL lanes of a warp hold a group, up to four vectors
 //           each, with the fewest idle slots; a thread keeps its group and walks
@@ -222,22 +228,26 @@ __global__ void __launch_bounds__(NT)
                 if (GATE) zr[u] = __ldcs(z + i);
             }
         }
-        float v[V][VN], s = 0.0f;
+        float v[V][VN];
+        float2 s2 = make_float2(0.0f, 0.0f);
 #pragma unroll
         for (int u = 0; u < V; ++u) {
             X::widen(xr[u], v[u]);
 #pragma unroll
-            for (int i = 0; i < VN; ++i) s += v[u][i];
+            for (int i = 0; i < VN; i += 2) s2 = __fadd2_rn(s2, pair(v[u] + i));
         }
-        const float mean = block_sum<NT>(s, red) * a.inv_d;
-        s = 0.0f;
+        const float mean = block_sum<NT>(s2.x + s2.y, red) * a.inv_d;
+        float s = 0.0f;
 #pragma unroll
         for (int u = 0; u < V; ++u) {
+            s2 = make_float2(0.0f, 0.0f);
 #pragma unroll
-            for (int i = 0; i < VN; ++i) {
-                v[u][i] -= mean;
-                if (threadIdx.x + u * NT < nv) s = fmaf(v[u][i], v[u][i], s);
+            for (int i = 0; i < VN; i += 2) {
+                const float2 c = __fadd2_rn(pair(v[u] + i), make_float2(-mean, -mean));
+                s2 = __ffma2_rn(c, c, s2);
+                v[u][i] = c.x, v[u][i + 1] = c.y;
             }
+            if (threadIdx.x + u * NT < nv) s += s2.x + s2.y;
         }
         const float rs = 1.0f / sqrtf(fmaf(block_sum<NT>(s, red), a.inv_d, a.eps));
 #pragma unroll
@@ -252,26 +262,26 @@ __global__ void __launch_bounds__(NT)
     }
 }
 
-// any sizes: one block per (row, group), three passes over the group
-template <typename IO>
-__global__ void __launch_bounds__(128)
+// any sizes: a block of NT threads per (row, group), three passes over the group
+template <typename IO, int NT>
+__global__ void __launch_bounds__(NT)
     group_norm_any_kernel(const NormArgs a) {
-    __shared__ float red[4];
+    __shared__ float red[NT / 32];
     const IO *x = static_cast<const IO *>(a.x), *z = static_cast<const IO *>(a.z);
     IO *y = static_cast<IO *>(a.y);
     for (int64_t rg = blockIdx.x; rg < a.N * a.G; rg += gridDim.x) {
         const int gi = int(rg % a.G);
         const int64_t at = rg * a.d;
         float s = 0.0f;
-        for (int i = threadIdx.x; i < a.d; i += 128) s += Io<IO>::to_f(x[at + i]);
-        const float mean = block_sum<128>(s, red) * a.inv_d;
+        for (int i = threadIdx.x; i < a.d; i += NT) s += Io<IO>::to_f(x[at + i]);
+        const float mean = block_sum<NT>(s, red) * a.inv_d;
         s = 0.0f;
-        for (int i = threadIdx.x; i < a.d; i += 128) {
+        for (int i = threadIdx.x; i < a.d; i += NT) {
             const float t = Io<IO>::to_f(x[at + i]) - mean;
             s = fmaf(t, t, s);
         }
-        const float rs = 1.0f / sqrtf(fmaf(block_sum<128>(s, red), a.inv_d, a.eps));
-        for (int i = threadIdx.x; i < a.d; i += 128) {
+        const float rs = 1.0f / sqrtf(fmaf(block_sum<NT>(s, red), a.inv_d, a.eps));
+        for (int i = threadIdx.x; i < a.d; i += NT) {
             const int c = gi * a.d + i;
             float n = (Io<IO>::to_f(x[at + i]) - mean) * rs;
             if (a.gamma != nullptr) n *= a.gamma[c];
@@ -287,7 +297,9 @@ template <typename X, int TL, int V, bool GATE>
 int launch_lanes(const NormArgs &a, int sms, cudaStream_t s) {
     constexpr int SETS = 256 / TL;
     // groups of a row per block: the count that leaves the fewest sets idle, the
-    // larger of two (neighbouring groups are neighbouring bytes)
+    // larger of two, since neighbouring groups are neighbouring bytes (16384 x 2048
+    // bf16, G 32, gate: the smaller 45.5 us against 36.1; 8192 x 4096 32.3 against
+    // 26.5)
     int gper = 1;
     double best = 0.0;
     for (int g = 1; g <= SETS && g <= a.G; ++g) {
@@ -296,12 +308,14 @@ int launch_lanes(const NormArgs &a, int sms, cudaStream_t s) {
     }
     const int rper = SETS / gper, gy = (a.G + gper - 1) / gper;
     const int64_t row_blocks = (a.N + rper - 1) / rper;
-    // rows in flight per thread, about four vectors in all, once every SM has
-    // its blocks (16384 x 2048 bf16 with gate: 4 rows of one vector 38 us, 2
-    // rows 41 us, 1 row 49 us; 8192 x 4096 without: 35 us, with 8 rows 45 us; 4,
-    // 8 or 16 blocks per SM instead of 6: 46, 41, 42 us); one row where there
-    // are few
-    constexpr int R = V == 1 ? 4 : V == 2 ? 2 : 1;
+    // Rows in flight per thread once every SM has its blocks, one where there
+    // are few.  bf16: 16384 x 2048, G 32, gate (one vector a lane) 1 row 41.5 us, 2
+    // rows 34.7, 4 rows 36.1; without gate 2 rows 30.0, 4 rows 27.3; 8192 x 4096,
+    // G 32 (two vectors) 1 row 28.8 us, 2 rows 26.5, 4 rows 32.9.  Three and four
+    // vectors: 4096 x 3200, G 40, gate 1 row 18.3 us, 2 rows 26.7.  Blocks per SM,
+    // 16384 x 2048, G 16, gate at one vector a lane: 4, 5, 6, 7, 8 of them 46, 40.4,
+    // 36.7, 39.7, 41 us.
+    constexpr int R = V == 1 ? (GATE ? 2 : 4) : V == 2 ? 2 : 1;
     const int64_t full = int64_t(sms) * 6;
     const bool deep = row_blocks * gy >= full * R;
     int64_t gx = deep ? (full + gy - 1) / gy : row_blocks;
@@ -316,7 +330,7 @@ int launch_lanes(const NormArgs &a, int sms, cudaStream_t s) {
 
 template <typename X, int NT, int V, bool GATE>
 int launch_block(const NormArgs &a, int sms, cudaStream_t s) {
-    const int64_t ng = a.N * a.G, most = int64_t(sms) * (2048 / NT) * 8;
+    const int64_t ng = a.N * a.G, most = int64_t(sms) * (2048 / NT) * 2;
     group_norm_block_kernel<X, NT, V, GATE><<<unsigned(ng < most ? ng : most), NT, 0, s>>>(a);
     return cudaGetLastError() == cudaSuccess ? LR_OK : LR_ERR_CUDA;
 }
@@ -324,20 +338,28 @@ int launch_block(const NormArgs &a, int sms, cudaStream_t s) {
 template <typename IO>
 int launch_any(const NormArgs &a, int sms, cudaStream_t s) {
     const int64_t ng = a.N * a.G, most = int64_t(sms) * 128;
-    group_norm_any_kernel<IO><<<unsigned(ng < most ? ng : most), 128, 0, s>>>(a);
+    const unsigned grid = unsigned(ng < most ? ng : most);
+    // one warp where a block's barriers cost more than its width gives (4096 x
+    // 999 fp32, G 9: 21.8 us against 36.4; 8192 x 1111, G 1: 25.6 against 20.2)
+    if (a.d <= 256)
+        group_norm_any_kernel<IO, 32><<<grid, 32, 0, s>>>(a);
+    else
+        group_norm_any_kernel<IO, 128><<<grid, 128, 0, s>>>(a);
     return cudaGetLastError() == cudaSuccess ? LR_OK : LR_ERR_CUDA;
 }
 
-// nv vectors per group: lanes x vectors with the fewest idle slots, the wider
-// lane set where two are equal
+// nv vectors per group: lanes x vectors with the fewest idle slots (4096 x 3200
+// bf16, 10 vectors: 4 x 3 18.2 us, 16 x 1 23.5).  Past a warp's 128 vectors a
+// block per group, up to four vectors a thread (2000 x 12000 bf16, G 8, gate, 375
+// vectors of 8 bytes: 128 x 4 31.3 us, 256 x 2 38.4).
 template <typename X, bool GATE>
 int launch_vec(const NormArgs &a, int nv, int sms, cudaStream_t s) {
     if (nv <= 4) return launch_lanes<X, 4, 1, GATE>(a, sms, s);
     if (nv <= 8) return launch_lanes<X, 8, 1, GATE>(a, sms, s);
     if (nv <= 12) return launch_lanes<X, 4, 3, GATE>(a, sms, s);
-    // two vectors a lane halve the shuffles (8192 x 4096 bf16 29 us against 35);
-    // with a gate's loads the narrower rows win (39 us against 43)
-    if (nv <= 16) return launch_lanes<X, GATE ? 16 : 8, GATE ? 1 : 2, GATE>(a, sms, s);
+    // two vectors a lane halve the shuffles: 16384 x 2048 bf16, G 16, gate 34.4 us
+    // against 36.9 with 16 lanes; 8192 x 4096 without gate 26.5 against 30.2
+    if (nv <= 16) return launch_lanes<X, 8, 2, GATE>(a, sms, s);
     if (nv <= 24) return launch_lanes<X, 8, 3, GATE>(a, sms, s);
     if (nv <= 32) return launch_lanes<X, 16, 2, GATE>(a, sms, s);
     if (nv <= 48) return launch_lanes<X, 16, 3, GATE>(a, sms, s);
@@ -345,7 +367,7 @@ int launch_vec(const NormArgs &a, int nv, int sms, cudaStream_t s) {
     if (nv <= 96) return launch_lanes<X, 32, 3, GATE>(a, sms, s);
     if (nv <= 128) return launch_lanes<X, 32, 4, GATE>(a, sms, s);
     if (nv <= 256) return launch_block<X, 128, 2, GATE>(a, sms, s);
-    if (nv <= 512) return launch_block<X, 256, 2, GATE>(a, sms, s);
+    if (nv <= 512) return launch_block<X, 128, 4, GATE>(a, sms, s);
     if (nv <= 1024) return launch_block<X, 256, 4, GATE>(a, sms, s);
     return launch_block<X, 512, 4, GATE>(a, sms, s);
 }
