@@ -16,6 +16,7 @@ There is no fallback: if the library is missing this module raises at import.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 import threading
 from typing import Optional, Tuple
@@ -113,6 +114,22 @@ def _load():
 
 _lib = _load()
 LIB_PATH = _build.LIB_PATH
+
+
+def _load_torch_module():
+    path = _build.TORCH_MODULE
+    if not os.path.exists(path):
+        raise ImportError(f"{path} is missing: build it with selective_state_space_chunked_gb300.build.build()")
+    spec = importlib.util.spec_from_file_location("_lrtorch", path)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    return mod
+
+
+# The helpers that run once per layer and token first offer their arguments to
+# this module, which takes those that are already what the kernels take and
+# answers None to the others.
+_lrtorch = _load_torch_module()
 
 
 class LrError(RuntimeError):
@@ -754,16 +771,8 @@ def _shaped(t: Optional[torch.Tensor], shape, name: str):
         raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
 
 
-# The helpers below are called once per layer and token, where the GPU's own
-# time is a few microseconds: tensors that are already what the kernel takes
-# pass through one test each, and the stream is read as a raw handle.
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-
-
 def _stream_of(t: torch.Tensor) -> int:
     """The current stream of t's GPU (a cudaStream_t as an int)."""
-    if _raw_stream is not None:
-        return _raw_stream(t.get_device())
     return torch.cuda.current_stream(t.device).cuda_stream
 
 
@@ -781,19 +790,6 @@ def _par(t: Optional[torch.Tensor], dev) -> Optional[torch.Tensor]:
     return _dev(t.float(), dev)
 
 
-# workspace sizes by problem (the query runs the library's plan)
-_DECAY_WS = {}
-
-
-def _decay_workspace_size(key) -> int:
-    n = _DECAY_WS.get(key)
-    if n is None:
-        if len(_DECAY_WS) >= 1024:
-            _DECAY_WS.clear()
-        n = _DECAY_WS[key] = lr_decay_attn_workspace_size(*key)
-    return n
-
-
 def decay_attn(q, k, v, H: int, Hk: Optional[int] = None, a_log=None, g=None, S0=None, lens=None,
                scale: float = 1.0, workspace=None, out=None,
                sync_host: bool = True) -> Tuple[torch.Tensor, torch.Tensor]:
@@ -809,6 +805,11 @@ def decay_attn(q, k, v, H: int, Hk: Optional[int] = None, a_log=None, g=None, S0
     inputs with host (or no) ``out`` run the library's host-buffer path (without
     ``lens``; ``sync_host=False`` queues it, as for ``selective_scan``).  A log
     decay above 0 sets LR_ERR_RANGE (see ``check_status``)."""
+    if workspace is None and out is None:
+        r = _lrtorch.decay_attn(q, k, v, H, Hk, a_log, g, S0, lens, scale)
+        if r is not None:
+            o, Sf, _tls.ws = r
+            return o, Sf
     (B, L, _), Hk, dk, dv, io = _heads_of(q, k, v, g, H, Hk, 3)
     if a_log is not None:
         _shaped(a_log, (H,), "a_log")
@@ -839,7 +840,7 @@ def decay_attn(q, k, v, H: int, Hk: Optional[int] = None, a_log=None, g=None, S0
         Sf = torch.empty((B, H, dv, dk), dtype=torch.float32, device=dev)
     else:
         (o, Sf), host_out = _outputs(out, specs, dev)
-    ws, wsb = _workspace(_decay_workspace_size((B, L, H, Hk, dk, dv, io)), dev, workspace)
+    ws, wsb = _workspace(lr_decay_attn_workspace_size(B, L, H, Hk, dk, dv, io), dev, workspace)
     rc = _lib.lr_decay_attn_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(a_log), _ptr(g), _ptr(lens), scale,
                                 _ptr(S0), o.data_ptr(), Sf.data_ptr(), B, L, H, Hk, dk, dv, io, ws.data_ptr(), wsb,
                                 _stream_of(q))
@@ -859,6 +860,9 @@ def group_norm_act(x, G: int, gamma=None, beta=None, z=None, act: str = "none", 
     a = _ACT.get(act)
     if a is None:
         raise ValueError(f"unknown activation {act!r}; use one of {sorted(_ACT)}")
+    y = _lrtorch.group_norm_act(x, G, gamma, beta, z, a, eps, out)
+    if y is not None:
+        return y
     shape = x.shape
     C = shape[-1]
     if G < 1 or C % G:
@@ -977,6 +981,9 @@ def decay_attn_step(q, k, v, H: int, Hk: Optional[int] = None, a_log=None, g=Non
     or None, one dtype on the GPU; a_log: (H,) fp32 or None; S: (B, H, dv, dk)
     fp32 or None (zero).  Returns (o (B, H*dv), S_new); ``S_out`` gives the
     buffer S_new is written to (it may be ``S`` itself)."""
+    r = _lrtorch.decay_attn_step(q, k, v, H, Hk, a_log, g, S, S_out, scale)
+    if r is not None:
+        return r
     (B, _), Hk, dk, dv, io = _heads_of(q, k, v, g, H, Hk, 2)
     shape = (B, H, dv, dk)
     if a_log is not None:

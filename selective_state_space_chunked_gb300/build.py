@@ -2,16 +2,20 @@
 
 Every translation unit under ``csrc/`` is compiled for sm_103a only
 (``-gencode arch=compute_103a,code=sm_103a``), in parallel, then linked into
-one shared library against the shared CUDA runtime.  The build is skipped
-when the library is newer than every source and header.
+one shared library against the shared CUDA runtime.  ``csrc/lr_torch.cpp``, the
+short path of the torch helpers, becomes the extension module ``_build/_lrtorch``
+beside it, against the library and the installed torch.  The build is skipped
+when both are newer than every source and header.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
+import sysconfig
 import tempfile
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -21,6 +25,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB_NAME = "liblrscan.so"
 LIB_PATH = os.path.join(BUILD_DIR, LIB_NAME)
+TORCH_SRC = os.path.join(CSRC, "lr_torch.cpp")
+TORCH_MODULE = os.path.join(BUILD_DIR, "_lrtorch" + sysconfig.get_config_var("EXT_SUFFIX"))
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
@@ -35,6 +41,10 @@ def _nvcc() -> str:
     raise RuntimeError("nvcc not found: the CUDA toolkit is required to build lrscan")
 
 
+def _torch_dir() -> str:
+    return list(importlib.util.find_spec("torch").submodule_search_locations)[0]
+
+
 def _sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
@@ -42,13 +52,13 @@ def _sources():
 def _deps():
     return (_sources() + glob.glob(os.path.join(CSRC, "*.cuh"))
             + glob.glob(os.path.join(CSRC, "*.h"))
-            + glob.glob(os.path.join(INCLUDE, "*.h")) + [__file__])
+            + glob.glob(os.path.join(INCLUDE, "*.h")) + [TORCH_SRC, __file__])
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB_PATH):
+    if not os.path.exists(LIB_PATH) or not os.path.exists(TORCH_MODULE):
         return False
-    t = os.path.getmtime(LIB_PATH)
+    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(TORCH_MODULE))
     return all(os.path.getmtime(p) <= t for p in _deps())
 
 
@@ -60,27 +70,40 @@ def build(force: bool = False, verbose: bool = False) -> str:
     nvcc = _nvcc()
     tmpdir = tempfile.mkdtemp(prefix="obj_", dir=BUILD_DIR)
     try:
+        torch_dir = _torch_dir()
+        cuda_dir = os.path.dirname(os.path.dirname(os.path.realpath(nvcc)))
+
         def compile_one(src):
             obj = os.path.join(tmpdir, os.path.basename(src) + ".o")
-            cmd = [nvcc, *ARCH, *NVCC_FLAGS, "-c", src, "-o", obj]
+            if src == TORCH_SRC:
+                cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-I" + INCLUDE,
+                       "-I" + os.path.join(torch_dir, "include"), "-I" + os.path.join(cuda_dir, "include"),
+                       "-I" + sysconfig.get_paths()["include"], "-c", src, "-o", obj]
+            else:
+                cmd = [nvcc, *ARCH, *NVCC_FLAGS, "-c", src, "-o", obj]
             r = subprocess.run(cmd, capture_output=True, text=True)
             if r.returncode != 0:
-                raise RuntimeError(f"nvcc failed on {src}:\n{r.stdout}\n{r.stderr}")
+                raise RuntimeError(f"{cmd[0]} failed on {src}:\n{r.stdout}\n{r.stderr}")
             if verbose and r.stderr:
                 print(r.stderr)
             return obj
 
+        def link(cmd, path):
+            fd, tmp_lib = tempfile.mkstemp(suffix=".so", dir=BUILD_DIR)
+            os.close(fd)
+            r = subprocess.run([*cmd, "-o", tmp_lib], capture_output=True, text=True)
+            if r.returncode != 0:
+                os.unlink(tmp_lib)
+                raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+            os.replace(tmp_lib, path)
+
         with cf.ThreadPoolExecutor(max_workers=max(1, min(8, os.cpu_count() or 1))) as ex:
-            objs = list(ex.map(compile_one, _sources()))
-        fd, tmp_lib = tempfile.mkstemp(suffix=".so", dir=BUILD_DIR)
-        os.close(fd)
-        cmd = [nvcc, *ARCH, "-shared", "-cudart", "shared", *objs, "-o", tmp_lib,
-               "-Xlinker", "-rpath,/usr/local/cuda/lib64"]
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            os.unlink(tmp_lib)
-            raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-        os.replace(tmp_lib, LIB_PATH)
+            *objs, torch_obj = ex.map(compile_one, [*_sources(), TORCH_SRC])
+        link([nvcc, *ARCH, "-shared", "-cudart", "shared", *objs, "-Xlinker", "-rpath,/usr/local/cuda/lib64"],
+             LIB_PATH)
+        link(["g++", "-shared", torch_obj, "-Wl,-rpath,$ORIGIN", "-L" + BUILD_DIR, "-l:" + LIB_NAME,
+              "-L" + os.path.join(torch_dir, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda",
+              f"-L{cuda_dir}/lib64", "-lcudart"], TORCH_MODULE)
     finally:
         shutil.rmtree(tmpdir, ignore_errors=True)
     return LIB_PATH
