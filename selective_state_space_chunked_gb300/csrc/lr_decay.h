@@ -28,6 +28,11 @@ struct DecayArgs {
     int64_t seg_len;
     float *seg_state;
     long long *seg_tot;
+    // Tensor cores, dk > 128: the key columns in parts of kPartKeys, each a
+    // recurrence of its own with the same decays; their outputs, fp32, in
+    // o_part [part][B][L][H][dv], are summed by a last launch.
+    int parts;
+    float *o_part;
 };
 
 struct DecayPlan {
@@ -35,7 +40,8 @@ struct DecayPlan {
     int n_seg = 1;
     int64_t seg_len = 0;
     bool narrow = false;     // CUDA cores: few columns per thread (short sequences)
-    size_t ws_bytes = 0;     // status, then seg_tot, then seg_state
+    int parts = 1;
+    size_t ws_bytes = 0;     // status, then seg_tot, seg_state, o_part
 };
 
 int decay_plan(int64_t B, int64_t L, int64_t H, int64_t Hk, int64_t dk, int64_t dv, lr_dtype io, DecayPlan *p);
@@ -44,10 +50,11 @@ int decay_attn_launch(DecayArgs a, lr_dtype io, const DecayPlan &p, void *worksp
 // CUDA-core kernel, one translation unit per I/O type
 template <typename IO>
 int decay_general_launch(const DecayArgs &a, const DecayPlan &p, StatusRef st, cudaStream_t stream);
-// tensor-core kernel: bf16 I/O, dk <= 128, dk and dv multiples of 8
+// tensor-core kernel: bf16 I/O, dk and dv multiples of 8
 int decay_tensor_launch(const DecayArgs &a, StatusRef st, cudaStream_t stream);
 constexpr int kDecayChunk = 128;    // its steps per chunk (segments are multiples of it)
 constexpr int kDecayRows = 64;      // its value rows per block
+constexpr int kPartKeys = 128;      // its key columns per block
 // rows of the state per block of the general kernel
 int decay_general_rows(int64_t dk, bool narrow);
 

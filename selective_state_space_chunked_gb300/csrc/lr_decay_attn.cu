@@ -31,12 +31,13 @@ int decay_plan(int64_t B, int64_t L, int64_t H, int64_t Hk, int64_t dk, int64_t 
     if (device_sm_count(&sms) != LR_OK) return LR_ERR_CUDA;
     int64_t n = 1, unit = 16;
     p->narrow = false;
-    p->path = io == LR_BF16 && dk <= 128 && dk % 8 == 0 && dv % 8 == 0 && L >= kTensorMinLen;
+    p->path = io == LR_BF16 && dk % 8 == 0 && dv % 8 == 0 && L >= kTensorMinLen;
+    p->parts = p->path == 1 ? int((dk + kPartKeys - 1) / kPartKeys) : 1;
     if (p->path == 1) {
         // one block per SM: waves of blocks, each as long as its chunks and a
         // block's start
         unit = kDecayChunk;
-        const int64_t chunks = (L + unit - 1) / unit, blocks = B * H * ((dv + kDecayRows - 1) / kDecayRows);
+        const int64_t chunks = (L + unit - 1) / unit, blocks = B * H * ((dv + kDecayRows - 1) / kDecayRows) * p->parts;
         auto waves = [&](int64_t b) { return double((b + sms - 1) / sms); };
         double best = waves(blocks) * (double(chunks) + kBlockCost);
         for (int64_t s = 2; s <= kMaxSeg && 2 * s <= chunks; ++s) {
@@ -71,6 +72,7 @@ int decay_plan(int64_t B, int64_t L, int64_t H, int64_t Hk, int64_t dk, int64_t 
     p->n_seg = int((L + p->seg_len - 1) / p->seg_len);
     const size_t segs = size_t(B) * H * (p->n_seg - 1);
     p->ws_bytes = kStatusBytes + (segs * sizeof(long long) + 15) / 16 * 16 + segs * dv * dk * sizeof(float);
+    if (p->parts > 1) p->ws_bytes += size_t(p->parts) * B * L * H * dv * sizeof(float);
     return LR_OK;
 }
 
@@ -81,6 +83,8 @@ int decay_attn_launch(DecayArgs a, lr_dtype io, const DecayPlan &p, void *worksp
     a.seg_len = p.seg_len;
     a.seg_tot = reinterpret_cast<long long *>(ws);
     a.seg_state = reinterpret_cast<float *>(ws + (segs * sizeof(long long) + 15) / 16 * 16);
+    a.parts = p.parts;
+    a.o_part = a.seg_state + segs * a.dv * a.dk;
     const StatusRef st = call_status(workspace);
     if (p.path == 1) return decay_tensor_launch(a, st, stream);
     return io == LR_BF16 ? decay_general_launch<__nv_bfloat16>(a, p, st, stream)

@@ -48,6 +48,13 @@
 //                for nothing else of the state's
 //   output (4)   o = scale / w O (a steep chunk's Q S^T is scaled by rows before
 //                PD V is added)
+// More than 128 keys (PARTS): the state's key columns are independent of one
+// another and o_t = sum over j of S_t[:, j] q_t[j], so each 128 of them run as a
+// recurrence of their own, in blocks of their own, and a last launch adds their
+// fp32 outputs and rounds the sum.  The scores' products with V are repeated by
+// every part; at B2 L1500 H8 dk256 dv128 52 us against 178 on the CUDA cores, B4
+// L4096 H16 dk256 dv128 265 against 1528, B4 L1024 H8 dk512 dv128 80 against 387,
+// B1 L64 H4 dk192 dv64 17 against 56.
 // TMEM: P 2 x 128 columns (PD inside), O 64, dS 3 x 64: all 512.
 // Loops over columns stay rolled and waits share one slow path: with every
 // role's code unrolled the warps waited for instruction fetches more than for
@@ -209,6 +216,7 @@ constexpr uint32_t TMEM_COLS = 256;
 constexpr uint32_t IDESC = umma_idesc_bf16(128, 192, 1, 1);
 }  // namespace ds
 
+template <bool PARTS>
 __global__ void __launch_bounds__(ds::THREADS, 1)
     decay_state_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                        const DecayArgs a, int n_vt, uint64_t timeout_ns, StatusRef sref) {
@@ -231,13 +239,16 @@ __global__ void __launch_bounds__(ds::THREADS, 1)
     int x = blockIdx.x;
     const int vt = x % n_vt;
     x /= n_vt;
+    const int part = PARTS ? x % a.parts : 0;
+    if (PARTS) x /= a.parts;
     const int seg = x % nseg, bh = x / nseg;
     const int b = bh / a.H, h = bh - b * a.H, hk = h / (a.H / a.Hk);
     const int len = dec::row_len(a.lens, b, a.L);
     const int s0 = int(int64_t(seg) * a.seg_len);
     const int nrun = max(0, min(len, int(min(a.L, int64_t(s0) + a.seg_len))) - s0);
     const int n_chunks = (nrun + C - 1) / C;
-    const int dk = a.dk, dv = a.dv;
+    // the block's key columns: k0 .. k0 + dk - 1 of ldk
+    const int ldk = a.dk, k0 = PARTS ? kPartKeys * part : 0, dk = PARTS ? min(kPartKeys, ldk - k0) : ldk, dv = a.dv;
     const bool two = dk > 64;
 
     uint64_t *bar = reinterpret_cast<uint64_t *>(sm + OFF_BAR);
@@ -270,8 +281,8 @@ __global__ void __launch_bounds__(ds::THREADS, 1)
     auto load_k = [&](int c) {
         const int st = c % NS;
         mbar_arrive_expect_tx(&bar[FULL_K + st], two ? K_BYTES : HALF);
-        tma_load_4d(sm + OFF_K + st * K_BYTES, &tm_k, &bar[FULL_K + st], 0, hk, s0 + c * C, b);
-        if (two) tma_load_4d(sm + OFF_K + st * K_BYTES + HALF, &tm_k, &bar[FULL_K + st], 64, hk, s0 + c * C, b);
+        tma_load_4d(sm + OFF_K + st * K_BYTES, &tm_k, &bar[FULL_K + st], k0, hk, s0 + c * C, b);
+        if (two) tma_load_4d(sm + OFF_K + st * K_BYTES + HALF, &tm_k, &bar[FULL_K + st], k0 + 64, hk, s0 + c * C, b);
     };
     auto load_v = [&](int c) {
         const int st = c % NS;
@@ -441,8 +452,8 @@ __global__ void __launch_bounds__(ds::THREADS, 1)
         tc_fence_after();
         const uint32_t D = tmem + 32 * sh + (uint32_t((warp & 3) * 32) << 16);
         const float f = dec::exp2_fix(tot);
-        const float *src = seg == 0 && a.S0 != nullptr ? a.S0 + (size_t(bh) * dv + i0) * dk + j : nullptr;
-        float *dst = a.seg_state + ((size_t(bh) * nseg + seg) * dv + i0) * dk + j;
+        const float *src = seg == 0 && a.S0 != nullptr ? a.S0 + (size_t(bh) * dv + i0) * ldk + k0 + j : nullptr;
+        float *dst = a.seg_state + ((size_t(bh) * nseg + seg) * dv + i0) * ldk + k0 + j;
 #pragma unroll
         for (int q = 0; q < 32; q += 16) {
             float d1[16] = {}, d2[16] = {}, d3[16] = {};
@@ -457,10 +468,10 @@ __global__ void __launch_bounds__(ds::THREADS, 1)
             for (int r = 0; r < 16; ++r)
                 if (j < dk && i0 + q + r < dv) {
                     const float y = d1[r] + (d2[r] + d3[r]);
-                    dst[size_t(q + r) * dk] = src != nullptr ? fmaf(f, src[size_t(q + r) * dk], y) : y;
+                    dst[size_t(q + r) * ldk] = src != nullptr ? fmaf(f, src[size_t(q + r) * ldk], y) : y;
                 }
         }
-        if (vt == 0 && tid == 0) a.seg_tot[size_t(bh) * nseg + seg] = tot;
+        if (vt == 0 && part == 0 && tid == 0) a.seg_tot[size_t(bh) * nseg + seg] = tot;
     }
     tc_fence_before();
     __syncthreads();
@@ -469,6 +480,8 @@ __global__ void __launch_bounds__(ds::THREADS, 1)
 }
 
 // ---------------------------------------------------------------------------
+// PARTS: the block's part of the key columns, its outputs a term of the sum
+template <bool PARTS>
 __global__ void __launch_bounds__(dt::THREADS, 1)
     decay_tensor_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                         const __grid_constant__ CUtensorMap tm_v, const DecayArgs a, int n_vt, uint64_t timeout_ns,
@@ -486,6 +499,8 @@ __global__ void __launch_bounds__(dt::THREADS, 1)
     int x = blockIdx.x;
     const int vt = x % n_vt;
     x /= n_vt;
+    const int part = PARTS ? x % a.parts : 0;
+    if (PARTS) x /= a.parts;
     const int seg = x % nseg, bh = x / nseg;
     const int b = bh / a.H, h = bh - b * a.H, hk = h / (a.H / a.Hk);
     const int len = dec::row_len(a.lens, b, a.L);
@@ -493,7 +508,8 @@ __global__ void __launch_bounds__(dt::THREADS, 1)
     const int send = int(min(a.L, int64_t(s0) + a.seg_len));
     const int nrun = max(0, min(len, send) - s0);
     const int n_chunks = (nrun + C - 1) / C;
-    const int dk = a.dk, dv = a.dv;
+    // the block's key columns: k0 .. k0 + dk - 1 of ldk
+    const int ldk = a.dk, k0 = PARTS ? kPartKeys * part : 0, dk = PARTS ? min(kPartKeys, ldk - k0) : ldk, dv = a.dv;
     const int nkk = (dk + 15) / 16;          // 16-wide steps over the key columns
     const bool two = dk > 64;                // two 64-column halves of Q and K
 
@@ -538,7 +554,7 @@ __global__ void __launch_bounds__(dt::THREADS, 1)
             const bool halves = two && warp != V_WARP;
             const uint32_t bytes = warp == V_WARP ? V_BYTES : Q_BYTES;
             unsigned char *dst = sm + (warp == K_WARP ? OFF_K : warp == Q_WARP ? OFF_Q : OFF_V);
-            const int x0 = warp == V_WARP ? vt * RB : 0, head = warp == V_WARP ? h : hk;
+            const int x0 = warp == V_WARP ? vt * RB : k0, head = warp == V_WARP ? h : hk;
             prefetch_tensormap(tm);
             int n = 0;
             for (; n < n_chunks; ++n) {
@@ -546,7 +562,7 @@ __global__ void __launch_bounds__(dt::THREADS, 1)
                 if (n >= 2 && !hw(empty + st, (n - 2) >> 1)) break;
                 mbar_arrive_expect_tx(&bar[full + st], halves ? 2 * HALF : HALF);
                 tma_load_4d(dst + st * bytes, tm, &bar[full + st], x0, head, t, b);
-                if (halves) tma_load_4d(dst + st * bytes + HALF, tm, &bar[full + st], 64, head, t, b);
+                if (halves) tma_load_4d(dst + st * bytes + HALF, tm, &bar[full + st], x0 + 64, head, t, b);
             }
             // copies still in flight land before the block exits
             for (int c = max(n - 2, 0); c < n; ++c) mbar_wait_bounded(&bar[full + (c & 1)], (c >> 1) & 1, timeout_ns);
@@ -866,7 +882,17 @@ __global__ void __launch_bounds__(dt::THREADS, 1)
 #pragma unroll
                 for (int r = 0; r < 8; ++r) {
                     const float2 y = __fmul2_rn(u2, make_float2(d[2 * r], d[2 * r + 1]));
-                    w[q / 2 + r] = pack(y.x, y.y);
+                    if (PARTS)
+                        d[2 * r] = y.x, d[2 * r + 1] = y.y;
+                    else
+                        w[q / 2 + r] = pack(y.x, y.y);
+                }
+                if (PARTS && valid) {   // steps past the row's end are the sum's to clear
+                    float *dst = a.o_part + ((size_t(part) * a.B + b) * a.L + s0 + t) * HV + size_t(h) * dv + i0 + q;
+#pragma unroll
+                    for (int r = 0; r < 16; r += 4)
+                        if (i0 + q + r < dv)
+                            *reinterpret_cast<float4 *>(dst + r) = make_float4(d[r], d[r + 1], d[r + 2], d[r + 3]);
                 }
             }
             tc_fence_before();
@@ -875,6 +901,7 @@ __global__ void __launch_bounds__(dt::THREADS, 1)
                 arrive(&bar[K_DONE + st]);
                 arrive(&bar[M_FREE + mt]);
             }
+            if (PARTS) continue;
             if (cut) {
 #pragma unroll
                 for (int r = 0; r < RB / 2; ++r) w[r] = valid ? w[r] : 0u;
@@ -897,8 +924,9 @@ __global__ void __launch_bounds__(dt::THREADS, 1)
         float S[32];
 #pragma unroll
         for (int r = 0; r < 32; ++r)
-            S[r] = a.S0 != nullptr && seg == 0 && j < dk && i0 + r < dv ? a.S0[(size_t(bh) * dv + i0 + r) * dk + j]
-                                                                        : 0.0f;
+            S[r] = a.S0 != nullptr && seg == 0 && j < dk && i0 + r < dv
+                       ? a.S0[(size_t(bh) * dv + i0 + r) * ldk + k0 + j]
+                       : 0.0f;
         if (seg > 0) {
             grid_dependency_wait();
             long long acc = 0;
@@ -907,10 +935,10 @@ __global__ void __launch_bounds__(dt::THREADS, 1)
                 const float f = dec::exp2_fix(acc);
                 if (f == 0.0f) break;
                 const size_t at = size_t(bh) * (a.n_seg - 1) + e;
-                const float *src = a.seg_state + (at * dv + i0) * dk + j;
+                const float *src = a.seg_state + (at * dv + i0) * ldk + k0 + j;
 #pragma unroll
                 for (int r = 0; r < 32; ++r)
-                    if (j < dk && i0 + r < dv) S[r] = fmaf(f, src[size_t(r) * dk], S[r]);
+                    if (j < dk && i0 + r < dv) S[r] = fmaf(f, src[size_t(r) * ldk], S[r]);
                 acc = max(acc + a.seg_tot[at], -(1ll << 60));
             }
         }
@@ -961,17 +989,17 @@ __global__ void __launch_bounds__(dt::THREADS, 1)
             if (lane == 0) arrive(&bar[DS_FREE]);
         }
         asm volatile("bar.sync 1, 288;" ::: "memory");   // the scan warp's last factor
-        float *out = seg == a.n_seg - 1 && a.S_final != nullptr ? a.S_final + size_t(bh) * dv * dk : nullptr;
+        float *out = seg == a.n_seg - 1 && a.S_final != nullptr ? a.S_final + size_t(bh) * dv * ldk + k0 : nullptr;
         if (out != nullptr && j < dk) {
             const float f = *reinterpret_cast<const float *>(sm + OFF_END);
 #pragma unroll
             for (int r = 0; r < 32; ++r)
-                if (i0 + r < dv) out[size_t(i0 + r) * dk + j] = f * S[r];
+                if (i0 + r < dv) out[size_t(i0 + r) * ldk + j] = f * S[r];
         }
     }
     if (warp == SCAN_WARP) asm volatile("bar.sync 1, 288;" ::: "memory");
 
-    {   // whole chunks past the row's end
+    if (!PARTS) {   // whole chunks past the row's end
         const int g8 = min(RB, dv - vt * RB) / 8;
         const int64_t first = s0 + int64_t(n_chunks) * C;
         bf *ob = static_cast<bf *>(a.o) + size_t(h) * dv + vt * RB;
@@ -983,6 +1011,30 @@ __global__ void __launch_bounds__(dt::THREADS, 1)
     __syncthreads();
     tc_fence_after();
     if (warp == 0) tmem_dealloc(tmem, 512);
+}
+
+// o = the parts' sum, rounded once; steps past a row's length are 0.  A block
+// takes whole steps (all heads of one token).
+__global__ void __launch_bounds__(256) decay_parts_kernel(const DecayArgs a) {
+    using dt::pack;
+    const int64_t rows = a.B * a.L, HV = int64_t(a.H) * a.dv;
+    for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
+        const int b = int(row / a.L);
+        const bool valid = row - b * a.L < dec::row_len(a.lens, b, a.L);
+        uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.o) + row * HV);
+        for (int i = threadIdx.x; i < HV / 8; i += 256) {
+            float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f), y = x;
+            if (valid) {
+                for (int p = 0; p < a.parts; ++p) {
+                    const float4 *src = reinterpret_cast<const float4 *>(a.o_part + (p * rows + row) * HV) + 2 * i;
+                    const float4 u = __ldcs(src), v = __ldcs(src + 1);
+                    x = make_float4(x.x + u.x, x.y + u.y, x.z + u.z, x.w + u.w);
+                    y = make_float4(y.x + v.x, y.y + v.y, y.z + v.z, y.w + v.w);
+                }
+            }
+            dst[i] = make_uint4(pack(x.x, x.y), pack(x.z, x.w), pack(y.x, y.y), pack(y.z, y.w));
+        }
+    }
 }
 
 namespace {
@@ -1019,10 +1071,11 @@ bool dt_setup_once() {
     static std::once_flag once;
     static bool ok = false;
     std::call_once(once, [] {
-        ok = cudaFuncSetAttribute(decay_state_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(ds::SMEM)) ==
-                 cudaSuccess &&
-             cudaFuncSetAttribute(decay_tensor_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(dt::SMEM)) ==
-                 cudaSuccess;
+        auto room = [](auto kern, uint32_t bytes) {
+            return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes)) == cudaSuccess;
+        };
+        ok = room(decay_state_kernel<false>, ds::SMEM) && room(decay_state_kernel<true>, ds::SMEM) &&
+             room(decay_tensor_kernel<false>, dt::SMEM) && room(decay_tensor_kernel<true>, dt::SMEM);
     });
     return ok;
 }
@@ -1035,10 +1088,11 @@ int decay_tensor_launch(const DecayArgs &a, StatusRef st, cudaStream_t stream) {
         !dt_map(&mv, a.v, a.dv, a.H, a.L, a.B) || !dt_setup_once())
         return LR_ERR_CUDA;
     const int n_vt = (a.dv + dt::RB - 1) / dt::RB;
-    const int64_t per_seg = a.B * a.H * n_vt;
+    const bool parts = a.parts > 1;
+    const int64_t per_seg = a.B * a.H * n_vt * a.parts;
     if (per_seg * a.n_seg > INT32_MAX) return LR_ERR_UNSUPPORTED;
     if (a.n_seg > 1) {
-        decay_state_kernel<<<unsigned(per_seg * (a.n_seg - 1)), ds::THREADS, ds::SMEM, stream>>>(
+        (parts ? decay_state_kernel<true> : decay_state_kernel<false>)<<<unsigned(per_seg * (a.n_seg - 1)), ds::THREADS, ds::SMEM, stream>>>(
             mk, mv, a, n_vt, kDefaultTimeoutNs, st);
         if (cudaGetLastError() != cudaSuccess) return LR_ERR_CUDA;
     }
@@ -1053,9 +1107,14 @@ int decay_tensor_launch(const DecayArgs &a, StatusRef st, cudaStream_t stream) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = a.n_seg > 1 ? 1 : 0;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, decay_tensor_kernel, mq, mk, mv, a, n_vt,
-                                             uint64_t(kDefaultTimeoutNs), st);
-    return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? LR_OK : LR_ERR_CUDA;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, parts ? decay_tensor_kernel<true> : decay_tensor_kernel<false>, mq,
+                                             mk, mv, a, n_vt, uint64_t(kDefaultTimeoutNs), st);
+    if (e != cudaSuccess) return LR_ERR_CUDA;
+    if (parts) {
+        const int64_t rows = a.B * a.L;
+        decay_parts_kernel<<<unsigned(rows < (1 << 20) ? rows : 1 << 20), 256, 0, stream>>>(a);
+    }
+    return cudaGetLastError() == cudaSuccess ? LR_OK : LR_ERR_CUDA;
 }
 
 }  // namespace lr
