@@ -12,17 +12,24 @@ namespace {
 // B4 L4096: 4 748, 9 (chosen) 682, 14 690; B1 L32768: 9 1821, 19 (chosen) 1304,
 // 24 1490.
 // Calls in one segment whose narrow blocks (one state row a thread) are no more
-// than two per SM take those: fp32 L100 d128, H4 25 us against 31, H16 26
-// against 32, but H64 59 against 32; at dk 512 98 against 41.
+// than four per SM take those.  L100 d128 fp32: H4 21.5 us against 28.3, H16 22.3
+// against 28.1, H32 28.3 on either, H64 55 against 28; bf16 L32 H4 8.2 against 11.1.
+// dk 256: fp32 H8 23.6 against 29.3, but bf16 L32 24.2 against 12.1, and dk 512 fp32
+// 98 against 41.
 constexpr int64_t kGenMinSeg = 64;
 constexpr double kGenBlockCost = 40.0, kGenStateCost = 0.5, kGenLaunchCost = 50.0;
 constexpr int64_t kMaxSeg = 32;
-// Tensor-core kernel: the shortest sequence it takes (bf16 B8 H16 d128: L48 25
-// us on either kernel, L64 24 against 28 on the CUDA cores, L96 24 against 39),
-// and costs in units of a chunk's time: a chunk of the first launch, a block's
-// start, and one segment's state read by a later one.
-constexpr int64_t kTensorMinLen = 64;
-constexpr double kFirstCost = 0.6, kBlockCost = 3.0, kStateCost = 0.5;
+// Tensor-core kernel: the shortest sequence it takes (bf16, on it and on the CUDA
+// cores: B1 L48 H4 d128 10.7 and 11.7 us, L32 10.5 and 8.2; B4 L48 H32 d64 11.0 and
+// 14.4; B1 H8 dk256, L48 13.1 and 16.2, L32 13.2 and 12.1; the other way, B8 L48 H16
+// d128 21.9 and 19.1), and costs in units of a chunk's time: a chunk of the first
+// launch, a block's start, and one segment's state read by a later one.  Against
+// sweeps of the segment count over 11 shapes the plan's choice is the best or
+// within 3 %: B1 L32768 H16 d128 1 segment 582 us, 2 447, 4 (chosen) 238, 8 256;
+// B1 L16384 H8 dk64 6 84, 8 69, 9 (chosen) 66, 12 95; B4 L2048 H16 1 (chosen) 49.5,
+// 2 74.
+constexpr int64_t kTensorMinLen = 48;
+constexpr double kFirstCost = 0.6, kBlockCost = 3.0, kStateCost = 1.0;
 }  // namespace
 
 int decay_plan(int64_t B, int64_t L, int64_t H, int64_t Hk, int64_t dk, int64_t dv, lr_dtype io, DecayPlan *p) {
@@ -66,7 +73,7 @@ int decay_plan(int64_t B, int64_t L, int64_t H, int64_t Hk, int64_t dk, int64_t 
             if (t < best) best = t, n = s;
         }
         const int64_t nrows = decay_general_rows(dk, true);
-        p->narrow = n == 1 && dk <= 256 && B * H * ((dv + nrows - 1) / nrows) <= 2 * sms;
+        p->narrow = n == 1 && dk <= (io == LR_BF16 ? 128 : 256) && B * H * ((dv + nrows - 1) / nrows) <= 4 * sms;
     }
     p->seg_len = ((L + n - 1) / n + unit - 1) / unit * unit;
     p->n_seg = int((L + p->seg_len - 1) / p->seg_len);

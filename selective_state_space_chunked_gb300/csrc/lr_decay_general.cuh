@@ -473,7 +473,10 @@ int decay_general_launch(const DecayArgs &a, const DecayPlan &p, StatusRef st, c
     if (a.dk <= 32) return launch_general_dk<IO, 32>(a, p.narrow, st, stream);
     if (a.dk <= 64) return launch_general_dk<IO, 64>(a, p.narrow, st, stream);
     if (a.dk <= 128) return launch_general_dk<IO, 128>(a, p.narrow, st, stream);
-    if (a.dk <= 256) return launch_general_dk<IO, 256>(a, p.narrow, st, stream);
+    if (a.dk <= 256) {
+        if constexpr (sizeof(IO) == 4) return launch_general_dk<IO, 256>(a, p.narrow, st, stream);
+        return launch_general_cfg<IO, DecCfg<256, false>>(a, st, stream);
+    }
     return launch_general_cfg<IO, DecCfg<512, false>>(a, st, stream);
 }
 
