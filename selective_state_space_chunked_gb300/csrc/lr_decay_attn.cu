@@ -8,9 +8,9 @@ namespace {
 // block: a block's start, one segment's state read by a later one, and the
 // second launch.  Fitted to sweeps of the segment count over 13 shapes, of which
 // the plan's choice is within 5 % of the best on 12 and within 12 % on one; at
-// fp32 H16 d128, B2 L2048: 4 segments 271 us, 7 242, 9 (chosen) 211, 12 246;
-// B4 L4096: 4 748, 9 (chosen) 682, 14 690; B1 L32768: 9 1821, 19 (chosen) 1304,
-// 24 1490.
+// fp32 H16 d128 (of a kernel 5 % slower), B2 L2048: 4 segments 271 us, 7 242, 9
+// (chosen) 210, 12 246; B4 L4096: 4 748, 9 (chosen) 682, 14 690; B1 L32768: 9 1821,
+// 19 (chosen) 1304, 24 1490.
 // Calls in one segment whose narrow blocks (one state row a thread) are no more
 // than four per SM take those.  L100 d128 fp32: H4 21.5 us against 28.3, H16 22.3
 // against 28.1, H32 28.3 on either, H64 55 against 28; bf16 L32 H4 8.2 against 11.1.

@@ -22,14 +22,17 @@
 //
 // The work is 2 dk dv fp32 fused multiply-adds per token and head and, in the
 // n - 1 of n segments that the first launch runs, dk dv more.  Measured (fp32,
-// H16 d128): B2 L2048 211 us, 9 segments, 3.1 G fused multiply-adds, 38 % of
-// the fp32 pipes' rate; B4 L4096 682 us; B1 L32768 1304 us.  What is left of
-// the rate goes to the latency of a step (its loads from shared memory, the
-// 16-deep chains of dependent sums, the sums over lanes), which four warps per
-// scheduler do not cover.  Chunks of 16 steps in two buffers rather than 8 in
-// three: 239 -> 222 us; the steep chunk's multiplications in a loop of their
-// own: 222 -> 205-211.  Two steps' sums over lanes taken together (spills): 210
-// against 205.  Blocks of 256 threads: 211.
+// H16 d128): B2 L2048 200 us, 9 segments, 3.1 G fused multiply-adds, 41 % of
+// the fp32 pipes' rate; B4 L4096 664 us; B1 L32768 1266 us.  The packed fp32 pipe
+// is busy 53-55 % of the time the SMs are; the rest goes to the latency of a step
+// (its loads from shared memory, the chains of dependent sums, the sums over
+// lanes), which four warps per scheduler do not cover, and to the last blocks.
+//   chunks of 16 steps in two buffers against 8 in three: 222 us against 239
+//   the steep chunk's multiplications in a loop of their own: 205 against 222
+//   one barrier a chunk (outputs in two buffers): 204 against 205.5
+//   two steps unrolled: 200 against 204; four: 213
+//   two steps' sums over lanes taken together: 210 against 205 (spills)
+//   blocks of 256 threads: 211 against 205; three blocks per SM: 266 against 204
 #pragma once
 
 #include "lr_decay.cuh"
@@ -71,7 +74,7 @@ struct DecCfg {
     static constexpr size_t smem_bytes() {
         constexpr int TC = steps<IO>();
         return sizeof(IO) * size_t(kGB) * (2 * pitch<IO>(TC * DKP) + pitch<IO>(TC * RB)) +
-               sizeof(float) * (TC * RB + 8 * TC) + kGB * sizeof(uint64_t) + 128;
+               sizeof(float) * (2 * TC * RB + 8 * TC) + kGB * sizeof(uint64_t) + 128;
     }
 };
 
@@ -138,8 +141,8 @@ __global__ void __launch_bounds__(C::NT, C::BPS)
     IO *ks = reinterpret_cast<IO *>(smem);   // [GB][NH][TC][KB] (pitch KT)
     IO *qs = ks + kGB * KT;
     IO *vs = qs + kGB * KT;                  // [GB][TC][RB] (pitch VTP)
-    float *os = reinterpret_cast<float *>(vs + kGB * VTP);   // [TC][RB]
-    float *mu = os + VT;                     // [2][TC] readout factors scale A_t
+    float *os = reinterpret_cast<float *>(vs + kGB * VTP);   // [2][TC][RB]: one barrier a chunk
+    float *mu = os + 2 * VT;                     // [2][TC] readout factors scale A_t
     float *mw = mu + 2 * TC;                 // [2][TC] 1 / A_t (1 in a steep chunk)
     float *ma = mw + 2 * TC;                 // [2][TC] a_t of a steep chunk
     float *mm = ma + 2 * TC;                 // [2][2] factors before and after the chunk
@@ -298,14 +301,7 @@ __global__ void __launch_bounds__(C::NT, C::BPS)
         if (tid < 32 && more) gn = load_g(c + 1);
         if (c + kGB - 1 < nchunks) stage(c + kGB - 1, (c + kGB - 1) % kGB);
         const bool ok = !tma || mbar_wait_bounded(&full[buf], (c / kGB) & 1, timeout_ns);
-        if (__syncthreads_or(!ok)) {
-            if (tid == 0) {
-                status_report(sref, LR_ERR_TIMEOUT);
-                for (int c2 = c + 1; c2 < c + kGB && c2 < nchunks; ++c2)
-                    mbar_wait_bounded(&full[c2 % kGB], (c2 / kGB) & 1, timeout_ns);
-            }
-            break;
-        }
+        float *oc = os + (c & 1) * VT;
         const int nt = min(TC, nrun - c * TC);
         const float *u = mu + (c & 1) * TC, *w = mw + (c & 1) * TC, *wa = ma + (c & 1) * TC, *mf = mm + (c & 1) * 2;
         const float after = mf[1];
@@ -353,7 +349,7 @@ __global__ void __launch_bounds__(C::NT, C::BPS)
                     r[rr] = (acc[rr][0].x + acc[rr][0].y) + (acc[rr][1].x + acc[rr][1].y);
                 row_sums<RT, P>(r, p);
                 const float ut = u[t];
-                if (p < RT) os[t * RB + rg * RT + p] = ut * r[0];
+                if (p < RT) oc[t * RB + rg * RT + p] = ut * r[0];
             }
         };
         if (steep) {   // a loop of its own: the common one carries no trace of it
@@ -364,16 +360,25 @@ __global__ void __launch_bounds__(C::NT, C::BPS)
                 step(t);
             }
         } else {
-#pragma unroll 1
+#pragma unroll 2
             for (int t = 0; t < nt; ++t) step(t);
             if (after != 1.0f) mul(after);
         }
         if (tid < 32 && more) factors(c + 1, gn);   // its buffer was last read in chunk c - 1
-        __syncthreads();   // chunk c's buffer, every os entry, the next factors
+        // chunk c's buffer, its outputs, the next factors.  After a wait that ran
+        // out every thread leaves here, once the copies in flight have landed.
+        if (__syncthreads_or(!ok)) {
+            if (tid == 0) {
+                status_report(sref, LR_ERR_TIMEOUT);
+                for (int c2 = c + 1; c2 < c + kGB && c2 < nchunks; ++c2)
+                    mbar_wait_bounded(&full[c2 % kGB], (c2 / kGB) & 1, timeout_ns);
+            }
+            break;
+        }
         if (!STATE_ONLY) {
             for (int e = tid; e < TC * RB; e += NT) {
                 const int t = e / RB, r = e % RB;
-                if (t < nt && r < rbv) ob[size_t(c * TC + t) * HV + r] = Io<IO>::from_f(os[e]);
+                if (t < nt && r < rbv) ob[size_t(c * TC + t) * HV + r] = Io<IO>::from_f(oc[e]);
             }
         }
     }
