@@ -301,7 +301,8 @@ int lr_hgrn2_fwd(const void *q, const void *k, const void *v, const void *g,
  *          carried state is not: it is accumulated to fp32 accuracy.
  * Workspace: the call's device status and, when the library cuts the sequence
  *          into segments that run in parallel, one state per segment but the
- *          last of every (batch row, head).
+ *          last of every (batch row, head); with bf16 I/O and more than 128
+ *          keys, an fp32 copy of o per 128 of them.
  */
 size_t lr_decay_attn_workspace_size(int64_t B, int64_t L, int64_t H, int64_t Hk,
                                     int64_t dk, int64_t dv, lr_dtype io);

@@ -62,5 +62,25 @@ __device__ __forceinline__ int row_len(const int32_t *lens, int b, int64_t L) {
     return n < 0 ? 0 : (n > L ? static_cast<int>(L) : n);
 }
 
+// The batch row of a grid's slot: rows by falling length, so that the longest
+// start first and the last blocks to run are short.  The whole block calls it, with
+// kOrderRows ints of shared memory.
+__device__ __forceinline__ int row_at(const DecayArgs &a, int slot, int *scratch) {
+    if (!a.by_length) return slot;
+    const int n = int(a.B);
+    for (int i = threadIdx.x; i < n; i += blockDim.x) scratch[i] = row_len(a.lens, i, a.L);
+    __syncthreads();
+    int at = -1;
+    for (int i = threadIdx.x; i < n; i += blockDim.x) {
+        int before = 0;
+        for (int j = 0; j < n; ++j) before += scratch[j] > scratch[i] || (scratch[j] == scratch[i] && j < i);
+        if (before == slot) at = i;
+    }
+    __syncthreads();
+    if (at >= 0) scratch[0] = at;
+    __syncthreads();
+    return scratch[0];
+}
+
 }  // namespace dec
 }  // namespace lr

@@ -33,6 +33,7 @@ struct DecayArgs {
     // o_part [part][B][L][H][dv], are summed by a last launch.
     int parts;
     float *o_part;
+    bool by_length;          // blocks take the batch rows by falling length
 };
 
 struct DecayPlan {
@@ -41,6 +42,7 @@ struct DecayPlan {
     int64_t seg_len = 0;
     bool narrow = false;     // CUDA cores: few columns per thread (short sequences)
     int parts = 1;
+    int64_t blocks = 0;      // of the (second) launch
     size_t ws_bytes = 0;     // status, then seg_tot, seg_state, o_part
 };
 
@@ -52,6 +54,7 @@ template <typename IO>
 int decay_general_launch(const DecayArgs &a, const DecayPlan &p, StatusRef st, cudaStream_t stream);
 // tensor-core kernel: bf16 I/O, dk and dv multiples of 8
 int decay_tensor_launch(const DecayArgs &a, StatusRef st, cudaStream_t stream);
+constexpr int kOrderRows = 64;      // the largest batch that is taken by length
 constexpr int kDecayChunk = 128;    // its steps per chunk (segments are multiples of it)
 constexpr int kDecayRows = 64;      // its value rows per block
 constexpr int kPartKeys = 128;      // its key columns per block

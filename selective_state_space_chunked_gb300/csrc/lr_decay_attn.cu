@@ -77,6 +77,8 @@ int decay_plan(int64_t B, int64_t L, int64_t H, int64_t Hk, int64_t dk, int64_t 
     }
     p->seg_len = ((L + n - 1) / n + unit - 1) / unit * unit;
     p->n_seg = int((L + p->seg_len - 1) / p->seg_len);
+    const int64_t rows = p->path == 1 ? kDecayRows : decay_general_rows(dk, p->narrow);
+    p->blocks = B * H * ((dv + rows - 1) / rows) * p->parts * p->n_seg;
     const size_t segs = size_t(B) * H * (p->n_seg - 1);
     p->ws_bytes = kStatusBytes + (segs * sizeof(long long) + 15) / 16 * 16 + segs * dv * dk * sizeof(float);
     if (p->parts > 1) p->ws_bytes += size_t(p->parts) * B * L * H * dv * sizeof(float);
@@ -91,6 +93,14 @@ int decay_attn_launch(DecayArgs a, lr_dtype io, const DecayPlan &p, void *worksp
     a.seg_tot = reinterpret_cast<long long *>(ws);
     a.seg_state = reinterpret_cast<float *>(ws + (segs * sizeof(long long) + 15) / 16 * 16);
     a.parts = p.parts;
+    // Ragged rows by falling length where the blocks are more than the SMs (bf16,
+    // lengths spread evenly: B8 L1017 H32 d64 46.4 -> 40.7 us, B16 L2048 H16 d128
+    // 139 -> 127, B64 L1024 H4 d64 48.7 -> 41.9, but B32 L500 H8 d128 63 -> 65; fp32
+    // B16 L1024 H16 d128 408 -> 353).  With fewer there is nothing to gain (B3 L3000
+    // H4 36.4 -> 37.8).
+    int sms = 0;
+    if (device_sm_count(&sms) != LR_OK) return LR_ERR_CUDA;
+    a.by_length = a.lens != nullptr && a.B > 1 && a.B <= kOrderRows && p.blocks > sms;
     a.o_part = a.seg_state + segs * a.dv * a.dk;
     const StatusRef st = call_status(workspace);
     if (p.path == 1) return decay_tensor_launch(a, st, stream);

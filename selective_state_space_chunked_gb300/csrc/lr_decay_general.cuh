@@ -153,8 +153,11 @@ __global__ void __launch_bounds__(C::NT, C::BPS)
     int x = blockIdx.x;
     const int rb = x % nrb;
     x /= nrb;
-    const int seg = x % nseg, bh = x / nseg;
-    const int b = bh / a.H, h = bh - b * a.H, hk = h / (a.H / a.Hk);
+    const int seg = x % nseg;
+    x /= nseg;
+    const int h = x % a.H, hk = h / (a.H / a.Hk);
+    static_assert(2 * VT >= kOrderRows, "os holds the rows' order before it holds outputs");
+    const int b = dec::row_at(a, x / a.H, reinterpret_cast<int *>(os)), bh = b * a.H + h;
     if (tid == 0 && blockIdx.x == 0) status_begin(sref);
     const int p = tid % P, rg = tid / P;
     const int row0 = rb * RB, dk = a.dk, dv = a.dv;

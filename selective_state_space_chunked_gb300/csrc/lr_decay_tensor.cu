@@ -241,8 +241,10 @@ __global__ void __launch_bounds__(ds::THREADS, 1)
     x /= n_vt;
     const int part = PARTS ? x % a.parts : 0;
     if (PARTS) x /= a.parts;
-    const int seg = x % nseg, bh = x / nseg;
-    const int b = bh / a.H, h = bh - b * a.H, hk = h / (a.H / a.Hk);
+    const int seg = x % nseg;
+    x /= nseg;
+    const int h = x % a.H, hk = h / (a.H / a.Hk);
+    const int b = dec::row_at(a, x / a.H, reinterpret_cast<int *>(sm + OFF_WT)), bh = b * a.H + h;
     const int len = dec::row_len(a.lens, b, a.L);
     const int s0 = int(int64_t(seg) * a.seg_len);
     const int nrun = max(0, min(len, int(min(a.L, int64_t(s0) + a.seg_len))) - s0);
@@ -501,8 +503,10 @@ __global__ void __launch_bounds__(dt::THREADS, 1)
     x /= n_vt;
     const int part = PARTS ? x % a.parts : 0;
     if (PARTS) x /= a.parts;
-    const int seg = x % nseg, bh = x / nseg;
-    const int b = bh / a.H, h = bh - b * a.H, hk = h / (a.H / a.Hk);
+    const int seg = x % nseg;
+    x /= nseg;
+    const int h = x % a.H, hk = h / (a.H / a.Hk);
+    const int b = dec::row_at(a, x / a.H, reinterpret_cast<int *>(sm + OFF_WT)), bh = b * a.H + h;
     const int len = dec::row_len(a.lens, b, a.L);
     const int s0 = int(int64_t(seg) * a.seg_len);
     const int send = int(min(a.L, int64_t(s0) + a.seg_len));
