@@ -6,19 +6,19 @@ namespace lr {
 namespace {
 // CUDA-core kernel: the shortest segment, and costs in units of a step of a
 // block: a block's start, one segment's state read by a later one, and the
-// second launch.  Fitted to sweeps of the segment count over 13 shapes, of which
-// the plan's choice is within 5 % of the best on 12 and within 12 % on one; at
-// fp32 H16 d128 (of a kernel 5 % slower), B2 L2048: 4 segments 271 us, 7 242, 9
-// (chosen) 210, 12 246; B4 L4096: 4 748, 9 (chosen) 682, 14 690; B1 L32768: 9 1821,
-// 19 (chosen) 1304, 24 1490.
+// second launch.  Chosen on sweeps of the segment count over 20 shapes.  fp32
+// H16 d128 (of a kernel 5 % slower), B2 L2048: 4 segments 271 us, 7 242, 9 (chosen)
+// 210, 12 246; B4 L4096: 1 999, 4 748, 9 (chosen) 682, 14 690; B1 L32768: 9 1821,
+// 19 (chosen) 1304, 24 1490; few heads: B1 L8192 H1 d128 32 114, 64 (chosen) 72, 96
+// 88; B1 L4096 H2 d64 32 57, 45 (chosen) 47, 64 68.
 // Calls in one segment whose narrow blocks (one state row a thread) are no more
 // than four per SM take those.  L100 d128 fp32: H4 21.5 us against 28.3, H16 22.3
 // against 28.1, H32 28.3 on either, H64 55 against 28; bf16 L32 H4 8.2 against 11.1.
 // dk 256: fp32 H8 23.6 against 29.3, but bf16 L32 24.2 against 12.1, and dk 512 fp32
 // 98 against 41.
 constexpr int64_t kGenMinSeg = 64;
-constexpr double kGenBlockCost = 40.0, kGenStateCost = 0.5, kGenLaunchCost = 50.0;
-constexpr int64_t kMaxSeg = 32;
+constexpr double kGenBlockCost = 40.0, kGenStateCost = 3.0, kGenLaunchCost = 50.0;
+constexpr int64_t kGenMaxSeg = 96;
 // Tensor-core kernel: the shortest sequence it takes (bf16, on it and on the CUDA
 // cores: B1 L48 H4 d128 10.7 and 11.7 us, L32 10.5 and 8.2; B4 L48 H32 d64 11.0 and
 // 14.4; B1 H8 dk256, L48 13.1 and 16.2, L32 13.2 and 12.1; the other way, B8 L48 H16
@@ -28,6 +28,7 @@ constexpr int64_t kMaxSeg = 32;
 // within 3 %: B1 L32768 H16 d128 1 segment 582 us, 2 447, 4 (chosen) 238, 8 256;
 // B1 L16384 H8 dk64 6 84, 8 69, 9 (chosen) 66, 12 95; B4 L2048 H16 1 (chosen) 49.5,
 // 2 74.
+constexpr int64_t kMaxSeg = 32;
 constexpr int64_t kTensorMinLen = 48;
 constexpr double kFirstCost = 0.6, kBlockCost = 3.0, kStateCost = 1.0;
 }  // namespace
@@ -57,16 +58,18 @@ int decay_plan(int64_t B, int64_t L, int64_t H, int64_t Hk, int64_t dk, int64_t 
         // Blocks of an SM share its fp32 pipes.  The SM with the most of them
         // takes, per step and in units of a block's share of a full SM, as long
         // as its slots for each full round (a partly filled last round of
-        // dependent launches packs three blocks as four) and 1.5 for a block
-        // that has the SM to itself.
+        // dependent launches packs three blocks as four), 2 where no SM has a
+        // second block (a step then takes 0.243 us against 0.49 for four blocks),
+        // and 1.5 for a block left over by the rounds, whose start overlaps them.
         const int64_t rows = decay_general_rows(dk, false), threads = dk <= 64 ? 64 : 128, slots = dk <= 128 ? 4 : 3;
         const int64_t blocks = B * H * ((dv + rows - 1) / rows);
         auto load = [&](int64_t b) {
             const int64_t most = (b * threads + 128 * sms - 1) / (128 * sms), rest = most % slots;
+            if (most == 1) return 2.0;
             return double(most - rest) + (rest == 0 ? 0.0 : rest == 1 ? 1.5 : rest == 2 ? 2.75 : double(slots));
         };
         double best = load(blocks) * (double(L) + kGenBlockCost);
-        for (int64_t s = 2; s <= kMaxSeg && s * kGenMinSeg <= L; ++s) {
+        for (int64_t s = 2; s <= kGenMaxSeg && s * kGenMinSeg <= L; ++s) {
             const double per = double((L + s - 1) / s);
             const double t = load(blocks * s) * (per + kGenBlockCost + kGenStateCost * double(s)) +
                              load(blocks * (s - 1)) * (0.5 * per + kGenBlockCost) + kGenLaunchCost;

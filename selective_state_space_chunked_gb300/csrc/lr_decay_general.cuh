@@ -46,13 +46,15 @@ constexpr int kGB = 2;    // staging buffers
 // per scheduler; 4 x 32 and 8 x 16 read less from shared memory per element but
 // leave 1.5, and the packed fp32 pipe was then busy 37 % of the time (278 against
 // 242 us at B2 L2048 H16 d128 fp32).  From 256 key columns three blocks per SM,
-// without spills, take 115 us against 137 (fp32 B3 L1111 H6 dk192 dv96); up to
+// without spills, take 115 us against 137 (fp32 B3 L1111 H6 dk192 dv96).  Up to
 // 64 key columns chunks of 32 steps take 104 us against 118 (fp32 B1 L8192 H4
-// d64).
+// d64), and 4 x 8 elements, which make twice the blocks, 73 against 91 there, 289
+// against 310 at B4 L4096 H16 d64, 98 against 87 at B8 L1000 H8 d64; at 128 columns
+// 4 x 8 take 410 us and 8 x 8 212 against 200 (B2 L2048 H16 d128).
 template <int DKP_, bool NARROW>
 struct DecCfg {
     static constexpr int DKP = DKP_;
-    static constexpr int CPT = DKP == 32 ? 8 : 16;
+    static constexpr int CPT = DKP <= 64 ? 8 : 16;
     static constexpr int RT = NARROW ? 1 : 4;
     static constexpr int NT = NARROW || DKP <= 64 ? 64 : 128;   // threads per block
     static constexpr int P = DKP / CPT;
