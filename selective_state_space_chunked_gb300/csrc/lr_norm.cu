@@ -8,10 +8,10 @@
 // mean, then the centred squares (no cancellation), then the output.
 //
 // Measured, inputs larger than L2 (share of the copy bandwidth): bf16 16384 x
-// 2048, G 16, gate 34.4 us (86 %); fp32 61 us (97 %); bf16 8192 x 4096, G 32 26.5
-// us (75 %); fp32 3001 x 1920, G 24 8.8 us (77 %); bf16 8192 x 4096, G 2, gate
+// 2048, G 16, gate 33.0 us (90 %); fp32 62 us (95 %); bf16 8192 x 4096, G 32 24.5
+// us (81 %); fp32 3001 x 1920, G 24 8.45 us (80 %); bf16 8192 x 4096, G 2, gate
 // 35.5 us (84 %; element by element 82 us).  Sums and the affine step in packed
-// fp32 pairs: the first 38.4 -> 36.7 us.
+// fp32 pairs: the first 38.4 -> 36.7 us at the time.
 //
 //   lanes   groups of up to 128 vectors (16 bytes; 8 for a bf16 group of an odd
 //           number of those): TL lanes of a warp hold a group, up to four vectors
@@ -312,11 +312,18 @@ int launch_lanes(const NormArgs &a, int sms, cudaStream_t s) {
     // are few.  bf16: 16384 x 2048, G 32, gate (one vector a lane) 1 row 41.5 us, 2
     // rows 34.7, 4 rows 36.1; without gate 2 rows 30.0, 4 rows 27.3; 8192 x 4096,
     // G 32 (two vectors) 1 row 28.8 us, 2 rows 26.5, 4 rows 32.9.  Three and four
-    // vectors: 4096 x 3200, G 40, gate 1 row 18.3 us, 2 rows 26.7.  Blocks per SM,
-    // 16384 x 2048, G 16, gate at one vector a lane: 4, 5, 6, 7, 8 of them 46, 40.4,
-    // 36.7, 39.7, 41 us.
+    // vectors: 4096 x 3200, G 40, gate 1 row 18.3 us, 2 rows 26.7.
     constexpr int R = V == 1 ? (GATE ? 2 : 4) : V == 2 ? 2 : 1;
-    const int64_t full = int64_t(sms) * 6;
+    // The blocks that fit, which then walk the rows, against six per SM: 16384 x
+    // 2048 bf16, gate, G 32 31.3 us against 34.6, G 16 33.0 against 34.4; 8192 x 4096
+    // 24.5 against 26.5; 591 x 8192 fp32, gate 9.8 against 11.3.  Groups of three
+    // vectors a lane take twice as many: 3001 x 1920 fp32 8.45 us against 9.1.
+    static const int fit = [] {
+        int n = 0;
+        return cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, group_norm_lanes_kernel<X, TL, V, R, GATE>, 256, 0) ==
+                           cudaSuccess && n > 0 ? n : 1;
+    }();
+    const int64_t full = int64_t(sms) * fit * (V == 3 ? 2 : 1);
     const bool deep = row_blocks * gy >= full * R;
     int64_t gx = deep ? (full + gy - 1) / gy : row_blocks;
     if (gx > row_blocks) gx = row_blocks;
