@@ -61,6 +61,23 @@ constexpr int kPartKeys = 128;      // its key columns per block
 // rows of the state per block of the general kernel
 int decay_general_rows(int64_t dk, bool narrow);
 
+// A launch that may start while the kernel before it on the stream drains; the
+// kernel waits for that one's results itself (grid_dependency_wait).
+template <typename... P, typename... A>
+int launch_early(void (*kern)(P...), dim3 grid, int threads, cudaStream_t stream, A... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, P(args)...) == cudaSuccess && cudaGetLastError() == cudaSuccess ? LR_OK
+                                                                                                       : LR_ERR_CUDA;
+}
+
 int decay_step_launch(const void *q, const void *k, const void *v, const float *a_log, const void *g,
                       float scale, const float *S_in, float *S_out, void *o, int64_t B, int64_t H, int64_t Hk,
                       int64_t dk, int64_t dv, int io_bf16, cudaStream_t stream);
