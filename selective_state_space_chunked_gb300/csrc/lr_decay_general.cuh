@@ -151,6 +151,9 @@ __global__ void __launch_bounds__(C::NT, C::BPS)
     uint64_t *full = reinterpret_cast<uint64_t *>(mm + 2 * TC);
 
     const int tid = threadIdx.x, lane = tid & 31;
+    // a call of one launch starts while the kernel before it drains
+    if (!STATE_ONLY && a.n_seg == 1) grid_dependency_wait();
+    if (!STATE_ONLY) launch_dependents();
     const int nseg = STATE_ONLY ? a.n_seg - 1 : a.n_seg;
     int x = blockIdx.x;
     const int rb = x % nrb;
@@ -455,7 +458,8 @@ int launch_general_cfg(const DecayArgs &a, StatusRef st, cudaStream_t stream) {
                                                                         st);
         if (cudaGetLastError() != cudaSuccess) return LR_ERR_CUDA;
     }
-    // dependent launch: segment 0 needs nothing of the first launch
+    // dependent launch: of the kernel before the call, or of the first launch, of
+    // which segment 0 needs nothing
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(unsigned(per_seg * a.n_seg));
     cfg.blockDim = dim3(C::NT);
@@ -465,7 +469,7 @@ int launch_general_cfg(const DecayArgs &a, StatusRef st, cudaStream_t stream) {
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = a.n_seg > 1 ? 1 : 0;
+    cfg.numAttrs = 1;
     const cudaError_t e = cudaLaunchKernelEx(&cfg, main, mq, mk, mv, a, nrb, tma, uint64_t(kDefaultTimeoutNs), st);
     return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? LR_OK : LR_ERR_CUDA;
 }

@@ -492,12 +492,16 @@ __global__ void __launch_bounds__(dt::THREADS, 1)
     using bf = __nv_bfloat16;
     extern __shared__ __align__(1024) unsigned char sm[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int nseg = a.n_seg;
+    // a call of one launch starts while the kernel before it drains; with segments
+    // the first launch has come after that kernel, and only later segments wait for it
+    if (nseg == 1) grid_dependency_wait();
+    launch_dependents();
     if (tid == 0 && blockIdx.x == 0) status_begin(sref);
     if ((smem_u32(sm) & 1023u) != 0) {   // swizzled tiles need a 1024-byte aligned base
         if (tid == 0) status_report(sref, LR_ERR_CUDA);
         return;
     }
-    const int nseg = a.n_seg;
     int x = blockIdx.x;
     const int vt = x % n_vt;
     x /= n_vt;
@@ -1100,7 +1104,8 @@ int decay_tensor_launch(const DecayArgs &a, StatusRef st, cudaStream_t stream) {
             mk, mv, a, n_vt, kDefaultTimeoutNs, st);
         if (cudaGetLastError() != cudaSuccess) return LR_ERR_CUDA;
     }
-    // dependent launch: segment 0 needs nothing of the first launch
+    // dependent launch: of the kernel before the call, or of the first launch, of
+    // which segment 0 needs nothing
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(unsigned(per_seg * a.n_seg));
     cfg.blockDim = dim3(dt::THREADS);
@@ -1110,7 +1115,7 @@ int decay_tensor_launch(const DecayArgs &a, StatusRef st, cudaStream_t stream) {
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = a.n_seg > 1 ? 1 : 0;
+    cfg.numAttrs = 1;
     const cudaError_t e = cudaLaunchKernelEx(&cfg, parts ? decay_tensor_kernel<true> : decay_tensor_kernel<false>, mq,
                                              mk, mv, a, n_vt, uint64_t(kDefaultTimeoutNs), st);
     if (e != cudaSuccess) return LR_ERR_CUDA;
