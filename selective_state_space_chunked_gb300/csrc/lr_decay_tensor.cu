@@ -52,13 +52,24 @@
 // another and o_t = sum over j of S_t[:, j] q_t[j], so each 128 of them run as a
 // recurrence of their own, in blocks of their own, and a last launch adds their
 // fp32 outputs and rounds the sum.  The scores' products with V are repeated by
-// every part; at B2 L1500 H8 dk256 dv128 52 us against 178 on the CUDA cores, B4
+// every part; at B2 L1500 H8 dk256 dv128 48 us against 178 on the CUDA cores, B4
 // L4096 H16 dk256 dv128 265 against 1528, B4 L1024 H8 dk512 dv128 80 against 387,
 // B1 L64 H4 dk192 dv64 17 against 56.
 // TMEM: P 2 x 128 columns (PD inside), O 64, dS 3 x 64: all 512.
 // Loops over columns stay rolled and waits share one slow path: with every
 // role's code unrolled the warps waited for instruction fetches more than for
-// anything else.
+// anything else (95 us against 90 at B4 L4096 H16 d128 for the last part of it).
+//
+// Measured (d128, H16): B4 L4096 86 us, 273 MB and 17 GFLOP, 47 % of the copy
+// bandwidth and 10 % of the tensor peak; B1 L32768 236 us in four segments; B1 L77
+// 9.9.  d64: B8 L1017 H32, ragged, 38.5.  No pipe is near its limit (tensor 36 %
+// busy, issue 45 %, DRAM 37 %): a chunk takes about 2.7 us, the chain of its
+// hand-overs, with one block per SM, which its operands (224 KB) and TMEM fill.
+// 128-step chunks rather than 64 halve the hand-overs; 64 value rows rather than
+// 128 make twice the blocks.  Measured against 91 us and not taken: P and dS issued
+// by one warp 98, weights by eight warps or by half chunks 98-100, one warp polling
+// for all products 192, two state terms instead of three 89 (with the state's error
+// a hundred times larger), sleeping waits 91.
 #include <cudaTypedefs.h>
 
 #include <mutex>
@@ -190,6 +201,9 @@ __device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, Ctl *ctl) 
 //   dS = K^T diag(w) V
 // runs through all chunks in one accumulator, with nothing read back between
 // them.  The total decay comes first, from a sum over the segment's gates.
+// Measured: B1 L16384 H16 d128, three of four segments, 46 us, 29 % of the DRAM
+// rate and 30 % of the tensor pipe, bound by the weights' chain; the second
+// launch's code, used for both before, took 280 us against 254 at B1 L32768 in all.
 // Roles: TMA (K, V three chunks deep), scan (4 warps, a step per lane: weights
 // of the next chunks), weight (8 warps: the three terms of w_s v_s, half chunks
 // in a ring of three), MMA (M=128 N=192).
