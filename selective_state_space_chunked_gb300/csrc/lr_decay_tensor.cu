@@ -1036,9 +1036,13 @@ __global__ void __launch_bounds__(dt::THREADS, 1)
 }
 
 // o = the parts' sum, rounded once; steps past a row's length are 0.  A block
-// takes whole steps (all heads of one token).
+// takes whole steps (all heads of one token).  Launched while the parts drain: B1
+// L100 H8 dk256 13.0 us against 15.3, B2 L1500 H8 dk256 49.4 against 51.5.  It lets
+// nothing start before its own end (B4 L4096 H16 dk256 277 us against 270: the next
+// call's blocks would take the SMs that it still needs).
 __global__ void __launch_bounds__(256) decay_parts_kernel(const DecayArgs a) {
     using dt::pack;
+    grid_dependency_wait();
     const int64_t rows = a.B * a.L, HV = int64_t(a.H) * a.dv;
     for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
         const int b = int(row / a.L);
@@ -1135,7 +1139,7 @@ int decay_tensor_launch(const DecayArgs &a, StatusRef st, cudaStream_t stream) {
     if (e != cudaSuccess) return LR_ERR_CUDA;
     if (parts) {
         const int64_t rows = a.B * a.L;
-        decay_parts_kernel<<<unsigned(rows < (1 << 20) ? rows : 1 << 20), 256, 0, stream>>>(a);
+        return launch_early(decay_parts_kernel, dim3(unsigned(rows < (1 << 20) ? rows : 1 << 20)), 256, stream, a);
     }
     return cudaGetLastError() == cudaSuccess ? LR_OK : LR_ERR_CUDA;
 }
