@@ -62,7 +62,7 @@
 //
 // Measured (d128, H16): B4 L4096 86 us, 273 MB and 17 GFLOP, 47 % of the copy
 // bandwidth and 10 % of the tensor peak; B1 L32768 236 us in four segments; B1 L77
-// 9.9.  d64: B8 L1017 H32, ragged, 38.5.  No pipe is near its limit (tensor 36 %
+// 9.9.  d64: B8 L1017 H32, ragged, 38-45.  No pipe is near its limit (tensor 36 %
 // busy, issue 45 %, DRAM 37 %): a chunk takes about 2.7 us, the chain of its
 // hand-overs, with one block per SM, which its operands (224 KB) and TMEM fill.
 // 128-step chunks rather than 64 halve the hand-overs; 64 value rows rather than

@@ -14,6 +14,8 @@ EXAMPLE = os.path.join(os.path.dirname(os.path.abspath(__file__)), "..", "exampl
 
 
 def _example():
+    from selective_state_space_chunked_gb300 import build
+    build.build()
     spec = importlib.util.spec_from_file_location("decay_attn_layer", EXAMPLE)
     mod = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(mod)

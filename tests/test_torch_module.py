@@ -4,11 +4,18 @@ import pytest
 
 torch = pytest.importorskip("torch")
 
-from selective_state_space_chunked_gb300 import binding as lr  # noqa: E402
 from selective_state_space_chunked_gb300 import workloads as wl  # noqa: E402
 
 
-def test_host_tensors_and_other_objects_are_declined():
+@pytest.fixture(scope="module")
+def lr():
+    from selective_state_space_chunked_gb300 import build
+    build.build()
+    from selective_state_space_chunked_gb300 import binding
+    return binding
+
+
+def test_host_tensors_and_other_objects_are_declined(lr):
     q, v, S = torch.zeros(2, 8), torch.zeros(2, 8), torch.zeros(2, 2, 4, 4)
     assert lr._lrtorch.decay_attn_step(q, q, v, 2, None, None, None, S, None, 1.0) is None
     assert lr._lrtorch.decay_attn(q[None], q[None], v[None], 2, None, None, None, None, None, 1.0) is None
@@ -28,7 +35,7 @@ def _step_args(io="bf16"):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("io", ["bf16", "f32"])
-def test_the_short_path_gives_the_helpers_results(io, monkeypatch):
+def test_the_short_path_gives_the_helpers_results(lr, io, monkeypatch):
     q, k, v, a, g, S = _step_args(io)
     x = torch.randn(7, 64, device="cuda").to(q.dtype)
     p = wl.decay_attn_inputs(2, 90, 4, 32, 16, 6, io=io, Hk=2, with_S0=True)
@@ -57,7 +64,7 @@ def test_the_short_path_gives_the_helpers_results(io, monkeypatch):
 
 
 @pytest.mark.gpu
-def test_what_it_takes_and_what_it_declines():
+def test_what_it_takes_and_what_it_declines(lr):
     q, k, v, a, g, S = _step_args()
     take = lambda *args: lr._lrtorch.decay_attn_step(*args)  # noqa: E731
     good = (q, k, v, 4, 2, a, g, S, None, 1.0)
@@ -78,7 +85,7 @@ def test_what_it_takes_and_what_it_declines():
 
 
 @pytest.mark.gpu
-def test_the_call_runs_on_the_current_stream():
+def test_the_call_runs_on_the_current_stream(lr):
     q, k, v, a, g, S = _step_args("f32")
     want, _ = lr.decay_attn_step(q, k, v, 4, Hk=2, a_log=a, g=g, S=S)
     torch.cuda.synchronize()
