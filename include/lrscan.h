@@ -289,6 +289,14 @@ int lr_hgrn2_fwd(const void *q, const void *k, const void *v, const void *g,
  * meaningful.  Decay products are formed from sums of log decays kept in 64-bit
  * fixed point, so no range of decays needs a special setting.
  *
+ * An infinity or a NaN in q reaches its own step's outputs; one in k, v or S0
+ * reaches the outputs and the state from its step on, as the recurrence says (an
+ * output that is infinite by it may be NaN), and no earlier step or other row.  No
+ * decay ends it, a reset included.  Tensor-core blocks that meet one run a step at
+ * a time (about 1 us each).  The state is held divided by its decay since the last
+ * rescale: on the CUDA cores (fp32 I/O; bf16 below 48 steps, or with dk or dv no
+ * multiple of 8) values of it past 2^79 may overflow.
+ *
  * Layouts: q, k: (B, L, Hk*dk); v, o: (B, L, H*dv); g: (B, L, H), all in `io`;
  *          a_log: (H) fp32; lens: (B) int32; S0, S_final: (B, H, dv, dk) fp32
  *          (row = value channel).  Optional: a_log, g, lens, S0, S_final.

@@ -62,6 +62,14 @@ __device__ __forceinline__ int row_len(const int32_t *lens, int b, int64_t L) {
     return n < 0 ? 0 : (n > L ? static_cast<int>(L) : n);
 }
 
+// Whether one of segments 0 .. last of (batch row, head) bh left a tile that
+// is not finite.  A whole warp calls it.
+__device__ __forceinline__ bool any_bad(const DecayArgs &a, int64_t bh, int last, int tile) {
+    int bad = 0;
+    for (int s = threadIdx.x & 31; s <= last; s += 32) bad |= a.seg_bad[(bh * (a.n_seg - 1) + s) * a.seg_tiles + tile];
+    return __any_sync(0xffffffffu, bad);
+}
+
 // The batch row of a grid's slot: rows by falling length, so that the longest
 // start first and the last blocks to run are short.  The whole block calls it, with
 // kOrderRows ints of shared memory.

@@ -23,11 +23,14 @@ struct DecayArgs {
     // that each range but the last builds from its own steps (range 0 from
     // S0) in seg_state [(b H + h)(n_seg - 1) + s][dv][dk] and its log2 decay,
     // in units of 2^-32, in seg_tot; the second launch starts every range
-    // from the decayed sum of the ranges before it.
-    int n_seg;
+    // from the decayed sum of the ranges before it.  seg_bad
+    // [((b H + h)(n_seg - 1) + s) seg_tiles + tile]: whether a block's tile of such a state
+    // holds an infinity or a NaN, which no decay ends.
+    int n_seg, seg_tiles;
     int64_t seg_len;
     float *seg_state;
     long long *seg_tot;
+    int *seg_bad;
     // Tensor cores, dk > 128: the key columns in parts of kPartKeys, each a
     // recurrence of its own with the same decays; their outputs, fp32, in
     // o_part [part][B][L][H][dv], are summed by a last launch.
@@ -42,8 +45,9 @@ struct DecayPlan {
     int64_t seg_len = 0;
     bool narrow = false;     // CUDA cores: few columns per thread (short sequences)
     int parts = 1;
+    int tiles = 1;           // blocks of one (batch row, head, segment)
     int64_t blocks = 0;      // of the (second) launch
-    size_t ws_bytes = 0;     // status, then seg_tot, seg_state, o_part
+    size_t ws_bytes = 0;     // status, then seg_tot, seg_bad, seg_state, o_part
 };
 
 int decay_plan(int64_t B, int64_t L, int64_t H, int64_t Hk, int64_t dk, int64_t dv, lr_dtype io, DecayPlan *p);

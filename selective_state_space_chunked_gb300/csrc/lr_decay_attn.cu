@@ -33,6 +33,11 @@ constexpr int64_t kTensorMinLen = 48;
 constexpr double kFirstCost = 0.6, kBlockCost = 3.0, kStateCost = 1.0;
 }  // namespace
 
+namespace {
+size_t tot_bytes(size_t segs) { return (segs * sizeof(long long) + 15) / 16 * 16; }
+size_t bad_bytes(size_t segs, const DecayPlan &p) { return (segs * p.tiles * sizeof(int) + 15) / 16 * 16; }
+}  // namespace
+
 int decay_plan(int64_t B, int64_t L, int64_t H, int64_t Hk, int64_t dk, int64_t dv, lr_dtype io, DecayPlan *p) {
     (void)Hk;
     int sms = 0;
@@ -81,9 +86,10 @@ int decay_plan(int64_t B, int64_t L, int64_t H, int64_t Hk, int64_t dk, int64_t 
     p->seg_len = ((L + n - 1) / n + unit - 1) / unit * unit;
     p->n_seg = int((L + p->seg_len - 1) / p->seg_len);
     const int64_t rows = p->path == 1 ? kDecayRows : decay_general_rows(dk, p->narrow);
-    p->blocks = B * H * ((dv + rows - 1) / rows) * p->parts * p->n_seg;
+    p->tiles = int((dv + rows - 1) / rows) * p->parts;
+    p->blocks = B * H * p->tiles * p->n_seg;
     const size_t segs = size_t(B) * H * (p->n_seg - 1);
-    p->ws_bytes = kStatusBytes + (segs * sizeof(long long) + 15) / 16 * 16 + segs * dv * dk * sizeof(float);
+    p->ws_bytes = kStatusBytes + tot_bytes(segs) + bad_bytes(segs, *p) + segs * dv * dk * sizeof(float);
     if (p->parts > 1) p->ws_bytes += size_t(p->parts) * B * L * H * dv * sizeof(float);
     return LR_OK;
 }
@@ -94,7 +100,9 @@ int decay_attn_launch(DecayArgs a, lr_dtype io, const DecayPlan &p, void *worksp
     a.n_seg = p.n_seg;
     a.seg_len = p.seg_len;
     a.seg_tot = reinterpret_cast<long long *>(ws);
-    a.seg_state = reinterpret_cast<float *>(ws + (segs * sizeof(long long) + 15) / 16 * 16);
+    a.seg_bad = reinterpret_cast<int *>(ws + tot_bytes(segs));
+    a.seg_state = reinterpret_cast<float *>(ws + tot_bytes(segs) + bad_bytes(segs, p));
+    a.seg_tiles = p.tiles;
     a.parts = p.parts;
     // Ragged rows by falling length where the blocks are more than the SMs (bf16,
     // lengths spread evenly: B8 L1017 H32 d64 46.4 -> 40.7 us, B16 L2048 H16 d128

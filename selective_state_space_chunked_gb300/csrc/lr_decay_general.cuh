@@ -290,7 +290,8 @@ __global__ void __launch_bounds__(C::NT, C::BPS)
         long long acc = 0;
         for (int s = seg - 1; s >= 0; --s) {
             const float f = dec::exp2_fix(acc);
-            if (f == 0.0f) break;
+            // nothing is left of the ranges before, unless it is not finite
+            if (f == 0.0f && !dec::any_bad(a, bh, s, rb)) break;
             const size_t at = size_t(bh) * (a.n_seg - 1) + s;
             add_state(a.seg_state + at * dv * dk, f);
             acc = max(acc + a.seg_tot[at], -(1ll << 60));
@@ -413,6 +414,16 @@ __global__ void __launch_bounds__(C::NT, C::BPS)
         __syncthreads();
         const float f = mm[0];
         const bool v4 = rows16(dst0);
+        if (STATE_ONLY) {
+            float2 zero = make_float2(0.0f, 0.0f);   // 0 times what is written
+#pragma unroll
+            for (int rr = 0; rr < RT; ++rr)
+#pragma unroll
+                for (int m = 0; m < CPT / 2; ++m)
+                    zero = __ffma2_rn(__fmul2_rn(S[rr][m], make_float2(f, f)), make_float2(0.0f, 0.0f), zero);
+            const int bad = __syncthreads_or(!(zero.x + zero.y == 0.0f));
+            if (tid == 0) a.seg_bad[(size_t(bh) * (a.n_seg - 1) + seg) * a.seg_tiles + rb] = bad;
+        }
 #pragma unroll
         for (int rr = 0; rr < RT; ++rr) {
             const int i = row0 + rg * RT + rr;

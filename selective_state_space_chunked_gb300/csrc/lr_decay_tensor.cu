@@ -56,6 +56,14 @@
 // L4096 H16 dk256 dv128 265 against 1528, B4 L1024 H8 dk512 dv128 80 against 387,
 // B1 L64 H4 dk192 dv64 17 against 56.
 // TMEM: P 2 x 128 columns (PD inside), O 64, dS 3 x 64: all 512.
+// Infinities and NaN.  The products take a masked score as 0, and 0 v_s is no 0
+// where v_s is not finite; the terms of an infinity, and finite values past about
+// 2^80 under a weight of 2^48, leave nothing finite either.  Whatever goes wrong so
+// is not finite in an output of the block or in the state that it leaves, so the
+// output and state warps look for that (one packed operation for four outputs), and
+// a block that finds it goes through its steps again as the recurrence itself
+// (redo_block): every row's earlier steps, and its infinities, are then what the
+// definition says.
 // Loops over columns stay rolled and waits share one slow path: with every
 // role's code unrolled the warps waited for instruction fetches more than for
 // anything else (95 us against 90 at B4 L4096 H16 d128 for the last part of it).
@@ -120,7 +128,7 @@ enum {
 constexpr uint32_t OFF_TMEM = OFF_BAR + NBAR * 8;
 constexpr uint32_t OFF_END = OFF_TMEM + 4;
 constexpr uint32_t OFF_CTL = OFF_TMEM + 8;
-constexpr uint32_t SMEM = OFF_CTL + 32;
+constexpr uint32_t SMEM = OFF_CTL + 40;
 static_assert(SMEM <= 227 * 1024, "one block per SM");
 
 constexpr uint32_t T_P = 0, T_O = 256, T_DS = 320;
@@ -162,8 +170,10 @@ struct Ctl {
     unsigned long long stamp;
     uint64_t timeout_ns;
     int abort_flag;
+    int redo;   // a value that is not finite was written
+    int row;    // the block's batch row
 };
-static_assert(sizeof(Ctl) <= 32, "");
+static_assert(sizeof(Ctl) <= 40, "");
 
 // The slow path of every wait (one copy of the code): bounded; the first to
 // run out makes every role leave its loop.
@@ -190,6 +200,134 @@ __device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, Ctl *ctl) 
             return false;
         }
     }
+}
+
+// 0 times the values that were written, added up: no 0 once one was not finite.
+__device__ __forceinline__ bool not_finite(float2 z) { return !(z.x + z.y == 0.0f); }
+
+// The block's value rows over its segment once more, a step at a time in fp32: the
+// recurrence as it stands, for blocks whose products met an infinity, a NaN or
+// an overflow.  The whole block calls it, with its operands' shared memory free.
+// Four lanes share a value row.  The decay comes in two floats: one, rounded the
+// same way at every step, would add up over the slow heads' thousands of steps.
+// About 1 us a step, against 0.02 of the matrix form; only blocks that met such a
+// value pay it.
+template <bool STATE_ONLY>
+__device__ __forceinline__ void redo_block(const DecayArgs &a, int b, int n_vt, unsigned char *sm) {
+    constexpr int T = 16, W = kPartKeys, RB = kDecayRows;
+    using bf = __nv_bfloat16;
+    float *sk = reinterpret_cast<float *>(sm), *sq = sk + T * W, *sv = sq + T * W;
+    float2 *sa = reinterpret_cast<float2 *>(sv + T * RB);
+    // [m][256]: key columns 4 p + 16 m .. + 3, each its thread's own (in registers, the
+    // call's 64 made the kernel's other code slower: 87.9 us against 87.0)
+    float4 *S = reinterpret_cast<float4 *>(sa + T) + threadIdx.x;
+    // the block's place in the grid
+    const int nseg = STATE_ONLY ? a.n_seg - 1 : a.n_seg;
+    int x = blockIdx.x;
+    const int vt = x % n_vt;
+    x /= n_vt;
+    const int part = x % a.parts;
+    x /= a.parts;
+    const int seg = x % nseg, h = x / nseg % a.H;
+    const int tid = threadIdx.x, i = tid >> 2, p = tid & 3, ldk = a.dk, k0 = W * part;
+    const int dk = min(W, ldk - k0), dv = a.dv, row = vt * RB + i, hk = h / (a.H / a.Hk);
+    const bool mine = tid < 4 * RB, in = mine && row < dv;   // whole warps
+    const int64_t bh = int64_t(b) * a.H + h, s0 = int64_t(seg) * a.seg_len;
+    const int nrun = int(max(int64_t(0), min(int64_t(dec::row_len(a.lens, b, a.L)), min(a.L, s0 + a.seg_len)) - s0));
+    const size_t HK = size_t(a.Hk) * ldk, HV = size_t(a.H) * dv, at0 = size_t(b) * a.L + s0;
+    const bf *q = static_cast<const bf *>(a.q) + at0 * HK + size_t(hk) * ldk + k0;
+    const bf *k = static_cast<const bf *>(a.k) + at0 * HK + size_t(hk) * ldk + k0;
+    const bf *v = static_cast<const bf *>(a.v) + at0 * HV + size_t(h) * dv + vt * RB;
+    const bf *g = a.g == nullptr ? nullptr : static_cast<const bf *>(a.g) + at0 * a.H + h;
+    bf *o = static_cast<bf *>(a.o) + at0 * HV + size_t(h) * dv + row;
+    float *op = a.parts > 1 ? a.o_part + ((size_t(part) * a.B + b) * a.L + s0) * HV + size_t(h) * dv + row : nullptr;
+    const float lh = a.a_log == nullptr ? 0.0f : a.a_log[h];
+    // this thread's columns: those that are there, of a row that is (dk is a multiple of 8)
+    const int nm = in ? (dk / 4 - p + 3) / 4 : 0;
+    const size_t at_S = size_t(row) * ldk + k0 + 4 * p;
+    auto four = [&](const float *src, int m) { return *reinterpret_cast<const float4 *>(src + at_S + 16 * m); };
+    const bool from_S0 = seg == 0 && a.S0 != nullptr;
+#pragma unroll 1
+    for (int m = 0; m < nm; ++m)
+        S[256 * m] = from_S0 ? four(a.S0 + bh * dv * ldk, m) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (!STATE_ONLY && seg > 0) {
+        grid_dependency_wait();
+        long long acc = 0;
+#pragma unroll 1
+        for (int e = seg - 1; e >= 0; --e) {
+            const size_t at = bh * (a.n_seg - 1) + e;
+            const float f = dec::exp2_fix(acc);
+#pragma unroll 1
+            for (int m = 0; m < nm; ++m) {
+                const float4 s = four(a.seg_state + at * dv * ldk, m), y = S[256 * m];
+                S[256 * m] = make_float4(fmaf(f, s.x, y.x), fmaf(f, s.y, y.y), fmaf(f, s.z, y.z), fmaf(f, s.w, y.w));
+            }
+            acc = max(acc + a.seg_tot[at], -(1ll << 60));
+        }
+    }
+#pragma unroll 1
+    for (int t0 = 0; t0 < nrun; t0 += T) {
+        const int n = min(T, nrun - t0);
+        __syncthreads();   // the last steps have been read
+#pragma unroll 1
+        for (int e = tid; e < n * W; e += blockDim.x) {
+            const int t = e / W, j = e % W;
+            const size_t at = size_t(t0 + t) * HK + j;
+            sk[e] = j < dk ? __bfloat162float(k[at]) : 0.0f;
+            if (!STATE_ONLY) sq[e] = j < dk ? __bfloat162float(q[at]) : 0.0f;
+        }
+#pragma unroll 1
+        for (int e = tid; e < n * RB; e += blockDim.x)
+            sv[e] = vt * RB + e % RB < dv ? __bfloat162float(v[size_t(t0 + e / RB) * HV + e % RB]) : 0.0f;
+        if (tid < n) {
+            float l = lh + (g != nullptr ? __bfloat162float(g[size_t(t0 + tid) * a.H]) : 0.0f);
+            if (!(l <= 0.0f)) l = 0.0f;   // (has been reported)
+            const float e = expm1f(l), hi = 1.0f + e;
+            sa[tid] = l > -1.0f ? make_float2(hi, e - (hi - 1.0f)) : make_float2(expf(l), 0.0f);
+        }
+        __syncthreads();
+        if (!mine) continue;
+#pragma unroll 1
+        for (int t = 0; t < n; ++t) {
+            const float2 at = sa[t];
+            const float vi = sv[t * RB + i];
+            float acc = 0.0f;
+            auto step = [&](float x, float kj) {
+                const float u = vi * kj;   // (the decay's rest may be 0 or negative: not times an infinity)
+                return fmaf(at.x, x, fabsf(x) <= 3.4e38f ? fmaf(at.y, x, u) : u);
+            };
+#pragma unroll 1
+            for (int m = 0; m < nm; ++m) {
+                const float4 x = S[256 * m], k4 = reinterpret_cast<const float4 *>(sk + t * W)[p + 4 * m];
+                const float4 y = make_float4(step(x.x, k4.x), step(x.y, k4.y), step(x.z, k4.z), step(x.w, k4.w));
+                S[256 * m] = y;
+                if (STATE_ONLY) continue;
+                const float4 q4 = reinterpret_cast<const float4 *>(sq + t * W)[p + 4 * m];
+                acc = fmaf(y.x, q4.x, fmaf(y.y, q4.y, fmaf(y.z, q4.z, fmaf(y.w, q4.w, acc))));
+            }
+            if (STATE_ONLY) continue;
+            acc += __shfl_xor_sync(0xffffffffu, acc, 1);
+            acc += __shfl_xor_sync(0xffffffffu, acc, 2);
+            if (in && p == 0) {
+                if (op != nullptr)
+                    op[size_t(t0 + t) * HV] = a.scale * acc;
+                else
+                    o[size_t(t0 + t) * HV] = __float2bfloat16_rn(a.scale * acc);
+            }
+        }
+    }
+    float *dst = STATE_ONLY ? a.seg_state + (bh * (a.n_seg - 1) + seg) * dv * ldk
+                 : seg == a.n_seg - 1 && a.S_final != nullptr ? a.S_final + bh * dv * ldk : nullptr;
+    if (dst == nullptr) return;
+#pragma unroll 1
+    for (int m = 0; m < nm; ++m) *reinterpret_cast<float4 *>(dst + at_S + 16 * m) = S[256 * m];
+}
+// The kernels' other code comes out best with this as a call without parts and
+// inlined with them (B4 L4096 H16 d128 87.0 us against 87.1, B1 L32768 234 against
+// 240; dk256 279 against 261).
+template <bool STATE_ONLY>
+__device__ __noinline__ void redo_call(const DecayArgs &a, int b, int n_vt, unsigned char *sm) {
+    redo_block<STATE_ONLY>(a, b, n_vt, sm);
 }
 }  // namespace dt
 
@@ -223,7 +361,7 @@ enum {
 };
 constexpr uint32_t OFF_TOT = OFF_BAR + NBAR * 8;   // the total, then 2 x 4 sums of the scan warps
 constexpr uint32_t OFF_CTL = OFF_TOT + 9 * 8;
-constexpr uint32_t OFF_TMEM = OFF_CTL + 32;
+constexpr uint32_t OFF_TMEM = OFF_CTL + 40;
 constexpr uint32_t SMEM = OFF_TMEM + 8;
 static_assert(SMEM <= 227 * 1024, "one block per SM");
 constexpr uint32_t TMEM_COLS = 256;
@@ -233,7 +371,7 @@ constexpr uint32_t IDESC = umma_idesc_bf16(128, 192, 1, 1);
 template <bool PARTS>
 __global__ void __launch_bounds__(ds::THREADS, 1)
     decay_state_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                       const DecayArgs a, int n_vt, uint64_t timeout_ns, StatusRef sref) {
+                       const __grid_constant__ DecayArgs a, int n_vt, uint64_t timeout_ns, StatusRef sref) {
     using namespace ds;
     using dt::arrive;
     using dt::Ctl;
@@ -277,7 +415,7 @@ __global__ void __launch_bounds__(ds::THREADS, 1)
             const bool by_weights = (i >= EMPTY_V && i < W_FREE) || (i >= M_FREE && i < DONE);
             mbar_init(&bar[i], by_weights ? WEIGHTS : i >= M_READY && i < M_FREE ? 4 : 1);
         }
-        *ctl = Ctl{sref.word, sref.stamp, timeout_ns, 0};
+        *ctl = Ctl{sref.word, sref.stamp, timeout_ns, 0, 0, b};
         *total = 0;
         fence_mbar_init();
     }
@@ -470,6 +608,7 @@ __global__ void __launch_bounds__(ds::THREADS, 1)
         const float f = dec::exp2_fix(tot);
         const float *src = seg == 0 && a.S0 != nullptr ? a.S0 + (size_t(bh) * dv + i0) * ldk + k0 + j : nullptr;
         float *dst = a.seg_state + ((size_t(bh) * nseg + seg) * dv + i0) * ldk + k0 + j;
+        float2 zero = make_float2(0.0f, 0.0f);
 #pragma unroll
         for (int q = 0; q < 32; q += 16) {
             float d1[16] = {}, d2[16] = {}, d3[16] = {};
@@ -483,16 +622,22 @@ __global__ void __launch_bounds__(ds::THREADS, 1)
 #pragma unroll
             for (int r = 0; r < 16; ++r)
                 if (j < dk && i0 + q + r < dv) {
-                    const float y = d1[r] + (d2[r] + d3[r]);
-                    dst[size_t(q + r) * ldk] = src != nullptr ? fmaf(f, src[size_t(q + r) * ldk], y) : y;
+                    float y = d1[r] + (d2[r] + d3[r]);
+                    if (src != nullptr) y = fmaf(f, src[size_t(q + r) * ldk], y);
+                    zero.x = fmaf(0.0f, y, zero.x);
+                    dst[size_t(q + r) * ldk] = y;
                 }
         }
+        if (dt::not_finite(zero)) ctl->redo = 1;
         if (vt == 0 && part == 0 && tid == 0) a.seg_tot[size_t(bh) * nseg + seg] = tot;
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     if (warp == 0) tmem_dealloc(tmem, TMEM_COLS);
+    const bool redo = ctl->redo != 0;
+    if (tid == 0) a.seg_bad[(size_t(bh) * nseg + seg) * a.seg_tiles + (PARTS ? vt * a.parts + part : vt)] = redo;
+    if (redo && ctl->abort_flag == 0) dt::redo_call<true>(a, ctl->row, n_vt, sm);
 }
 
 // ---------------------------------------------------------------------------
@@ -500,8 +645,8 @@ __global__ void __launch_bounds__(ds::THREADS, 1)
 template <bool PARTS>
 __global__ void __launch_bounds__(dt::THREADS, 1)
     decay_tensor_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                        const __grid_constant__ CUtensorMap tm_v, const DecayArgs a, int n_vt, uint64_t timeout_ns,
-                        StatusRef sref) {
+                        const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ DecayArgs a, int n_vt,
+                        uint64_t timeout_ns, StatusRef sref) {
     using namespace dt;
     using bf = __nv_bfloat16;
     extern __shared__ __align__(1024) unsigned char sm[];
@@ -555,7 +700,7 @@ __global__ void __launch_bounds__(dt::THREADS, 1)
             if (i == MMA_END) n = 3;
             mbar_init(&bar[i], n);
         }
-        *ctl = Ctl{sref.word, sref.stamp, timeout_ns, 0};
+        *ctl = Ctl{sref.word, sref.stamp, timeout_ns, 0, 0, b};
         fence_mbar_init();
     }
     if (warp == 0) tmem_alloc(tmem_slot, 512);
@@ -863,6 +1008,8 @@ __global__ void __launch_bounds__(dt::THREADS, 1)
         const int i0 = vt * RB;
         const size_t HV = size_t(a.H) * dv;
         bf *ob = static_cast<bf *>(a.o) + (size_t(b) * a.L + s0) * HV + size_t(h) * dv + i0;
+        float2 zero = make_float2(0.0f, 0.0f);
+        __nv_bfloat162 seen = {0, 0};
         for (int c = 0; c < n_chunks; ++c) {
             const int st = c & 1, mt = c & (NM - 1);
             const uint32_t O = tmem + T_O + lanes;
@@ -904,6 +1051,7 @@ __global__ void __launch_bounds__(dt::THREADS, 1)
 #pragma unroll
                 for (int r = 0; r < 8; ++r) {
                     const float2 y = __fmul2_rn(u2, make_float2(d[2 * r], d[2 * r + 1]));
+                    if (PARTS && valid) zero = __ffma2_rn(y, make_float2(0.0f, 0.0f), zero);
                     if (PARTS)
                         d[2 * r] = y.x, d[2 * r + 1] = y.y;
                     else
@@ -928,6 +1076,10 @@ __global__ void __launch_bounds__(dt::THREADS, 1)
 #pragma unroll
                 for (int r = 0; r < RB / 2; ++r) w[r] = valid ? w[r] : 0u;
             }
+#pragma unroll
+            for (int r = 0; r < RB / 2; r += 2)   // (outputs past 2^63 may look the same, and lose time only)
+                seen = __hfma2(reinterpret_cast<__nv_bfloat162 &>(w[r]), reinterpret_cast<__nv_bfloat162 &>(w[r + 1]),
+                               seen);
             bf *dst = ob + size_t(t) * HV;
             if (store) {
 #pragma unroll
@@ -937,6 +1089,7 @@ __global__ void __launch_bounds__(dt::THREADS, 1)
                             make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
             }
         }
+        if (not_finite(PARTS ? zero : __bfloat1622float2(__hmul2(seen, __nv_bfloat162{0, 0})))) ctl->redo = 1;
     } else {   // --------------------------------------------------------- state
         // key column: this thread's TMEM lane; value rows 32 sh .. of the block's 64
         const int j = tid & 127, sh = warp >> 2;
@@ -955,7 +1108,8 @@ __global__ void __launch_bounds__(dt::THREADS, 1)
 #pragma unroll 1
             for (int e = seg - 1; e >= 0; --e) {
                 const float f = dec::exp2_fix(acc);
-                if (f == 0.0f) break;
+                // nothing is left of the ranges before, unless it is not finite
+                if (f == 0.0f && !dec::any_bad(a, bh, e, PARTS ? vt * a.parts + part : vt)) break;
                 const size_t at = size_t(bh) * (a.n_seg - 1) + e;
                 const float *src = a.seg_state + (at * dv + i0) * ldk + k0 + j;
 #pragma unroll
@@ -1014,9 +1168,15 @@ __global__ void __launch_bounds__(dt::THREADS, 1)
         float *out = seg == a.n_seg - 1 && a.S_final != nullptr ? a.S_final + size_t(bh) * dv * ldk + k0 : nullptr;
         if (out != nullptr && j < dk) {
             const float f = *reinterpret_cast<const float *>(sm + OFF_END);
+            float2 zero = make_float2(0.0f, 0.0f);
 #pragma unroll
             for (int r = 0; r < 32; ++r)
-                if (i0 + r < dv) out[size_t(i0 + r) * ldk + j] = f * S[r];
+                if (i0 + r < dv) {
+                    const float y = f * S[r];
+                    zero.x = fmaf(0.0f, y, zero.x);
+                    out[size_t(i0 + r) * ldk + j] = y;
+                }
+            if (not_finite(zero)) ctl->redo = 1;
         }
     }
     if (warp == SCAN_WARP) asm volatile("bar.sync 1, 288;" ::: "memory");
@@ -1033,6 +1193,12 @@ __global__ void __launch_bounds__(dt::THREADS, 1)
     __syncthreads();
     tc_fence_after();
     if (warp == 0) tmem_dealloc(tmem, 512);
+    if (ctl->redo != 0 && ctl->abort_flag == 0) {
+        if constexpr (PARTS)
+            redo_block<false>(a, ctl->row, n_vt, sm);
+        else
+            redo_call<false>(a, ctl->row, n_vt, sm);
+    }
 }
 
 // o = the parts' sum, rounded once; steps past a row's length are 0.  A block
