@@ -128,7 +128,7 @@ def _load_torch_module():
 
 # The helpers that run once per layer and token first offer their arguments to
 # this module, which takes those that are already what the kernels take and
-# answers None to the others.
+# answers None to the others (a status, where a call failed past its checks).
 _lrtorch = _load_torch_module()
 
 
@@ -807,9 +807,11 @@ def decay_attn(q, k, v, H: int, Hk: Optional[int] = None, a_log=None, g=None, S0
     decay above 0 sets LR_ERR_RANGE (see ``check_status``)."""
     if workspace is None and out is None:
         r = _lrtorch.decay_attn(q, k, v, H, Hk, a_log, g, S0, lens, scale)
-        if r is not None:
+        if type(r) is tuple:
             o, Sf, _tls.ws = r
             return o, Sf
+        if r is not None:
+            _check(r, "lr_decay_attn_fwd")
     (B, L, _), Hk, dk, dv, io = _heads_of(q, k, v, g, H, Hk, 3)
     if a_log is not None:
         _shaped(a_log, (H,), "a_log")
@@ -861,6 +863,8 @@ def group_norm_act(x, G: int, gamma=None, beta=None, z=None, act: str = "none", 
     if a is None:
         raise ValueError(f"unknown activation {act!r}; use one of {sorted(_ACT)}")
     y = _lrtorch.group_norm_act(x, G, gamma, beta, z, a, eps, out)
+    if type(y) is int:
+        _check(y, "lr_group_norm_act")
     if y is not None:
         return y
     shape = x.shape
@@ -982,8 +986,10 @@ def decay_attn_step(q, k, v, H: int, Hk: Optional[int] = None, a_log=None, g=Non
     fp32 or None (zero).  Returns (o (B, H*dv), S_new); ``S_out`` gives the
     buffer S_new is written to (it may be ``S`` itself)."""
     r = _lrtorch.decay_attn_step(q, k, v, H, Hk, a_log, g, S, S_out, scale)
-    if r is not None:
+    if type(r) is tuple:
         return r
+    if r is not None:
+        _check(r, "lr_decay_attn_step")
     (B, _), Hk, dk, dv, io = _heads_of(q, k, v, g, H, Hk, 2)
     shape = (B, H, dv, dk)
     if a_log is not None:

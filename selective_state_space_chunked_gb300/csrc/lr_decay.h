@@ -65,21 +65,30 @@ constexpr int kPartKeys = 128;      // its key columns per block
 // rows of the state per block of the general kernel
 int decay_general_rows(int64_t dk, bool narrow);
 
-// A launch that may start while the kernel before it on the stream drains; the
-// kernel waits for that one's results itself (grid_dependency_wait).
+// One launch, and its own status: an error that an earlier call of the thread left
+// unread says nothing about it (a caller that is told of a failure may launch
+// again, onto a state that has been updated).  early: it may start while the kernel
+// before it on the stream drains, and waits for that one's results itself
+// (grid_dependency_wait).
 template <typename... P, typename... A>
-int launch_early(void (*kern)(P...), dim3 grid, int threads, cudaStream_t stream, A... args) {
+int launch_kernel(void (*kern)(P...), bool early, dim3 grid, int threads, size_t smem, cudaStream_t stream, A... args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, P(args)...) == cudaSuccess && cudaGetLastError() == cudaSuccess ? LR_OK
-                                                                                                       : LR_ERR_CUDA;
+    cfg.numAttrs = early ? 1 : 0;
+    if (cudaLaunchKernelEx(&cfg, kern, P(args)...) == cudaSuccess) return LR_OK;
+    (void)cudaGetLastError();   // reported here
+    return LR_ERR_CUDA;
+}
+template <typename... P, typename... A>
+int launch_early(void (*kern)(P...), dim3 grid, int threads, cudaStream_t stream, A... args) {
+    return launch_kernel(kern, true, grid, threads, 0, stream, args...);
 }
 
 int decay_step_launch(const void *q, const void *k, const void *v, const float *a_log, const void *g,

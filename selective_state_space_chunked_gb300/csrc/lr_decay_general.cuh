@@ -465,24 +465,14 @@ int launch_general_cfg(const DecayArgs &a, StatusRef st, cudaStream_t stream) {
     const int64_t per_seg = a.B * a.H * nrb;
     if (per_seg * a.n_seg > INT32_MAX) return LR_ERR_UNSUPPORTED;
     if (a.n_seg > 1) {
-        first<<<unsigned(per_seg * (a.n_seg - 1)), C::NT, smem, stream>>>(mq, mk, mv, a, nrb, tma, kDefaultTimeoutNs,
-                                                                        st);
-        if (cudaGetLastError() != cudaSuccess) return LR_ERR_CUDA;
+        const int rc = launch_kernel(first, false, dim3(unsigned(per_seg * (a.n_seg - 1))), C::NT, smem, stream, mq,
+                                     mk, mv, a, nrb, tma, kDefaultTimeoutNs, st);
+        if (rc != LR_OK) return rc;
     }
     // dependent launch: of the kernel before the call, or of the first launch, of
     // which segment 0 needs nothing
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(unsigned(per_seg * a.n_seg));
-    cfg.blockDim = dim3(C::NT);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, main, mq, mk, mv, a, nrb, tma, uint64_t(kDefaultTimeoutNs), st);
-    return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? LR_OK : LR_ERR_CUDA;
+    return launch_kernel(main, true, dim3(unsigned(per_seg * a.n_seg)), C::NT, smem, stream, mq, mk, mv, a, nrb, tma,
+                         kDefaultTimeoutNs, st);
 }
 
 template <typename IO, int DKP>

@@ -1283,31 +1283,20 @@ int decay_tensor_launch(const DecayArgs &a, StatusRef st, cudaStream_t stream) {
     const bool parts = a.parts > 1;
     const int64_t per_seg = a.B * a.H * n_vt * a.parts;
     if (per_seg * a.n_seg > INT32_MAX) return LR_ERR_UNSUPPORTED;
-    if (a.n_seg > 1) {
-        (parts ? decay_state_kernel<true> : decay_state_kernel<false>)<<<unsigned(per_seg * (a.n_seg - 1)), ds::THREADS, ds::SMEM, stream>>>(
-            mk, mv, a, n_vt, kDefaultTimeoutNs, st);
-        if (cudaGetLastError() != cudaSuccess) return LR_ERR_CUDA;
-    }
+    int rc = LR_OK;
+    if (a.n_seg > 1)
+        rc = launch_kernel(parts ? decay_state_kernel<true> : decay_state_kernel<false>, false,
+                           dim3(unsigned(per_seg * (a.n_seg - 1))), ds::THREADS, ds::SMEM, stream, mk, mv, a, n_vt,
+                           kDefaultTimeoutNs, st);
     // dependent launch: of the kernel before the call, or of the first launch, of
     // which segment 0 needs nothing
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(unsigned(per_seg * a.n_seg));
-    cfg.blockDim = dim3(dt::THREADS);
-    cfg.dynamicSmemBytes = dt::SMEM;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, parts ? decay_tensor_kernel<true> : decay_tensor_kernel<false>, mq,
-                                             mk, mv, a, n_vt, uint64_t(kDefaultTimeoutNs), st);
-    if (e != cudaSuccess) return LR_ERR_CUDA;
-    if (parts) {
-        const int64_t rows = a.B * a.L;
-        return launch_early(decay_parts_kernel, dim3(unsigned(rows < (1 << 20) ? rows : 1 << 20)), 256, stream, a);
-    }
-    return cudaGetLastError() == cudaSuccess ? LR_OK : LR_ERR_CUDA;
+    if (rc == LR_OK)
+        rc = launch_kernel(parts ? decay_tensor_kernel<true> : decay_tensor_kernel<false>, true,
+                           dim3(unsigned(per_seg * a.n_seg)), dt::THREADS, dt::SMEM, stream, mq, mk, mv, a, n_vt,
+                           kDefaultTimeoutNs, st);
+    if (rc != LR_OK || !parts) return rc;
+    const int64_t rows = a.B * a.L;
+    return launch_early(decay_parts_kernel, dim3(unsigned(rows < (1 << 20) ? rows : 1 << 20)), 256, stream, a);
 }
 
 }  // namespace lr

@@ -7,8 +7,10 @@
 // Each function takes what its helper in binding.py takes and returns what it
 // returns, or None where an argument is not already what the kernels take
 // (another type or device, not contiguous, shapes that do not match, empty) or
-// the call was refused; nothing has been launched then, and the helper goes on to
-// its own checks and conversions, which convert the argument or say what is wrong.
+// the call's own checks refused it; nothing has been launched then, and the helper
+// goes on to its own checks and conversions, which convert the argument or say what
+// is wrong.  Any other status comes back as an int, for the helper to raise: part of
+// the call may have run, and it may have updated a state in place.
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
@@ -105,6 +107,13 @@ PyObject *declined() {
     Py_RETURN_NONE;
 }
 
+// What a call that was not LR_OK gives: None after the checks that come before
+// every launch, else the status.
+PyObject *refused(int rc) {
+    if (rc == LR_ERR_INVALID_ARG || rc == LR_ERR_UNSUPPORTED || rc == LR_ERR_MISALIGNED) Py_RETURN_NONE;
+    return PyLong_FromLong(rc);
+}
+
 // (q, k, v, H, Hk, a_log, g, S, S_out, scale) -> (o, S_new)
 PyObject *decay_attn_step(PyObject *, PyObject *const *args, Py_ssize_t n) {
     if (n != 10) Py_RETURN_NONE;
@@ -134,10 +143,10 @@ PyObject *decay_attn_step(PyObject *, PyObject *const *args, Py_ssize_t n) {
         const Ref po(THPVariable_Wrap(o)), ps(Sn.defined() ? THPVariable_Wrap(Sn) : Ref::share(args[8]));
         Ref result(po.o && ps.o ? PyTuple_Pack(2, po.o, ps.o) : nullptr);
         if (result.o == nullptr) return declined();
-        if (lr_decay_attn_step(q->data_ptr(), k, v, static_cast<float *>(a), g, scale, static_cast<float *>(S_in),
-                               static_cast<float *>(S_out), o.data_ptr(), B, s.H, s.Hk, s.dk, s.dv, c.io,
-                               c.stream()) != LR_OK)
-            Py_RETURN_NONE;
+        const int rc = lr_decay_attn_step(q->data_ptr(), k, v, static_cast<float *>(a), g, scale,
+                                          static_cast<float *>(S_in), static_cast<float *>(S_out), o.data_ptr(), B,
+                                          s.H, s.Hk, s.dk, s.dv, c.io, c.stream());
+        if (rc != LR_OK) return refused(rc);
         return Ref::share(result.o);
     } catch (...) {   // an allocation that failed: the helper's own says so
         return declined();
@@ -170,10 +179,10 @@ PyObject *decay_attn(PyObject *, PyObject *const *args, Py_ssize_t n) {
         const Ref po(THPVariable_Wrap(o)), ps(THPVariable_Wrap(Sf)), pw(THPVariable_Wrap(ws));
         Ref result(po.o && ps.o && pw.o ? PyTuple_Pack(3, po.o, ps.o, pw.o) : nullptr);
         if (result.o == nullptr) return declined();
-        if (lr_decay_attn_fwd(q->data_ptr(), k, v, static_cast<float *>(a), g, static_cast<int32_t *>(lens), scale,
-                              static_cast<float *>(S0), o.data_ptr(), Sf.data_ptr<float>(), B, L, s.H, s.Hk, s.dk,
-                              s.dv, c.io, ws.data_ptr(), wsb, c.stream()) != LR_OK)
-            Py_RETURN_NONE;
+        const int rc = lr_decay_attn_fwd(q->data_ptr(), k, v, static_cast<float *>(a), g, static_cast<int32_t *>(lens),
+                                         scale, static_cast<float *>(S0), o.data_ptr(), Sf.data_ptr<float>(), B, L,
+                                         s.H, s.Hk, s.dk, s.dv, c.io, ws.data_ptr(), wsb, c.stream());
+        if (rc != LR_OK) return refused(rc);
         return Ref::share(result.o);
     } catch (...) {
         return declined();
@@ -204,9 +213,9 @@ PyObject *group_norm_act(PyObject *, PyObject *const *args, Py_ssize_t n) {
         }
         Ref result(y.defined() ? THPVariable_Wrap(y) : Ref::share(args[7]));
         if (result.o == nullptr) return declined();
-        if (lr_group_norm_act(x->data_ptr(), z, static_cast<float *>(gamma), static_cast<float *>(beta), out,
-                              x->numel() / C, C, G, eps, static_cast<lr_act>(act), c.io, c.stream()) != LR_OK)
-            Py_RETURN_NONE;
+        const int rc = lr_group_norm_act(x->data_ptr(), z, static_cast<float *>(gamma), static_cast<float *>(beta),
+                                         out, x->numel() / C, C, G, eps, static_cast<lr_act>(act), c.io, c.stream());
+        if (rc != LR_OK) return refused(rc);
         return Ref::share(result.o);
     } catch (...) {
         return declined();
