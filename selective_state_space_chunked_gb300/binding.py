@@ -376,12 +376,19 @@ def _ptr(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
 
+def _aligned(t: torch.Tensor) -> torch.Tensor:
+    """t, contiguous, from a 16-byte boundary: a contiguous view starts anywhere
+    (a step of one row, a row of an odd width, a layer of stacked parameters)."""
+    t = t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
 def _dev(t: Optional[torch.Tensor], device) -> Optional[torch.Tensor]:
     if t is None:
         return None
     if t.device.type != "cuda":
         t = t.to(device, non_blocking=True)
-    return t.contiguous()
+    return _aligned(t)
 
 
 def _check(rc: int, where: str):
@@ -485,7 +492,7 @@ def _h(t: Optional[torch.Tensor], dtype=None) -> Optional[torch.Tensor]:
         t = t.cpu()
     if dtype is not None:
         t = t.to(dtype)
-    return t.contiguous()
+    return _aligned(t)
 
 
 def _host_outputs(out, specs):
@@ -777,15 +784,15 @@ def _stream_of(t: torch.Tensor) -> int:
 
 
 def _act(t: Optional[torch.Tensor], dev) -> Optional[torch.Tensor]:
-    """t on the GPU, contiguous."""
-    if t is None or (t.is_cuda and t.is_contiguous()):
+    """t on the GPU, contiguous and aligned."""
+    if t is None or (t.is_cuda and t.is_contiguous() and t.data_ptr() % 16 == 0):
         return t
     return _dev(t, dev)
 
 
 def _par(t: Optional[torch.Tensor], dev) -> Optional[torch.Tensor]:
     """As _act, in float32 (parameters and states)."""
-    if t is None or (t.dtype is torch.float32 and t.is_cuda and t.is_contiguous()):
+    if t is None or (t.dtype is torch.float32 and t.is_cuda and t.is_contiguous() and t.data_ptr() % 16 == 0):
         return t
     return _dev(t.float(), dev)
 
@@ -880,9 +887,7 @@ def group_norm_act(x, G: int, gamma=None, beta=None, z=None, act: str = "none", 
     if beta is not None:
         _shaped(beta, (C,), "beta")
     dev = x.device if x.is_cuda else _target_device(x)
-    z, gamma, beta = _act(z, dev), _par(gamma, dev), _par(beta, dev)
-    if not (x.is_cuda and x.is_contiguous()):
-        x = _dev(x, dev)
+    x, z, gamma, beta = _act(x, dev), _act(z, dev), _par(gamma, dev), _par(beta, dev)
     if out is None:
         out = torch.empty_like(x)
     elif out.shape != shape or out.dtype != x.dtype or out.device != dev or not out.is_contiguous():

@@ -1,18 +1,69 @@
 """The torch helpers of the decayed attention, its step and the group norm as a
-program calls them: errors."""
+program calls them: views at any offset, and errors."""
 import ctypes
 
 import pytest
 import torch
 
+import oracle
+from conftest import rel_err
 from selective_state_space_chunked_gb300 import workloads as wl
-from test_decay_attn_gpu import cuda, lr  # noqa: F401
+from test_decay_attn_gpu import TOL, TOL_S, cuda, lr  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
 
 def step_args(p, t):
     return p["q"][:, t], p["k"][:, t], p["v"][:, t]
+
+
+# ------------------------------------------------------------------ views
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_steps_on_views_of_one_row(lr, io):  # noqa: F811
+    """[:, t] of one row is contiguous and starts anywhere."""
+    L, H, dk, dv = 9, 6, 20, 12
+    p = wl.decay_attn_inputs(1, L, H, dk, dv, seed=3, io=io, Hk=3, with_S0=True)
+    a_log = torch.stack([p["a_log"]] * 3)
+    d = cuda(p)
+    S, outs = d["S0"].clone(), []
+    for t in range(L):
+        o, _ = lr.decay_attn_step(*step_args(d, t), H, Hk=3, a_log=a_log.cuda()[1], g=d["g"][:, t], S=S, S_out=S)
+        outs.append(o[:, None])
+    orf, Srf = oracle.decay_attn(p["q"], p["k"], p["v"], H, Hk=3, a_log=p["a_log"], g=p["g"], S0=p["S0"])
+    assert rel_err(torch.cat(outs, 1).float().cpu(), orf) <= TOL[io] and rel_err(S.cpu(), Srf) <= TOL_S
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("host", [False, True])
+def test_prompts_on_views(lr, io, host):  # noqa: F811
+    L, H, d = 60, 3, 33
+    p = wl.decay_attn_inputs(3, L, H, d, d, seed=4, io=io, with_S0=True)
+    lens = torch.tensor([7, 60, 31], dtype=torch.int32)
+    orf, Srf = oracle.decay_attn(p["q"], p["k"], p["v"], H, a_log=p["a_log"], g=p["g"], S0=p["S0"],
+                                 lens=None if host else lens)
+    q, k, v, g, S0 = (p[n] if host else p[n].cuda() for n in ("q", "k", "v", "g", "S0"))
+    a_log = torch.stack([p["a_log"]] * 3)[1] if host else torch.stack([p["a_log"]] * 3).cuda()[1]
+    if host:   # rows, steps of a row: contiguous from any offset
+        o, S = lr.decay_attn(q[1:2, 1:], k[1:2, 1:], v[1:2, 1:], H, a_log=a_log, g=g[1:2, 1:], S0=S0[1:2])
+        orf, Srf = oracle.decay_attn(p["q"][1:2, 1:], p["k"][1:2, 1:], p["v"][1:2, 1:], H, a_log=p["a_log"],
+                                     g=p["g"][1:2, 1:], S0=p["S0"][1:2])
+    else:
+        o, S = lr.decay_attn(q[1:], k[1:], v[1:], H, a_log=a_log, g=g[1:], S0=S0[1:], lens=lens.cuda()[1:])
+        orf, Srf = orf[1:], Srf[1:]
+    assert rel_err(o.float().cpu(), orf) <= TOL[io] and rel_err(S.cpu(), Srf) <= TOL_S
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_group_norm_on_views(lr, io):  # noqa: F811
+    gen = torch.Generator().manual_seed(2)
+    x, z = (torch.randn(5, 33, generator=gen).to(torch.float32 if io == "f32" else torch.bfloat16) for _ in range(2))
+    gamma = torch.randn(3, 33, generator=gen)
+    y = lr.group_norm_act(x.cuda()[1:], 3, gamma=gamma.cuda()[1], z=z.cuda()[1:])
+    # fp32: see test_group_norm_gpu; bf16: the store's rounding
+    assert rel_err(y.float().cpu(), oracle.group_norm_act(x[1:], 3, gamma[1], None, z[1:])) <= {"f32": 5e-6,
+                                                                                              "bf16": 4e-3}[io]
+    with pytest.raises(lr.LrError):
+        lr.group_norm_act(x.cuda(), 3, out=torch.empty(6, 33, dtype=x.dtype, device="cuda")[1:])
 
 
 # ----------------------------------------------------------------- errors
