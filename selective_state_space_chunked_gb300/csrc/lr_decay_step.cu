@@ -27,6 +27,11 @@
 namespace lr {
 namespace {
 
+// The inputs are plain pointers: a const __restrict__ one says that its data stays
+// the same while the kernel lives, and a kernel that starts early lives while the
+// one before it may still be writing them.  So all are read before the first store
+// (B64 24.6 us with v read between the stores).
+
 template <typename IO>
 __device__ __forceinline__ float4 step_ld4(const IO *p);
 template <>
@@ -43,13 +48,12 @@ __device__ __forceinline__ float4 step_ld4<__nv_bfloat16>(const __nv_bfloat16 *p
 constexpr int kStepT = 64;
 
 // dk % 4 == 0 and dk <= 4 TL V: V groups of four keys per lane.
-// A warp takes 32 / TL rows at a time, R times.
+// A warp takes 32 / TL rows at a time, R times.  20 blocks per SM leave 48 registers
+// (B64 22.9 us with 52).
 template <typename IO, int TL, int R, int V>
-__global__ void __launch_bounds__(kStepT)
-    decay_step_kernel(const IO *__restrict__ q, const IO *__restrict__ k, const IO *__restrict__ v,
-                      const float *__restrict__ a_log, const IO *__restrict__ g, float scale,
-                      const float *S_in, float *S_out, IO *__restrict__ o, int64_t BH, int H, int Hk, int dk,
-                      int dv, int tiles) {
+__global__ void __launch_bounds__(kStepT, V == 1 ? 20 : V == 2 ? 1 : 12)
+    decay_step_kernel(const IO *q, const IO *k, const IO *v, const float *a_log, const IO *g, float scale,
+                      const float *S_in, float *S_out, IO *o, int64_t BH, int H, int Hk, int dk, int dv, int tiles) {
     constexpr int RPW = 32 / TL;          // rows a warp holds at once
     constexpr int ROWS = RPW * R;         // rows per warp
     const int lane = threadIdx.x & 31, sub = lane / TL, j0 = 4 * (lane % TL);
@@ -83,6 +87,12 @@ __global__ void __launch_bounds__(kStepT)
         k4[u] = j < dk ? step_ld4(k + kat) : zero;
         q4[u] = j < dk ? step_ld4(q + kat) : zero;
     }
+    float vr[R];   // before the first store, which may be to anywhere
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const int i = row0 + r * RPW + sub;
+        vr[r] = i < dv ? Io<IO>::to_f(v[base + i]) : 0.0f;
+    }
     float l = a_log != nullptr ? a_log[h] : 0.0f;
     if (g != nullptr) l += Io<IO>::to_f(g[bh]);
     const float a = expf(l);
@@ -90,7 +100,7 @@ __global__ void __launch_bounds__(kStepT)
     for (int r = 0; r < R; ++r) {
         const int i = row0 + r * RPW + sub;
         const bool in = i < dv;
-        const float vi = in ? Io<IO>::to_f(v[base + i]) : 0.0f;
+        const float vi = vr[r];
         float acc = 0.0f;
 #pragma unroll
         for (int u = 0; u < V; ++u) {
@@ -110,10 +120,8 @@ __global__ void __launch_bounds__(kStepT)
 // any dk: one warp per row
 template <typename IO>
 __global__ void __launch_bounds__(kStepT)
-    decay_step_any_kernel(const IO *__restrict__ q, const IO *__restrict__ k, const IO *__restrict__ v,
-                          const float *__restrict__ a_log, const IO *__restrict__ g, float scale,
-                          const float *S_in, float *S_out, IO *__restrict__ o, int64_t BH, int H, int Hk,
-                          int dk, int dv) {
+    decay_step_any_kernel(const IO *q, const IO *k, const IO *v, const float *a_log, const IO *g, float scale,
+                          const float *S_in, float *S_out, IO *o, int64_t BH, int H, int Hk, int dk, int dv) {
     const int64_t row = int64_t(blockIdx.x) * (kStepT / 32) + (threadIdx.x >> 5);
     const int lane = threadIdx.x & 31;
     launch_dependents();

@@ -1,5 +1,6 @@
 """The torch helpers of the decayed attention, its step and the group norm as a
-program calls them: views at any offset, and errors."""
+program calls them: views at any offset, calls that follow one another with nothing
+between, and errors."""
 import ctypes
 
 import pytest
@@ -64,6 +65,39 @@ def test_group_norm_on_views(lr, io):  # noqa: F811
                                                                                               "bf16": 4e-3}[io]
     with pytest.raises(lr.LrError):
         lr.group_norm_act(x.cuda(), 3, out=torch.empty(6, 33, dtype=x.dtype, device="cuda")[1:])
+# ------------------------------------------- calls with nothing between them
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("B,H,dk,dv", [(1, 4, 64, 64), (16, 16, 128, 128), (300, 4, 32, 32), (7, 5, 33, 10)])
+def test_calls_follow_one_another(lr, io, B, H, dk, dv):  # noqa: F811
+    """prompt -> step -> step in place -> norm onto v -> step that reads it: each
+    starts while the one before it drains, and reads what that one wrote."""
+    n = 5
+    p = wl.decay_attn_inputs(B, n, H, dk, dv, seed=B, io=io)
+    d = cuda(p)
+    qs, ks, gs = ([d[x][:, t].contiguous() for t in range(n)] for x in ("q", "k", "g"))
+    vs = [d["v"][:, t].contiguous() for t in range(n)]
+    prompt = [d[x][:, :1].contiguous() for x in ("q", "k", "v", "g")]
+    a = d["a_log"]
+    torch.cuda.synchronize()
+    o, S = lr.decay_attn(*prompt[:3], H, a_log=a, g=prompt[3])
+    outs = [o[:, 0]]
+    for t in range(1, n):
+        o, _ = lr.decay_attn_step(qs[t], ks[t], vs[t], H, a_log=a, g=gs[t], S=S, S_out=S)
+        outs.append(o)
+        if t + 1 < n:
+            lr.group_norm_act(o, H, out=vs[t + 1])
+    torch.cuda.synchronize()
+    v = p["v"].clone()
+    Sr, ref = None, []
+    for t in range(n):   # the next v from the kernel's own output: no error is carried over
+        orf, Sr = oracle.decay_attn(p["q"][:, t:t + 1], p["k"][:, t:t + 1], v[:, t:t + 1], H, a_log=p["a_log"],
+                                    g=p["g"][:, t:t + 1], S0=Sr)
+        assert rel_err(outs[t].float().cpu(), orf[:, 0]) <= TOL[io], t
+        if 1 <= t < n - 1:
+            want = oracle.group_norm_act(outs[t].float().cpu(), H)
+            assert rel_err(vs[t + 1].float().cpu(), want) <= {"f32": 5e-6, "bf16": 4e-3}[io]
+            v[:, t + 1] = vs[t + 1].cpu()
+    assert rel_err(S.cpu(), Sr) <= TOL_S
 
 
 # ----------------------------------------------------------------- errors
