@@ -1259,17 +1259,15 @@ bool dt_map(CUtensorMap *tm, const void *base, uint64_t d, uint64_t heads, uint6
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-bool dt_setup_once() {
-    static std::once_flag once;
-    static bool ok = false;
-    std::call_once(once, [] {
+bool dt_setup() {
+    static DeviceSetup setup;
+    return setup.run([] {
         auto room = [](auto kern, uint32_t bytes) {
             return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes)) == cudaSuccess;
         };
-        ok = room(decay_state_kernel<false>, ds::SMEM) && room(decay_state_kernel<true>, ds::SMEM) &&
-             room(decay_tensor_kernel<false>, dt::SMEM) && room(decay_tensor_kernel<true>, dt::SMEM);
+        return room(decay_state_kernel<false>, ds::SMEM) && room(decay_state_kernel<true>, ds::SMEM) &&
+               room(decay_tensor_kernel<false>, dt::SMEM) && room(decay_tensor_kernel<true>, dt::SMEM);
     });
-    return ok;
 }
 
 }  // namespace
@@ -1277,7 +1275,7 @@ bool dt_setup_once() {
 int decay_tensor_launch(const DecayArgs &a, StatusRef st, cudaStream_t stream) {
     CUtensorMap mq, mk, mv;
     if (!dt_map(&mq, a.q, a.dk, a.Hk, a.L, a.B) || !dt_map(&mk, a.k, a.dk, a.Hk, a.L, a.B) ||
-        !dt_map(&mv, a.v, a.dv, a.H, a.L, a.B) || !dt_setup_once())
+        !dt_map(&mv, a.v, a.dv, a.H, a.L, a.B) || !dt_setup())
         return LR_ERR_CUDA;
     const int n_vt = (a.dv + dt::RB - 1) / dt::RB;
     const bool parts = a.parts > 1;

@@ -626,7 +626,6 @@ bool make_map_3d(CUtensorMap *tm, const void *base, CUtensorMapDataType type, si
 }
 
 // Per-device facts and per-kernel attributes, looked up once.
-constexpr int kMaxDevices = 64;
 
 struct DeviceInfo {
     std::once_flag once;

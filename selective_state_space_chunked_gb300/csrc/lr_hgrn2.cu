@@ -822,14 +822,12 @@ bool hg_smem_attr(K kern) {
            cudaSuccess;
 }
 
-bool hg_setup_once() {
-    static std::once_flag once;
-    static bool ok = false;
-    std::call_once(once, [] {
-        ok = hg_smem_attr(hgrn2_chunk_kernel<false, false>) && hg_smem_attr(hgrn2_chunk_kernel<false, true>) &&
-             hg_smem_attr(hgrn2_chunk_kernel<true, false>) && hg_smem_attr(hgrn2_chunk_kernel<true, true>);
+bool hg_setup() {
+    static DeviceSetup setup;
+    return setup.run([] {
+        return hg_smem_attr(hgrn2_chunk_kernel<false, false>) && hg_smem_attr(hgrn2_chunk_kernel<false, true>) &&
+               hg_smem_attr(hgrn2_chunk_kernel<true, false>) && hg_smem_attr(hgrn2_chunk_kernel<true, true>);
     });
-    return ok;
 }
 
 // A lower-bounded gate g >= lb keeps every quarter of a chunk within
@@ -853,7 +851,7 @@ int hgrn2_launch(const void *q, const void *k, const void *v, const void *g, con
     if (!hg_map(&mq, q, HK, L, B, 64, true) || !hg_map(&mk, k, HK, L, B, 64, true) ||
         !hg_map(&mv, v, HV, L, B, hg::RB, false) || !hg_map(&mg, g, HV, L, B, hg::RB, false))
         return LR_ERR_CUDA;
-    if (!hg_setup_once()) return LR_ERR_CUDA;
+    if (!hg_setup()) return LR_ERR_CUDA;
     const int n_chunks = static_cast<int>((L + hg::C - 1) / hg::C);
     const int64_t grid = B * H * hg::NRB;
     const uint64_t timeout = g_withheld_split >= 1 ? uint64_t(g_withheld_timeout_ms) * 1000000ull

@@ -31,8 +31,6 @@
 // that is not a finite number sets LR_ERR_RANGE.
 #include <cudaTypedefs.h>
 
-#include <mutex>
-
 #include "lr_device.cuh"
 #include "lr_internal.h"
 
@@ -432,11 +430,9 @@ bool hf_smem_attr(K kern) {
            cudaSuccess;
 }
 
-bool hf_setup_once() {
-    static std::once_flag once;
-    static bool ok = false;
-    std::call_once(once, [] { ok = hf_smem_attr(hgrn2_f32_kernel<false>) && hf_smem_attr(hgrn2_f32_kernel<true>); });
-    return ok;
+bool hf_setup() {
+    static DeviceSetup setup;
+    return setup.run([] { return hf_smem_attr(hgrn2_f32_kernel<false>) && hf_smem_attr(hgrn2_f32_kernel<true>); });
 }
 
 }  // namespace
@@ -449,7 +445,7 @@ int hgrn2_f32_launch(const void *q, const void *k, const void *v, const void *g,
     if (!encode_map_3d(&mq, q, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, HK, uint64_t(L), uint64_t(B), hf::DK, hf::C, 1) ||
         !encode_map_3d(&mk, k, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, HK, uint64_t(L), uint64_t(B), hf::DK, hf::C, 1))
         return LR_ERR_CUDA;
-    if (!hf_setup_once()) return LR_ERR_CUDA;
+    if (!hf_setup()) return LR_ERR_CUDA;
     const int n_chunks = static_cast<int>((L + hf::C - 1) / hf::C);
     const int64_t grid = B * H * hf::NRB;
     const uint64_t timeout = g_withheld_split >= 1 ? uint64_t(g_withheld_timeout_ms) * 1000000ull : kDefaultTimeoutNs;

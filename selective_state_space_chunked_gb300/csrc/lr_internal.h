@@ -4,6 +4,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -68,6 +70,23 @@ extern int64_t g_selective_warmup_steps;   // lr_set_selective_warmup
 constexpr uint64_t kDefaultTimeoutNs = 1000000000ull;  // 1 s
 
 int device_sm_count(int *sms);  // LR_OK / LR_ERR_CUDA
+
+constexpr int kMaxDevices = 64;
+// What is set up once on every device of the process (a kernel's attributes are a
+// device's own): f, on the current device, until it has succeeded there.
+struct DeviceSetup {
+    std::atomic<bool> done[kMaxDevices] = {};
+    template <typename F>
+    bool run(F f) {
+        int dev = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return false;
+        if (!done[dev].load(std::memory_order_acquire)) {
+            if (!f()) return false;
+            done[dev].store(true, std::memory_order_release);
+        }
+        return true;
+    }
+};
 
 int rglru_plan(int64_t B, int64_t L, int64_t D, lr_dtype io, DiagPlan *p);
 int rglru_launch(const void *x, const void *r, const void *i, const float *a_log, float c,

@@ -327,11 +327,17 @@ int launch_lanes(const NormArgs &a, int sms, cudaStream_t s) {
     // 2048 bf16, gate, G 32 31.3 us against 34.6, G 16 33.0 against 34.4; 8192 x 4096
     // 24.5 against 26.5; 591 x 8192 fp32, gate 9.8 against 11.3.  Groups of three
     // vectors a lane take twice as many: 3001 x 1920 fp32 8.45 us against 9.1.
-    static const int fit = [] {
-        int n = 0;
-        return cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, group_norm_lanes_kernel<X, TL, V, R, GATE>, 256, 0) ==
-                           cudaSuccess && n > 0 ? n : 1;
-    }();
+    static DeviceSetup setup;
+    static std::atomic<int> fit{1};   // (the same on every GPU that runs this code)
+    if (!setup.run([] {
+            int n = 0;
+            if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, group_norm_lanes_kernel<X, TL, V, R, GATE>, 256, 0) !=
+                    cudaSuccess || n < 1)
+                return false;
+            fit = n;
+            return true;
+        }))
+        return LR_ERR_CUDA;
     const int64_t full = int64_t(sms) * fit * (V == 3 ? 2 : 1);
     const bool deep = row_blocks * gy >= full * R;
     int64_t gx = deep ? (full + gy - 1) / gy : row_blocks;

@@ -1354,7 +1354,6 @@ __global__ void __launch_bounds__(kWpb * 32, SelCfg<IO, CPL>::MINB)
 // ----------------------------------------------------------------------------
 // Compiled variants
 // ----------------------------------------------------------------------------
-constexpr int kMaxDevices = 64;
 
 template <typename IO>
 using HostCfg = SelCfg<IO, cpl_of<IO>()>;

@@ -8,13 +8,14 @@ typedef struct { unsigned x, y, z; } Dim3;
 typedef struct { Dim3 grid, block; size_t smem; void *stream, *attrs; unsigned n_attrs; } Config;
 
 enum { MAX = 512, INVALID_VALUE = 1 };
-static int device, pending, launches, fail_next;
+static int device, pending, launches, fail_next, fail_attribute;
 static struct { int dev; const void *func; size_t limit; } limits[MAX];
 static int n_limits;
 
 void fake_set_device(int d) { device = d; }
 void fake_set_pending_error(int e) { pending = e; }
 void fake_fail_next_launch(int n) { fail_next = n; }   /* the n-th from now */
+void fake_fail_next_attribute(void) { fail_attribute = 1; }
 int fake_launches(void) { return launches; }
 
 int cudaGetDevice(int *d) { *d = device; return 0; }
@@ -22,7 +23,10 @@ int cudaDeviceGetAttribute(int *v, int attr, int dev) { (void)attr, (void)dev; *
 int cudaGetLastError(void) { int e = pending; pending = 0; return e; }
 
 int cudaFuncSetAttribute(const void *func, int attr, int value) {
-    if (attr != 8 || n_limits == MAX) return INVALID_VALUE;   /* MaxDynamicSharedMemorySize */
+    if (attr != 8 || n_limits == MAX || fail_attribute) {   /* MaxDynamicSharedMemorySize */
+        fail_attribute = 0;
+        return INVALID_VALUE;
+    }
     limits[n_limits].dev = device, limits[n_limits].func = func, limits[n_limits].limit = (size_t)value;
     ++n_limits;
     return 0;

@@ -1,7 +1,7 @@
 """The launches of the C entry points against a stand-in for the CUDA runtime
 (fake_cudart.c, preloaded in a child process; nothing runs on a GPU and the
-pointers are never dereferenced): what a call answers where a launch fails, and where
-an older error of the thread was never read."""
+pointers are never dereferenced): what a call answers where a launch fails, where an
+older error of the thread was never read, and on the second device of a process."""
 import os
 import subprocess
 import sys
@@ -18,6 +18,7 @@ lib = ctypes.CDLL(sys.argv[1])
 P, I, F = ctypes.c_void_p, ctypes.c_int64, ctypes.c_float
 p = lambda: P(0x7F0000000000)
 lib.lr_decay_attn_workspace_size.restype = ctypes.c_size_t
+lib.lr_hgrn2_workspace_size.restype = ctypes.c_size_t
 F32, BF16 = 0, 1
 
 
@@ -33,6 +34,12 @@ def step(io, dk):
 
 def norm(io, C, G):
     return lib.lr_group_norm_act(p(), p(), p(), p(), p(), I(8), I(C), I(G), F(1e-5), 0, io, None)
+
+
+def hgrn2(io):
+    n = lib.lr_hgrn2_workspace_size(I(1), I(64), I(2), I(128), I(128), io)
+    return lib.lr_hgrn2_fwd(p(), p(), p(), p(), p(), p(), p(), I(1), I(64), I(2), I(128), I(128), I(64), io, p(),
+                            ctypes.c_size_t(n), None)
 
 
 # (call, its launches): one launch, segments, key columns in parts, both kernels
@@ -88,4 +95,21 @@ for i, (call, n) in enumerate(decay):
         fake.fake_fail_next_launch(k)
         assert run(call) == (-5, k - 1), (i, k)
     assert run(call) == (0, n), i
+""")
+
+
+def test_every_device_of_a_process(child):
+    """Limits on a kernel's shared memory are a device's own, and a device where
+    setting one failed is tried again."""
+    child("""
+for dev in (0, 3, 0, 1):
+    fake.fake_set_device(dev)
+    for i, (call, n) in enumerate(decay):
+        assert run(call) == (0, n), (dev, i)
+    for io in (BF16, F32):
+        assert hgrn2(io) == 0, (dev, io)
+for dev, call in ((4, decay[0][0]), (5, lambda: hgrn2(BF16)), (6, lambda: hgrn2(F32))):
+    fake.fake_set_device(dev)
+    fake.fake_fail_next_attribute()
+    assert call() == -5 and call() == 0, dev
 """)
