@@ -11,7 +11,8 @@ in the library's CUDA kernels:
   inputs to the current CUDA device and the outputs back (the end-to-end
   path); given device tensors they stay on the device.
 
-There is no fallback: if the library is missing this module raises at import.
+There is no fallback: if the library is missing this module raises at import (the
+extension module with the helpers' short path may be missing; a warning says so).
 """
 from __future__ import annotations
 
@@ -19,6 +20,7 @@ import ctypes
 import importlib.util
 import os
 import threading
+import warnings
 from typing import Optional, Tuple
 
 import torch
@@ -116,14 +118,29 @@ _lib = _load()
 LIB_PATH = _build.LIB_PATH
 
 
+class _NoTorchModule:
+    """In the place of an extension module that cannot be loaded: declines every
+    call, so that the helpers take their own path."""
+
+    @staticmethod
+    def _decline(*args):
+        return None
+
+    decay_attn = decay_attn_step = group_norm_act = _decline
+
+
 def _load_torch_module():
-    path = _build.TORCH_MODULE
-    if not os.path.exists(path):
-        raise ImportError(f"{path} is missing: build it with selective_state_space_chunked_gb300.build.build()")
-    spec = importlib.util.spec_from_file_location("_lrtorch", path)
-    mod = importlib.util.module_from_spec(spec)
-    spec.loader.exec_module(mod)
-    return mod
+    try:
+        if not _build.torch_module_matches():
+            raise ImportError("missing, or built against another torch")
+        spec = importlib.util.spec_from_file_location("_lrtorch", _build.TORCH_MODULE)
+        mod = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(mod)
+        return mod
+    except (ImportError, OSError) as e:
+        warnings.warn(f"{_build.TORCH_MODULE} cannot be used ({e}): calls of one token take longer; build it with "
+                      "selective_state_space_chunked_gb300.build.build()", RuntimeWarning)
+        return _NoTorchModule()
 
 
 # The helpers that run once per layer and token first offer their arguments to

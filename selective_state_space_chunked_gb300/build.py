@@ -4,8 +4,9 @@ Every translation unit under ``csrc/`` is compiled for sm_103a only
 (``-gencode arch=compute_103a,code=sm_103a``), in parallel, then linked into
 one shared library against the shared CUDA runtime.  ``csrc/lr_torch.cpp``, the
 short path of the torch helpers, becomes the extension module ``_build/_lrtorch``
-beside it, against the library and the installed torch.  The build is skipped
-when both are newer than every source and header.
+beside it, against the library and the installed torch, whose version is recorded.
+The build is skipped when both are newer than every source and header and torch is
+still that version.
 """
 from __future__ import annotations
 
@@ -27,6 +28,7 @@ LIB_NAME = "liblrscan.so"
 LIB_PATH = os.path.join(BUILD_DIR, LIB_NAME)
 TORCH_SRC = os.path.join(CSRC, "lr_torch.cpp")
 TORCH_MODULE = os.path.join(BUILD_DIR, "_lrtorch" + sysconfig.get_config_var("EXT_SUFFIX"))
+TORCH_VERSION = os.path.join(BUILD_DIR, "_lrtorch.torch")   # of the torch it was built against
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
@@ -45,6 +47,17 @@ def _torch_dir() -> str:
     return list(importlib.util.find_spec("torch").submodule_search_locations)[0]
 
 
+def torch_module_matches() -> bool:
+    """Whether the extension module is there and was built against the installed
+    torch (its C++ interface is that version's alone)."""
+    import torch
+    try:
+        with open(TORCH_VERSION) as f:
+            return f.read() == torch.__version__ and os.path.exists(TORCH_MODULE)
+    except OSError:
+        return False
+
+
 def _sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
@@ -56,7 +69,7 @@ def _deps():
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB_PATH) or not os.path.exists(TORCH_MODULE):
+    if not os.path.exists(LIB_PATH) or not torch_module_matches():
         return False
     t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(TORCH_MODULE))
     return all(os.path.getmtime(p) <= t for p in _deps())
@@ -98,12 +111,17 @@ def build(force: bool = False, verbose: bool = False) -> str:
             os.replace(tmp_lib, path)
 
         with cf.ThreadPoolExecutor(max_workers=max(1, min(8, os.cpu_count() or 1))) as ex:
-            *objs, torch_obj = ex.map(compile_one, [*_sources(), TORCH_SRC])
+            torch_obj = ex.submit(compile_one, TORCH_SRC)
+            objs = list(ex.map(compile_one, _sources()))
         link([nvcc, *ARCH, "-shared", "-cudart", "shared", *objs, "-Xlinker", "-rpath,/usr/local/cuda/lib64"],
              LIB_PATH)
-        link(["g++", "-shared", torch_obj, "-Wl,-rpath,$ORIGIN", "-L" + BUILD_DIR, "-l:" + LIB_NAME,
+        # the library stands without the module
+        link(["g++", "-shared", torch_obj.result(), "-Wl,-rpath,$ORIGIN", "-L" + BUILD_DIR, "-l:" + LIB_NAME,
               "-L" + os.path.join(torch_dir, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda",
               f"-L{cuda_dir}/lib64", "-lcudart"], TORCH_MODULE)
+        import torch
+        with open(TORCH_VERSION, "w") as f:
+            f.write(torch.__version__)
     finally:
         shutil.rmtree(tmpdir, ignore_errors=True)
     return LIB_PATH
