@@ -10,7 +10,8 @@
 // the call's own checks refused it; nothing has been launched then, and the helper
 // goes on to its own checks and conversions, which convert the argument or say what
 // is wrong.  Any other status comes back as an int, for the helper to raise: part of
-// the call may have run, and it may have updated a state in place.
+// the call may have run, and it may have updated a state in place.  The interpreter
+// is released for the allocations and the call: both may wait for the GPU.
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
@@ -102,9 +103,23 @@ struct Ref {
     }
 };
 
-PyObject *declined() {
-    PyErr_Clear();
-    Py_RETURN_NONE;
+// The interpreter released while it lives.
+struct Unlocked {
+    PyThreadState *state = PyEval_SaveThread();
+    Unlocked() = default;
+    Unlocked(const Unlocked &) = delete;
+    ~Unlocked() { PyEval_RestoreThread(state); }
+};
+
+// After a C++ exception: before the launch it is the helper's turn (an allocation
+// that failed: its own says so), after it there is nothing to try again.
+PyObject *thrown(bool launched) {
+    if (!launched) {
+        PyErr_Clear();
+        Py_RETURN_NONE;
+    }
+    if (!PyErr_Occurred()) PyErr_SetString(PyExc_RuntimeError, "the call ran, its results could not be returned");
+    return nullptr;
 }
 
 // What a call that was not LR_OK gives: None after the checks that come before
@@ -117,6 +132,7 @@ PyObject *refused(int rc) {
 // (q, k, v, H, Hk, a_log, g, S, S_out, scale) -> (o, S_new)
 PyObject *decay_attn_step(PyObject *, PyObject *const *args, Py_ssize_t n) {
     if (n != 10) Py_RETURN_NONE;
+    bool launched = false;
     try {
         Call c;
         Heads s;
@@ -133,29 +149,32 @@ PyObject *decay_attn_step(PyObject *, PyObject *const *args, Py_ssize_t n) {
             !c.take(args[7], at::kFloat, ss, true, &S_in) || !c.take(args[8], at::kFloat, ss, true, &S_out) ||
             !to_float(args[9], &scale))
             Py_RETURN_NONE;
-        const at::Tensor o = at::empty(vs, q->options());
-        at::Tensor Sn;
-        if (S_out == nullptr) {
-            Sn = at::empty(ss, q->options().dtype(at::kFloat));
-            S_out = Sn.data_ptr();
+        at::Tensor o, Sn;
+        int rc;
+        {
+            const Unlocked unlocked;
+            o = at::empty(vs, q->options());
+            if (S_out == nullptr) {
+                Sn = at::empty(ss, q->options().dtype(at::kFloat));
+                S_out = Sn.data_ptr();
+            }
+            launched = true;
+            rc = lr_decay_attn_step(q->data_ptr(), k, v, static_cast<float *>(a), g, scale, static_cast<float *>(S_in),
+                                    static_cast<float *>(S_out), o.data_ptr(), B, s.H, s.Hk, s.dk, s.dv, c.io,
+                                    c.stream());
         }
-        // every object is made before the launch, which may update S in place
-        const Ref po(THPVariable_Wrap(o)), ps(Sn.defined() ? THPVariable_Wrap(Sn) : Ref::share(args[8]));
-        Ref result(po.o && ps.o ? PyTuple_Pack(2, po.o, ps.o) : nullptr);
-        if (result.o == nullptr) return declined();
-        const int rc = lr_decay_attn_step(q->data_ptr(), k, v, static_cast<float *>(a), g, scale,
-                                          static_cast<float *>(S_in), static_cast<float *>(S_out), o.data_ptr(), B,
-                                          s.H, s.Hk, s.dk, s.dv, c.io, c.stream());
         if (rc != LR_OK) return refused(rc);
-        return Ref::share(result.o);
-    } catch (...) {   // an allocation that failed: the helper's own says so
-        return declined();
+        const Ref po(THPVariable_Wrap(o)), ps(Sn.defined() ? THPVariable_Wrap(Sn) : Ref::share(args[8]));
+        return po.o && ps.o ? PyTuple_Pack(2, po.o, ps.o) : nullptr;
+    } catch (...) {
+        return thrown(launched);
     }
 }
 
 // (q, k, v, H, Hk, a_log, g, S0, lens, scale) -> (o, S_final, workspace)
 PyObject *decay_attn(PyObject *, PyObject *const *args, Py_ssize_t n) {
     if (n != 10) Py_RETURN_NONE;
+    bool launched = false;
     try {
         Call c;
         Heads s;
@@ -174,24 +193,30 @@ PyObject *decay_attn(PyObject *, PyObject *const *args, Py_ssize_t n) {
             Py_RETURN_NONE;
         const size_t wsb = lr_decay_attn_workspace_size(B, L, s.H, s.Hk, s.dk, s.dv, c.io);
         if (wsb == 0 || wsb > size_t(INT64_MAX)) Py_RETURN_NONE;
-        const at::Tensor o = at::empty(vs, q->options()), Sf = at::empty(ss, q->options().dtype(at::kFloat)),
-                         ws = at::empty({static_cast<int64_t>(wsb)}, q->options().dtype(at::kByte));
-        const Ref po(THPVariable_Wrap(o)), ps(THPVariable_Wrap(Sf)), pw(THPVariable_Wrap(ws));
-        Ref result(po.o && ps.o && pw.o ? PyTuple_Pack(3, po.o, ps.o, pw.o) : nullptr);
-        if (result.o == nullptr) return declined();
-        const int rc = lr_decay_attn_fwd(q->data_ptr(), k, v, static_cast<float *>(a), g, static_cast<int32_t *>(lens),
-                                         scale, static_cast<float *>(S0), o.data_ptr(), Sf.data_ptr<float>(), B, L,
-                                         s.H, s.Hk, s.dk, s.dv, c.io, ws.data_ptr(), wsb, c.stream());
+        at::Tensor o, Sf, ws;
+        int rc;
+        {
+            const Unlocked unlocked;
+            o = at::empty(vs, q->options());
+            Sf = at::empty(ss, q->options().dtype(at::kFloat));
+            ws = at::empty({static_cast<int64_t>(wsb)}, q->options().dtype(at::kByte));
+            launched = true;
+            rc = lr_decay_attn_fwd(q->data_ptr(), k, v, static_cast<float *>(a), g, static_cast<int32_t *>(lens), scale,
+                                   static_cast<float *>(S0), o.data_ptr(), Sf.data_ptr<float>(), B, L, s.H, s.Hk, s.dk,
+                                   s.dv, c.io, ws.data_ptr(), wsb, c.stream());
+        }
         if (rc != LR_OK) return refused(rc);
-        return Ref::share(result.o);
+        const Ref po(THPVariable_Wrap(o)), ps(THPVariable_Wrap(Sf)), pw(THPVariable_Wrap(ws));
+        return po.o && ps.o && pw.o ? PyTuple_Pack(3, po.o, ps.o, pw.o) : nullptr;
     } catch (...) {
-        return declined();
+        return thrown(launched);
     }
 }
 
 // (x, G, gamma, beta, z, act code, eps, out) -> y
 PyObject *group_norm_act(PyObject *, PyObject *const *args, Py_ssize_t n) {
     if (n != 8) Py_RETURN_NONE;
+    bool launched = false;
     try {
         Call c;
         const at::Tensor *x = c.first(args[0]);
@@ -207,18 +232,21 @@ PyObject *group_norm_act(PyObject *, PyObject *const *args, Py_ssize_t n) {
             !c.take(args[4], c.type, x->sizes(), true, &z) || !c.take(args[7], c.type, x->sizes(), true, &out))
             Py_RETURN_NONE;
         at::Tensor y;
-        if (out == nullptr) {
-            y = at::empty(x->sizes(), x->options());
-            out = y.data_ptr();
+        int rc;
+        {
+            const Unlocked unlocked;
+            if (out == nullptr) {
+                y = at::empty(x->sizes(), x->options());
+                out = y.data_ptr();
+            }
+            launched = true;
+            rc = lr_group_norm_act(x->data_ptr(), z, static_cast<float *>(gamma), static_cast<float *>(beta), out,
+                                   x->numel() / C, C, G, eps, static_cast<lr_act>(act), c.io, c.stream());
         }
-        Ref result(y.defined() ? THPVariable_Wrap(y) : Ref::share(args[7]));
-        if (result.o == nullptr) return declined();
-        const int rc = lr_group_norm_act(x->data_ptr(), z, static_cast<float *>(gamma), static_cast<float *>(beta),
-                                         out, x->numel() / C, C, G, eps, static_cast<lr_act>(act), c.io, c.stream());
         if (rc != LR_OK) return refused(rc);
-        return Ref::share(result.o);
+        return y.defined() ? THPVariable_Wrap(y) : Ref::share(args[7]);
     } catch (...) {
-        return declined();
+        return thrown(launched);
     }
 }
 

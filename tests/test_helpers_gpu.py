@@ -1,7 +1,9 @@
 """The torch helpers of the decayed attention, its step and the group norm as a
 program calls them: views at any offset, calls that follow one another with nothing
-between, and errors."""
+between, an error that an earlier call left unread, and other Python threads."""
 import ctypes
+import threading
+import time
 
 import pytest
 import torch
@@ -147,3 +149,42 @@ def test_a_failed_launch_is_raised_not_repeated(lr, monkeypatch):  # noqa: F811
     with pytest.raises(lr.LrError):
         lr.group_norm_act(S, 2, out=S)
     assert torch.equal(S, p["S0"])
+
+
+# ---------------------------------------------------------------- threads
+def test_other_threads_run_while_a_launch_waits(lr):  # noqa: F811
+    """A launch onto a full queue waits for the GPU; Python's other threads do not.
+    The queue is held for 1.5 s by a host function that needs no interpreter."""
+    p = cuda(wl.decay_attn_inputs(1, 1, 2, 32, 32, 5, io="f32", with_S0=True))
+    args, S = tuple(t.contiguous() for t in step_args(p, 0)), p["S0"]
+    rt, libc = ctypes.CDLL("libcudart.so.13"), ctypes.CDLL(None)
+    s = torch.cuda.Stream()
+    stop, gaps = threading.Event(), [0.0]
+
+    def tick():
+        last = time.perf_counter()
+        while not stop.is_set():
+            time.sleep(0.002)
+            now = time.perf_counter()
+            gaps[0] = max(gaps[0], now - last)
+            last = now
+
+    with torch.cuda.stream(s):
+        lr.decay_attn_step(*args, 2, S=S, S_out=S)
+        s.synchronize()
+        th = threading.Thread(target=tick)
+        th.start()
+        try:
+            fn = ctypes.cast(libc.usleep, ctypes.c_void_p)
+            assert rt.cudaLaunchHostFunc(ctypes.c_void_p(s.cuda_stream), fn, ctypes.c_void_p(1500000)) == 0
+            t0 = time.perf_counter()
+            for _ in range(4000):
+                lr.decay_attn_step(*args, 2, S=S, S_out=S)
+            waited = time.perf_counter() - t0
+        finally:
+            stop.set()
+            th.join()
+        s.synchronize()
+    if waited < 1.0:
+        pytest.skip("the queue took every launch")
+    assert gaps[0] < 0.5
