@@ -3,7 +3,8 @@
 // Log decays are summed in fixed point: a step's log2 decay becomes a 64-bit
 // integer in units of 2^-32, so sums over any range are exact and do not
 // depend on how the sequence is cut, and a reset (a decay of 0) does not eat
-// the precision of the differences after it.
+// the precision of the differences after it (2^-17 in a steep chunk's scores,
+// whose exponents are kept in units of 2^-16).
 #pragma once
 
 #include "lr_decay.h"
@@ -47,6 +48,12 @@ __device__ __forceinline__ long long to_fix(float l, bool &bad) {
 __device__ __forceinline__ float fix_f(long long x) {
     return fmaf(static_cast<float>(static_cast<uint32_t>(x)), kFixInv, static_cast<float>(static_cast<int>(x >> 32)));
 }
+
+// An exponent of a chunk of 128 steps in units of 2^-16 (128 floors of -200.6 are above
+// -2^15), so that a difference of two is exact however many resets lie before
+// both; and one, or a difference, as a float.
+__device__ __forceinline__ int units_of(long long x) { return static_cast<int>((x + (1 << 15)) >> 16); }
+__device__ __forceinline__ float units_f(int u) { return 1.52587890625e-5f * static_cast<float>(u); }
 
 // 2^x of a fixed-point exponent, for x below 127: 2^fraction times 2^integer,
 // so the result is as exact for large exponents as for small ones (these

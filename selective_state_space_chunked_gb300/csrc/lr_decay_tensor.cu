@@ -104,7 +104,7 @@ constexpr uint32_t OFF_W = OFF_V + 2 * V_BYTES;     // three terms [128 s][64 i]
 constexpr uint32_t OFF_SB = OFF_W + 3 * V_BYTES;    // bf16 state [128 j][64 i]
 constexpr int NM = 4;                               // chunks whose factors are held
 constexpr uint32_t OFF_WT = OFF_SB + 128 * RB * 2;  // NM x [128] fp32: w
-constexpr uint32_t OFF_L = OFF_WT + NM * C * 4;     // [128] fp32: L of the last steep chunk
+constexpr uint32_t OFF_L = OFF_WT + NM * C * 4;     // [128] int: L of the last steep chunk, see units_of
 // NM x (m: the state's factor, steep: the readout's base, 0 in a steep chunk, -)
 constexpr uint32_t OFF_F = OFF_L + C * 4;
 constexpr uint32_t OFF_BAR = OFF_F + NM * 16;
@@ -683,8 +683,8 @@ __global__ void __launch_bounds__(dt::THREADS, 1)
     uint64_t *bar = reinterpret_cast<uint64_t *>(sm + OFF_BAR);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + OFF_TMEM);
     Ctl *ctl = reinterpret_cast<Ctl *>(sm + OFF_CTL);
-    float *sW = reinterpret_cast<float *>(sm + OFF_WT), *sL = reinterpret_cast<float *>(sm + OFF_L),
-          *sF = reinterpret_cast<float *>(sm + OFF_F);
+    float *sW = reinterpret_cast<float *>(sm + OFF_WT), *sF = reinterpret_cast<float *>(sm + OFF_F);
+    int *sL = reinterpret_cast<int *>(sm + OFF_L);
     if (tid == 0) {
         for (int i = 0; i < NBAR; ++i) {
             int n = 1;
@@ -876,9 +876,9 @@ __global__ void __launch_bounds__(dt::THREADS, 1)
                 ok = last < 0 || c - last >= NM || hw(M_FREE + (last & (NM - 1)), last / NM);
                 if (!__all_sync(0xffffffffu, ok)) break;
                 last = c;
-                *reinterpret_cast<float4 *>(sL + 4 * lane) =
-                    make_float4(dec::fix_f(before + cum[0]), dec::fix_f(before + cum[1]), dec::fix_f(before + cum[2]),
-                                dec::fix_f(before + cum[3]));
+                *reinterpret_cast<int4 *>(sL + 4 * lane) =
+                    make_int4(dec::units_of(before + cum[0]), dec::units_of(before + cum[1]),
+                              dec::units_of(before + cum[2]), dec::units_of(before + cum[3]));
             }
             *reinterpret_cast<float4 *>(sW + (c & (NM - 1)) * C + 4 * lane) = make_float4(wv[0], wv[1], wv[2], wv[3]);
             if (lane == 0)
@@ -979,8 +979,8 @@ __global__ void __launch_bounds__(dt::THREADS, 1)
                     tmem_st8_nowait(P + 8 * kb, r);
                 }
             } else {   // a steep chunk
-                const float *f = sL + 64 * hf;
-                const float lt = sL[t];
+                const int *f = sL + 64 * hf;
+                const int lt = sL[t];
 #pragma unroll 1
                 for (int kb = 0; kb < 4; ++kb) {
                     float p[16];
@@ -990,9 +990,9 @@ __global__ void __launch_bounds__(dt::THREADS, 1)
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
                         const int s = 16 * kb + 2 * e;
-                        const float2 ls = *reinterpret_cast<const float2 *>(f + s);
-                        r[e] = pack(s < n ? p[2 * e] * ex2_approx(lt - ls.x) : 0.0f,
-                                    s + 1 < n ? p[2 * e + 1] * ex2_approx(lt - ls.y) : 0.0f);
+                        const int2 ls = *reinterpret_cast<const int2 *>(f + s);
+                        r[e] = pack(s < n ? p[2 * e] * ex2_approx(dec::units_f(lt - ls.x)) : 0.0f,
+                                    s + 1 < n ? p[2 * e + 1] * ex2_approx(dec::units_f(lt - ls.y)) : 0.0f);
                     }
                     tmem_st8_nowait(P + 8 * kb, r);
                 }
@@ -1019,7 +1019,7 @@ __global__ void __launch_bounds__(dt::THREADS, 1)
             if (f.z == 0.0f) {   // steep: rows of Q S^T by 2^(base + L) before PD V is added
                 if (!__all_sync(0xffffffffu, hw(OX_DONE + st, c >> 1))) break;
                 tc_fence_after();
-                const float e = exp2f(f.y + sL[row]);
+                const float e = exp2f(f.y + dec::units_f(sL[row]));
 #pragma unroll 1
                 for (int q = 0; q < RB; q += 16) {
                     float d[16];

@@ -1,6 +1,6 @@
 """Values at the edges of the decayed linear attention, in steps that belong to a
-row, against the float64 oracle: infinities and NaN, and values whose scaled form
-leaves fp32.  Tolerances of finite values: see
+row, against the float64 oracle: infinities and NaN, values whose scaled form
+leaves fp32, and slow steps behind many resets.  Tolerances of finite values: see
 test_decay_attn_gpu; that a value is finite, and in the state whether it is an
 infinity and of which sign, has no tolerance."""
 import numpy as np
@@ -99,3 +99,24 @@ def test_values_far_from_one(lr, d, e):  # noqa: F811
     p["a_log"] = torch.tensor([-0.1, -0.003])
     p["v"], p["S0"] = p["v"] * 2.0 ** e, p["S0"] * 2.0 ** e
     check(lr, p, "bf16")
+
+
+def test_slow_steps_behind_many_resets(lr):  # noqa: F811
+    """100 resets, then slow steps, in one chunk.  One step has a value and q.k = 1,
+    so o_t is the decay factor alone, rounded to bf16 once as a score (the store
+    changes nothing more): the rounding of a factor within 2^-14 of the exact one."""
+    B, H, L = 4, 8, 128
+    q = torch.zeros(B, L, H * 64)
+    q[..., ::64] = 1.0
+    v = torch.zeros(B, L, H * 64)
+    v[:, 100] = 1.0
+    gen = torch.Generator().manual_seed(1)
+    g = -0.05 * torch.rand(B, L, H, generator=gen)
+    g[:, :100] = -float("inf")
+    p = {"q": q.bfloat16(), "k": q.bfloat16(), "v": v.bfloat16(), "g": g.bfloat16(), "a_log": None, "S0": None,
+         "H": H, "Hk": H}
+    o, _ = check(lr, p, "bf16")
+    want, _ = oracle.decay_attn(p["q"], p["k"], p["v"], H, g=p["g"])
+    low, high = (torch.tensor(want * (1 + e)).bfloat16() for e in (-2.0 ** -14, 2.0 ** -14))
+    o = o.cpu()
+    assert torch.all((low <= o) & (o <= high))
