@@ -288,14 +288,17 @@ __global__ void __launch_bounds__(C::NT, C::BPS)
     if (seg == 0 && a.S0 != nullptr) add_state(a.S0 + size_t(bh) * dv * dk, 1.0f);
     if (!STATE_ONLY && seg > 0) {   // the decayed sum of the ranges before this one
         long long acc = 0;
-        for (int s = seg - 1; s >= 0; --s) {
+        int s = seg - 1;
+        for (; s >= 0; --s) {
             const float f = dec::exp2_fix(acc);
-            // nothing is left of the ranges before, unless it is not finite
-            if (f == 0.0f && !dec::any_bad(a, bh, s, rb)) break;
+            if (f == 0.0f) break;
             const size_t at = size_t(bh) * (a.n_seg - 1) + s;
             add_state(a.seg_state + at * dv * dk, f);
             acc = max(acc + a.seg_tot[at], -(1ll << 60));
         }
+        // nothing is left of the ranges before, unless it is not finite
+        if (s >= 0 && dec::any_bad(a, bh, s, rb))
+            for (; s >= 0; --s) add_state(a.seg_state + (size_t(bh) * (a.n_seg - 1) + s) * dv * dk, 0.0f);
     }
     if (STATE_ONLY) launch_dependents();
 
