@@ -104,14 +104,16 @@ int decay_attn_launch(DecayArgs a, lr_dtype io, const DecayPlan &p, void *worksp
     a.seg_state = reinterpret_cast<float *>(ws + tot_bytes(segs) + bad_bytes(segs, p));
     a.seg_tiles = p.tiles;
     a.parts = p.parts;
-    // Ragged rows by falling length where the blocks are more than the SMs (bf16,
-    // lengths spread evenly: B8 L1017 H32 d64 46.4 -> 40.7 us, B16 L2048 H16 d128
-    // 139 -> 127, B64 L1024 H4 d64 48.7 -> 41.9, but B32 L500 H8 d128 63 -> 65; fp32
-    // B16 L1024 H16 d128 408 -> 353).  With fewer there is nothing to gain (B3 L3000
-    // H4 36.4 -> 37.8).
+    // Ragged rows by falling length where the blocks are more than the SMs hold at once.
+    // Lengths drawn evenly: bf16 B8 L1017 H32 d64 47.6 -> 38.7 us, B16 L2048 H16 d128
+    // 146 -> 140, B64 L1024 H4 d64 47.0 -> 42.6, but B32 L500 H8 d128 61.8 -> 63.0; fp32
+    // B64 L500 H8 d64 167 -> 109, B32 L300 H32 d128 353 -> 294.  Blocks that all run at
+    // once are slower so, with the long ones side by side on the same SMs (fp32 B16
+    // L1024 H16 d128 392 -> 428, 386 -> 476 with lengths that rise along the batch).
     int sms = 0;
     if (device_sm_count(&sms) != LR_OK) return LR_ERR_CUDA;
-    a.by_length = a.lens != nullptr && a.B > 1 && a.B <= kOrderRows && p.blocks > sms;
+    const int64_t at_once = int64_t(sms) * (p.path == 1 ? 1 : a.dk <= 64 ? 8 : a.dk <= 128 ? 4 : 3);
+    a.by_length = a.lens != nullptr && a.B > 1 && a.B <= kOrderRows && p.blocks > at_once;
     a.o_part = a.seg_state + segs * a.dv * a.dk;
     const StatusRef st = call_status(workspace);
     if (p.path == 1) return decay_tensor_launch(a, st, stream);
