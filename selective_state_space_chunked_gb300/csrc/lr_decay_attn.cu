@@ -12,10 +12,12 @@ namespace {
 // 19 (chosen) 1304, 24 1490; few heads: B1 L8192 H1 d128 32 114, 64 (chosen) 72, 96
 // 88; B1 L4096 H2 d64 32 57, 45 (chosen) 47, 64 68.
 // Calls in one segment whose narrow blocks (one state row a thread) are no more
-// than four per SM take those.  L100 d128 fp32: H4 21.5 us against 28.3, H16 22.3
-// against 28.1, H32 28.3 on either, H64 55 against 28; bf16 L32 H4 8.2 against 11.1.
-// dk 256: fp32 H8 23.6 against 29.3, but bf16 L32 24.2 against 12.1, and dk 512 fp32
-// 98 against 41.
+// than four per SM, with fp32 I/O and more than 64 keys three, take those.  L100 fp32:
+// d128 H4 20.2 us against 28.2, H16 21.0 against 28.5, H28 23.5 against 28.2, H32 32.8
+// against 28.2; d64 H16 15.0 against 20.1, H76 19.5 against 20.2; dk 256 H12 24.7
+// against 27.4, H16 44.0 against 27.5.  bf16 L32 d128: H4 8.0 against 11.0, H32 8.5
+// against 10.6.  (At dk 256, bf16 L32 24.2 against 12.1, and at dk 512, fp32 98
+// against 41, when the narrow form came in.)
 constexpr int64_t kGenMinSeg = 64;
 constexpr double kGenBlockCost = 40.0, kGenStateCost = 3.0, kGenLaunchCost = 50.0;
 constexpr int64_t kGenMaxSeg = 96;
@@ -81,7 +83,8 @@ int decay_plan(int64_t B, int64_t L, int64_t H, int64_t Hk, int64_t dk, int64_t 
             if (t < best) best = t, n = s;
         }
         const int64_t nrows = decay_general_rows(dk, true);
-        p->narrow = n == 1 && dk <= (io == LR_BF16 ? 128 : 256) && B * H * ((dv + nrows - 1) / nrows) <= 4 * sms;
+        const int64_t narrow_per_sm = io == LR_BF16 || dk <= 64 ? 4 : 3;
+        p->narrow = n == 1 && dk <= (io == LR_BF16 ? 128 : 256) && B * H * ((dv + nrows - 1) / nrows) <= narrow_per_sm * sms;
     }
     p->seg_len = ((L + n - 1) / n + unit - 1) / unit * unit;
     p->n_seg = int((L + p->seg_len - 1) / p->seg_len);
