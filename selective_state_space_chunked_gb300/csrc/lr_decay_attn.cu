@@ -7,10 +7,10 @@ namespace {
 // CUDA-core kernel: the shortest segment, and costs in units of a step of a
 // block: a block's start, one segment's state read by a later one, and the
 // second launch.  Chosen on sweeps of the segment count over 20 shapes.  fp32
-// H16 d128 (of a kernel 5 % slower), B2 L2048: 4 segments 271 us, 7 242, 9 (chosen)
-// 210, 12 246; B4 L4096: 1 999, 4 748, 9 (chosen) 682, 14 690; B1 L32768: 9 1821,
-// 19 (chosen) 1304, 24 1490; few heads: B1 L8192 H1 d128 32 114, 64 (chosen) 72, 96
-// 88; B1 L4096 H2 d64 32 57, 45 (chosen) 47, 64 68.
+// H16 d128, B2 L2048: 4 segments 263 us, 7 232, 9 (chosen) 202, 12 245; B4 L4096: 1
+// 1060, 4 726, 9 (chosen) 668, 14 681; B1 L32768: 9 1791, 19 (chosen) 1267, 24 1484;
+// few heads: B1 L8192 H1 d128 32 116, 64 (chosen) 73.5, 96 93; B1 L4096 H2 d64 32
+// 48.6, 41 (chosen) 48.6, 45 59, 64 50.
 // Calls in one segment whose narrow blocks (one state row a thread) are no more
 // than four per SM, with fp32 I/O and more than 64 keys three, take those.  L100 fp32:
 // d128 H4 20.2 us against 28.2, H16 21.0 against 28.5, H28 23.5 against 28.2, H32 32.8
@@ -22,14 +22,14 @@ constexpr int64_t kGenMinSeg = 64;
 constexpr double kGenBlockCost = 40.0, kGenStateCost = 3.0, kGenLaunchCost = 50.0;
 constexpr int64_t kGenMaxSeg = 96;
 // Tensor-core kernel: the shortest sequence it takes (bf16, on it and on the CUDA
-// cores: B1 L48 H4 d128 10.7 and 11.7 us, L32 10.5 and 8.2; B4 L48 H32 d64 11.0 and
-// 14.4; B1 H8 dk256, L48 13.1 and 16.2, L32 13.2 and 12.1; the other way, B8 L48 H16
-// d128 21.9 and 19.1), and costs in units of a chunk's time: a chunk of the first
+// cores: B1 L48 H4 d128 9.6 and 10.9 us, L32 9.7 and 8.1; B4 L48 H32 d64 10.8 and
+// 11.4; B1 H8 dk256, L48 12.0 and 15.2, L32 12.0 and 10.8; the other way, B8 L48 H16
+// d128 21.4 and 19.1), and costs in units of a chunk's time: a chunk of the first
 // launch, a block's start, and one segment's state read by a later one.  Against
 // sweeps of the segment count over 11 shapes the plan's choice is the best or
-// within 3 %: B1 L32768 H16 d128 1 segment 582 us, 2 447, 4 (chosen) 238, 8 256;
-// B1 L16384 H8 dk64 6 84, 8 69, 9 (chosen) 66, 12 95; B4 L2048 H16 1 (chosen) 49.5,
-// 2 74.
+// within 4 %: B1 L32768 H16 d128 1 segment 571 us, 2 433, 4 (chosen) 234, 8 274;
+// B1 L16384 H8 dk64 6 81, 9 60, 12 50.5, 16 (chosen) 47.0, 19 45.4, 24 68; B4 L2048
+// H16 1 (chosen) 48.4, 2 76.
 constexpr int64_t kMaxSeg = 32;
 constexpr int64_t kTensorMinLen = 48;
 constexpr double kFirstCost = 0.6, kBlockCost = 3.0, kStateCost = 1.0;
@@ -107,16 +107,16 @@ int decay_attn_launch(DecayArgs a, lr_dtype io, const DecayPlan &p, void *worksp
     a.seg_state = reinterpret_cast<float *>(ws + tot_bytes(segs) + bad_bytes(segs, p));
     a.seg_tiles = p.tiles;
     a.parts = p.parts;
-    // Ragged rows by falling length where the blocks are more than the SMs hold at once.
-    // Lengths drawn evenly: bf16 B8 L1017 H32 d64 47.6 -> 38.7 us, B16 L2048 H16 d128
-    // 146 -> 140, B64 L1024 H4 d64 47.0 -> 42.6, but B32 L500 H8 d128 61.8 -> 63.0; fp32
-    // B64 L500 H8 d64 167 -> 109, B32 L300 H32 d128 353 -> 294.  Blocks that all run at
-    // once are slower so, with the long ones side by side on the same SMs (fp32 B16
-    // L1024 H16 d128 392 -> 428, 386 -> 476 with lengths that rise along the batch).
+    // Ragged rows by falling length, lengths drawn evenly (us in the batch's order, by
+    // length).  Tensor cores, more blocks than SMs: bf16 B8 L1017 H32 d64 47.6, 38.7;
+    // B16 L2048 H16 d128 146, 140; B64 L1024 H4 d64 47.0, 42.6; but B32 L500 H8 d128
+    // 61.8, 63.0.  CUDA cores, more than four blocks per SM: fp32 B64 L500 H8 d64 (6.7)
+    // 167, 109; B32 L300 H32 d128 (13.5) 353, 294.  With fewer, the long rows stand
+    // beside one another on some SMs: B16 L1024 H16 d128 (3.4) 392, 428, and 386, 476
+    // with lengths that rise along the batch; B8 L1017 H32 d64 (3.4) 175, 179.
     int sms = 0;
     if (device_sm_count(&sms) != LR_OK) return LR_ERR_CUDA;
-    const int64_t at_once = int64_t(sms) * (p.path == 1 ? 1 : a.dk <= 64 ? 8 : a.dk <= 128 ? 4 : 3);
-    a.by_length = a.lens != nullptr && a.B > 1 && a.B <= kOrderRows && p.blocks > at_once;
+    a.by_length = a.lens != nullptr && a.B > 1 && a.B <= kOrderRows && p.blocks > (p.path == 1 ? 1 : 4) * sms;
     a.o_part = a.seg_state + segs * a.dv * a.dk;
     const StatusRef st = call_status(workspace);
     if (p.path == 1) return decay_tensor_launch(a, st, stream);
