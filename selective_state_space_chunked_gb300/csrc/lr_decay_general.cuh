@@ -22,8 +22,8 @@
 //
 // The work is 2 dk dv fp32 fused multiply-adds per token and head and, in the
 // n - 1 of n segments that the first launch runs, dk dv more.  Measured (fp32,
-// H16 d128): B2 L2048 200 us, 9 segments, 3.1 G fused multiply-adds, 41 % of
-// the fp32 pipes' rate; B4 L4096 664 us; B1 L32768 1266 us.  The packed fp32 pipe
+// H16 d128): B2 L2048 201 us, 9 segments, 3.1 G fused multiply-adds, 41 % of
+// the fp32 pipes' rate; B4 L4096 668 us; B1 L32768 1267 us.  The packed fp32 pipe
 // is busy 53-55 % of the time the SMs are; the rest goes to the latency of a step
 // (its loads from shared memory, the chains of dependent sums, the sums over
 // lanes), which four warps per scheduler do not cover, and to the last blocks.
@@ -33,6 +33,12 @@
 //   two steps unrolled: 200 against 204; four: 213
 //   two steps' sums over lanes taken together: 210 against 205 (spills)
 //   blocks of 256 threads: 211 against 205; three blocks per SM: 266 against 204
+// (each pair measured on the kernel of its time)
+//
+// Infinities and NaN go through the state as the recurrence takes them.  A segment
+// says whether the state it leaves is finite (seg_bad), so that a later one does not
+// pass over an infinity whose decay factor is 0.  S^ is up to 2^48 times S, so a
+// state past 2^79 may overflow.
 #pragma once
 
 #include "lr_decay.cuh"

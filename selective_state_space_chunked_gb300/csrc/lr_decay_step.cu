@@ -7,9 +7,9 @@
 // row, each holding groups of four consecutive keys; a warp has its R rows'
 // loads in flight before the first is used.  fp32 throughout; o is rounded once.
 //
-// Measured back to back in one graph, state larger than L2 (bf16 H16 d128): B64
-// 22.6 us, 88 % of the copy bandwidth; B32 12.9; B8 5.3; B1 2.5.  fp32 B32 H16
-// dk256 dv128 21.2 us, 93 %.
+// Measured back to back in one graph, states in turn (bf16 H16 d128): B64 22.1 us,
+// 90 % of the copy bandwidth; B32 12.5; B8 4.6; B1 2.35.  fp32 B32 H16 dk256 dv128
+// 21.2 us, 93 %.
 //   four rows of a warp in flight against one: B64 23 us against 35, B8 5.4
 //   against 6.2; at B1, where it leaves fewer warps, 2.4 against 2.3.  Eight: B64
 //   22.6 against 23.2, but B1 3.1
@@ -20,7 +20,7 @@
 //   launched while the kernel before it drains (the kernel waits for that one's
 //   results): calls one after another B64 24.6 -> 22.5 us, B8 7.8 -> 5.6; a step and
 //   a gated norm at B8 H16 d128 10.3 -> 7.5
-//   dk up to 512 in the same form: B32 H16 dk192 16.9 us against 36 with a row
+//   dk up to 512 in the same form: B32 H16 dk192 18.7 us against 36 with a row
 //   read element by element, which stays for dk that is no multiple of four
 #include "lr_decay.cuh"
 

@@ -52,9 +52,10 @@
 // another and o_t = sum over j of S_t[:, j] q_t[j], so each 128 of them run as a
 // recurrence of their own, in blocks of their own, and a last launch adds their
 // fp32 outputs and rounds the sum.  The scores' products with V are repeated by
-// every part; at B2 L1500 H8 dk256 dv128 48 us against 178 on the CUDA cores, B4
-// L4096 H16 dk256 dv128 265 against 1528, B4 L1024 H8 dk512 dv128 80 against 387,
-// B1 L64 H4 dk192 dv64 17 against 56.
+// every part; at B2 L1500 H8 dk256 dv128 48 us against 169 on the CUDA cores, B4
+// L4096 H16 dk256 dv128 262 against 1528, B4 L1024 H8 dk512 dv128 76 against 387,
+// B1 L64 H4 dk192 dv64 12 against 56 (the last three of the CUDA cores as measured
+// when the parts came in).
 // TMEM: P 2 x 128 columns (PD inside), O 64, dS 3 x 64: all 512.
 // Infinities and NaN.  The products take a masked score as 0, and 0 v_s is no 0
 // where v_s is not finite; the terms of an infinity, and finite values past about
@@ -68,11 +69,13 @@
 // role's code unrolled the warps waited for instruction fetches more than for
 // anything else (95 us against 90 at B4 L4096 H16 d128 for the last part of it).
 //
-// Measured (d128, H16): B4 L4096 86 us, 273 MB and 17 GFLOP, 47 % of the copy
-// bandwidth and 10 % of the tensor peak; B1 L32768 236 us in four segments; B1 L77
-// 9.9.  d64: B8 L1017 H32, ragged, 38-45.  No pipe is near its limit (tensor 36 %
-// busy, issue 45 %, DRAM 37 %): a chunk takes about 2.7 us, the chain of its
-// hand-overs, with one block per SM, which its operands (224 KB) and TMEM fill.
+// Measured (d128, H16): B4 L4096 86.5 us, 273 MB and 17 GFLOP, 47 % of the copy
+// bandwidth and 10 % of the tensor peak, 110.5 us with steep chunks alone; B1 L32768
+// 235-243 us in four segments; B1 L77 9.8.  d64: B8 L1017 H32, ragged, 38-47.  No pipe
+// is near its limit (over all SMs tensor 28 % busy, issue 36 %, DRAM 36 %): a chunk
+// takes about 2.7 us, the chain of its hand-overs, with one block per SM, which its
+// operands (227 KB) and TMEM fill.  At 64 registers a thread 100 bytes spill (120 with
+// parts); a variant that spilled 40 took 88 us.
 // 128-step chunks rather than 64 halve the hand-overs; 64 value rows rather than
 // 128 make twice the blocks.  Measured against 91 us and not taken: P and dS issued
 // by one warp 98, weights by eight warps or by half chunks 98-100, one warp polling
@@ -339,8 +342,8 @@ __device__ __noinline__ void redo_call(const DecayArgs &a, int b, int n_vt, unsi
 //   dS = K^T diag(w) V
 // runs through all chunks in one accumulator, with nothing read back between
 // them.  The total decay comes first, from a sum over the segment's gates.
-// Measured: B1 L16384 H16 d128, three of four segments, 46 us, 29 % of the DRAM
-// rate and 30 % of the tensor pipe, bound by the weights' chain; the second
+// Measured: B1 L16384 H16 d128, three of four segments, 43 us, 30 % of the DRAM
+// rate and 18 % of the tensor pipe, bound by the weights' chain; the second
 // launch's code, used for both before, took 280 us against 254 at B1 L32768 in all.
 // Roles: TMA (K, V three chunks deep), scan (4 warps, a step per lane: weights
 // of the next chunks), weight (8 warps: the three terms of w_s v_s, half chunks
@@ -1203,7 +1206,8 @@ __global__ void __launch_bounds__(dt::THREADS, 1)
 
 // o = the parts' sum, rounded once; steps past a row's length are 0.  A block
 // takes whole steps (all heads of one token).  Launched while the parts drain: B1
-// L100 H8 dk256 13.0 us against 15.3, B2 L1500 H8 dk256 49.4 against 51.5.  It lets
+// L100 H8 dk256 13.0 us against 15.3, B2 L1500 H8 dk256 49.4 against 51.5 (11.9 and
+// 48.0 now).  It lets
 // nothing start before its own end (B4 L4096 H16 dk256 277 us against 270: the next
 // call's blocks would take the SMs that it still needs).
 __global__ void __launch_bounds__(256) decay_parts_kernel(const DecayArgs a) {

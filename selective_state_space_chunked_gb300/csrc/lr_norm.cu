@@ -7,14 +7,16 @@
 // kernel.  A group stays in the registers of the lanes that share it: the
 // mean, then the centred squares (no cancellation), then the output.
 //
-// Measured, inputs larger than L2 (share of the copy bandwidth): bf16 16384 x
-// 2048, G 16, gate 33.0 us (90 %); fp32 62 us (95 %); bf16 8192 x 4096, G 32 24.5
-// us (81 %); fp32 3001 x 1920, G 24 8.45 us (80 %); bf16 8192 x 4096, G 2, gate
-// 35.5 us (84 %; element by element 82 us).  Sums and the affine step in packed
-// fp32 pairs: the first 38.4 -> 36.7 us at the time.
+// Measured in a graph of calls, 600 MB of inputs and outputs in turn (share of the copy
+// bandwidth): bf16 16384 x 2048, G 16, gate 34.8 us (85 %; 32.4 onto one output
+// tensor, half of which stays in L2); fp32 62.3 us (95 %); bf16 8192 x 4096, G 32
+// 24.5 us (81 %); fp32 3001 x 1920, G 24 9.5 us (72 %; 7.5 onto one output); bf16 8192 x
+// 4096, G 2, gate 36.2 us (82 %; element by element 82 us).  Sums and the affine step in
+// packed fp32 pairs: the first 38.4 -> 36.7 us at the time.
 //
-// Launched while the kernel before it drains: calls one after another 35.0 -> 33.0 us
-// for the first, 10.5 -> 8.4 for 3001 x 1920.
+// The figures at the variants below were taken onto one output.  Launched while the
+// kernel before it drains: calls one after another 35.0 -> 33.0 us for the first, 10.5
+// -> 8.4 for 3001 x 1920, so measured.
 //
 //   lanes   groups of up to 128 vectors (16 bytes; 8 for a bf16 group of an odd
 //           number of those): TL lanes of a warp hold a group, up to four vectors
@@ -30,7 +32,7 @@ namespace lr {
 namespace {
 
 // silu in fp32: x / (1 + e^-x).  The fast division gives 0 for divisors past
-// 2^126, where the quotient is 0 to fp32.
+// 2^126, where the quotient is below 1.2e-36.
 __device__ __forceinline__ float silu_f(float x) { return __fdividef(x, 1.0f + ex2_approx(-x * kLog2e)); }
 __device__ __forceinline__ float2 pair(const float *v) { return make_float2(v[0], v[1]); }
 
