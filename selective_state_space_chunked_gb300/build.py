@@ -115,7 +115,9 @@ def build(force: bool = False, verbose: bool = False) -> str:
             objs = list(ex.map(compile_one, _sources()))
         link([nvcc, *ARCH, "-shared", "-cudart", "shared", *objs, "-Xlinker", "-rpath,/usr/local/cuda/lib64"],
              LIB_PATH)
-        # the library stands without the module
+        # the library stands without the module, and no longer goes with an older one
+        if os.path.exists(TORCH_VERSION):
+            os.unlink(TORCH_VERSION)
         link(["g++", "-shared", torch_obj.result(), "-Wl,-rpath,$ORIGIN", "-L" + BUILD_DIR, "-l:" + LIB_NAME,
               "-L" + os.path.join(torch_dir, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda",
               f"-L{cuda_dir}/lib64", "-lcudart"], TORCH_MODULE)

@@ -53,3 +53,20 @@ def test_a_module_of_another_torch_is_neither_used_nor_up_to_date(tmp_path, monk
     assert not build.up_to_date()
     monkeypatch.setattr(build, "TORCH_VERSION", str(tmp_path / "none"))
     assert not build.up_to_date()
+
+
+def test_a_build_that_fails_at_the_module_leaves_the_library_and_no_older_module(tmp_path, monkeypatch):
+    import torch
+    for name in ("LIB_PATH", "TORCH_MODULE", "TORCH_VERSION"):
+        monkeypatch.setattr(build, name, str(tmp_path / name))
+    monkeypatch.setattr(build, "BUILD_DIR", str(tmp_path))
+    (tmp_path / "TORCH_MODULE").write_text("the last build's")
+    (tmp_path / "TORCH_VERSION").write_text(torch.__version__)
+    assert build.torch_module_matches()
+
+    def run(cmd, **kw):   # every CUDA file compiles and links, the module does not
+        return subprocess.CompletedProcess(cmd, 1 if cmd[0] == "g++" else 0, "", "no")
+    monkeypatch.setattr(build.subprocess, "run", run)
+    with pytest.raises(RuntimeError):
+        build.build(force=True)
+    assert (tmp_path / "LIB_PATH").exists() and not build.torch_module_matches()
