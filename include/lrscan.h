@@ -351,6 +351,78 @@ int lr_group_norm_act(const void *x, const void *z, const float *gamma,
                       float eps, lr_act act, lr_dtype io, lr_stream_t stream);
 
 /* ------------------------------------------------------------------------ */
+/* Short causal convolution, channels last                                   */
+/* ------------------------------------------------------------------------ */
+
+/*
+ * The convolution that stands before a selective layer's scan: every channel with
+ * its own W taps (the source pages have no counterpart).
+ *
+ *   y_t[b,c] = act(bias[c] + sum_{j < W} w[c,j] x_{t - W + 1 + j}[b,c])
+ *
+ * for t < lens[b].  Inputs before a row's first step come from its state, the
+ * W - 1 inputs before it, oldest first (state == NULL: zeros); state_out gets the
+ * row's last W - 1 inputs, those of the state among them where the row is shorter.
+ * y_t is 0 for t >= lens[b], whatever x holds there.  lens == NULL: every row has
+ * L steps; values outside [0, L] are clamped to it.  An infinity or a NaN reaches
+ * the W outputs that it is an input of.
+ *
+ * Layouts: x: (B, L, C) in `io`, its B L rows ldx elements apart (a slice of a wider
+ *          tensor; ldx == C: dense); w: (C, W) fp32; bias: (C) fp32; lens: (B) int32;
+ *          state, state_out: (B, W - 1, C) in `io` (inputs, so exact); y: (B, L, C).
+ * Optional: bias, state, lens, state_out.  state_out may be state itself; other
+ *          outputs must not overlap inputs.
+ * Requirements: B, L, C >= 0, W >= 2, ldx >= C, act one of lr_act (else
+ *          LR_ERR_INVALID_ARG); W <= 4 (else LR_ERR_UNSUPPORTED).  No workspace.
+ *          Whole 16-byte vectors are moved where C and ldx are multiples of them.
+ */
+int lr_causal_conv_fwd(const void *x, int64_t ldx, const float *w, const float *bias,
+                       const void *state, const int32_t *lens, void *y, void *state_out,
+                       int64_t B, int64_t L, int64_t C, int64_t W, lr_act act, lr_dtype io,
+                       lr_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* Norm and rotation of queries and keys                                     */
+/* ------------------------------------------------------------------------ */
+
+/* Norm of lr_head_norm_rope, and which values of a head are a pair: value i and value
+ * i + rot / 2, or values 2 i and 2 i + 1. */
+typedef enum { LR_NORM_NONE = 0, LR_NORM_RMS = 1, LR_NORM_L2 = 2 } lr_norm;
+typedef enum { LR_PAIRS_HALVES = 0, LR_PAIRS_NEIGHBOURS = 1 } lr_pairs;
+
+/*
+ * Normalises every head of q and of k and rotates the pairs of its first rot values
+ * by the token's position, in one pass; attention's queries and keys (C and B of a
+ * selective scan) are treated so before it (the source pages have no counterpart).
+ * For every token n and head, with x its d values:
+ *
+ *   r = gamma[i] x[i] / sqrt(mean(x^2) + eps)    LR_NORM_RMS
+ *     = gamma[i] x[i] / sqrt(sum(x^2) + eps)     LR_NORM_L2
+ *     = gamma[i] x[i]                            LR_NORM_NONE
+ *   (a, b) = pair i of r, i < rot / 2:   (a cos p - b sin p, b cos p + a sin p),
+ *   p = pos[n] freqs[i]
+ *
+ * and the values from rot on are r.  Arithmetic in fp32, outputs rounded once; the
+ * angle is formed in 64-bit fixed point, so far positions are as exact as near ones.
+ * A head with an infinity or a NaN keeps it to itself; squares past fp32's range
+ * (values past 1.8e19) give 0.
+ *
+ * Layouts: q: (N, H*d), k: (N, Hk*d) in `io`, rows ldq and ldk elements apart (slices
+ *          of a wider tensor); gamma_q, gamma_k: (d) fp32; freqs: (rot/2) fp32, radians
+ *          a position; pos: (N) int32, of any sign; q_out, k_out: dense.
+ * Optional: gamma_q, gamma_k (1); k and k_out (Hk == 0).  q_out may be q where ldq ==
+ *          H*d, k_out k alike; other outputs must not overlap inputs.
+ * Requirements: N, Hk >= 0, H, d >= 1, 0 <= rot <= d, rot even, ldq >= H*d, ldk >= Hk*d,
+ *          eps >= 0 and finite (else LR_ERR_INVALID_ARG); d <= 512 (else
+ *          LR_ERR_UNSUPPORTED); freqs finite, below 2^20 in size.  No workspace.
+ */
+int lr_head_norm_rope(const void *q, int64_t ldq, const void *k, int64_t ldk,
+                      const float *gamma_q, const float *gamma_k, const float *freqs,
+                      const int32_t *pos, void *q_out, void *k_out, int64_t N, int64_t H,
+                      int64_t Hk, int64_t d, int64_t rot, lr_norm norm, float eps,
+                      lr_pairs pairs, lr_dtype io, lr_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
 /* Gates given before their activation                                       */
 /* ------------------------------------------------------------------------ */
 
@@ -598,6 +670,13 @@ int lr_decay_attn_step(const void *q, const void *k, const void *v,
                        const float *S_in, float *S_out, void *o,
                        int64_t B, int64_t H, int64_t Hk, int64_t dk, int64_t dv,
                        lr_dtype io, lr_stream_t stream);
+
+/* Short causal convolution, one token: lr_causal_conv_fwd with L = 1.  x: (B, C), rows
+ * ldx elements apart; y: (B, C); state_in (NULL = zeros), state_out: (B, W-1, C) in io,
+ * state_out always written; it may be state_in. */
+int lr_causal_conv_step(const void *x, int64_t ldx, const float *w, const float *bias,
+                        const void *state_in, void *state_out, void *y, int64_t B, int64_t C,
+                        int64_t W, lr_act act, lr_dtype io, lr_stream_t stream);
 
 /* ------------------------------------------------------------------------ */
 /* Tuning and test hooks                                                     */

@@ -22,9 +22,13 @@ Functions (sources are cited in ``lro_oracle.c``):
 
 * :func:`decay_attn`      -- linear attention with a decay for each head.
 * :func:`group_norm_act`  -- group norm per row with an activation and a gate.
+* :func:`selective_heads` -- selective scan with heads (by :func:`decay_attn`).
+* :func:`causal_conv`     -- short causal convolution, channels last (numpy).
+* :func:`head_norm_rope`  -- norm and rotation of heads (numpy).
 
 All are pinned against closed forms, brute force and library routines in
-``tests/test_oracle_pins.py`` and ``tests/test_decay_oracle_pins.py``.
+``tests/test_oracle_pins.py``, ``tests/test_decay_oracle_pins.py`` and
+``tests/test_layer_oracle_pins.py``.
 """
 from __future__ import annotations
 
@@ -263,3 +267,73 @@ def group_norm_act(x, G, gamma=None, beta=None, z=None, act="none", eps=1e-5, th
     if rc != 0:
         raise ValueError("lro_group_norm_act_ref rejected its arguments")
     return y
+
+
+def _silu(x):
+    with np.errstate(over="ignore"):   # e^-x past float64's range: the quotient is 0
+        return x / (1.0 + np.exp(-x))
+
+
+def _lengths(lens, Bsz, L):
+    if lens is None:
+        return [L] * Bsz
+    return [min(max(int(n), 0), L) for n in lens]
+
+
+def selective_heads(x, dt, Bm, Cm, A_log, H, G=1, z=None, Dskip=None, dt_bias=None, S0=None, lens=None,
+                    dt_softplus=True, threads=0):
+    """Selective scan with heads in float64: S = exp(-exp(A_log) delta) S + delta x B^T,
+    y = (S C + Dskip x) silu(z), delta = softplus(dt + dt_bias).
+
+    x, z: (B, L, H*P); dt: (B, L, H); Bm, Cm: (B, L, G*N); A_log, Dskip, dt_bias: (H,);
+    S0: (B, H, P, N); lens: (B,).  Returns ``(y (B, L, H*P), S_final)``.
+    """
+    x, dt, Bm, Cm, A_log, z, Dskip, dt_bias = map(_f64, (x, dt, Bm, Cm, A_log, z, Dskip, dt_bias))
+    Bsz, L, HP = x.shape
+    delta = dt if dt_bias is None else dt + dt_bias
+    if dt_softplus:
+        delta = np.logaddexp(delta, 0.0)
+    xh = x.reshape(Bsz, L, H, HP // H)
+    y, Sf = decay_attn(Cm, Bm, (delta[..., None] * xh).reshape(x.shape), H, Hk=G, g=-np.exp(A_log) * delta, S0=S0,
+                       lens=lens, threads=threads)
+    if Dskip is not None:
+        y = y + (Dskip[:, None] * xh).reshape(x.shape)
+    if z is not None:
+        y = y * _silu(z)
+    for b, n in enumerate(_lengths(lens, Bsz, L)):
+        y[b, n:] = 0.0
+    return y, Sf
+
+
+def causal_conv(x, w, bias=None, state=None, lens=None, act="silu"):
+    """Short causal convolution in float64.  x: (B, L, C); w: (C, W); bias: (C,);
+    state: (B, W-1, C); lens: (B,).  Returns ``(y (B, L, C), state (B, W-1, C))``."""
+    x, w, bias, state = map(_f64, (x, w, bias, state))
+    Bsz, L, C = x.shape
+    W = w.shape[1]
+    y, new = np.zeros((Bsz, L, C)), np.zeros((Bsz, W - 1, C))
+    for b, n in enumerate(_lengths(lens, Bsz, L)):
+        v = np.concatenate([np.zeros((W - 1, C)) if state is None else state[b], x[b, :n]])
+        acc = np.zeros((n, C)) + (0.0 if bias is None else bias)
+        for j in range(W):
+            acc += w[:, j] * v[j:j + n]
+        y[b, :n] = _silu(acc) if act == "silu" else acc
+        new[b] = v[n:]
+    return y, new
+
+
+def head_norm_rope(x, H, norm="rms", gamma=None, freqs=None, pos=None, pairs="halves", eps=1e-6):
+    """Norm and rotation of the heads of x (..., H*d) in float64 (one of q and k)."""
+    x, gamma, freqs, pos = map(_f64, (x, gamma, freqs, pos))
+    v = x.reshape(*x.shape[:-1], H, -1).copy()
+    if norm != "none":
+        s = (v * v).mean(-1, keepdims=True) if norm == "rms" else (v * v).sum(-1, keepdims=True)
+        v = v / np.sqrt(s + eps)
+    if gamma is not None:
+        v = v * gamma
+    if freqs is not None:
+        m = len(freqs)
+        a, b = (slice(0, m), slice(m, 2 * m)) if pairs == "halves" else (slice(0, 2 * m, 2), slice(1, 2 * m, 2))
+        p = (pos[..., None] * freqs)[..., None, :]
+        v[..., a], v[..., b] = v[..., a] * np.cos(p) - v[..., b] * np.sin(p), v[..., b] * np.cos(p) + v[..., a] * np.sin(p)
+    return v.reshape(x.shape)

@@ -32,6 +32,8 @@ LR_OK = 0
 LR_ERR_INVALID_ARG, LR_ERR_UNSUPPORTED, LR_ERR_MISALIGNED = -1, -2, -3
 LR_ERR_WORKSPACE, LR_ERR_CUDA, LR_ERR_TIMEOUT, LR_ERR_RANGE = -4, -5, -6, -7
 LR_ACT_NONE, LR_ACT_SILU = 0, 1
+LR_NORM_NONE, LR_NORM_RMS, LR_NORM_L2 = 0, 1, 2
+LR_PAIRS_HALVES, LR_PAIRS_NEIGHBOURS = 0, 1
 
 _IO = {torch.float32: LR_F32, torch.bfloat16: LR_BF16}
 
@@ -97,6 +99,10 @@ SIGNATURES = {
     "lr_decay_attn_fwd_host_async": (_I, [_P, _P, _P, _P, _P, _F, _P, _P, _P, _I64, _I64, _I64, _I64,
                                           _I64, _I64, _I, _P, _SZ, _P]),
     "lr_group_norm_act": (_I, [_P, _P, _P, _P, _P, _I64, _I64, _I64, _F, _I, _I, _P]),
+    "lr_causal_conv_fwd": (_I, [_P, _I64, _P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _I, _I, _P]),
+    "lr_causal_conv_step": (_I, [_P, _I64, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I, _I, _P]),
+    "lr_head_norm_rope": (_I, [_P, _I64, _P, _I64, _P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _I64, _I, _F,
+                               _I, _I, _P]),
 }
 
 
@@ -386,6 +392,20 @@ def lr_decay_attn_fwd_host_async(q, k, v, a_log, g, scale, S0, o, S_final, B, L,
 
 def lr_group_norm_act(x, z, gamma, beta, y, N, C, G, eps, act, io, stream) -> int:
     return _lib.lr_group_norm_act(x, z, gamma, beta, y, N, C, G, eps, act, io, stream)
+
+
+def lr_causal_conv_fwd(x, ldx, w, bias, state, lens, y, state_out, B, L, C, W, act, io, stream) -> int:
+    return _lib.lr_causal_conv_fwd(x, ldx, w, bias, state, lens, y, state_out, B, L, C, W, act, io, stream)
+
+
+def lr_causal_conv_step(x, ldx, w, bias, state_in, state_out, y, B, C, W, act, io, stream) -> int:
+    return _lib.lr_causal_conv_step(x, ldx, w, bias, state_in, state_out, y, B, C, W, act, io, stream)
+
+
+def lr_head_norm_rope(q, ldq, k, ldk, gamma_q, gamma_k, freqs, pos, q_out, k_out, N, H, Hk, d, rot, norm, eps, pairs,
+                      io, stream) -> int:
+    return _lib.lr_head_norm_rope(q, ldq, k, ldk, gamma_q, gamma_k, freqs, pos, q_out, k_out, N, H, Hk, d, rot, norm,
+                                  eps, pairs, io, stream)
 
 
 # ------------------------------------------------------------ torch helpers
@@ -917,6 +937,168 @@ def group_norm_act(x, G: int, gamma=None, beta=None, z=None, act: str = "none", 
 
 
 _ACT = {"none": LR_ACT_NONE, "silu": LR_ACT_SILU}
+
+
+def _rows(t: Optional[torch.Tensor], dev, whole: bool = False):
+    """(t on the GPU, elements between its rows) for t (..., C) whose rows lie evenly
+    apart, as the slices of a projection's output do; a copy where they do not, or
+    where t does not start on a 16-byte boundary (``whole``: its rows too, unless dense)."""
+    if t is None:
+        return None, 0
+    if not t.is_cuda:
+        t = t.to(dev, non_blocking=True)
+    C = t.shape[-1]
+    ld, size = None, 1
+    for n, st in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):   # rows from the last axis on
+        if n == 1:
+            continue
+        if ld is None:
+            ld = st
+        elif st != ld * size:
+            ld = -1
+        size *= n
+    if ld is None:
+        ld = C
+    if t.numel() == 0 or (C > 1 and t.stride(-1) != 1) or ld < C or t.data_ptr() % 16 or (
+            whole and ld != C and ld * t.element_size() % 16):
+        return _aligned(t), C
+    return t, ld
+
+
+def _lens_of(lens: Optional[torch.Tensor], B: int, L: int, dev):
+    """lens as the kernels read them."""
+    if lens is None:
+        return None
+    _shaped(lens, (B,), "lens")
+    if lens.is_floating_point() or lens.dtype is torch.bool:
+        raise TypeError("lens must be integers")
+    return _act(lens if lens.dtype is torch.int32 else lens.clamp(0, L).to(torch.int32), dev)   # (clamped before)
+
+
+def _out_like(out: Optional[torch.Tensor], shape, dtype, dev, name: str = "out"):
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    if out.shape != torch.Size(shape) or out.dtype != dtype or out.device != dev or not out.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} GPU tensor of shape {tuple(shape)}")
+    return out
+
+
+def _conv_args(x, w, bias, state, act: str, ndim: int):
+    a = _ACT.get(act)
+    if a is None:
+        raise ValueError(f"unknown activation {act!r}; use one of {sorted(_ACT)}")
+    if x.dim() != ndim or w.dim() != 2 or w.shape[0] != x.shape[-1]:
+        raise ValueError(f"x {tuple(x.shape)} and w {tuple(w.shape)} do not match")
+    C, W = w.shape
+    if bias is not None:
+        _shaped(bias, (C,), "bias")
+    if state is not None:
+        _shaped(state, (x.shape[0], W - 1, C), "state")
+        _same(x, state)
+    return a, C, W, _io_of(x)
+
+
+def causal_conv(x, w, bias=None, state=None, lens=None, act: str = "silu",
+                out=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Short causal convolution of every channel:
+    y_t = act(bias + sum_j w[:, j] x_{t - W + 1 + j}).
+
+    x: (B, L, C) on the GPU, float32 or bfloat16 (a slice of a wider tensor is read
+    where it stands); w: (C, W) and bias: (C,) fp32, 2 <= W <= 4; state: (B, W-1, C) in
+    x's dtype, the inputs before the first step, oldest first, or None (zeros); lens:
+    (B,) integers or None: row b has lens[b] steps (its later outputs are 0); ``act``:
+    "silu" or "none".  Returns (y (B, L, C), the state after each row's last step);
+    ``out=(y, state)`` gives the result tensors (the state may be ``state`` itself)."""
+    a, C, W, io = _conv_args(x, w, bias, state, act, 3)
+    B, L, _ = x.shape
+    dev = _target_device(x)
+    y, new = out if out is not None else (None, None)
+    with torch.cuda.device(dev):
+        x, ldx = _rows(x, dev)
+        lens = _lens_of(lens, B, L, dev)
+        w, bias, state = _par(w, dev), _par(bias, dev), _act(state, dev)
+        y = _out_like(y, (B, L, C), x.dtype, dev)
+        new = _out_like(new, (B, W - 1, C), x.dtype, dev)
+        _check(lr_causal_conv_fwd(_ptr(x), ldx, _ptr(w), _ptr(bias), _ptr(state), _ptr(lens), _ptr(y), _ptr(new),
+                                  B, L, C, W, a, io, _stream_of(x)), "lr_causal_conv_fwd")
+    return y, new
+
+
+def causal_conv_step(x, w, bias=None, state=None, state_out=None,
+                     act: str = "silu") -> Tuple[torch.Tensor, torch.Tensor]:
+    """One token of ``causal_conv``.  x: (B, C); state: (B, W-1, C) or None (zeros).
+    Returns (y (B, C), the new state); ``state_out`` gives the buffer that it is
+    written to (it may be ``state`` itself)."""
+    a, C, W, io = _conv_args(x, w, bias, state, act, 2)
+    B = x.shape[0]
+    dev = _target_device(x)
+    with torch.cuda.device(dev):
+        x, ldx = _rows(x, dev)
+        w, bias, state = _par(w, dev), _par(bias, dev), _act(state, dev)
+        new = _out_like(state_out, (B, W - 1, C), x.dtype, dev, "state_out")
+        y = torch.empty((B, C), dtype=x.dtype, device=dev)
+        _check(lr_causal_conv_step(_ptr(x), ldx, _ptr(w), _ptr(bias), _ptr(state), _ptr(new), _ptr(y), B, C, W, a, io,
+                                   _stream_of(x)), "lr_causal_conv_step")
+    return y, new
+
+
+_NORM = {"none": LR_NORM_NONE, "rms": LR_NORM_RMS, "l2": LR_NORM_L2}
+_PAIRS = {"halves": LR_PAIRS_HALVES, "neighbours": LR_PAIRS_NEIGHBOURS}
+
+
+def head_norm_rope(q, k, H: int, Hk: Optional[int] = None, norm: str = "rms", gamma_q=None, gamma_k=None, freqs=None,
+                   pos=None, pairs: str = "halves", eps: float = 1e-6, out=None):
+    """Norm of every head of q and k, and the rotation of its pairs by the token's
+    position, in one pass.
+
+    q: (..., H*d), k: (..., Hk*d) or None, on the GPU, one dtype (bfloat16 or float32;
+    slices of a wider tensor are read where they stand); ``Hk``: key heads (default H);
+    ``norm``: "rms" (x / sqrt(mean(x^2) + eps)), "l2" (the sum of the squares) or "none";
+    gamma_q, gamma_k: (d,) fp32 factors after it, or None; freqs: (rot/2,) fp32, radians
+    a position, or None (no rotation): the first rot values of a head are rotated, their
+    ``pairs`` being values i and i + rot/2 ("halves") or 2i and 2i + 1 ("neighbours");
+    pos: (...) integers within int32.  Returns (q, k) as new dense tensors; ``out`` gives
+    them (dense inputs themselves are allowed)."""
+    n, p = _NORM.get(norm), _PAIRS.get(pairs)
+    if n is None or p is None:
+        raise ValueError(f"unknown norm {norm!r} or pairs {pairs!r}; use one of {sorted(_NORM)} and {sorted(_PAIRS)}")
+    lead, Hk = q.shape[:-1], 0 if k is None else H if Hk is None else Hk
+    if H < 1 or q.shape[-1] % H or q.shape[-1] == 0:
+        raise ValueError(f"width {q.shape[-1]} is not divisible by {H} heads")
+    d = q.shape[-1] // H
+    if k is not None:
+        _shaped(k, (*lead, Hk * d), "k")
+        _same(q, k)
+    for g, what in ((gamma_q, "gamma_q"), (gamma_k, "gamma_k")):
+        if g is not None:
+            _shaped(g, (d,), what)
+    rot = 0
+    if freqs is not None:
+        rot = 2 * freqs.numel()
+        if freqs.dim() != 1 or rot > d:
+            raise ValueError(f"freqs must have shape (rot / 2,), rot <= {d}, not {tuple(freqs.shape)}")
+        if pos is None:
+            raise ValueError("a rotation needs pos")
+        _shaped(pos, lead, "pos")
+        if pos.is_floating_point() or pos.dtype is torch.bool:
+            raise TypeError("pos must be integers")
+    io = _io_of(q)
+    dev = _target_device(q)
+    qo, ko = out if out is not None else (None, None)
+    with torch.cuda.device(dev):
+        q, ldq = _rows(q, dev)
+        k, ldk = _rows(k, dev)
+        if rot:
+            freqs, pos = _par(freqs, dev), _act(pos if pos.dtype is torch.int32 else pos.to(torch.int32), dev)
+        else:
+            freqs = pos = None
+        gamma_q, gamma_k = _par(gamma_q, dev), _par(gamma_k, dev)
+        qo = _out_like(qo, (*lead, H * d), q.dtype, dev)
+        ko = None if k is None else _out_like(ko, (*lead, Hk * d), q.dtype, dev)
+        _check(lr_head_norm_rope(_ptr(q), ldq, _ptr(k), ldk, _ptr(gamma_q), _ptr(gamma_k), _ptr(freqs), _ptr(pos),
+                                 _ptr(qo), _ptr(ko), q.numel() // (H * d), H, Hk, d, rot, n, float(eps), p, io,
+                                 _stream_of(q)), "lr_head_norm_rope")
+    return qo, ko
 
 
 def _step_state(state, shape, dev, state_out):

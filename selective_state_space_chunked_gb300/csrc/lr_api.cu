@@ -562,6 +562,68 @@ extern "C" int lr_group_norm_act(const void *x, const void *z, const float *gamm
                                      reinterpret_cast<cudaStream_t>(stream));
 }
 
+// ------------------------------- short convolution, norm and rotation of heads
+namespace {
+int validate_conv(const void *x, int64_t ldx, const float *w, const float *bias, const void *state,
+                  const int32_t *lens, const void *y, const void *state_out, int64_t B, int64_t L, int64_t C,
+                  int64_t W, lr_act act, lr_dtype io) {
+    if (B < 0 || L < 0 || C < 0 || W < 2 || ldx < C || !io_ok(io) || (act != LR_ACT_NONE && act != LR_ACT_SILU))
+        return LR_ERR_INVALID_ARG;
+    if (B > 0 && C > 0 && L > 0 && (!x || !w || !y)) return LR_ERR_INVALID_ARG;
+    if (W > 4 || !fits_int(B) || !fits_int(L) || !fits_int(C)) return LR_ERR_UNSUPPORTED;
+    const void *ptrs[] = {x, w, bias, state, lens, y, state_out};
+    for (const void *p : ptrs)
+        if (misaligned(p)) return LR_ERR_MISALIGNED;
+    return LR_OK;
+}
+}  // namespace
+
+extern "C" int lr_causal_conv_fwd(const void *x, int64_t ldx, const float *w, const float *bias, const void *state,
+                                  const int32_t *lens, void *y, void *state_out, int64_t B, int64_t L, int64_t C,
+                                  int64_t W, lr_act act, lr_dtype io, lr_stream_t stream) {
+    const int rc = validate_conv(x, ldx, w, bias, state, lens, y, state_out, B, L, C, W, act, io);
+    if (rc != LR_OK) return rc;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (L == 0) {   // the state stays
+        const size_t bytes = size_t(B) * (W - 1) * C * (io == LR_BF16 ? 2 : 4);
+        if (state_out == nullptr || state_out == state || bytes == 0) return LR_OK;
+        const cudaError_t e = state != nullptr ? cudaMemcpyAsync(state_out, state, bytes, cudaMemcpyDeviceToDevice, st)
+                                               : cudaMemsetAsync(state_out, 0, bytes, st);
+        return e == cudaSuccess ? LR_OK : LR_ERR_CUDA;
+    }
+    return lr::causal_conv_launch(x, ldx, w, bias, state, lens, y, state_out, B, L, C, int(W), act, io == LR_BF16,
+                                  false, st);
+}
+
+extern "C" int lr_causal_conv_step(const void *x, int64_t ldx, const float *w, const float *bias,
+                                   const void *state_in, void *state_out, void *y, int64_t B, int64_t C, int64_t W,
+                                   lr_act act, lr_dtype io, lr_stream_t stream) {
+    const int rc = validate_conv(x, ldx, w, bias, state_in, nullptr, y, state_out, B, 1, C, W, act, io);
+    if (rc == LR_ERR_INVALID_ARG || (B > 0 && C > 0 && state_out == nullptr)) return LR_ERR_INVALID_ARG;
+    if (rc != LR_OK) return rc;
+    return lr::causal_conv_launch(x, ldx, w, bias, state_in, nullptr, y, state_out, B, 1, C, int(W), act,
+                                  io == LR_BF16, true, reinterpret_cast<cudaStream_t>(stream));
+}
+
+extern "C" int lr_head_norm_rope(const void *q, int64_t ldq, const void *k, int64_t ldk, const float *gamma_q,
+                                 const float *gamma_k, const float *freqs, const int32_t *pos, void *q_out,
+                                 void *k_out, int64_t N, int64_t H, int64_t Hk, int64_t d, int64_t rot, lr_norm norm,
+                                 float eps, lr_pairs pairs, lr_dtype io, lr_stream_t stream) {
+    if (N < 0 || H <= 0 || Hk < 0 || d <= 0 || rot < 0 || rot > d || rot % 2 != 0 || !io_ok(io) ||
+        !std::isfinite(eps) || eps < 0.0f || norm < LR_NORM_NONE || norm > LR_NORM_L2 || pairs < LR_PAIRS_HALVES ||
+        pairs > LR_PAIRS_NEIGHBOURS)
+        return LR_ERR_INVALID_ARG;
+    if (d > 512 || !fits_int(N) || !fits_int(H) || !fits_int(Hk) || !fits_int((H + Hk) * d)) return LR_ERR_UNSUPPORTED;
+    if (ldq < H * d || ldk < Hk * d) return LR_ERR_INVALID_ARG;
+    if (N > 0 && (!q || !q_out || (Hk > 0 && (!k || !k_out)) || (rot > 0 && (!freqs || !pos))))
+        return LR_ERR_INVALID_ARG;
+    const void *ptrs[] = {q, k, gamma_q, gamma_k, freqs, pos, q_out, k_out};
+    for (const void *p : ptrs)
+        if (misaligned(p)) return LR_ERR_MISALIGNED;
+    return lr::head_norm_rope_launch(q, ldq, k, ldk, gamma_q, gamma_k, freqs, pos, q_out, k_out, N, H, Hk, d, rot,
+                                     norm, eps, pairs, io == LR_BF16, reinterpret_cast<cudaStream_t>(stream));
+}
+
 // ---------------------------------------------------------------- host buffers
 // The same scans with every tensor in host memory: the engine in lr_host.cu
 // runs the sequence through the GPU in time chunks, each chunk one call of

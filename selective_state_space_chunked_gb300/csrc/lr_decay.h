@@ -98,4 +98,12 @@ int decay_step_launch(const void *q, const void *k, const void *v, const float *
 int group_norm_act_launch(const void *x, const void *z, const float *gamma, const float *beta, void *y,
                           int64_t N, int64_t C, int64_t G, float eps, int act, int io_bf16, cudaStream_t stream);
 
+int causal_conv_launch(const void *x, int64_t ldx, const float *w, const float *bias, const void *state,
+                       const int32_t *lens, void *y, void *state_out, int64_t B, int64_t L, int64_t C, int W, int act,
+                       int io_bf16, bool step, cudaStream_t stream);
+
+int head_norm_rope_launch(const void *q, int64_t ldq, const void *k, int64_t ldk, const float *gq, const float *gk,
+                          const float *freqs, const int32_t *pos, void *qo, void *ko, int64_t N, int64_t H, int64_t Hk,
+                          int64_t d, int64_t rot, int norm, float eps, int pairs, int io_bf16, cudaStream_t stream);
+
 }  // namespace lr
