@@ -323,6 +323,51 @@ int lr_decay_attn_fwd(const void *q, const void *k, const void *v,
                       void *workspace, size_t ws_bytes, lr_stream_t stream);
 
 /* ------------------------------------------------------------------------ */
+/* Selective scan with heads                                                 */
+/* ------------------------------------------------------------------------ */
+
+/*
+ * The selective scan in the form with heads (the source pages have no counterpart):
+ * one decay rate and one step size per head, a P x N state per head, B and C shared by
+ * the H / G heads of a group.  Per batch b and head h, with the group j = h / (H / G)
+ * and S = S0[b,h] (zero when NULL):
+ *
+ *   delta_t = softplus(dt[b,t,h] + dt_bias[h])     (as in lr_selective_scan_fwd;
+ *             dt_softplus == 0: dt + dt_bias, which must be >= 0)
+ *   S_t = exp(-exp(A_log[h]) delta_t) S_{t-1} + delta_t x_t B_t^T
+ *   y_t = (S_t C_t + Dskip[h] x_t) * silu(z_t)     (after the update at t)
+ *
+ * for t < lens[b], and S_final[b,h] = S after the last of them; rows past their
+ * length, resets (a decay of 0), infinities and NaN, the range of the scaled state
+ * and the precision are those of lr_decay_attn_fwd, whose kernels run this with q = C,
+ * k = B, v = delta x.  The step size, the decay and delta x B^T are formed in fp32
+ * whatever `io`.  An infinity or a NaN in z reaches its own output.  A step size that
+ * is negative or NaN sets LR_ERR_RANGE; that call's outputs are then not meaningful.
+ *
+ * Layouts: x, z, y: (B, L, H*P); dt: (B, L, H); Bm, Cm: (B, L, G*N), all in `io`;
+ *          A_log, dt_bias, Dskip: (H) fp32; lens: (B) int32; S0, S_final: (B, H, P, N)
+ *          fp32.  y is dense; the B L rows of the others lie ld* elements apart (slices
+ *          of a projection's or a convolution's output; ld == the width: dense).
+ * Optional: z (no gate), dt_bias (0), Dskip (no skip), lens (every row has L steps), S0,
+ *          S_final.  Outputs must not overlap inputs.
+ * Requirements: H, G, P, N >= 1, H % G == 0, ld* >= their widths (else
+ *          LR_ERR_INVALID_ARG); N <= 512 (else LR_ERR_UNSUPPORTED); ldx, ldb, ldc, ldz
+ *          the width or a multiple of 16 bytes (else LR_ERR_MISALIGNED).
+ * Workspace: that of lr_decay_attn_workspace_size(B, L, H, G, N, P, io).
+ */
+size_t lr_selective_heads_workspace_size(int64_t B, int64_t L, int64_t H, int64_t G,
+                                         int64_t P, int64_t N, lr_dtype io);
+
+int lr_selective_heads_fwd(const void *x, int64_t ldx, const void *dt, int64_t lddt,
+                           const void *Bm, int64_t ldb, const void *Cm, int64_t ldc,
+                           const void *z, int64_t ldz, const float *A_log,
+                           const float *dt_bias, const float *Dskip, const int32_t *lens,
+                           const float *S0, void *y, float *S_final, int64_t B, int64_t L,
+                           int64_t H, int64_t G, int64_t P, int64_t N, lr_dtype io,
+                           int dt_softplus, void *workspace, size_t ws_bytes,
+                           lr_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
 /* Group norm with an activation, channels last                              */
 /* ------------------------------------------------------------------------ */
 
@@ -670,6 +715,18 @@ int lr_decay_attn_step(const void *q, const void *k, const void *v,
                        const float *S_in, float *S_out, void *o,
                        int64_t B, int64_t H, int64_t Hk, int64_t dk, int64_t dv,
                        lr_dtype io, lr_stream_t stream);
+
+/* Selective scan with heads, one token: lr_selective_heads_fwd with L = 1, without its
+ * limit on N; step sizes are not checked on the device.  x, z, y: (B, H*P); dt: (B, H);
+ * Bm, Cm: (B, G*N); S_in (NULL = zero), S_out: (B, H, P, N) fp32, S_out always written;
+ * it may be S_in. */
+int lr_selective_heads_step(const void *x, int64_t ldx, const void *dt, int64_t lddt,
+                            const void *Bm, int64_t ldb, const void *Cm, int64_t ldc,
+                            const void *z, int64_t ldz, const float *A_log,
+                            const float *dt_bias, const float *Dskip, const float *S_in,
+                            float *S_out, void *y, int64_t B, int64_t H, int64_t G,
+                            int64_t P, int64_t N, lr_dtype io, int dt_softplus,
+                            lr_stream_t stream);
 
 /* Short causal convolution, one token: lr_causal_conv_fwd with L = 1.  x: (B, C), rows
  * ldx elements apart; y: (B, C); state_in (NULL = zeros), state_out: (B, W-1, C) in io,

@@ -1,5 +1,5 @@
 """GB300-native gated linear-recurrence scans: selective SSM, RG-LRU, HGRN2,
-linear attention with a decay for each head.
+linear attention with a decay for each head, the selective scan with heads.
 
 The compute path is the CUDA library ``_build/liblrscan.so`` (C ABI in
 ``include/lrscan.h``); :mod:`.binding` marshals torch tensors to it.  The
@@ -9,7 +9,8 @@ generators in :mod:`.workloads` load without the library.
 from . import workloads  # noqa: F401  (pure torch, holds no scan arithmetic)
 
 __all__ = ["workloads", "binding", "selective_scan", "rglru_scan", "hgrn2",
-           "decay_attn", "decay_attn_step", "group_norm_act", "check_status", "LrError"]
+           "decay_attn", "decay_attn_step", "group_norm_act", "selective_heads", "selective_heads_step",
+           "causal_conv", "causal_conv_step", "head_norm_rope", "check_status", "LrError"]
 
 
 def __getattr__(name):

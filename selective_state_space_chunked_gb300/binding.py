@@ -99,6 +99,11 @@ SIGNATURES = {
     "lr_decay_attn_fwd_host_async": (_I, [_P, _P, _P, _P, _P, _F, _P, _P, _P, _I64, _I64, _I64, _I64,
                                           _I64, _I64, _I, _P, _SZ, _P]),
     "lr_group_norm_act": (_I, [_P, _P, _P, _P, _P, _I64, _I64, _I64, _F, _I, _I, _P]),
+    "lr_selective_heads_workspace_size": (_SZ, [_I64, _I64, _I64, _I64, _I64, _I64, _I]),
+    "lr_selective_heads_fwd": (_I, [_P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _P, _P, _P, _P, _P, _P,
+                                    _I64, _I64, _I64, _I64, _I64, _I64, _I, _I, _P, _SZ, _P]),
+    "lr_selective_heads_step": (_I, [_P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _P, _P, _P, _P, _P,
+                                     _I64, _I64, _I64, _I64, _I64, _I, _I, _P]),
     "lr_causal_conv_fwd": (_I, [_P, _I64, _P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _I, _I, _P]),
     "lr_causal_conv_step": (_I, [_P, _I64, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I, _I, _P]),
     "lr_head_norm_rope": (_I, [_P, _I64, _P, _I64, _P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _I64, _I, _F,
@@ -392,6 +397,22 @@ def lr_decay_attn_fwd_host_async(q, k, v, a_log, g, scale, S0, o, S_final, B, L,
 
 def lr_group_norm_act(x, z, gamma, beta, y, N, C, G, eps, act, io, stream) -> int:
     return _lib.lr_group_norm_act(x, z, gamma, beta, y, N, C, G, eps, act, io, stream)
+
+
+def lr_selective_heads_workspace_size(B, L, H, G, P, N, io) -> int:
+    return int(_lib.lr_selective_heads_workspace_size(B, L, H, G, P, N, io))
+
+
+def lr_selective_heads_fwd(x, ldx, dt, lddt, Bm, ldb, Cm, ldc, z, ldz, A_log, dt_bias, Dskip, lens, S0, y, S_final,
+                           B, L, H, G, P, N, io, dt_softplus, workspace, ws_bytes, stream) -> int:
+    return _lib.lr_selective_heads_fwd(x, ldx, dt, lddt, Bm, ldb, Cm, ldc, z, ldz, A_log, dt_bias, Dskip, lens, S0, y,
+                                       S_final, B, L, H, G, P, N, io, dt_softplus, workspace, ws_bytes, stream)
+
+
+def lr_selective_heads_step(x, ldx, dt, lddt, Bm, ldb, Cm, ldc, z, ldz, A_log, dt_bias, Dskip, S_in, S_out, y, B, H, G,
+                            P, N, io, dt_softplus, stream) -> int:
+    return _lib.lr_selective_heads_step(x, ldx, dt, lddt, Bm, ldb, Cm, ldc, z, ldz, A_log, dt_bias, Dskip, S_in, S_out,
+                                        y, B, H, G, P, N, io, dt_softplus, stream)
 
 
 def lr_causal_conv_fwd(x, ldx, w, bias, state, lens, y, state_out, B, L, C, W, act, io, stream) -> int:
@@ -965,13 +986,16 @@ def _rows(t: Optional[torch.Tensor], dev, whole: bool = False):
     return t, ld
 
 
-def _lens_of(lens: Optional[torch.Tensor], B: int, L: int, dev):
+def _integers(t: Optional[torch.Tensor], shape, name: str):
+    _shaped(t, shape, name)
+    if t is not None and (t.is_floating_point() or t.dtype is torch.bool):
+        raise TypeError(f"{name} must be integers")
+
+
+def _lens_of(lens: Optional[torch.Tensor], L: int, dev):
     """lens as the kernels read them."""
     if lens is None:
         return None
-    _shaped(lens, (B,), "lens")
-    if lens.is_floating_point() or lens.dtype is torch.bool:
-        raise TypeError("lens must be integers")
     return _act(lens if lens.dtype is torch.int32 else lens.clamp(0, L).to(torch.int32), dev)   # (clamped before)
 
 
@@ -981,6 +1005,83 @@ def _out_like(out: Optional[torch.Tensor], shape, dtype, dev, name: str = "out")
     if out.shape != torch.Size(shape) or out.dtype != dtype or out.device != dev or not out.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} GPU tensor of shape {tuple(shape)}")
     return out
+
+
+def _heads_args(x, dt, Bm, Cm, A_log, H: int, G: int, z, Dskip, dt_bias, S, ndim: int):
+    """(leading shape, P, N, I/O type) of a selective scan with heads."""
+    if H < 1 or G < 1 or H % G:
+        raise ValueError(f"{H} heads cannot share {G} groups of B and C")
+    lead = x.shape[:-1]
+    if x.dim() != ndim or x.shape[-1] == 0 or x.shape[-1] % H:
+        raise ValueError(f"x {tuple(x.shape)} does not hold {H} heads")
+    if Bm.shape[:-1] != lead or Cm.shape != Bm.shape or Bm.shape[-1] == 0 or Bm.shape[-1] % G:
+        raise ValueError(f"x {tuple(x.shape)}, Bm {tuple(Bm.shape)}, Cm {tuple(Cm.shape)} do not match")
+    P, N = x.shape[-1] // H, Bm.shape[-1] // G
+    _shaped(dt, (*lead, H), "dt")
+    _shaped(z, x.shape, "z")
+    _shaped(A_log, (H,), "A_log")
+    _shaped(dt_bias, (H,), "dt_bias")
+    _shaped(Dskip, (H,), "Dskip")
+    _shaped(S, (x.shape[0], H, P, N), "the state")
+    _same(x, dt, Bm, Cm, z)
+    return lead, P, N, _io_of(x)
+
+
+def selective_heads(x, dt, Bm, Cm, A_log, H: int, G: int = 1, z=None, Dskip=None, dt_bias=None, S0=None, lens=None,
+                    dt_softplus: bool = True, workspace=None, out=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Selective scan with heads: S_t = exp(-exp(A_log) delta_t) S_{t-1} + delta_t x_t B_t^T,
+    y_t = (S_t C_t + Dskip x_t) silu(z_t), delta = softplus(dt + dt_bias).
+
+    x, z: (B, L, H*P); dt: (B, L, H); Bm, Cm: (B, L, G*N), on the GPU, one dtype (bfloat16
+    or float32); slices of wider tensors are read where they stand if their rows keep to
+    16-byte boundaries.  A_log, Dskip, dt_bias: (H,) fp32; ``G`` groups of B and C, each
+    shared by H/G heads; S0: (B, H, P, N) fp32 or None; lens: (B,) integers or None: row b
+    has lens[b] steps (its later outputs are 0 and its state stays); ``dt_softplus=False``:
+    delta = dt + dt_bias, at least 0.  z, Dskip, dt_bias may be None.  Returns (y
+    (B, L, H*P), S_final (B, H, P, N) fp32); ``out=(y, S_final)`` gives the result tensors.
+    A negative or NaN step size sets LR_ERR_RANGE (see ``check_status``)."""
+    (B, L), P, N, io = _heads_args(x, dt, Bm, Cm, A_log, H, G, z, Dskip, dt_bias, S0, 3)
+    _integers(lens, (B,), "lens")
+    dev = _target_device(x)
+    y, S = out if out is not None else (None, None)
+    with torch.cuda.device(dev):
+        x, ldx = _rows(x, dev, True)
+        dt, lddt = _rows(dt, dev)
+        Bm, ldb = _rows(Bm, dev, True)
+        Cm, ldc = _rows(Cm, dev, True)
+        z, ldz = _rows(z, dev, True)
+        lens = _lens_of(lens, L, dev)
+        A_log, Dskip, dt_bias, S0 = (_par(t, dev) for t in (A_log, Dskip, dt_bias, S0))
+        y = _out_like(y, (B, L, H * P), x.dtype, dev)
+        S = _out_like(S, (B, H, P, N), torch.float32, dev)
+        ws, wsb = _workspace(lr_selective_heads_workspace_size(B, L, H, G, P, N, io), dev, workspace)
+        _check(lr_selective_heads_fwd(_ptr(x), ldx, _ptr(dt), lddt, _ptr(Bm), ldb, _ptr(Cm), ldc, _ptr(z), ldz,
+                                      _ptr(A_log), _ptr(dt_bias), _ptr(Dskip), _ptr(lens), _ptr(S0), _ptr(y), _ptr(S),
+                                      B, L, H, G, P, N, io, int(bool(dt_softplus)), _ptr(ws), wsb, _stream_of(x)),
+               "lr_selective_heads_fwd")
+    return y, S
+
+
+def selective_heads_step(x, dt, Bm, Cm, A_log, H: int, G: int = 1, z=None, Dskip=None, dt_bias=None, S=None,
+                         S_out=None, dt_softplus: bool = True) -> Tuple[torch.Tensor, torch.Tensor]:
+    """One token of ``selective_heads``.  x, z: (B, H*P); dt: (B, H); Bm, Cm: (B, G*N); S:
+    (B, H, P, N) fp32 or None (zero).  Returns (y (B, H*P), S_new); ``S_out`` gives the
+    buffer S_new is written to (it may be ``S`` itself)."""
+    (B,), P, N, io = _heads_args(x, dt, Bm, Cm, A_log, H, G, z, Dskip, dt_bias, S, 2)
+    dev = _target_device(x)
+    with torch.cuda.device(dev):
+        x, ldx = _rows(x, dev, True)
+        dt, lddt = _rows(dt, dev)
+        Bm, ldb = _rows(Bm, dev, True)
+        Cm, ldc = _rows(Cm, dev, True)
+        z, ldz = _rows(z, dev, True)
+        A_log, Dskip, dt_bias, S = (_par(t, dev) for t in (A_log, Dskip, dt_bias, S))
+        S_out = _out_like(S_out, (B, H, P, N), torch.float32, dev, "S_out")
+        y = torch.empty((B, H * P), dtype=x.dtype, device=dev)
+        _check(lr_selective_heads_step(_ptr(x), ldx, _ptr(dt), lddt, _ptr(Bm), ldb, _ptr(Cm), ldc, _ptr(z), ldz,
+                                       _ptr(A_log), _ptr(dt_bias), _ptr(Dskip), _ptr(S), _ptr(S_out), _ptr(y), B, H, G,
+                                       P, N, io, int(bool(dt_softplus)), _stream_of(x)), "lr_selective_heads_step")
+    return y, S_out
 
 
 def _conv_args(x, w, bias, state, act: str, ndim: int):
@@ -1011,11 +1112,12 @@ def causal_conv(x, w, bias=None, state=None, lens=None, act: str = "silu",
     ``out=(y, state)`` gives the result tensors (the state may be ``state`` itself)."""
     a, C, W, io = _conv_args(x, w, bias, state, act, 3)
     B, L, _ = x.shape
+    _integers(lens, (B,), "lens")
     dev = _target_device(x)
     y, new = out if out is not None else (None, None)
     with torch.cuda.device(dev):
         x, ldx = _rows(x, dev)
-        lens = _lens_of(lens, B, L, dev)
+        lens = _lens_of(lens, L, dev)
         w, bias, state = _par(w, dev), _par(bias, dev), _act(state, dev)
         y = _out_like(y, (B, L, C), x.dtype, dev)
         new = _out_like(new, (B, W - 1, C), x.dtype, dev)
@@ -1079,9 +1181,7 @@ def head_norm_rope(q, k, H: int, Hk: Optional[int] = None, norm: str = "rms", ga
             raise ValueError(f"freqs must have shape (rot / 2,), rot <= {d}, not {tuple(freqs.shape)}")
         if pos is None:
             raise ValueError("a rotation needs pos")
-        _shaped(pos, lead, "pos")
-        if pos.is_floating_point() or pos.dtype is torch.bool:
-            raise TypeError("pos must be integers")
+        _integers(pos, lead, "pos")
     io = _io_of(q)
     dev = _target_device(q)
     qo, ko = out if out is not None else (None, None)

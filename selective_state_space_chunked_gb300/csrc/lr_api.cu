@@ -527,7 +527,7 @@ extern "C" int lr_decay_attn_fwd(const void *q, const void *k, const void *v, co
     lr::DecayArgs a{};
     a.q = q, a.k = k, a.v = v, a.a_log = a_log, a.g = g, a.lens = lens, a.S0 = S0, a.o = o, a.S_final = S_final;
     a.B = B, a.L = L, a.H = int(H), a.Hk = int(Hk), a.dk = int(dk), a.dv = int(dv), a.scale = scale;
-    return lr::decay_attn_launch(a, io, p, workspace, st);
+    return lr::decay_attn_launch(a, io, p, false, workspace, st);
 }
 
 extern "C" int lr_decay_attn_step(const void *q, const void *k, const void *v, const float *a_log, const void *g,
@@ -541,7 +541,7 @@ extern "C" int lr_decay_attn_step(const void *q, const void *k, const void *v, c
         const void *all[] = {q, k, v, a_log, g, S_in, S_out, o};
         if ((rc = validate_step_common(req, 5, all, 8)) != LR_OK) return rc;
     }
-    return lr::decay_step_launch(q, k, v, a_log, g, scale, S_in, S_out, o, B, H, Hk, dk, dv, io == LR_BF16,
+    return lr::decay_step_launch(q, k, v, a_log, g, scale, S_in, S_out, o, B, H, Hk, dk, dv, io == LR_BF16, nullptr,
                                  reinterpret_cast<cudaStream_t>(stream));
 }
 
@@ -560,6 +560,80 @@ extern "C" int lr_group_norm_act(const void *x, const void *z, const float *gamm
     }
     return lr::group_norm_act_launch(x, z, gamma, beta, y, N, C, G, eps, act, io == LR_BF16,
                                      reinterpret_cast<cudaStream_t>(stream));
+}
+
+// ------------------------------------------------- selective scan with heads
+namespace {
+// rows of `width` elements, dense or ld apart with every row on a 16-byte boundary
+bool rows_bad(int64_t ld, int64_t width) { return ld < width; }
+bool rows_off(int64_t ld, int64_t width, lr_dtype io) { return ld != width && ld % (io == LR_BF16 ? 8 : 4) != 0; }
+
+int validate_heads(const void *x, int64_t ldx, const void *dt, int64_t lddt, const void *Bm, int64_t ldb,
+                   const void *Cm, int64_t ldc, const void *z, int64_t ldz, const float *A_log, const float *dt_bias,
+                   const float *Dskip, const int32_t *lens, const float *S0, const void *y, const float *S_final,
+                   int64_t B, int64_t L, int64_t H, int64_t G, int64_t P, int64_t N, lr_dtype io) {
+    const int rc = validate_decay_sizes(B, L, H, G, N, P, io);
+    if (rc == LR_ERR_INVALID_ARG) return rc;
+    if (B > 0 && L > 0 && (!x || !dt || !Bm || !Cm || !A_log || !y)) return LR_ERR_INVALID_ARG;
+    if (rc != LR_OK) return rc;
+    if (!fits_int(H * P) || !fits_int(G * N)) return LR_ERR_UNSUPPORTED;
+    if (rows_bad(ldx, H * P) || rows_bad(lddt, H) || rows_bad(ldb, G * N) || rows_bad(ldc, G * N) ||
+        (z != nullptr && rows_bad(ldz, H * P)))
+        return LR_ERR_INVALID_ARG;
+    const void *ptrs[] = {x, dt, Bm, Cm, z, A_log, dt_bias, Dskip, lens, S0, y, S_final};
+    for (const void *p : ptrs)
+        if (misaligned(p)) return LR_ERR_MISALIGNED;
+    if (rows_off(ldx, H * P, io) || rows_off(ldb, G * N, io) || rows_off(ldc, G * N, io) ||
+        (z != nullptr && rows_off(ldz, H * P, io)))
+        return LR_ERR_MISALIGNED;
+    return LR_OK;
+}
+}  // namespace
+
+extern "C" size_t lr_selective_heads_workspace_size(int64_t B, int64_t L, int64_t H, int64_t G, int64_t P, int64_t N,
+                                                    lr_dtype io) {
+    return lr_decay_attn_workspace_size(B, L, H, G, N, P, io);
+}
+
+extern "C" int lr_selective_heads_fwd(const void *x, int64_t ldx, const void *dt, int64_t lddt, const void *Bm,
+                                      int64_t ldb, const void *Cm, int64_t ldc, const void *z, int64_t ldz,
+                                      const float *A_log, const float *dt_bias, const float *Dskip,
+                                      const int32_t *lens, const float *S0, void *y, float *S_final, int64_t B,
+                                      int64_t L, int64_t H, int64_t G, int64_t P, int64_t N, lr_dtype io,
+                                      int dt_softplus, void *workspace, size_t ws_bytes, lr_stream_t stream) {
+    int rc = validate_heads(x, ldx, dt, lddt, Bm, ldb, Cm, ldc, z, ldz, A_log, dt_bias, Dskip, lens, S0, y, S_final, B,
+                            L, H, G, P, N, io);
+    if (rc != LR_OK) return rc;
+    if (N > 512) return LR_ERR_UNSUPPORTED;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (B == 0) return lr::status_ok_no_launch(workspace, ws_bytes, st);
+    if (L == 0) {
+        if ((rc = copy_state(S0, S_final, size_t(B) * H * P * N, st)) != LR_OK) return rc;
+        return lr::status_ok_no_launch(workspace, ws_bytes, st);
+    }
+    lr::DecayPlan p;
+    if ((rc = lr::decay_plan(B, L, H, G, N, P, io, &p)) != LR_OK) return rc;
+    if (workspace == nullptr || ws_bytes < p.ws_bytes) return LR_ERR_WORKSPACE;
+    if (misaligned(workspace)) return LR_ERR_MISALIGNED;
+    lr::DecayArgs a{};
+    a.q = Cm, a.k = Bm, a.v = x, a.a_log = A_log, a.g = dt, a.lens = lens, a.S0 = S0, a.o = y, a.S_final = S_final;
+    a.B = B, a.L = L, a.H = int(H), a.Hk = int(G), a.dk = int(N), a.dv = int(P), a.scale = 1.0f;
+    a.hd = lr::HeadsArgs{dt_bias, Dskip, z, ldc, ldb, ldx, lddt, ldz, dt_softplus != 0};
+    return lr::decay_attn_launch(a, io, p, true, workspace, st);
+}
+
+extern "C" int lr_selective_heads_step(const void *x, int64_t ldx, const void *dt, int64_t lddt, const void *Bm,
+                                       int64_t ldb, const void *Cm, int64_t ldc, const void *z, int64_t ldz,
+                                       const float *A_log, const float *dt_bias, const float *Dskip, const float *S_in,
+                                       float *S_out, void *y, int64_t B, int64_t H, int64_t G, int64_t P, int64_t N,
+                                       lr_dtype io, int dt_softplus, lr_stream_t stream) {
+    const int rc = validate_heads(x, ldx, dt, lddt, Bm, ldb, Cm, ldc, z, ldz, A_log, dt_bias, Dskip, nullptr, S_in, y,
+                                  S_out, B, 1, H, G, P, N, io);
+    if (rc == LR_ERR_INVALID_ARG || (B > 0 && S_out == nullptr)) return LR_ERR_INVALID_ARG;
+    if (rc != LR_OK) return rc;
+    const lr::HeadsArgs hd{dt_bias, Dskip, z, ldc, ldb, ldx, lddt, ldz, dt_softplus != 0};
+    return lr::decay_step_launch(Cm, Bm, x, A_log, dt, 1.0f, S_in, S_out, y, B, H, G, N, P, io == LR_BF16, &hd,
+                                 reinterpret_cast<cudaStream_t>(stream));
 }
 
 // ------------------------------- short convolution, norm and rotation of heads

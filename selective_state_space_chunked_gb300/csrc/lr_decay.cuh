@@ -63,6 +63,34 @@ __device__ __forceinline__ float exp2_fix(long long x) {
     return ex2_approx(static_cast<float>(static_cast<uint32_t>(x)) * kFixInv) * __int_as_float((n + 127) << 23);
 }
 
+// Step size of a selective scan with heads from dt + dt_bias.
+__device__ __forceinline__ float step_size(float d, int softplus) {
+    return softplus == 0 || d > 20.0f ? d : log1pf(expf(d));
+}
+
+// A head's decays: of a step with gate value g the log decay, and in `w` the factor of
+// its v k^T.
+template <bool HEADS>
+struct Gates {
+    float l0, bias;
+    int softplus;
+    __device__ __forceinline__ Gates(const DecayArgs &a, int h) {
+        l0 = a.a_log == nullptr ? 0.0f : a.a_log[h];
+        if (HEADS) {
+            l0 = -expf(l0);
+            bias = a.hd.dt_bias == nullptr ? 0.0f : a.hd.dt_bias[h];
+            softplus = a.hd.softplus;
+        }
+    }
+    __device__ __forceinline__ float of(float g, float &w) const {
+        w = HEADS ? step_size(g + bias, softplus) : 1.0f;
+        if (HEADS) return w >= 0.0f ? l0 * w : 1.0f;   // (a negative or NaN step size is out of range)
+        return l0 + g;
+    }
+    // elements between the gates of two steps
+    __device__ __forceinline__ static int64_t pitch(const DecayArgs &a) { return HEADS ? a.hd.ldg : a.H; }
+};
+
 __device__ __forceinline__ int row_len(const int32_t *lens, int b, int64_t L) {
     if (lens == nullptr) return static_cast<int>(L);
     const int n = lens[b];

@@ -6,6 +6,19 @@
 
 namespace lr {
 
+// What a selective scan with heads has beside the decayed attention (HEADS kernels,
+// with q = C, k = B, v = x, g = dt, a_log = A_log, o = y; see lr_selective_heads_fwd):
+//   delta_t = softplus(dt_t + dt_bias),  log decay -exp(A_log) delta_t,
+//   S_t = a_t S_{t-1} + delta_t x_t B_t^T,  y_t = (S_t C_t + skip x_t) silu(z_t)
+// and inputs whose rows lie ld* elements apart.
+struct HeadsArgs {
+    const float *dt_bias;    // (H) or NULL
+    const float *skip;       // (H) or NULL
+    const void *z;           // like v, or NULL
+    int64_t ldq, ldk, ldv, ldg, ldz;
+    int softplus;
+};
+
 // One call, as its kernels see it (device pointers; see lr_decay_attn_fwd).
 struct DecayArgs {
     const void *q, *k, *v;
@@ -37,6 +50,7 @@ struct DecayArgs {
     int parts;
     float *o_part;
     bool by_length;          // blocks take the batch rows by falling length
+    HeadsArgs hd;            // HEADS kernels alone
 };
 
 struct DecayPlan {
@@ -51,12 +65,14 @@ struct DecayPlan {
 };
 
 int decay_plan(int64_t B, int64_t L, int64_t H, int64_t Hk, int64_t dk, int64_t dv, lr_dtype io, DecayPlan *p);
-int decay_attn_launch(DecayArgs a, lr_dtype io, const DecayPlan &p, void *workspace, cudaStream_t stream);
+// heads: a selective scan with heads (a.hd)
+int decay_attn_launch(DecayArgs a, lr_dtype io, const DecayPlan &p, bool heads, void *workspace, cudaStream_t stream);
 
 // CUDA-core kernel, one translation unit per I/O type
-template <typename IO>
+template <typename IO, bool HEADS>
 int decay_general_launch(const DecayArgs &a, const DecayPlan &p, StatusRef st, cudaStream_t stream);
 // tensor-core kernel: bf16 I/O, dk and dv multiples of 8
+template <bool HEADS>
 int decay_tensor_launch(const DecayArgs &a, StatusRef st, cudaStream_t stream);
 constexpr int kOrderRows = 64;      // the largest batch that is taken by length
 constexpr int kDecayChunk = 128;    // its steps per chunk (segments are multiples of it)
@@ -91,9 +107,10 @@ int launch_early(void (*kern)(P...), dim3 grid, int threads, cudaStream_t stream
     return launch_kernel(kern, true, grid, threads, 0, stream, args...);
 }
 
+// hd: a selective scan with heads, or NULL
 int decay_step_launch(const void *q, const void *k, const void *v, const float *a_log, const void *g,
                       float scale, const float *S_in, float *S_out, void *o, int64_t B, int64_t H, int64_t Hk,
-                      int64_t dk, int64_t dv, int io_bf16, cudaStream_t stream);
+                      int64_t dk, int64_t dv, int io_bf16, const HeadsArgs *hd, cudaStream_t stream);
 
 int group_norm_act_launch(const void *x, const void *z, const float *gamma, const float *beta, void *y,
                           int64_t N, int64_t C, int64_t G, float eps, int act, int io_bf16, cudaStream_t stream);

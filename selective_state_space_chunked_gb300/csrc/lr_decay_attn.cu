@@ -97,7 +97,7 @@ int decay_plan(int64_t B, int64_t L, int64_t H, int64_t Hk, int64_t dk, int64_t 
     return LR_OK;
 }
 
-int decay_attn_launch(DecayArgs a, lr_dtype io, const DecayPlan &p, void *workspace, cudaStream_t stream) {
+int decay_attn_launch(DecayArgs a, lr_dtype io, const DecayPlan &p, bool heads, void *workspace, cudaStream_t stream) {
     unsigned char *ws = static_cast<unsigned char *>(workspace) + kStatusBytes;
     const size_t segs = size_t(a.B) * a.H * (p.n_seg - 1);
     a.n_seg = p.n_seg;
@@ -119,9 +119,14 @@ int decay_attn_launch(DecayArgs a, lr_dtype io, const DecayPlan &p, void *worksp
     a.by_length = a.lens != nullptr && a.B > 1 && a.B <= kOrderRows && p.blocks > (p.path == 1 ? 1 : 4) * sms;
     a.o_part = a.seg_state + segs * a.dv * a.dk;
     const StatusRef st = call_status(workspace);
-    if (p.path == 1) return decay_tensor_launch(a, st, stream);
-    return io == LR_BF16 ? decay_general_launch<__nv_bfloat16>(a, p, st, stream)
-                         : decay_general_launch<float>(a, p, st, stream);
+    if (heads) {
+        if (p.path == 1) return decay_tensor_launch<true>(a, st, stream);
+        return io == LR_BF16 ? decay_general_launch<__nv_bfloat16, true>(a, p, st, stream)
+                             : decay_general_launch<float, true>(a, p, st, stream);
+    }
+    if (p.path == 1) return decay_tensor_launch<false>(a, st, stream);
+    return io == LR_BF16 ? decay_general_launch<__nv_bfloat16, false>(a, p, st, stream)
+                         : decay_general_launch<float, false>(a, p, st, stream);
 }
 
 }  // namespace lr

@@ -3,5 +3,5 @@
 #include "lr_decay_general.cuh"
 
 namespace lr {
-template int decay_general_launch<__nv_bfloat16>(const DecayArgs &, const DecayPlan &, StatusRef, cudaStream_t);
+template int decay_general_launch<__nv_bfloat16, false>(const DecayArgs &, const DecayPlan &, StatusRef, cudaStream_t);
 }

@@ -3,7 +3,7 @@
 #include "lr_decay_general.cuh"
 
 namespace lr {
-template int decay_general_launch<float>(const DecayArgs &, const DecayPlan &, StatusRef, cudaStream_t);
+template int decay_general_launch<float, false>(const DecayArgs &, const DecayPlan &, StatusRef, cudaStream_t);
 
 namespace {
 template <int DKP>

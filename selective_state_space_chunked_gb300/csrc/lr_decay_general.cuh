@@ -42,6 +42,7 @@
 #pragma once
 
 #include "lr_decay.cuh"
+#include "lr_vec.cuh"
 
 namespace lr {
 namespace {
@@ -136,8 +137,8 @@ __device__ __forceinline__ void state_st4(float *r, int j, int dk, bool v4, floa
 }
 
 // STATE_ONLY: the first launch of a segmented call (no q, no output; segments
-// 0 .. n_seg - 2).
-template <typename IO, typename C, bool STATE_ONLY>
+// 0 .. n_seg - 2).  HEADS: a selective scan with heads (see HeadsArgs).
+template <typename IO, typename C, bool STATE_ONLY, bool HEADS>
 __global__ void __launch_bounds__(C::NT, C::BPS)
     decay_general_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                          const __grid_constant__ CUtensorMap tm_v, const DecayArgs a, int nrb, bool tma,
@@ -178,12 +179,22 @@ __global__ void __launch_bounds__(C::NT, C::BPS)
     const int64_t s0 = int64_t(seg) * a.seg_len;
     const int64_t send = min(L, s0 + a.seg_len);             // the segment's end
     const int nrun = int(max(int64_t(0), min(int64_t(len), send) - s0));   // its steps inside the row
-    const size_t HK = size_t(a.Hk) * dk, HV = size_t(a.H) * dv;
+    const size_t HV = size_t(a.H) * dv, GP = dec::Gates<HEADS>::pitch(a);
+    const size_t LK = HEADS ? size_t(a.hd.ldk) : size_t(a.Hk) * dk, LQ = HEADS ? size_t(a.hd.ldq) : LK;
+    const size_t LV = HEADS ? size_t(a.hd.ldv) : HV;
     const size_t t_base = size_t(b) * L + s0;
-    const IO *kb = static_cast<const IO *>(a.k) + t_base * HK + size_t(hk) * dk;
-    const IO *qb = static_cast<const IO *>(a.q) + t_base * HK + size_t(hk) * dk;
-    const IO *vb = static_cast<const IO *>(a.v) + t_base * HV + size_t(h) * dv + row0;
-    const IO *gb = a.g == nullptr ? nullptr : static_cast<const IO *>(a.g) + t_base * a.H + h;
+    const IO *kb = static_cast<const IO *>(a.k) + t_base * LK + size_t(hk) * dk;
+    const IO *qb = static_cast<const IO *>(a.q) + t_base * LQ + size_t(hk) * dk;
+    const IO *vb = static_cast<const IO *>(a.v) + t_base * LV + size_t(h) * dv + row0;
+    const IO *gb = a.g == nullptr ? nullptr : static_cast<const IO *>(a.g) + t_base * GP + h;
+    const IO *zb = nullptr;
+    float skip = 0.0f;
+    const bool has_skip = HEADS && a.hd.skip != nullptr;
+    if constexpr (HEADS && !STATE_ONLY) {
+        if (a.hd.z != nullptr)
+            zb = static_cast<const IO *>(a.hd.z) + t_base * size_t(a.hd.ldz) + size_t(h) * dv + row0;
+        if (has_skip) skip = a.hd.skip[h];
+    }
     IO *ob = static_cast<IO *>(a.o) + t_base * HV + size_t(h) * dv + row0;
 
     if (tma) {
@@ -214,11 +225,11 @@ __global__ void __launch_bounds__(C::NT, C::BPS)
         } else {
             const int nt = min(TC, nrun - t0);
             for (int t = 0; t < nt; ++t) {
-                const size_t sk = size_t(t0 + t) * HK, sv = size_t(t0 + t) * HV;
+                const size_t sk = size_t(t0 + t) * LK, sq = size_t(t0 + t) * LQ, sv = size_t(t0 + t) * LV;
                 for (int j = tid; j < dk; j += NT) {
                     const int at = (j / KB) * TC * KB + t * KB + j % KB;
                     kd[at] = kb[sk + j];
-                    if (!STATE_ONLY) qd[at] = qb[sk + j];
+                    if (!STATE_ONLY) qd[at] = qb[sq + j];
                 }
                 for (int r = tid; r < rbv; r += NT) vd[t * RB + r] = vb[sv + r];
             }
@@ -227,16 +238,18 @@ __global__ void __launch_bounds__(C::NT, C::BPS)
 
     // decay factors of a chunk by warp 0, lane t its step t.  base: log2 decay
     // since the last rescale; tot: since the segment's start.
-    const float lh = a.a_log == nullptr ? 0.0f : a.a_log[h];
+    const dec::Gates<HEADS> gates(a, h);
     long long base = 0, tot = 0;
     bool bad = false;
     auto load_g = [&](int c) -> float {
         const int t = c * TC + lane;
-        return gb != nullptr && lane < TC && t < nrun ? Io<IO>::to_f(gb[size_t(t) * a.H]) : 0.0f;
+        return gb != nullptr && lane < TC && t < nrun ? Io<IO>::to_f(gb[size_t(t) * GP]) : 0.0f;
     };
     auto factors = [&](int c, float gv) {   // warp 0
         const int t = c * TC + lane;
-        const long long own = lane < TC && t < nrun ? dec::to_fix(lh + gv, bad) : 0;
+        float wt;
+        const float lt = gates.of(gv, wt);
+        const long long own = lane < TC && t < nrun ? dec::to_fix(lt, bad) : 0;
         long long cum = own;
 #pragma unroll
         for (int m = 1; m < TC; m <<= 1) {
@@ -249,6 +262,7 @@ __global__ void __launch_bounds__(C::NT, C::BPS)
         if (lane < TC) {
             u[lane] = a.scale * (steep ? 1.0f : dec::exp2_fix(base + cum));
             w[lane] = steep ? 1.0f : dec::exp2_fix(-(base + cum));
+            if (HEADS) w[lane] *= wt;
             ma[(c & 1) * TC + lane] = steep ? dec::exp2_fix(own) : 1.0f;
         }
         if (steep) {
@@ -367,7 +381,10 @@ __global__ void __launch_bounds__(C::NT, C::BPS)
                     r[rr] = (acc[rr][0].x + acc[rr][0].y) + (acc[rr][1].x + acc[rr][1].y);
                 row_sums<RT, P>(r, p);
                 const float ut = u[t];
-                if (p < RT) oc[t * RB + rg * RT + p] = ut * r[0];
+                if (p < RT) {
+                    const float y = ut * r[0];
+                    oc[t * RB + rg * RT + p] = has_skip ? fmaf(skip, Io<IO>::to_f(vr[t * RB + p]), y) : y;
+                }
             }
         };
         if (steep) {   // a loop of its own: the common one carries no trace of it
@@ -396,7 +413,12 @@ __global__ void __launch_bounds__(C::NT, C::BPS)
         if (!STATE_ONLY) {
             for (int e = tid; e < TC * RB; e += NT) {
                 const int t = e / RB, r = e % RB;
-                if (t < nt && r < rbv) ob[size_t(c * TC + t) * HV + r] = Io<IO>::from_f(oc[e]);
+                if (t < nt && r < rbv) {
+                    float y = oc[e];
+                    if constexpr (HEADS)
+                        if (zb != nullptr) y *= silu_f(Io<IO>::to_f(zb[size_t(c * TC + t) * a.hd.ldz + r]));
+                    ob[size_t(c * TC + t) * HV + r] = Io<IO>::from_f(y);
+                }
             }
         }
     }
@@ -447,7 +469,7 @@ __global__ void __launch_bounds__(C::NT, C::BPS)
     }
 }
 
-template <typename IO, typename C>
+template <typename IO, typename C, bool HEADS>
 int launch_general_cfg(const DecayArgs &a, StatusRef st, cudaStream_t stream) {
     constexpr int TC = C::template steps<IO>();
     const int nrb = (a.dv + C::RB - 1) / C::RB;
@@ -460,13 +482,14 @@ int launch_general_cfg(const DecayArgs &a, StatusRef st, cudaStream_t stream) {
     if (tma) {
         const auto tt = Io<IO>::kTmType;
         const uint64_t rows = uint64_t(a.B) * a.L;
-        tma = encode_map_3d(&mq, a.q, tt, es, a.dk, a.Hk, rows, C::KB, 1, TC) &&
-              encode_map_3d(&mk, a.k, tt, es, a.dk, a.Hk, rows, C::KB, 1, TC) &&
-              encode_map_3d(&mv, a.v, tt, es, a.dv, a.H, rows, C::RB, 1, TC);
+        const HeadsArgs &hd = a.hd;   // (its pitches are 0 without heads: dense)
+        tma = encode_map_3d(&mq, a.q, tt, es, a.dk, a.Hk, rows, C::KB, 1, TC, hd.ldq) &&
+              encode_map_3d(&mk, a.k, tt, es, a.dk, a.Hk, rows, C::KB, 1, TC, hd.ldk) &&
+              encode_map_3d(&mv, a.v, tt, es, a.dv, a.H, rows, C::RB, 1, TC, hd.ldv);
     }
     const size_t smem = C::template smem_bytes<IO>();
-    auto first = decay_general_kernel<IO, C, true>;
-    auto main = decay_general_kernel<IO, C, false>;
+    auto first = decay_general_kernel<IO, C, true, HEADS>;
+    auto main = decay_general_kernel<IO, C, false, HEADS>;
     if (smem > 48 * 1024 &&
         (cudaFuncSetAttribute(first, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)) != cudaSuccess ||
          cudaFuncSetAttribute(main, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)) != cudaSuccess))
@@ -484,24 +507,24 @@ int launch_general_cfg(const DecayArgs &a, StatusRef st, cudaStream_t stream) {
                          kDefaultTimeoutNs, st);
 }
 
-template <typename IO, int DKP>
+template <typename IO, int DKP, bool HEADS>
 int launch_general_dk(const DecayArgs &a, bool narrow, StatusRef st, cudaStream_t stream) {
-    return narrow ? launch_general_cfg<IO, DecCfg<DKP, true>>(a, st, stream)
-                  : launch_general_cfg<IO, DecCfg<DKP, false>>(a, st, stream);
+    return narrow ? launch_general_cfg<IO, DecCfg<DKP, true>, HEADS>(a, st, stream)
+                  : launch_general_cfg<IO, DecCfg<DKP, false>, HEADS>(a, st, stream);
 }
 
 }  // namespace
 
-template <typename IO>
+template <typename IO, bool HEADS>
 int decay_general_launch(const DecayArgs &a, const DecayPlan &p, StatusRef st, cudaStream_t stream) {
-    if (a.dk <= 32) return launch_general_dk<IO, 32>(a, p.narrow, st, stream);
-    if (a.dk <= 64) return launch_general_dk<IO, 64>(a, p.narrow, st, stream);
-    if (a.dk <= 128) return launch_general_dk<IO, 128>(a, p.narrow, st, stream);
+    if (a.dk <= 32) return launch_general_dk<IO, 32, HEADS>(a, p.narrow, st, stream);
+    if (a.dk <= 64) return launch_general_dk<IO, 64, HEADS>(a, p.narrow, st, stream);
+    if (a.dk <= 128) return launch_general_dk<IO, 128, HEADS>(a, p.narrow, st, stream);
     if (a.dk <= 256) {
-        if constexpr (sizeof(IO) == 4) return launch_general_dk<IO, 256>(a, p.narrow, st, stream);
-        return launch_general_cfg<IO, DecCfg<256, false>>(a, st, stream);
+        if constexpr (sizeof(IO) == 4) return launch_general_dk<IO, 256, HEADS>(a, p.narrow, st, stream);
+        return launch_general_cfg<IO, DecCfg<256, false>, HEADS>(a, st, stream);
     }
-    return launch_general_cfg<IO, DecCfg<512, false>>(a, st, stream);
+    return launch_general_cfg<IO, DecCfg<512, false>, HEADS>(a, st, stream);
 }
 
 }  // namespace lr

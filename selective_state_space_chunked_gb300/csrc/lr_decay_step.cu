@@ -23,6 +23,7 @@
 //   dk up to 512 in the same form: B32 H16 dk192 18.7 us against 36 with a row
 //   read element by element, which stays for dk that is no multiple of four
 #include "lr_decay.cuh"
+#include "lr_vec.cuh"
 
 namespace lr {
 namespace {
@@ -47,13 +48,37 @@ __device__ __forceinline__ float4 step_ld4<__nv_bfloat16>(const __nv_bfloat16 *p
 
 constexpr int kStepT = 64;
 
+// A head's decay of the token and what its output takes beside the state's.
+template <bool HEADS>
+struct StepDecay {
+    float a, delta, skip;
+    __device__ __forceinline__ StepDecay(const float *a_log, float g, const HeadsArgs &hd, int h) {
+        float l = a_log != nullptr ? a_log[h] : 0.0f;
+        if (HEADS) {
+            delta = dec::step_size(g + (hd.dt_bias != nullptr ? hd.dt_bias[h] : 0.0f), hd.softplus);
+            skip = hd.skip != nullptr ? hd.skip[h] : 0.0f;
+            l = -expf(l) * delta;
+        } else {
+            l += g;
+        }
+        a = expf(l);
+    }
+    __device__ __forceinline__ float out(float y, float x, float z, const HeadsArgs &hd) const {
+        if (!HEADS) return y;
+        if (hd.skip != nullptr) y = fmaf(skip, x, y);
+        return hd.z != nullptr ? y * silu_f(z) : y;
+    }
+};
+
 // dk % 4 == 0 and dk <= 4 TL V: V groups of four keys per lane.
 // A warp takes 32 / TL rows at a time, R times.  20 blocks per SM leave 48 registers
 // (B64 22.9 us with 52).
-template <typename IO, int TL, int R, int V>
+// HEADS: one token of a selective scan with heads (see HeadsArgs).
+template <typename IO, int TL, int R, int V, bool HEADS>
 __global__ void __launch_bounds__(kStepT, V == 1 ? 20 : V == 2 ? 1 : 12)
     decay_step_kernel(const IO *q, const IO *k, const IO *v, const float *a_log, const IO *g, float scale,
-                      const float *S_in, float *S_out, IO *o, int64_t BH, int H, int Hk, int dk, int dv, int tiles) {
+                      const float *S_in, float *S_out, IO *o, int64_t BH, int H, int Hk, int dk, int dv, int tiles,
+                      HeadsArgs hd) {
     constexpr int RPW = 32 / TL;          // rows a warp holds at once
     constexpr int ROWS = RPW * R;         // rows per warp
     const int lane = threadIdx.x & 31, sub = lane / TL, j0 = 4 * (lane % TL);
@@ -83,24 +108,29 @@ __global__ void __launch_bounds__(kStepT, V == 1 ? 20 : V == 2 ? 1 : 12)
 #pragma unroll
     for (int u = 0; u < V; ++u) {
         const int j = j0 + 4 * TL * u;
-        const int64_t kat = (b * Hk + hk) * dk + j;
+        const int64_t kat = (HEADS ? b * hd.ldk + int64_t(hk) * dk : (b * Hk + hk) * dk) + j;
+        const int64_t qat = HEADS ? b * hd.ldq + int64_t(hk) * dk + j : kat;
         k4[u] = j < dk ? step_ld4(k + kat) : zero;
-        q4[u] = j < dk ? step_ld4(q + kat) : zero;
+        q4[u] = j < dk ? step_ld4(q + qat) : zero;
     }
-    float vr[R];   // before the first store, which may be to anywhere
+    float vr[R], zr[HEADS ? R : 1];   // before the first store, which may be to anywhere
 #pragma unroll
     for (int r = 0; r < R; ++r) {
         const int i = row0 + r * RPW + sub;
-        vr[r] = i < dv ? Io<IO>::to_f(v[base + i]) : 0.0f;
+        vr[r] = i < dv ? Io<IO>::to_f(v[HEADS ? b * hd.ldv + int64_t(h) * dv + i : base + i]) : 0.0f;
+        if (HEADS)
+            zr[r] = hd.z != nullptr && i < dv
+                        ? Io<IO>::to_f(static_cast<const IO *>(hd.z)[b * hd.ldz + int64_t(h) * dv + i])
+                        : 0.0f;
     }
-    float l = a_log != nullptr ? a_log[h] : 0.0f;
-    if (g != nullptr) l += Io<IO>::to_f(g[bh]);
-    const float a = expf(l);
+    const StepDecay<HEADS> dc(a_log, HEADS ? Io<IO>::to_f(g[b * hd.ldg + h]) : g != nullptr ? Io<IO>::to_f(g[bh]) : 0.0f,
+                              hd, h);
+    const float a = dc.a;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
         const int i = row0 + r * RPW + sub;
         const bool in = i < dv;
-        const float vi = vr[r];
+        const float vi = HEADS ? dc.delta * vr[r] : vr[r];
         float acc = 0.0f;
 #pragma unroll
         for (int u = 0; u < V; ++u) {
@@ -113,15 +143,16 @@ __global__ void __launch_bounds__(kStepT, V == 1 ? 20 : V == 2 ? 1 : 12)
         }
 #pragma unroll
         for (int m = TL / 2; m >= 1; m >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, m);
-        if (in && lane % TL == 0) o[base + i] = Io<IO>::from_f(scale * acc);
+        if (in && lane % TL == 0) o[base + i] = Io<IO>::from_f(dc.out(scale * acc, vr[r], HEADS ? zr[r] : 0.0f, hd));
     }
 }
 
 // any dk: one warp per row
-template <typename IO>
+template <typename IO, bool HEADS>
 __global__ void __launch_bounds__(kStepT)
     decay_step_any_kernel(const IO *q, const IO *k, const IO *v, const float *a_log, const IO *g, float scale,
-                          const float *S_in, float *S_out, IO *o, int64_t BH, int H, int Hk, int dk, int dv) {
+                          const float *S_in, float *S_out, IO *o, int64_t BH, int H, int Hk, int dk, int dv,
+                          HeadsArgs hd) {
     const int64_t row = int64_t(blockIdx.x) * (kStepT / 32) + (threadIdx.x >> 5);
     const int lane = threadIdx.x & 31;
     launch_dependents();
@@ -129,10 +160,13 @@ __global__ void __launch_bounds__(kStepT)
     if (row >= BH * dv) return;   // warp-uniform
     const int64_t bh = row / dv, b = bh / H;
     const int h = int(bh - b * H), hk = h / (H / Hk);
-    float l = a_log != nullptr ? a_log[h] : 0.0f;
-    if (g != nullptr) l += Io<IO>::to_f(g[bh]);
-    const float a = expf(l), vi = Io<IO>::to_f(v[row]);
-    const IO *kb = k + (b * Hk + hk) * dk, *qb = q + (b * Hk + hk) * dk;
+    const StepDecay<HEADS> dc(a_log, HEADS ? Io<IO>::to_f(g[b * hd.ldg + h]) : g != nullptr ? Io<IO>::to_f(g[bh]) : 0.0f,
+                              hd, h);
+    const int64_t at = int64_t(h) * dv + (row - bh * dv);
+    const float a = dc.a, x = Io<IO>::to_f(v[HEADS ? b * hd.ldv + at : row]), vi = HEADS ? dc.delta * x : x;
+    const float z = HEADS && hd.z != nullptr ? Io<IO>::to_f(static_cast<const IO *>(hd.z)[b * hd.ldz + at]) : 0.0f;
+    const IO *kb = k + (HEADS ? b * hd.ldk + int64_t(hk) * dk : (b * Hk + hk) * dk);
+    const IO *qb = q + (HEADS ? b * hd.ldq + int64_t(hk) * dk : (b * Hk + hk) * dk);
     float acc = 0.0f;
 #pragma unroll 4
     for (int j = lane; j < dk; j += 32) {
@@ -143,47 +177,49 @@ __global__ void __launch_bounds__(kStepT)
     }
 #pragma unroll
     for (int m = 16; m >= 1; m >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, m);
-    if (lane == 0) o[row] = Io<IO>::from_f(scale * acc);
+    if (lane == 0) o[row] = Io<IO>::from_f(dc.out(scale * acc, x, z, hd));
 }
 
-template <typename IO>
+template <typename IO, bool HEADS>
 int step_io(const IO *q, const IO *k, const IO *v, const float *a_log, const IO *g, float scale,
             const float *S_in, float *S_out, IO *o, int64_t B, int64_t H, int64_t Hk, int64_t dk, int64_t dv,
-            cudaStream_t s) {
+            const HeadsArgs &hd, cudaStream_t s) {
     const int64_t BH = B * H;
     auto go = [&](auto kern, int rows) -> int {
         const int64_t tiles = (dv + rows - 1) / rows;
         const int64_t grid = (BH * tiles + kStepT / 32 - 1) / (kStepT / 32);
         if (grid > INT32_MAX) return LR_ERR_UNSUPPORTED;
         return launch_early(kern, dim3(unsigned(grid)), kStepT, s, q, k, v, a_log, g, scale, S_in, S_out, o, BH, H,
-                            Hk, dk, dv, tiles);
+                            Hk, dk, dv, tiles, hd);
     };
     if (dk % 4 == 0 && dk <= 512) {
-        if (dk <= 32) return go(decay_step_kernel<IO, 8, 4, 1>, 16);
-        if (dk <= 64) return go(decay_step_kernel<IO, 16, 4, 1>, 8);
-        if (dk <= 128) return go(decay_step_kernel<IO, 32, 4, 1>, 4);
-        if (dk <= 256) return go(decay_step_kernel<IO, 32, 2, 2>, 2);
-        return go(decay_step_kernel<IO, 32, 2, 4>, 2);
+        if (dk <= 32) return go(decay_step_kernel<IO, 8, 4, 1, HEADS>, 16);
+        if (dk <= 64) return go(decay_step_kernel<IO, 16, 4, 1, HEADS>, 8);
+        if (dk <= 128) return go(decay_step_kernel<IO, 32, 4, 1, HEADS>, 4);
+        if (dk <= 256) return go(decay_step_kernel<IO, 32, 2, 2, HEADS>, 2);
+        return go(decay_step_kernel<IO, 32, 2, 4, HEADS>, 2);
     }
     const int64_t grid = (BH * dv + kStepT / 32 - 1) / (kStepT / 32);
     if (grid > INT32_MAX) return LR_ERR_UNSUPPORTED;
-    return launch_early(decay_step_any_kernel<IO>, dim3(unsigned(grid)), kStepT, s, q, k, v, a_log, g, scale, S_in,
-                        S_out, o, BH, H, Hk, dk, dv);
+    return launch_early(decay_step_any_kernel<IO, HEADS>, dim3(unsigned(grid)), kStepT, s, q, k, v, a_log, g, scale, S_in,
+                        S_out, o, BH, H, Hk, dk, dv, hd);
 }
 
 }  // namespace
 
 int decay_step_launch(const void *q, const void *k, const void *v, const float *a_log, const void *g,
                       float scale, const float *S_in, float *S_out, void *o, int64_t B, int64_t H, int64_t Hk,
-                      int64_t dk, int64_t dv, int io_bf16, cudaStream_t stream) {
+                      int64_t dk, int64_t dv, int io_bf16, const HeadsArgs *hd, cudaStream_t stream) {
     if (B == 0) return LR_OK;
-    using bf = __nv_bfloat16;
-    return io_bf16 ? step_io<bf>(static_cast<const bf *>(q), static_cast<const bf *>(k), static_cast<const bf *>(v),
-                                 a_log, static_cast<const bf *>(g), scale, S_in, S_out, static_cast<bf *>(o), B, H,
-                                 Hk, dk, dv, stream)
-                   : step_io<float>(static_cast<const float *>(q), static_cast<const float *>(k),
-                                    static_cast<const float *>(v), a_log, static_cast<const float *>(g), scale, S_in,
-                                    S_out, static_cast<float *>(o), B, H, Hk, dk, dv, stream);
+    auto io = [&](auto one) {
+        using IO = decltype(one);
+        auto c = [](const void *p) { return static_cast<const IO *>(p); };
+        return hd != nullptr ? step_io<IO, true>(c(q), c(k), c(v), a_log, c(g), scale, S_in, S_out, static_cast<IO *>(o), B,
+                                                 H, Hk, dk, dv, *hd, stream)
+                             : step_io<IO, false>(c(q), c(k), c(v), a_log, c(g), scale, S_in, S_out, static_cast<IO *>(o),
+                                                  B, H, Hk, dk, dv, HeadsArgs{}, stream);
+    };
+    return io_bf16 ? io(__nv_bfloat16()) : io(0.0f);
 }
 
 }  // namespace lr

@@ -117,8 +117,9 @@ int hgrn2_launch(const void *q, const void *k, const void *v, const void *g, con
                  cudaStream_t stream, bool preact = false, float lb = 0.0f);
 // 3-D TMA map over a row-major (d2, d1, d0) tensor with a (b0, b1, b2) box,
 // no swizzle, zero fill outside the tensor; false if the driver refuses it.
+// ld: elements between neighbours of d2, 0: d0 d1.
 bool encode_map_3d(CUtensorMap *tm, const void *base, CUtensorMapDataType type, size_t esize,
-                   uint64_t d0, uint64_t d1, uint64_t d2, uint32_t b0, uint32_t b1, uint32_t b2);
+                   uint64_t d0, uint64_t d1, uint64_t d2, uint32_t b0, uint32_t b1, uint32_t b2, uint64_t ld = 0);
 
 // HGRN2 for fp32 I/O and head dims other than 128 x 128 (CUDA cores, step by step)
 // redo != NULL: only the heads whose redo word holds `stamp` run (the heads

@@ -215,6 +215,30 @@ def decay_attn_inputs(B: int, L: int, H: int, dk: int, dv: int, seed: int, io: s
     }
 
 
+def selective_heads_inputs(B: int, L: int, H: int, G: int, P: int, N: int, seed: int, io: str = "bf16",
+                           z: bool = True, skip: bool = True, with_S0: bool = False, rate=(1.0, 16.0),
+                           device="cpu") -> dict:
+    """Inputs of the selective scan with heads: step sizes log-uniform over 1e-3 .. 1e-1
+    per head (as dt_bias) under noise, decay rates spread over ``rate``.  Draw order: x,
+    dt, Bm, Cm, z, dt_bias, Dskip, S0."""
+    gen = _gen(seed, device)
+    dt = _dtype(io)
+
+    def normal(*shape, std=1.0):
+        return std * torch.randn(*shape, generator=gen, device=device)
+
+    x, d, Bm, Cm = normal(B, L, H * P), normal(B, L, H, std=0.5), normal(B, L, G * N), normal(B, L, G * N)
+    zz = normal(B, L, H * P)
+    size = torch.exp(math.log(1e-3) + math.log(100.0) * torch.rand(H, generator=gen, device=device))
+    sk = 1.0 + 0.1 * normal(H)
+    S0 = normal(B, H, P, N, std=0.5) if with_S0 else None
+    return {
+        "x": x.to(dt), "dt": d.to(dt), "Bm": Bm.to(dt), "Cm": Cm.to(dt), "z": zz.to(dt) if z else None,
+        "A_log": torch.linspace(math.log(rate[0]), math.log(rate[1]), H, device=device),
+        "dt_bias": torch.log(torch.expm1(size)), "Dskip": sk if skip else None, "S0": S0, "H": H, "G": G,
+    }
+
+
 def make_inputs(cfg: Config, device="cpu", B: Optional[int] = None,
                 L: Optional[int] = None) -> dict:
     """Inputs of a workload, optionally with B or L overridden (same seed and

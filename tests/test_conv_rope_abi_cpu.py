@@ -66,6 +66,10 @@ def test_helpers_refuse_wrong_shapes_and_types(lr):  # noqa: F811
             lr.causal_conv(x, bad)
     with pytest.raises(ValueError):
         lr.causal_conv(x[0], w)
+    with pytest.raises(ValueError):
+        lr.causal_conv(x, w, lens=t(3, dtype=torch.int32))
+    with pytest.raises(TypeError):
+        lr.causal_conv(x, w, lens=t(2))
     with pytest.raises(TypeError):
         lr.causal_conv(x, w, state=t(2, 3, 64).bfloat16())
     with pytest.raises(TypeError):
