@@ -353,7 +353,8 @@ int lr_decay_attn_fwd(const void *q, const void *k, const void *v,
  * Requirements: H, G, P, N >= 1, H % G == 0, ld* >= their widths (else
  *          LR_ERR_INVALID_ARG); N <= 512 (else LR_ERR_UNSUPPORTED); ldx, ldb, ldc, ldz
  *          the width or a multiple of 16 bytes (else LR_ERR_MISALIGNED).
- * Workspace: that of lr_decay_attn_workspace_size(B, L, H, G, N, P, io).
+ * Workspace: as for lr_decay_attn_fwd, and with bf16 I/O on the tensor cores about 25
+ *          bytes for every step of every head, which hold what its gates come to.
  */
 size_t lr_selective_heads_workspace_size(int64_t B, int64_t L, int64_t H, int64_t G,
                                          int64_t P, int64_t N, lr_dtype io);

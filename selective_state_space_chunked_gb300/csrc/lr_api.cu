@@ -504,7 +504,7 @@ extern "C" size_t lr_decay_attn_workspace_size(int64_t B, int64_t L, int64_t H, 
     if (validate_decay_sizes(B, L, H, Hk, dk, dv, io) != LR_OK || dk > 512) return 0;
     if (B == 0 || L == 0) return lr::kStatusBytes;
     lr::DecayPlan p;
-    if (lr::decay_plan(B, L, H, Hk, dk, dv, io, &p) != LR_OK) return SIZE_MAX;
+    if (lr::decay_plan(B, L, H, Hk, dk, dv, io, false, &p) != LR_OK) return SIZE_MAX;
     return p.ws_bytes;
 }
 
@@ -521,7 +521,7 @@ extern "C" int lr_decay_attn_fwd(const void *q, const void *k, const void *v, co
         return lr::status_ok_no_launch(workspace, ws_bytes, st);
     }
     lr::DecayPlan p;
-    if ((rc = lr::decay_plan(B, L, H, Hk, dk, dv, io, &p)) != LR_OK) return rc;
+    if ((rc = lr::decay_plan(B, L, H, Hk, dk, dv, io, false, &p)) != LR_OK) return rc;
     if (workspace == nullptr || ws_bytes < p.ws_bytes) return LR_ERR_WORKSPACE;
     if (misaligned(workspace)) return LR_ERR_MISALIGNED;
     lr::DecayArgs a{};
@@ -592,7 +592,11 @@ int validate_heads(const void *x, int64_t ldx, const void *dt, int64_t lddt, con
 
 extern "C" size_t lr_selective_heads_workspace_size(int64_t B, int64_t L, int64_t H, int64_t G, int64_t P, int64_t N,
                                                     lr_dtype io) {
-    return lr_decay_attn_workspace_size(B, L, H, G, N, P, io);
+    if (validate_decay_sizes(B, L, H, G, N, P, io) != LR_OK || N > 512) return 0;
+    if (B == 0 || L == 0) return lr::kStatusBytes;
+    lr::DecayPlan p;
+    if (lr::decay_plan(B, L, H, G, N, P, io, true, &p) != LR_OK) return SIZE_MAX;
+    return p.ws_bytes;
 }
 
 extern "C" int lr_selective_heads_fwd(const void *x, int64_t ldx, const void *dt, int64_t lddt, const void *Bm,
@@ -612,7 +616,7 @@ extern "C" int lr_selective_heads_fwd(const void *x, int64_t ldx, const void *dt
         return lr::status_ok_no_launch(workspace, ws_bytes, st);
     }
     lr::DecayPlan p;
-    if ((rc = lr::decay_plan(B, L, H, G, N, P, io, &p)) != LR_OK) return rc;
+    if ((rc = lr::decay_plan(B, L, H, G, N, P, io, true, &p)) != LR_OK) return rc;
     if (workspace == nullptr || ws_bytes < p.ws_bytes) return LR_ERR_WORKSPACE;
     if (misaligned(workspace)) return LR_ERR_MISALIGNED;
     lr::DecayArgs a{};

@@ -63,9 +63,25 @@ __device__ __forceinline__ float exp2_fix(long long x) {
     return ex2_approx(static_cast<float>(static_cast<uint32_t>(x)) * kFixInv) * __int_as_float((n + 127) << 23);
 }
 
-// Step size of a selective scan with heads from dt + dt_bias.
-__device__ __forceinline__ float step_size(float d, int softplus) {
-    return softplus == 0 || d > 20.0f ? d : log1pf(expf(d));
+// Step size of a selective scan with heads from dt + dt_bias.  softplus(x) = max(x, 0) +
+// log1p(e), e = exp(-|x|) in (0, 1], with log1p(e) / e as a polynomial of degree 9 (its
+// interpolation at Chebyshev nodes): 1.5e-7 relative with the roundings, at every x.
+// The library's log1pf(expf(x)), four times in a row in one warp, took a chunk of the
+// tensor-core kernel 10000 clocks against 4200 without.
+__device__ __forceinline__ float step_size(float x, int softplus) {
+    if (softplus == 0) return x;
+    const float e = expf(-fabsf(x));
+    float q = -0.00325637846f;
+    q = fmaf(q, e, 0.0199071616f);
+    q = fmaf(q, e, -0.0570642017f);
+    q = fmaf(q, e, 0.106142648f);
+    q = fmaf(q, e, -0.153118625f);
+    q = fmaf(q, e, 0.196781173f);
+    q = fmaf(q, e, -0.249545589f);
+    q = fmaf(q, e, 0.333300054f);
+    q = fmaf(q, e, -0.499999046f);
+    q = fmaf(q, e, 1.0f);
+    return fmaf(q, e, x > 0.0f ? x : 0.0f);
 }
 
 // A head's decays: of a step with gate value g the log decay, and in `w` the factor of

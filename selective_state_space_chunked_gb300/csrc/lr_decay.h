@@ -17,7 +17,15 @@ struct HeadsArgs {
     const void *z;           // like v, or NULL
     int64_t ldq, ldk, ldv, ldg, ldz;
     int softplus;
+    // Tensor cores: what a first launch makes of the gates (lr_heads_tensor.cu), for
+    // every step of every (batch row, head), in whole chunks, and for every chunk.
+    float *weight, *readout, *to_end;
+    float2 *own;
+    unsigned char *chunk;
+    float *left;             // [batch row, head][segment]
 };
+constexpr int kChunkRecord = 560;   // bytes of a chunk's
+
 
 // One call, as its kernels see it (device pointers; see lr_decay_attn_fwd).
 struct DecayArgs {
@@ -64,16 +72,17 @@ struct DecayPlan {
     size_t ws_bytes = 0;     // status, then seg_tot, seg_bad, seg_state, o_part
 };
 
-int decay_plan(int64_t B, int64_t L, int64_t H, int64_t Hk, int64_t dk, int64_t dv, lr_dtype io, DecayPlan *p);
 // heads: a selective scan with heads (a.hd)
+int decay_plan(int64_t B, int64_t L, int64_t H, int64_t Hk, int64_t dk, int64_t dv, lr_dtype io, bool heads,
+               DecayPlan *p);
 int decay_attn_launch(DecayArgs a, lr_dtype io, const DecayPlan &p, bool heads, void *workspace, cudaStream_t stream);
 
 // CUDA-core kernel, one translation unit per I/O type
 template <typename IO, bool HEADS>
 int decay_general_launch(const DecayArgs &a, const DecayPlan &p, StatusRef st, cudaStream_t stream);
-// tensor-core kernel: bf16 I/O, dk and dv multiples of 8
-template <bool HEADS>
+// tensor-core kernels: bf16 I/O, dk and dv multiples of 8
 int decay_tensor_launch(const DecayArgs &a, StatusRef st, cudaStream_t stream);
+int heads_tensor_launch(const DecayArgs &a, StatusRef st, cudaStream_t stream);
 constexpr int kOrderRows = 64;      // the largest batch that is taken by length
 constexpr int kDecayChunk = 128;    // its steps per chunk (segments are multiples of it)
 constexpr int kDecayRows = 64;      // its value rows per block

@@ -37,10 +37,17 @@ constexpr double kFirstCost = 0.6, kBlockCost = 3.0, kStateCost = 1.0;
 
 namespace {
 size_t tot_bytes(size_t segs) { return (segs * sizeof(long long) + 15) / 16 * 16; }
+// a scan's gates: per step a weight, a readout factor, one to the segment's end and
+// two of its own; per chunk a record; per segment what is left
+size_t gate_bytes(size_t bh, int64_t L, int n_seg) {
+    const size_t chunks = bh * size_t((L + kDecayChunk - 1) / kDecayChunk);
+    return chunks * (kDecayChunk * 5 * sizeof(float) + kChunkRecord) + (bh * n_seg * sizeof(float) + 15) / 16 * 16;
+}
 size_t bad_bytes(size_t segs, const DecayPlan &p) { return (segs * p.tiles * sizeof(int) + 15) / 16 * 16; }
 }  // namespace
 
-int decay_plan(int64_t B, int64_t L, int64_t H, int64_t Hk, int64_t dk, int64_t dv, lr_dtype io, DecayPlan *p) {
+int decay_plan(int64_t B, int64_t L, int64_t H, int64_t Hk, int64_t dk, int64_t dv, lr_dtype io, bool heads,
+               DecayPlan *p) {
     (void)Hk;
     int sms = 0;
     if (device_sm_count(&sms) != LR_OK) return LR_ERR_CUDA;
@@ -94,6 +101,7 @@ int decay_plan(int64_t B, int64_t L, int64_t H, int64_t Hk, int64_t dk, int64_t 
     const size_t segs = size_t(B) * H * (p->n_seg - 1);
     p->ws_bytes = kStatusBytes + tot_bytes(segs) + bad_bytes(segs, *p) + segs * dv * dk * sizeof(float);
     if (p->parts > 1) p->ws_bytes += size_t(p->parts) * B * L * H * dv * sizeof(float);
+    if (heads && p->path == 1) p->ws_bytes = (p->ws_bytes + 15) / 16 * 16 + gate_bytes(B * H, L, p->n_seg);
     return LR_OK;
 }
 
@@ -120,11 +128,22 @@ int decay_attn_launch(DecayArgs a, lr_dtype io, const DecayPlan &p, bool heads, 
     a.o_part = a.seg_state + segs * a.dv * a.dk;
     const StatusRef st = call_status(workspace);
     if (heads) {
-        if (p.path == 1) return decay_tensor_launch<true>(a, st, stream);
+        if (p.path == 1) {
+            const size_t bh = size_t(a.B) * a.H, chunks = bh * size_t((a.L + kDecayChunk - 1) / kDecayChunk);
+            const size_t steps = chunks * kDecayChunk;
+            unsigned char *g = static_cast<unsigned char *>(workspace) + p.ws_bytes - gate_bytes(bh, a.L, p.n_seg);
+            a.hd.chunk = g;
+            a.hd.weight = reinterpret_cast<float *>(g + chunks * kChunkRecord);
+            a.hd.readout = a.hd.weight + steps;
+            a.hd.to_end = a.hd.readout + steps;
+            a.hd.own = reinterpret_cast<float2 *>(a.hd.to_end + steps);
+            a.hd.left = reinterpret_cast<float *>(a.hd.own + steps);
+            return heads_tensor_launch(a, st, stream);
+        }
         return io == LR_BF16 ? decay_general_launch<__nv_bfloat16, true>(a, p, st, stream)
                              : decay_general_launch<float, true>(a, p, st, stream);
     }
-    if (p.path == 1) return decay_tensor_launch<false>(a, st, stream);
+    if (p.path == 1) return decay_tensor_launch(a, st, stream);
     return io == LR_BF16 ? decay_general_launch<__nv_bfloat16, false>(a, p, st, stream)
                          : decay_general_launch<float, false>(a, p, st, stream);
 }

@@ -1,6 +1,1079 @@
-// lr_heads_tensor.cu -- selective scan with heads on the tensor cores
+// lr_heads_tensor.cu -- selective scan with heads, bf16 I/O, on the sm_103a tensor
+// cores (tcgen05, accumulators in TMEM, operands by TMA):
+//
+//   S_t = a_t S_{t-1} + d_t x_t B_t^T,   y_t = (S_t C_t + skip x_t) silu(z_t),
+//   d_t = softplus(dt_t + bias),   a_t = exp(-exp(A_log) d_t)
+//
+// The chunked form is the decayed attention's (lr_decay_tensor.cu, whose comment has the
+// mathematics, the precision and what infinities do), with q = C, k = B, v = x and a
+// step size beside every decay weight:
+//
+//   O  = [(Q K^T) . D + skip I] V + diag(2^L) Q S^T,   D_ts = d_s 2^(L_t - L_s), s <= t
+//   S' = 2^L_C S + sum_s d_s 2^(L_C - L_s) v_s k_s^T
+//
+// The step sizes go into the factors that the columns of Q K^T and the state's weights
+// have anyway, and the skip onto the diagonal before it is rounded to bf16, so both cost
+// the chain of a chunk's hand-overs nothing.
+//
+// What the gates come to is made by a launch of its own: softplus, the sums of log
+// decays in 64-bit fixed point and the powers are the same for every block of a head's
+// value rows, and one warp of the main kernel that did them took longer than a chunk
+// (10000 clocks of a chunk's 4600 with the library's log1pf, 4200 without a softplus).
+// Per step it leaves the state's weight, the readout's factor and the step's own two
+// values, per chunk the column factors, and each role of the main kernel loads its own
+// a chunk ahead.
+//
+// A steep chunk (past 2^-40) forms D in blocks of 16 columns: rows past the block take it
+// as 2^(L_t - L_e) times the columns' d_s 2^(L_e - L_s), e the block's last step, both
+// <= 1; only the two blocks that a row's diagonal crosses take a power an element.
+//
+// A thread block owns 64 value rows of one (batch row, head, time segment), 128 key
+// columns.  Roles, connected by mbarriers: state (8 warps), output (8: 32 rows by 32
+// columns a warp, so that all of a thread's outputs are in registers before the
+// accumulator is handed back, and gate and stores come after that), front (8), weight (4),
+// TMA, and one warp for each of dS, P and O's products.  TMEM: P 2 x 128 columns (PD
+// inside), O 64, dS 3 x 64.
 #include "lr_decay_tensor.cuh"
 
 namespace lr {
-template int decay_tensor_launch<true>(const DecayArgs &, StatusRef, cudaStream_t);
+
+namespace ht {
+using dt::arrive;
+using dt::Ctl;
+using dt::elect_one;
+using dt::hi_f;
+using dt::kRescaleTensor;
+using dt::kSteepChunk;
+using dt::lo_f;
+using dt::not_finite;
+using dt::pack;
+using dt::three_terms;
+using dt::wait_slow;
+constexpr int C = kDecayChunk;
+constexpr int RB = kDecayRows;
+constexpr int OUT = 8, FRONT = 16, WEIGHT = 24, TMA_WARP = 28, DS_WARP = 29, P_WARP = 30;   // 31: O
+constexpr int THREADS = 32 * 32;
+
+// What the gates' launch leaves of a chunk.
+struct Chunk {
+    float col[C];    // column factors of P: w d; steep: d 2^(L_e - L_s), e the last step of s' 16
+    float m;         // the state's factor (1: none)
+    int steep;
+    int pad[2];
+    int last[8];     // steep: L of every 16 steps' last, see units_of
+};
+static_assert(sizeof(Chunk) == kChunkRecord, "");
+
+constexpr uint32_t HALF = C * 128;              // 64 columns of Q or K: 128 rows of 128 bytes
+constexpr uint32_t Q_BYTES = 2 * HALF, V_BYTES = C * RB * 2;
+constexpr uint32_t OFF_Q = 0, OFF_K = 2 * Q_BYTES, OFF_V = 4 * Q_BYTES;
+constexpr uint32_t OFF_W = OFF_V + 2 * V_BYTES;     // three terms [128 s][64 i]
+constexpr uint32_t OFF_SB = OFF_W + 3 * V_BYTES;    // bf16 state [128 j][64 i]
+constexpr uint32_t OFF_G = OFF_SB + 128 * RB * 2;   // 2 x Chunk
+constexpr uint32_t OFF_BAR = OFF_G + 2 * kChunkRecord;
+// barriers; [2] by chunk parity, [4] by quarter
+enum {
+    FULL_Q = 0, EMPTY_Q = 2, FULL_K = 4, EMPTY_K = 6, FULL_V = 8, EMPTY_V = 10,
+    FULL_G = 12,     // the chunk's record
+    P_READY = 14,    // P_c complete
+    F_DONE = 16,     // PD_c written (8 front warps)
+    K_DONE = 18,     // chunk c's outputs read (8 output warps)
+    OX_DONE = 20,    // Q S^T complete: the bf16 state has been read
+    O_DONE = 22,
+    W_READY = 24,    // weighted values of a quarter
+    W_FREE = 28,
+    SB_READY = 32,   // bf16 state before chunk c (8 state warps)
+    DS_DONE, DS_FREE,
+    FIX,             // a steep chunk's Q S^T scaled (8 output warps)
+    MMA_END, NBAR
+};
+constexpr uint32_t OFF_TMEM = OFF_BAR + NBAR * 8;
+constexpr uint32_t OFF_CTL = OFF_TMEM + 8;
+constexpr uint32_t SMEM = OFF_CTL + 40;
+static_assert(OFF_BAR % 8 == 0 && OFF_CTL % 8 == 0, "");
+static_assert(SMEM <= 227 * 1024, "one block per SM");
+
+constexpr uint32_t T_P = 0, T_O = 256, T_DS = 320;
+constexpr uint32_t IDESC_P = umma_idesc_bf16(128, 128, 0, 0);
+constexpr uint32_t IDESC_O = umma_idesc_bf16(128, 64, 0, 1);
+constexpr uint32_t IDESC_DS = umma_idesc_bf16(128, 192, 1, 1);
+
+// `bytes` (a multiple of 16) from global to shared memory, both 16-byte aligned.
+__device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_u32(dst)),
+        "l"(src), "r"(bytes), "r"(smem_u32(bar))
+        : "memory");
 }
+
+// Position of a (batch row, head)'s step in the gates' arrays, and of its chunk's record.
+__device__ __forceinline__ size_t step_at(const DecayArgs &a, int64_t bh, int64_t t) {
+    return size_t(bh) * ((a.L + C - 1) / C * C) + t;
+}
+__device__ __forceinline__ const unsigned char *record_at(const DecayArgs &a, int64_t bh, int64_t t) {
+    return a.hd.chunk + step_at(a, bh, t) / C * kChunkRecord;
+}
+}  // namespace ht
+
+// ---------------------------------------------------------------------------
+// The gates.  A block takes one (batch row, head, segment), a warp one chunk at a time
+// (lane i: steps 4 i .. 4 i + 3), as many chunks at once as it has warps: sums within
+// the chunk, then, from the chunks' totals, which every warp goes through, whether the
+// state is rescaled at each and what decay has been left before it.
+__global__ void __launch_bounds__(1024) heads_gates_kernel(const __grid_constant__ DecayArgs a, StatusRef sref) {
+    using namespace ht;
+    using bf = __nv_bfloat16;
+    __shared__ long long totals[2][32];
+    // the main kernel reads the call's inputs as soon as it runs, so it may start only
+    // once the kernel before this one has ended
+    grid_dependency_wait();
+    launch_dependents();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+    if (threadIdx.x == 0 && blockIdx.x == 0) status_begin(sref);
+    const int seg = blockIdx.x % a.n_seg;
+    const int64_t bh = blockIdx.x / a.n_seg;
+    const int h = int(bh % a.H), b = int(bh / a.H);
+    const int64_t s0 = int64_t(seg) * a.seg_len;
+    const int nrun = int(max(int64_t(0), min(int64_t(dec::row_len(a.lens, b, a.L)), min(a.L, s0 + a.seg_len)) - s0));
+    const int n_chunks = (nrun + C - 1) / C;
+    const dec::Gates<true> gates(a, h);
+    const bf *g = static_cast<const bf *>(a.g) + (size_t(b) * a.L + s0) * a.hd.ldg + h;
+    bool bad = false;
+    long long base = 0, tot = 0;
+    // steps 4 lane .. of chunk c: step sizes and decays since the chunk's start
+    float delta[4];
+    long long l[4], all;
+    auto chunk = [&](int c) {
+        float gv[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int t = c * C + 4 * lane + i;
+            gv[i] = t < nrun ? __bfloat162float(g[size_t(t) * a.hd.ldg]) : 0.0f;
+        }
+        long long run = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float ld = gates.of(gv[i], delta[i]);
+            if (c * C + 4 * lane + i < nrun)
+                run += dec::to_fix(ld, bad);
+            else
+                delta[i] = 0.0f;
+            l[i] = run;
+        }
+        long long incl = run;
+#pragma unroll
+        for (int m = 1; m < 32; m <<= 1) {
+            const long long up = __shfl_up_sync(0xffffffffu, incl, m);
+            if (lane >= m) incl += up;
+        }
+        all = __shfl_sync(0xffffffffu, incl, 31);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) l[i] += incl - run;
+    };
+    for (int c0 = 0; c0 < n_chunks; c0 += warps) {
+        const int c = c0 + warp, buf = (c0 / warps) & 1;
+        all = 0;
+        if (c < n_chunks) chunk(c);
+        if (lane == 0) totals[buf][warp] = all;
+        __syncthreads();   // (the other buffer: a warp is at most one round ahead)
+        long long end = 0;
+        bool steep = false, re = false;
+        long long before = base;
+        const int n = min(warps, n_chunks - c0);
+        for (int j = 0; j < n; ++j) {
+            const long long t = totals[buf][j], e = base + t;
+            const bool s = t < kSteepChunk, r = s || e < kRescaleTensor;
+            if (j == warp) before = base, end = e, steep = s, re = r;
+            base = r ? 0 : e;
+            tot = max(tot + t, -(1ll << 60));
+        }
+        if (c >= n_chunks) continue;
+        float w[4], r[4], x[4], col[4];
+        int u[4];
+        const long long last = __shfl_sync(0xffffffffu, l[3], lane | 3);   // of the lane's 16 steps
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const long long e = re ? all - l[i] : -(before + l[i]);
+            const float p = dec::exp2_fix(e);
+            w[i] = p * delta[i];
+            u[i] = dec::units_of(l[i]);
+            if (steep) {
+                r[i] = -dec::exp2_fix(before + l[i]);   // (its sign says so, -0 too)
+                x[i] = delta[i];
+                col[i] = delta[i] * dec::exp2_fix(last - l[i]);
+            } else {
+                r[i] = dec::exp2_fix(-e);
+                x[i] = p;
+                col[i] = w[i];
+            }
+        }
+        const size_t at = step_at(a, bh, s0 + int64_t(c) * C + 4 * lane);
+        *reinterpret_cast<float4 *>(a.hd.weight + at) = make_float4(w[0], w[1], w[2], w[3]);
+        *reinterpret_cast<float4 *>(a.hd.readout + at) = make_float4(r[0], r[1], r[2], r[3]);
+        float4 *own = reinterpret_cast<float4 *>(a.hd.own + at);
+        own[0] = make_float4(x[0], __int_as_float(u[0]), x[1], __int_as_float(u[1]));
+        own[1] = make_float4(x[2], __int_as_float(u[2]), x[3], __int_as_float(u[3]));
+        Chunk *rec = reinterpret_cast<Chunk *>(const_cast<unsigned char *>(record_at(a, bh, s0 + int64_t(c) * C)));
+        reinterpret_cast<float4 *>(rec->col)[lane] = make_float4(col[0], col[1], col[2], col[3]);
+        if ((lane & 3) == 3) rec->last[lane >> 2] = u[3];
+        if (lane == 0) rec->m = re ? dec::exp2_fix(end) : 1.0f, rec->steep = steep;
+    }
+    // the decay that the scaled state still lacks when the segment is done
+    if (threadIdx.x == 0) a.hd.left[bh * a.n_seg + seg] = dec::exp2_fix(base);
+    if (seg < a.n_seg - 1) {   // weights to the segment's end, for the state that it leaves; from the last chunk back
+        if (threadIdx.x == 0) a.seg_tot[bh * (a.n_seg - 1) + seg] = tot;
+        long long after = 0;
+        for (int c1 = n_chunks; c1 > 0; c1 -= warps) {
+            const int c = c1 - 1 - warp;
+            all = 0;
+            if (c >= 0) chunk(c);
+            __syncthreads();   // the last round's totals have been read
+            if (lane == 0) totals[0][warp] = all;
+            __syncthreads();
+            long long own = after;
+            for (int j = 0; j < warps; ++j) {
+                if (j < warp) own += totals[0][j];
+                after += totals[0][j];
+            }
+            after = max(after, -(1ll << 60));
+            if (c < 0) continue;
+            float w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = delta[i] * dec::exp2_fix(own + all - l[i]);
+            *reinterpret_cast<float4 *>(a.hd.to_end + step_at(a, bh, s0 + int64_t(c) * C + 4 * lane)) =
+                make_float4(w[0], w[1], w[2], w[3]);
+        }
+    }
+    if (bad) status_report(sref, LR_ERR_RANGE);
+}
+
+// ---------------------------------------------------------------------------
+// The state that a segment builds from its own steps (segmented calls): the decayed
+// attention's kernel of this kind (lr_decay_tensor.cu), with the weights to the
+// segment's end from the gates' launch.
+namespace hs {
+constexpr int C = kDecayChunk, RB = kDecayRows;
+constexpr int NS = 3, NW = 3;
+constexpr int WEIGHTS = 8, TMA_WARP = 8, MMA_WARP = 9, THREADS = 10 * 32;
+constexpr uint32_t HALF = C * 128, K_BYTES = 2 * HALF, V_BYTES = C * RB * 2;
+constexpr uint32_t T_BYTES = 64 * RB * 2;      // one term of half a chunk
+constexpr uint32_t OFF_K = 0, OFF_V = NS * K_BYTES, OFF_W = OFF_V + NS * V_BYTES;
+constexpr uint32_t OFF_BAR = OFF_W + NW * 3 * T_BYTES;
+enum {
+    FULL_K = 0, EMPTY_K = FULL_K + NS, FULL_V = EMPTY_K + NS, EMPTY_V = FULL_V + NS,
+    W_READY = EMPTY_V + NS, W_FREE = W_READY + NW, DONE = W_FREE + NW, NBAR
+};
+constexpr uint32_t OFF_CTL = OFF_BAR + NBAR * 8;
+constexpr uint32_t OFF_TMEM = OFF_CTL + 40;
+constexpr uint32_t SMEM = OFF_TMEM + 8;
+static_assert(SMEM <= 227 * 1024, "one block per SM");
+constexpr uint32_t TMEM_COLS = 256;
+constexpr uint32_t IDESC = umma_idesc_bf16(128, 192, 1, 1);
+}  // namespace hs
+
+template <bool PARTS>
+__global__ void __launch_bounds__(hs::THREADS, 1)
+    heads_state_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                       const __grid_constant__ DecayArgs a, int n_vt, uint64_t timeout_ns, StatusRef sref) {
+    using namespace hs;
+    using dt::arrive;
+    using dt::Ctl;
+    using dt::hi_f;
+    using dt::lo_f;
+    using dt::pack;
+    using bf = __nv_bfloat16;
+    extern __shared__ __align__(1024) unsigned char sm[];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    // the gates.  The main launch's first segments read them too, and wait for nothing
+    // else, so it may start only once they are there
+    grid_dependency_wait();
+    launch_dependents();
+    if (tid == 0 && blockIdx.x == 0) status_begin(sref);
+    if ((smem_u32(sm) & 1023u) != 0) {   // swizzled tiles need a 1024-byte aligned base
+        if (tid == 0) status_report(sref, LR_ERR_CUDA);
+        return;
+    }
+    const int nseg = a.n_seg - 1;
+    int x = blockIdx.x;
+    const int vt = x % n_vt;
+    x /= n_vt;
+    const int part = PARTS ? x % a.parts : 0;
+    if (PARTS) x /= a.parts;
+    const int seg = x % nseg;
+    x /= nseg;
+    const int h = x % a.H, hk = h / (a.H / a.Hk);
+    const int b = dec::row_at(a, x / a.H, reinterpret_cast<int *>(sm + OFF_W)), bh = b * a.H + h;
+    const int len = dec::row_len(a.lens, b, a.L);
+    const int s0 = int(int64_t(seg) * a.seg_len);
+    const int nrun = max(0, min(len, int(min(a.L, int64_t(s0) + a.seg_len))) - s0);
+    const int n_chunks = (nrun + C - 1) / C;
+    // the block's key columns: k0 .. k0 + dk - 1 of ldk
+    const int ldk = a.dk, k0 = PARTS ? kPartKeys * part : 0, dk = PARTS ? min(kPartKeys, ldk - k0) : ldk, dv = a.dv;
+    const bool two = dk > 64;
+
+    uint64_t *bar = reinterpret_cast<uint64_t *>(sm + OFF_BAR);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + OFF_TMEM);
+    Ctl *ctl = reinterpret_cast<Ctl *>(sm + OFF_CTL);
+    if (tid == 0) {
+        for (int i = 0; i < NBAR; ++i) {
+            mbar_init(&bar[i], i >= EMPTY_V && i < W_FREE ? WEIGHTS : 1);
+        }
+        *ctl = Ctl{sref.word, sref.stamp, timeout_ns, 0, 0, b};
+        fence_mbar_init();
+    }
+    if (warp == 0) tmem_alloc(tmem_slot, TMEM_COLS);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    auto hw = [&](int i, int phase) -> bool {
+        const uint32_t parity = uint32_t(phase) & 1u;
+        return mbar_try_wait(&bar[i], parity) || dt::wait_slow(smem_u32(&bar[i]), parity, ctl);
+    };
+    if (warp == TMA_WARP && lane == 0) {   // the first chunks are on their way during the sum
+        prefetch_tensormap(&tm_k);
+        prefetch_tensormap(&tm_v);
+    }
+    auto load_k = [&](int c) {
+        const int st = c % NS;
+        mbar_arrive_expect_tx(&bar[FULL_K + st], two ? K_BYTES : HALF);
+        tma_load_4d(sm + OFF_K + st * K_BYTES, &tm_k, &bar[FULL_K + st], k0, hk, s0 + c * C, b);
+        if (two) tma_load_4d(sm + OFF_K + st * K_BYTES + HALF, &tm_k, &bar[FULL_K + st], k0 + 64, hk, s0 + c * C, b);
+    };
+    auto load_v = [&](int c) {
+        const int st = c % NS;
+        mbar_arrive_expect_tx(&bar[FULL_V + st], V_BYTES);
+        tma_load_4d(sm + OFF_V + st * V_BYTES, &tm_v, &bar[FULL_V + st], vt * RB, h, s0 + c * C, b);
+    };
+    const int first = min(NS, n_chunks);
+    if (warp == TMA_WARP && lane == 0)
+        for (int c = 0; c < first; ++c) {
+            load_k(c);
+            load_v(c);
+        }
+    if (warp == TMA_WARP) {
+        if (lane == 0) {
+            int nk = first, nv = first;
+            for (; nv < n_chunks; ++nv) {   // V is released first
+                if (!hw(EMPTY_V + nv % NS, nv / NS - 1)) break;
+                load_v(nv);
+                if (!hw(EMPTY_K + nk % NS, nk / NS - 1)) break;
+                load_k(nk);
+                ++nk;
+            }
+            // copies still in flight land before the block exits
+            for (int c = max(nk - NS, 0); c < nk; ++c) mbar_wait_bounded(&bar[FULL_K + c % NS], (c / NS) & 1, timeout_ns);
+            for (int c = max(nv - NS, 0); c < nv; ++c) mbar_wait_bounded(&bar[FULL_V + c % NS], (c / NS) & 1, timeout_ns);
+        }
+    } else if (warp == MMA_WARP) {
+        auto hu = [&](int i, int phase) -> bool { return __all_sync(0xffffffffu, hw(i, phase)); };
+        const bool lead = dt::elect_one();
+        const uint32_t base = __shfl_sync(0xffffffffu, smem_u32(sm), 0);
+        bool ok = true;
+        for (int c = 0; ok && c < n_chunks; ++c) {
+            const int st = c % NS;
+            ok = hu(FULL_K + st, c / NS);
+            const uint64_t dK = umma_smem_desc(base + OFF_K + st * K_BYTES, HALF, 1024);
+            for (int hf = 0; ok && hf < 2; ++hf) {
+                const int q = 2 * c + hf, slot = q % NW;
+                ok = hu(W_READY + slot, q / NW);
+                if (!ok) break;
+                tc_fence_after();
+                const uint64_t dW = umma_smem_desc(base + OFF_W + slot * 3 * T_BYTES, T_BYTES, 1024);
+                if (lead) {   // 16 steps are 2048 bytes on, 128 in the descriptors' units
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        umma_bf16(tmem, dK + 512 * hf + 128 * kk, dW + 128 * kk, IDESC, q > 0 || kk > 0);
+                    umma_commit(&bar[W_FREE + slot]);
+                    if (hf == 1) umma_commit(&bar[EMPTY_K + st]);
+                }
+                __syncwarp();
+            }
+        }
+        if (lead) {
+            umma_commit(&bar[DONE]);
+            mbar_wait_bounded(&bar[DONE], 0, timeout_ns);
+        }
+        __syncwarp();
+    } else if (warp < WEIGHTS) {
+        // 16-byte group (8 value rows) k8 of steps r32 and r32 + 32 of each half
+        const int r32 = tid >> 3, k8 = tid & 7;
+        const float *to_end = a.hd.to_end + ht::step_at(a, bh, s0) + r32;
+        float wn[4] = {};   // the next chunk's
+        auto load = [&](int c) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) wn[i] = __ldcg(to_end + c * C + 32 * i);
+        };
+        if (n_chunks > 0) load(0);
+        for (int c = 0; c < n_chunks; ++c) {
+            const int st = c % NS;
+            unsigned char *V = sm + OFF_V + st * V_BYTES;
+            const bool tail = c * C + C > nrun;
+            float wc[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) wc[i] = wn[i];
+            if (c + 1 < n_chunks) load(c + 1);
+            bool ok = hw(FULL_V + st, c / NS);
+            if (ok && tail) ok = hw(FULL_K + st, c / NS);
+            ok = __all_sync(0xffffffffu, ok);
+#pragma unroll 1
+            for (int hf = 0; ok && hf < 2; ++hf) {
+                const int q = 2 * c + hf, slot = q % NW;
+                uint4 u[2];
+                float w[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int s = 64 * hf + 32 * i + r32;   // step of the chunk
+                    const uint32_t at = sw128_offset(s, 8 * k8);
+                    u[i] = *reinterpret_cast<const uint4 *>(V + at);
+                    w[i] = hf == 0 ? wc[i] : wc[2 + i];
+                    if (tail && c * C + s >= nrun) {   // whatever stands there must not reach the product
+                        u[i] = make_uint4(0, 0, 0, 0);
+                        *reinterpret_cast<uint4 *>(sm + OFF_K + st * K_BYTES + at) = u[i];
+                        if (two) *reinterpret_cast<uint4 *>(sm + OFF_K + st * K_BYTES + HALF + at) = u[i];
+                    }
+                }
+                if (q >= NW && !__all_sync(0xffffffffu, hw(W_FREE + slot, q / NW - 1))) {
+                    ok = false;
+                    break;
+                }
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const uint32_t uv[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+                    uint32_t t1[4], t2[4], t3[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) dt::three_terms(w[i], uv[e], t1[e], t2[e], t3[e]);
+                    unsigned char *W = sm + OFF_W + slot * 3 * T_BYTES + sw128_offset(32 * i + r32, 8 * k8);
+                    *reinterpret_cast<uint4 *>(W) = make_uint4(t1[0], t1[1], t1[2], t1[3]);
+                    *reinterpret_cast<uint4 *>(W + T_BYTES) = make_uint4(t2[0], t2[1], t2[2], t2[3]);
+                    *reinterpret_cast<uint4 *>(W + 2 * T_BYTES) = make_uint4(t3[0], t3[1], t3[2], t3[3]);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) arrive(&bar[W_READY + slot]);
+            }
+            if (!ok) break;
+            if (lane == 0) arrive(&bar[EMPTY_V + st]);
+        }
+        // key column j, value rows 32 sh .. of the block's 64
+        const int j = 32 * (warp & 3) + lane, sh = warp >> 2, i0 = vt * RB + 32 * sh;
+        const bool done = n_chunks > 0 && __all_sync(0xffffffffu, hw(DONE, 0));
+        tc_fence_after();
+        const uint32_t D = tmem + 32 * sh + (uint32_t((warp & 3) * 32) << 16);
+        const float f = dec::exp2_fix(a.seg_tot[size_t(bh) * nseg + seg]);
+        const float *src = seg == 0 && a.S0 != nullptr ? a.S0 + (size_t(bh) * dv + i0) * ldk + k0 + j : nullptr;
+        float *dst = a.seg_state + ((size_t(bh) * nseg + seg) * dv + i0) * ldk + k0 + j;
+        float2 zero = make_float2(0.0f, 0.0f);
+#pragma unroll
+        for (int q = 0; q < 32; q += 16) {
+            float d1[16] = {}, d2[16] = {}, d3[16] = {};
+            if (done) {
+                tmem_ld16_nowait(D + q, d1);
+                tmem_ld16_nowait(D + 64 + q, d2);
+                tmem_ld16_nowait(D + 128 + q, d3);
+                tmem_ld_wait_tied(d1, d2);
+                tmem_ld_wait_tied(d3);
+            }
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+                if (j < dk && i0 + q + r < dv) {
+                    float y = d1[r] + (d2[r] + d3[r]);
+                    if (src != nullptr) y = fmaf(f, src[size_t(q + r) * ldk], y);
+                    zero.x = fmaf(0.0f, y, zero.x);
+                    dst[size_t(q + r) * ldk] = y;
+                }
+        }
+        if (dt::not_finite(zero)) ctl->redo = 1;
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 0) tmem_dealloc(tmem, TMEM_COLS);
+    const bool redo = ctl->redo != 0;
+    if (tid == 0) a.seg_bad[(size_t(bh) * nseg + seg) * a.seg_tiles + (PARTS ? vt * a.parts + part : vt)] = redo;
+    if (redo && ctl->abort_flag == 0) dt::redo_call<true, true>(a, ctl->row, n_vt, sm);
+}
+
+// ---------------------------------------------------------------------------
+// PARTS: the block's part of the key columns, its outputs a term of the sum
+template <bool PARTS>
+__global__ void __launch_bounds__(ht::THREADS, 1)
+    heads_tensor_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                        const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ DecayArgs a, int n_vt,
+                        uint64_t timeout_ns, StatusRef sref) {
+    using namespace ht;
+    using bf = __nv_bfloat16;
+    extern __shared__ __align__(1024) unsigned char sm[];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int nseg = a.n_seg;
+    launch_dependents();
+    if (tid == 0 && blockIdx.x == 0) status_begin(sref);
+    if ((smem_u32(sm) & 1023u) != 0) {   // swizzled tiles need a 1024-byte aligned base
+        if (tid == 0) status_report(sref, LR_ERR_CUDA);
+        return;
+    }
+    int x = blockIdx.x;
+    const int vt = x % n_vt;
+    x /= n_vt;
+    const int part = PARTS ? x % a.parts : 0;
+    if (PARTS) x /= a.parts;
+    const int seg = x % nseg;
+    x /= nseg;
+    const int h = x % a.H, hk = h / (a.H / a.Hk);
+    const int b = dec::row_at(a, x / a.H, reinterpret_cast<int *>(sm + OFF_W)), bh = b * a.H + h;
+    const int len = dec::row_len(a.lens, b, a.L);
+    const int s0 = int(int64_t(seg) * a.seg_len);
+    const int send = int(min(a.L, int64_t(s0) + a.seg_len));
+    const int nrun = max(0, min(len, send) - s0);
+    const int n_chunks = (nrun + C - 1) / C;
+    // the block's key columns: k0 .. k0 + dk - 1 of ldk
+    const int ldk = a.dk, k0 = PARTS ? kPartKeys * part : 0, dk = PARTS ? min(kPartKeys, ldk - k0) : ldk, dv = a.dv;
+    const int nkk = (dk + 15) / 16;          // 16-wide steps over the key columns
+    const bool two = dk > 64;                // two 64-column halves of Q and K
+    const size_t g0 = step_at(a, bh, s0);    // the segment's gates
+
+    uint64_t *bar = reinterpret_cast<uint64_t *>(sm + OFF_BAR);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + OFF_TMEM);
+    Ctl *ctl = reinterpret_cast<Ctl *>(sm + OFF_CTL);
+    const Chunk *rec = reinterpret_cast<const Chunk *>(sm + OFF_G);
+    if (tid == 0) {
+        for (int i = 0; i < NBAR; ++i) {
+            int n = 1;
+            if (i >= F_DONE && i < K_DONE + 2) n = 8;
+            if (i == SB_READY || i == DS_FREE || i == FIX) n = 8;
+            // K is read by dS and P, Q by P and OX, V by the weight warps (through dS) and OI
+            if ((i >= EMPTY_Q && i < EMPTY_Q + 2) || (i >= EMPTY_K && i < EMPTY_K + 2) ||
+                (i >= EMPTY_V && i < EMPTY_V + 2))
+                n = 2;
+            if (i == MMA_END) n = 3;
+            mbar_init(&bar[i], n);
+        }
+        *ctl = Ctl{sref.word, sref.stamp, timeout_ns, 0, 0, b};
+        fence_mbar_init();
+    }
+    if (warp == 0) tmem_alloc(tmem_slot, 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    auto hw = [&](int i, int phase) -> bool {
+        const uint32_t parity = uint32_t(phase) & 1u;
+        return mbar_try_wait(&bar[i], parity) || wait_slow(smem_u32(&bar[i]), parity, ctl);
+    };
+    // What is read of the gates' launch waits for it; in a segmented call the launch
+    // between has waited for it before this one could start, and segments past the
+    // first wait for that one's states.
+    auto gates_wait = [&]() {
+        if (nseg == 1 || seg > 0) grid_dependency_wait();
+    };
+
+    if (warp == TMA_WARP) {   // --------------------------------------- TMA
+        if (lane == 0) {
+            prefetch_tensormap(&tm_q);
+            prefetch_tensormap(&tm_k);
+            prefetch_tensormap(&tm_v);
+            auto load_qk = [&](int n, const CUtensorMap *tm, int off, int full) {
+                const int st = n & 1, t = s0 + n * C;
+                unsigned char *dst = sm + off + st * Q_BYTES;
+                mbar_arrive_expect_tx(&bar[full + st], two ? 2 * HALF : HALF);
+                tma_load_4d(dst, tm, &bar[full + st], k0, hk, t, b);
+                if (two) tma_load_4d(dst + HALF, tm, &bar[full + st], k0 + 64, hk, t, b);
+            };
+            auto load_v = [&](int n) {
+                const int st = n & 1;
+                mbar_arrive_expect_tx(&bar[FULL_V + st], V_BYTES);
+                tma_load_4d(sm + OFF_V + st * V_BYTES, &tm_v, &bar[FULL_V + st], vt * RB, h, s0 + n * C, b);
+            };
+            auto load_g = [&](int n) {
+                const int st = n & 1;
+                mbar_arrive_expect_tx(&bar[FULL_G + st], kChunkRecord);
+                bulk_load(sm + OFF_G + st * kChunkRecord, record_at(a, bh, s0 + int64_t(n) * C), kChunkRecord,
+                          &bar[FULL_G + st]);
+            };
+            int nq = 0, nk = 0, nv = 0, ng = 0;
+            for (; nv < 2 && nv < n_chunks; ++nv, ++nq, ++nk) {
+                load_qk(nv, &tm_q, OFF_Q, FULL_Q);
+                load_qk(nv, &tm_k, OFF_K, FULL_K);
+                load_v(nv);
+            }
+            gates_wait();
+            fence_proxy_async_global();
+            for (; ng < nv; ++ng) load_g(ng);
+            // in the order in which a chunk lets go of them; once its last products (O's) have
+            // let go of V nobody reads its record either
+            for (int n = 2; n < n_chunks; ++n) {
+                const int st = n & 1, ph = (n - 2) >> 1;
+                if (!hw(EMPTY_Q + st, ph)) break;
+                load_qk(n, &tm_q, OFF_Q, FULL_Q), ++nq;
+                if (!hw(EMPTY_K + st, ph)) break;
+                load_qk(n, &tm_k, OFF_K, FULL_K), ++nk;
+                if (!hw(EMPTY_V + st, ph)) break;
+                load_v(n), ++nv;
+                load_g(n), ++ng;
+            }
+            // copies still in flight land before the block exits
+            auto land = [&](int full, int n) {
+                for (int c = max(n - 2, 0); c < n; ++c) mbar_wait_bounded(&bar[full + (c & 1)], (c >> 1) & 1, timeout_ns);
+            };
+            land(FULL_Q, nq);
+            land(FULL_K, nk);
+            land(FULL_V, nv);
+            land(FULL_G, ng);
+        }
+    } else if (warp >= DS_WARP) {   // -------------------------------- products
+        // every wait's answer is made warp-uniform, and so is all that follows
+        auto hu = [&](int i, int phase) -> bool { return __all_sync(0xffffffffu, hw(i, phase)); };
+        const bool lead = elect_one();
+        const uint32_t base = __shfl_sync(0xffffffffu, smem_u32(sm), 0);
+        if (warp == DS_WARP) {
+            const uint64_t dW = umma_smem_desc(base + OFF_W, V_BYTES, 1024);
+            for (int c = 0; c < n_chunks; ++c) {
+                const int st = c & 1;
+                // the last dS has been read
+                if (!hu(FULL_K + st, c >> 1) || (c >= 1 && !hu(DS_FREE, c - 1))) break;
+                const uint64_t dK = umma_smem_desc(base + OFF_K + st * Q_BYTES, HALF, 1024);
+                bool ok = true;
+#pragma unroll 1
+                for (int qt = 0; qt < 4; ++qt) {
+                    ok = ok && hu(W_READY + qt, c);
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (lead) {   // 16 steps are 2048 bytes on, 128 in the descriptors' units
+                        umma_bf16(tmem + T_DS, dK + 256 * qt, dW + 256 * qt, IDESC_DS, qt > 0);
+                        umma_bf16(tmem + T_DS, dK + 256 * qt + 128, dW + 256 * qt + 128, IDESC_DS, 1);
+                        umma_commit(&bar[W_FREE + qt]);
+                        if (qt == 3) {
+                            umma_commit(&bar[DS_DONE]);
+                            umma_commit(&bar[EMPTY_K + st]);
+                            umma_commit(&bar[EMPTY_V + st]);
+                        }
+                    }
+                    __syncwarp();
+                }
+                if (!ok) break;
+            }
+        } else if (warp == P_WARP) {
+            for (int c = 0; c < n_chunks; ++c) {
+                const int st = c & 1;
+                if (!hu(FULL_K + st, c >> 1) || !hu(FULL_Q + st, c >> 1)) break;
+                if (c >= 2 && !hu(O_DONE + st, (c - 2) >> 1)) break;   // chunk c - 2's PD has been used
+                tc_fence_after();
+                const uint64_t dQ = umma_smem_desc(base + OFF_Q + st * Q_BYTES, 16, 1024),
+                               dK = umma_smem_desc(base + OFF_K + st * Q_BYTES, 16, 1024);
+                if (lead) {
+#pragma unroll 1
+                    for (int kk = 0; kk < nkk; ++kk) {
+                        const uint32_t off = ((kk >> 2) * HALF + (kk & 3) * 32) >> 4;
+                        umma_bf16(tmem + T_P + st * 128, dQ + off, dK + off, IDESC_P, kk > 0);
+                    }
+                    umma_commit(&bar[P_READY + st]);
+                    umma_commit(&bar[EMPTY_K + st]);
+                    umma_commit(&bar[EMPTY_Q + st]);
+                }
+                __syncwarp();
+            }
+        } else {
+            const uint64_t dS = umma_smem_desc(base + OFF_SB, HALF, 1024);
+            int n_steep = 0;
+            for (int c = 0; c < n_chunks; ++c) {
+                const int st = c & 1;
+                // the state before chunk c; the last outputs have been read
+                if (!hu(SB_READY, c) || !hu(FULL_Q + st, c >> 1)) break;
+                if (c >= 1 && !hu(K_DONE + ((c - 1) & 1), (c - 1) >> 1)) break;
+                tc_fence_after();
+                const uint64_t dQ = umma_smem_desc(base + OFF_Q + st * Q_BYTES, 16, 1024);
+                if (lead) {
+#pragma unroll 1
+                    for (int kk = 0; kk < nkk; ++kk)
+                        umma_bf16(tmem + T_O, dQ + (((kk >> 2) * HALF + (kk & 3) * 32) >> 4), dS + 128 * kk, IDESC_O,
+                                  kk > 0);
+                    umma_commit(&bar[OX_DONE + st]);
+                    umma_commit(&bar[EMPTY_Q + st]);
+                }
+                __syncwarp();
+                if (!hu(F_DONE + st, c >> 1) || !hu(FULL_V + st, c >> 1)) break;
+                if (!hu(FULL_G + st, c >> 1) || (rec[st].steep != 0 && !hu(FIX, n_steep++))) break;
+                if (c * C + C > nrun) {   // the last chunk: V's rows past the end have been zeroed
+                    bool ok = true;
+                    for (int qt = 0; qt < 4; ++qt) ok = ok && hu(W_READY + qt, c);
+                    if (!ok) break;
+                }
+                tc_fence_after();
+                const uint64_t dV = umma_smem_desc(base + OFF_V + st * V_BYTES, HALF, 1024);
+                if (lead) {   // onto Q S^T: same shape and accumulator, so in order
+#pragma unroll 1
+                    for (int kk = 0; kk < C / 16; ++kk)
+                        umma_bf16_ts(tmem + T_O, tmem + T_P + st * 128 + (kk >> 2) * 64 + (kk & 3) * 8, dV + 128 * kk,
+                                     IDESC_O, 1);
+                    umma_commit(&bar[O_DONE + st]);
+                    umma_commit(&bar[EMPTY_V + st]);
+                }
+                __syncwarp();
+            }
+        }
+        // nothing of this block's may still run on the tensor cores when its TMEM is released
+        if (lead) {
+            umma_commit(&bar[MMA_END]);
+            mbar_wait_bounded(&bar[MMA_END], 0, timeout_ns);
+        }
+        __syncwarp();
+    } else if (warp >= WEIGHT) {   // ----------------------------------- weight
+        const int s = tid - 32 * WEIGHT;   // this thread's step of the chunk
+        const int qt = warp - WEIGHT;
+        gates_wait();
+        const float *src = a.hd.weight + g0 + s;
+        float wn = n_chunks > 0 ? __ldcg(src) : 0.0f;
+        for (int c = 0; c < n_chunks; ++c) {
+            const int st = c & 1;
+            unsigned char *V = sm + OFF_V + st * V_BYTES;
+            const bool in = c * C + s < nrun;
+            const float w = wn;
+            if (c + 1 < n_chunks) wn = __ldcg(src + (c + 1) * C);
+            bool ok = hw(FULL_V + st, c >> 1);
+            if (ok && c * C + C > nrun) ok = hw(FULL_K + st, c >> 1);
+            if (ok && c >= 1) ok = hw(W_FREE + qt, c - 1);
+            if (!__all_sync(0xffffffffu, ok)) break;
+#pragma unroll 1
+            for (int k = 0; k < 8; ++k) {
+                const uint32_t at = sw128_offset(s, 0) ^ (k << 4);   // group k of row s
+                uint4 u = *reinterpret_cast<const uint4 *>(V + at);
+                if (!in) u = make_uint4(0, 0, 0, 0);
+                const uint32_t uv[4] = {u.x, u.y, u.z, u.w};
+                uint32_t t1[4], t2[4], t3[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) three_terms(w, uv[e], t1[e], t2[e], t3[e]);
+                *reinterpret_cast<uint4 *>(sm + OFF_W + at) = make_uint4(t1[0], t1[1], t1[2], t1[3]);
+                *reinterpret_cast<uint4 *>(sm + OFF_W + V_BYTES + at) = make_uint4(t2[0], t2[1], t2[2], t2[3]);
+                *reinterpret_cast<uint4 *>(sm + OFF_W + 2 * V_BYTES + at) = make_uint4(t3[0], t3[1], t3[2], t3[3]);
+            }
+            if (!in) {   // past the row's end: whatever stands there must not reach a product
+                const uint4 z = make_uint4(0, 0, 0, 0);
+#pragma unroll 1
+                for (int k = 0; k < 8; ++k) {
+                    *reinterpret_cast<uint4 *>(V + s * 128 + 16 * k) = z;
+                    *reinterpret_cast<uint4 *>(sm + OFF_K + st * Q_BYTES + s * 128 + 16 * k) = z;
+                    if (two) *reinterpret_cast<uint4 *>(sm + OFF_K + st * Q_BYTES + HALF + s * 128 + 16 * k) = z;
+                }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) arrive(&bar[W_READY + qt]);
+        }
+    } else if (warp >= FRONT) {   // ------------------------------------- front
+        // rows 32 fw .. of P, columns 64 hf .. in blocks of 16; PD's go to the
+        // first half of the same columns, which the warp has read by then
+        const int fw = warp & 3, hf = (warp - FRONT) >> 2, t = 32 * fw + lane;
+        const bool has_skip = a.hd.skip != nullptr && part == 0;
+        const float skip = has_skip ? a.hd.skip[h] : 0.0f;
+        gates_wait();
+        const float2 *src = a.hd.own + g0 + t;
+        float2 next = n_chunks > 0 ? __ldcg(src) : make_float2(0.0f, 0.0f);
+        for (int c = 0; c < n_chunks; ++c) {
+            const int st = c & 1;
+            const uint32_t P = tmem + T_P + st * 128 + 64 * hf + (uint32_t(fw * 32) << 16);
+            const float2 own = next;
+            if (c + 1 < n_chunks) next = __ldcg(src + (c + 1) * C);
+            const bool ok = hw(FULL_G + st, c >> 1) && hw(P_READY + st, c >> 1);
+            if (!__all_sync(0xffffffffu, ok)) break;
+            tc_fence_after();
+            const int n = min(t + 1, nrun - c * C) - 64 * hf;   // columns that this row sees
+            const bool cut = nrun - c * C < C;
+            const bool steep = rec[st].steep != 0;
+            const float *f = rec[st].col + 64 * hf;
+            const int lt = __float_as_int(own.y);               // steep
+            const float dg = skip * (steep ? 1.0f : own.x);
+#pragma unroll 1
+            for (int kb = 0; kb < 4; ++kb) {
+                const int b0 = 64 * hf + 16 * kb;   // the block's first column
+                uint32_t r[8];
+                if (b0 > 32 * fw + 31) {   // no row of the warp sees the block
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) r[e] = 0;
+                    tmem_st8_nowait(P + 8 * kb, r);
+                    continue;
+                }
+                const bool diag = b0 + 15 > 32 * fw;   // it holds some row's diagonal
+                float p[16];
+                tmem_ld16_nowait(P + 16 * kb, p);
+                if (steep && diag) {
+                    tmem_ld_wait_tied(p);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {   // the warp's own steps
+                        const int from = (b0 & 16) + e;
+                        const float ds = __shfl_sync(0xffffffffu, own.x, from);
+                        const int ls = __shfl_sync(0xffffffffu, lt, from);
+                        // (a step past the row's is cut below; its power may be any)
+                        p[e] = p[e] * ds * ex2_approx(dec::units_f(min(lt - ls, 0)));
+                    }
+                } else {
+                    // rows past a steep chunk's block: as one factor more
+                    const float rf = steep ? ex2_approx(dec::units_f(lt - rec[st].last[b0 >> 4])) : 1.0f;
+                    float4 w4[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) w4[e] = *reinterpret_cast<const float4 *>(f + 16 * kb + 4 * e);
+                    tmem_ld_wait_tied(p);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float2 y0 = __fmul2_rn(make_float2(p[4 * e], p[4 * e + 1]), make_float2(w4[e].x, w4[e].y));
+                        const float2 y1 =
+                            __fmul2_rn(make_float2(p[4 * e + 2], p[4 * e + 3]), make_float2(w4[e].z, w4[e].w));
+                        p[4 * e] = y0.x, p[4 * e + 1] = y0.y, p[4 * e + 2] = y1.x, p[4 * e + 3] = y1.y;
+                    }
+                    if (steep) {
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) p[e] *= rf;
+                    }
+                }
+                if (diag) {
+                    if (has_skip) {
+                        const int d = t - b0;
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) p[e] += e == d ? dg : 0.0f;
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < 8; ++e) r[e] = pack(p[2 * e], p[2 * e + 1]);
+                if (cut || diag) {   // cut bits, whatever the others hold
+                    const int m = n - 16 * kb;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) r[e] &= 2 * e + 1 < m ? 0xffffffffu : 2 * e < m ? 0xffffu : 0u;
+                }
+                tmem_st8_nowait(P + 8 * kb, r);
+            }
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) arrive(&bar[F_DONE + st]);
+        }
+    } else if (warp >= OUT) {   // --------------------------------------- output
+        // row 32 (warp & 3) + lane of the chunk, value columns 32 oh ..
+        const int row = 32 * (warp & 3) + lane, oh = (warp - OUT) >> 2;
+        const uint32_t O = tmem + T_O + 32 * oh + (uint32_t((warp & 3) * 32) << 16);
+        const int i0 = vt * RB + 32 * oh;
+        const size_t HV = size_t(a.H) * dv;
+        bf *ob = static_cast<bf *>(a.o) + (size_t(b) * a.L + s0) * HV + size_t(h) * dv + i0;
+        const bf *zb = nullptr;
+        if (!PARTS && a.hd.z != nullptr)
+            zb = static_cast<const bf *>(a.hd.z) + (size_t(b) * a.L + s0) * a.hd.ldz + size_t(h) * dv + i0;
+        gates_wait();
+        const float *src = a.hd.readout + g0 + row;
+        float next = n_chunks > 0 ? __ldcg(src) : 0.0f;
+        float2 zero = make_float2(0.0f, 0.0f);
+        for (int c = 0; c < n_chunks; ++c) {
+            const int st = c & 1;
+            float u = next;
+            if (c + 1 < n_chunks) next = __ldcg(src + (c + 1) * C);
+            const int t = c * C + row;
+            const bool valid = t < nrun, store = s0 + t < send;
+            uint4 z[4];   // the gate's row, on its way while the products finish
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                z[q] = make_uint4(0, 0, 0, 0);
+                if (!PARTS && zb != nullptr && valid && i0 + 8 * q < dv)
+                    z[q] = *reinterpret_cast<const uint4 *>(zb + size_t(t) * a.hd.ldz + 8 * q);
+            }
+            if (__float_as_int(u) < 0) {   // steep: rows of Q S^T by 2^(base + L) before PD V is added
+                if (!__all_sync(0xffffffffu, hw(OX_DONE + st, c >> 1))) break;
+                tc_fence_after();
+#pragma unroll 1
+                for (int q = 0; q < 32; q += 16) {
+                    float d[16];
+                    tmem_ld16_nowait(O + q, d);
+                    tmem_ld_wait_tied(d);
+                    uint32_t w[16];
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) w[r] = __float_as_uint(-u * d[r]);
+                    tmem_st16_nowait(O + q, w);
+                }
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) arrive(&bar[FIX]);
+                u = 1.0f;
+            }
+            if (!__all_sync(0xffffffffu, hw(O_DONE + st, c >> 1))) break;
+            tc_fence_after();
+            float d[32];
+            tmem_ld32_nowait(O, d);
+            tmem_ld_wait_tied(d);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) arrive(&bar[K_DONE + st]);   // the rest is off the chain
+            const float2 u2 = make_float2(u, u);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const uint32_t zq[4] = {z[q].x, z[q].y, z[q].z, z[q].w};
+                uint32_t w[4];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    float2 y = __fmul2_rn(u2, make_float2(d[8 * q + 2 * r], d[8 * q + 2 * r + 1]));
+                    if (valid) zero = __ffma2_rn(y, make_float2(0.0f, 0.0f), zero);
+                    if (!PARTS && zb != nullptr) y = __fmul2_rn(y, make_float2(silu_f(lo_f(zq[r])), silu_f(hi_f(zq[r]))));
+                    d[8 * q + 2 * r] = y.x, d[8 * q + 2 * r + 1] = y.y;
+                    w[r] = pack(y.x, y.y);
+                }
+                if (i0 + 8 * q >= dv) continue;
+                if (PARTS) {   // steps past the row's end are the sum's to clear
+                    if (!valid) continue;
+                    float *dst = a.o_part + ((size_t(part) * a.B + b) * a.L + s0 + t) * HV + size_t(h) * dv + i0 + 8 * q;
+#pragma unroll
+                    for (int r = 0; r < 8; r += 4)
+                        *reinterpret_cast<float4 *>(dst + r) =
+                            make_float4(d[8 * q + r], d[8 * q + r + 1], d[8 * q + r + 2], d[8 * q + r + 3]);
+                } else if (store) {
+                    *reinterpret_cast<uint4 *>(ob + size_t(t) * HV + 8 * q) =
+                        valid ? make_uint4(w[0], w[1], w[2], w[3]) : make_uint4(0, 0, 0, 0);
+                }
+            }
+        }
+        if (not_finite(zero)) ctl->redo = 1;
+    } else {   // --------------------------------------------------------- state
+        // key column: this thread's TMEM lane; value rows 32 sh .. of the block's 64
+        const int j = tid & 127, sh = warp >> 2;
+        const uint32_t D = tmem + T_DS + 32 * sh + (uint32_t((warp & 3) * 32) << 16);
+        const int i0 = vt * RB + 32 * sh;
+        // the state before the segment: S0, or the decayed sum of the ranges before
+        float S[32];
+#pragma unroll
+        for (int r = 0; r < 32; ++r)
+            S[r] = a.S0 != nullptr && seg == 0 && j < dk && i0 + r < dv
+                       ? a.S0[(size_t(bh) * dv + i0 + r) * ldk + k0 + j]
+                       : 0.0f;
+        gates_wait();
+        if (seg > 0) {
+            long long acc = 0;
+#pragma unroll 1
+            for (int e = seg - 1; e >= 0; --e) {
+                const float f = dec::exp2_fix(acc);
+                // nothing is left of the ranges before, unless it is not finite
+                if (f == 0.0f && !dec::any_bad(a, bh, e, PARTS ? vt * a.parts + part : vt)) break;
+                const size_t at = size_t(bh) * (a.n_seg - 1) + e;
+                const float *src = a.seg_state + (at * dv + i0) * ldk + k0 + j;
+#pragma unroll
+                for (int r = 0; r < 32; ++r)
+                    if (j < dk && i0 + r < dv) S[r] = fmaf(f, src[size_t(r) * ldk], S[r]);
+                acc = max(acc + a.seg_tot[at], -(1ll << 60));
+            }
+        }
+        for (int c = 0; c < n_chunks; ++c) {
+            const int st = c & 1;
+            bool ok = hw(FULL_G + st, c >> 1);
+            // the bf16 copy's buffer is free
+            if (ok && c >= 1) ok = hw(OX_DONE + ((c - 1) & 1), (c - 1) >> 1);
+            if (!__all_sync(0xffffffffu, ok)) break;
+            const float m = rec[st].m;
+            // a rescale belongs before the copy (the chunk's weights assume it) but
+            // after it in a steep chunk, which applies its factors by rows
+            const bool steep = rec[st].steep != 0;
+            auto scale_state = [&]() {
+#pragma unroll
+                for (int e = 0; e < 32; ++e) S[e] *= m;
+            };
+            if (m != 1.0f && !steep) scale_state();
+            // the copy: row j of 64 value rows in 8 swizzled groups
+#pragma unroll
+            for (int q = 0; q < 32; q += 8)
+                *reinterpret_cast<uint4 *>(sm + OFF_SB + sw128_offset(j, 32 * sh + q)) =
+                    make_uint4(pack(S[q], S[q + 1]), pack(S[q + 2], S[q + 3]), pack(S[q + 4], S[q + 5]),
+                               pack(S[q + 6], S[q + 7]));
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) arrive(&bar[SB_READY]);
+            if (steep) scale_state();
+            if (!__all_sync(0xffffffffu, hw(DS_DONE, c))) break;
+            tc_fence_after();
+#pragma unroll
+            for (int q = 0; q < 32; q += 8) {   // small terms first
+                float d1[8], d2[8], d3[8];
+                tmem_ld8_nowait(D + q, d1);
+                tmem_ld8_nowait(D + 64 + q, d2);
+                tmem_ld8_nowait(D + 128 + q, d3);
+                tmem_ld_wait_tied(d1, d2, d3);
+#pragma unroll
+                for (int e = 0; e < 8; e += 2) {
+                    const float2 y = __fadd2_rn(make_float2(d1[e], d1[e + 1]),
+                                                __fadd2_rn(make_float2(d2[e], d2[e + 1]), make_float2(d3[e], d3[e + 1])));
+                    const float2 z = __fadd2_rn(make_float2(S[q + e], S[q + e + 1]), y);
+                    S[q + e] = z.x, S[q + e + 1] = z.y;
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) arrive(&bar[DS_FREE]);
+        }
+        float *out = seg == a.n_seg - 1 && a.S_final != nullptr ? a.S_final + size_t(bh) * dv * ldk + k0 : nullptr;
+        if (out != nullptr && j < dk) {
+            const float f = __ldcg(a.hd.left + size_t(bh) * nseg + seg);
+            float2 zero = make_float2(0.0f, 0.0f);
+#pragma unroll
+            for (int r = 0; r < 32; ++r)
+                if (i0 + r < dv) {
+                    const float y = f * S[r];
+                    zero.x = fmaf(0.0f, y, zero.x);
+                    out[size_t(i0 + r) * ldk + j] = y;
+                }
+            if (not_finite(zero)) ctl->redo = 1;
+        }
+    }
+
+    if (!PARTS) {   // whole chunks past the row's end
+        const int g8 = min(RB, dv - vt * RB) / 8;
+        const int64_t first = s0 + int64_t(n_chunks) * C;
+        bf *ob = static_cast<bf *>(a.o) + size_t(h) * dv + vt * RB;
+        for (int64_t e = tid; e < (send - first) * g8; e += THREADS)
+            *reinterpret_cast<uint4 *>(ob + (size_t(b) * a.L + first + e / g8) * size_t(a.H) * dv + (e % g8) * 8) =
+                make_uint4(0, 0, 0, 0);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 0) tmem_dealloc(tmem, 512);
+    if (ctl->redo != 0 && ctl->abort_flag == 0) {
+        if constexpr (PARTS)
+            dt::redo_block<false, true>(a, ctl->row, n_vt, sm);
+        else
+            dt::redo_call<false, true>(a, ctl->row, n_vt, sm);
+    }
+}
+
+namespace {
+
+bool ht_setup() {
+    static DeviceSetup setup;
+    return setup.run([] {
+        auto room = [](auto kern, uint32_t bytes) {
+            return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes)) == cudaSuccess;
+        };
+        return room(heads_state_kernel<false>, hs::SMEM) && room(heads_state_kernel<true>, hs::SMEM) &&
+               room(heads_tensor_kernel<false>, ht::SMEM) && room(heads_tensor_kernel<true>, ht::SMEM);
+    });
+}
+
+}  // namespace
+
+int heads_tensor_launch(const DecayArgs &a, StatusRef st, cudaStream_t stream) {
+    CUtensorMap mq, mk, mv;
+    if (!dt_map(&mq, a.q, a.dk, a.Hk, a.L, a.B, a.hd.ldq) || !dt_map(&mk, a.k, a.dk, a.Hk, a.L, a.B, a.hd.ldk) ||
+        !dt_map(&mv, a.v, a.dv, a.H, a.L, a.B, a.hd.ldv) || !ht_setup())
+        return LR_ERR_CUDA;
+    const int n_vt = (a.dv + ht::RB - 1) / ht::RB;
+    const bool parts = a.parts > 1;
+    const int64_t per_seg = a.B * a.H * n_vt * a.parts;
+    if (per_seg * a.n_seg > INT32_MAX) return LR_ERR_UNSUPPORTED;
+    const int64_t chunks = (a.seg_len + ht::C - 1) / ht::C;
+    int rc = launch_early(heads_gates_kernel, dim3(unsigned(a.B * a.H * a.n_seg)), int(32 * (chunks < 32 ? chunks : 32)),
+                          stream, a, st);
+    if (rc == LR_OK && a.n_seg > 1)
+        rc = launch_kernel(parts ? heads_state_kernel<true> : heads_state_kernel<false>, true,
+                           dim3(unsigned(per_seg * (a.n_seg - 1))), hs::THREADS, hs::SMEM, stream, mk, mv, a, n_vt,
+                           kDefaultTimeoutNs, st);
+    if (rc == LR_OK)
+        rc = launch_kernel(parts ? heads_tensor_kernel<true> : heads_tensor_kernel<false>, true,
+                           dim3(unsigned(per_seg * a.n_seg)), ht::THREADS, ht::SMEM, stream, mq, mk, mv, a, n_vt,
+                           kDefaultTimeoutNs, st);
+    if (rc != LR_OK || !parts) return rc;
+    const int64_t rows = a.B * a.L;
+    return launch_early(decay_parts_kernel<true>, dim3(unsigned(rows < (1 << 20) ? rows : 1 << 20)), 256, stream, a);
+}
+
+}  // namespace lr
