@@ -502,4 +502,10 @@ __device__ __forceinline__ void tmem_ld_wait_tied(float (&a)[8], float (&b)[8], 
                  :
                  : "memory");
 }
+__device__ __forceinline__ void tmem_ld_wait_tied(float (&a)[8]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+f"(a[0]), "+f"(a[1]), "+f"(a[2]), "+f"(a[3]), "+f"(a[4]), "+f"(a[5]), "+f"(a[6]), "+f"(a[7])
+                 :
+                 : "memory");
+}
 }  // namespace lr

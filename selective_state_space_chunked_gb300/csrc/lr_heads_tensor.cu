@@ -77,7 +77,7 @@ enum {
     FULL_G = 12,     // the chunk's record
     P_READY = 14,    // P_c complete
     F_DONE = 16,     // PD_c written (8 front warps)
-    K_DONE = 18,     // chunk c's outputs read (8 output warps)
+    K_DONE = 18,     // chunk c's accumulator read (8 output warps)
     OX_DONE = 20,    // Q S^T complete: the bf16 state has been read
     O_DONE = 22,
     W_READY = 24,    // weighted values of a quarter
@@ -85,7 +85,9 @@ enum {
     SB_READY = 32,   // bf16 state before chunk c (8 state warps)
     DS_DONE, DS_FREE,
     FIX,             // a steep chunk's Q S^T scaled (8 output warps)
-    MMA_END, NBAR
+    MMA_END,
+    Y_DONE,          // [2] chunk c's outputs have left P's columns (8 output warps)
+    NBAR = Y_DONE + 2
 };
 constexpr uint32_t OFF_TMEM = OFF_BAR + NBAR * 8;
 constexpr uint32_t OFF_CTL = OFF_TMEM + 8;
@@ -104,6 +106,19 @@ __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t b
         "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_u32(dst)),
         "l"(src), "r"(bytes), "r"(smem_u32(bar))
         : "memory");
+}
+
+// The neighbouring lane's value.
+__device__ __forceinline__ uint4 xor1(uint4 v) {
+    return make_uint4(__shfl_xor_sync(0xffffffffu, v.x, 1), __shfl_xor_sync(0xffffffffu, v.y, 1),
+                      __shfl_xor_sync(0xffffffffu, v.z, 1), __shfl_xor_sync(0xffffffffu, v.w, 1));
+}
+
+// silu of a pair of bf16 values.
+__device__ __forceinline__ float2 silu2(uint32_t z) {
+    const float2 x = make_float2(lo_f(z), hi_f(z)), e = __fmul2_rn(x, make_float2(-kLog2e, -kLog2e));
+    const float2 d = __fadd2_rn(make_float2(ex2_approx(e.x), ex2_approx(e.y)), make_float2(1.0f, 1.0f));
+    return __fmul2_rn(x, make_float2(rcp_approx(d.x), rcp_approx(d.y)));
 }
 
 // Position of a (batch row, head)'s step in the gates' arrays, and of its chunk's record.
@@ -540,7 +555,7 @@ __global__ void __launch_bounds__(ht::THREADS, 1)
         for (int i = 0; i < NBAR; ++i) {
             int n = 1;
             if (i >= F_DONE && i < K_DONE + 2) n = 8;
-            if (i == SB_READY || i == DS_FREE || i == FIX) n = 8;
+            if (i == SB_READY || i == DS_FREE || i == FIX || i >= Y_DONE) n = 8;
             // K is read by dS and P, Q by P and OX, V by the weight warps (through dS) and OI
             if ((i >= EMPTY_Q && i < EMPTY_Q + 2) || (i >= EMPTY_K && i < EMPTY_K + 2) ||
                 (i >= EMPTY_V && i < EMPTY_V + 2))
@@ -656,7 +671,8 @@ __global__ void __launch_bounds__(ht::THREADS, 1)
             for (int c = 0; c < n_chunks; ++c) {
                 const int st = c & 1;
                 if (!hu(FULL_K + st, c >> 1) || !hu(FULL_Q + st, c >> 1)) break;
-                if (c >= 2 && !hu(O_DONE + st, (c - 2) >> 1)) break;   // chunk c - 2's PD has been used
+                // chunk c - 2's PD has been used and its outputs are gone
+                if (c >= 2 && !hu(Y_DONE + st, (c - 2) >> 1)) break;
                 tc_fence_after();
                 const uint64_t dQ = umma_smem_desc(base + OFF_Q + st * Q_BYTES, 16, 1024),
                                dK = umma_smem_desc(base + OFF_K + st * Q_BYTES, 16, 1024);
@@ -847,7 +863,7 @@ __global__ void __launch_bounds__(ht::THREADS, 1)
         }
     } else if (warp >= OUT) {   // --------------------------------------- output
         // row 32 (warp & 3) + lane of the chunk, value columns 32 oh ..
-        const int row = 32 * (warp & 3) + lane, oh = (warp - OUT) >> 2;
+        const int row = 32 * (warp & 3) + lane, oh = (warp - OUT) >> 2, odd = lane & 1;
         const uint32_t O = tmem + T_O + 32 * oh + (uint32_t((warp & 3) * 32) << 16);
         const int i0 = vt * RB + 32 * oh;
         const size_t HV = size_t(a.H) * dv;
@@ -864,14 +880,19 @@ __global__ void __launch_bounds__(ht::THREADS, 1)
             float u = next;
             if (c + 1 < n_chunks) next = __ldcg(src + (c + 1) * C);
             const int t = c * C + row;
-            const bool valid = t < nrun, store = s0 + t < send;
-            uint4 z[4];   // the gate's row, on its way while the products finish
+            const bool valid = t < nrun;
+            // the gate, on its way while the products finish: lanes 2 g and 2 g + 1 take 16
+            // bytes each of row 2 g and of row 2 g + 1, for either half of the columns
+            uint4 z[2][2];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                z[q] = make_uint4(0, 0, 0, 0);
-                if (!PARTS && zb != nullptr && valid && i0 + 8 * q < dv)
-                    z[q] = *reinterpret_cast<const uint4 *>(zb + size_t(t) * a.hd.ldz + 8 * q);
-            }
+            for (int q = 0; q < 2; ++q)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int tr = t - odd + i;
+                    z[q][i] = make_uint4(0, 0, 0, 0);
+                    if (!PARTS && zb != nullptr && tr < nrun && i0 + 16 * q + 8 * odd < dv)
+                        z[q][i] = *reinterpret_cast<const uint4 *>(zb + size_t(tr) * a.hd.ldz + 16 * q + 8 * odd);
+                }
             if (__float_as_int(u) < 0) {   // steep: rows of Q S^T by 2^(base + L) before PD V is added
                 if (!__all_sync(0xffffffffu, hw(OX_DONE + st, c >> 1))) break;
                 tc_fence_after();
@@ -893,38 +914,78 @@ __global__ void __launch_bounds__(ht::THREADS, 1)
             }
             if (!__all_sync(0xffffffffu, hw(O_DONE + st, c >> 1))) break;
             tc_fence_after();
-            float d[32];
-            tmem_ld32_nowait(O, d);
-            tmem_ld_wait_tied(d);
+            // out of the accumulator into those columns of P's that PD leaves free, so that the
+            // next chunk's Q S^T can start
+            const uint32_t Y = tmem + T_P + st * 128 + 32 + 64 * oh + (uint32_t((warp & 3) * 32) << 16);
+#pragma unroll 1
+            for (int q = 0; q < 32; q += 16) {
+                float d[16];
+                tmem_ld16_nowait(O + q, d);
+                tmem_ld_wait_tied(d);
+                uint32_t w[16];
+#pragma unroll
+                for (int r = 0; r < 16; ++r) w[r] = __float_as_uint(u * d[r]);
+                tmem_st16_nowait(Y + q, w);
+            }
+            tmem_st_wait();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) arrive(&bar[K_DONE + st]);   // the rest is off the chain
-            const float2 u2 = make_float2(u, u);
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const uint32_t zq[4] = {z[q].x, z[q].y, z[q].z, z[q].w};
-                uint32_t w[4];
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    float2 y = __fmul2_rn(u2, make_float2(d[8 * q + 2 * r], d[8 * q + 2 * r + 1]));
-                    if (valid) zero = __ffma2_rn(y, make_float2(0.0f, 0.0f), zero);
-                    if (!PARTS && zb != nullptr) y = __fmul2_rn(y, make_float2(silu_f(lo_f(zq[r])), silu_f(hi_f(zq[r]))));
-                    d[8 * q + 2 * r] = y.x, d[8 * q + 2 * r + 1] = y.y;
-                    w[r] = pack(y.x, y.y);
-                }
-                if (i0 + 8 * q >= dv) continue;
+            if (lane == 0) arrive(&bar[K_DONE + st]);
+#pragma unroll 1
+            for (int q = 0; q < 2; ++q) {
+                float d[16];
+                tmem_ld16_nowait(Y + 16 * q, d);
+                const int col = i0 + 16 * q;
                 if (PARTS) {   // steps past the row's end are the sum's to clear
-                    if (!valid) continue;
-                    float *dst = a.o_part + ((size_t(part) * a.B + b) * a.L + s0 + t) * HV + size_t(h) * dv + i0 + 8 * q;
+                    tmem_ld_wait_tied(d);
+                    float *dst = a.o_part + ((size_t(part) * a.B + b) * a.L + s0 + t) * HV + size_t(h) * dv + col;
 #pragma unroll
-                    for (int r = 0; r < 8; r += 4)
-                        *reinterpret_cast<float4 *>(dst + r) =
-                            make_float4(d[8 * q + r], d[8 * q + r + 1], d[8 * q + r + 2], d[8 * q + r + 3]);
-                } else if (store) {
-                    *reinterpret_cast<uint4 *>(ob + size_t(t) * HV + 8 * q) =
-                        valid ? make_uint4(w[0], w[1], w[2], w[3]) : make_uint4(0, 0, 0, 0);
+                    for (int r = 0; r < 16; r += 4) {
+                        if (valid && col + r < dv)
+                            *reinterpret_cast<float4 *>(dst + r) = make_float4(d[r], d[r + 1], d[r + 2], d[r + 3]);
+                    }
+#pragma unroll
+                    for (int r = 0; r < 16; ++r)
+                        if (valid) zero.x = fmaf(0.0f, d[r], zero.x);
+                    continue;
+                }
+                uint32_t w[8];
+                if (zb != nullptr) {   // this thread's row: its own 16 bytes and the partner's
+                    const uint4 z0 = z[0][0], z1 = z[0][1];
+                    const uint4 mine = odd ? z1 : z0, give = odd ? z0 : z1;
+                    const uint4 got = xor1(give), lo = odd ? got : mine, hi = odd ? mine : got;
+                    const uint32_t zw[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+                    tmem_ld_wait_tied(d);
+#pragma unroll
+                    for (int r = 0; r < 8; ++r) {
+                        float2 y = make_float2(d[2 * r], d[2 * r + 1]);
+                        if (valid) zero = __ffma2_rn(y, make_float2(0.0f, 0.0f), zero);
+                        y = __fmul2_rn(y, silu2(zw[r]));
+                        w[r] = pack(y.x, y.y);
+                    }
+                    z[0][0] = z[1][0], z[0][1] = z[1][1];
+                } else {
+                    tmem_ld_wait_tied(d);
+#pragma unroll
+                    for (int r = 0; r < 8; ++r) {
+                        const float2 y = make_float2(d[2 * r], d[2 * r + 1]);
+                        if (valid) zero = __ffma2_rn(y, make_float2(0.0f, 0.0f), zero);
+                        w[r] = pack(y.x, y.y);
+                    }
+                }
+                // whole 32-byte sectors: each lane stores 16 bytes of both rows of the pair
+                uint4 lo = make_uint4(w[0], w[1], w[2], w[3]), hi = make_uint4(w[4], w[5], w[6], w[7]);
+                if (!valid) lo = hi = make_uint4(0, 0, 0, 0);
+                const uint4 mine = odd ? hi : lo, got = xor1(odd ? lo : hi);
+                bf *dst = ob + size_t(t - odd) * HV + 16 * q + 8 * odd;   // the pair's first row
+                if (col + 8 * odd < dv) {
+                    if (s0 + t - odd < send) *reinterpret_cast<uint4 *>(dst) = odd ? got : mine;
+                    if (s0 + t - odd + 1 < send) *reinterpret_cast<uint4 *>(dst + HV) = odd ? mine : got;
                 }
             }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) arrive(&bar[Y_DONE + st]);
         }
         if (not_finite(zero)) ctl->redo = 1;
     } else {   // --------------------------------------------------------- state
