@@ -133,12 +133,14 @@ __device__ __forceinline__ const unsigned char *record_at(const DecayArgs &a, in
 // ---------------------------------------------------------------------------
 // The gates.  A block takes one (batch row, head, segment), a warp one chunk at a time
 // (lane i: steps 4 i .. 4 i + 3), as many chunks at once as it has warps: sums within
-// the chunk, then, from the chunks' totals, which every warp goes through, whether the
-// state is rescaled at each and what decay has been left before it.
+// the chunk, then, from the chunks' totals, which warp 0 goes through, whether the state
+// is rescaled at each and what decay has been left before it.  (Every warp going through
+// them: 15.7 us under a profiler at B4 L4096 H16, and most of that issue slots.)
 __global__ void __launch_bounds__(1024) heads_gates_kernel(const __grid_constant__ DecayArgs a, StatusRef sref) {
     using namespace ht;
     using bf = __nv_bfloat16;
-    __shared__ long long totals[2][32];
+    __shared__ long long totals[32], before_of[32];
+    __shared__ int how_of[32];   // bit 0: rescaled, bit 1: steep
     // the main kernel reads the call's inputs as soon as it runs, so it may start only
     // once the kernel before this one has ended
     grid_dependency_wait();
@@ -186,22 +188,29 @@ __global__ void __launch_bounds__(1024) heads_gates_kernel(const __grid_constant
         for (int i = 0; i < 4; ++i) l[i] += incl - run;
     };
     for (int c0 = 0; c0 < n_chunks; c0 += warps) {
-        const int c = c0 + warp, buf = (c0 / warps) & 1;
+        const int c = c0 + warp;
         all = 0;
         if (c < n_chunks) chunk(c);
-        if (lane == 0) totals[buf][warp] = all;
-        __syncthreads();   // (the other buffer: a warp is at most one round ahead)
-        long long end = 0;
-        bool steep = false, re = false;
-        long long before = base;
-        const int n = min(warps, n_chunks - c0);
-        for (int j = 0; j < n; ++j) {
-            const long long t = totals[buf][j], e = base + t;
-            const bool s = t < kSteepChunk, r = s || e < kRescaleTensor;
-            if (j == warp) before = base, end = e, steep = s, re = r;
-            base = r ? 0 : e;
-            tot = max(tot + t, -(1ll << 60));
+        if (lane == 0) totals[warp] = all;
+        __syncthreads();
+        if (warp == 0) {   // (it alone holds base and tot)
+            const long long mine = lane < warps ? totals[lane] : 0;
+            long long kept = 0;
+            int how = 0;
+#pragma unroll 4
+            for (int j = 0; j < min(warps, n_chunks - c0); ++j) {
+                const long long t = __shfl_sync(0xffffffffu, mine, j), e = base + t;
+                const bool s = t < kSteepChunk, r = s || e < kRescaleTensor;
+                if (j == lane) kept = base, how = int(r) + 2 * int(s);
+                base = r ? 0 : e;
+                tot = max(tot + t, -(1ll << 60));
+            }
+            before_of[lane] = kept;
+            how_of[lane] = how;
         }
+        __syncthreads();
+        const long long before = before_of[warp], end = before + all;
+        const bool re = how_of[warp] & 1, steep = how_of[warp] & 2;
         if (c >= n_chunks) continue;
         float w[4], r[4], x[4], col[4];
         int u[4];
@@ -243,12 +252,12 @@ __global__ void __launch_bounds__(1024) heads_gates_kernel(const __grid_constant
             all = 0;
             if (c >= 0) chunk(c);
             __syncthreads();   // the last round's totals have been read
-            if (lane == 0) totals[0][warp] = all;
+            if (lane == 0) totals[warp] = all;
             __syncthreads();
             long long own = after;
             for (int j = 0; j < warps; ++j) {
-                if (j < warp) own += totals[0][j];
-                after += totals[0][j];
+                if (j < warp) own += totals[j];
+                after += totals[j];
             }
             after = max(after, -(1ll << 60));
             if (c < 0) continue;
@@ -792,7 +801,6 @@ __global__ void __launch_bounds__(ht::THREADS, 1)
             const bool ok = hw(FULL_G + st, c >> 1) && hw(P_READY + st, c >> 1);
             if (!__all_sync(0xffffffffu, ok)) break;
             tc_fence_after();
-            const int n = min(t + 1, nrun - c * C) - 64 * hf;   // columns that this row sees
             const bool cut = nrun - c * C < C;
             const bool steep = rec[st].steep != 0;
             const float *f = rec[st].col + 64 * hf;
@@ -840,17 +848,18 @@ __global__ void __launch_bounds__(ht::THREADS, 1)
                         for (int e = 0; e < 16; ++e) p[e] *= rf;
                     }
                 }
-                if (diag) {
-                    if (has_skip) {
-                        const int d = t - b0;
+                if (diag) {   // row t sees columns up to its own, which takes the skip
+                    const int d = t - b0;
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) p[e] += e == d ? dg : 0.0f;
+                    for (int e = 0; e < 16; ++e) {
+                        if (has_skip && e == d) p[e] += dg;
+                        if (e > d) p[e] = 0.0f;
                     }
                 }
 #pragma unroll
                 for (int e = 0; e < 8; ++e) r[e] = pack(p[2 * e], p[2 * e + 1]);
-                if (cut || diag) {   // cut bits, whatever the others hold
-                    const int m = n - 16 * kb;
+                if (cut) {   // no columns past the row's end, whatever they hold
+                    const int m = nrun - c * C - b0;
 #pragma unroll
                     for (int e = 0; e < 8; ++e) r[e] &= 2 * e + 1 < m ? 0xffffffffu : 2 * e < m ? 0xffffu : 0u;
                 }
@@ -924,13 +933,14 @@ __global__ void __launch_bounds__(ht::THREADS, 1)
                 tmem_ld_wait_tied(d);
                 uint32_t w[16];
 #pragma unroll
-                for (int r = 0; r < 16; ++r) w[r] = __float_as_uint(u * d[r]);
+                for (int r = 0; r < 16; ++r) w[r] = __float_as_uint(d[r]);
                 tmem_st16_nowait(Y + q, w);
             }
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) arrive(&bar[K_DONE + st]);
+            const float2 u2 = make_float2(u, u);
 #pragma unroll 1
             for (int q = 0; q < 2; ++q) {
                 float d[16];
@@ -941,12 +951,10 @@ __global__ void __launch_bounds__(ht::THREADS, 1)
                     float *dst = a.o_part + ((size_t(part) * a.B + b) * a.L + s0 + t) * HV + size_t(h) * dv + col;
 #pragma unroll
                     for (int r = 0; r < 16; r += 4) {
-                        if (valid && col + r < dv)
-                            *reinterpret_cast<float4 *>(dst + r) = make_float4(d[r], d[r + 1], d[r + 2], d[r + 3]);
+                        const float4 y = make_float4(u * d[r], u * d[r + 1], u * d[r + 2], u * d[r + 3]);
+                        if (valid && col + r < dv) *reinterpret_cast<float4 *>(dst + r) = y;
+                        if (valid) zero.x = fmaf(0.0f, y.x, fmaf(0.0f, y.y, fmaf(0.0f, y.z, fmaf(0.0f, y.w, zero.x))));
                     }
-#pragma unroll
-                    for (int r = 0; r < 16; ++r)
-                        if (valid) zero.x = fmaf(0.0f, d[r], zero.x);
                     continue;
                 }
                 uint32_t w[8];
@@ -958,7 +966,7 @@ __global__ void __launch_bounds__(ht::THREADS, 1)
                     tmem_ld_wait_tied(d);
 #pragma unroll
                     for (int r = 0; r < 8; ++r) {
-                        float2 y = make_float2(d[2 * r], d[2 * r + 1]);
+                        float2 y = __fmul2_rn(u2, make_float2(d[2 * r], d[2 * r + 1]));
                         if (valid) zero = __ffma2_rn(y, make_float2(0.0f, 0.0f), zero);
                         y = __fmul2_rn(y, silu2(zw[r]));
                         w[r] = pack(y.x, y.y);
@@ -968,7 +976,7 @@ __global__ void __launch_bounds__(ht::THREADS, 1)
                     tmem_ld_wait_tied(d);
 #pragma unroll
                     for (int r = 0; r < 8; ++r) {
-                        const float2 y = make_float2(d[2 * r], d[2 * r + 1]);
+                        const float2 y = __fmul2_rn(u2, make_float2(d[2 * r], d[2 * r + 1]));
                         if (valid) zero = __ffma2_rn(y, make_float2(0.0f, 0.0f), zero);
                         w[r] = pack(y.x, y.y);
                     }
