@@ -138,6 +138,7 @@ class _NoTorchModule:
         return None
 
     decay_attn = decay_attn_step = group_norm_act = _decline
+    causal_conv = causal_conv_step = selective_heads = selective_heads_step = head_norm_rope = _decline
 
 
 def _load_torch_module():
@@ -1040,6 +1041,13 @@ def selective_heads(x, dt, Bm, Cm, A_log, H: int, G: int = 1, z=None, Dskip=None
     delta = dt + dt_bias, at least 0.  z, Dskip, dt_bias may be None.  Returns (y
     (B, L, H*P), S_final (B, H, P, N) fp32); ``out=(y, S_final)`` gives the result tensors.
     A negative or NaN step size sets LR_ERR_RANGE (see ``check_status``)."""
+    if workspace is None and out is None:
+        r = _lrtorch.selective_heads(x, dt, Bm, Cm, A_log, H, G, z, Dskip, dt_bias, S0, lens, bool(dt_softplus))
+        if type(r) is tuple:
+            y, S, _tls.ws = r
+            return y, S
+        if r is not None:
+            _check(r, "lr_selective_heads_fwd")
     (B, L), P, N, io = _heads_args(x, dt, Bm, Cm, A_log, H, G, z, Dskip, dt_bias, S0, 3)
     _integers(lens, (B,), "lens")
     dev = _target_device(x)
@@ -1067,6 +1075,11 @@ def selective_heads_step(x, dt, Bm, Cm, A_log, H: int, G: int = 1, z=None, Dskip
     """One token of ``selective_heads``.  x, z: (B, H*P); dt: (B, H); Bm, Cm: (B, G*N); S:
     (B, H, P, N) fp32 or None (zero).  Returns (y (B, H*P), S_new); ``S_out`` gives the
     buffer S_new is written to (it may be ``S`` itself)."""
+    r = _lrtorch.selective_heads_step(x, dt, Bm, Cm, A_log, H, G, z, Dskip, dt_bias, S, S_out, bool(dt_softplus))
+    if type(r) is tuple:
+        return r
+    if r is not None:
+        _check(r, "lr_selective_heads_step")
     (B,), P, N, io = _heads_args(x, dt, Bm, Cm, A_log, H, G, z, Dskip, dt_bias, S, 2)
     dev = _target_device(x)
     with torch.cuda.device(dev):
@@ -1110,6 +1123,12 @@ def causal_conv(x, w, bias=None, state=None, lens=None, act: str = "silu",
     (B,) integers or None: row b has lens[b] steps (its later outputs are 0); ``act``:
     "silu" or "none".  Returns (y (B, L, C), the state after each row's last step);
     ``out=(y, state)`` gives the result tensors (the state may be ``state`` itself)."""
+    if out is None:
+        r = _lrtorch.causal_conv(x, w, bias, state, lens, _ACT.get(act))
+        if type(r) is tuple:
+            return r
+        if r is not None:
+            _check(r, "lr_causal_conv_fwd")
     a, C, W, io = _conv_args(x, w, bias, state, act, 3)
     B, L, _ = x.shape
     _integers(lens, (B,), "lens")
@@ -1131,6 +1150,11 @@ def causal_conv_step(x, w, bias=None, state=None, state_out=None,
     """One token of ``causal_conv``.  x: (B, C); state: (B, W-1, C) or None (zeros).
     Returns (y (B, C), the new state); ``state_out`` gives the buffer that it is
     written to (it may be ``state`` itself)."""
+    r = _lrtorch.causal_conv_step(x, w, bias, state, state_out, _ACT.get(act))
+    if type(r) is tuple:
+        return r
+    if r is not None:
+        _check(r, "lr_causal_conv_step")
     a, C, W, io = _conv_args(x, w, bias, state, act, 2)
     B = x.shape[0]
     dev = _target_device(x)
@@ -1162,6 +1186,12 @@ def head_norm_rope(q, k, H: int, Hk: Optional[int] = None, norm: str = "rms", ga
     pos: (...) integers within int32.  Returns (q, k) as new dense tensors; ``out`` gives
     them (dense inputs themselves are allowed)."""
     n, p = _NORM.get(norm), _PAIRS.get(pairs)
+    if out is None:
+        r = _lrtorch.head_norm_rope(q, k, H, Hk, n, gamma_q, gamma_k, freqs, pos, p, eps)
+        if type(r) is tuple:
+            return r
+        if r is not None:
+            _check(r, "lr_head_norm_rope")
     if n is None or p is None:
         raise ValueError(f"unknown norm {norm!r} or pairs {pairs!r}; use one of {sorted(_NORM)} and {sorted(_PAIRS)}")
     lead, Hk = q.shape[:-1], 0 if k is None else H if Hk is None else Hk

@@ -6,7 +6,8 @@
 //
 // Each function takes what its helper in binding.py takes and returns what it
 // returns, or None where an argument is not already what the kernels take
-// (another type or device, not contiguous, shapes that do not match, empty) or
+// (another type or device, not contiguous or in rows that are not evenly apart, shapes
+// that do not match, empty) or
 // the call's own checks refused it; nothing has been launched then, and the helper
 // goes on to its own checks and conversions, which convert the argument or say what
 // is wrong.  Any other status comes back as an int, for the helper to raise: part of
@@ -19,6 +20,8 @@
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
+
+#include <vector>
 
 #include "lrscan.h"
 
@@ -54,6 +57,50 @@ struct Call {
             return false;
         *p = t.data_ptr();
         return true;
+    }
+    // a tensor whose rows of `width` lie evenly apart (a slice of a wider one): the elements
+    // from one to the next.  whole: on 16-byte boundaries, unless they are dense.
+    bool rows(PyObject *o, bool whole, bool optional, void **p, int64_t *ld, at::IntArrayRef shape) const {
+        if (o == Py_None) {
+            *p = nullptr, *ld = 0;
+            return optional;
+        }
+        if (!THPVariable_CheckExact(o)) return false;
+        const at::Tensor &t = THPVariable_Unpack(o);
+        if (!t.is_cuda() || t.layout() != at::kStrided || t.get_device() != dev || t.scalar_type() != type ||
+            t.sizes() != shape)
+            return false;
+        *ld = pitch(t);
+        *p = t.data_ptr();
+        return *ld > 0 && reinterpret_cast<uintptr_t>(*p) % 16 == 0 &&
+               (!whole || *ld == t.size(-1) || *ld * t.element_size() % 16 == 0);
+    }
+    // ... which names the call's GPU and dtype
+    const at::Tensor *first_rows(PyObject *o, int64_t dims) {
+        if (!THPVariable_CheckExact(o)) return nullptr;
+        const at::Tensor &t = THPVariable_Unpack(o);
+        if (!t.is_cuda() || t.layout() != at::kStrided || t.numel() == 0 || (dims > 0 && t.dim() != dims) || t.dim() < 1)
+            return nullptr;
+        type = t.scalar_type();
+        if (type != at::kFloat && type != at::kBFloat16) return nullptr;
+        io = type == at::kBFloat16 ? LR_BF16 : LR_F32;
+        dev = t.get_device();
+        return dev == c10::cuda::current_device() ? &t : nullptr;
+    }
+    // elements between the rows of t (..., C), 0 where they are not evenly apart
+    static int64_t pitch(const at::Tensor &t) {
+        const int64_t n = t.dim(), C = t.size(-1);
+        if (C != 1 && t.stride(-1) != 1) return 0;
+        int64_t ld = -1, size = 1;
+        for (int64_t i = n - 2; i >= 0; --i) {
+            if (t.size(i) == 1) continue;
+            if (ld < 0)
+                ld = t.stride(i);
+            else if (t.stride(i) != ld * size)
+                return 0;
+            size *= t.size(i);
+        }
+        return ld < 0 ? C : ld < C ? 0 : ld;
     }
     lr_stream_t stream() const {
         return reinterpret_cast<lr_stream_t>(c10::cuda::getCurrentCUDAStream(dev).stream());
@@ -250,6 +297,231 @@ PyObject *group_norm_act(PyObject *, PyObject *const *args, Py_ssize_t n) {
     }
 }
 
+// A pair of results: new tensors, or the caller's own where one was given.
+PyObject *pair_of(const at::Tensor &a, const at::Tensor &b, PyObject *given_b) {
+    const Ref pa(THPVariable_Wrap(a)), pb(b.defined() ? THPVariable_Wrap(b) : Ref::share(given_b));
+    return pa.o && pb.o ? PyTuple_Pack(2, pa.o, pb.o) : nullptr;
+}
+
+// (x, w, bias, state, lens, act code) -> (y, state)
+PyObject *causal_conv(PyObject *, PyObject *const *args, Py_ssize_t n) {
+    if (n != 6) Py_RETURN_NONE;
+    bool launched = false;
+    try {
+        Call c;
+        const at::Tensor *x = c.first_rows(args[0], 3);
+        int64_t act, ldx;
+        if (x == nullptr || !THPVariable_CheckExact(args[1]) || !to_int(args[5], &act)) Py_RETURN_NONE;
+        const at::Tensor &wt = THPVariable_Unpack(args[1]);
+        const int64_t B = x->size(0), L = x->size(1), C = x->size(2), W = wt.dim() == 2 ? wt.size(1) : 0;
+        if (W < 2) Py_RETURN_NONE;
+        const int64_t ws[] = {C, W}, ss[] = {B, W - 1, C};
+        void *px, *w, *bias, *state, *lens;
+        if (!c.rows(args[0], false, false, &px, &ldx, x->sizes()) || !c.take(args[1], at::kFloat, ws, false, &w) ||
+            !c.take(args[2], at::kFloat, {C}, true, &bias) || !c.take(args[3], c.type, ss, true, &state) ||
+            !c.take(args[4], at::kInt, {B}, true, &lens))
+            Py_RETURN_NONE;
+        at::Tensor y, Sn;
+        int rc;
+        {
+            const Unlocked unlocked;
+            y = at::empty(x->sizes(), x->options());
+            Sn = at::empty(ss, x->options());
+            launched = true;
+            rc = lr_causal_conv_fwd(px, ldx, static_cast<float *>(w), static_cast<float *>(bias), state,
+                                    static_cast<int32_t *>(lens), y.data_ptr(), Sn.data_ptr(), B, L, C, W,
+                                    static_cast<lr_act>(act), c.io, c.stream());
+        }
+        if (rc != LR_OK) return refused(rc);
+        return pair_of(y, Sn, nullptr);
+    } catch (...) {
+        return thrown(launched);
+    }
+}
+
+// (x, w, bias, state, state_out, act code) -> (y, state)
+PyObject *causal_conv_step(PyObject *, PyObject *const *args, Py_ssize_t n) {
+    if (n != 6) Py_RETURN_NONE;
+    bool launched = false;
+    try {
+        Call c;
+        const at::Tensor *x = c.first_rows(args[0], 2);
+        int64_t act, ldx;
+        if (x == nullptr || !THPVariable_CheckExact(args[1]) || !to_int(args[5], &act)) Py_RETURN_NONE;
+        const at::Tensor &wt = THPVariable_Unpack(args[1]);
+        const int64_t B = x->size(0), C = x->size(1), W = wt.dim() == 2 ? wt.size(1) : 0;
+        if (W < 2) Py_RETURN_NONE;
+        const int64_t ws[] = {C, W}, ss[] = {B, W - 1, C};
+        void *px, *w, *bias, *state, *out;
+        if (!c.rows(args[0], false, false, &px, &ldx, x->sizes()) || !c.take(args[1], at::kFloat, ws, false, &w) ||
+            !c.take(args[2], at::kFloat, {C}, true, &bias) || !c.take(args[3], c.type, ss, true, &state) ||
+            !c.take(args[4], c.type, ss, true, &out))
+            Py_RETURN_NONE;
+        at::Tensor y, Sn;
+        int rc;
+        {
+            const Unlocked unlocked;
+            y = at::empty(x->sizes(), x->options());
+            if (out == nullptr) {
+                Sn = at::empty(ss, x->options());
+                out = Sn.data_ptr();
+            }
+            launched = true;
+            rc = lr_causal_conv_step(px, ldx, static_cast<float *>(w), static_cast<float *>(bias), state, out,
+                                     y.data_ptr(), B, C, W, static_cast<lr_act>(act), c.io, c.stream());
+        }
+        if (rc != LR_OK) return refused(rc);
+        return pair_of(y, Sn, args[4]);
+    } catch (...) {
+        return thrown(launched);
+    }
+}
+
+// What both forms of the selective scan with heads take: (x, dt, Bm, Cm, A_log, H, G, z,
+// Dskip, dt_bias, state, ..., softplus)
+struct Scan {
+    int64_t H, G, P, N, ldx, lddt, ldb, ldc, ldz;
+    void *x, *dt, *Bm, *Cm, *z, *A, *skip, *bias, *S;
+    bool of(const Call &c, const at::Tensor &xt, PyObject *const *args) {
+        if (!to_int(args[5], &H) || !to_int(args[6], &G) || H < 1 || G < 1 || H % G != 0 || xt.size(-1) % H != 0 ||
+            !THPVariable_CheckExact(args[2]))
+            return false;
+        const at::Tensor &bt = THPVariable_Unpack(args[2]);
+        const bool prompt = xt.dim() == 3;
+        if (bt.dim() != xt.dim() || bt.size(-1) % G != 0) return false;
+        P = xt.size(-1) / H, N = bt.size(-1) / G;
+        if (P < 1 || N < 1) return false;
+        const int64_t B = xt.size(0), L = prompt ? xt.size(1) : 1;
+        const int64_t dt3[] = {B, L, H}, bc3[] = {B, L, G * N}, dt2[] = {B, H}, bc2[] = {B, G * N}, ss[] = {B, H, P, N};
+        const at::IntArrayRef ds = prompt ? at::IntArrayRef(dt3) : at::IntArrayRef(dt2);
+        const at::IntArrayRef bs = prompt ? at::IntArrayRef(bc3) : at::IntArrayRef(bc2);
+        return c.rows(args[0], true, false, &x, &ldx, xt.sizes()) && c.rows(args[1], false, false, &dt, &lddt, ds) &&
+               c.rows(args[2], true, false, &Bm, &ldb, bs) && c.rows(args[3], true, false, &Cm, &ldc, bs) &&
+               c.take(args[4], at::kFloat, {H}, false, &A) && c.rows(args[7], true, true, &z, &ldz, xt.sizes()) &&
+               c.take(args[8], at::kFloat, {H}, true, &skip) && c.take(args[9], at::kFloat, {H}, true, &bias) &&
+               c.take(args[10], at::kFloat, ss, true, &S);
+    }
+};
+float *f32(void *p) { return static_cast<float *>(p); }
+
+// (x, dt, Bm, Cm, A_log, H, G, z, Dskip, dt_bias, S0, lens, softplus) -> (y, S_final, workspace)
+PyObject *selective_heads(PyObject *, PyObject *const *args, Py_ssize_t n) {
+    if (n != 13) Py_RETURN_NONE;
+    bool launched = false;
+    try {
+        Call c;
+        Scan s;
+        int64_t soft;
+        void *lens;
+        const at::Tensor *x = c.first_rows(args[0], 3);
+        if (x == nullptr || !s.of(c, *x, args) || !to_int(args[12], &soft)) Py_RETURN_NONE;
+        const int64_t B = x->size(0), L = x->size(1);
+        if (!c.take(args[11], at::kInt, {B}, true, &lens)) Py_RETURN_NONE;
+        const size_t wsb = lr_selective_heads_workspace_size(B, L, s.H, s.G, s.P, s.N, c.io);
+        if (wsb == 0 || wsb > size_t(INT64_MAX)) Py_RETURN_NONE;
+        at::Tensor y, Sf, ws;
+        int rc;
+        {
+            const Unlocked unlocked;
+            y = at::empty(x->sizes(), x->options());
+            Sf = at::empty({B, s.H, s.P, s.N}, x->options().dtype(at::kFloat));
+            ws = at::empty({static_cast<int64_t>(wsb)}, x->options().dtype(at::kByte));
+            launched = true;
+            rc = lr_selective_heads_fwd(s.x, s.ldx, s.dt, s.lddt, s.Bm, s.ldb, s.Cm, s.ldc, s.z, s.ldz, f32(s.A),
+                                        f32(s.bias), f32(s.skip), static_cast<int32_t *>(lens), f32(s.S), y.data_ptr(),
+                                        Sf.data_ptr<float>(), B, L, s.H, s.G, s.P, s.N, c.io, soft != 0, ws.data_ptr(),
+                                        wsb, c.stream());
+        }
+        if (rc != LR_OK) return refused(rc);
+        const Ref py(THPVariable_Wrap(y)), ps(THPVariable_Wrap(Sf)), pw(THPVariable_Wrap(ws));
+        return py.o && ps.o && pw.o ? PyTuple_Pack(3, py.o, ps.o, pw.o) : nullptr;
+    } catch (...) {
+        return thrown(launched);
+    }
+}
+
+// (x, dt, Bm, Cm, A_log, H, G, z, Dskip, dt_bias, S, S_out, softplus) -> (y, S_new)
+PyObject *selective_heads_step(PyObject *, PyObject *const *args, Py_ssize_t n) {
+    if (n != 13) Py_RETURN_NONE;
+    bool launched = false;
+    try {
+        Call c;
+        Scan s;
+        int64_t soft;
+        void *out;
+        const at::Tensor *x = c.first_rows(args[0], 2);
+        if (x == nullptr || !s.of(c, *x, args) || !to_int(args[12], &soft)) Py_RETURN_NONE;
+        const int64_t B = x->size(0), ss[] = {B, s.H, s.P, s.N};
+        if (!c.take(args[11], at::kFloat, ss, true, &out)) Py_RETURN_NONE;
+        at::Tensor y, Sn;
+        int rc;
+        {
+            const Unlocked unlocked;
+            y = at::empty(x->sizes(), x->options());
+            if (out == nullptr) {
+                Sn = at::empty(ss, x->options().dtype(at::kFloat));
+                out = Sn.data_ptr();
+            }
+            launched = true;
+            rc = lr_selective_heads_step(s.x, s.ldx, s.dt, s.lddt, s.Bm, s.ldb, s.Cm, s.ldc, s.z, s.ldz, f32(s.A),
+                                         f32(s.bias), f32(s.skip), f32(s.S), f32(out), y.data_ptr(), B, s.H, s.G, s.P,
+                                         s.N, c.io, soft != 0, c.stream());
+        }
+        if (rc != LR_OK) return refused(rc);
+        return pair_of(y, Sn, args[11]);
+    } catch (...) {
+        return thrown(launched);
+    }
+}
+
+// (q, k, H, Hk, norm code, gamma_q, gamma_k, freqs, pos, pairs code, eps) -> (q, k)
+PyObject *head_norm_rope(PyObject *, PyObject *const *args, Py_ssize_t n) {
+    if (n != 11) Py_RETURN_NONE;
+    bool launched = false;
+    try {
+        Call c;
+        const at::Tensor *q = c.first_rows(args[0], 0);
+        int64_t H, Hk, norm, pairs, ldq, ldk, rot = 0;
+        float eps;
+        if (q == nullptr || !to_int(args[2], &H) || H < 1 || !to_int(args[4], &norm) || !to_int(args[9], &pairs) ||
+            !to_float(args[10], &eps) || q->size(-1) % H != 0)
+            Py_RETURN_NONE;
+        Hk = H;
+        if (args[3] != Py_None && (!to_int(args[3], &Hk) || Hk < 1)) Py_RETURN_NONE;
+        if (args[1] == Py_None) Hk = 0;
+        const int64_t d = q->size(-1) / H;
+        std::vector<int64_t> lead(q->sizes().begin(), q->sizes().end() - 1), ks(lead);
+        ks.push_back(Hk * d);
+        void *pq, *pk, *gq, *gk, *freqs = nullptr, *pos = nullptr;
+        if (!c.rows(args[0], false, false, &pq, &ldq, q->sizes()) || !c.rows(args[1], false, true, &pk, &ldk, ks) ||
+            !c.take(args[5], at::kFloat, {d}, true, &gq) || !c.take(args[6], at::kFloat, {d}, true, &gk))
+            Py_RETURN_NONE;
+        if (args[7] != Py_None) {
+            if (!THPVariable_CheckExact(args[7])) Py_RETURN_NONE;
+            const int64_t m = THPVariable_Unpack(args[7]).numel();
+            if (m < 1 || 2 * m > d || !c.take(args[7], at::kFloat, {m}, false, &freqs) ||
+                !c.take(args[8], at::kInt, lead, false, &pos))
+                Py_RETURN_NONE;
+            rot = 2 * m;
+        }
+        at::Tensor qo, ko;
+        int rc;
+        {
+            const Unlocked unlocked;
+            qo = at::empty(q->sizes(), q->options());
+            if (Hk > 0) ko = at::empty(ks, q->options());
+            launched = true;
+            rc = lr_head_norm_rope(pq, ldq, pk, ldk, f32(gq), f32(gk), f32(freqs), static_cast<int32_t *>(pos),
+                                   qo.data_ptr(), ko.defined() ? ko.data_ptr() : nullptr, q->numel() / (H * d), H, Hk, d,
+                                   rot, static_cast<lr_norm>(norm), eps, static_cast<lr_pairs>(pairs), c.io, c.stream());
+        }
+        if (rc != LR_OK) return refused(rc);
+        return pair_of(qo, ko, Py_None);
+    } catch (...) {
+        return thrown(launched);
+    }
+}
+
 template <typename F>
 PyCFunction fast(F f) {
     return reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f));
@@ -259,6 +531,11 @@ PyMethodDef kMethods[] = {
     {"decay_attn", fast(decay_attn), METH_FASTCALL, nullptr},
     {"decay_attn_step", fast(decay_attn_step), METH_FASTCALL, nullptr},
     {"group_norm_act", fast(group_norm_act), METH_FASTCALL, nullptr},
+    {"causal_conv", fast(causal_conv), METH_FASTCALL, nullptr},
+    {"causal_conv_step", fast(causal_conv_step), METH_FASTCALL, nullptr},
+    {"selective_heads", fast(selective_heads), METH_FASTCALL, nullptr},
+    {"selective_heads_step", fast(selective_heads_step), METH_FASTCALL, nullptr},
+    {"head_norm_rope", fast(head_norm_rope), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_lrtorch", nullptr, -1, kMethods, nullptr, nullptr, nullptr, nullptr};
