@@ -5,9 +5,19 @@
 //
 // Every input is read once and every output written once (2 W operations an
 // element), so memory bandwidth bounds the prompt form and the launch's latency
-// the step.  A thread owns one vector of neighbouring channels over a range of
-// steps: its taps and the last W - 1 inputs stay in registers, and kGroup steps'
-// loads are in flight before the first is used.
+// the step.  A thread owns one vector of four channels (one where rows do not fit
+// vectors) over a range of steps: its taps and the last W - 1 inputs stay in registers,
+// and the steps' loads are in flight in groups, each sent for again as soon as it is
+// used.  Measured, in turn over 500 MB: bf16 B4 L4096 C2304 W4, a slice, 29.0 us (77 % of
+// the copy bandwidth); B1 L32768 52.5 (85 %); fp32 B4 L4096 W2 47.0 (95 %); fp32 B8 L1017
+// C1320 W3 17.6, C1321 (a value at a time) 18.7; bf16 B1 L77 3.3.  In bf16 the operations
+// count: two special functions a value for silu alone.
+//   eight channels a thread: bf16 36-40 us (217 registers without a bound: 48)
+//   eight steps' loads, used before the next are sent for 31.1 us; four groups of four in
+//   turn 29.0, two 31.9; fp32 two 47.0, four 50.4
+//   one reciprocal for two values of silu: 29.3
+#include <type_traits>
+
 #include "lr_decay.cuh"
 #include "lr_vec.cuh"
 
@@ -15,7 +25,6 @@ namespace lr {
 namespace {
 
 constexpr int kConvT = 128;    // threads per block
-constexpr int kGroup = 8;      // steps whose loads are in flight
 
 struct ConvArgs {
     const void *x;
@@ -54,20 +63,25 @@ __device__ __forceinline__ void load_taps(const ConvArgs &a, int c, float (&wt)[
     }
 }
 
-// The output of one step from the W inputs that end there.
+// The output of one step from the W inputs that end there; two channels at a time.
 template <typename X, int W>
 __device__ __forceinline__ typename X::Raw conv_one(const float (*in)[X::N], const float (&wt)[W][X::N],
                                                     const float (&be)[X::N], int act) {
     float v[X::N];
+    if constexpr (X::N % 2 == 0) {
 #pragma unroll
-    for (int i = 0; i < X::N; ++i) {
-        v[i] = be[i];
+        for (int i = 0; i < X::N; i += 2) {
+            float2 y = pair(be + i);
 #pragma unroll
-        for (int j = 0; j < W; ++j) v[i] = fmaf(wt[j][i], in[j][i], v[i]);
-    }
-    if (act == LR_ACT_SILU) {
+            for (int j = 0; j < W; ++j) y = __ffma2_rn(pair(wt[j] + i), pair(in[j] + i), y);
+            if (act == LR_ACT_SILU) y = silu2_f(y);
+            v[i] = y.x, v[i + 1] = y.y;
+        }
+    } else {
+        v[0] = be[0];
 #pragma unroll
-        for (int i = 0; i < X::N; ++i) v[i] = silu_f(v[i]);
+        for (int j = 0; j < W; ++j) v[0] = fmaf(wt[j][0], in[j][0], v[0]);
+        if (act == LR_ACT_SILU) v[0] = silu_f(v[0]);
     }
     return X::narrow(v);
 }
@@ -82,9 +96,9 @@ __device__ __forceinline__ Raw input_at(const Raw *x, int64_t ld, const Raw *sta
 // Range 0 of a row alone reads the row's old state and writes its new one, which
 // may be the same memory: each of its threads has read all it needs by then.
 template <typename X, int W>
-__global__ void __launch_bounds__(kConvT) conv_kernel(const ConvArgs a) {
+__global__ void __launch_bounds__(kConvT, X::N == 1 ? 8 : 4) conv_kernel(const ConvArgs a) {
     using Raw = typename X::Raw;
-    constexpr int VN = X::N;
+    constexpr int VN = X::N, R = sizeof(Raw) == 16 ? 2 : 4, Q = 4;
     launch_dependents();
     grid_dependency_wait();
     const int nvec = a.C / VN;
@@ -110,24 +124,39 @@ __global__ void __launch_bounds__(kConvT) conv_kernel(const ConvArgs a) {
     int t = t0;
     if (t < te) {
         load_taps<VN, W>(a, cv * VN, wt, be);
-        float in[W - 1 + kGroup][VN];
+        float in[W - 1 + Q][VN];
 #pragma unroll
         for (int j = 0; j < W - 1; ++j) X::widen(input_at<Raw, W>(x, ld, state, nvec, t0 - (W - 1) + j), in[j]);
-        for (; t < te; t += kGroup) {
-            Raw r[kGroup];
-            const bool full = t + kGroup <= te;
+        Raw r[R][Q];   // steps t ..: R groups of Q, each loaded again as soon as it is widened
+        const Raw *next = x + int64_t(t) * ld;
+        Raw *dst = y + int64_t(t) * nvec;
 #pragma unroll
-            for (int k = 0; k < kGroup; ++k) r[k] = full || t + k < te ? x[int64_t(t + k) * ld] : Raw{};
+        for (int g = 0; g < R; ++g)
 #pragma unroll
-            for (int k = 0; k < kGroup; ++k) X::widen(r[k], in[W - 1 + k]);
+            for (int k = 0; k < Q; ++k) r[g][k] = t + g * Q + k < te ? next[(g * Q + k) * ld] : Raw{};
+        auto round = [&](auto whole) {   // whole: the next R groups are there too
+            constexpr bool ALL = decltype(whole)::value;
+            next += R * Q * ld;
 #pragma unroll
-            for (int k = 0; k < kGroup; ++k)
-                if (full || t + k < te) y[int64_t(t + k) * nvec] = conv_one<X, W>(in + k, wt, be, a.act);
+            for (int g = 0; g < R; ++g) {
 #pragma unroll
-            for (int j = 0; j < W - 1; ++j)
+                for (int k = 0; k < Q; ++k) X::widen(r[g][k], in[W - 1 + k]);
 #pragma unroll
-                for (int i = 0; i < VN; ++i) in[j][i] = in[kGroup + j][i];
-        }
+                for (int k = 0; k < Q; ++k)
+                    if (ALL || t + (R + g) * Q + k < te) r[g][k] = next[(g * Q + k) * ld];
+#pragma unroll
+                for (int k = 0; k < Q; ++k)
+                    if (ALL || t + g * Q + k < te) dst[int64_t(g * Q + k) * nvec] = conv_one<X, W>(in + k, wt, be, a.act);
+#pragma unroll
+                for (int j = 0; j < W - 1; ++j)
+#pragma unroll
+                    for (int i = 0; i < VN; ++i) in[j][i] = in[Q + j][i];
+            }
+            t += R * Q;
+            dst += int64_t(R * Q) * nvec;
+        };
+        while (t + 2 * R * Q <= te) round(std::true_type{});
+        while (t < te) round(std::false_type{});
     }
     for (t = max(t0, te); t < t1; ++t) y[int64_t(t) * nvec] = Raw{};   // past the row's end
     if (tile == 0 && a.state_out != nullptr) {
@@ -176,9 +205,9 @@ int conv_go(ConvArgs a, bool step, cudaStream_t s) {
     int sms = 0;
     if (device_sm_count(&sms) != LR_OK) return LR_ERR_CUDA;
     // the longest ranges that still give every SM its threads: a range reads its
-    // taps and the W - 1 inputs before it again
+    // taps and the W - 1 inputs before it again (B4 L4096: 32 steps 31.8 us, 64 29.0, 128 29.1)
     a.steps = 64;
-    while (a.steps > kGroup && a.B * ((a.L + a.steps - 1) / a.steps) * nvec < int64_t(sms) * 512) a.steps /= 2;
+    while (a.steps > 16 && a.B * ((a.L + a.steps - 1) / a.steps) * nvec < int64_t(sms) * 512) a.steps /= 2;
     const int64_t tiles = (a.L + a.steps - 1) / a.steps, grid = (a.B * tiles * nvec + kConvT - 1) / kConvT;
     if (grid > INT32_MAX) return LR_ERR_UNSUPPORTED;
     a.tiles = int(tiles);
@@ -198,7 +227,7 @@ int conv_taps(const ConvArgs &a, int W, bool step, cudaStream_t s) {
 template <typename IO>
 int conv_io(const ConvArgs &a, int W, bool step, cudaStream_t s) {
     // whole vectors where every row of x and y starts on one
-    constexpr int V = 16 / sizeof(IO);
+    constexpr int V = 4;
     if (a.C % V == 0 && a.ldx % V == 0) return conv_taps<Vec<IO, V>>(a, W, step, s);
     return conv_taps<Vec<IO, 1>>(a, W, step, s);
 }

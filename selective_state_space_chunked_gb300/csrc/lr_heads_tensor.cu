@@ -114,13 +114,6 @@ __device__ __forceinline__ uint4 xor1(uint4 v) {
                       __shfl_xor_sync(0xffffffffu, v.z, 1), __shfl_xor_sync(0xffffffffu, v.w, 1));
 }
 
-// silu of a pair of bf16 values.
-__device__ __forceinline__ float2 silu2(uint32_t z) {
-    const float2 x = make_float2(lo_f(z), hi_f(z)), e = __fmul2_rn(x, make_float2(-kLog2e, -kLog2e));
-    const float2 d = __fadd2_rn(make_float2(ex2_approx(e.x), ex2_approx(e.y)), make_float2(1.0f, 1.0f));
-    return __fmul2_rn(x, make_float2(rcp_approx(d.x), rcp_approx(d.y)));
-}
-
 // Position of a (batch row, head)'s step in the gates' arrays, and of its chunk's record.
 __device__ __forceinline__ size_t step_at(const DecayArgs &a, int64_t bh, int64_t t) {
     return size_t(bh) * ((a.L + C - 1) / C * C) + t;
@@ -968,7 +961,7 @@ __global__ void __launch_bounds__(ht::THREADS, 1)
                     for (int r = 0; r < 8; ++r) {
                         float2 y = __fmul2_rn(u2, make_float2(d[2 * r], d[2 * r + 1]));
                         if (valid) zero = __ffma2_rn(y, make_float2(0.0f, 0.0f), zero);
-                        y = __fmul2_rn(y, silu2(zw[r]));
+                        y = __fmul2_rn(y, silu2_f(make_float2(lo_f(zw[r]), hi_f(zw[r]))));
                         w[r] = pack(y.x, y.y);
                     }
                     z[0][0] = z[1][0], z[0][1] = z[1][1];

@@ -43,6 +43,13 @@ template <> struct Vec<__nv_bfloat16, 4> {
     __device__ __forceinline__ static void widen(const Raw &u, float *v) { widen2(u.x, v), widen2(u.y, v + 2); }
     __device__ __forceinline__ static Raw narrow(const float *v) { return make_uint2(narrow2(v), narrow2(v + 2)); }
 };
+// silu of a pair
+__device__ __forceinline__ float2 silu2_f(float2 x) {
+    const float2 e = __fmul2_rn(x, make_float2(-kLog2e, -kLog2e));
+    const float2 d = __fadd2_rn(make_float2(ex2_approx(e.x), ex2_approx(e.y)), make_float2(1.0f, 1.0f));
+    return __fmul2_rn(x, make_float2(rcp_approx(d.x), rcp_approx(d.y)));
+}
+
 // a value at a time
 template <> struct Vec<float, 1> {
     static constexpr int N = 1;
