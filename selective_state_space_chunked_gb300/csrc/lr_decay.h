@@ -24,7 +24,7 @@ struct HeadsArgs {
     unsigned char *chunk;
     float *left;             // [batch row, head][segment]
 };
-constexpr int kChunkRecord = 560;   // bytes of a chunk's
+constexpr int kChunkRecord = 576;   // bytes of a chunk's
 
 
 // One call, as its kernels see it (device pointers; see lr_decay_attn_fwd).

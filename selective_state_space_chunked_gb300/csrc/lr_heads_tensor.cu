@@ -59,8 +59,10 @@ struct Chunk {
     float col[C];    // column factors of P: w d; steep: d 2^(L_e - L_s), e the last step of s' 16
     float m;         // the state's factor (1: none)
     int steep;
-    int pad[2];
+    long long total; // the chunk's log2 decay
     int last[8];     // steep: L of every 16 steps' last, see units_of
+    float after;     // the decay of the segment's chunks after it (segments but the last)
+    int pad[3];
 };
 static_assert(sizeof(Chunk) == kChunkRecord, "");
 
@@ -148,6 +150,9 @@ __global__ void __launch_bounds__(1024) heads_gates_kernel(const __grid_constant
     const int n_chunks = (nrun + C - 1) / C;
     const dec::Gates<true> gates(a, h);
     const bf *g = static_cast<const bf *>(a.g) + (size_t(b) * a.L + s0) * a.hd.ldg + h;
+    auto record_of = [&](int c) {
+        return reinterpret_cast<Chunk *>(const_cast<unsigned char *>(record_at(a, bh, s0 + int64_t(c) * C)));
+    };
     bool bad = false;
     long long base = 0, tot = 0;
     // steps 4 lane .. of chunk c: step sizes and decays since the chunk's start
@@ -187,19 +192,24 @@ __global__ void __launch_bounds__(1024) heads_gates_kernel(const __grid_constant
         if (lane == 0) totals[warp] = all;
         __syncthreads();
         if (warp == 0) {   // (it alone holds base and tot)
-            const long long mine = lane < warps ? totals[lane] : 0;
+            const int n = min(warps, n_chunks - c0);
+            const long long mine = lane < n ? totals[lane] : 0;
+            const uint32_t steep_of = __ballot_sync(0xffffffffu, mine < kSteepChunk);
             long long kept = 0;
-            int how = 0;
-#pragma unroll 4
-            for (int j = 0; j < min(warps, n_chunks - c0); ++j) {
-                const long long t = __shfl_sync(0xffffffffu, mine, j), e = base + t;
-                const bool s = t < kSteepChunk, r = s || e < kRescaleTensor;
-                if (j == lane) kept = base, how = int(r) + 2 * int(s);
-                base = r ? 0 : e;
-                tot = max(tot + t, -(1ll << 60));
+            uint32_t re_of = 0;
+            static_assert((kRescaleTensor & 0xffffffffll) == 0, "a comparison of the upper halves");
+#pragma unroll 8
+            for (int j = 0; j < n; ++j) {   // few operations: one warp, and each needs the last
+                if (j == lane) kept = base;
+                base += __shfl_sync(0xffffffffu, mine, j);
+                if ((steep_of >> j & 1) != 0 || int(base >> 32) < int(kRescaleTensor >> 32)) base = 0, re_of |= 1u << j;
             }
             before_of[lane] = kept;
-            how_of[lane] = how;
+            how_of[lane] = int(re_of >> lane & 1) + 2 * int(steep_of >> lane & 1);
+            long long sum = mine;
+#pragma unroll
+            for (int m = 16; m >= 1; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
+            tot = max(tot + sum, -(1ll << 60));
         }
         __syncthreads();
         const long long before = before_of[warp], end = before + all;
@@ -230,35 +240,37 @@ __global__ void __launch_bounds__(1024) heads_gates_kernel(const __grid_constant
         float4 *own = reinterpret_cast<float4 *>(a.hd.own + at);
         own[0] = make_float4(x[0], __int_as_float(u[0]), x[1], __int_as_float(u[1]));
         own[1] = make_float4(x[2], __int_as_float(u[2]), x[3], __int_as_float(u[3]));
-        Chunk *rec = reinterpret_cast<Chunk *>(const_cast<unsigned char *>(record_at(a, bh, s0 + int64_t(c) * C)));
+        if (seg < a.n_seg - 1) {   // weights to the chunk's end, for the state that the segment leaves
+            float e[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) e[i] = delta[i] * dec::exp2_fix(all - l[i]);
+            *reinterpret_cast<float4 *>(a.hd.to_end + at) = make_float4(e[0], e[1], e[2], e[3]);
+        }
+        Chunk *rec = record_of(c);
         reinterpret_cast<float4 *>(rec->col)[lane] = make_float4(col[0], col[1], col[2], col[3]);
         if ((lane & 3) == 3) rec->last[lane >> 2] = u[3];
-        if (lane == 0) rec->m = re ? dec::exp2_fix(end) : 1.0f, rec->steep = steep;
+        if (lane == 0) rec->m = re ? dec::exp2_fix(end) : 1.0f, rec->steep = steep, rec->total = all;
     }
     // the decay that the scaled state still lacks when the segment is done
     if (threadIdx.x == 0) a.hd.left[bh * a.n_seg + seg] = dec::exp2_fix(base);
-    if (seg < a.n_seg - 1) {   // weights to the segment's end, for the state that it leaves; from the last chunk back
-        if (threadIdx.x == 0) a.seg_tot[bh * (a.n_seg - 1) + seg] = tot;
-        long long after = 0;
-        for (int c1 = n_chunks; c1 > 0; c1 -= warps) {
-            const int c = c1 - 1 - warp;
-            all = 0;
-            if (c >= 0) chunk(c);
-            __syncthreads();   // the last round's totals have been read
-            if (lane == 0) totals[warp] = all;
-            __syncthreads();
-            long long own = after;
-            for (int j = 0; j < warps; ++j) {
-                if (j < warp) own += totals[j];
-                after += totals[j];
-            }
-            after = max(after, -(1ll << 60));
-            if (c < 0) continue;
-            float w[4];
+    if (seg < a.n_seg - 1) {   // what decays after each chunk, from the last one back
+        __syncthreads();       // the records
+        if (warp == 0) {
+            if (lane == 0) a.seg_tot[bh * (a.n_seg - 1) + seg] = tot;
+            long long after = 0;
+            for (int c1 = n_chunks; c1 > 0; c1 -= 32) {
+                const int c = c1 - 1 - lane;
+                Chunk *rec = c >= 0 ? record_of(c) : nullptr;
+                const long long t = c >= 0 ? rec->total : 0;
+                long long incl = t;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) w[i] = delta[i] * dec::exp2_fix(own + all - l[i]);
-            *reinterpret_cast<float4 *>(a.hd.to_end + step_at(a, bh, s0 + int64_t(c) * C + 4 * lane)) =
-                make_float4(w[0], w[1], w[2], w[3]);
+                for (int m = 1; m < 32; m <<= 1) {
+                    const long long up = __shfl_up_sync(0xffffffffu, incl, m);
+                    if (lane >= m) incl += up;
+                }
+                if (c >= 0) rec->after = dec::exp2_fix(after + incl - t);
+                after = max(after + __shfl_sync(0xffffffffu, incl, 31), -(1ll << 60));
+            }
         }
     }
     if (bad) status_report(sref, LR_ERR_RANGE);
@@ -416,10 +428,11 @@ __global__ void __launch_bounds__(hs::THREADS, 1)
         // 16-byte group (8 value rows) k8 of steps r32 and r32 + 32 of each half
         const int r32 = tid >> 3, k8 = tid & 7;
         const float *to_end = a.hd.to_end + ht::step_at(a, bh, s0) + r32;
-        float wn[4] = {};   // the next chunk's
+        float wn[4] = {}, fn = 0.0f;   // the next chunk's, and what decays after it
         auto load = [&](int c) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) wn[i] = __ldcg(to_end + c * C + 32 * i);
+            fn = __ldcg(&reinterpret_cast<const ht::Chunk *>(ht::record_at(a, bh, s0 + int64_t(c) * C))->after);
         };
         if (n_chunks > 0) load(0);
         for (int c = 0; c < n_chunks; ++c) {
@@ -428,7 +441,7 @@ __global__ void __launch_bounds__(hs::THREADS, 1)
             const bool tail = c * C + C > nrun;
             float wc[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) wc[i] = wn[i];
+            for (int i = 0; i < 4; ++i) wc[i] = wn[i] * fn;
             if (c + 1 < n_chunks) load(c + 1);
             bool ok = hw(FULL_V + st, c / NS);
             if (ok && tail) ok = hw(FULL_K + st, c / NS);
@@ -838,7 +851,10 @@ __global__ void __launch_bounds__(ht::THREADS, 1)
                     }
                     if (steep) {
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) p[e] *= rf;
+                        for (int e = 0; e < 16; e += 2) {
+                            const float2 y = __fmul2_rn(make_float2(p[e], p[e + 1]), make_float2(rf, rf));
+                            p[e] = y.x, p[e + 1] = y.y;
+                        }
                     }
                 }
                 if (diag) {   // row t sees columns up to its own, which takes the skip
@@ -938,9 +954,14 @@ __global__ void __launch_bounds__(ht::THREADS, 1)
             for (int q = 0; q < 2; ++q) {
                 float d[16];
                 tmem_ld16_nowait(Y + 16 * q, d);
+                tmem_ld_wait_tied(d);
+                if (q == 1) {   // P's columns are free; the rest of the outputs is off every chain
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) arrive(&bar[Y_DONE + st]);
+                }
                 const int col = i0 + 16 * q;
                 if (PARTS) {   // steps past the row's end are the sum's to clear
-                    tmem_ld_wait_tied(d);
                     float *dst = a.o_part + ((size_t(part) * a.B + b) * a.L + s0 + t) * HV + size_t(h) * dv + col;
 #pragma unroll
                     for (int r = 0; r < 16; r += 4) {
@@ -956,7 +977,6 @@ __global__ void __launch_bounds__(ht::THREADS, 1)
                     const uint4 mine = odd ? z1 : z0, give = odd ? z0 : z1;
                     const uint4 got = xor1(give), lo = odd ? got : mine, hi = odd ? mine : got;
                     const uint32_t zw[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-                    tmem_ld_wait_tied(d);
 #pragma unroll
                     for (int r = 0; r < 8; ++r) {
                         float2 y = __fmul2_rn(u2, make_float2(d[2 * r], d[2 * r + 1]));
@@ -966,7 +986,6 @@ __global__ void __launch_bounds__(ht::THREADS, 1)
                     }
                     z[0][0] = z[1][0], z[0][1] = z[1][1];
                 } else {
-                    tmem_ld_wait_tied(d);
 #pragma unroll
                     for (int r = 0; r < 8; ++r) {
                         const float2 y = __fmul2_rn(u2, make_float2(d[2 * r], d[2 * r + 1]));
@@ -984,9 +1003,6 @@ __global__ void __launch_bounds__(ht::THREADS, 1)
                     if (s0 + t - odd + 1 < send) *reinterpret_cast<uint4 *>(dst + HV) = odd ? mine : got;
                 }
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) arrive(&bar[Y_DONE + st]);
         }
         if (not_finite(zero)) ctl->redo = 1;
     } else {   // --------------------------------------------------------- state
