@@ -29,10 +29,11 @@
 //
 // A thread block owns 64 value rows of one (batch row, head, time segment), 128 key
 // columns.  Roles, connected by mbarriers: state (8 warps), output (8: 32 rows by 32
-// columns a warp, so that all of a thread's outputs are in registers before the
-// accumulator is handed back, and gate and stores come after that), front (8), weight (4),
-// TMA, and one warp for each of dS, P and O's products.  TMEM: P 2 x 128 columns (PD
-// inside), O 64, dS 3 x 64.
+// columns a warp), front (8), weight (4), TMA, and one warp for each of dS, P and O's
+// products.  TMEM: P 2 x 128 columns (PD inside), O 2 x 64, so that the gate and the stores
+// of one chunk's outputs stand in no chunk's way, dS 64, onto which the three terms of the
+// state's weights add up (side by side, as in the decayed attention, they would take the
+// columns of O's second buffer).
 #include "lr_decay_tensor.cuh"
 
 namespace lr {
@@ -69,9 +70,12 @@ static_assert(sizeof(Chunk) == kChunkRecord, "");
 constexpr uint32_t HALF = C * 128;              // 64 columns of Q or K: 128 rows of 128 bytes
 constexpr uint32_t Q_BYTES = 2 * HALF, V_BYTES = C * RB * 2;
 constexpr uint32_t OFF_Q = 0, OFF_K = 2 * Q_BYTES, OFF_V = 4 * Q_BYTES;
-constexpr uint32_t OFF_W = OFF_V + 2 * V_BYTES;     // three terms [128 s][64 i]
-constexpr uint32_t OFF_SB = OFF_W + 3 * V_BYTES;    // bf16 state [128 j][64 i]
-constexpr uint32_t OFF_G = OFF_SB + 128 * RB * 2;   // 2 x Chunk
+// The state's weighted values, three terms of [4 quarters][16 s][64 i]: half of a quarter's
+// steps at a time, which leaves the room for the gate's tile.
+constexpr uint32_t OFF_W = OFF_V + 2 * V_BYTES, TERM = V_BYTES / 2;
+constexpr uint32_t OFF_SB = OFF_W + 3 * TERM;       // bf16 state [128 j][64 i]
+constexpr uint32_t OFF_Z = OFF_SB + 128 * RB * 2;   // the gate [128 s][64 i]
+constexpr uint32_t OFF_G = OFF_Z + V_BYTES;         // 2 x Chunk
 constexpr uint32_t OFF_BAR = OFF_G + 2 * kChunkRecord;
 // barriers; [2] by chunk parity, [4] by quarter
 enum {
@@ -82,14 +86,13 @@ enum {
     K_DONE = 18,     // chunk c's accumulator read (8 output warps)
     OX_DONE = 20,    // Q S^T complete: the bf16 state has been read
     O_DONE = 22,
-    W_READY = 24,    // weighted values of a quarter
+    W_READY = 24,    // weighted values of half a quarter, twice a chunk
     W_FREE = 28,
-    SB_READY = 32,   // bf16 state before chunk c (8 state warps)
-    DS_DONE, DS_FREE,
+    DS_DONE = 32, DS_FREE = 34,   // [2]
+    FULL_Z = 36, EMPTY_Z,
+    SB_READY,        // bf16 state before chunk c (8 state warps)
     FIX,             // a steep chunk's Q S^T scaled (8 output warps)
-    MMA_END,
-    Y_DONE,          // [2] chunk c's outputs have left P's columns (8 output warps)
-    NBAR = Y_DONE + 2
+    MMA_END, NBAR
 };
 constexpr uint32_t OFF_TMEM = OFF_BAR + NBAR * 8;
 constexpr uint32_t OFF_CTL = OFF_TMEM + 8;
@@ -97,10 +100,10 @@ constexpr uint32_t SMEM = OFF_CTL + 40;
 static_assert(OFF_BAR % 8 == 0 && OFF_CTL % 8 == 0, "");
 static_assert(SMEM <= 227 * 1024, "one block per SM");
 
-constexpr uint32_t T_P = 0, T_O = 256, T_DS = 320;
+constexpr uint32_t T_P = 0, T_O = 256, T_DS = 384;   // 2 x 128, 2 x 64, 2 x 64 columns
 constexpr uint32_t IDESC_P = umma_idesc_bf16(128, 128, 0, 0);
 constexpr uint32_t IDESC_O = umma_idesc_bf16(128, 64, 0, 1);
-constexpr uint32_t IDESC_DS = umma_idesc_bf16(128, 192, 1, 1);
+constexpr uint32_t IDESC_DS = umma_idesc_bf16(128, 64, 1, 1);
 
 // `bytes` (a multiple of 16) from global to shared memory, both 16-byte aligned.
 __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
@@ -525,12 +528,13 @@ __global__ void __launch_bounds__(hs::THREADS, 1)
 }
 
 // ---------------------------------------------------------------------------
-// PARTS: the block's part of the key columns, its outputs a term of the sum
-template <bool PARTS>
+// PARTS: the block's part of the key columns, its outputs a term of the sum, which the sum
+// gates; GATE: outputs are gated here
+template <bool PARTS, bool GATE>
 __global__ void __launch_bounds__(ht::THREADS, 1)
     heads_tensor_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                        const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ DecayArgs a, int n_vt,
-                        uint64_t timeout_ns, StatusRef sref) {
+                        const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_z,
+                        const __grid_constant__ DecayArgs a, int n_vt, uint64_t timeout_ns, StatusRef sref) {
     using namespace ht;
     using bf = __nv_bfloat16;
     extern __shared__ __align__(1024) unsigned char sm[];
@@ -570,7 +574,7 @@ __global__ void __launch_bounds__(ht::THREADS, 1)
         for (int i = 0; i < NBAR; ++i) {
             int n = 1;
             if (i >= F_DONE && i < K_DONE + 2) n = 8;
-            if (i == SB_READY || i == DS_FREE || i == FIX || i >= Y_DONE) n = 8;
+            if (i == DS_FREE || i == DS_FREE + 1 || i == EMPTY_Z || i == SB_READY || i == FIX) n = 8;
             // K is read by dS and P, Q by P and OX, V by the weight warps (through dS) and OI
             if ((i >= EMPTY_Q && i < EMPTY_Q + 2) || (i >= EMPTY_K && i < EMPTY_K + 2) ||
                 (i >= EMPTY_V && i < EMPTY_V + 2))
@@ -602,6 +606,7 @@ __global__ void __launch_bounds__(ht::THREADS, 1)
             prefetch_tensormap(&tm_q);
             prefetch_tensormap(&tm_k);
             prefetch_tensormap(&tm_v);
+            if (GATE) prefetch_tensormap(&tm_z);
             auto load_qk = [&](int n, const CUtensorMap *tm, int off, int full) {
                 const int st = n & 1, t = s0 + n * C;
                 unsigned char *dst = sm + off + st * Q_BYTES;
@@ -620,26 +625,37 @@ __global__ void __launch_bounds__(ht::THREADS, 1)
                 bulk_load(sm + OFF_G + st * kChunkRecord, record_at(a, bh, s0 + int64_t(n) * C), kChunkRecord,
                           &bar[FULL_G + st]);
             };
-            int nq = 0, nk = 0, nv = 0, ng = 0;
+            auto load_z = [&](int n) {   // the one tile
+                mbar_arrive_expect_tx(&bar[FULL_Z], V_BYTES);
+                tma_load_4d(sm + OFF_Z, &tm_z, &bar[FULL_Z], vt * RB, h, s0 + n * C, b);
+            };
+            int nq = 0, nk = 0, nv = 0, ng = 0, nz = 0;
             for (; nv < 2 && nv < n_chunks; ++nv, ++nq, ++nk) {
                 load_qk(nv, &tm_q, OFF_Q, FULL_Q);
                 load_qk(nv, &tm_k, OFF_K, FULL_K);
                 load_v(nv);
             }
+            if (GATE && n_chunks > 0) load_z(nz), ++nz;
             gates_wait();
             fence_proxy_async_global();
             for (; ng < nv; ++ng) load_g(ng);
             // in the order in which a chunk lets go of them; once its last products (O's) have
             // let go of V nobody reads its record either
-            for (int n = 2; n < n_chunks; ++n) {
+            for (int n = 2; n <= n_chunks; ++n) {
                 const int st = n & 1, ph = (n - 2) >> 1;
-                if (!hw(EMPTY_Q + st, ph)) break;
-                load_qk(n, &tm_q, OFF_Q, FULL_Q), ++nq;
-                if (!hw(EMPTY_K + st, ph)) break;
-                load_qk(n, &tm_k, OFF_K, FULL_K), ++nk;
-                if (!hw(EMPTY_V + st, ph)) break;
-                load_v(n), ++nv;
-                load_g(n), ++ng;
+                if (n < n_chunks) {
+                    if (!hw(EMPTY_Q + st, ph)) break;
+                    load_qk(n, &tm_q, OFF_Q, FULL_Q), ++nq;
+                    if (!hw(EMPTY_K + st, ph)) break;
+                    load_qk(n, &tm_k, OFF_K, FULL_K), ++nk;
+                    if (!hw(EMPTY_V + st, ph)) break;
+                    load_v(n), ++nv;
+                    load_g(n), ++ng;
+                }
+                if (GATE) {
+                    if (!hw(EMPTY_Z, n - 2)) break;
+                    load_z(n - 1), ++nz;
+                }
             }
             // copies still in flight land before the block exits
             auto land = [&](int full, int n) {
@@ -649,6 +665,7 @@ __global__ void __launch_bounds__(ht::THREADS, 1)
             land(FULL_K, nk);
             land(FULL_V, nv);
             land(FULL_G, ng);
+            if (nz > 0) mbar_wait_bounded(&bar[FULL_Z], (nz - 1) & 1, timeout_ns);
         }
     } else if (warp >= DS_WARP) {   // -------------------------------- products
         // every wait's answer is made warp-uniform, and so is all that follows
@@ -656,24 +673,28 @@ __global__ void __launch_bounds__(ht::THREADS, 1)
         const bool lead = elect_one();
         const uint32_t base = __shfl_sync(0xffffffffu, smem_u32(sm), 0);
         if (warp == DS_WARP) {
-            const uint64_t dW = umma_smem_desc(base + OFF_W, V_BYTES, 1024);
+            const uint64_t dW = umma_smem_desc(base + OFF_W, HALF, 1024);
             for (int c = 0; c < n_chunks; ++c) {
                 const int st = c & 1;
-                // the last dS has been read
-                if (!hu(FULL_K + st, c >> 1) || (c >= 1 && !hu(DS_FREE, c - 1))) break;
+                // the last dS in these columns has been read
+                if (!hu(FULL_K + st, c >> 1) || (c >= 2 && !hu(DS_FREE + st, (c - 2) >> 1))) break;
                 const uint64_t dK = umma_smem_desc(base + OFF_K + st * Q_BYTES, HALF, 1024);
                 bool ok = true;
 #pragma unroll 1
-                for (int qt = 0; qt < 4; ++qt) {
-                    ok = ok && hu(W_READY + qt, c);
+                for (int e = 0; e < 8; ++e) {   // the quarters' first halves, then their second ones
+                    const int qt = e & 3, hf = e >> 2;
+                    ok = ok && hu(W_READY + qt, 2 * c + hf);
                     if (!ok) break;
                     tc_fence_after();
                     if (lead) {   // 16 steps are 2048 bytes on, 128 in the descriptors' units
-                        umma_bf16(tmem + T_DS, dK + 256 * qt, dW + 256 * qt, IDESC_DS, qt > 0);
-                        umma_bf16(tmem + T_DS, dK + 256 * qt + 128, dW + 256 * qt + 128, IDESC_DS, 1);
+                        // the three terms onto one accumulator, small ones first
+#pragma unroll
+                        for (int term = 2; term >= 0; --term)
+                            umma_bf16(tmem + T_DS + st * 64, dK + 256 * qt + 128 * hf, dW + (TERM >> 4) * term + 128 * qt,
+                                      IDESC_DS, e > 0 || term < 2);
                         umma_commit(&bar[W_FREE + qt]);
-                        if (qt == 3) {
-                            umma_commit(&bar[DS_DONE]);
+                        if (e == 7) {
+                            umma_commit(&bar[DS_DONE + st]);
                             umma_commit(&bar[EMPTY_K + st]);
                             umma_commit(&bar[EMPTY_V + st]);
                         }
@@ -686,8 +707,7 @@ __global__ void __launch_bounds__(ht::THREADS, 1)
             for (int c = 0; c < n_chunks; ++c) {
                 const int st = c & 1;
                 if (!hu(FULL_K + st, c >> 1) || !hu(FULL_Q + st, c >> 1)) break;
-                // chunk c - 2's PD has been used and its outputs are gone
-                if (c >= 2 && !hu(Y_DONE + st, (c - 2) >> 1)) break;
+                if (c >= 2 && !hu(O_DONE + st, (c - 2) >> 1)) break;   // chunk c - 2's PD has been used
                 tc_fence_after();
                 const uint64_t dQ = umma_smem_desc(base + OFF_Q + st * Q_BYTES, 16, 1024),
                                dK = umma_smem_desc(base + OFF_K + st * Q_BYTES, 16, 1024);
@@ -708,15 +728,15 @@ __global__ void __launch_bounds__(ht::THREADS, 1)
             int n_steep = 0;
             for (int c = 0; c < n_chunks; ++c) {
                 const int st = c & 1;
-                // the state before chunk c; the last outputs have been read
+                // the state before chunk c; chunk c - 2's outputs have been read
                 if (!hu(SB_READY, c) || !hu(FULL_Q + st, c >> 1)) break;
-                if (c >= 1 && !hu(K_DONE + ((c - 1) & 1), (c - 1) >> 1)) break;
+                if (c >= 2 && !hu(K_DONE + st, (c - 2) >> 1)) break;
                 tc_fence_after();
                 const uint64_t dQ = umma_smem_desc(base + OFF_Q + st * Q_BYTES, 16, 1024);
                 if (lead) {
 #pragma unroll 1
                     for (int kk = 0; kk < nkk; ++kk)
-                        umma_bf16(tmem + T_O, dQ + (((kk >> 2) * HALF + (kk & 3) * 32) >> 4), dS + 128 * kk, IDESC_O,
+                        umma_bf16(tmem + T_O + st * 64, dQ + (((kk >> 2) * HALF + (kk & 3) * 32) >> 4), dS + 128 * kk, IDESC_O,
                                   kk > 0);
                     umma_commit(&bar[OX_DONE + st]);
                     umma_commit(&bar[EMPTY_Q + st]);
@@ -724,17 +744,14 @@ __global__ void __launch_bounds__(ht::THREADS, 1)
                 __syncwarp();
                 if (!hu(F_DONE + st, c >> 1) || !hu(FULL_V + st, c >> 1)) break;
                 if (!hu(FULL_G + st, c >> 1) || (rec[st].steep != 0 && !hu(FIX, n_steep++))) break;
-                if (c * C + C > nrun) {   // the last chunk: V's rows past the end have been zeroed
-                    bool ok = true;
-                    for (int qt = 0; qt < 4; ++qt) ok = ok && hu(W_READY + qt, c);
-                    if (!ok) break;
-                }
+                // the last chunk: V's rows past the end have been zeroed for dS
+                if (c * C + C > nrun && !hu(DS_DONE + st, c >> 1)) break;
                 tc_fence_after();
                 const uint64_t dV = umma_smem_desc(base + OFF_V + st * V_BYTES, HALF, 1024);
                 if (lead) {   // onto Q S^T: same shape and accumulator, so in order
 #pragma unroll 1
                     for (int kk = 0; kk < C / 16; ++kk)
-                        umma_bf16_ts(tmem + T_O, tmem + T_P + st * 128 + (kk >> 2) * 64 + (kk & 3) * 8, dV + 128 * kk,
+                        umma_bf16_ts(tmem + T_O + st * 64, tmem + T_P + st * 128 + (kk >> 2) * 64 + (kk & 3) * 8, dV + 128 * kk,
                                      IDESC_O, 1);
                     umma_commit(&bar[O_DONE + st]);
                     umma_commit(&bar[EMPTY_V + st]);
@@ -749,41 +766,43 @@ __global__ void __launch_bounds__(ht::THREADS, 1)
         }
         __syncwarp();
     } else if (warp >= WEIGHT) {   // ----------------------------------- weight
-        const int s = tid - 32 * WEIGHT;   // this thread's step of the chunk
-        const int qt = warp - WEIGHT;
+        // lanes i and i + 16: step i of half a quarter, 32 value columns each
+        const int qt = warp - WEIGHT, i = lane & 15, wh = lane >> 4, r = 16 * qt + i;
         gates_wait();
-        const float *src = a.hd.weight + g0 + s;
+        const float *src = a.hd.weight + g0 + 32 * qt + i;
         float wn = n_chunks > 0 ? __ldcg(src) : 0.0f;
-        for (int c = 0; c < n_chunks; ++c) {
-            const int st = c & 1;
+        for (int c2 = 0; c2 < 2 * n_chunks; ++c2) {
+            const int c = c2 >> 1, st = c & 1, s = 32 * qt + 16 * (c2 & 1) + i;   // s: of the chunk
             unsigned char *V = sm + OFF_V + st * V_BYTES;
             const bool in = c * C + s < nrun;
             const float w = wn;
-            if (c + 1 < n_chunks) wn = __ldcg(src + (c + 1) * C);
+            if (c2 + 1 < 2 * n_chunks) wn = __ldcg(src + (c2 + 1 >> 1) * C + 16 * (c2 + 1 & 1));
             bool ok = hw(FULL_V + st, c >> 1);
             if (ok && c * C + C > nrun) ok = hw(FULL_K + st, c >> 1);
-            if (ok && c >= 1) ok = hw(W_FREE + qt, c - 1);
+            if (ok && c2 >= 1) ok = hw(W_FREE + qt, c2 - 1);
             if (!__all_sync(0xffffffffu, ok)) break;
+            const uint32_t from = sw128_offset(s, 32 * wh), to = OFF_W + sw128_offset(r, 32 * wh);
 #pragma unroll 1
-            for (int k = 0; k < 8; ++k) {
-                const uint32_t at = sw128_offset(s, 0) ^ (k << 4);   // group k of row s
-                uint4 u = *reinterpret_cast<const uint4 *>(V + at);
+            for (int k = 0; k < 4; ++k) {   // groups of 8 columns
+                uint4 u = *reinterpret_cast<const uint4 *>(V + (from ^ (k << 4)));
                 if (!in) u = make_uint4(0, 0, 0, 0);
                 const uint32_t uv[4] = {u.x, u.y, u.z, u.w};
                 uint32_t t1[4], t2[4], t3[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) three_terms(w, uv[e], t1[e], t2[e], t3[e]);
-                *reinterpret_cast<uint4 *>(sm + OFF_W + at) = make_uint4(t1[0], t1[1], t1[2], t1[3]);
-                *reinterpret_cast<uint4 *>(sm + OFF_W + V_BYTES + at) = make_uint4(t2[0], t2[1], t2[2], t2[3]);
-                *reinterpret_cast<uint4 *>(sm + OFF_W + 2 * V_BYTES + at) = make_uint4(t3[0], t3[1], t3[2], t3[3]);
+                unsigned char *W = sm + (to ^ (k << 4));
+                *reinterpret_cast<uint4 *>(W) = make_uint4(t1[0], t1[1], t1[2], t1[3]);
+                *reinterpret_cast<uint4 *>(W + TERM) = make_uint4(t2[0], t2[1], t2[2], t2[3]);
+                *reinterpret_cast<uint4 *>(W + 2 * TERM) = make_uint4(t3[0], t3[1], t3[2], t3[3]);
             }
             if (!in) {   // past the row's end: whatever stands there must not reach a product
                 const uint4 z = make_uint4(0, 0, 0, 0);
 #pragma unroll 1
-                for (int k = 0; k < 8; ++k) {
-                    *reinterpret_cast<uint4 *>(V + s * 128 + 16 * k) = z;
-                    *reinterpret_cast<uint4 *>(sm + OFF_K + st * Q_BYTES + s * 128 + 16 * k) = z;
-                    if (two) *reinterpret_cast<uint4 *>(sm + OFF_K + st * Q_BYTES + HALF + s * 128 + 16 * k) = z;
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t at = s * 128 + 64 * wh + 16 * k;
+                    *reinterpret_cast<uint4 *>(V + at) = z;
+                    *reinterpret_cast<uint4 *>(sm + OFF_K + st * Q_BYTES + at) = z;
+                    if (two) *reinterpret_cast<uint4 *>(sm + OFF_K + st * Q_BYTES + HALF + at) = z;
                 }
             }
             fence_proxy_async_smem();
@@ -882,35 +901,21 @@ __global__ void __launch_bounds__(ht::THREADS, 1)
     } else if (warp >= OUT) {   // --------------------------------------- output
         // row 32 (warp & 3) + lane of the chunk, value columns 32 oh ..
         const int row = 32 * (warp & 3) + lane, oh = (warp - OUT) >> 2, odd = lane & 1;
-        const uint32_t O = tmem + T_O + 32 * oh + (uint32_t((warp & 3) * 32) << 16);
         const int i0 = vt * RB + 32 * oh;
         const size_t HV = size_t(a.H) * dv;
         bf *ob = static_cast<bf *>(a.o) + (size_t(b) * a.L + s0) * HV + size_t(h) * dv + i0;
-        const bf *zb = nullptr;
-        if (!PARTS && a.hd.z != nullptr)
-            zb = static_cast<const bf *>(a.hd.z) + (size_t(b) * a.L + s0) * a.hd.ldz + size_t(h) * dv + i0;
         gates_wait();
         const float *src = a.hd.readout + g0 + row;
         float next = n_chunks > 0 ? __ldcg(src) : 0.0f;
         float2 zero = make_float2(0.0f, 0.0f);
+        const uint32_t zat = OFF_Z + sw128_offset(row, 32 * oh);   // this thread's part of the gate's tile
         for (int c = 0; c < n_chunks; ++c) {
             const int st = c & 1;
+            const uint32_t O = tmem + T_O + st * 64 + 32 * oh + (uint32_t((warp & 3) * 32) << 16);
             float u = next;
             if (c + 1 < n_chunks) next = __ldcg(src + (c + 1) * C);
             const int t = c * C + row;
             const bool valid = t < nrun;
-            // the gate, on its way while the products finish: lanes 2 g and 2 g + 1 take 16
-            // bytes each of row 2 g and of row 2 g + 1, for either half of the columns
-            uint4 z[2][2];
-#pragma unroll
-            for (int q = 0; q < 2; ++q)
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int tr = t - odd + i;
-                    z[q][i] = make_uint4(0, 0, 0, 0);
-                    if (!PARTS && zb != nullptr && tr < nrun && i0 + 16 * q + 8 * odd < dv)
-                        z[q][i] = *reinterpret_cast<const uint4 *>(zb + size_t(tr) * a.hd.ldz + 16 * q + 8 * odd);
-                }
             if (__float_as_int(u) < 0) {   // steep: rows of Q S^T by 2^(base + L) before PD V is added
                 if (!__all_sync(0xffffffffu, hw(OX_DONE + st, c >> 1))) break;
                 tc_fence_after();
@@ -930,35 +935,20 @@ __global__ void __launch_bounds__(ht::THREADS, 1)
                 if (lane == 0) arrive(&bar[FIX]);
                 u = 1.0f;
             }
-            if (!__all_sync(0xffffffffu, hw(O_DONE + st, c >> 1))) break;
+            bool there = hw(O_DONE + st, c >> 1);
+            if (GATE && there) there = hw(FULL_Z, c);
+            if (!__all_sync(0xffffffffu, there)) break;
             tc_fence_after();
-            // out of the accumulator into those columns of P's that PD leaves free, so that the
-            // next chunk's Q S^T can start
-            const uint32_t Y = tmem + T_P + st * 128 + 32 + 64 * oh + (uint32_t((warp & 3) * 32) << 16);
-#pragma unroll 1
-            for (int q = 0; q < 32; q += 16) {
-                float d[16];
-                tmem_ld16_nowait(O + q, d);
-                tmem_ld_wait_tied(d);
-                uint32_t w[16];
-#pragma unroll
-                for (int r = 0; r < 16; ++r) w[r] = __float_as_uint(d[r]);
-                tmem_st16_nowait(Y + q, w);
-            }
-            tmem_st_wait();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) arrive(&bar[K_DONE + st]);
             const float2 u2 = make_float2(u, u);
-#pragma unroll 1
+#pragma unroll
             for (int q = 0; q < 2; ++q) {
                 float d[16];
-                tmem_ld16_nowait(Y + 16 * q, d);
+                tmem_ld16_nowait(O + 16 * q, d);
                 tmem_ld_wait_tied(d);
-                if (q == 1) {   // P's columns are free; the rest of the outputs is off every chain
+                if (q == 1) {   // the accumulator is free
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) arrive(&bar[Y_DONE + st]);
+                    if (lane == 0) arrive(&bar[K_DONE + st]);
                 }
                 const int col = i0 + 16 * q;
                 if (PARTS) {   // steps past the row's end are the sum's to clear
@@ -972,10 +962,13 @@ __global__ void __launch_bounds__(ht::THREADS, 1)
                     continue;
                 }
                 uint32_t w[8];
-                if (zb != nullptr) {   // this thread's row: its own 16 bytes and the partner's
-                    const uint4 z0 = z[0][0], z1 = z[0][1];
-                    const uint4 mine = odd ? z1 : z0, give = odd ? z0 : z1;
-                    const uint4 got = xor1(give), lo = odd ? got : mine, hi = odd ? mine : got;
+                if constexpr (GATE) {
+                    const uint4 lo = *reinterpret_cast<const uint4 *>(sm + (zat ^ (32 * q)));
+                    const uint4 hi = *reinterpret_cast<const uint4 *>(sm + (zat ^ (32 * q + 16)));
+                    if (q == 1) {   // the tile is free
+                        __syncwarp();
+                        if (lane == 0) arrive(&bar[EMPTY_Z]);
+                    }
                     const uint32_t zw[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
 #pragma unroll
                     for (int r = 0; r < 8; ++r) {
@@ -984,7 +977,6 @@ __global__ void __launch_bounds__(ht::THREADS, 1)
                         y = __fmul2_rn(y, silu2_f(make_float2(lo_f(zw[r]), hi_f(zw[r]))));
                         w[r] = pack(y.x, y.y);
                     }
-                    z[0][0] = z[1][0], z[0][1] = z[1][1];
                 } else {
 #pragma unroll
                     for (int r = 0; r < 8; ++r) {
@@ -1058,26 +1050,22 @@ __global__ void __launch_bounds__(ht::THREADS, 1)
             __syncwarp();
             if (lane == 0) arrive(&bar[SB_READY]);
             if (steep) scale_state();
-            if (!__all_sync(0xffffffffu, hw(DS_DONE, c))) break;
+            if (!__all_sync(0xffffffffu, hw(DS_DONE + st, c >> 1))) break;
             tc_fence_after();
 #pragma unroll
-            for (int q = 0; q < 32; q += 8) {   // small terms first
-                float d1[8], d2[8], d3[8];
-                tmem_ld8_nowait(D + q, d1);
-                tmem_ld8_nowait(D + 64 + q, d2);
-                tmem_ld8_nowait(D + 128 + q, d3);
-                tmem_ld_wait_tied(d1, d2, d3);
+            for (int q = 0; q < 32; q += 16) {
+                float d[16];
+                tmem_ld16_nowait(D + st * 64 + q, d);
+                tmem_ld_wait_tied(d);
 #pragma unroll
-                for (int e = 0; e < 8; e += 2) {
-                    const float2 y = __fadd2_rn(make_float2(d1[e], d1[e + 1]),
-                                                __fadd2_rn(make_float2(d2[e], d2[e + 1]), make_float2(d3[e], d3[e + 1])));
-                    const float2 z = __fadd2_rn(make_float2(S[q + e], S[q + e + 1]), y);
+                for (int e = 0; e < 16; e += 2) {
+                    const float2 z = __fadd2_rn(make_float2(S[q + e], S[q + e + 1]), make_float2(d[e], d[e + 1]));
                     S[q + e] = z.x, S[q + e + 1] = z.y;
                 }
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) arrive(&bar[DS_FREE]);
+            if (lane == 0) arrive(&bar[DS_FREE + st]);
         }
         float *out = seg == a.n_seg - 1 && a.S_final != nullptr ? a.S_final + size_t(bh) * dv * ldk + k0 : nullptr;
         if (out != nullptr && j < dk) {
@@ -1123,17 +1111,20 @@ bool ht_setup() {
             return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes)) == cudaSuccess;
         };
         return room(heads_state_kernel<false>, hs::SMEM) && room(heads_state_kernel<true>, hs::SMEM) &&
-               room(heads_tensor_kernel<false>, ht::SMEM) && room(heads_tensor_kernel<true>, ht::SMEM);
+               room(heads_tensor_kernel<false, false>, ht::SMEM) && room(heads_tensor_kernel<false, true>, ht::SMEM) &&
+               room(heads_tensor_kernel<true, false>, ht::SMEM);
     });
 }
 
 }  // namespace
 
 int heads_tensor_launch(const DecayArgs &a, StatusRef st, cudaStream_t stream) {
-    CUtensorMap mq, mk, mv;
+    CUtensorMap mq, mk, mv, mz;
     if (!dt_map(&mq, a.q, a.dk, a.Hk, a.L, a.B, a.hd.ldq) || !dt_map(&mk, a.k, a.dk, a.Hk, a.L, a.B, a.hd.ldk) ||
         !dt_map(&mv, a.v, a.dv, a.H, a.L, a.B, a.hd.ldv) || !ht_setup())
         return LR_ERR_CUDA;
+    mz = mv;   // (not read without a gate)
+    if (a.hd.z != nullptr && !dt_map(&mz, a.hd.z, a.dv, a.H, a.L, a.B, a.hd.ldz)) return LR_ERR_CUDA;
     const int n_vt = (a.dv + ht::RB - 1) / ht::RB;
     const bool parts = a.parts > 1;
     const int64_t per_seg = a.B * a.H * n_vt * a.parts;
@@ -1146,8 +1137,11 @@ int heads_tensor_launch(const DecayArgs &a, StatusRef st, cudaStream_t stream) {
                            dim3(unsigned(per_seg * (a.n_seg - 1))), hs::THREADS, hs::SMEM, stream, mk, mv, a, n_vt,
                            kDefaultTimeoutNs, st);
     if (rc == LR_OK)
-        rc = launch_kernel(parts ? heads_tensor_kernel<true> : heads_tensor_kernel<false>, true,
-                           dim3(unsigned(per_seg * a.n_seg)), ht::THREADS, ht::SMEM, stream, mq, mk, mv, a, n_vt,
+        rc = launch_kernel(parts                 ? heads_tensor_kernel<true, false>
+                           : a.hd.z != nullptr ? heads_tensor_kernel<false, true>
+                                                 : heads_tensor_kernel<false, false>,
+                           true,
+                           dim3(unsigned(per_seg * a.n_seg)), ht::THREADS, ht::SMEM, stream, mq, mk, mv, mz, a, n_vt,
                            kDefaultTimeoutNs, st);
     if (rc != LR_OK || !parts) return rc;
     const int64_t rows = a.B * a.L;
