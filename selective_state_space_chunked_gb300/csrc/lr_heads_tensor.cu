@@ -52,7 +52,12 @@ using dt::three_terms;
 using dt::wait_slow;
 constexpr int C = kDecayChunk;
 constexpr int RB = kDecayRows;
-constexpr int OUT = 8, FRONT = 16, WEIGHT = 24, TMA_WARP = 28, DS_WARP = 29, P_WARP = 30;   // 31: O
+// State warps 0 .. 7, output 8 .. 15, then front and weight.  A warp reaches the TMEM rows of
+// its number modulo 4, which is also the scheduler that it runs on, and rows 32 w .. of P
+// have 2 w + 2 blocks of columns under the diagonal: one front warp for the first rows,
+// two, two and three for the others, and the weight warps where there are fewer of them.
+constexpr int OUT = 8, FRONT = 16, TMA_WARP = 28, DS_WARP = 29, P_WARP = 30;   // 31: O
+__device__ __forceinline__ bool is_weight(int warp) { return warp == 20 || (warp >= 24 && warp < 27); }
 constexpr int THREADS = 32 * 32;
 
 // What the gates' launch leaves of a chunk.
@@ -70,12 +75,18 @@ static_assert(sizeof(Chunk) == kChunkRecord, "");
 constexpr uint32_t HALF = C * 128;              // 64 columns of Q or K: 128 rows of 128 bytes
 constexpr uint32_t Q_BYTES = 2 * HALF, V_BYTES = C * RB * 2;
 constexpr uint32_t OFF_Q = 0, OFF_K = 2 * Q_BYTES, OFF_V = 4 * Q_BYTES;
-// The state's weighted values, three terms of [4 quarters][16 s][64 i]: half of a quarter's
-// steps at a time, which leaves the room for the gate's tile.
-constexpr uint32_t OFF_W = OFF_V + 2 * V_BYTES, TERM = V_BYTES / 2;
-constexpr uint32_t OFF_SB = OFF_W + 3 * TERM;       // bf16 state [128 j][64 i]
-constexpr uint32_t OFF_Z = OFF_SB + 128 * RB * 2;   // the gate [128 s][64 i]
-constexpr uint32_t OFF_G = OFF_Z + V_BYTES;         // 2 x Chunk
+constexpr uint32_t OFF_SB = OFF_V + 2 * V_BYTES;    // bf16 state [128 j][64 i]
+// The state's weighted values, three terms of [4 quarters][32 s][64 i].  With a gate half of a
+// quarter's steps at a time, and its tile [128 s][64 i] in the room that this leaves (without
+// a gate that costs 90 -> 103 us at B4 L4096 H16 P128 N128).
+template <bool GATE>
+struct Weights {
+    static constexpr int HALVES = GATE ? 2 : 1, STEPS = 32 / HALVES, GROUPS = 8 / HALVES;
+    static constexpr uint32_t TERM = 4 * STEPS * RB * 2;
+};
+constexpr uint32_t OFF_W = OFF_SB + 128 * RB * 2, OFF_Z = OFF_W + 3 * Weights<true>::TERM;
+constexpr uint32_t OFF_G = OFF_W + 3 * Weights<false>::TERM;   // 2 x Chunk
+static_assert(OFF_Z + V_BYTES <= OFF_G, "the gate's tile");
 constexpr uint32_t OFF_BAR = OFF_G + 2 * kChunkRecord;
 // barriers; [2] by chunk parity, [4] by quarter
 enum {
@@ -86,7 +97,7 @@ enum {
     K_DONE = 18,     // chunk c's accumulator read (8 output warps)
     OX_DONE = 20,    // Q S^T complete: the bf16 state has been read
     O_DONE = 22,
-    W_READY = 24,    // weighted values of half a quarter, twice a chunk
+    W_READY = 24,    // weighted values of a quarter, or of half of it, twice a chunk
     W_FREE = 28,
     DS_DONE = 32, DS_FREE = 34,   // [2]
     FULL_Z = 36, EMPTY_Z,
@@ -537,6 +548,7 @@ __global__ void __launch_bounds__(ht::THREADS, 1)
                         const __grid_constant__ DecayArgs a, int n_vt, uint64_t timeout_ns, StatusRef sref) {
     using namespace ht;
     using bf = __nv_bfloat16;
+    using Wt = Weights<GATE>;
     extern __shared__ __align__(1024) unsigned char sm[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int nseg = a.n_seg;
@@ -681,19 +693,22 @@ __global__ void __launch_bounds__(ht::THREADS, 1)
                 const uint64_t dK = umma_smem_desc(base + OFF_K + st * Q_BYTES, HALF, 1024);
                 bool ok = true;
 #pragma unroll 1
-                for (int e = 0; e < 8; ++e) {   // the quarters' first halves, then their second ones
+                for (int e = 0; e < 4 * Wt::HALVES; ++e) {   // quarters, or their first halves, then their second ones
                     const int qt = e & 3, hf = e >> 2;
-                    ok = ok && hu(W_READY + qt, 2 * c + hf);
+                    ok = ok && hu(W_READY + qt, Wt::HALVES * c + hf);
                     if (!ok) break;
                     tc_fence_after();
                     if (lead) {   // 16 steps are 2048 bytes on, 128 in the descriptors' units
                         // the three terms onto one accumulator, small ones first
 #pragma unroll
-                        for (int term = 2; term >= 0; --term)
-                            umma_bf16(tmem + T_DS + st * 64, dK + 256 * qt + 128 * hf, dW + (TERM >> 4) * term + 128 * qt,
-                                      IDESC_DS, e > 0 || term < 2);
+                        for (int kk = 0; kk < Wt::STEPS / 16; ++kk)
+#pragma unroll
+                            for (int term = 2; term >= 0; --term)
+                                umma_bf16(tmem + T_DS + st * 64, dK + 256 * qt + 128 * (hf + kk),
+                                          dW + (Wt::TERM >> 4) * term + 8 * Wt::STEPS * qt + 128 * kk, IDESC_DS,
+                                          e > 0 || kk > 0 || term < 2);
                         umma_commit(&bar[W_FREE + qt]);
-                        if (e == 7) {
+                        if (e == 4 * Wt::HALVES - 1) {
                             umma_commit(&bar[DS_DONE + st]);
                             umma_commit(&bar[EMPTY_K + st]);
                             umma_commit(&bar[EMPTY_V + st]);
@@ -751,7 +766,7 @@ __global__ void __launch_bounds__(ht::THREADS, 1)
                 if (lead) {   // onto Q S^T: same shape and accumulator, so in order
 #pragma unroll 1
                     for (int kk = 0; kk < C / 16; ++kk)
-                        umma_bf16_ts(tmem + T_O + st * 64, tmem + T_P + st * 128 + (kk >> 2) * 64 + (kk & 3) * 8, dV + 128 * kk,
+                        umma_bf16_ts(tmem + T_O + st * 64, tmem + T_P + st * 128 + 16 * kk, dV + 128 * kk,
                                      IDESC_O, 1);
                     umma_commit(&bar[O_DONE + st]);
                     umma_commit(&bar[EMPTY_V + st]);
@@ -765,25 +780,25 @@ __global__ void __launch_bounds__(ht::THREADS, 1)
             mbar_wait_bounded(&bar[MMA_END], 0, timeout_ns);
         }
         __syncwarp();
-    } else if (warp >= WEIGHT) {   // ----------------------------------- weight
-        // lanes i and i + 16: step i of half a quarter, 32 value columns each
-        const int qt = warp - WEIGHT, i = lane & 15, wh = lane >> 4, r = 16 * qt + i;
+    } else if (is_weight(warp)) {   // ---------------------------------- weight
+        // lane: a step of the quarter; or, i and i + 16, step i of half of it, 32 value columns each
+        const int qt = warp == 20 ? 0 : warp - 23, i = lane % Wt::STEPS, wh = lane / Wt::STEPS, r = Wt::STEPS * qt + i;
         gates_wait();
         const float *src = a.hd.weight + g0 + 32 * qt + i;
         float wn = n_chunks > 0 ? __ldcg(src) : 0.0f;
-        for (int c2 = 0; c2 < 2 * n_chunks; ++c2) {
-            const int c = c2 >> 1, st = c & 1, s = 32 * qt + 16 * (c2 & 1) + i;   // s: of the chunk
+        for (int p = 0; p < Wt::HALVES * n_chunks; ++p) {
+            const int c = p / Wt::HALVES, hf = p % Wt::HALVES, st = c & 1, s = 32 * qt + 16 * hf + i;   // s: of the chunk
             unsigned char *V = sm + OFF_V + st * V_BYTES;
             const bool in = c * C + s < nrun;
             const float w = wn;
-            if (c2 + 1 < 2 * n_chunks) wn = __ldcg(src + (c2 + 1 >> 1) * C + 16 * (c2 + 1 & 1));
+            if (p + 1 < Wt::HALVES * n_chunks) wn = __ldcg(src + (p + 1) / Wt::HALVES * C + 16 * ((p + 1) % Wt::HALVES));
             bool ok = hw(FULL_V + st, c >> 1);
             if (ok && c * C + C > nrun) ok = hw(FULL_K + st, c >> 1);
-            if (ok && c2 >= 1) ok = hw(W_FREE + qt, c2 - 1);
+            if (ok && p >= 1) ok = hw(W_FREE + qt, p - 1);
             if (!__all_sync(0xffffffffu, ok)) break;
             const uint32_t from = sw128_offset(s, 32 * wh), to = OFF_W + sw128_offset(r, 32 * wh);
 #pragma unroll 1
-            for (int k = 0; k < 4; ++k) {   // groups of 8 columns
+            for (int k = 0; k < Wt::GROUPS; ++k) {   // 8 columns
                 uint4 u = *reinterpret_cast<const uint4 *>(V + (from ^ (k << 4)));
                 if (!in) u = make_uint4(0, 0, 0, 0);
                 const uint32_t uv[4] = {u.x, u.y, u.z, u.w};
@@ -792,13 +807,13 @@ __global__ void __launch_bounds__(ht::THREADS, 1)
                 for (int e = 0; e < 4; ++e) three_terms(w, uv[e], t1[e], t2[e], t3[e]);
                 unsigned char *W = sm + (to ^ (k << 4));
                 *reinterpret_cast<uint4 *>(W) = make_uint4(t1[0], t1[1], t1[2], t1[3]);
-                *reinterpret_cast<uint4 *>(W + TERM) = make_uint4(t2[0], t2[1], t2[2], t2[3]);
-                *reinterpret_cast<uint4 *>(W + 2 * TERM) = make_uint4(t3[0], t3[1], t3[2], t3[3]);
+                *reinterpret_cast<uint4 *>(W + Wt::TERM) = make_uint4(t2[0], t2[1], t2[2], t2[3]);
+                *reinterpret_cast<uint4 *>(W + 2 * Wt::TERM) = make_uint4(t3[0], t3[1], t3[2], t3[3]);
             }
             if (!in) {   // past the row's end: whatever stands there must not reach a product
                 const uint4 z = make_uint4(0, 0, 0, 0);
 #pragma unroll 1
-                for (int k = 0; k < 4; ++k) {
+                for (int k = 0; k < Wt::GROUPS; ++k) {
                     const uint32_t at = s * 128 + 64 * wh + 16 * k;
                     *reinterpret_cast<uint4 *>(V + at) = z;
                     *reinterpret_cast<uint4 *>(sm + OFF_K + st * Q_BYTES + at) = z;
@@ -810,9 +825,12 @@ __global__ void __launch_bounds__(ht::THREADS, 1)
             if (lane == 0) arrive(&bar[W_READY + qt]);
         }
     } else if (warp >= FRONT) {   // ------------------------------------- front
-        // rows 32 fw .. of P, columns 64 hf .. in blocks of 16; PD's go to the
-        // first half of the same columns, which the warp has read by then
-        const int fw = warp & 3, hf = (warp - FRONT) >> 2, t = 32 * fw + lane;
+        // Rows 32 fw .. of P, blocks of 16 columns first .. end of those that some row sees; the
+        // others are cleared.  A block's PD goes to the first half of its own columns.
+        const int fw = warp & 3, k = warp == 27 ? 2 : (warp - FRONT) >> 2, t = 32 * fw + lane;
+        const int seen = 2 * fw + 2, sharers = fw == 0 ? 1 : fw == 3 ? 3 : 2, each = (seen + sharers - 1) / sharers;
+        const int first = k * each, end = min(seen, first + each);
+        const int clear = (8 - seen) / sharers, clear0 = seen + k * clear;   // (evenly shared)
         const bool has_skip = a.hd.skip != nullptr && part == 0;
         const float skip = has_skip ? a.hd.skip[h] : 0.0f;
         gates_wait();
@@ -820,7 +838,7 @@ __global__ void __launch_bounds__(ht::THREADS, 1)
         float2 next = n_chunks > 0 ? __ldcg(src) : make_float2(0.0f, 0.0f);
         for (int c = 0; c < n_chunks; ++c) {
             const int st = c & 1;
-            const uint32_t P = tmem + T_P + st * 128 + 64 * hf + (uint32_t(fw * 32) << 16);
+            const uint32_t P = tmem + T_P + st * 128 + (uint32_t(fw * 32) << 16);
             const float2 own = next;
             if (c + 1 < n_chunks) next = __ldcg(src + (c + 1) * C);
             const bool ok = hw(FULL_G + st, c >> 1) && hw(P_READY + st, c >> 1);
@@ -828,19 +846,18 @@ __global__ void __launch_bounds__(ht::THREADS, 1)
             tc_fence_after();
             const bool cut = nrun - c * C < C;
             const bool steep = rec[st].steep != 0;
-            const float *f = rec[st].col + 64 * hf;
+            const float *f = rec[st].col;
             const int lt = __float_as_int(own.y);               // steep
             const float dg = skip * (steep ? 1.0f : own.x);
 #pragma unroll 1
-            for (int kb = 0; kb < 4; ++kb) {
-                const int b0 = 64 * hf + 16 * kb;   // the block's first column
+            for (int kb = clear0; kb < clear0 + clear; ++kb) {
+                const uint32_t r[8] = {};
+                tmem_st8_nowait(P + 16 * kb, r);
+            }
+#pragma unroll 1
+            for (int kb = first; kb < end; ++kb) {
+                const int b0 = 16 * kb;   // the block's first column
                 uint32_t r[8];
-                if (b0 > 32 * fw + 31) {   // no row of the warp sees the block
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) r[e] = 0;
-                    tmem_st8_nowait(P + 8 * kb, r);
-                    continue;
-                }
                 const bool diag = b0 + 15 > 32 * fw;   // it holds some row's diagonal
                 float p[16];
                 tmem_ld16_nowait(P + 16 * kb, p);
@@ -859,7 +876,7 @@ __global__ void __launch_bounds__(ht::THREADS, 1)
                     const float rf = steep ? ex2_approx(dec::units_f(lt - rec[st].last[b0 >> 4])) : 1.0f;
                     float4 w4[4];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) w4[e] = *reinterpret_cast<const float4 *>(f + 16 * kb + 4 * e);
+                    for (int e = 0; e < 4; ++e) w4[e] = *reinterpret_cast<const float4 *>(f + b0 + 4 * e);
                     tmem_ld_wait_tied(p);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
@@ -891,7 +908,7 @@ __global__ void __launch_bounds__(ht::THREADS, 1)
 #pragma unroll
                     for (int e = 0; e < 8; ++e) r[e] &= 2 * e + 1 < m ? 0xffffffffu : 2 * e < m ? 0xffffu : 0u;
                 }
-                tmem_st8_nowait(P + 8 * kb, r);
+                tmem_st8_nowait(P + b0, r);
             }
             tmem_st_wait();
             tc_fence_before();
