@@ -459,8 +459,8 @@ typedef enum { LR_PAIRS_HALVES = 0, LR_PAIRS_NEIGHBOURS = 1 } lr_pairs;
  * Optional: gamma_q, gamma_k (1); k and k_out (Hk == 0).  q_out may be q where ldq ==
  *          H*d, k_out k alike; other outputs must not overlap inputs.
  * Requirements: N, Hk >= 0, H, d >= 1, 0 <= rot <= d, rot even, ldq >= H*d, ldk >= Hk*d,
- *          eps >= 0 and finite (else LR_ERR_INVALID_ARG); d <= 512 (else
- *          LR_ERR_UNSUPPORTED); freqs finite, below 2^20 in size.  No workspace.
+ *          eps >= 0 and finite (else LR_ERR_INVALID_ARG); d <= 512, at most half a million
+ *          heads (else LR_ERR_UNSUPPORTED); freqs finite, below 2^20 in size.  No workspace.
  */
 int lr_head_norm_rope(const void *q, int64_t ldq, const void *k, int64_t ldk,
                       const float *gamma_q, const float *gamma_k, const float *freqs,

@@ -648,7 +648,8 @@ int validate_conv(const void *x, int64_t ldx, const float *w, const float *bias,
     if (B < 0 || L < 0 || C < 0 || W < 2 || ldx < C || !io_ok(io) || (act != LR_ACT_NONE && act != LR_ACT_SILU))
         return LR_ERR_INVALID_ARG;
     if (B > 0 && C > 0 && L > 0 && (!x || !w || !y)) return LR_ERR_INVALID_ARG;
-    if (W > 4 || !fits_int(B) || !fits_int(L) || !fits_int(C)) return LR_ERR_UNSUPPORTED;
+    // (the kernel looks up to 64 steps past a row's end)
+    if (W > 4 || !fits_int(B) || !fits_int(L + 64) || !fits_int(C)) return LR_ERR_UNSUPPORTED;
     const void *ptrs[] = {x, w, bias, state, lens, y, state_out};
     for (const void *p : ptrs)
         if (misaligned(p)) return LR_ERR_MISALIGNED;
@@ -691,7 +692,7 @@ extern "C" int lr_head_norm_rope(const void *q, int64_t ldq, const void *k, int6
         !std::isfinite(eps) || eps < 0.0f || norm < LR_NORM_NONE || norm > LR_NORM_L2 || pairs < LR_PAIRS_HALVES ||
         pairs > LR_PAIRS_NEIGHBOURS)
         return LR_ERR_INVALID_ARG;
-    if (d > 512 || !fits_int(N) || !fits_int(H) || !fits_int(Hk) || !fits_int((H + Hk) * d)) return LR_ERR_UNSUPPORTED;
+    if (d > 512 || !fits_int(N) || H > 500000 || Hk > 500000 || H + Hk > 500000) return LR_ERR_UNSUPPORTED;
     if (ldq < H * d || ldk < Hk * d) return LR_ERR_INVALID_ARG;
     if (N > 0 && (!q || !q_out || (Hk > 0 && (!k || !k_out)) || (rot > 0 && (!freqs || !pos))))
         return LR_ERR_INVALID_ARG;

@@ -95,7 +95,7 @@ __global__ void __launch_bounds__(kRopeT) rope_kernel(const RopeArgs a) {
     grid_dependency_wait();
     const int l = threadIdx.x % TL;
     // a block takes whole tokens, or of one that has more sets than it a part
-    int first = blockIdx.y * (blockDim.x / TL) + threadIdx.x / TL;
+    int first = int(blockIdx.y * (blockDim.x / TL) + threadIdx.x / TL);
     const int token = first / a.sets;
     first -= token * a.sets;
     const int64_t n0 = int64_t(blockIdx.x) * a.tokens, n = n0 + token;
@@ -235,17 +235,17 @@ int rope_go(RopeArgs a, cudaStream_t s) {
     a.sets = int(sets(a.heads));
     a.q_sets = (a.H + a.heads - 1) / a.heads;
     // tokens of a block: whole warps with the fewest idle lanes, of about 128 threads
-    auto threads = [&](int t) { return (t * a.sets * TL + 31) / 32 * 32; };
+    auto threads = [&](int64_t t) { return (t * a.sets * TL + 31) / 32 * 32; };
     a.tokens = 1;
-    int block = threads(1) < kRopeT ? threads(1) : kRopeT;
+    int block = int(threads(1) < kRopeT ? threads(1) : kRopeT);
     double best = 0.0;
     for (int t = 1; t == 1 || threads(t) <= kRopeT; ++t) {
-        const double used = double(t * a.sets * TL) / threads(t) + (threads(t) >= 128 ? 0.1 : 0.0);
-        if (threads(t) <= kRopeT && used > best) best = used, a.tokens = t, block = threads(t);
+        const double used = double(int64_t(t) * a.sets * TL) / double(threads(t)) + (threads(t) >= 128 ? 0.1 : 0.0);
+        if (threads(t) <= kRopeT && used > best) best = used, a.tokens = t, block = int(threads(t));
         if (threads(t) >= 128 && best >= 1.1) break;
     }
-    const dim3 grid(unsigned((a.N + a.tokens - 1) / a.tokens), unsigned((a.sets * TL * a.tokens + block - 1) / block));
-    if (grid.y > 65535) return LR_ERR_UNSUPPORTED;
+    const int64_t parts = (int64_t(a.sets) * TL * a.tokens + block - 1) / block;   // (500000 heads: 62500)
+    const dim3 grid(unsigned((a.N + a.tokens - 1) / a.tokens), unsigned(parts));
     // a head a set: without the registers of the others (decode: 2.6 us against 2.9)
     return launch_kernel(a.heads == 1 ? rope_kernel<X, TL, U, 1, NB> : rope_kernel<X, TL, U, NH, NB>, true,
                          grid, block, size_t(a.tokens) * (a.rot / 2) * sizeof(float2), s, a);

@@ -84,6 +84,9 @@ def test_ragged_rows(lr, io, C, W):  # noqa: F811
     for b, n in enumerate(lens):
         assert torch.all(y[b, max(n, 0):] == 0)
     assert torch.equal(new[0], p["state"][0])
+    S = p["state"].clone()   # in place: rows shorter than the taps keep inputs of the old state
+    _, same = lr.causal_conv(**dict(p, state=S), lens=torch.tensor(lens).cuda(), out=(torch.empty_like(y), S))
+    assert same is S and torch.equal(S, new)
 
 
 @pytest.mark.parametrize("io", ["f32", "bf16"])

@@ -13,7 +13,7 @@ CONV_BAD = [(dict(x=None), -1), (dict(w=None), -1), (dict(y=None), -1), (dict(B=
             (dict(bias=FAKE + 4), -3), (dict(y=FAKE + 2), -3)]
 
 
-@pytest.mark.parametrize("kw,code", CONV_BAD + [(dict(L=-1), -1), (dict(L=1 << 40), -2), (dict(lens=FAKE + 4), -3),
+@pytest.mark.parametrize("kw,code", CONV_BAD + [(dict(L=-1), -1), (dict(L=1 << 40), -2), (dict(L=2 ** 31 - 60), -2), (dict(lens=FAKE + 4), -3),
                                                 (dict(state=FAKE + 2), -3), (dict(state_out=FAKE + 2), -3)])
 def test_convolution(lr, kw, code):  # noqa: F811
     a = dict(x=FAKE, ldx=64, w=FAKE, bias=FAKE, state=FAKE, lens=FAKE, y=FAKE, state_out=FAKE, B=2, L=9, C=64, W=4,
@@ -35,7 +35,7 @@ def test_convolution_step(lr, kw, code):  # noqa: F811
     (dict(pos=None), -1), (dict(N=-1), -1), (dict(H=0), -1), (dict(Hk=-1), -1), (dict(d=0), -1), (dict(rot=-2), -1),
     (dict(rot=66), -1), (dict(rot=3), -1), (dict(ldq=255), -1), (dict(ldk=127), -1), (dict(norm=3), -1),
     (dict(norm=-1), -1), (dict(pairs=2), -1), (dict(eps=-1.0), -1), (dict(eps=float("nan")), -1), (dict(io=2), -1),
-    (dict(d=513, rot=0), -2), (dict(N=1 << 33), -2), (dict(H=1 << 33), -2), (dict(q=FAKE + 8), -3),
+    (dict(d=513, rot=0), -2), (dict(N=1 << 33), -2), (dict(H=1 << 33), -2), (dict(H=1 << 24, ldq=1 << 30), -2), (dict(q=FAKE + 8), -3),
     (dict(k=FAKE + 8), -3), (dict(gamma_q=FAKE + 4), -3), (dict(freqs=FAKE + 4), -3), (dict(pos=FAKE + 4), -3),
     (dict(k_out=FAKE + 8), -3)])
 def test_norm_and_rotation(lr, kw, code):  # noqa: F811

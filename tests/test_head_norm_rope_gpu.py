@@ -46,7 +46,9 @@ def check(got, p, io, norm="rms", pairs="halves", eps=1e-6, tol=None):
     (1, 1, 16, 16), (4, 2, 32, 32), (3, 1, 64, 64), (16, 4, 128, 128), (2, 2, 128, 64), (6, 3, 80, 80), (2, 1, 96, 32),
     (2, 2, 192, 192), (1, 1, 256, 256), (1, 1, 512, 512), (2, 1, 512, 128), (3, 2, 40, 20), (1, 1, 8, 8), (2, 2, 24, 2),
     (3, 3, 33, 32), (5, 1, 7, 4), (2, 1, 1, 0), (2, 1, 2, 2), (1, 1, 511, 510), (1, 1, 300, 250), (4, 0, 64, 64),
-    (2, 2, 64, 0), (1, 1, 130, 130)])
+    (2, 2, 64, 0), (1, 1, 130, 130),
+    # more heads than a block has lanes for
+    (100, 20, 128, 128), (70, 9, 64, 32), (3000, 3000, 2, 2), (33, 0, 256, 128)])
 def test_head_layouts(lr, io, pairs, H, Hk, d, rot):  # noqa: F811
     p = inputs((2, 5), H, Hk, d, rot, io, seed=d + rot)
     check(lr.head_norm_rope(**p, pairs=pairs), p, io, pairs=pairs)

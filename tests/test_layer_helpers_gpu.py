@@ -25,7 +25,7 @@ def inputs(io, L=70, B=3, H=4, G=2, P=32, N=16, apart=0):
                 z=zdt[..., :H * P], dt=zdt[..., H * P:H * P + H], A=p["A_log"], skip=p["Dskip"], bias=p["dt_bias"], S=p["S0"],
                 w=(torch.rand(C, 4, generator=g) - 0.5).cuda(), b=torch.randn(C, generator=g).cuda(),
                 cs=torch.randn(B, 3, C, generator=g).to(xbc.dtype).cuda(), H=H, G=G,
-                lens=torch.tensor([L, 0, 33], dtype=torch.int32).cuda(), gamma=torch.randn(N, generator=g).cuda(),
+                lens=torch.tensor([L, 0, 33, 5][:B], dtype=torch.int32).cuda(), gamma=torch.randn(N, generator=g).cuda(),
                 freqs=(0.1 ** torch.arange(N // 2)).cuda(),
                 pos=torch.arange(L, dtype=torch.int32).expand(B, L).contiguous().cuda())
 
@@ -169,3 +169,53 @@ def test_together_as_a_layer(lr, io, tol, tol_s, L, n):  # noqa: F811
         assert rel_err(got[b, rows].float().cpu(), ref) <= tol
         assert rel_err(S[b].cpu(), Sr[0]) <= tol_s and rel_err(cs[b].float().cpu(), csr[0]) == 0.0
         assert not got[b, m:L].any()
+
+
+def layer(lr, d, L):  # noqa: F811
+    """The operators of a prompt in a row."""
+    HP, GN, G, H = d["x"].shape[-1], d["Bm"].shape[-1], d["G"], d["H"]
+    y, cs = lr.causal_conv(d["xbc"], d["w"], bias=d["b"])
+    Cm, Bm = lr.head_norm_rope(y[..., HP + GN:], y[..., HP:HP + GN], G, gamma_q=d["gamma"], freqs=d["freqs"], pos=d["pos"])
+    y, S = lr.selective_heads(y[..., :HP], d["dt"], Bm, Cm, d["A"], H, G=G, z=d["z"], Dskip=d["skip"], dt_bias=d["bias"])
+    return lr.group_norm_act(y, H), cs, S
+
+
+@pytest.mark.parametrize("L", [30, 300, 3000])
+def test_a_layer_captured_and_replayed_on_new_inputs(lr, L):  # noqa: F811
+    d = inputs("bf16", L=L, B=1, P=64, N=64)
+    s, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        layer(lr, d, L)
+        s.synchronize()
+        with torch.cuda.graph(graph, stream=s):
+            got = layer(lr, d, L)
+    for k in range(3):
+        gen = torch.Generator(device="cuda").manual_seed(k)
+        d["xbc"].normal_(generator=gen)
+        d["z"].normal_(generator=gen)
+        torch.cuda.synchronize()
+        want = [t.clone() for t in layer(lr, d, L)]
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+
+
+def test_two_streams_at_once(lr):  # noqa: F811
+    ds = [inputs("bf16", L=900, B=2 + i, P=64, N=64) for i in range(2)]
+    for d in ds:
+        d["xbc"].normal_(generator=torch.Generator(device="cuda").manual_seed(d["xbc"].shape[0]))
+    want = [layer(lr, d, 900) for d in ds]
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in ds], [[], []]
+    for _ in range(20):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(layer(lr, ds[i], 900))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for r in got[i]:
+            for a, b in zip(r, want[i]):
+                assert torch.equal(a, b)
