@@ -65,7 +65,7 @@ struct DecayPlan {
     int path = 0;            // 0: CUDA cores, 1: tensor cores
     int n_seg = 1;
     int64_t seg_len = 0;
-    bool narrow = false;     // CUDA cores: few columns per thread (short sequences)
+    int thread_rows = 4;     // CUDA cores: state rows per thread
     int parts = 1;
     int tiles = 1;           // blocks of one (batch row, head, segment)
     int64_t blocks = 0;      // of the (second) launch
@@ -88,7 +88,7 @@ constexpr int kDecayChunk = 128;    // its steps per chunk (segments are multipl
 constexpr int kDecayRows = 64;      // its value rows per block
 constexpr int kPartKeys = 128;      // its key columns per block
 // rows of the state per block of the general kernel
-int decay_general_rows(int64_t dk, bool narrow);
+int decay_general_rows(int64_t dk, int thread_rows);
 
 // One launch, and its own status: an error that an earlier call of the thread left
 // unread says nothing about it (a caller that is told of a failure may launch

@@ -11,16 +11,22 @@ namespace {
 // 1060, 4 726, 9 (chosen) 668, 14 681; B1 L32768: 9 1791, 19 (chosen) 1267, 24 1484;
 // few heads: B1 L8192 H1 d128 32 116, 64 (chosen) 73.5, 96 93; B1 L4096 H2 d64 32
 // 48.6, 41 (chosen) 48.6, 45 59, 64 50.
-// Calls in one segment whose narrow blocks (one state row a thread) are no more
-// than four per SM, with fp32 I/O and more than 64 keys three, take those.  L100 fp32:
-// d128 H4 20.2 us against 28.2, H16 21.0 against 28.5, H28 23.5 against 28.2, H32 32.8
-// against 28.2; d64 H16 15.0 against 20.1, H76 19.5 against 20.2; dk 256 H12 24.7
-// against 27.4, H16 44.0 against 27.5.  bf16 L32 d128: H4 8.0 against 11.0, H32 8.5
-// against 10.6.  (At dk 256, bf16 L32 24.2 against 12.1, and at dk 512, fp32 98
-// against 41, when the narrow form came in.)
+// Blocks with one or two state rows a thread, where four would leave the SMs with few
+// blocks.  A step's time in us, costs in steps; kWideUnit: the unit in us of the
+// four-row form's costs.  Fitted to sweeps of the rows and the segment count over 39
+// shapes; us with the four-row form's plan (and one row where a call had one segment and
+// few blocks), and with this: selective scan with heads, fp32, B2 L700 H12 P80 N96 93,
+// 50.5 (2 rows, 5 segments); B1 L300 H8 P64 N64 37, 13 (1, 6); B8 L500 H16 P64 N128
+// 193, 102 (2, 1); B8 L1017 H32 P64 N64 469, 260 (2, 1); B32 L100 H16 P64 N64 73, 66;
+// decayed attention, fp32, B1 L300 H8 d64 28, 12.5; B1 L8192 H1 d128 73.5, 62; B16
+// L512 H16 dk64 dv128 219, 219 (4, 1; two rows 193); bf16 B1 L40 H16 d128 9.5, 7.4.
+// Of 55 shapes none got more than 1 % slower.
 constexpr int64_t kGenMinSeg = 64;
 constexpr double kGenBlockCost = 40.0, kGenStateCost = 3.0, kGenLaunchCost = 50.0;
 constexpr int64_t kGenMaxSeg = 96;
+constexpr double kWideUnit = 0.115, kWideUnitNarrowKeys = 0.09;
+constexpr int64_t kFewMinSeg = 48;
+constexpr double kFewBlockCost = 15.0, kFewStateCost = 4.0, kFewLaunchTime = 3.0, kFewMargin = 1.05;
 // Tensor-core kernel: the shortest sequence it takes (bf16, on it and on the CUDA
 // cores: B1 L48 H4 d128 9.6 and 10.9 us, L32 9.7 and 8.1; B4 L48 H32 d64 10.8 and
 // 11.4; B1 H8 dk256, L48 12.0 and 15.2, L32 12.0 and 10.8; the other way, B8 L48 H16
@@ -52,7 +58,7 @@ int decay_plan(int64_t B, int64_t L, int64_t H, int64_t Hk, int64_t dk, int64_t 
     int sms = 0;
     if (device_sm_count(&sms) != LR_OK) return LR_ERR_CUDA;
     int64_t n = 1, unit = 16;
-    p->narrow = false;
+    p->thread_rows = 4;
     p->path = io == LR_BF16 && dk % 8 == 0 && dv % 8 == 0 && L >= kTensorMinLen;
     p->parts = p->path == 1 ? int((dk + kPartKeys - 1) / kPartKeys) : 1;
     if (p->path == 1) {
@@ -75,7 +81,7 @@ int decay_plan(int64_t B, int64_t L, int64_t H, int64_t Hk, int64_t dk, int64_t 
         // dependent launches packs three blocks as four), 2 where no SM has a
         // second block (a step then takes 0.243 us against 0.49 for four blocks),
         // and 1.5 for a block left over by the rounds, whose start overlaps them.
-        const int64_t rows = decay_general_rows(dk, false), threads = dk <= 64 ? 64 : 128, slots = dk <= 128 ? 4 : 3;
+        const int64_t rows = decay_general_rows(dk, 4), threads = dk <= 64 ? 64 : 128, slots = dk <= 128 ? 4 : 3;
         const int64_t blocks = B * H * ((dv + rows - 1) / rows);
         auto load = [&](int64_t b) {
             const int64_t most = (b * threads + 128 * sms - 1) / (128 * sms), rest = most % slots;
@@ -89,13 +95,34 @@ int decay_plan(int64_t B, int64_t L, int64_t H, int64_t Hk, int64_t dk, int64_t 
                              load(blocks * (s - 1)) * (0.5 * per + kGenBlockCost) + kGenLaunchCost;
             if (t < best) best = t, n = s;
         }
-        const int64_t nrows = decay_general_rows(dk, true);
-        const int64_t narrow_per_sm = io == LR_BF16 || dk <= 64 ? 4 : 3;
-        p->narrow = n == 1 && dk <= (io == LR_BF16 ? 128 : 256) && B * H * ((dv + nrows - 1) / nrows) <= narrow_per_sm * sms;
+        // fewer rows a thread: from the time of a step (us) with one block on the
+        // fullest SM to that with as many as it holds
+        struct Step {
+            double one, full;
+        };
+        static constexpr Step kSteps[3][2] = {{{0.07, 0.09}, {0.08, 0.125}},     // to 64 keys: one row, two
+                                              {{0.095, 0.175}, {0.154, 0.2}},    // to 128
+                                              {{0.1, 0.2}, {0.15, 0.24}}};       // to 256
+        best *= dk <= 64 ? kWideUnitNarrowKeys : kWideUnit;
+        for (int r = 1; r <= 2 && dk <= (io == LR_BF16 ? 128 : 256); ++r) {
+            const Step &st = kSteps[dk <= 64 ? 0 : dk <= 128 ? 1 : 2][r - 1];
+            const int64_t few_rows = decay_general_rows(dk, r), few = B * H * ((dv + few_rows - 1) / few_rows);
+            auto step_time = [&](int64_t b) {   // of all rounds of blocks
+                const int64_t most = (b + sms - 1) / sms, full = most / slots, rest = most % slots;
+                const double last = rest == 0 ? 0.0 : st.one + (st.full - st.one) * double(rest - 1) / double(slots - 1);
+                return double(full) * st.full + (full > 0 ? 0.84 : 1.0) * last;
+            };
+            for (int64_t s = 1; s == 1 || (s <= kGenMaxSeg && s * kFewMinSeg <= L); ++s) {
+                const double per = double(((L + s - 1) / s + unit - 1) / unit * unit);
+                double t = step_time(few * s) * (per + kFewBlockCost + kFewStateCost * double(s));
+                if (s > 1) t += step_time(few * (s - 1)) * (0.36 * per + kFewBlockCost) + kFewLaunchTime;
+                if (kFewMargin * t < best) best = kFewMargin * t, n = s, p->thread_rows = r;
+            }
+        }
     }
     p->seg_len = ((L + n - 1) / n + unit - 1) / unit * unit;
     p->n_seg = int((L + p->seg_len - 1) / p->seg_len);
-    const int64_t rows = p->path == 1 ? kDecayRows : decay_general_rows(dk, p->narrow);
+    const int64_t rows = p->path == 1 ? kDecayRows : decay_general_rows(dk, p->thread_rows);
     p->tiles = int((dv + rows - 1) / rows) * p->parts;
     p->blocks = B * H * p->tiles * p->n_seg;
     const size_t segs = size_t(B) * H * (p->n_seg - 1);

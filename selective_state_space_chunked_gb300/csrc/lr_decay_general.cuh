@@ -35,11 +35,32 @@
 //   blocks of 256 threads: 211 against 205; three blocks per SM: 266 against 204
 // (each pair measured on the kernel of its time)
 //
+// Few blocks.  A step's time is then its own latency, not the pipes' rate: with one block
+// of four rows a thread on an SM it took 0.26 us (0.34 with a scan's gates), 240 cycles of
+// which are arithmetic.  Forms with one or two rows a thread make four or two times the
+// blocks, take the sums over lanes of 8 or 4 steps together (7 shuffles for 8 steps instead
+// of 24), and leave the decay factors, 400 cycles a chunk, to a warp of their own: 0.095 and
+// 0.15 us a step.  They read more from shared memory per product (a lane's k_t and q_t serve
+// one or two rows), which bounds them with four blocks on an SM at 0.175 and 0.19 us a step.
+// Which form and how many segments: decay_plan.  One row a thread against its form before,
+// one step at a time: fp32 B1 L128 H16 d128 25.5 -> 16.8 us.  Three staging buffers and the
+// gates a chunk earlier: no change; chunks of 32 steps at 128 keys: 85 -> 94 us (fp32 B2
+// L700 H12 P80 N96, one segment).
+//
+// A selective scan with heads (HEADS): the step size goes into 1 / A_t, the skip and the
+// gate into the outputs.  The gates of a chunk's outputs are read together, ahead of the
+// barrier: with a load per output behind it, B2 L2048 H16 P128 N128 took 255 us against 227
+// (decayed attention 198), B8 L1017 H32 P64 N64 469 against 312.  fp32 B2 L700 H12 P80
+// N96: 50.5 us (two rows a thread, 5 segments; 26 MB), 5 TFLOP/s; B4 L4096 H16 P128
+// N128: 774 us, 22 TFLOP/s.
+//
 // Infinities and NaN go through the state as the recurrence takes them.  A segment
 // says whether the state it leaves is finite (seg_bad), so that a later one does not
 // pass over an infinity whose decay factor is 0.  S^ is up to 2^48 times S, so a
 // state past 2^79 may overflow.
 #pragma once
+
+#include <type_traits>
 
 #include "lr_decay.cuh"
 #include "lr_vec.cuh"
@@ -58,17 +79,20 @@ constexpr int kGB = 2;    // staging buffers
 // d64), and 4 x 8 elements, which make twice the blocks, 73 against 91 there, 289
 // against 310 at B4 L4096 H16 d64, 98 against 87 at B8 L1000 H8 d64; at 128 columns
 // 4 x 8 take 410 us and 8 x 8 212 against 200 (B2 L2048 H16 d128).
-template <int DKP_, bool NARROW>
+template <int DKP_, int RT_>
 struct DecCfg {
     static constexpr int DKP = DKP_;
     static constexpr int CPT = DKP <= 64 ? 8 : 16;
-    static constexpr int RT = NARROW ? 1 : 4;
+    static constexpr int RT = RT_;
+    static constexpr bool NARROW = RT < 4;   // few blocks (see above)
     static constexpr int NT = NARROW || DKP <= 64 ? 64 : 128;   // threads per block
     static constexpr int P = DKP / CPT;
+    static constexpr int GS = NARROW ? (P < 8 ? P : 8) / RT : 1;   // steps whose sums over lanes are taken together
+    static constexpr int NW = NARROW ? 32 : 0;                     // a warp for the decay factors alone
     static constexpr int RB = RT * NT / P;
     static constexpr int KB = DKP < 256 ? DKP : 256;   // key columns per TMA box
     static constexpr int NH = DKP / KB;
-    static constexpr int BPS = DKP >= 256 ? 3 : 512 / NT;   // blocks an SM is to hold
+    static constexpr int BPS = DKP >= 256 ? 3 : NARROW ? 4 : 512 / NT;   // blocks an SM is to hold
     // steps per staged chunk
     template <typename IO>
     __host__ __device__ static constexpr int steps() {
@@ -139,17 +163,17 @@ __device__ __forceinline__ void state_st4(float *r, int j, int dk, bool v4, floa
 // STATE_ONLY: the first launch of a segmented call (no q, no output; segments
 // 0 .. n_seg - 2).  HEADS: a selective scan with heads (see HeadsArgs).
 template <typename IO, typename C, bool STATE_ONLY, bool HEADS>
-__global__ void __launch_bounds__(C::NT, C::BPS)
+__global__ void __launch_bounds__(C::NT + C::NW, C::BPS)
     decay_general_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                          const __grid_constant__ CUtensorMap tm_v, const DecayArgs a, int nrb, bool tma,
                          uint64_t timeout_ns, StatusRef sref) {
-    constexpr int CPT = C::CPT, RT = C::RT, P = C::P, RB = C::RB, KB = C::KB, NT = C::NT;
+    constexpr int CPT = C::CPT, RT = C::RT, P = C::P, RB = C::RB, KB = C::KB, NT = C::NT, GS = C::GS;
     constexpr int TC = C::template steps<IO>(), VT = TC * RB;
     constexpr int KT = C::template pitch<IO>(TC * C::DKP), VTP = C::template pitch<IO>(VT);
     extern __shared__ __align__(128) unsigned char smem[];
-    IO *ks = reinterpret_cast<IO *>(smem);   // [GB][NH][TC][KB] (pitch KT)
+    IO *ks = reinterpret_cast<IO *>(smem);   // [kGB][NH][TC][KB] (pitch KT)
     IO *qs = ks + kGB * KT;
-    IO *vs = qs + kGB * KT;                  // [GB][TC][RB] (pitch VTP)
+    IO *vs = qs + kGB * KT;                  // [kGB][TC][RB] (pitch VTP)
     float *os = reinterpret_cast<float *>(vs + kGB * VTP);   // [2][TC][RB]: one barrier a chunk
     float *mu = os + 2 * VT;                     // [2][TC] readout factors scale A_t
     float *mw = mu + 2 * TC;                 // [2][TC] 1 / A_t (1 in a steep chunk)
@@ -172,6 +196,8 @@ __global__ void __launch_bounds__(C::NT, C::BPS)
     const int b = dec::row_at(a, x / a.H, reinterpret_cast<int *>(os)), bh = b * a.H + h;
     if (tid == 0 && blockIdx.x == 0) status_begin(sref);
     const int p = tid % P, rg = tid / P;
+    // the threads that hold the state; the warp of the decay factors
+    const bool holds = C::NW == 0 || tid < NT, factor_warp = C::NW == 0 ? tid < 32 : tid >= NT;
     const int row0 = rb * RB, dk = a.dk, dv = a.dv;
     const int rbv = min(RB, dv - row0);
     const int64_t L = a.L;
@@ -203,8 +229,8 @@ __global__ void __launch_bounds__(C::NT, C::BPS)
             fence_mbar_init();
         }
     } else {   // what the element copies never write: columns past dk, rows past dv
-        for (int e = tid; e < kGB * KT; e += NT) ks[e] = qs[e] = Io<IO>::from_f(0.0f);
-        for (int e = tid; e < kGB * VTP; e += NT) vs[e] = Io<IO>::from_f(0.0f);
+        for (int e = tid; e < kGB * KT; e += NT + C::NW) ks[e] = qs[e] = Io<IO>::from_f(0.0f);
+        for (int e = tid; e < kGB * VTP; e += NT + C::NW) vs[e] = Io<IO>::from_f(0.0f);
     }
 
     const int nchunks = (nrun + TC - 1) / TC;
@@ -224,19 +250,33 @@ __global__ void __launch_bounds__(C::NT, C::BPS)
             }
         } else {
             const int nt = min(TC, nrun - t0);
-            for (int t = 0; t < nt; ++t) {
-                const size_t sk = size_t(t0 + t) * LK, sq = size_t(t0 + t) * LQ, sv = size_t(t0 + t) * LV;
-                for (int j = tid; j < dk; j += NT) {
+            constexpr int NE = C::NW > 0 ? 4 : 1;   // steps at a time; with four rows a thread, no registers for it
+            for (int t = 0; t < nt; t += NE) {
+                for (int j = tid; j < dk; j += NT + C::NW) {
                     const int at = (j / KB) * TC * KB + t * KB + j % KB;
-                    kd[at] = kb[sk + j];
-                    if (!STATE_ONLY) qd[at] = qb[sq + j];
+                    IO kx[NE], qx[NE];
+#pragma unroll
+                    for (int i = 0; i < NE; ++i) {
+                        if (NE > 1 && t + i >= nt) continue;
+                        kx[i] = kb[size_t(t0 + t + i) * LK + j];
+                        if (!STATE_ONLY) qx[i] = qb[size_t(t0 + t + i) * LQ + j];
+                    }
+#pragma unroll
+                    for (int i = 0; i < NE; ++i) {
+                        if (NE > 1 && t + i >= nt) continue;
+                        kd[at + i * KB] = kx[i];
+                        if (!STATE_ONLY) qd[at + i * KB] = qx[i];
+                    }
                 }
-                for (int r = tid; r < rbv; r += NT) vd[t * RB + r] = vb[sv + r];
+                for (int e = tid; e < NE * RB; e += NT + C::NW) {
+                    const int i = e / RB, r = e % RB;
+                    if (r < rbv && t + i < nt) vd[(t + i) * RB + r] = vb[size_t(t0 + t + i) * LV + r];
+                }
             }
         }
     };
 
-    // decay factors of a chunk by warp 0, lane t its step t.  base: log2 decay
+    // decay factors of a chunk by one warp, lane t its step t.  base: log2 decay
     // since the last rescale; tot: since the segment's start.
     const dec::Gates<HEADS> gates(a, h);
     long long base = 0, tot = 0;
@@ -245,7 +285,7 @@ __global__ void __launch_bounds__(C::NT, C::BPS)
         const int t = c * TC + lane;
         return gb != nullptr && lane < TC && t < nrun ? Io<IO>::to_f(gb[size_t(t) * GP]) : 0.0f;
     };
-    auto factors = [&](int c, float gv) {   // warp 0
+    auto factors = [&](int c, float gv) {
         const int t = c * TC + lane;
         float wt;
         const float lt = gates.of(gv, wt);
@@ -292,7 +332,7 @@ __global__ void __launch_bounds__(C::NT, C::BPS)
 #pragma unroll
         for (int rr = 0; rr < RT; ++rr) {
             const int i = row0 + rg * RT + rr;
-            if (i >= dv) continue;
+            if (i >= dv || !holds) continue;
 #pragma unroll
             for (int m = 0; m < CPT / 4; ++m) {
                 const float4 s = state_ld4(src + size_t(i) * dk, 4 * (m * P + p), dk, v4);
@@ -322,16 +362,28 @@ __global__ void __launch_bounds__(C::NT, C::BPS)
     }
     if (STATE_ONLY) launch_dependents();
 
-    if (tid < 32 && nchunks > 0) factors(0, load_g(0));
+    if (factor_warp && nchunks > 0) factors(0, load_g(0));
     __syncthreads();   // barriers initialised or buffers cleared, factors of chunk 0
     for (int c = 0; c < kGB - 1 && c < nchunks; ++c) stage(c, c);
     if (!tma) __syncthreads();
+    constexpr bool kGated = HEADS && !STATE_ONLY;
+    constexpr int ZN = kGated ? (VT / NT < 8 ? VT / NT : 8) : 1;   // outputs a thread takes at a time
+    auto load_z = [&](int c, int e0, float (&zs)[ZN]) {
+#pragma unroll
+        for (int i = 0; i < ZN; ++i) {
+            const int e = e0 + tid + i * NT, t = c * TC + e / RB, r = e % RB;
+            zs[i] = zb != nullptr && t < nrun && r < rbv ? Io<IO>::to_f(zb[size_t(t) * a.hd.ldz + r]) : 0.0f;
+        }
+    };
     for (int c = 0; c < nchunks; ++c) {
         const int buf = c % kGB;
         const bool more = c + 1 < nchunks;
         float gn = 0.0f;
-        if (tid < 32 && more) gn = load_g(c + 1);
+        if (factor_warp && more) gn = load_g(c + 1);
         if (c + kGB - 1 < nchunks) stage(c + kGB - 1, (c + kGB - 1) % kGB);
+        [[maybe_unused]] float zs[ZN];   // with registers to spare read here, else behind the steps
+        if constexpr (kGated && C::NW > 0)
+            if (holds) load_z(c, 0, zs);
         const bool ok = !tma || mbar_wait_bounded(&full[buf], (c / kGB) & 1, timeout_ns);
         float *oc = os + (c & 1) * VT;
         const int nt = min(TC, nrun - c * TC);
@@ -346,60 +398,77 @@ __global__ void __launch_bounds__(C::NT, C::BPS)
 #pragma unroll
                 for (int m = 0; m < CPT / 2; ++m) S[rr][m] = __fmul2_rn(S[rr][m], f2);
         };
-        auto step = [&](int t) {
-            const IO *kr = ks + buf * KT + t * KB + 4 * p, *qr = qs + buf * KT + t * KB + 4 * p;
-            const float wt = w[t];
-            float2 v2[RT], acc[RT][2];
+        // N steps; their outputs' sums over lanes are taken together
+        auto steps = [&](int first, auto count) {
+            constexpr int N = count.value;
+            float r[N * RT];
 #pragma unroll
-            for (int rr = 0; rr < RT; ++rr) {
-                const float vv = wt * Io<IO>::to_f(vr[t * RB + rr]);
-                v2[rr] = make_float2(vv, vv);
-                acc[rr][0] = acc[rr][1] = make_float2(0.0f, 0.0f);
-            }
-#pragma unroll
-            for (int m = 0; m < CPT / 4; ++m) {
-                const int off = ((4 * P * m) / KB) * TC * KB + (4 * P * m) % KB;
-                const float4 k4 = dec_ld4<IO>(kr + off);
-                const float2 k01 = make_float2(k4.x, k4.y), k23 = make_float2(k4.z, k4.w);
-                float4 q4 = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                if (!STATE_ONLY) q4 = dec_ld4<IO>(qr + off);
-                const float2 q01 = make_float2(q4.x, q4.y), q23 = make_float2(q4.z, q4.w);
+            for (int i = 0; i < N; ++i) {
+                const int t = first + i;
+                const IO *kr = ks + buf * KT + t * KB + 4 * p, *qr = qs + buf * KT + t * KB + 4 * p;
+                const float wt = w[t];
+                float2 v2[RT], acc[RT][2];
 #pragma unroll
                 for (int rr = 0; rr < RT; ++rr) {
-                    S[rr][2 * m] = __ffma2_rn(v2[rr], k01, S[rr][2 * m]);
-                    S[rr][2 * m + 1] = __ffma2_rn(v2[rr], k23, S[rr][2 * m + 1]);
-                    if (!STATE_ONLY) {
-                        acc[rr][0] = __ffma2_rn(S[rr][2 * m], q01, acc[rr][0]);
-                        acc[rr][1] = __ffma2_rn(S[rr][2 * m + 1], q23, acc[rr][1]);
+                    const float vv = wt * Io<IO>::to_f(vr[t * RB + rr]);
+                    v2[rr] = make_float2(vv, vv);
+                    acc[rr][0] = acc[rr][1] = make_float2(0.0f, 0.0f);
+                }
+#pragma unroll
+                for (int m = 0; m < CPT / 4; ++m) {
+                    const int off = ((4 * P * m) / KB) * TC * KB + (4 * P * m) % KB;
+                    const float4 k4 = dec_ld4<IO>(kr + off);
+                    const float2 k01 = make_float2(k4.x, k4.y), k23 = make_float2(k4.z, k4.w);
+                    float4 q4 = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    if (!STATE_ONLY) q4 = dec_ld4<IO>(qr + off);
+                    const float2 q01 = make_float2(q4.x, q4.y), q23 = make_float2(q4.z, q4.w);
+#pragma unroll
+                    for (int rr = 0; rr < RT; ++rr) {
+                        S[rr][2 * m] = __ffma2_rn(v2[rr], k01, S[rr][2 * m]);
+                        S[rr][2 * m + 1] = __ffma2_rn(v2[rr], k23, S[rr][2 * m + 1]);
+                        if (!STATE_ONLY) {
+                            acc[rr][0] = __ffma2_rn(S[rr][2 * m], q01, acc[rr][0]);
+                            acc[rr][1] = __ffma2_rn(S[rr][2 * m + 1], q23, acc[rr][1]);
+                        }
                     }
+                }
+                if (!STATE_ONLY) {
+#pragma unroll
+                    for (int rr = 0; rr < RT; ++rr)
+                        r[i * RT + rr] = (acc[rr][0].x + acc[rr][0].y) + (acc[rr][1].x + acc[rr][1].y);
                 }
             }
             if (!STATE_ONLY) {
-                float r[RT];
-#pragma unroll
-                for (int rr = 0; rr < RT; ++rr)
-                    r[rr] = (acc[rr][0].x + acc[rr][0].y) + (acc[rr][1].x + acc[rr][1].y);
-                row_sums<RT, P>(r, p);
-                const float ut = u[t];
-                if (p < RT) {
+                row_sums<N * RT, P>(r, p);
+                const int at = N == 1 ? first : first + p / RT, row = N == 1 ? p : p % RT;
+                const float ut = u[at];
+                if (p < N * RT) {   // lane p: of step p / RT, row p % RT
                     const float y = ut * r[0];
-                    oc[t * RB + rg * RT + p] = has_skip ? fmaf(skip, Io<IO>::to_f(vr[t * RB + p]), y) : y;
+                    oc[at * RB + rg * RT + row] = has_skip ? fmaf(skip, Io<IO>::to_f(vr[at * RB + row]), y) : y;
                 }
             }
         };
-        if (steep) {   // a loop of its own: the common one carries no trace of it
+        using One = std::integral_constant<int, 1>;
+        if (!holds) {
+        } else if (steep) {   // a loop of its own: the common one carries no trace of it
             mul(mf[0]);
 #pragma unroll 1
             for (int t = 0; t < nt; ++t) {
                 mul(wa[t]);
-                step(t);
+                steps(t, One{});
             }
         } else {
-#pragma unroll 2
-            for (int t = 0; t < nt; ++t) step(t);
+            int t0 = 0;
+            if constexpr (GS > 1) {
+#pragma unroll 1
+                for (; t0 + GS <= nt; t0 += GS) steps(t0, std::integral_constant<int, GS>{});
+            }
+#pragma unroll(GS > 1 ? 1 : 2)
+            for (int t = GS > 1 ? t0 : 0; t < nt; ++t) steps(t, One{});
             if (after != 1.0f) mul(after);
         }
-        if (tid < 32 && more) factors(c + 1, gn);   // its buffer was last read in chunk c - 1
+        if constexpr (kGated && C::NW == 0) load_z(c, 0, zs);
+        if (factor_warp && more) factors(c + 1, gn);   // its buffer was last read in chunk c - 1
         // chunk c's buffer, its outputs, the next factors.  After a wait that ran
         // out every thread leaves here, once the copies in flight have landed.
         if (__syncthreads_or(!ok)) {
@@ -410,24 +479,32 @@ __global__ void __launch_bounds__(C::NT, C::BPS)
             }
             break;
         }
-        if (!STATE_ONLY) {
-            for (int e = tid; e < TC * RB; e += NT) {
-                const int t = e / RB, r = e % RB;
-                if (t < nt && r < rbv) {
-                    float y = oc[e];
-                    if constexpr (HEADS)
-                        if (zb != nullptr) y *= silu_f(Io<IO>::to_f(zb[size_t(c * TC + t) * a.hd.ldz + r]));
-                    ob[size_t(c * TC + t) * HV + r] = Io<IO>::from_f(y);
+        if (!STATE_ONLY && holds) {
+            if constexpr (kGated) {
+#pragma unroll 1
+                for (int e0 = 0; e0 < VT; e0 += ZN * NT) {
+                    if (e0 > 0) load_z(c, e0, zs);
+#pragma unroll
+                    for (int i = 0; i < ZN; ++i) {
+                        const int e = e0 + tid + i * NT, t = e / RB, r = e % RB;
+                        if (t < nt && r < rbv)
+                            ob[size_t(c * TC + t) * HV + r] = Io<IO>::from_f(zb != nullptr ? oc[e] * silu_f(zs[i]) : oc[e]);
+                    }
+                }
+            } else {
+                for (int e = tid; e < TC * RB; e += NT) {
+                    const int t = e / RB, r = e % RB;
+                    if (t < nt && r < rbv) ob[size_t(c * TC + t) * HV + r] = Io<IO>::from_f(oc[e]);
                 }
             }
         }
     }
 
-    if (tid < 32 && bad) status_report(sref, LR_ERR_RANGE);
+    if (factor_warp && bad) status_report(sref, LR_ERR_RANGE);
     // steps of the segment past the row's length
     if (!STATE_ONLY) {
         const int64_t nseg_steps = send - s0;
-        for (int64_t e = int64_t(nrun) * RB + tid; e < nseg_steps * RB; e += NT) {
+        for (int64_t e = int64_t(nrun) * RB + tid; e < nseg_steps * RB; e += NT + C::NW) {
             const int64_t t = e / RB;
             const int r = int(e % RB);
             if (r < rbv) ob[size_t(t) * HV + r] = Io<IO>::from_f(0.0f);
@@ -439,9 +516,9 @@ __global__ void __launch_bounds__(C::NT, C::BPS)
         dst0 = a.seg_state + (size_t(bh) * (a.n_seg - 1) + seg) * dv * dk;
     else if (seg == a.n_seg - 1 && a.S_final != nullptr)
         dst0 = a.S_final + size_t(bh) * dv * dk;
-    if (STATE_ONLY && rb == 0 && tid == 0) a.seg_tot[size_t(bh) * (a.n_seg - 1) + seg] = tot;
+    if (STATE_ONLY && rb == 0 && (C::NW ? tid == NT : tid == 0)) a.seg_tot[size_t(bh) * (a.n_seg - 1) + seg] = tot;
     if (dst0 != nullptr) {
-        if (tid == 0) mm[0] = dec::exp2_fix(base);   // warp 0 holds base
+        if (C::NW ? tid == NT : tid == 0) mm[0] = dec::exp2_fix(base);
         __syncthreads();
         const float f = mm[0];
         const bool v4 = rows16(dst0);
@@ -458,7 +535,7 @@ __global__ void __launch_bounds__(C::NT, C::BPS)
 #pragma unroll
         for (int rr = 0; rr < RT; ++rr) {
             const int i = row0 + rg * RT + rr;
-            if (i >= dv) continue;
+            if (i >= dv || !holds) continue;
 #pragma unroll
             for (int m = 0; m < CPT / 4; ++m) {
                 const float2 s0 = S[rr][2 * m], s1 = S[rr][2 * m + 1];
@@ -497,34 +574,35 @@ int launch_general_cfg(const DecayArgs &a, StatusRef st, cudaStream_t stream) {
     const int64_t per_seg = a.B * a.H * nrb;
     if (per_seg * a.n_seg > INT32_MAX) return LR_ERR_UNSUPPORTED;
     if (a.n_seg > 1) {
-        const int rc = launch_kernel(first, false, dim3(unsigned(per_seg * (a.n_seg - 1))), C::NT, smem, stream, mq,
+        const int rc = launch_kernel(first, false, dim3(unsigned(per_seg * (a.n_seg - 1))), C::NT + C::NW, smem, stream, mq,
                                      mk, mv, a, nrb, tma, kDefaultTimeoutNs, st);
         if (rc != LR_OK) return rc;
     }
     // dependent launch: of the kernel before the call, or of the first launch, of
     // which segment 0 needs nothing
-    return launch_kernel(main, true, dim3(unsigned(per_seg * a.n_seg)), C::NT, smem, stream, mq, mk, mv, a, nrb, tma,
+    return launch_kernel(main, true, dim3(unsigned(per_seg * a.n_seg)), C::NT + C::NW, smem, stream, mq, mk, mv, a, nrb, tma,
                          kDefaultTimeoutNs, st);
 }
 
 template <typename IO, int DKP, bool HEADS>
-int launch_general_dk(const DecayArgs &a, bool narrow, StatusRef st, cudaStream_t stream) {
-    return narrow ? launch_general_cfg<IO, DecCfg<DKP, true>, HEADS>(a, st, stream)
-                  : launch_general_cfg<IO, DecCfg<DKP, false>, HEADS>(a, st, stream);
+int launch_general_dk(const DecayArgs &a, int rows, StatusRef st, cudaStream_t stream) {
+    if (rows == 1) return launch_general_cfg<IO, DecCfg<DKP, 1>, HEADS>(a, st, stream);
+    if (rows == 2) return launch_general_cfg<IO, DecCfg<DKP, 2>, HEADS>(a, st, stream);
+    return launch_general_cfg<IO, DecCfg<DKP, 4>, HEADS>(a, st, stream);
 }
 
 }  // namespace
 
 template <typename IO, bool HEADS>
 int decay_general_launch(const DecayArgs &a, const DecayPlan &p, StatusRef st, cudaStream_t stream) {
-    if (a.dk <= 32) return launch_general_dk<IO, 32, HEADS>(a, p.narrow, st, stream);
-    if (a.dk <= 64) return launch_general_dk<IO, 64, HEADS>(a, p.narrow, st, stream);
-    if (a.dk <= 128) return launch_general_dk<IO, 128, HEADS>(a, p.narrow, st, stream);
+    if (a.dk <= 32) return launch_general_dk<IO, 32, HEADS>(a, p.thread_rows, st, stream);
+    if (a.dk <= 64) return launch_general_dk<IO, 64, HEADS>(a, p.thread_rows, st, stream);
+    if (a.dk <= 128) return launch_general_dk<IO, 128, HEADS>(a, p.thread_rows, st, stream);
     if (a.dk <= 256) {
-        if constexpr (sizeof(IO) == 4) return launch_general_dk<IO, 256, HEADS>(a, p.narrow, st, stream);
-        return launch_general_cfg<IO, DecCfg<256, false>, HEADS>(a, st, stream);
+        if constexpr (sizeof(IO) == 4) return launch_general_dk<IO, 256, HEADS>(a, p.thread_rows, st, stream);
+        return launch_general_cfg<IO, DecCfg<256, 4>, HEADS>(a, st, stream);
     }
-    return launch_general_cfg<IO, DecCfg<512, false>, HEADS>(a, st, stream);
+    return launch_general_cfg<IO, DecCfg<512, 4>, HEADS>(a, st, stream);
 }
 
 }  // namespace lr
