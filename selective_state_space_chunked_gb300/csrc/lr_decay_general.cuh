@@ -398,13 +398,14 @@ __global__ void __launch_bounds__(C::NT + C::NW, C::BPS)
 #pragma unroll
                 for (int m = 0; m < CPT / 2; ++m) S[rr][m] = __fmul2_rn(S[rr][m], f2);
         };
-        // N steps; their outputs' sums over lanes are taken together
-        auto steps = [&](int first, auto count) {
+        // N steps; their outputs' sums over lanes are taken together.  each: S decays at every step
+        auto steps = [&](int first, auto count, auto each) {
             constexpr int N = count.value;
             float r[N * RT];
 #pragma unroll
             for (int i = 0; i < N; ++i) {
                 const int t = first + i;
+                if (each) mul(wa[t]);
                 const IO *kr = ks + buf * KT + t * KB + 4 * p, *qr = qs + buf * KT + t * KB + 4 * p;
                 const float wt = w[t];
                 float2 v2[RT], acc[RT][2];
@@ -448,23 +449,22 @@ __global__ void __launch_bounds__(C::NT + C::NW, C::BPS)
                 }
             }
         };
-        using One = std::integral_constant<int, 1>;
-        if (!holds) {
-        } else if (steep) {   // a loop of its own: the common one carries no trace of it
-            mul(mf[0]);
-#pragma unroll 1
-            for (int t = 0; t < nt; ++t) {
-                mul(wa[t]);
-                steps(t, One{});
-            }
-        } else {
+        auto all_steps = [&](auto each) {
+            using One = std::integral_constant<int, 1>;
             int t0 = 0;
             if constexpr (GS > 1) {
 #pragma unroll 1
-                for (; t0 + GS <= nt; t0 += GS) steps(t0, std::integral_constant<int, GS>{});
+                for (; t0 + GS <= nt; t0 += GS) steps(t0, std::integral_constant<int, GS>{}, each);
             }
-#pragma unroll(GS > 1 ? 1 : 2)
-            for (int t = GS > 1 ? t0 : 0; t < nt; ++t) steps(t, One{});
+#pragma unroll(GS > 1 || each ? 1 : 2)
+            for (int t = GS > 1 ? t0 : 0; t < nt; ++t) steps(t, One{}, each);
+        };
+        if (!holds) {
+        } else if (steep) {   // a loop of its own: the common one carries no trace of it
+            mul(mf[0]);
+            all_steps(std::true_type{});
+        } else {
+            all_steps(std::false_type{});
             if (after != 1.0f) mul(after);
         }
         if constexpr (kGated && C::NW == 0) load_z(c, 0, zs);

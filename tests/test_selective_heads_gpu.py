@@ -100,6 +100,25 @@ def test_large_and_small_step_sizes(lr, io, N):  # noqa: F811
     check(lr, p, io)
 
 
+@pytest.mark.parametrize("io,B,L,H,G,P,N", [
+    ("f32", 1, 90, 4, 1, 64, 128), ("f32", 1, 333, 2, 1, 24, 20), ("f32", 2, 700, 12, 3, 80, 96), ("f32", 4, 37, 16, 1, 128, 128),
+    ("f32", 8, 101, 16, 4, 64, 128), ("f32", 5, 203, 9, 3, 70, 250), ("f32", 3, 411, 6, 1, 33, 61), ("f32", 32, 50, 16, 2, 64, 64),
+    ("f32", 2, 150, 8, 2, 64, 32), ("bf16", 1, 40, 16, 2, 128, 128), ("bf16", 8, 47, 16, 1, 64, 128), ("bf16", 2, 300, 5, 5, 50, 60)])
+@pytest.mark.parametrize("ragged", [False, True])
+def test_rows_a_thread_and_segments(lr, io, B, L, H, G, P, N, ragged):  # noqa: F811
+    """Few blocks and many, one segment and several, aligned rows and others; heads that
+    hardly decay beside heads whose every chunk decays below 2^-32."""
+    p = wl.selective_heads_inputs(B, L, H, G, P, N, seed=L + N, io=io, with_S0=True)
+    dt = p["dt"].float()
+    dt[..., 0] = 4.0
+    if H > 2:
+        dt[..., 1] = -12.0
+        dt[:, L // 3:, 2] = 2.0
+    p["dt"] = dt.to(p["dt"].dtype)
+    lens = [(L * (b + 1) * 7) % (L + 1) for b in range(B)] if ragged else None
+    check(lr, p, io, lens=lens)
+
+
 @pytest.mark.parametrize("io", ["f32", "bf16"])
 def test_step_sizes_given_as_they_are(lr, io):  # noqa: F811
     p = wl.selective_heads_inputs(2, 200, 2, 1, 64, 64, seed=4, io=io)
