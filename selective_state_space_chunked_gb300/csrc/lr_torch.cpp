@@ -7,8 +7,8 @@
 // Each function takes what its helper in binding.py takes and returns what it
 // returns, or None where an argument is not already what the kernels take
 // (another type or device, not contiguous or in rows that are not evenly apart, shapes
-// that do not match, empty) or
-// the call's own checks refused it; nothing has been launched then, and the helper
+// that do not match, empty; the selective scan with heads copies what only stands in the
+// wrong place) or the call's own checks refused it; nothing has been launched then, and the helper
 // goes on to its own checks and conversions, which convert the argument or say what
 // is wrong.  Any other status comes back as an int, for the helper to raise: part of
 // the call may have run, and it may have updated a state in place.  The interpreter
@@ -16,6 +16,7 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
+#include <ATen/core/grad_mode.h>
 #include <ATen/ops/empty.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
@@ -58,6 +59,13 @@ struct Call {
         *p = t.data_ptr();
         return true;
     }
+    // a tensor of the given shape, of the call's GPU and dtype
+    bool like(PyObject *o, at::IntArrayRef shape) const {
+        if (!THPVariable_CheckExact(o)) return false;
+        const at::Tensor &t = THPVariable_Unpack(o);
+        return t.is_cuda() && t.layout() == at::kStrided && t.get_device() == dev && t.scalar_type() == type &&
+               t.sizes() == shape;
+    }
     // a tensor whose rows of `width` lie evenly apart (a slice of a wider one): the elements
     // from one to the next.  whole: on 16-byte boundaries, unless they are dense.
     bool rows(PyObject *o, bool whole, bool optional, void **p, int64_t *ld, at::IntArrayRef shape) const {
@@ -65,11 +73,8 @@ struct Call {
             *p = nullptr, *ld = 0;
             return optional;
         }
-        if (!THPVariable_CheckExact(o)) return false;
+        if (!like(o, shape)) return false;
         const at::Tensor &t = THPVariable_Unpack(o);
-        if (!t.is_cuda() || t.layout() != at::kStrided || t.get_device() != dev || t.scalar_type() != type ||
-            t.sizes() != shape)
-            return false;
         *ld = pitch(t);
         *p = t.data_ptr();
         return *ld > 0 && reinterpret_cast<uintptr_t>(*p) % 16 == 0 &&
@@ -382,6 +387,30 @@ PyObject *causal_conv_step(PyObject *, PyObject *const *args, Py_ssize_t n) {
 struct Scan {
     int64_t H, G, P, N, ldx, lddt, ldb, ldc, ldz;
     void *x, *dt, *Bm, *Cm, *z, *A, *skip, *bias, *S;
+    // tensors whose rows leave 16-byte boundaries, to be copied: a projection's z does where
+    // dt, one column a head, stands beside it
+    struct Apart {
+        at::Tensor t;
+        void **p;
+        int64_t *ld;
+    };
+    std::vector<Apart> apart;
+    bool whole_rows(const Call &c, PyObject *o, bool optional, void **p, int64_t *ld, at::IntArrayRef shape) {
+        if (c.rows(o, true, optional, p, ld, shape)) return true;
+        if (!c.like(o, shape)) return false;
+        apart.push_back({THPVariable_Unpack(o), p, ld});
+        return true;
+    }
+    // (with the interpreter released)
+    void copy_apart() {
+        if (apart.empty()) return;
+        const at::NoGradGuard no_grad;
+        for (Apart &a : apart) {
+            a.t = a.t.clone(at::MemoryFormat::Contiguous);
+            *a.p = a.t.data_ptr();
+            *a.ld = a.t.size(-1);
+        }
+    }
     bool of(const Call &c, const at::Tensor &xt, PyObject *const *args) {
         if (!to_int(args[5], &H) || !to_int(args[6], &G) || H < 1 || G < 1 || H % G != 0 || xt.size(-1) % H != 0 ||
             !THPVariable_CheckExact(args[2]))
@@ -395,9 +424,9 @@ struct Scan {
         const int64_t dt3[] = {B, L, H}, bc3[] = {B, L, G * N}, dt2[] = {B, H}, bc2[] = {B, G * N}, ss[] = {B, H, P, N};
         const at::IntArrayRef ds = prompt ? at::IntArrayRef(dt3) : at::IntArrayRef(dt2);
         const at::IntArrayRef bs = prompt ? at::IntArrayRef(bc3) : at::IntArrayRef(bc2);
-        return c.rows(args[0], true, false, &x, &ldx, xt.sizes()) && c.rows(args[1], false, false, &dt, &lddt, ds) &&
-               c.rows(args[2], true, false, &Bm, &ldb, bs) && c.rows(args[3], true, false, &Cm, &ldc, bs) &&
-               c.take(args[4], at::kFloat, {H}, false, &A) && c.rows(args[7], true, true, &z, &ldz, xt.sizes()) &&
+        return whole_rows(c, args[0], false, &x, &ldx, xt.sizes()) && c.rows(args[1], false, false, &dt, &lddt, ds) &&
+               whole_rows(c, args[2], false, &Bm, &ldb, bs) && whole_rows(c, args[3], false, &Cm, &ldc, bs) &&
+               c.take(args[4], at::kFloat, {H}, false, &A) && whole_rows(c, args[7], true, &z, &ldz, xt.sizes()) &&
                c.take(args[8], at::kFloat, {H}, true, &skip) && c.take(args[9], at::kFloat, {H}, true, &bias) &&
                c.take(args[10], at::kFloat, ss, true, &S);
     }
@@ -423,6 +452,7 @@ PyObject *selective_heads(PyObject *, PyObject *const *args, Py_ssize_t n) {
         int rc;
         {
             const Unlocked unlocked;
+            s.copy_apart();
             y = at::empty(x->sizes(), x->options());
             Sf = at::empty({B, s.H, s.P, s.N}, x->options().dtype(at::kFloat));
             ws = at::empty({static_cast<int64_t>(wsb)}, x->options().dtype(at::kByte));
@@ -457,6 +487,7 @@ PyObject *selective_heads_step(PyObject *, PyObject *const *args, Py_ssize_t n) 
         int rc;
         {
             const Unlocked unlocked;
+            s.copy_apart();
             y = at::empty(x->sizes(), x->options());
             if (out == nullptr) {
                 Sn = at::empty(ss, x->options().dtype(at::kFloat));
