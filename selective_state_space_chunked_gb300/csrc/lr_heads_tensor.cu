@@ -34,6 +34,18 @@
 // of one chunk's outputs stand in no chunk's way, dS 64, onto which the three terms of the
 // state's weights add up (side by side, as in the decayed attention, they would take the
 // columns of O's second buffer).
+//
+// Measured (bf16 H16 P128 N128, back to back in a graph): B4 L4096 with gate 109.6 us, which
+// is 1.95 TB/s of its 214 MB and 157 TFLOP/s; without 98.6; every chunk steep 111.7; B1
+// L32768 286, 4 segments (gates 20, the segments' states 70, outputs 190).  The chunk is a
+// chain of hand-overs between the roles, with one block on 128 of 152 SMs: issue 40 %,
+// tensor pipe 24 %, DRAM 28 %.  What carried it there (B4 L4096, us): gates by a launch of
+// their own 222 -> 146; outputs by whole sectors 130; shared work evenly over the
+// schedulers and fewer operations 124.6; the gate's tile by TMA and two accumulators of
+// outputs 112; whole quarters of weights 109.6.  Rejected: z a chunk ahead in registers
+// 149 to 153 (spills); the weights' loop unrolled twice 112, four times 125 (the roles
+// share an instruction cache); two or four buffers of column factors, and a suspend
+// time in the waits: no change.
 #include "lr_decay_tensor.cuh"
 
 namespace lr {
@@ -144,7 +156,9 @@ __device__ __forceinline__ const unsigned char *record_at(const DecayArgs &a, in
 // (lane i: steps 4 i .. 4 i + 3), as many chunks at once as it has warps: sums within
 // the chunk, then, from the chunks' totals, which warp 0 goes through, whether the state
 // is rescaled at each and what decay has been left before it.  (Every warp going through
-// them: 15.7 us under a profiler at B4 L4096 H16, and most of that issue slots.)
+// them: 15.7 us under a profiler at B4 L4096 H16, most of that issue slots; so 12.5, of which
+// the loads of dt, H elements apart, are most.  In clusters of four blocks: no change behind
+// the call.)
 __global__ void __launch_bounds__(1024) heads_gates_kernel(const __grid_constant__ DecayArgs a, StatusRef sref) {
     using namespace ht;
     using bf = __nv_bfloat16;
