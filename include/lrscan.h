@@ -340,8 +340,8 @@ int lr_decay_attn_fwd(const void *q, const void *k, const void *v,
  * for t < lens[b], and S_final[b,h] = S after the last of them; rows past their
  * length, resets (a decay of 0), infinities and NaN, the range of the scaled state
  * and the precision are those of lr_decay_attn_fwd, whose kernels run this with q = C,
- * k = B, v = delta x.  The step size, the decay and delta x B^T are formed in fp32
- * whatever `io`.  An infinity or a NaN in z reaches its own output.  A step size that
+ * k = B, v = delta x.  The step size, the decay, delta x B^T and the skip are formed in
+ * fp32 whatever `io`.  An infinity or a NaN in z reaches its own output.  A step size that
  * is negative or NaN sets LR_ERR_RANGE; that call's outputs are then not meaningful.
  *
  * Layouts: x, z, y: (B, L, H*P); dt: (B, L, H); Bm, Cm: (B, L, G*N), all in `io`;

@@ -8,12 +8,14 @@
 // mathematics, the precision and what infinities do), with q = C, k = B, v = x and a
 // step size beside every decay weight:
 //
-//   O  = [(Q K^T) . D + skip I] V + diag(2^L) Q S^T,   D_ts = d_s 2^(L_t - L_s), s <= t
+//   O  = [(Q K^T) . D] V + diag(2^L) Q S^T + skip V,   D_ts = d_s 2^(L_t - L_s), s <= t
 //   S' = 2^L_C S + sum_s d_s 2^(L_C - L_s) v_s k_s^T
 //
 // The step sizes go into the factors that the columns of Q K^T and the state's weights
-// have anyway, and the skip onto the diagonal before it is rounded to bf16, so both cost
-// the chain of a chunk's hand-overs nothing.
+// have anyway.  The skip is added by the output warps in fp32 (on the diagonal of Q K^T,
+// which is rounded to bf16, it would lose its own last bits); they take their part of V
+// into registers before they wait for the chunk's products, so that they hold its tile no
+// longer than the products do.
 //
 // What the gates come to is made by a launch of its own: softplus, the sums of log
 // decays in 64-bit fixed point and the powers are the same for every block of a head's
@@ -35,17 +37,20 @@
 // state's weights add up (side by side, as in the decayed attention, they would take the
 // columns of O's second buffer).
 //
-// Measured (bf16 H16 P128 N128, back to back in a graph): B4 L4096 with gate 109.6 us, which
-// is 1.95 TB/s of its 214 MB and 157 TFLOP/s; without 98.6; every chunk steep 111.7; B1
-// L32768 286, 4 segments (gates 20, the segments' states 70, outputs 190).  The chunk is a
-// chain of hand-overs between the roles, with one block on 128 of 152 SMs: issue 40 %,
-// tensor pipe 24 %, DRAM 28 %.  What carried it there (B4 L4096, us): gates by a launch of
-// their own 222 -> 146; outputs by whole sectors 130; shared work evenly over the
-// schedulers and fewer operations 124.6; the gate's tile by TMA and two accumulators of
-// outputs 112; whole quarters of weights 109.6.  Rejected: z a chunk ahead in registers
-// 149 to 153 (spills); the weights' loop unrolled twice 112, four times 125 (the roles
-// share an instruction cache); two or four buffers of column factors, and a suspend
-// time in the waits: no change.
+// Measured (bf16 H16 P128 N128, back to back in a graph): B4 L4096 with skip and gate 118 us,
+// which is 1.8 TB/s of its 214 MB; without the gate 99, without the skip 108; every chunk
+// steep 120; B1 L32768 306, without the gate 263, 4 segments (gates 20, the segments' states
+// 70, the rest outputs).  The chunk is a chain of hand-overs between the roles, with one block
+// on 128 of 152 SMs: no unit is near its limit (profiles/selective_heads_conv_rope.md).  What
+// carried it there (B4 L4096, us): gates by a launch of their own 222 -> 146; outputs by whole
+// sectors 130; shared work evenly over the schedulers and fewer operations 124.6; the gate's
+// tile by TMA and two accumulators of outputs 112; whole quarters of weights 109.6; the skip in
+// fp32 instead of on the diagonal 118.  Rejected: z a chunk ahead in registers 149 to 153
+// (spills); the weights' loop unrolled twice 112, four times 125 (the roles share an
+// instruction cache); two or four buffers of column factors, and a suspend time in the waits:
+// no change.  The skip in other places: into the accumulator ahead of the products 135 (it waits
+// for the next V), x read once the products are there 120, from global memory 137, with the
+// gate's tile taken early too 132 to 139 (registers), on the diagonal in two bf16 terms 116.
 #include "lr_decay_tensor.cuh"
 
 namespace lr {
@@ -134,6 +139,17 @@ __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t b
         "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_u32(dst)),
         "l"(src), "r"(bytes), "r"(smem_u32(bar))
         : "memory");
+}
+
+// 16 bytes of shared memory, read here: a plain load whose value only some lanes come to use
+// was moved down to them, past the hand-over of what it reads.
+__device__ __forceinline__ uint4 read_now(const void *p) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(smem_u32(p))
+                 : "memory");
+    return v;
 }
 
 // The neighbouring lane's value.
@@ -243,7 +259,7 @@ __global__ void __launch_bounds__(1024) heads_gates_kernel(const __grid_constant
         const long long before = before_of[warp], end = before + all;
         const bool re = how_of[warp] & 1, steep = how_of[warp] & 2;
         if (c >= n_chunks) continue;
-        float w[4], r[4], x[4], col[4];
+        float w[4], r[4], col[4];
         int u[4];
         const long long last = __shfl_sync(0xffffffffu, l[3], lane | 3);   // of the lane's 16 steps
 #pragma unroll
@@ -254,11 +270,9 @@ __global__ void __launch_bounds__(1024) heads_gates_kernel(const __grid_constant
             u[i] = dec::units_of(l[i]);
             if (steep) {
                 r[i] = -dec::exp2_fix(before + l[i]);   // (its sign says so, -0 too)
-                x[i] = delta[i];
                 col[i] = delta[i] * dec::exp2_fix(last - l[i]);
             } else {
                 r[i] = dec::exp2_fix(-e);
-                x[i] = p;
                 col[i] = w[i];
             }
         }
@@ -266,8 +280,8 @@ __global__ void __launch_bounds__(1024) heads_gates_kernel(const __grid_constant
         *reinterpret_cast<float4 *>(a.hd.weight + at) = make_float4(w[0], w[1], w[2], w[3]);
         *reinterpret_cast<float4 *>(a.hd.readout + at) = make_float4(r[0], r[1], r[2], r[3]);
         float4 *own = reinterpret_cast<float4 *>(a.hd.own + at);
-        own[0] = make_float4(x[0], __int_as_float(u[0]), x[1], __int_as_float(u[1]));
-        own[1] = make_float4(x[2], __int_as_float(u[2]), x[3], __int_as_float(u[3]));
+        own[0] = make_float4(delta[0], __int_as_float(u[0]), delta[1], __int_as_float(u[1]));
+        own[1] = make_float4(delta[2], __int_as_float(u[2]), delta[3], __int_as_float(u[3]));
         if (seg < a.n_seg - 1) {   // weights to the chunk's end, for the state that the segment leaves
             float e[4];
 #pragma unroll
@@ -554,8 +568,8 @@ __global__ void __launch_bounds__(hs::THREADS, 1)
 
 // ---------------------------------------------------------------------------
 // PARTS: the block's part of the key columns, its outputs a term of the sum, which the sum
-// gates; GATE: outputs are gated here
-template <bool PARTS, bool GATE>
+// gates; GATE: outputs are gated here; SKIP: there may be a skip (PARTS: in the first part's blocks)
+template <bool PARTS, bool GATE, bool SKIP>
 __global__ void __launch_bounds__(ht::THREADS, 1)
     heads_tensor_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                         const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_z,
@@ -591,6 +605,7 @@ __global__ void __launch_bounds__(ht::THREADS, 1)
     const int nkk = (dk + 15) / 16;          // 16-wide steps over the key columns
     const bool two = dk > 64;                // two 64-column halves of Q and K
     const size_t g0 = step_at(a, bh, s0);    // the segment's gates
+    const bool has_skip = SKIP && (!PARTS || (a.hd.skip != nullptr && part == 0));
 
     uint64_t *bar = reinterpret_cast<uint64_t *>(sm + OFF_BAR);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + OFF_TMEM);
@@ -601,10 +616,12 @@ __global__ void __launch_bounds__(ht::THREADS, 1)
             int n = 1;
             if (i >= F_DONE && i < K_DONE + 2) n = 8;
             if (i == DS_FREE || i == DS_FREE + 1 || i == EMPTY_Z || i == SB_READY || i == FIX) n = 8;
-            // K is read by dS and P, Q by P and OX, V by the weight warps (through dS) and OI
+            // K is read by dS and P, Q by P and OX, V by the weight warps (through dS), by OI and,
+            // with a skip, by the output warps
             if ((i >= EMPTY_Q && i < EMPTY_Q + 2) || (i >= EMPTY_K && i < EMPTY_K + 2) ||
                 (i >= EMPTY_V && i < EMPTY_V + 2))
                 n = 2;
+            if (has_skip && i >= EMPTY_V && i < EMPTY_V + 2) n = 2 + 8;
             if (i == MMA_END) n = 3;
             mbar_init(&bar[i], n);
         }
@@ -845,8 +862,6 @@ __global__ void __launch_bounds__(ht::THREADS, 1)
         const int seen = 2 * fw + 2, sharers = fw == 0 ? 1 : fw == 3 ? 3 : 2, each = (seen + sharers - 1) / sharers;
         const int first = k * each, end = min(seen, first + each);
         const int clear = (8 - seen) / sharers, clear0 = seen + k * clear;   // (evenly shared)
-        const bool has_skip = a.hd.skip != nullptr && part == 0;
-        const float skip = has_skip ? a.hd.skip[h] : 0.0f;
         gates_wait();
         const float2 *src = a.hd.own + g0 + t;
         float2 next = n_chunks > 0 ? __ldcg(src) : make_float2(0.0f, 0.0f);
@@ -862,7 +877,6 @@ __global__ void __launch_bounds__(ht::THREADS, 1)
             const bool steep = rec[st].steep != 0;
             const float *f = rec[st].col;
             const int lt = __float_as_int(own.y);               // steep
-            const float dg = skip * (steep ? 1.0f : own.x);
 #pragma unroll 1
             for (int kb = clear0; kb < clear0 + clear; ++kb) {
                 const uint32_t r[8] = {};
@@ -907,13 +921,11 @@ __global__ void __launch_bounds__(ht::THREADS, 1)
                         }
                     }
                 }
-                if (diag) {   // row t sees columns up to its own, which takes the skip
+                if (diag) {   // row t sees columns up to its own
                     const int d = t - b0;
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        if (has_skip && e == d) p[e] += dg;
+                    for (int e = 0; e < 16; ++e)
                         if (e > d) p[e] = 0.0f;
-                    }
                 }
 #pragma unroll
                 for (int e = 0; e < 8; ++e) r[e] = pack(p[2 * e], p[2 * e + 1]);
@@ -935,11 +947,12 @@ __global__ void __launch_bounds__(ht::THREADS, 1)
         const int i0 = vt * RB + 32 * oh;
         const size_t HV = size_t(a.H) * dv;
         bf *ob = static_cast<bf *>(a.o) + (size_t(b) * a.L + s0) * HV + size_t(h) * dv + i0;
+        const float skip = has_skip ? a.hd.skip[h] : 0.0f;
         gates_wait();
         const float *src = a.hd.readout + g0 + row;
         float next = n_chunks > 0 ? __ldcg(src) : 0.0f;
         float2 zero = make_float2(0.0f, 0.0f);
-        const uint32_t zat = OFF_Z + sw128_offset(row, 32 * oh);   // this thread's part of the gate's tile
+        const uint32_t at = sw128_offset(row, 32 * oh);   // this thread's part of the tiles of V and of the gate
         for (int c = 0; c < n_chunks; ++c) {
             const int st = c & 1;
             const uint32_t O = tmem + T_O + st * 64 + 32 * oh + (uint32_t((warp & 3) * 32) << 16);
@@ -947,6 +960,14 @@ __global__ void __launch_bounds__(ht::THREADS, 1)
             if (c + 1 < n_chunks) next = __ldcg(src + (c + 1) * C);
             const int t = c * C + row;
             const bool valid = t < nrun;
+            uint4 x[4] = {};   // 8 columns each
+            if (SKIP && has_skip) {
+                if (!__all_sync(0xffffffffu, hw(FULL_V + st, c >> 1))) break;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) x[k] = read_now(sm + OFF_V + st * V_BYTES + (at ^ (16 * k)));
+                __syncwarp();
+                if (lane == 0) arrive(&bar[EMPTY_V + st]);
+            }
             if (__float_as_int(u) < 0) {   // steep: rows of Q S^T by 2^(base + L) before PD V is added
                 if (!__all_sync(0xffffffffu, hw(OX_DONE + st, c >> 1))) break;
                 tc_fence_after();
@@ -970,7 +991,7 @@ __global__ void __launch_bounds__(ht::THREADS, 1)
             if (GATE && there) there = hw(FULL_Z, c);
             if (!__all_sync(0xffffffffu, there)) break;
             tc_fence_after();
-            const float2 u2 = make_float2(u, u);
+            const float2 u2 = make_float2(u, u), s2 = make_float2(skip, skip);
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
                 float d[16];
@@ -981,12 +1002,20 @@ __global__ void __launch_bounds__(ht::THREADS, 1)
                     __syncwarp();
                     if (lane == 0) arrive(&bar[K_DONE + st]);
                 }
+                const uint32_t xw[8] = {x[2 * q].x,     x[2 * q].y,     x[2 * q].z,     x[2 * q].w,
+                                        x[2 * q + 1].x, x[2 * q + 1].y, x[2 * q + 1].z, x[2 * q + 1].w};
+                auto out = [&](int r) {   // values 2 r and 2 r + 1 before the gate
+                    float2 y = __fmul2_rn(u2, make_float2(d[2 * r], d[2 * r + 1]));
+                    if (SKIP) y = __ffma2_rn(s2, make_float2(lo_f(xw[r]), hi_f(xw[r])), y);
+                    return y;
+                };
                 const int col = i0 + 16 * q;
                 if (PARTS) {   // steps past the row's end are the sum's to clear
                     float *dst = a.o_part + ((size_t(part) * a.B + b) * a.L + s0 + t) * HV + size_t(h) * dv + col;
 #pragma unroll
                     for (int r = 0; r < 16; r += 4) {
-                        const float4 y = make_float4(u * d[r], u * d[r + 1], u * d[r + 2], u * d[r + 3]);
+                        const float2 y0 = out(r / 2), y1 = out(r / 2 + 1);
+                        const float4 y = make_float4(y0.x, y0.y, y1.x, y1.y);
                         if (valid && col + r < dv) *reinterpret_cast<float4 *>(dst + r) = y;
                         if (valid) zero.x = fmaf(0.0f, y.x, fmaf(0.0f, y.y, fmaf(0.0f, y.z, fmaf(0.0f, y.w, zero.x))));
                     }
@@ -994,8 +1023,8 @@ __global__ void __launch_bounds__(ht::THREADS, 1)
                 }
                 uint32_t w[8];
                 if constexpr (GATE) {
-                    const uint4 lo = *reinterpret_cast<const uint4 *>(sm + (zat ^ (32 * q)));
-                    const uint4 hi = *reinterpret_cast<const uint4 *>(sm + (zat ^ (32 * q + 16)));
+                    const uint4 lo = *reinterpret_cast<const uint4 *>(sm + OFF_Z + (at ^ (32 * q)));
+                    const uint4 hi = *reinterpret_cast<const uint4 *>(sm + OFF_Z + (at ^ (32 * q + 16)));
                     if (q == 1) {   // the tile is free
                         __syncwarp();
                         if (lane == 0) arrive(&bar[EMPTY_Z]);
@@ -1003,7 +1032,7 @@ __global__ void __launch_bounds__(ht::THREADS, 1)
                     const uint32_t zw[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
 #pragma unroll
                     for (int r = 0; r < 8; ++r) {
-                        float2 y = __fmul2_rn(u2, make_float2(d[2 * r], d[2 * r + 1]));
+                        float2 y = out(r);
                         if (valid) zero = __ffma2_rn(y, make_float2(0.0f, 0.0f), zero);
                         y = __fmul2_rn(y, silu2_f(make_float2(lo_f(zw[r]), hi_f(zw[r]))));
                         w[r] = pack(y.x, y.y);
@@ -1011,7 +1040,7 @@ __global__ void __launch_bounds__(ht::THREADS, 1)
                 } else {
 #pragma unroll
                     for (int r = 0; r < 8; ++r) {
-                        const float2 y = __fmul2_rn(u2, make_float2(d[2 * r], d[2 * r + 1]));
+                        const float2 y = out(r);
                         if (valid) zero = __ffma2_rn(y, make_float2(0.0f, 0.0f), zero);
                         w[r] = pack(y.x, y.y);
                     }
@@ -1142,8 +1171,11 @@ bool ht_setup() {
             return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes)) == cudaSuccess;
         };
         return room(heads_state_kernel<false>, hs::SMEM) && room(heads_state_kernel<true>, hs::SMEM) &&
-               room(heads_tensor_kernel<false, false>, ht::SMEM) && room(heads_tensor_kernel<false, true>, ht::SMEM) &&
-               room(heads_tensor_kernel<true, false>, ht::SMEM);
+               room(heads_tensor_kernel<false, false, false>, ht::SMEM) &&
+               room(heads_tensor_kernel<false, false, true>, ht::SMEM) &&
+               room(heads_tensor_kernel<false, true, false>, ht::SMEM) &&
+               room(heads_tensor_kernel<false, true, true>, ht::SMEM) &&
+               room(heads_tensor_kernel<true, false, true>, ht::SMEM);
     });
 }
 
@@ -1167,10 +1199,11 @@ int heads_tensor_launch(const DecayArgs &a, StatusRef st, cudaStream_t stream) {
         rc = launch_kernel(parts ? heads_state_kernel<true> : heads_state_kernel<false>, true,
                            dim3(unsigned(per_seg * (a.n_seg - 1))), hs::THREADS, hs::SMEM, stream, mk, mv, a, n_vt,
                            kDefaultTimeoutNs, st);
+    const bool z = a.hd.z != nullptr, skip = a.hd.skip != nullptr;
     if (rc == LR_OK)
-        rc = launch_kernel(parts                 ? heads_tensor_kernel<true, false>
-                           : a.hd.z != nullptr ? heads_tensor_kernel<false, true>
-                                                 : heads_tensor_kernel<false, false>,
+        rc = launch_kernel(parts ? heads_tensor_kernel<true, false, true>
+                           : z   ? (skip ? heads_tensor_kernel<false, true, true> : heads_tensor_kernel<false, true, false>)
+                                 : (skip ? heads_tensor_kernel<false, false, true> : heads_tensor_kernel<false, false, false>),
                            true,
                            dim3(unsigned(per_seg * a.n_seg)), ht::THREADS, ht::SMEM, stream, mq, mk, mv, mz, a, n_vt,
                            kDefaultTimeoutNs, st);
