@@ -783,7 +783,9 @@ int64_t lr_set_host_chunk_steps(int64_t steps);
  * Test hook for the bounded look-back wait: when `split` >= 1, the thread
  * blocks of that time split never publish their carries, so their successors'
  * waits run out (after about `timeout_ms` milliseconds), set LR_ERR_TIMEOUT
- * and finish with a zero carry.  -1 disables.  Process-wide, not
+ * and finish with a zero carry.  Meanwhile that limit is also the one of the bounded
+ * waits of the tensor-core kernels (HGRN2 in bf16, decayed attention, selective scan with
+ * heads).  -1 disables.  Process-wide, not
  * thread-safe.  Returns LR_OK.
  */
 int lr_test_withhold_split(int split, int timeout_ms);

@@ -1028,13 +1028,13 @@ int decay_tensor_launch(const DecayArgs &a, StatusRef st, cudaStream_t stream) {
     if (a.n_seg > 1)
         rc = launch_kernel(parts ? decay_state_kernel<true> : decay_state_kernel<false>, false,
                            dim3(unsigned(per_seg * (a.n_seg - 1))), ds::THREADS, ds::SMEM, stream, mk, mv, a, n_vt,
-                           kDefaultTimeoutNs, st);
+                           dt::wait_limit_ns(), st);
     // dependent launch: of the kernel before the call, or of the first launch, of
     // which segment 0 needs nothing
     if (rc == LR_OK)
         rc = launch_kernel(parts ? decay_tensor_kernel<true> : decay_tensor_kernel<false>, true,
                            dim3(unsigned(per_seg * a.n_seg)), dt::THREADS, dt::SMEM, stream, mq, mk, mv, a, n_vt,
-                           kDefaultTimeoutNs, st);
+                           dt::wait_limit_ns(), st);
     if (rc != LR_OK || !parts) return rc;
     const int64_t rows = a.B * a.L;
     return launch_early(decay_parts_kernel<false>, dim3(unsigned(rows < (1 << 20) ? rows : 1 << 20)), 256, stream, a);

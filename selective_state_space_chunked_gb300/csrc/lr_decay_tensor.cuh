@@ -59,9 +59,13 @@ struct Ctl {
 static_assert(sizeof(Ctl) <= 40, "");
 
 // The slow path of every wait (one copy of the code): bounded; the first to
-// run out makes every role leave its loop.
+// run out makes every role leave its loop.  The limit is for this launch's own work: a
+// role may be waiting for another that still waits for an earlier launch of the call, which
+// may take longer (a segment's steps one at a time are 1 us each), so the first time that the
+// limit runs out that launch's end is awaited and the limit starts over.
 static __device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, Ctl *ctl) {
     uint64_t t0 = 0;
+    bool alone = false;   // no earlier launch is still running
     for (uint32_t n = 1;; ++n) {
         uint32_t ok;
         asm volatile(
@@ -77,12 +81,21 @@ static __device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, Ctl
         if (*reinterpret_cast<volatile int *>(&ctl->abort_flag) != 0) return false;
         const uint64_t now = globaltimer_ns();
         if (t0 == 0) t0 = now;
-        if (now - t0 > ctl->timeout_ns) {
+        if (now - t0 > ctl->timeout_ns && !alone) {
+            grid_dependency_wait();
+            alone = true;
+            t0 = globaltimer_ns();
+        } else if (now - t0 > ctl->timeout_ns) {
             *reinterpret_cast<volatile int *>(&ctl->abort_flag) = 1;
             status_report(StatusRef{ctl->word, ctl->stamp}, LR_ERR_TIMEOUT);
             return false;
         }
     }
+}
+
+// The limit of a call's waits.
+inline uint64_t wait_limit_ns() {
+    return g_withheld_split >= 1 ? uint64_t(g_withheld_timeout_ms) * 1000000ull : kDefaultTimeoutNs;
 }
 
 // 0 times the values that were written, added up: no 0 once one was not finite.

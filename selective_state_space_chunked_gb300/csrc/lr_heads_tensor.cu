@@ -1198,7 +1198,7 @@ int heads_tensor_launch(const DecayArgs &a, StatusRef st, cudaStream_t stream) {
     if (rc == LR_OK && a.n_seg > 1)
         rc = launch_kernel(parts ? heads_state_kernel<true> : heads_state_kernel<false>, true,
                            dim3(unsigned(per_seg * (a.n_seg - 1))), hs::THREADS, hs::SMEM, stream, mk, mv, a, n_vt,
-                           kDefaultTimeoutNs, st);
+                           dt::wait_limit_ns(), st);
     const bool z = a.hd.z != nullptr, skip = a.hd.skip != nullptr;
     if (rc == LR_OK)
         rc = launch_kernel(parts ? heads_tensor_kernel<true, false, true>
@@ -1206,7 +1206,7 @@ int heads_tensor_launch(const DecayArgs &a, StatusRef st, cudaStream_t stream) {
                                  : (skip ? heads_tensor_kernel<false, false, true> : heads_tensor_kernel<false, false, false>),
                            true,
                            dim3(unsigned(per_seg * a.n_seg)), ht::THREADS, ht::SMEM, stream, mq, mk, mv, mz, a, n_vt,
-                           kDefaultTimeoutNs, st);
+                           dt::wait_limit_ns(), st);
     if (rc != LR_OK || !parts) return rc;
     const int64_t rows = a.B * a.L;
     return launch_early(decay_parts_kernel<true>, dim3(unsigned(rows < (1 << 20) ? rows : 1 << 20)), 256, stream, a);
