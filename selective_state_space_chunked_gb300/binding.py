@@ -856,6 +856,14 @@ def _par(t: Optional[torch.Tensor], dev) -> Optional[torch.Tensor]:
     return _dev(t.float(), dev)
 
 
+def _lens_of(lens: Optional[torch.Tensor], L: int, dev):
+    """lens as the kernels read them: clamped before they are narrowed, and in 64 bits, since
+    L need not fit a narrower type."""
+    if lens is None:
+        return None
+    return _act(lens if lens.dtype is torch.int32 else lens.to(torch.int64).clamp(0, L).to(torch.int32), dev)
+
+
 def decay_attn(q, k, v, H: int, Hk: Optional[int] = None, a_log=None, g=None, S0=None, lens=None,
                scale: float = 1.0, workspace=None, out=None,
                sync_host: bool = True) -> Tuple[torch.Tensor, torch.Tensor]:
@@ -900,8 +908,7 @@ def decay_attn(q, k, v, H: int, Hk: Optional[int] = None, a_log=None, g=None, S0
     dev = _target_device(q)
     q, k, v, g = _act(q, dev), _act(k, dev), _act(v, dev), _act(g, dev)
     a_log, S0 = _par(a_log, dev), _par(S0, dev)
-    if lens is not None:   # (clamped before it is narrowed)
-        lens = _act(lens if lens.dtype is torch.int32 else lens.clamp(0, L).to(torch.int32), dev)
+    lens = _lens_of(lens, L, dev)
     host_out = None
     if out is None:
         o = torch.empty((B, L, H * dv), dtype=q.dtype, device=dev)
@@ -993,11 +1000,6 @@ def _integers(t: Optional[torch.Tensor], shape, name: str):
         raise TypeError(f"{name} must be integers")
 
 
-def _lens_of(lens: Optional[torch.Tensor], L: int, dev):
-    """lens as the kernels read them."""
-    if lens is None:
-        return None
-    return _act(lens if lens.dtype is torch.int32 else lens.clamp(0, L).to(torch.int32), dev)   # (clamped before)
 
 
 def _out_like(out: Optional[torch.Tensor], shape, dtype, dev, name: str = "out"):
