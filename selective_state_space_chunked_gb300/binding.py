@@ -445,7 +445,7 @@ def _aligned(t: torch.Tensor) -> torch.Tensor:
 def _dev(t: Optional[torch.Tensor], device) -> Optional[torch.Tensor]:
     if t is None:
         return None
-    if t.device.type != "cuda":
+    if t.device != device:   # (of another GPU too: its memory is not the kernels' to read)
         t = t.to(device, non_blocking=True)
     return _aligned(t)
 
@@ -844,14 +844,14 @@ def _stream_of(t: torch.Tensor) -> int:
 
 def _act(t: Optional[torch.Tensor], dev) -> Optional[torch.Tensor]:
     """t on the GPU, contiguous and aligned."""
-    if t is None or (t.is_cuda and t.is_contiguous() and t.data_ptr() % 16 == 0):
+    if t is None or (t.device == dev and t.is_contiguous() and t.data_ptr() % 16 == 0):
         return t
     return _dev(t, dev)
 
 
 def _par(t: Optional[torch.Tensor], dev) -> Optional[torch.Tensor]:
     """As _act, in float32 (parameters and states)."""
-    if t is None or (t.dtype is torch.float32 and t.is_cuda and t.is_contiguous() and t.data_ptr() % 16 == 0):
+    if t is None or (t.dtype is torch.float32 and t.device == dev and t.is_contiguous() and t.data_ptr() % 16 == 0):
         return t
     return _dev(t.float(), dev)
 
@@ -974,7 +974,7 @@ def _rows(t: Optional[torch.Tensor], dev, whole: bool = False):
     where t does not start on a 16-byte boundary (``whole``: its rows too, unless dense)."""
     if t is None:
         return None, 0
-    if not t.is_cuda:
+    if t.device != dev:
         t = t.to(dev, non_blocking=True)
     C = t.shape[-1]
     ld, size = None, 1
