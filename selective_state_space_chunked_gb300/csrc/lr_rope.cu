@@ -166,17 +166,14 @@ __global__ void __launch_bounds__(kRopeT) rope_kernel(const RopeArgs a) {
     const float inv_d = a.norm == LR_NORM_RMS ? 1.0f / float(a.d) : 1.0f;
     // (every lane of the warp goes through all a.heads turns: the sum needs them)
     auto head = [&](Raw (&rk)[U][2], bool in) {
-        float x[U][2][VN];
+        float x[U][2 * VN];   // a unit's two vectors
         float2 s2 = make_float2(0.0f, 0.0f);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            X::widen(rk[u][0], x[u][0]);
-            X::widen(rk[u][1], x[u][1]);
+            X::widen(rk[u][0], x[u]);
+            X::widen(rk[u][1], x[u] + VN);
 #pragma unroll
-            for (int e = 0; e < VN; ++e) {
-                const float2 v = VN == 1 ? make_float2(x[u][0][0], x[u][1][0]) : pair(x[u][0] + 2 * e);   // (both vectors)
-                s2 = __ffma2_rn(v, v, s2);
-            }
+            for (int e = 0; e < VN; ++e) s2 = __ffma2_rn(pair(x[u] + 2 * e), pair(x[u] + 2 * e), s2);
         }
         float rs = 1.0f;
         if (a.norm != LR_NORM_NONE) {
@@ -188,11 +185,11 @@ __global__ void __launch_bounds__(kRopeT) rope_kernel(const RopeArgs a) {
         const float2 rs2 = make_float2(rs, rs);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            float *p = x[u][0], *q = x[u][1];
+            float *p = x[u], *q = x[u] + VN;
             if constexpr (VN == 1 || INSIDE) {
 #pragma unroll
                 for (int e = 0; e < VN; ++e) {
-                    float &v = !INSIDE ? p[e] : x[u][0][2 * e], &w = !INSIDE ? q[e] : x[u][0][2 * e + 1];
+                    float &v = x[u][INSIDE ? 2 * e : e], &w = x[u][INSIDE ? 2 * e + 1 : VN + e];
                     const float v0 = v * rs, w0 = w * rs;
                     v = A[u][e] * v0, w = Cc[u][e] * w0;
                     if (e < turned[u]) v = fmaf(Bc[u][e], w0, v), w = fmaf(Dc[u][e], v0, w);
