@@ -449,7 +449,8 @@ typedef enum { LR_PAIRS_HALVES = 0, LR_PAIRS_NEIGHBOURS = 1 } lr_pairs;
  *   p = pos[n] freqs[i]
  *
  * and the values from rot on are r.  Arithmetic in fp32, outputs rounded once; the
- * angle is formed in 64-bit fixed point, so far positions are as exact as near ones.
+ * angle is formed in 64-bit fixed point, off by |pos[n]| 2^-64 turns at most, so far
+ * positions are as exact as near ones.
  * A head with an infinity or a NaN keeps it to itself; squares past fp32's range
  * (values past 1.8e19) give 0.
  *

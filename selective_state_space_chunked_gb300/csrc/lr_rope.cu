@@ -16,9 +16,9 @@
 //   one head ahead in flight 38 us, four heads' loads at once 36
 //   blocks of whole tokens, without 64-bit divisions, in sizes that fit them 32.6
 //
-// Angles.  freqs is turned into turns (1 / 2 pi) as two floats, to 2^-48 of it, and
-// those into a 64-bit fraction of a turn, whose product with the position wraps by
-// itself: far positions lose nothing to the size of their angle.
+// Angles.  freqs is turned into a 64-bit fraction of a turn, exact to 2^-64, whose product
+// with the position wraps by itself: far positions and high frequencies lose nothing to the
+// size of their angle (2^-33 of a turn at position 2^31).
 #include "lr_decay.cuh"
 #include "lr_vec.cuh"
 
@@ -41,14 +41,22 @@ struct RopeArgs {
     int tokens;                // of a block
 };
 
-// The part of a turn that a position adds, in units of 2^-64.
-__device__ __forceinline__ long long turn_of(float f) {
-    constexpr double kTurn = 0.15915494309189535;   // 1 / 2 pi
-    constexpr float kHi = float(kTurn), kLo = float(kTurn - double(kHi)), k62 = 4611686018427387904.0f;
-    float p = f * kHi;
-    const float r = fmaf(f, kLo, fmaf(f, kHi, -p));
-    p -= rintf(p);   // whole turns; exact
-    return static_cast<long long>(static_cast<unsigned long long>(__float2ll_rn(p * k62) + __float2ll_rn(r * k62)) << 2);
+// The part of a turn that a position adds, in units of 2^-64: the float's own 24 bits times
+// 1 / 2 pi in 128.
+__device__ __forceinline__ unsigned long long turn_of(float f) {
+    constexpr unsigned long long kHi = 0x28be60db9391054aull, kLo = 0x7f09d5f47d4d3770ull;   // 1 / 2 pi, in units of 2^-64 and 2^-128
+    const uint32_t u = __float_as_uint(f);
+    const int ex = max(int(u >> 23 & 255), 1), s = 150 - ex;              // |f| = m 2^-s
+    const unsigned long long m = (u & 0x7fffff) | ((u >> 23 & 255) != 0 ? 0x800000u : 0u);
+    const unsigned long long c = __umul64hi(m, kLo), lo = m * kHi + c, hi = __umul64hi(m, kHi) + (lo < c);
+    unsigned long long t = 0;
+    if (s <= 0)
+        t = s > -64 ? lo << -s : 0;
+    else if (s < 64)
+        t = lo >> s | hi << (64 - s);
+    else if (s < 128)
+        t = hi >> (s - 64);
+    return u >> 31 ? 0 - t : t;
 }
 
 // Sine and cosine of a fraction of a turn.  EXACT: to fp32's last places; else by the
@@ -134,8 +142,8 @@ __global__ void __launch_bounds__(kRopeT) rope_kernel(const RopeArgs a) {
         const int tokens = int(min(int64_t(a.tokens), a.N - n0));
         for (int i = threadIdx.x; i < tokens * nr; i += blockDim.x) {
             const int t = i / nr;
-            const unsigned long long at = static_cast<unsigned long long>(turn_of(a.freqs[i - t * nr])) *
-                                          static_cast<unsigned long long>(static_cast<long long>(a.pos[n0 + t]));
+            const unsigned long long at =
+                turn_of(a.freqs[i - t * nr]) * static_cast<unsigned long long>(static_cast<long long>(a.pos[n0 + t]));
             float s, c;
             sin_cos<sizeof(Raw) == VN * 4>(at, s, c);
             turns[i] = make_float2(c, s);
