@@ -341,8 +341,12 @@ int lr_decay_attn_fwd(const void *q, const void *k, const void *v,
  * length, resets (a decay of 0), infinities and NaN, the range of the scaled state
  * and the precision are those of lr_decay_attn_fwd, whose kernels run this with q = C,
  * k = B, v = delta x.  The step size, the decay, delta x B^T and the skip are formed in
- * fp32 whatever `io`.  An infinity or a NaN in z reaches its own output.  A step size that
- * is negative or NaN sets LR_ERR_RANGE; that call's outputs are then not meaningful.
+ * fp32 whatever `io`; with bf16 I/O, L >= 48 and P and N multiples of 8 the decayed scores
+ * and the copy of the state that an output is read from are rounded to bf16 (2e-3 of a
+ * usual output off in the mean square, of which the output's own rounding is 1.7e-3),
+ * other calls round the output alone.  An infinity or a NaN in z reaches its own output.
+ * A step size that is negative or NaN sets LR_ERR_RANGE; that call's outputs are then not
+ * meaningful.
  *
  * Layouts: x, z, y: (B, L, H*P); dt: (B, L, H); Bm, Cm: (B, L, G*N), all in `io`;
  *          A_log, dt_bias, Dskip: (H) fp32; lens: (B) int32; S0, S_final: (B, H, P, N)
@@ -420,7 +424,7 @@ int lr_group_norm_act(const void *x, const void *z, const float *gamma,
  *          outputs must not overlap inputs.
  * Requirements: B, L, C >= 0, W >= 2, ldx >= C, act one of lr_act (else
  *          LR_ERR_INVALID_ARG); W <= 4 (else LR_ERR_UNSUPPORTED).  No workspace.
- *          Whole 16-byte vectors are moved where C and ldx are multiples of them.
+ *          Vectors of four values are moved where C and ldx are multiples of four.
  */
 int lr_causal_conv_fwd(const void *x, int64_t ldx, const float *w, const float *bias,
                        const void *state, const int32_t *lens, void *y, void *state_out,
@@ -452,7 +456,8 @@ typedef enum { LR_PAIRS_HALVES = 0, LR_PAIRS_NEIGHBOURS = 1 } lr_pairs;
  * angle is formed in 64-bit fixed point, off by |pos[n]| 2^-64 turns at most, so far
  * positions are as exact as near ones.
  * A head with an infinity or a NaN keeps it to itself; squares past fp32's range
- * (values past 1.8e19) give 0.
+ * (values past 1.8e19) give 0, and a head whose squares all lie below it (values under
+ * 1e-23) with eps = 0 an infinity or a NaN.
  *
  * Layouts: q: (N, H*d), k: (N, Hk*d) in `io`, rows ldq and ldk elements apart (slices
  *          of a wider tensor); gamma_q, gamma_k: (d) fp32; freqs: (rot/2) fp32, radians
@@ -786,8 +791,7 @@ int64_t lr_set_host_chunk_steps(int64_t steps);
  * waits run out (after about `timeout_ms` milliseconds), set LR_ERR_TIMEOUT
  * and finish with a zero carry.  Meanwhile that limit is also the one of the bounded
  * waits of the tensor-core kernels (HGRN2 in bf16, decayed attention, selective scan with
- * heads).  -1 disables.  Process-wide, not
- * thread-safe.  Returns LR_OK.
+ * heads).  -1 disables.  Process-wide, not thread-safe.  Returns LR_OK.
  */
 int lr_test_withhold_split(int split, int timeout_ms);
 

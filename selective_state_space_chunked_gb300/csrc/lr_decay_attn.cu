@@ -36,6 +36,8 @@ constexpr double kFewBlockCost = 15.0, kFewStateCost = 4.0, kFewLaunchTime = 3.0
 // within 4 %: B1 L32768 H16 d128 1 segment 571 us, 2 433, 4 (chosen) 234, 8 274;
 // B1 L16384 H8 dk64 6 81, 9 60, 12 50.5, 16 (chosen) 47.0, 19 45.4, 24 68; B4 L2048
 // H16 1 (chosen) 48.4, 2 76.
+// The scan with heads takes the same costs, though its chunks are longer and a chunk of its
+// first launch is 0.37 of one of the last (70 us of 190 at B1 L32768 H16 P128 N128).
 constexpr int64_t kMaxSeg = 32;
 constexpr int64_t kTensorMinLen = 48;
 constexpr double kFirstCost = 0.6, kBlockCost = 3.0, kStateCost = 1.0;

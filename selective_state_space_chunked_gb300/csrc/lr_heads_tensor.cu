@@ -33,24 +33,29 @@
 // columns.  Roles, connected by mbarriers: state (8 warps), output (8: 32 rows by 32
 // columns a warp), front (8), weight (4), TMA, and one warp for each of dS, P and O's
 // products.  TMEM: P 2 x 128 columns (PD inside), O 2 x 64, so that the gate and the stores
-// of one chunk's outputs stand in no chunk's way, dS 64, onto which the three terms of the
-// state's weights add up (side by side, as in the decayed attention, they would take the
-// columns of O's second buffer).
+// of one chunk's outputs stand in no chunk's way, dS 2 x 64, onto which the three terms of
+// the state's weights add up (side by side, as in the decayed attention, they would take
+// the columns of O's second buffer).
 //
-// Measured (bf16 H16 P128 N128, back to back in a graph): B4 L4096 with skip and gate 118 us,
-// which is 1.8 TB/s of its 214 MB; without the gate 99, without the skip 108; every chunk
-// steep 120; B1 L32768 306, without the gate 263, 4 segments (gates 20, the segments' states
-// 70, the rest outputs).  The chunk is a chain of hand-overs between the roles, with one block
-// on 128 of 152 SMs: no unit is near its limit (profiles/selective_heads_conv_rope.md).  What
-// carried it there (B4 L4096, us): gates by a launch of their own 222 -> 146; outputs by whole
-// sectors 130; shared work evenly over the schedulers and fewer operations 124.6; the gate's
-// tile by TMA and two accumulators of outputs 112; whole quarters of weights 109.6; the skip in
-// fp32 instead of on the diagonal 118.  Rejected: z a chunk ahead in registers 149 to 153
-// (spills); the weights' loop unrolled twice 112, four times 125 (the roles share an
-// instruction cache); two or four buffers of column factors, and a suspend time in the waits:
-// no change.  The skip in other places: into the accumulator ahead of the products 135 (it waits
-// for the next V), x read once the products are there 120, from global memory 137, with the
-// gate's tile taken early too 132 to 139 (registers), on the diagonal in two bf16 terms 116.
+// Measured (bf16 H16 P128 N128, back to back in a graph): B4 L4096 with skip and gate 118.5
+// us, which is 1.8 TB/s of its 214 MB and 145 TFLOP/s; without the gate 99.5, without the
+// skip 108; every chunk steep 121; B1 L32768 308, without the gate 264, 4 segments (gates
+// 20, the segments' states 70, the rest outputs); B8 L1017 H32 P64 N64 69.7.  The chunk is
+// a chain of hand-overs between the roles, with one block on 128 of 152 SMs: issue 38 %,
+// tensor pipe 22 %, LSU 40 %, DRAM 26 %.
+//   adopted, each against the one before (B4 L4096 with gate, us): gates by a launch of their
+//   own 222 -> 146; outputs through P's free columns, stores by whole sectors 130; work
+//   shared evenly over the schedulers, fewer operations 124.6; the gate's tile by TMA and two
+//   accumulators of outputs 112; whole quarters of weights without a gate 109.6; the skip in
+//   fp32 instead of on the bf16 diagonal 118.5
+//   rejected: z a chunk ahead in registers 149 to 153 (spills); the weights' loop unrolled
+//   twice 112, four times 125 (the roles share an instruction cache); two or four buffers of
+//   column factors, a suspend time in the waits, the gates' launch in clusters of four: no
+//   change.  Of the skip: into the accumulator ahead of the products, by the output warps 135
+//   (it waits for the next V), by the front warps 125; x read once the products are there 120,
+//   from global memory 137; the gate's tile taken early too 132 to 139 (registers); the next
+//   tiles of V and of the gate prefetched into L2 117.5; on the diagonal in two bf16 terms 116,
+//   16 bits
 #include "lr_decay_tensor.cuh"
 
 namespace lr {

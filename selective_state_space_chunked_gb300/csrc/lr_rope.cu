@@ -8,10 +8,11 @@
 // partners of their pairs, so the norm is one sum over lanes and the rotation needs no
 // exchange; gamma times cosine and sine stay in registers for all heads of a token that
 // a set of lanes takes.  Measured on slices of a projection, in turn over 500 MB: bf16
-// 16384 tokens, 16 + 4 heads of 128 32.6 us (76 % of the copy bandwidth), half rotated in
-// neighbouring pairs 32.2; fp32 8192 tokens 27.4 (90 %); bf16 16384 tokens, 32 + 8 heads of
-// 64 28.7; 8 tokens 1.9.  The bf16 kernel is bound by its operations (about 100 a vector
-// pair, 27 million warp instructions at first):
+// 16384 tokens, 16 + 4 heads of 128 32.5 us (76 % of the copy bandwidth), half rotated in
+// neighbouring pairs 32.5; fp32 8192 tokens 27.7 (90 %); bf16 16384 tokens, 32 + 8 heads of
+// 64 28.8; 8 tokens 2.0.  No unit is near its limit in bf16 (issue 59 %, LSU 38 %, fp32 pipe
+// 24 %, 43 % of the warps): a set's loads wait for its last ones' sums and stores.  What its
+// operations and loads cost on the way (27 million warp instructions at first):
 //   angles for every set of lanes 37 us, once a token into shared memory 36
 //   one head ahead in flight 38 us, four heads' loads at once 36
 //   blocks of whole tokens, without 64-bit divisions, in sizes that fit them 32.6
