@@ -1028,8 +1028,8 @@ __global__ void __launch_bounds__(ht::THREADS, 1)
                 }
                 uint32_t w[8];
                 if constexpr (GATE) {
-                    const uint4 lo = *reinterpret_cast<const uint4 *>(sm + OFF_Z + (at ^ (32 * q)));
-                    const uint4 hi = *reinterpret_cast<const uint4 *>(sm + OFF_Z + (at ^ (32 * q + 16)));
+                    const uint4 lo = read_now(sm + OFF_Z + (at ^ (32 * q)));
+                    const uint4 hi = read_now(sm + OFF_Z + (at ^ (32 * q + 16)));
                     if (q == 1) {   // the tile is free
                         __syncwarp();
                         if (lane == 0) arrive(&bar[EMPTY_Z]);
