@@ -37,7 +37,7 @@
 // the state's weights add up (side by side, as in the decayed attention, they would take
 // the columns of O's second buffer).
 //
-// Measured (bf16 H16 P128 N128, back to back in a graph): B4 L4096 with skip and gate 118.5
+// Measured (bf16 H16 P128 N128, back to back in a graph): B4 L4096 with skip and gate 117.7
 // us, which is 1.8 TB/s of its 214 MB and 145 TFLOP/s; without the gate 99.5, without the
 // skip 108; every chunk steep 121; B1 L32768 308, without the gate 264, 4 segments (gates
 // 20, the segments' states 70, the rest outputs); B8 L1017 H32 P64 N64 69.7.  The chunk is
@@ -47,7 +47,7 @@
 //   own 222 -> 146; outputs through P's free columns, stores by whole sectors 130; work
 //   shared evenly over the schedulers, fewer operations 124.6; the gate's tile by TMA and two
 //   accumulators of outputs 112; whole quarters of weights without a gate 109.6; the skip in
-//   fp32 instead of on the bf16 diagonal 118.5
+//   fp32 instead of on the bf16 diagonal 118.5, the gate's tile handed back earlier 117.7
 //   rejected: z a chunk ahead in registers 149 to 153 (spills); the weights' loop unrolled
 //   twice 112, four times 125 (the roles share an instruction cache); two or four buffers of
 //   column factors, a suspend time in the waits, the gates' launch in clusters of four: no
